@@ -473,7 +473,8 @@ def run(s):
         if own:
             cache = _cache(s, pa)
             if "ws" not in s:  # a serving loop keeps its workspace
-                s["ws"] = pa.new_paged_workspace(cache, s["q"].shape[0], s["t_max"])
+                s["ws"] = pa.new_paged_workspace(cache, s["q"].shape[0], s["t_max"],
+                                                   Hq=s["q"].shape[1])
             args = (s["q"], s["k"], s["v"], s["w"], s["beta"])
             if s["log_f"] is None:
                 out = pa.path_paged_extend(*args, s["cu"], cache, s["t_max"], workspace=s["ws"])
