@@ -9,10 +9,12 @@ CUDA device every call raises.
 
 Entry points keep the C names: ``path_attn_fwd``, ``path_fox_fwd``,
 ``path_fwd_prepare``, ``path_fwd_scan``, ``path_decode_step``, ``path_fox_decode_step``,
-``path_wbeta_produce``,
-``path_workspace_bytes``, ``path_check_workspace``, ``path_status_string``.
+``path_wbeta_produce``, ``path_paged_extend``, ``path_fox_paged_extend``,
+``path_paged_reserve``, ``path_paged_fork``, ``path_paged_free``, ``path_paged_compact`` (on a
+``PathPagedCache``), ``path_workspace_bytes``, ``path_check_workspace``, ``path_status_string``.
 """
 import ctypes
+import dataclasses
 import math
 import os
 
@@ -20,7 +22,7 @@ from . import build as _build
 
 # status codes and enums, mirroring include/path_attn.h
 OK, ERR_NULL, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_WORKSPACE, ERR_CAPACITY, ERR_TIMEOUT, \
-    ERR_CUDA, ERR_ARG = range(10)
+    ERR_CUDA, ERR_ARG, ERR_CACHE = range(11)
 F32, BF16 = 0, 1
 OP_FWD, OP_FOX_FWD, OP_DECODE, OP_FOX_DECODE, OP_BWD, OP_FOX_BWD = 0, 1, 2, 3, 4, 5
 HEAD_DIM = 64
@@ -29,9 +31,22 @@ EXPORTED = ("path_workspace_bytes", "path_attn_fwd", "path_fox_fwd", "path_fwd_p
             "path_fwd_scan", "path_decode_step", "path_check_workspace", "path_status_string",
             "path_decode_step_noalloc", "path_fox_first_blocks", "path_fox_decode_step",
             "path_wbeta_workspace_bytes", "path_wbeta_produce", "path_attn_bwd",
-            "path_fox_bwd")
+            "path_fox_bwd", "path_paged_workspace_bytes", "path_paged_extend",
+            "path_fox_paged_extend", "path_paged_reserve", "path_paged_fork", "path_paged_free",
+            "path_paged_compact")
 
 _lib = None
+
+
+class _CPagedCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "g_pages", "k_table",
+                                               "v_table", "k_ref", "v_ref", "lens")] + \
+               [(n, ctypes.c_int) for n in ("seqs", "max_pages", "page", "num_k_pages",
+                                            "num_v_pages", "Hq", "Hkv", "d", "dtype")]
+
+
+class _CPagedStrides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64 * 2) for n in ("q", "k", "v", "w", "beta", "log_f", "out")]
 
 
 class PathError(RuntimeError):
@@ -87,6 +102,22 @@ def _load():
     lib.path_decode_step_noalloc.restype = I
     lib.path_fox_first_blocks.argtypes = [P, S, I, I, I, I, I, P, P]
     lib.path_fox_first_blocks.restype = I
+    C = ctypes.POINTER(_CPagedCache)
+    T = ctypes.POINTER(_CPagedStrides)
+    lib.path_paged_workspace_bytes.argtypes = [C, I, I]
+    lib.path_paged_workspace_bytes.restype = S
+    lib.path_paged_extend.argtypes = [C, P, P, P, P, P, P, I, I, F, P, T, P, S, P]
+    lib.path_paged_extend.restype = I
+    lib.path_fox_paged_extend.argtypes = [C, P, P, P, P, P, P, P, I, I, F, P, T, P, S, P]
+    lib.path_fox_paged_extend.restype = I
+    lib.path_paged_reserve.argtypes = [C, P, P, S, P]
+    lib.path_paged_reserve.restype = I
+    lib.path_paged_fork.argtypes = [C, P, P, I, P, S, P]
+    lib.path_paged_fork.restype = I
+    lib.path_paged_free.argtypes = [C, P, I, P, S, P]
+    lib.path_paged_free.restype = I
+    lib.path_paged_compact.argtypes = [C, P, S, P]
+    lib.path_paged_compact.restype = I
     lib.path_check_workspace.argtypes = [P, P]
     lib.path_check_workspace.restype = I
     lib.path_status_string.argtypes = [I]
@@ -464,3 +495,260 @@ def path_wbeta_produce(x, w_down, w_up, conv, u, bias, beta_max=2.0, w_out=None,
                                       _stream(stream, x.device)),
            "path_wbeta_produce")
     return w_out, beta_out
+
+
+# ---------------------------------------------------------------- paged cache
+
+@dataclasses.dataclass
+class PathPagedCache:
+    """The tensors of a paged cache (see path_paged_cache in include/path_attn.h): k_pages
+    (pages, Hkv, page, d) and v_pages of the same form, bfloat16 or float32; k_table, v_table
+    (seqs, max_pages) and lens (seqs) int32; k_ref, v_ref (pages) int32, which only the page
+    calls need; g_pages (K pages, Hq, page) float32 for PaTH-FoX. The object holds no state of
+    its own: calls read and update the tensors, and the caller advances ``lens``."""
+    k_pages: object
+    v_pages: object
+    k_table: object
+    v_table: object
+    lens: object
+    g_pages: object = None
+    k_ref: object = None
+    v_ref: object = None
+
+
+def new_paged_cache(seqs, max_pages, num_k_pages, num_v_pages=None, Hq=1, Hkv=None, d=HEAD_DIM,
+                    page=64, dtype=None, fox=False, device="cuda"):
+    """An empty PathPagedCache: all pages free, no slot mapped, all lengths 0. Keys and values
+    are not initialised (nothing reads a position before it is written)."""
+    torch = _torch()
+    Hkv = Hq if Hkv is None else Hkv
+    nv = num_k_pages if num_v_pages is None else num_v_pages
+    dtype = torch.bfloat16 if dtype is None else dtype
+    i32 = dict(dtype=torch.int32, device=device)
+    return PathPagedCache(
+        k_pages=torch.empty((num_k_pages, Hkv, page, d), dtype=dtype, device=device),
+        v_pages=torch.empty((nv, Hkv, page, d), dtype=dtype, device=device),
+        k_table=torch.full((seqs, max_pages), -1, **i32),
+        v_table=torch.full((seqs, max_pages), -1, **i32),
+        lens=torch.zeros(seqs, **i32),
+        g_pages=torch.empty((num_k_pages, Hq, page), dtype=torch.float32, device=device)
+        if fox else None,
+        k_ref=torch.zeros(num_k_pages, **i32), v_ref=torch.zeros(nv, **i32))
+
+
+def _paged_devices(named, device):
+    for t, n in named:
+        if not t.is_cuda:
+            raise TypeError("%s must be a CUDA tensor" % n)
+        if t.device != device:
+            raise ValueError("%s must be on %s" % (n, device))
+
+
+def _paged_cache(cache, counts=False, Hq=None, on_gpu=True):
+    """Checks the cache's tensors and returns its C form. Shapes and dtypes are checked before
+    devices (on_gpu=False: the caller checks those with _paged_devices), so that every size
+    error is raised before any call."""
+    torch = _torch()
+    if not isinstance(cache, PathPagedCache):
+        raise TypeError("cache must be a PathPagedCache")
+    kp, vp, kt = cache.k_pages, cache.v_pages, cache.k_table
+    named = [(kp, "k_pages"), (vp, "v_pages"), (kt, "k_table"), (cache.v_table, "v_table"),
+             (cache.lens, "lens")]
+    if counts or cache.k_ref is not None or cache.v_ref is not None:
+        named += [(cache.k_ref, "k_ref"), (cache.v_ref, "v_ref")]
+    if cache.g_pages is not None:
+        named.append((cache.g_pages, "g_pages"))
+    for t, n in named:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a tensor" % n)
+    if kp.dim() != 4 or vp.dim() != 4 or kp.shape[1:] != vp.shape[1:]:
+        raise ValueError("k_pages and v_pages must be (pages, Hkv, page, d) of equal pages")
+    if vp.dtype != kp.dtype:
+        raise TypeError("v_pages must be %s, got %s" % (kp.dtype, vp.dtype))
+    dt = _dtype_code(kp)
+    nk, Hkv, page, d = kp.shape
+    if kt.dim() != 2 or cache.v_table.shape != kt.shape:
+        raise ValueError("k_table and v_table must be (seqs, max_pages) of equal shape")
+    seqs, max_pages = kt.shape
+    if cache.lens.shape != (seqs,):
+        raise ValueError("lens must be (seqs,)")
+    for t, n in named[2:]:
+        want = torch.float32 if n == "g_pages" else torch.int32
+        if t.dtype != want:
+            raise TypeError("%s must be %s, got %s" % (n, want, t.dtype))
+    if len(named) > 5 and named[5][1] == "k_ref":
+        if cache.k_ref.shape != (nk,) or cache.v_ref.shape != (vp.shape[0],):
+            raise ValueError("k_ref and v_ref must hold one count per page")
+    if cache.g_pages is not None:
+        if cache.g_pages.dim() != 3 or cache.g_pages.shape[0] != nk or \
+                cache.g_pages.shape[2] != page or (Hq is not None and cache.g_pages.shape[1] != Hq):
+            raise ValueError("g_pages must be (K pages, Hq, page)")
+        Hq = cache.g_pages.shape[1]
+    for t, n in named:
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % n)
+    if on_gpu:
+        _paged_devices(named, kp.device)
+    ptr = [t.data_ptr() if t is not None else None
+           for t in (kp, vp, cache.g_pages, kt, cache.v_table, cache.k_ref, cache.v_ref,
+                     cache.lens)]
+    return _CPagedCache(*ptr, seqs, max_pages, page, nk, vp.shape[0],
+                        Hkv if Hq is None else Hq, Hkv, d, dt)
+
+
+def path_paged_workspace_bytes(cache, num_tokens=0, max_chunk=0, Hq=None):
+    """Workspace bytes of every call on `cache` with up to num_tokens new tokens in all and
+    max_chunk per sequence (0: the page calls alone). Hq: query heads, where the cache has no
+    g_pages to tell (default: the key heads)."""
+    c = _paged_cache(cache, Hq=Hq)
+    return int(_load().path_paged_workspace_bytes(ctypes.byref(c), int(num_tokens),
+                                                  int(max_chunk)))
+
+
+def new_paged_workspace(cache, num_tokens=0, max_chunk=0, Hq=None):
+    """A workspace of path_paged_workspace_bytes, its status word cleared."""
+    torch = _torch()
+    n = path_paged_workspace_bytes(cache, num_tokens, max_chunk, Hq)
+    if n == 0:
+        raise PathError(ERR_SHAPE, "path_paged_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=cache.k_pages.device)
+    ws[:256].zero_()
+    return ws
+
+
+def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, scale, out,
+                  workspace, stream):
+    torch = _torch()
+    kp = cache.k_pages if isinstance(cache, PathPagedCache) else None
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (w, "w"), (beta, "beta"), (cu_tokens, "cu_tokens"),
+                 (kp, "cache.k_pages")) + (((log_f, "log_f"),) if log_f is not None else ()):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a tensor" % n)
+    if q.dim() != 3:
+        raise ValueError("q must be (tokens, Hq, d)")
+    if kp.dim() != 4:
+        raise ValueError("k_pages must be (pages, Hkv, page, d)")
+    N, Hq, d = q.shape
+    Hkv = kp.shape[1]
+    new_out = out is None
+    if new_out:
+        out = torch.empty((N, Hq, d), dtype=q.dtype, device="meta")
+    f32, dt, dev = torch.float32, kp.dtype, kp.device
+    c = _paged_cache(cache, Hq=Hq, on_gpu=False)
+    row = [(q, "q", (N, Hq, d), dt), (k, "k", (N, Hkv, d), dt), (v, "v", (N, Hkv, d), dt),
+           (w, "w", (N, Hkv, d), dt), (beta, "beta", (N, Hkv), f32),
+           (log_f, "log_f", (N, Hq), f32), (out, "out", (N, Hq, d), dt),
+           (cu_tokens, "cu_tokens", (c.seqs + 1,), torch.int32)]
+    st = []
+    for t, n, shape, want in row:
+        if t is None:
+            st += [0, 0]
+            continue
+        if t.dtype != want:
+            raise TypeError("%s must be %s, got %s" % (n, want, t.dtype))
+        if tuple(t.shape) != shape:
+            raise ValueError("%s must have shape %s, got %s" % (n, shape, tuple(t.shape)))
+        s = t.stride()
+        if t.dim() == 3 and s[2] != 1 or n == "cu_tokens" and s[0] != 1:
+            raise ValueError("the last axis of %s must be contiguous" % n)
+        if n != "cu_tokens":  # the stride of an axis of one element says nothing
+            st += [s[0] if t.shape[0] > 1 else 0, s[1] if t.shape[1] > 1 else 0]
+    if d != c.d:
+        raise ValueError("q has head size %d, the cache %d" % (d, c.d))
+    if out.numel() and (N > 1 and out.stride(0) == 0 or Hq > 1 and out.stride(1) == 0):
+        raise ValueError("out must not repeat its own memory")
+    _paged_devices([(t, n) for t, n in [(getattr(cache, f.name), f.name)
+                                        for f in dataclasses.fields(cache)] +
+                    [(r[0], r[1]) for r in row if not (new_out and r[1] == "out")]
+                    if t is not None], dev)
+    strides = _CPagedStrides(*[(ctypes.c_int64 * 2)(*st[i:i + 2]) for i in range(0, 14, 2)])
+    gate = () if log_f is None else (log_f.data_ptr(),)
+    # what is allocated here belongs to the stream that the call runs on
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        if new_out:
+            out = torch.empty((N, Hq, d), dtype=dt, device=dev)
+        if workspace is None and N > 0 and c.seqs > 0:
+            workspace = new_paged_workspace(cache, N, max_chunk, Hq)
+        _check(getattr(_load(), name)(
+            ctypes.byref(c), q.data_ptr(), k.data_ptr(), v.data_ptr(), w.data_ptr(),
+            beta.data_ptr(), *gate, cu_tokens.data_ptr(), N, int(max_chunk), _scale(scale, d),
+            out.data_ptr(), ctypes.byref(strides), _ptr(workspace),
+            0 if workspace is None else workspace.numel(), _stream(stream, dev)), name)
+    return out
+
+
+def path_paged_extend(q, k, v, w, beta, cu_tokens, cache, max_chunk, scale=None, out=None,
+                      workspace=None, stream=None):
+    """Attention of every sequence's new tokens over its paged cache, the cached keys' update
+    and the new tokens' entry into the cache; returns out (tokens, Hq, d). q: (tokens, Hq, d);
+    k, v, w: (tokens, Hkv, d); beta: (tokens, Hkv); any strides with a contiguous last axis.
+    cu_tokens: (seqs + 1) int32, where each sequence's tokens begin; max_chunk: the most of one
+    sequence. The pages must be mapped (path_paged_reserve); the caller advances cache.lens."""
+    return _paged_extend("path_paged_extend", q, k, v, w, beta, None, cu_tokens, cache, max_chunk,
+                         scale, out, workspace, stream)
+
+
+def path_fox_paged_extend(q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, scale=None,
+                          out=None, workspace=None, stream=None):
+    """path_paged_extend with the forget gates of PaTH-FoX: log_f (tokens, Hq) fp32, and
+    cache.g_pages advanced like the keys."""
+    torch = _torch()
+    if not isinstance(log_f, torch.Tensor):
+        raise TypeError("log_f must be a tensor")
+    if isinstance(cache, PathPagedCache) and cache.g_pages is None:
+        raise TypeError("cache.g_pages must be a tensor")
+    return _paged_extend("path_fox_paged_extend", q, k, v, w, beta, log_f, cu_tokens, cache,
+                         max_chunk, scale, out, workspace, stream)
+
+
+def _paged_call(name, cache, workspace, stream, *args):
+    torch = _torch()
+    c = _paged_cache(cache, counts=True)
+    dev = cache.k_pages.device
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        if workspace is None:
+            workspace = new_paged_workspace(cache)
+        _check(getattr(_load(), name)(ctypes.byref(c), *args, workspace.data_ptr(),
+                                      workspace.numel(), _stream(stream, dev)), name)
+
+
+def _rows(rows):
+    rows = [int(r) for r in rows]
+    return (ctypes.c_int * max(len(rows), 1))(*rows), len(rows)
+
+
+def path_paged_reserve(extra, cache, workspace=None, stream=None):
+    """Maps the lowest free pages so that every sequence can hold lens + extra tokens (extra:
+    (seqs) int32 on the device). Nothing changes if the pages run out: the workspace's status
+    word says so (path_check_workspace)."""
+    torch = _torch()
+    if not isinstance(extra, torch.Tensor):
+        raise TypeError("extra must be a tensor")
+    if extra.dtype != torch.int32:
+        raise TypeError("extra must be torch.int32, got %s" % extra.dtype)
+    if isinstance(cache, PathPagedCache) and tuple(extra.shape) != tuple(cache.lens.shape):
+        raise ValueError("extra must be (seqs,)")
+    _cuda_tensor(extra, "extra")
+    if isinstance(cache, PathPagedCache) and extra.device != cache.k_pages.device:
+        raise ValueError("extra must be on %s" % cache.k_pages.device)
+    _paged_call("path_paged_reserve", cache, workspace, stream, extra.data_ptr())
+
+
+def path_paged_fork(src, dst, cache, workspace=None, stream=None):
+    """Rows dst (empty) become copies of rows src (lists of ints): keys copied, full value
+    pages shared, a value page that still fills copied."""
+    (a, n), (b, m) = _rows(src), _rows(dst)
+    if n != m:
+        raise ValueError("src and dst must be equally long")
+    _paged_call("path_paged_fork", cache, workspace, stream, a, b, n)
+
+
+def path_paged_free(rows, cache, workspace=None, stream=None):
+    """Empties rows (a list of ints): their pages go back, their lengths become 0."""
+    a, n = _rows(rows)
+    _paged_call("path_paged_free", cache, workspace, stream, a, n)
+
+
+def path_paged_compact(cache, workspace=None, stream=None):
+    """Moves the pages in use to the front of each pool; the tables follow."""
+    _paged_call("path_paged_compact", cache, workspace, stream)

@@ -489,7 +489,10 @@ path_status path_check_workspace(void *ws, void *stream) {
     if (cudaMemcpy(&word, ws, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
         return PATH_ERR_CUDA;
     if (word != 0 && cudaMemset(ws, 0, sizeof(word)) != cudaSuccess) return PATH_ERR_CUDA;
-    return word == 0 ? PATH_OK : (word == kStatusTimeout ? PATH_ERR_TIMEOUT : PATH_ERR_CUDA);
+    if (word == 0) return PATH_OK;
+    if (word == PATH_ERR_TIMEOUT || word == PATH_ERR_CAPACITY || word == PATH_ERR_CACHE)
+        return static_cast<path_status>(word);
+    return PATH_ERR_CUDA;
 }
 
 const char *path_status_string(int status) {
@@ -500,10 +503,11 @@ const char *path_status_string(int status) {
         case PATH_ERR_DTYPE: return "PATH_ERR_DTYPE: unsupported dtype";
         case PATH_ERR_ALIGN: return "PATH_ERR_ALIGN: misaligned pointer";
         case PATH_ERR_WORKSPACE: return "PATH_ERR_WORKSPACE: workspace too small";
-        case PATH_ERR_CAPACITY: return "PATH_ERR_CAPACITY: decode cache is full";
+        case PATH_ERR_CAPACITY: return "PATH_ERR_CAPACITY: the decode cache is full or the pages ran out";
         case PATH_ERR_TIMEOUT: return "PATH_ERR_TIMEOUT: a kernel gave up a bounded wait";
         case PATH_ERR_CUDA: return "PATH_ERR_CUDA: a CUDA call failed";
         case PATH_ERR_ARG: return "PATH_ERR_ARG: scalar argument out of range";
+        case PATH_ERR_CACHE: return "PATH_ERR_CACHE: a paged cache's lengths or pages do not fit";
         default: return "PATH_ERR_UNKNOWN";
     }
 }

@@ -53,7 +53,9 @@ typedef enum {
     PATH_ERR_CAPACITY = 6,  /* decode: cache_len + 1 > cache_cap */
     PATH_ERR_TIMEOUT = 7,   /* a kernel gave up a bounded wait (see path_check_workspace) */
     PATH_ERR_CUDA = 8,      /* a CUDA call failed */
-    PATH_ERR_ARG = 9        /* a scalar argument is out of range (e.g. non-finite scale) */
+    PATH_ERR_ARG = 9,       /* a scalar argument is out of range (e.g. non-finite scale) */
+    PATH_ERR_CACHE = 10     /* paged cache: lengths or page numbers on the device do not fit it
+                               (see path_check_workspace) */
 } path_status;
 
 typedef enum { PATH_F32 = 0, PATH_BF16 = 1 } path_dtype;
@@ -303,10 +305,135 @@ path_status path_wbeta_produce(const void *x, const void *w_down, const void *w_
                                int D, int R, int H, int d, int dtype, void *ws, size_t ws_bytes,
                                void *stream);
 
+/* ------------------------------------------------------------------------------------------
+ * A paged cache: sequences of different lengths whose keys and values lie in pages of `page`
+ * tokens, and steps that take any number of new tokens per sequence. (Review "거리에서 경로로,
+ * PaTH Attention" §9 and technical summary "技術要約: PaTH Attention" §3 "推論" give the
+ * scheme for one token: cached keys are updated in place; the pages do not treat paging.)
+ *
+ *   k_pages : (num_k_pages, Hkv, page, d) dtype, v_pages : (num_v_pages, Hkv, page, d) dtype
+ *   g_pages : (num_k_pages, Hq, page) fp32, PaTH-FoX gate sums per key and query head; NULL
+ *             where no gates are used
+ *   k_table, v_table : (seqs, max_pages) int32: the page of each slot of `page` tokens of a
+ *             sequence; -1 where there is none
+ *   k_ref, v_ref : (num_k_pages), (num_v_pages) int32: how many table entries hold a page; 0
+ *             is a free page. Only the page calls (reserve, fork, free, compact) need them.
+ *   lens    : (seqs) int32 cached tokens. Sequence s holds its token i in slot i / page.
+ * Hq query heads share Hkv key heads, Hq / Hkv to each (query head h uses key head
+ * h / (Hq / Hkv)); w and beta go with the key heads, gates with the query heads.
+ * d = 64 or 128; page = 16, 32, 64, 128 or 256; max_pages * page <= PATH_MAX_LEN.
+ * A page of k_pages belongs to one sequence (every step rewrites its keys); a full page of
+ * v_pages may belong to several. Tables, counts and lengths live on the device and are read
+ * by the kernels, so calls can be captured in a graph and replayed while they change.
+ *
+ * What the device finds wrong (a length or chunk that does not fit the cache or the step, a
+ * page number outside the pool) sets the status word of the workspace, which keeps the first
+ * such code until path_check_workspace reads it: PATH_ERR_CACHE, or PATH_ERR_CAPACITY where
+ * pages run out. The first 256 bytes of a workspace must be zero before its first use. A
+ * workspace serves one call at a time (calls ordered on a stream, captured or not).
+ */
+typedef struct {
+    void *k_pages, *v_pages;
+    float *g_pages;
+    int *k_table, *v_table, *k_ref, *v_ref, *lens;
+    int seqs, max_pages, page, num_k_pages, num_v_pages, Hq, Hkv, d, dtype;
+} path_paged_cache;
+
+/* Element strides {token, head} of a step's tensors; the d values of a head are contiguous.
+ * Rows of q, k, v, w and out must start on 16-byte boundaries. */
+typedef struct {
+    int64_t q[2], k[2], v[2], w[2], beta[2], log_f[2], out[2];
+} path_paged_strides;
+
+/*
+ * Workspace bytes for every paged call on `cache` with up to num_tokens new tokens in all and
+ * max_chunk per sequence (0, 0: the page calls alone). No pointer of `cache` is looked at.
+ * Returns 0 for invalid sizes.
+ */
+size_t path_paged_workspace_bytes(const path_paged_cache *cache, int num_tokens, int max_chunk);
+
+/*
+ * Attention of new tokens over the paged cache, and the cache's update. Sequence s brings the
+ * tokens cu_tokens[s] .. cu_tokens[s + 1] - 1 (T of them, none is allowed) behind its
+ * n = lens[s] cached ones. With H_i = I - beta_i w_i w_i^T over its new tokens:
+ *   1. out_i = softmax over the cached keys j (logit scale * k_j^T (H_1 ... H_i) q_i) and the
+ *      new keys j <= i (logit scale * k_j^T (H_{j+1} ... H_i) q_i) of v_j;
+ *   2. cached keys:  k_j <- (H_1 ... H_T)^T k_j in place (rounded to dtype);
+ *   3. new keys (H_{j+1} ... H_T)^T k_j and new values are written at positions n .. n + T - 1.
+ * The same as T calls of one token each but for the roundings of the cached keys between them.
+ *   q, out : (num_tokens, Hq, d) dtype; k, v, w : (num_tokens, Hkv, d) dtype; beta :
+ *            (num_tokens, Hkv) fp32; strides NULL for packed tensors
+ *   cu_tokens : (seqs + 1) int32 on the device, from 0, not falling; tokens at or past
+ *            cu_tokens[seqs] are not read and their out rows are left as they are
+ *   max_chunk : the most new tokens of a sequence, 1 .. num_tokens (a sequence with more is
+ *            left out, with PATH_ERR_CACHE)
+ *   ws     : path_paged_workspace_bytes(cache, num_tokens, max_chunk) bytes
+ * The pages of positions 0 .. n + T - 1 must be in the tables (path_paged_reserve). lens is
+ * not changed: the caller adds T. A sequence whose lengths do not fit is left as it was, its
+ * out rows too; positions on a page outside the pool count as absent. No new token anywhere
+ * (num_tokens = 0) or no sequence is valid and launches nothing.
+ */
+path_status path_paged_extend(const path_paged_cache *cache, const void *q, const void *k,
+                              const void *v, const void *w, const float *beta,
+                              const int *cu_tokens, int num_tokens, int max_chunk, float scale,
+                              void *out, const path_paged_strides *strides, void *ws,
+                              size_t ws_bytes, void *stream);
+
+/*
+ * path_paged_extend with the forget gates of PaTH-FoX (review §4; technical summary §2 "拡張:
+ * PaTH-FoX"): the logit of key j at query i gains sum_{s=j+1..i} log f_s, over cached and new
+ * tokens. g_pages holds every cached key's sum up to the last cached token; it is advanced
+ * like the keys (cached: + the whole chunk's sum; new key j: the sum behind j).
+ *   log_f : (num_tokens, Hq) fp32, any finite value
+ */
+path_status path_fox_paged_extend(const path_paged_cache *cache, const void *q, const void *k,
+                                  const void *v, const void *w, const float *beta,
+                                  const float *log_f, const int *cu_tokens, int num_tokens,
+                                  int max_chunk, float scale, void *out,
+                                  const path_paged_strides *strides, void *ws, size_t ws_bytes,
+                                  void *stream);
+
+/*
+ * Maps free pages so that sequence s can hold lens[s] + extra[s] tokens (extra: (seqs) int32
+ * on the device, >= 0): every missing slot below that, in the order of the sequences and
+ * slots, takes the lowest free page of the key pool and of the value pool. If either pool has
+ * too few, or a sequence would pass max_pages, nothing changes and the status word is
+ * PATH_ERR_CAPACITY.
+ */
+path_status path_paged_reserve(const path_paged_cache *cache, const int *extra, void *ws,
+                               size_t ws_bytes, void *stream);
+
+/*
+ * Sequence dst[i] becomes a copy of src[i], for i < pairs <= 1024 (host lists). Keys and gate
+ * sums are copied to the lowest free pages; full value pages are shared and counted, and a last
+ * value page that still fills is copied. Every dst row must be empty (no page, length 0), dst
+ * rows differ from each other and from every src row (PATH_ERR_ARG otherwise); a source may
+ * appear more than once. If pages run out (PATH_ERR_CAPACITY in the status word) or a row is not
+ * as it must be (PATH_ERR_CACHE), nothing changes.
+ */
+path_status path_paged_fork(const path_paged_cache *cache, const int *src, const int *dst, int pairs,
+                            void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Empties the given rows (host list of at most 1024, none twice): their pages' counts fall by
+ * one, their table entries become -1 and their lengths 0.
+ */
+path_status path_paged_free(const path_paged_cache *cache, const int *rows, int num_rows, void *ws,
+                            size_t ws_bytes, void *stream);
+
+/*
+ * Moves the pages in use to the front of each pool, so that its last pages are free: with L
+ * pages in use, the k-th free page below L takes the contents and the count of the k-th used
+ * page at or above L, and the tables follow. Pages below L that are in use stay.
+ */
+path_status path_paged_compact(const path_paged_cache *cache, void *ws, size_t ws_bytes,
+                               void *stream);
+
 /*
  * Waits for `stream`, then reads and clears the status word that kernels of
- * earlier calls on this workspace wrote. Returns PATH_OK, PATH_ERR_TIMEOUT or
- * PATH_ERR_CUDA (if the synchronisation or the read failed).
+ * earlier calls on this workspace wrote. Returns PATH_OK, PATH_ERR_TIMEOUT, for the
+ * paged calls PATH_ERR_CACHE or PATH_ERR_CAPACITY, or PATH_ERR_CUDA (if the
+ * synchronisation or the read failed).
  */
 path_status path_check_workspace(void *ws, void *stream);
 
