@@ -1,5 +1,6 @@
 // Host side of the paged-cache entry points of include/path_attn.h: argument checks
 // (synchronous, before any launch), workspace sizes and kernel dispatch.
+#include <climits>
 #include <cmath>
 
 #include "paged.cuh"
@@ -12,7 +13,9 @@ bool decode_takes(int G);
 size_t decode_part_bytes(const Cache &c, int d);
 cudaError_t launch_decode(const Step &a, int d, bool bf16, float *part, cudaStream_t stream);
 size_t f32_ws_bytes(const Cache &c, int N, int d, bool fox);
-cudaError_t launch_f32(const Step &a, int d, bool bf16, void *ws, cudaStream_t stream);
+cudaError_t launch_f32(const Step &a, int d, void *ws, cudaStream_t stream);
+size_t tc_ws_bytes(const Cache &c, int N, int max_chunk, int d, bool fox);
+cudaError_t launch_tc(const Step &a, int d, void *ws, uint64_t limit_ns, cudaStream_t stream);
 size_t pages_ws_bytes(const Cache &c);
 cudaError_t launch_reserve(const Cache &c, const int *extra, void *ws, cudaStream_t stream);
 cudaError_t launch_fork(const Cache &c, const Rows &src, const Rows &dst, int row_bytes, void *ws,
@@ -28,6 +31,8 @@ using namespace path;
 using paged::Cache;
 using paged::Rows;
 
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bounded waits of the tensor-core kernels
+
 bool is_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Sizes of a cache (no pointer is looked at): the workspace sizes go by them alone.
@@ -40,6 +45,9 @@ path_status check_cache_sizes(const path_paged_cache *p) {
         p->num_v_pages < 0 || p->Hq < 1 || p->Hkv < 1 || p->Hq > PATH_MAX_HEADS || p->Hq % p->Hkv != 0)
         return PATH_ERR_SHAPE;
     if ((long long)p->max_pages * p->page > PATH_MAX_LEN) return PATH_ERR_SHAPE;
+    // a page of one head is one index of the kernels' tensor maps
+    if ((long long)p->num_k_pages * p->Hkv > INT_MAX || (long long)p->num_v_pages * p->Hkv > INT_MAX)
+        return PATH_ERR_SHAPE;
     return PATH_OK;
 }
 
@@ -76,12 +84,13 @@ path_status check_workspace(const void *ws, size_t bytes, size_t need) {
 }
 
 // The step's kernels: one token per sequence at most takes the one-pass kernel where it has
-// the query heads per key head, everything else the block kernels.
+// the query heads per key head, everything else the block kernels of the type.
 bool one_pass(const Cache &c, int max_chunk) { return max_chunk == 1 && paged::decode_takes(c.G); }
 
 size_t step_ws_bytes(const path_paged_cache *p, int N, int max_chunk, bool fox) {
     const Cache c = to_cache(p);
     if (one_pass(c, max_chunk)) return 256 + align256(paged::decode_part_bytes(c, p->d));
+    if (p->dtype == PATH_BF16) return paged::tc_ws_bytes(c, N, max_chunk, p->d, fox);
     return paged::f32_ws_bytes(c, N, p->d, fox);
 }
 
@@ -137,7 +146,8 @@ path_status extend(const path_paged_cache *p, const void *q, const void *k, cons
     if (one_pass(c, max_chunk))
         return cuda_status(paged::launch_decode(a, p->d, p->dtype == PATH_BF16,
                                                 reinterpret_cast<float *>(static_cast<char *>(ws) + 256), s));
-    return cuda_status(paged::launch_f32(a, p->d, p->dtype == PATH_BF16, ws, s));
+    if (p->dtype == PATH_BF16) return cuda_status(paged::launch_tc(a, p->d, ws, kWaitLimitNs, s));
+    return cuda_status(paged::launch_f32(a, p->d, ws, s));
 }
 
 // A list of sequence rows from the host: in range, none twice.

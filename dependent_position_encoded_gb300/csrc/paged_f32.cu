@@ -126,34 +126,25 @@ __device__ __forceinline__ void load_rows(float *dst, const float *src) {
     }
 }
 
-// four consecutive elements to and from fp32
 __device__ __forceinline__ float4 get4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 get4(const __nv_bfloat16 *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    const float2 x = unpack_bf16x2(u.x), y = unpack_bf16x2(u.y);
-    return make_float4(x.x, x.y, y.x, y.y);
-}
 __device__ __forceinline__ void set4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
-__device__ __forceinline__ void set4(__nv_bfloat16 *p, float4 v) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
 
 // tokens i0 .. of one head (rows past `rows` zero) into D / 64 shared tiles
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void load_tokens(float *dst, const void *src, Stride st, long long first,
                                             int head, int rows) {
     for (int e = threadIdx.x; e < kC * D / 4; e += kThr) {
         const int r = 4 * e / D, c = 4 * e % D;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < rows)
-            x = get4(static_cast<const T *>(src) + (first + r) * st.tok + head * st.head + c);
+            x = get4(static_cast<const float *>(src) + (first + r) * st.tok + head * st.head + c);
         *reinterpret_cast<float4 *>(dst + (c >> 6) * TILE + r * LD + (c & 63)) = x;
     }
 }
 
 // 64 cached positions from j0 of one key head into shared tiles; positions at or past n and
 // those of bad pages are zero. ids: page numbers of the positions' slots from slot0.
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void load_cached(float *dst, const void *pages, const Cache &c, const int *ids,
                                             int slot0, int h, int j0, int n) {
     for (int e = threadIdx.x; e < kC * D / 4; e += kThr) {
@@ -161,7 +152,7 @@ __device__ __forceinline__ void load_cached(float *dst, const void *pages, const
         const int id = j < n ? ids[(j >> c.page_shift) - slot0] : -1;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (id >= 0)
-            x = get4(static_cast<const T *>(pages) +
+            x = get4(static_cast<const float *>(pages) +
                      ((((size_t)id * c.Hkv + h) << c.page_shift) + (j & (c.page - 1))) * D + col);
         *reinterpret_cast<float4 *>(dst + (col >> 6) * TILE + r * LD + (col & 63)) = x;
     }
@@ -235,7 +226,7 @@ template <int D> constexpr size_t kPart = (size_t)kC * (D + 2);
 template <int D>
 constexpr size_t prep_smem() { return ((size_t)(4 * (D / 64) + 4) * TILE + 6 * kC) * 4 + 2 * kC * 8; }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y) {
     constexpr int NH = D / 64;
     extern __shared__ float sm[];
@@ -250,8 +241,8 @@ __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y
     if (!block_of(a, slot, b, c, s)) return;
     const int i0 = c * kC, rows = min(kC, s.T - i0);
     const long long first = s.first + i0;
-    load_tokens<T, D>(W, a.w, a.sw, first, h, rows);
-    load_tokens<T, D>(K, a.k, a.sk, first, h, rows);
+    load_tokens<D>(W, a.w, a.sw, first, h, rows);
+    load_tokens<D>(K, a.k, a.sk, first, h, rows);
     if (tid < kC) beta[tid] = tid < rows ? a.beta[(first + tid) * a.sb.tok + h * a.sb.head] : 0.f;
     __syncthreads();
     Acc c0;
@@ -328,12 +319,12 @@ __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y
     }
     __syncthreads();
     float *V = U;
-    load_tokens<T, D>(V, a.v, a.sv, first, h, rows);
+    load_tokens<D>(V, a.v, a.sv, first, h, rows);
     for (int g = 0; g < a.c.G; ++g) {
         const int hq = h * a.c.G + g;
         const size_t bq = (size_t)slot * a.c.Hq + hq;
         __syncthreads();
-        load_tokens<T, D>(Q, a.q, a.sq, first, hq, rows);
+        load_tokens<D>(Q, a.q, a.sq, first, hq, rows);
         if (a.log_f != nullptr && tid == 0) {
             double t = 0.0;
             for (int i = 0; i < kC; ++i) {
@@ -412,7 +403,7 @@ constexpr size_t scan_smem() {
     return ((size_t)(3 * (D / 64) + (D / 64) * (D / 64) + 1) * TILE + 5 * kC) * 4;
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr) f32_scan_kernel(const Step a, const Ws y) {
     constexpr int NH = D / 64;
     extern __shared__ float sm[];
@@ -447,7 +438,7 @@ __global__ void __launch_bounds__(kThr) f32_scan_kernel(const Step a, const Ws y
         const size_t kh = (size_t)ks * a.c.Hkv + h;
         __syncthreads();
         load_rows<D>(K, y.kt + kh * kC * D);
-        load_tokens<T, D>(V, a.v, a.sv, (long long)s.first + kb * kC, h, kC);
+        load_tokens<D>(V, a.v, a.sv, (long long)s.first + kb * kC, h, kC);
 #pragma unroll
         for (int x = 0; x < NH; ++x) load_rows<D>(P + x * NH * TILE, y.pb + (kh * D + 64 * x) * D);
         if (a.log_f != nullptr && tid < kC) gt[tid] = y.gt[((size_t)ks * a.c.Hq + hq) * kC + tid];
@@ -506,7 +497,7 @@ __device__ __forceinline__ void split_range(int n, int splits, int sp, int &j0, 
 template <int D>
 constexpr size_t cached_smem() { return ((size_t)(3 * (D / 64) + 1) * TILE + 4 * kC) * 4 + 16 * 4; }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr) f32_cached_kernel(const Step a, const Ws y) {
     constexpr int NH = D / 64;
     extern __shared__ float sm[];
@@ -540,8 +531,8 @@ __global__ void __launch_bounds__(kThr) f32_cached_kernel(const Step a, const Ws
             vid[tid] = page_of(a, a.c.v_table, b, slot0 + tid, a.c.nv);
         }
         __syncthreads();
-        load_cached<T, D>(K, a.c.k_pages, a.c, kid, slot0, h, j, j1);
-        load_cached<T, D>(V, a.c.v_pages, a.c, vid, slot0, h, j, j1);
+        load_cached<D>(K, a.c.k_pages, a.c, kid, slot0, h, j, j1);
+        load_cached<D>(V, a.c.v_pages, a.c, vid, slot0, h, j, j1);
         if (tid < kC) {
             // the key's gate sum; -inf where there is no such key
             const int jj = j + tid, sl = (jj >> a.c.page_shift) - slot0;
@@ -574,7 +565,7 @@ __global__ void __launch_bounds__(kThr) f32_cached_kernel(const Step a, const Ws
 }
 
 // ---------------------------------------------------------------- combine
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr) f32_combine_kernel(const Step a, const Ws y) {
     const int slot = blockIdx.x, hq = blockIdx.y;
     int b, c;
@@ -596,8 +587,7 @@ __global__ void __launch_bounds__(kThr) f32_combine_kernel(const Step a, const W
             Ls = fmaf(p[kC * D + kC + r], f, Ls);
             O = fmaf(p[r * D + q], f, O);
         }
-        static_cast<T *>(a.out)[(long long)(s.first + c * kC + r) * a.so.tok + hq * a.so.head + q] =
-            Elt<T>::from_f(O / Ls);
+        static_cast<float *>(a.out)[(long long)(s.first + c * kC + r) * a.so.tok + hq * a.so.head + q] = O / Ls;
     }
 }
 
@@ -606,7 +596,7 @@ template <int D>
 constexpr size_t carry_smem() { return (size_t)(D / 64 + (D / 64) * (D / 64)) * TILE * 4; }
 
 // Items of a key head: the slots, then D / 64 row tiles of the identity per sequence.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr) f32_carry_kernel(const Step a, const Ws y, int nslots) {
     constexpr int NH = D / 64;
     extern __shared__ float sm[];
@@ -663,11 +653,11 @@ __global__ void __launch_bounds__(kThr) f32_carry_kernel(const Step a, const Ws 
         const int sl = pos >> a.c.page_shift, off = pos & (a.c.page - 1);
         const int kid = page_of(a, a.c.k_table, b, sl, a.c.nk), vid = page_of(a, a.c.v_table, b, sl, a.c.nv);
         if (kid >= 0)
-            set4(static_cast<T *>(a.c.k_pages) + ((((size_t)kid * a.c.Hkv + h) << a.c.page_shift) + off) * D + q,
+            set4(static_cast<float *>(a.c.k_pages) + ((((size_t)kid * a.c.Hkv + h) << a.c.page_shift) + off) * D + q,
                  *reinterpret_cast<const float4 *>(Y + (q >> 6) * TILE + r * LD + (q & 63)));
         if (vid >= 0)
-            set4(static_cast<T *>(a.c.v_pages) + ((((size_t)vid * a.c.Hkv + h) << a.c.page_shift) + off) * D + q,
-                 get4(static_cast<const T *>(a.v) + (long long)(s.first + c * kC + r) * a.sv.tok +
+            set4(static_cast<float *>(a.c.v_pages) + ((((size_t)vid * a.c.Hkv + h) << a.c.page_shift) + off) * D + q,
+                 get4(static_cast<const float *>(a.v) + (long long)(s.first + c * kC + r) * a.sv.tok +
                       h * a.sv.head + q));
     }
     if (a.log_f != nullptr)
@@ -687,7 +677,7 @@ constexpr size_t transform_smem() { return (size_t)(D / 64 + (D / 64) * (D / 64)
 
 // grid (parts, key heads, sequences): a CTA keeps P in shared memory and takes every parts-th
 // tile of 64 cached keys.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThr) f32_transform_kernel(const Step a, const Ws y) {
     constexpr int NH = D / 64;
     extern __shared__ float sm[];
@@ -705,7 +695,7 @@ __global__ void __launch_bounds__(kThr) f32_transform_kernel(const Step a, const
         __syncthreads();
         if (tid <= last - slot0) kid[tid] = page_of(a, a.c.k_table, b, slot0 + tid, a.c.nk);
         __syncthreads();
-        load_cached<T, D>(K, a.c.k_pages, a.c, kid, slot0, h, j, jend);
+        load_cached<D>(K, a.c.k_pages, a.c, kid, slot0, h, j, jend);
         __syncthreads();
 #pragma unroll
         for (int x1 = 0; x1 < NH; ++x1) {
@@ -718,7 +708,7 @@ __global__ void __launch_bounds__(kThr) f32_transform_kernel(const Step a, const
                 const int jj = j + ty + 16 * i;
                 const int id = jj < jend ? kid[(jj >> a.c.page_shift) - slot0] : -1;
                 if (id >= 0)
-                    set4(static_cast<T *>(a.c.k_pages) + ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) +
+                    set4(static_cast<float *>(a.c.k_pages) + ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) +
                                                           (jj & (a.c.page - 1))) * D + 64 * x1 + 4 * tx,
                          make_float4(c0[i][0], c0[i][1], c0[i][2], c0[i][3]));
             }
@@ -741,26 +731,26 @@ cudaError_t big_smem(K kern, size_t bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_d(const Step &a, const Ws &y, cudaStream_t stream) {
     const int nslots = slots_of(a.N, a.c.seqs), Hq = a.c.Hq, Hkv = a.c.Hkv;
     cudaError_t e;
-    if ((e = big_smem(f32_prep_kernel<T, D>, prep_smem<D>())) != cudaSuccess ||
-        (e = big_smem(f32_scan_kernel<T, D>, scan_smem<D>())) != cudaSuccess ||
-        (e = big_smem(f32_cached_kernel<T, D>, cached_smem<D>())) != cudaSuccess ||
-        (e = big_smem(f32_carry_kernel<T, D>, carry_smem<D>())) != cudaSuccess ||
-        (e = big_smem(f32_transform_kernel<T, D>, transform_smem<D>())) != cudaSuccess)
+    if ((e = big_smem(f32_prep_kernel<D>, prep_smem<D>())) != cudaSuccess ||
+        (e = big_smem(f32_scan_kernel<D>, scan_smem<D>())) != cudaSuccess ||
+        (e = big_smem(f32_cached_kernel<D>, cached_smem<D>())) != cudaSuccess ||
+        (e = big_smem(f32_carry_kernel<D>, carry_smem<D>())) != cudaSuccess ||
+        (e = big_smem(f32_transform_kernel<D>, transform_smem<D>())) != cudaSuccess)
         return e;
-    f32_prep_kernel<T, D><<<dim3(nslots, Hkv), kThr, prep_smem<D>(), stream>>>(a, y);
+    f32_prep_kernel<D><<<dim3(nslots, Hkv), kThr, prep_smem<D>(), stream>>>(a, y);
     if (a.max_chunk > kC)
-        f32_scan_kernel<T, D><<<dim3(nslots, Hq), kThr, scan_smem<D>(), stream>>>(a, y);
-    f32_cached_kernel<T, D><<<dim3(nslots, Hq, y.splits), kThr, cached_smem<D>(), stream>>>(a, y);
-    f32_combine_kernel<T, D><<<dim3(nslots, Hq), kThr, 0, stream>>>(a, y);
-    f32_carry_kernel<T, D><<<dim3(nslots + a.c.seqs * (D / 64), Hkv), kThr, carry_smem<D>(), stream>>>(
+        f32_scan_kernel<D><<<dim3(nslots, Hq), kThr, scan_smem<D>(), stream>>>(a, y);
+    f32_cached_kernel<D><<<dim3(nslots, Hq, y.splits), kThr, cached_smem<D>(), stream>>>(a, y);
+    f32_combine_kernel<D><<<dim3(nslots, Hq), kThr, 0, stream>>>(a, y);
+    f32_carry_kernel<D><<<dim3(nslots + a.c.seqs * (D / 64), Hkv), kThr, carry_smem<D>(), stream>>>(
         a, y, nslots);
     const long long cap = (long long)a.c.max_pages << a.c.page_shift;
     const int parts = (int)((cap + 4 * kC - 1) / (4 * kC));
-    f32_transform_kernel<T, D><<<dim3(parts, Hkv, a.c.seqs), kThr, transform_smem<D>(), stream>>>(a, y);
+    f32_transform_kernel<D><<<dim3(parts, Hkv, a.c.seqs), kThr, transform_smem<D>(), stream>>>(a, y);
     return cudaGetLastError();
 }
 
@@ -803,15 +793,13 @@ F32Layout f32_layout(const Cache &c, int N, int d, bool fox) {
 
 size_t f32_ws_bytes(const Cache &c, int N, int d, bool fox) { return f32_layout(c, N, d, fox).total; }
 
-cudaError_t launch_f32(const Step &a, int d, bool bf16, void *ws, cudaStream_t stream) {
+cudaError_t launch_f32(const Step &a, int d, void *ws, cudaStream_t stream) {
     const F32Layout f = f32_layout(a.c, a.N, d, a.log_f != nullptr);
     char *w = static_cast<char *>(ws);
     auto at = [&](size_t off) { return reinterpret_cast<float *>(w + off); };
     const Ws y{at(f.qt), at(f.kt), at(f.pb), at(f.part), at(f.gq), at(f.gt), at(f.ptot),
                reinterpret_cast<double *>(w + f.gtot), f.splits};
-    if (bf16)
-        return d == 64 ? launch_d<__nv_bfloat16, 64>(a, y, stream) : launch_d<__nv_bfloat16, 128>(a, y, stream);
-    return d == 64 ? launch_d<float, 64>(a, y, stream) : launch_d<float, 128>(a, y, stream);
+    return d == 64 ? launch_d<64>(a, y, stream) : launch_d<128>(a, y, stream);
 }
 
 }  // namespace paged

@@ -1,0 +1,688 @@
+// The bf16 block path of a step over a paged cache, except its attention: per-block factors,
+// the new keys' way into the cache, the cached keys' update and the joining of the softmax
+// parts. Warp-level MMAs (mma.sync, bf16 operands, fp32 accumulators): every product here is
+// 64 x 64 x d or the pass is bound by memory, and none of them is worth a tensor-memory
+// pipeline; the attention itself is in paged_attn_tc.cu.
+//
+// Precision. The inputs are bf16; what is computed from them (A, U, Lq A, R A^T, P_b) enters
+// further products as a high and a low bf16 part (16 bits of significand, see split2), so
+// carried keys and transitions are exact to 2^-16 before the cache rounds the keys to bf16.
+// The factor A = (I + D N)^{-1} D is solved in fp32. Only the carried queries, the softmax
+// weights and, in the scan over a chunk's blocks, keys and transitions are rounded to bf16.
+#include "paged_tc.cuh"
+
+namespace path {
+namespace paged {
+
+namespace {
+
+constexpr int kThr = 256;
+using bf = __nv_bfloat16;
+
+// ---------------------------------------------------------------- prep
+// One CTA per 64-token block and key head. With the block's tokens in `nt` tiles of 16 rows,
+// every product is cut to those (a step of a few tokens costs a few tiles).
+template <int D>
+struct PrepSmem {
+    static constexpr int LDD = D + 8, LDS = 72, LDF = 68;  // row strides: 16-byte phases differ
+    static constexpr size_t big = (size_t)kC * LDD * 2, sml = (size_t)kC * LDS * 2;
+    static constexpr size_t W = 0, K = big, Q = 2 * big, V = 3 * big;  // U (hi, lo) lies in Q, V
+    static constexpr size_t Ah = 4 * big, Al = Ah + sml, Rh = Al + sml, Rl = Rh + sml, Lh = Rl + sml,
+                            Ll = Lh + sml, Th = Ll + sml, Tl = Th + sml, F = Th;
+    // fp32 64 x 68 (E, the logits) lies in [Th, Tl]; the pair Lh, Ll holds Lq and R A^T, then P
+    static constexpr size_t vec = Tl + sml;  // beta, m, l: 64 floats each; cum: 64 doubles
+    static constexpr size_t bytes = vec + 3 * kC * 4 + kC * 8;
+};
+
+// 64 tokens (rows past `rows` zero) of one head into a shared tile
+template <int D>
+__device__ __forceinline__ void load_block(bf *dst, const void *src, Stride st, long long first, int head,
+                                           int rows) {
+    constexpr int LDD = D + 8, PER = D / 8;
+    const bf *p = static_cast<const bf *>(src) + head * st.head;
+    for (int e = threadIdx.x; e < kC * PER; e += kThr) {
+        const int r = e / PER, c = e % PER * 8;
+        const uint4 x = r < rows ? *reinterpret_cast<const uint4 *>(p + (first + r) * st.tok + c)
+                                 : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(dst + r * LDD + c) = x;
+    }
+}
+
+__device__ __forceinline__ void put2(bf *t, int ld, int r, int c, uint32_t v) {
+    *reinterpret_cast<uint32_t *>(t + r * ld + c) = v;
+}
+
+// (I + E)^{-1} D in fp32 for a strictly lower triangular E (shared, stride 68): the four 16 x
+// 16 diagonal blocks by substitution (one column per thread), then X21 = -X22 E21 X11 for the
+// 16- and the 32-blocks; every factor is bounded (products of contractions), so nothing
+// grows. `Y`: 32 x 36 floats of scratch. The columns are scaled by beta at the end.
+__device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid) {
+    constexpr int LD = 68, YL = 36;
+    const int b0 = (tid >> 4) << 4, lu = tid & 15;
+    float x[16];
+    if (tid < kC) {
+#pragma unroll
+        for (int l = 0; l < 16; ++l) x[l] = l == lu ? 1.f : 0.f;
+#pragma unroll
+        for (int m = 0; m < 15; ++m)
+#pragma unroll
+            for (int l = m + 1; l < 16; ++l) x[l] = fmaf(-E[(b0 + l) * LD + b0 + m], x[m], x[l]);
+    }
+    __syncthreads();
+    if (tid < kC)
+#pragma unroll
+        for (int l = 0; l < 16; ++l) E[(b0 + l) * LD + tid] = x[l];
+    __syncthreads();
+    // level 1: two 32-blocks at o, X21 (16 x 16)
+    for (int pass = 0; pass < 2; ++pass) {
+        float v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = tid + i * kThr, o = 32 * (e >> 8), r = (e >> 4) & 15, c = e & 15;
+            float t = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                t = pass == 0 ? fmaf(E[(o + 16 + r) * LD + o + k], E[(o + k) * LD + o + c], t)
+                              : fmaf(E[(o + 16 + r) * LD + o + 16 + k], Y[((o >> 1) + k) * YL + c], t);
+            v[i] = t;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = tid + i * kThr, o = 32 * (e >> 8), r = (e >> 4) & 15, c = e & 15;
+            if (pass == 0) Y[((o >> 1) + r) * YL + c] = v[i];
+            else E[(o + 16 + r) * LD + o + c] = -v[i];
+        }
+        __syncthreads();
+    }
+    // level 2: X21 (32 x 32)
+    for (int pass = 0; pass < 2; ++pass) {
+        float v[4];
+        const int r = tid >> 3, c0 = (tid & 7) * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) {
+            const float l = pass == 0 ? E[(32 + r) * LD + k] : E[(32 + r) * LD + 32 + k];
+            const float4 q = *reinterpret_cast<const float4 *>(pass == 0 ? E + k * LD + c0 : Y + k * YL + c0);
+            v[0] = fmaf(l, q.x, v[0]);
+            v[1] = fmaf(l, q.y, v[1]);
+            v[2] = fmaf(l, q.z, v[2]);
+            v[3] = fmaf(l, q.w, v[3]);
+        }
+        __syncthreads();
+        float *dst = pass == 0 ? Y + r * YL + c0 : E + (32 + r) * LD + c0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = pass == 0 ? v[i] : -v[i];
+        __syncthreads();
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const Step a, const TcWs y) {
+    using S = PrepSmem<D>;
+    constexpr int LDD = S::LDD, LDS = S::LDS, LDF = S::LDF, NH = D / 64;
+    extern __shared__ __align__(16) uint8_t smem[];
+    bf *const W = reinterpret_cast<bf *>(smem + S::W), *const K = reinterpret_cast<bf *>(smem + S::K),
+       *const Q = reinterpret_cast<bf *>(smem + S::Q), *const V = reinterpret_cast<bf *>(smem + S::V),
+       *const Uh = Q, *const Ul = V, *const Ah = reinterpret_cast<bf *>(smem + S::Ah),
+       *const Al = reinterpret_cast<bf *>(smem + S::Al), *const Rh = reinterpret_cast<bf *>(smem + S::Rh),
+       *const Rl = reinterpret_cast<bf *>(smem + S::Rl), *const Lh = reinterpret_cast<bf *>(smem + S::Lh),
+       *const Ll = reinterpret_cast<bf *>(smem + S::Ll), *const Th = reinterpret_cast<bf *>(smem + S::Th),
+       *const Tl = reinterpret_cast<bf *>(smem + S::Tl);
+    float *const F = reinterpret_cast<float *>(smem + S::F);
+    float *const beta = reinterpret_cast<float *>(smem + S::vec), *const rm = beta + kC, *const rl = rm + kC;
+    double *const cum = reinterpret_cast<double *>(rl + kC);
+    const int slot = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.c.G;
+    int b, c;
+    Seq s;
+    if (!block_of(a, slot, b, c, s)) return;
+    const int rows = min(kC, s.T - c * kC), nt = (rows + 15) >> 4;
+    const bool single = s.T <= kC;
+    const long long first = s.first + c * kC;
+    const size_t bh = (size_t)slot * a.c.Hkv + h;
+    load_block<D>(W, a.w, a.sw, first, h, rows);
+    load_block<D>(K, a.k, a.sk, first, h, rows);
+    if (tid < kC) beta[tid] = tid < rows ? a.beta[(first + tid) * a.sb.tok + h * a.sb.head] : 0.f;
+    __syncthreads();
+    // a warp's 16 x 32 piece of a 64 x 64 product
+    const int m0 = 16 * (warp & 3), n0 = 32 * (warp >> 2);
+    const bool live = (warp & 3) < nt && n0 < 16 * nt;  // the piece has rows and columns
+    {
+        float e[4][4], r[4][4];
+        zero_acc(e);
+        zero_acc(r);
+        if (live) {
+            warp_mma<4, false, false>(e, W, LDD, m0, W, LDD, n0, D / 16);
+            warp_mma<4, false, false>(r, K, LDD, m0, W, LDD, n0, D / 16);
+        }
+        each_pair(e, m0, n0, [&](int i, int j, float x, float z) {
+            F[i * LDF + j] = j < i ? beta[i] * x : 0.f;
+            F[i * LDF + j + 1] = j + 1 < i ? beta[i] * z : 0.f;
+        });
+        each_pair(r, m0, n0, [&](int i, int j, float x, float z) {
+            uint32_t hi, lo;
+            split2(j > i ? x : 0.f, j + 1 > i ? z : 0.f, hi, lo);
+            put2(Rh, LDS, i, j, hi);
+            put2(Rl, LDS, i, j, lo);
+        });
+    }
+    __syncthreads();
+    unit_lower_inverse(F, reinterpret_cast<float *>(Lh), tid);
+    for (int e = tid; e < kC * kC / 2; e += kThr) {
+        const int i = e / 32, j = 2 * (e % 32);
+        uint32_t hi, lo;
+        split2(j <= i ? F[i * LDF + j] * beta[j] : 0.f, j + 1 <= i ? F[i * LDF + j + 1] * beta[j + 1] : 0.f,
+               hi, lo);
+        put2(Ah, LDS, i, j, hi);
+        put2(Al, LDS, i, j, lo);
+    }
+    __syncthreads();
+    // U = A W (64 x D) and R A^T (64 x 64)
+#pragma unroll
+    for (int x = 0; x < NH; ++x) {
+        float u[4][4];
+        zero_acc(u);
+        if ((warp & 3) < nt) {
+            warp_mma<4, false, true>(u, Ah, LDS, m0, W, LDD, 64 * x + n0, nt);
+            warp_mma<4, false, true>(u, Al, LDS, m0, W, LDD, 64 * x + n0, nt);
+        }
+        each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
+            uint32_t hi, lo;
+            split2(p, q, hi, lo);
+            put2(Uh, LDD, i, j, hi);
+            put2(Ul, LDD, i, j, lo);
+        });
+    }
+    {
+        float r[4][4];
+        zero_acc(r);
+        if (live) {
+            warp_mma<4, false, false>(r, Rh, LDS, m0, Ah, LDS, n0, nt);
+            warp_mma<4, false, false>(r, Rl, LDS, m0, Ah, LDS, n0, nt);
+            warp_mma<4, false, false>(r, Rh, LDS, m0, Al, LDS, n0, nt);
+        }
+        each_pair(r, m0, n0, [&](int i, int j, float p, float q) {
+            uint32_t hi, lo;
+            split2(p, q, hi, lo);
+            put2(Lh, LDS, i, j, hi);
+            put2(Ll, LDS, i, j, lo);
+        });
+    }
+    __syncthreads();
+    // P_b - I = -U^T W (D x D): to the chunk's product or the block's factors
+    {
+        bf *const mh = single ? y.mt + ((size_t)b * a.c.Hkv + h) * 2 * D * D : y.kh + (bh * (kC + D) + kC) * D;
+        bf *const ml = single ? mh + (size_t)D * D : y.kl + (bh * (kC + D) + kC) * D;
+#pragma unroll 1
+        for (int t = warp; t < D / 16 * (D / 32); t += kThr / 32) {
+            const int r0 = 16 * (t % (D / 16)), c0 = 32 * (t / (D / 16));
+            float u[4][4];
+            zero_acc(u);
+            warp_mma<4, true, true>(u, Uh, LDD, r0, W, LDD, c0, nt);
+            warp_mma<4, true, true>(u, Ul, LDD, r0, W, LDD, c0, nt);
+            each_pair(u, r0, c0, [&](int i, int j, float p, float q) {
+                uint32_t hi, lo;
+                split2(-p, -q, hi, lo);
+                *reinterpret_cast<uint32_t *>(mh + (size_t)i * D + j) = hi;
+                *reinterpret_cast<uint32_t *>(ml + (size_t)i * D + j) = lo;
+            });
+        }
+    }
+    // k~ = K - (R A^T) W: into the pages (the chunk's only block) or the block's factors
+#pragma unroll
+    for (int x = 0; x < NH; ++x) {
+        if (single && (warp & 3) >= nt) break;
+        float u[4][4];
+        zero_acc(u);
+        warp_mma<4, false, true>(u, Lh, LDS, m0, W, LDD, 64 * x + n0, nt);
+        warp_mma<4, false, true>(u, Ll, LDS, m0, W, LDD, 64 * x + n0, nt);
+        each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
+            const float2 k2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(K + i * LDD + j));
+            p = k2.x - p;
+            q = k2.y - q;
+            if (single) {
+                if (i >= rows) return;
+                const int pos = s.n + i, id = page_of(a, a.c.k_table, b, pos >> a.c.page_shift, a.c.nk);
+                if (id >= 0)
+                    *reinterpret_cast<uint32_t *>(
+                        static_cast<bf *>(a.c.k_pages) +
+                        ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) + (pos & (a.c.page - 1))) * D + j) =
+                        pack_bf16x2(p, q);
+            } else {
+                uint32_t hi, lo;
+                split2(p, q, hi, lo);
+                *reinterpret_cast<uint32_t *>(y.kh + (bh * (kC + D) + i) * D + j) = hi;
+                *reinterpret_cast<uint32_t *>(y.kl + (bh * (kC + D) + i) * D + j) = lo;
+            }
+        });
+    }
+    __syncthreads();
+    load_block<D>(V, a.v, a.sv, first, h, rows);
+    __syncthreads();
+    // the block's values: into the pages, and beside the factors for the scan
+    for (int e = tid; e < kC * D / 8; e += kThr) {
+        const int r = e / (D / 8), q = e % (D / 8) * 8;
+        const uint4 x = *reinterpret_cast<const uint4 *>(V + r * LDD + q);
+        if (!single) *reinterpret_cast<uint4 *>(y.vb + (bh * kC + r) * D + q) = x;
+        if (r >= rows) continue;
+        const int pos = s.n + c * kC + r, id = page_of(a, a.c.v_table, b, pos >> a.c.page_shift, a.c.nv);
+        if (id >= 0)
+            *reinterpret_cast<uint4 *>(
+                static_cast<bf *>(a.c.v_pages) +
+                ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) + (pos & (a.c.page - 1))) * D + q) = x;
+    }
+    for (int g = 0; g < G; ++g) {
+        const int hq = h * G + g;
+        const size_t bq = (size_t)slot * a.c.Hq + hq;
+        // the row of token t: its place in the step's packed rows
+        auto row_of = [&](int t) { return (size_t)h * y.R + (first + t) * G + g; };
+        __syncthreads();
+        load_block<D>(Q, a.q, a.sq, first, hq, rows);
+        if (a.log_f != nullptr && warp == 0) {
+            // inclusive prefix sums of the 64 gates
+            double p = 0.0;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int t = 32 * half + lane;
+                double x = t < rows ? (double)a.log_f[(first + t) * a.sf.tok + hq * a.sf.head] : 0.0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double z = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += z;
+                }
+                cum[t] = p + x;
+                p += __shfl_sync(0xffffffffu, x, 31);
+            }
+            if (lane == 0) y.gtot[bq] = p;
+        }
+        __syncthreads();
+        if (a.log_f != nullptr && tid < kC) {
+            const float behind = (float)(cum[kC - 1] - cum[tid]);
+            y.gt[bq * kC + tid] = behind;
+            if (tid < rows) {
+                y.gq[row_of(tid)] = (float)cum[tid];
+                if (single) {
+                    const int pos = s.n + tid, id = page_of(a, a.c.k_table, b, pos >> a.c.page_shift, a.c.nk);
+                    if (id >= 0)
+                        a.c.g_pages[(((size_t)id * a.c.Hq + hq) << a.c.page_shift) + (pos & (a.c.page - 1))] =
+                            behind;
+                }
+            }
+        }
+        {  // Lq = tril(Q W^T)
+            float u[4][4];
+            zero_acc(u);
+            if (live) warp_mma<4, false, false>(u, Q, LDD, m0, W, LDD, n0, D / 16);
+            each_pair(u, m0, n0, [&](int i, int j, float p, float q) {
+                uint32_t hi, lo;
+                split2(j <= i ? p : 0.f, j + 1 <= i ? q : 0.f, hi, lo);
+                put2(Lh, LDS, i, j, hi);
+                put2(Ll, LDS, i, j, lo);
+            });
+        }
+        __syncthreads();
+        {  // Lq A
+            float u[4][4];
+            zero_acc(u);
+            if (live) {
+                warp_mma<4, false, true>(u, Lh, LDS, m0, Ah, LDS, n0, nt);
+                warp_mma<4, false, true>(u, Ll, LDS, m0, Ah, LDS, n0, nt);
+                warp_mma<4, false, true>(u, Lh, LDS, m0, Al, LDS, n0, nt);
+            }
+            each_pair(u, m0, n0, [&](int i, int j, float p, float q) {
+                uint32_t hi, lo;
+                split2(p, q, hi, lo);
+                put2(Th, LDS, i, j, hi);
+                put2(Tl, LDS, i, j, lo);
+            });
+        }
+        __syncthreads();
+        // q~ = Q - (Lq A) W
+#pragma unroll
+        for (int x = 0; x < NH; ++x) {
+            if ((warp & 3) >= nt) break;
+            float u[4][4];
+            zero_acc(u);
+            warp_mma<4, false, true>(u, Th, LDS, m0, W, LDD, 64 * x + n0, nt);
+            warp_mma<4, false, true>(u, Tl, LDS, m0, W, LDD, 64 * x + n0, nt);
+            each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
+                if (i >= rows) return;
+                const float2 q2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(Q + i * LDD + j));
+                *reinterpret_cast<uint32_t *>(y.qt + row_of(i) * D + j) = pack_bf16x2(q2.x - p, q2.y - q);
+            });
+        }
+        {  // the block's logits Q K^T - (Lq A) R^T
+            float u[4][4], z[4][4];
+            zero_acc(u);
+            zero_acc(z);
+            if (live) {
+                warp_mma<4, false, false>(u, Q, LDD, m0, K, LDD, n0, D / 16);
+                warp_mma<4, false, false>(z, Th, LDS, m0, Rh, LDS, n0, nt);
+                warp_mma<4, false, false>(z, Tl, LDS, m0, Rh, LDS, n0, nt);
+                warp_mma<4, false, false>(z, Th, LDS, m0, Rl, LDS, n0, nt);
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[n][i] = (u[n][i] - z[n][i]) * a.scale_log2;
+            __syncthreads();  // Lq A has been read; the logits take its place
+            each_pair(u, m0, n0, [&](int i, int j, float p, float q) {
+                if (a.log_f != nullptr) {
+                    if (j < i) p = fmaf((float)(cum[i] - cum[j]), kLog2e, p);
+                    if (j + 1 < i) q = fmaf((float)(cum[i] - cum[j + 1]), kLog2e, q);
+                }
+                F[i * LDF + j] = j <= i ? p : -INFINITY;
+                F[i * LDF + j + 1] = j + 1 <= i ? q : -INFINITY;
+            });
+        }
+        __syncthreads();
+        // row maxima and sums; the weights, rounded to bf16, for the product with the values
+        for (int i = warp; i < 16 * nt; i += kThr / 32) {
+            const float x0 = F[i * LDF + 2 * lane], x1 = F[i * LDF + 2 * lane + 1];
+            float m = fmaxf(x0, x1);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float p0 = exp2f(x0 - m), p1 = exp2f(x1 - m);  // the row's own key is never masked
+            float l = p0 + p1;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            put2(Lh, LDS, i, 2 * lane, pack_bf16x2(p0, p1));
+            if (lane == 0) {
+                rm[i] = m;
+                rl[i] = l;
+            }
+        }
+        __syncthreads();
+        if (tid < rows) y.pml[row_of(tid)] = make_float2(rm[tid], rl[tid]);
+#pragma unroll
+        for (int x = 0; x < NH; ++x) {
+            if ((warp & 3) >= nt) break;
+            float u[4][4];
+            zero_acc(u);
+            warp_mma<4, false, true>(u, Lh, LDS, m0, V, LDD, 64 * x + n0, nt);
+            each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
+                if (i < rows) *reinterpret_cast<float2 *>(y.po + row_of(i) * D + j) = make_float2(p, q);
+            });
+        }
+    }
+}
+
+// ---------------------------------------------------------------- carry
+// Chunks of several blocks: the new keys of a block through the later ones, Y <- Y P_b for
+// b = c + 1 .. last, into their pages; and the identity through all blocks, which gives the
+// chunk's own product. Y is split into 16-bit pairs at every step, its sum stays in fp32
+// registers (Y + Y (P_b - I)), four warps of 16 rows each.
+template <int D>
+struct CarrySmem {
+    static constexpr int LDD = D + 8;
+    static constexpr size_t Mh = 0, Ml = (size_t)D * LDD * 2, Yh = 2 * Ml, Yl = Yh + (size_t)kC * LDD * 2,
+                            bytes = Yl + (size_t)kC * LDD * 2;
+};
+
+template <int D>
+__global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs y) {
+    using S = CarrySmem<D>;
+    constexpr int LDD = S::LDD, NT = D / 8, PER = D / 8;
+    extern __shared__ __align__(16) uint8_t smem[];
+    bf *const Mh = reinterpret_cast<bf *>(smem + S::Mh), *const Ml = reinterpret_cast<bf *>(smem + S::Ml),
+       *const Yh = reinterpret_cast<bf *>(smem + S::Yh), *const Yl = reinterpret_cast<bf *>(smem + S::Yl);
+    const int h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, m0 = 16 * warp;
+    const bool ident = (int)blockIdx.x < a.c.seqs * (D / 64);  // the longest ways first
+    int b, c = -1, tile = 0;
+    Seq s;
+    float acc[NT][4];
+    if (ident) {
+        b = blockIdx.x / (D / 64);
+        tile = blockIdx.x % (D / 64);
+        s = seq_of(a, b);
+        if (s.T <= kC || s.n == 0) return;
+        zero_acc(acc);
+        const int lane = tid & 31, r = 64 * tile + m0 + (lane >> 2), q = 2 * (lane & 3);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] = (8 * n + q + (i & 1) == r + 8 * (i >> 1)) ? 1.f : 0.f;
+    } else {
+        const int slot = blockIdx.x - a.c.seqs * (D / 64);
+        if (!block_of(a, slot, b, c, s) || s.T <= kC) return;
+        const size_t base = ((size_t)slot * a.c.Hkv + h) * (kC + D);
+        zero_acc(acc);
+        const int lane = tid & 31;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const size_t at = (base + m0 + (lane >> 2) + 8 * i) * D + 8 * n + 2 * (lane & 3);
+                const float2 p = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(y.kh + at));
+                const float2 q = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(y.kl + at));
+                acc[n][2 * i] = p.x + q.x;
+                acc[n][2 * i + 1] = p.y + q.y;
+            }
+    }
+    const int nb = (s.T + kC - 1) / kC;
+    for (int kb = c + 1; kb < nb; ++kb) {
+        const size_t base = (((size_t)slot_of(s, b, kb) * a.c.Hkv + h) * (kC + D) + kC) * D;
+        __syncthreads();
+        for (int e = tid; e < D * PER; e += 128) {
+            const int r = e / PER, q = e % PER * 8;
+            *reinterpret_cast<uint4 *>(Mh + r * LDD + q) = *reinterpret_cast<const uint4 *>(y.kh + base + (size_t)r * D + q);
+            *reinterpret_cast<uint4 *>(Ml + r * LDD + q) = *reinterpret_cast<const uint4 *>(y.kl + base + (size_t)r * D + q);
+        }
+        each_pair(acc, m0, 0, [&](int i, int j, float p, float q) {
+            uint32_t hi, lo;
+            split2(p, q, hi, lo);
+            put2(Yh, LDD, i, j, hi);
+            put2(Yl, LDD, i, j, lo);
+        });
+        __syncthreads();
+        warp_mma<NT, false, true>(acc, Yh, LDD, m0, Mh, LDD, 0, D / 16);
+        warp_mma<NT, false, true>(acc, Yl, LDD, m0, Mh, LDD, 0, D / 16);
+        warp_mma<NT, false, true>(acc, Yh, LDD, m0, Ml, LDD, 0, D / 16);
+    }
+    if (ident) {
+        bf *const mh = y.mt + ((size_t)b * a.c.Hkv + h) * 2 * D * D, *const ml = mh + (size_t)D * D;
+        each_pair(acc, 64 * tile + m0, 0, [&](int i, int j, float p, float q) {
+            uint32_t hi, lo;
+            split2(p - (i == j), q - (i == j + 1), hi, lo);
+            *reinterpret_cast<uint32_t *>(mh + (size_t)i * D + j) = hi;
+            *reinterpret_cast<uint32_t *>(ml + (size_t)i * D + j) = lo;
+        });
+        return;
+    }
+    const int rows = min(kC, s.T - c * kC);
+    each_pair(acc, m0, 0, [&](int i, int j, float p, float q) {
+        if (i >= rows) return;
+        const int pos = s.n + c * kC + i, id = page_of(a, a.c.k_table, b, pos >> a.c.page_shift, a.c.nk);
+        if (id >= 0)
+            *reinterpret_cast<uint32_t *>(
+                static_cast<bf *>(a.c.k_pages) +
+                ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) + (pos & (a.c.page - 1))) * D + j) =
+                pack_bf16x2(p, q);
+    });
+    if (a.log_f != nullptr) {
+        const int slot = blockIdx.x - a.c.seqs * (D / 64);
+        for (int e = tid; e < rows * a.c.G; e += 128) {
+            const int r = e % rows, hq = h * a.c.G + e / rows, pos = s.n + c * kC + r;
+            double g = y.gt[((size_t)slot * a.c.Hq + hq) * kC + r];
+            for (int kb = c + 1; kb < nb; ++kb) g += y.gtot[(size_t)slot_of(s, b, kb) * a.c.Hq + hq];
+            const int id = page_of(a, a.c.k_table, b, pos >> a.c.page_shift, a.c.nk);
+            if (id >= 0)
+                a.c.g_pages[(((size_t)id * a.c.Hq + hq) << a.c.page_shift) + (pos & (a.c.page - 1))] = (float)g;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- transform
+// K <- K + K (P - I) in place for sequences whose rows fill several tiles (with one tile the
+// attention pass does it on the keys that it has loaded). Bound by HBM: a key is read and
+// written once. grid (parts, key heads, sequences), a CTA keeps P - I in shared memory.
+template <int D>
+__global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, const TcWs y, int tile_rows) {
+    using S = CarrySmem<D>;
+    constexpr int LDD = S::LDD, NT = D / 8, PER = D / 8;
+    extern __shared__ __align__(16) uint8_t smem[];
+    bf *const Mh = reinterpret_cast<bf *>(smem + S::Mh), *const Ml = reinterpret_cast<bf *>(smem + S::Ml),
+       *const Kt = reinterpret_cast<bf *>(smem + S::Yh);  // 16 rows per warp: 128 in all
+    const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Seq s = seq_of(a, b);
+    if ((long long)s.T * a.c.G <= tile_rows || (int)blockIdx.x * 128 >= s.n) return;
+    const bf *const m = y.mt + ((size_t)b * a.c.Hkv + h) * 2 * D * D;
+    for (int e = tid; e < D * PER; e += kThr) {
+        const int r = e / PER, q = e % PER * 8;
+        *reinterpret_cast<uint4 *>(Mh + r * LDD + q) = *reinterpret_cast<const uint4 *>(m + (size_t)r * D + q);
+        *reinterpret_cast<uint4 *>(Ml + r * LDD + q) = *reinterpret_cast<const uint4 *>(m + (size_t)(D + r) * D + q);
+    }
+    __syncthreads();
+    bf *const mine = Kt + warp * 16 * LDD;
+    bf *const pool = static_cast<bf *>(a.c.k_pages);
+    for (int j0 = (blockIdx.x * 8 + warp) * 16; j0 < s.n; j0 += gridDim.x * 128) {
+        // 16 positions of one page (pages are multiples of 16)
+        const int id = page_of(a, a.c.k_table, b, j0 >> a.c.page_shift, a.c.nk);
+        if (id < 0) continue;  // the same for the warp
+        const int left = min(16, s.n - j0);
+        bf *const src = pool + ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) + (j0 & (a.c.page - 1))) * D;
+        __syncwarp();
+#pragma unroll
+        for (int e = lane; e < 16 * PER; e += 32) {
+            const int r = e / PER, q = e % PER * 8;
+            *reinterpret_cast<uint4 *>(mine + r * LDD + q) =
+                r < left ? *reinterpret_cast<const uint4 *>(src + (size_t)r * D + q) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+        float acc[NT][4];
+        zero_acc(acc);
+        warp_mma<NT, false, true>(acc, mine, LDD, 0, Mh, LDD, 0, D / 16);
+        warp_mma<NT, false, true>(acc, mine, LDD, 0, Ml, LDD, 0, D / 16);
+        __syncwarp();
+        each_pair(acc, 0, 0, [&](int i, int j, float p, float q) {
+            uint32_t *at = reinterpret_cast<uint32_t *>(mine + i * LDD + j);
+            const float2 k2 = unpack_bf16x2(*at);
+            *at = pack_bf16x2(k2.x + p, k2.y + q);
+        });
+        __syncwarp();
+#pragma unroll
+        for (int e = lane; e < 16 * PER; e += 32) {
+            const int r = e / PER, q = e % PER * 8;
+            if (r < left)
+                *reinterpret_cast<uint4 *>(src + (size_t)r * D + q) =
+                    *reinterpret_cast<const uint4 *>(mine + r * LDD + q);
+        }
+    }
+}
+
+// PaTH-FoX: every cached key's gate sums advance by the chunk's. grid (parts, Hq, seqs).
+__global__ void __launch_bounds__(kThr) tc_gates_kernel(const Step a, const TcWs y) {
+    const int hq = blockIdx.y, b = blockIdx.z;
+    const Seq s = seq_of(a, b);
+    if (s.T == 0 || (int)blockIdx.x * kThr >= s.n) return;
+    const int nb = (s.T + kC - 1) / kC;
+    double t = 0.0;
+    for (int kb = 0; kb < nb; ++kb) t += y.gtot[(size_t)slot_of(s, b, kb) * a.c.Hq + hq];
+    for (int j = blockIdx.x * kThr + threadIdx.x; j < s.n; j += gridDim.x * kThr) {
+        const int id = page_of(a, a.c.k_table, b, j >> a.c.page_shift, a.c.nk);
+        if (id < 0) continue;
+        float *g = a.c.g_pages + (((size_t)id * a.c.Hq + hq) << a.c.page_shift) + (j & (a.c.page - 1));
+        *g = (float)((double)*g + t);
+    }
+}
+
+// ---------------------------------------------------------------- combine
+// Positions of split sp of n cached ones, in tiles of 128; how many splits have any.
+__device__ __forceinline__ int used_splits(int n, int splits) {
+    const int tiles = (n + 127) / 128, per = (tiles + splits - 1) / splits;
+    return per > 0 ? (tiles + per - 1) / per : 0;
+}
+
+// One warp per row: joins its softmax parts. grid (slots, key heads).
+template <int D>
+__global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const TcWs y) {
+    constexpr int E = D / 32;
+    const int slot = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.c.G;
+    int b, c;
+    Seq s;
+    if (!block_of(a, slot, b, c, s)) return;
+    const int rows = min(kC, s.T - c * kC) * G, parts = 1 + used_splits(s.n, y.splits);
+    const size_t stride = (size_t)a.c.Hkv * y.R;
+    for (int i = warp; i < rows; i += kThr / 32) {
+        const long long tok = s.first + c * kC + i / G;
+        const int hq = h * G + i % G;
+        const size_t row = (size_t)h * y.R + tok * G + i % G;
+        float M = -INFINITY, L = 0.f, O[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) O[e] = 0.f;
+        for (int p = 0; p < parts; ++p) M = fmaxf(M, y.pml[row + p * stride].x);
+        for (int p = 0; p < parts; ++p) {
+            const float2 ml = y.pml[row + p * stride];
+            if (ml.x == -INFINITY) continue;
+            const float f = exp2f(ml.x - M);
+            L = fmaf(ml.y, f, L);
+            const float *o = y.po + (row + p * stride) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) O[e] = fmaf(o[e], f, O[e]);
+        }
+        bf *dst = static_cast<bf *>(a.out) + tok * a.so.tok + hq * a.so.head + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16x2(O[e] / L, O[e + 1] / L);
+    }
+}
+
+template <typename K>
+cudaError_t big_smem(K kern, size_t bytes) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+}  // namespace
+
+template <int D>
+cudaError_t launch_tc_prep(const Step &a, const TcWs &y, cudaStream_t stream) {
+    const cudaError_t e = big_smem(tc_prep_kernel<D>, PrepSmem<D>::bytes);
+    if (e != cudaSuccess) return e;
+    tc_prep_kernel<D><<<dim3(slots_of(a.N, a.c.seqs), a.c.Hkv), kThr, PrepSmem<D>::bytes, stream>>>(a, y);
+    return cudaGetLastError();
+}
+
+// Chunks of several blocks: new keys into the pages and the chunks' products (before the
+// attention, which takes those of short sequences).
+template <int D>
+cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
+    const cudaError_t e = big_smem(tc_carry_kernel<D>, CarrySmem<D>::bytes);
+    if (e != cudaSuccess) return e;
+    tc_carry_kernel<D><<<dim3(a.c.seqs * (D / 64) + slots_of(a.N, a.c.seqs), a.c.Hkv), 128, CarrySmem<D>::bytes,
+                         stream>>>(a, y);
+    return cudaGetLastError();
+}
+
+// The rest of a step after its attention: outputs, the cached keys of sequences with more than
+// tile_rows rows, the gate sums.
+template <int D>
+cudaError_t launch_tc_finish(const Step &a, const TcWs &y, int tile_rows, cudaStream_t stream) {
+    const int nslots = slots_of(a.N, a.c.seqs);
+    const long long cap = (long long)a.c.max_pages << a.c.page_shift;
+    tc_combine_kernel<D><<<dim3(nslots, a.c.Hkv), kThr, 0, stream>>>(a, y);
+    cudaError_t e;
+    if ((long long)a.max_chunk * a.c.G > tile_rows) {
+        const size_t bytes = CarrySmem<D>::Yh + (size_t)128 * CarrySmem<D>::LDD * 2;
+        if ((e = big_smem(tc_transform_kernel<D>, bytes)) != cudaSuccess) return e;
+        const long long tiles = (cap + 127) / 128;  // four per CTA: P is loaded once for 512 keys
+        tc_transform_kernel<D><<<dim3((unsigned)((tiles + 3) / 4), a.c.Hkv, a.c.seqs), kThr, bytes, stream>>>(
+            a, y, tile_rows);
+    }
+    if (a.log_f != nullptr)
+        tc_gates_kernel<<<dim3((unsigned)((cap + 4 * kThr - 1) / (4 * kThr)), a.c.Hq, a.c.seqs), kThr, 0, stream>>>(
+            a, y);
+    return cudaGetLastError();
+}
+
+template cudaError_t launch_tc_prep<64>(const Step &, const TcWs &, cudaStream_t);
+template cudaError_t launch_tc_prep<128>(const Step &, const TcWs &, cudaStream_t);
+template cudaError_t launch_tc_carry<64>(const Step &, const TcWs &, cudaStream_t);
+template cudaError_t launch_tc_carry<128>(const Step &, const TcWs &, cudaStream_t);
+template cudaError_t launch_tc_finish<64>(const Step &, const TcWs &, int, cudaStream_t);
+template cudaError_t launch_tc_finish<128>(const Step &, const TcWs &, int, cudaStream_t);
+
+}  // namespace paged
+}  // namespace path

@@ -1,0 +1,140 @@
+// The bf16 block path of a step over a paged cache: workspace and warp-level product helpers.
+//
+// Rows. The Hq / Hkv = G query heads of a key head are taken together: row t G + g of a
+// sequence is query head g of its new token t, so that 128 consecutive rows (one tensor-core
+// tile) hold as many tokens as share the cached keys. All sequences' rows of a key head stand
+// one behind the other, R = N G of them.
+#pragma once
+
+#include "paged.cuh"
+
+namespace path {
+namespace paged {
+
+// Workspace of the bf16 block path, behind the 256-byte status header:
+//   qt   (Hkv, R, D) bf16       queries carried to the chunk's start
+//   po   (1 + splits, Hkv, R, D) fp32, pml (1 + splits, Hkv, R) fp32 pairs: unnormalised softmax
+//        parts and their (maximum in log2 units, sum): 0 the step's own tokens, then the splits
+//   gq   (Hkv, R) fp32          PaTH-FoX: gate sum of a row from the chunk's start
+//   gt   (slots, Hq, 64) fp32   PaTH-FoX: gate sum behind a key to its block's end
+//   gtot (slots, Hq) fp64       PaTH-FoX: gate sum of a block
+//   mt   (seqs, Hkv, 2, D, D)   bf16 high and low parts of (H_1 ... H_T) - I of the whole chunk
+// and, where a chunk may have several blocks of 64 tokens:
+//   kh, kl (slots, Hkv, 64 + D, D) bf16 high and low parts of [k~; P_b - I]
+//   vb   (slots, Hkv, 64, D) bf16 the block's values, zero past its tokens
+struct TcWs {
+    __nv_bfloat16 *qt, *mt, *kh, *kl, *vb;
+    float *po;
+    float2 *pml;
+    float *gq, *gt;
+    double *gtot;
+    int splits;
+    long long R;
+};
+
+// Rows of `rows` per tile over all sequences: tile i of sequence b is slot
+// cu[b] G / rows + b + i (as slots_of).
+__host__ __device__ __forceinline__ int tile_slots(int N, int G, int seqs, int rows) {
+    return (int)((long long)N * G / rows) + seqs;
+}
+__device__ __forceinline__ bool tile_of(const Step &a, int slot, int rows, int &b, int &i, Seq &s) {
+    const int G = a.c.G;
+    int lo = 0, hi = a.c.seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int)((long long)__ldg(a.cu + mid) * G / rows) + mid <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    b = lo;
+    s = seq_of(a, b);
+    i = slot - ((int)((long long)s.first * G / rows) + b);
+    return i >= 0 && (long long)i * rows < (long long)s.T * G;
+}
+
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Fragments of a 16 x 16 piece at (r0, k0) of a row-major bf16 shared tile (ld elements per
+// row): A rows r0.., as stored ([m][k]) or from [k][m].
+__device__ __forceinline__ void frag_a(uint32_t (&r)[4], const __nv_bfloat16 *t, int ld, int m0, int k0) {
+    const int lane = threadIdx.x & 31;
+    ldm4(r, smem_u32(t + (m0 + (lane & 15)) * ld + k0 + (lane >> 4) * 8));
+}
+__device__ __forceinline__ void frag_at(uint32_t (&r)[4], const __nv_bfloat16 *t, int ld, int m0, int k0) {
+    const int lane = threadIdx.x & 31, i = lane >> 3;
+    ldm4t(r, smem_u32(t + (k0 + (lane & 7) + (i >> 1) * 8) * ld + m0 + (i & 1) * 8));
+}
+// Two n-tiles (n0, n0 + 8) of B from [n][k] or [k][n]: b0, b1 of the first, then of the second.
+__device__ __forceinline__ void frag_bt(uint32_t (&r)[4], const __nv_bfloat16 *t, int ld, int n0, int k0) {
+    const int lane = threadIdx.x & 31, i = lane >> 3;
+    ldm4(r, smem_u32(t + (n0 + (lane & 7) + (i >> 1) * 8) * ld + k0 + (i & 1) * 8));
+}
+__device__ __forceinline__ void frag_b(uint32_t (&r)[4], const __nv_bfloat16 *t, int ld, int n0, int k0) {
+    const int lane = threadIdx.x & 31, i = lane >> 3;
+    ldm4t(r, smem_u32(t + (k0 + (lane & 7) + (i & 1) * 8) * ld + n0 + (i >> 1) * 8));
+}
+
+// One warp: acc (16 rows from m0, 8 NT columns from n0) += A B over K, K = 16 ksteps. AT: A is
+// stored [k][m]; BN: B is stored [k][n] (else [n][k]). acc[n][0..1]: row lane / 4, columns
+// 2 (lane % 4), + 1; acc[n][2..3]: row + 8.
+template <int NT, bool AT, bool BN>
+__device__ __forceinline__ void warp_mma(float (&acc)[NT][4], const __nv_bfloat16 *A, int lda, int m0,
+                                         const __nv_bfloat16 *B, int ldb, int n0, int ksteps) {
+#pragma unroll 2
+    for (int k = 0; k < ksteps; ++k) {
+        uint32_t a[4];
+        if (AT) frag_at(a, A, lda, m0, 16 * k);
+        else frag_a(a, A, lda, m0, 16 * k);
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+            uint32_t b[4];
+            if (BN) frag_b(b, B, ldb, n0 + 8 * n, 16 * k);
+            else frag_bt(b, B, ldb, n0 + 8 * n, 16 * k);
+            mma_bf16(acc[n], a, b[0], b[1]);
+            mma_bf16(acc[n + 1], a, b[2], b[3]);
+        }
+    }
+}
+
+template <int NT>
+__device__ __forceinline__ void zero_acc(float (&acc)[NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+}
+
+// x as a high and a low bf16 part: together 16 bits of significand, so a product of split
+// operands (three MMAs, low x low left out) is off by 2^-16 of its terms
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack_bf16x2(x, y);
+    const float2 h = unpack_bf16x2(hi);
+    lo = pack_bf16x2(x - h.x, y - h.y);
+}
+
+// fn(row, column, value, value of the next column) over a warp's accumulator tile
+template <int NT, typename F>
+__device__ __forceinline__ void each_pair(float (&acc)[NT][4], int m0, int n0, F fn) {
+    const int lane = threadIdx.x & 31, r = m0 + (lane >> 2), c = n0 + 2 * (lane & 3);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        fn(r, c + 8 * n, acc[n][0], acc[n][1]);
+        fn(r + 8, c + 8 * n, acc[n][2], acc[n][3]);
+    }
+}
+
+}  // namespace paged
+}  // namespace path
