@@ -45,8 +45,8 @@ class _CPagedCache(ctypes.Structure):
                                             "num_v_pages", "Hq", "Hkv", "d", "dtype")]
 
 
-class _CPagedStrides(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int64 * 2) for n in ("q", "k", "v", "w", "beta", "log_f", "out")]
+# path_paged_strides: {token, head} strides of q, k, v, w, beta, log_f, out
+_C14 = ctypes.c_int64 * 14
 
 
 class PathError(RuntimeError):
@@ -103,7 +103,7 @@ def _load():
     lib.path_fox_first_blocks.argtypes = [P, S, I, I, I, I, I, P, P]
     lib.path_fox_first_blocks.restype = I
     C = ctypes.POINTER(_CPagedCache)
-    T = ctypes.POINTER(_CPagedStrides)
+    T = ctypes.POINTER(ctypes.c_int64)
     lib.path_paged_workspace_bytes.argtypes = [C, I, I]
     lib.path_paged_workspace_bytes.restype = S
     lib.path_paged_extend.argtypes = [C, P, P, P, P, P, P, I, I, F, P, T, P, S, P]
@@ -536,12 +536,7 @@ def new_paged_cache(seqs, max_pages, num_k_pages, num_v_pages=None, Hq=1, Hkv=No
         k_ref=torch.zeros(num_k_pages, **i32), v_ref=torch.zeros(nv, **i32))
 
 
-def _paged_devices(named, device):
-    for t, n in named:
-        if not t.is_cuda:
-            raise TypeError("%s must be a CUDA tensor" % n)
-        if t.device != device:
-            raise ValueError("%s must be on %s" % (n, device))
+_I32_FIELDS = ("k_table", "v_table", "lens", "k_ref", "v_ref")
 
 
 def _paged_cache(cache, counts=False, Hq=None, on_gpu=True):
@@ -551,49 +546,85 @@ def _paged_cache(cache, counts=False, Hq=None, on_gpu=True):
     torch = _torch()
     if not isinstance(cache, PathPagedCache):
         raise TypeError("cache must be a PathPagedCache")
-    kp, vp, kt = cache.k_pages, cache.v_pages, cache.k_table
-    named = [(kp, "k_pages"), (vp, "v_pages"), (kt, "k_table"), (cache.v_table, "v_table"),
-             (cache.lens, "lens")]
-    if counts or cache.k_ref is not None or cache.v_ref is not None:
-        named += [(cache.k_ref, "k_ref"), (cache.v_ref, "v_ref")]
-    if cache.g_pages is not None:
-        named.append((cache.g_pages, "g_pages"))
-    for t, n in named:
-        if not isinstance(t, torch.Tensor):
+    kp, vp, gp = cache.k_pages, cache.v_pages, cache.g_pages
+    ints = (cache.k_table, cache.v_table, cache.lens, cache.k_ref, cache.v_ref)
+    used = 5 if counts or ints[3] is not None or ints[4] is not None else 3
+    Tensor, i32 = torch.Tensor, torch.int32
+    if not isinstance(kp, Tensor) or not isinstance(vp, Tensor):
+        raise TypeError("k_pages and v_pages must be tensors")
+    for t, n in zip(ints[:used], _I32_FIELDS):
+        if not isinstance(t, Tensor):
             raise TypeError("%s must be a tensor" % n)
-    if kp.dim() != 4 or vp.dim() != 4 or kp.shape[1:] != vp.shape[1:]:
+        if t.dtype != i32:
+            raise TypeError("%s must be %s, got %s" % (n, i32, t.dtype))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % n)
+    ks, vs = kp.shape, vp.shape
+    if len(ks) != 4 or len(vs) != 4 or ks[1:] != vs[1:]:
         raise ValueError("k_pages and v_pages must be (pages, Hkv, page, d) of equal pages")
     if vp.dtype != kp.dtype:
         raise TypeError("v_pages must be %s, got %s" % (kp.dtype, vp.dtype))
     dt = _dtype_code(kp)
-    nk, Hkv, page, d = kp.shape
-    if kt.dim() != 2 or cache.v_table.shape != kt.shape:
+    nk, Hkv, page, d = ks
+    ts = ints[0].shape
+    if len(ts) != 2 or ints[1].shape != ts:
         raise ValueError("k_table and v_table must be (seqs, max_pages) of equal shape")
-    seqs, max_pages = kt.shape
-    if cache.lens.shape != (seqs,):
+    seqs, max_pages = ts
+    if ints[2].shape != (seqs,):
         raise ValueError("lens must be (seqs,)")
-    for t, n in named[2:]:
-        want = torch.float32 if n == "g_pages" else torch.int32
-        if t.dtype != want:
-            raise TypeError("%s must be %s, got %s" % (n, want, t.dtype))
-    if len(named) > 5 and named[5][1] == "k_ref":
-        if cache.k_ref.shape != (nk,) or cache.v_ref.shape != (vp.shape[0],):
-            raise ValueError("k_ref and v_ref must hold one count per page")
-    if cache.g_pages is not None:
-        if cache.g_pages.dim() != 3 or cache.g_pages.shape[0] != nk or \
-                cache.g_pages.shape[2] != page or (Hq is not None and cache.g_pages.shape[1] != Hq):
+    if used == 5 and (ints[3].shape != (nk,) or ints[4].shape != (vs[0],)):
+        raise ValueError("k_ref and v_ref must hold one count per page")
+    if gp is not None:
+        if not isinstance(gp, Tensor):
+            raise TypeError("g_pages must be a tensor")
+        if gp.dtype != torch.float32:
+            raise TypeError("g_pages must be %s, got %s" % (torch.float32, gp.dtype))
+        gs = gp.shape
+        if len(gs) != 3 or gs[0] != nk or gs[2] != page or (Hq is not None and gs[1] != Hq):
             raise ValueError("g_pages must be (K pages, Hq, page)")
-        Hq = cache.g_pages.shape[1]
-    for t, n in named:
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % n)
+        if not gp.is_contiguous():
+            raise ValueError("g_pages must be contiguous")
+        Hq = gs[1]
+    if not kp.is_contiguous() or not vp.is_contiguous():
+        raise ValueError("k_pages and v_pages must be contiguous")
     if on_gpu:
-        _paged_devices(named, kp.device)
-    ptr = [t.data_ptr() if t is not None else None
-           for t in (kp, vp, cache.g_pages, kt, cache.v_table, cache.k_ref, cache.v_ref,
-                     cache.lens)]
-    return _CPagedCache(*ptr, seqs, max_pages, page, nk, vp.shape[0],
+        _paged_devices(cache)
+    return _CPagedCache(kp.data_ptr(), vp.data_ptr(), None if gp is None else gp.data_ptr(),
+                        *[t.data_ptr() for t in ints[:2]],
+                        *([t.data_ptr() for t in ints[3:]] if used == 5 else (None, None)),
+                        ints[2].data_ptr(), seqs, max_pages, page, nk, vs[0],
                         Hkv if Hq is None else Hq, Hkv, d, dt)
+
+
+def _paged_devices(cache, *more):
+    """Every tensor on the GPU that holds k_pages; `more`: tensors or None."""
+    dev = cache.k_pages.get_device()
+    for t in (cache.k_pages, cache.v_pages, cache.g_pages, cache.k_table, cache.v_table,
+              cache.lens, cache.k_ref, cache.v_ref) + more:
+        if t is not None and (t.get_device() != dev or not t.is_cuda):
+            if not t.is_cuda:
+                raise TypeError("the cache and the step's tensors must be CUDA tensors")
+            raise ValueError("the cache and the step's tensors must be on one device")
+
+
+class _on:
+    """The device and, where one is given, the stream of a call, as torch's current ones: what is
+    allocated inside belongs to the stream that the call runs on."""
+    __slots__ = ("guards",)
+
+    def __init__(self, dev, stream):
+        cuda = _torch().cuda
+        self.guards = [] if dev.index == cuda.current_device() else [cuda.device(dev)]
+        if stream is not None:
+            self.guards.append(cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+
+    def __exit__(self, *e):
+        for g in reversed(self.guards):
+            g.__exit__(*e)
 
 
 def path_paged_workspace_bytes(cache, num_tokens=0, max_chunk=0, Hq=None):
@@ -619,60 +650,56 @@ def new_paged_workspace(cache, num_tokens=0, max_chunk=0, Hq=None):
 def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, scale, out,
                   workspace, stream):
     torch = _torch()
+    Tensor, f32 = torch.Tensor, torch.float32
     kp = cache.k_pages if isinstance(cache, PathPagedCache) else None
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (w, "w"), (beta, "beta"), (cu_tokens, "cu_tokens"),
-                 (kp, "cache.k_pages")) + (((log_f, "log_f"),) if log_f is not None else ()):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a tensor" % n)
+    if not isinstance(q, Tensor) or not isinstance(kp, Tensor):
+        raise TypeError("q must be a tensor and cache a PathPagedCache of tensors")
     if q.dim() != 3:
         raise ValueError("q must be (tokens, Hq, d)")
     if kp.dim() != 4:
         raise ValueError("k_pages must be (pages, Hkv, page, d)")
-    N, Hq, d = q.shape
-    Hkv = kp.shape[1]
-    new_out = out is None
-    if new_out:
-        out = torch.empty((N, Hq, d), dtype=q.dtype, device="meta")
-    f32, dt, dev = torch.float32, kp.dtype, kp.device
+    qs = q.shape
+    N, Hq, d = qs
+    Hkv, dt, dev = kp.shape[1], kp.dtype, kp.device
     c = _paged_cache(cache, Hq=Hq, on_gpu=False)
-    row = [(q, "q", (N, Hq, d), dt), (k, "k", (N, Hkv, d), dt), (v, "v", (N, Hkv, d), dt),
-           (w, "w", (N, Hkv, d), dt), (beta, "beta", (N, Hkv), f32),
-           (log_f, "log_f", (N, Hq), f32), (out, "out", (N, Hq, d), dt),
-           (cu_tokens, "cu_tokens", (c.seqs + 1,), torch.int32)]
+    ks, bs = (N, Hkv, d), (N, Hkv)
     st = []
-    for t, n, shape, want in row:
-        if t is None:
-            st += [0, 0]
+    for t, n, shape, want in ((q, "q", qs, dt), (k, "k", ks, dt), (v, "v", ks, dt), (w, "w", ks, dt),
+                              (beta, "beta", bs, f32), (log_f, "log_f", qs[:2], f32),
+                              (out, "out", qs, dt)):
+        if t is None and (n == "log_f" or n == "out"):
+            st += (0, 0) if n == "log_f" else (Hq * d, d)
             continue
+        if not isinstance(t, Tensor):
+            raise TypeError("%s must be a tensor" % n)
         if t.dtype != want:
             raise TypeError("%s must be %s, got %s" % (n, want, t.dtype))
-        if tuple(t.shape) != shape:
-            raise ValueError("%s must have shape %s, got %s" % (n, shape, tuple(t.shape)))
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s, got %s" % (n, tuple(shape), tuple(t.shape)))
         s = t.stride()
-        if t.dim() == 3 and s[2] != 1 or n == "cu_tokens" and s[0] != 1:
+        if len(s) == 3 and s[2] != 1:
             raise ValueError("the last axis of %s must be contiguous" % n)
-        if n != "cu_tokens":  # the stride of an axis of one element says nothing
-            st += [s[0] if t.shape[0] > 1 else 0, s[1] if t.shape[1] > 1 else 0]
+        # the stride of an axis of one element says nothing
+        st += (s[0] if N > 1 else 0, s[1] if shape[1] > 1 else 0)
+    if not isinstance(cu_tokens, Tensor) or cu_tokens.dtype != torch.int32:
+        raise TypeError("cu_tokens must be an int32 tensor")
+    if cu_tokens.shape != (c.seqs + 1,) or not cu_tokens.is_contiguous():
+        raise ValueError("cu_tokens must be (seqs + 1,), contiguous")
     if d != c.d:
         raise ValueError("q has head size %d, the cache %d" % (d, c.d))
-    if out.numel() and (N > 1 and out.stride(0) == 0 or Hq > 1 and out.stride(1) == 0):
+    if out is not None and out.numel() and (N > 1 and st[12] == 0 or Hq > 1 and st[13] == 0):
         raise ValueError("out must not repeat its own memory")
-    _paged_devices([(t, n) for t, n in [(getattr(cache, f.name), f.name)
-                                        for f in dataclasses.fields(cache)] +
-                    [(r[0], r[1]) for r in row if not (new_out and r[1] == "out")]
-                    if t is not None], dev)
-    strides = _CPagedStrides(*[(ctypes.c_int64 * 2)(*st[i:i + 2]) for i in range(0, 14, 2)])
+    _paged_devices(cache, q, k, v, w, beta, log_f, out, cu_tokens)
     gate = () if log_f is None else (log_f.data_ptr(),)
-    # what is allocated here belongs to the stream that the call runs on
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
-        if new_out:
-            out = torch.empty((N, Hq, d), dtype=dt, device=dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(qs, dtype=dt, device=dev)
         if workspace is None and N > 0 and c.seqs > 0:
             workspace = new_paged_workspace(cache, N, max_chunk, Hq)
         _check(getattr(_load(), name)(
             ctypes.byref(c), q.data_ptr(), k.data_ptr(), v.data_ptr(), w.data_ptr(),
             beta.data_ptr(), *gate, cu_tokens.data_ptr(), N, int(max_chunk), _scale(scale, d),
-            out.data_ptr(), ctypes.byref(strides), _ptr(workspace),
+            out.data_ptr(), _C14(*st), None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel(), _stream(stream, dev)), name)
     return out
 
@@ -702,10 +729,9 @@ def path_fox_paged_extend(q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, 
 
 
 def _paged_call(name, cache, workspace, stream, *args):
-    torch = _torch()
     c = _paged_cache(cache, counts=True)
     dev = cache.k_pages.device
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
+    with _on(dev, stream):
         if workspace is None:
             workspace = new_paged_workspace(cache)
         _check(getattr(_load(), name)(ctypes.byref(c), *args, workspace.data_ptr(),

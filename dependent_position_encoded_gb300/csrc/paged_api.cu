@@ -97,7 +97,8 @@ size_t step_ws_bytes(const path_paged_cache *p, int N, int max_chunk, bool fox) 
 path_status check_step_sizes(const path_paged_cache *p, int N, int max_chunk) {
     if (N < 0 || N > PATH_MAX_LEN || max_chunk < 0 || max_chunk > N) return PATH_ERR_SHAPE;
     if (N > 0 && max_chunk < 1) return PATH_ERR_SHAPE;
-    (void)p;
+    // rows of a key head (query heads that share it, taken together) are counted in an int
+    if ((long long)N * (p->Hq / p->Hkv) > INT_MAX / 2) return PATH_ERR_SHAPE;
     return PATH_OK;
 }
 

@@ -91,13 +91,15 @@ __device__ __forceinline__ void tmem_scale(uint32_t taddr, float f) {
 constexpr float kRescale = 8.f;  // the running maximum may lag by 2^8 before O is rescaled
 
 // ================================================================ cached keys
-// A CTA takes NT tiles of 128 rows of one sequence and key head and a range of key tiles of
-// 128 positions. Keys and values stream through one ring of shared-memory slots (TMA, one
-// box per page; a slot holds 128 rows of D bf16 in 128-byte-swizzled atoms of 64 columns).
-// Per key tile and row tile: S = X K^T (N = 128) into TMEM, softmax by the 128 threads of a
-// warpgroup, one row each, which write the weights as bf16 over S, and O += P V with the
-// weights as the A operand in TMEM. With NT = 2 the two row tiles share every slot and take
-// turns on the tensor core, one in its softmax while the other multiplies.
+// Persistent: a CTA walks its stretches of units (paged_tc.cuh), each of them one item: NT tiles
+// of 128 rows of one sequence and key head against consecutive key tiles of 128 positions. Keys
+// and values stream through one ring of shared-memory slots (TMA, one box per page; a slot
+// holds 128 rows of D bf16 in 128-byte-swizzled atoms of 64 columns), which runs on from
+// stretch to stretch, as every barrier's phase does. Per key tile and row tile: S = X K^T (N =
+// 128) into TMEM, softmax by the 128 threads of a warpgroup, one row each, which write the
+// weights as bf16 over S, and O += P V with the weights as the A operand in TMEM. With NT = 2
+// the two row tiles share every slot and take turns on the tensor core, one in its softmax
+// while the other multiplies.
 //
 // NT = 1 is for sequences whose rows fit one tile (a few tokens: bound by the cache's bytes)
 // and updates the keys too: a second MMA forms K (P - I) with the loaded keys as the A operand
@@ -105,36 +107,52 @@ constexpr float kRescale = 8.f;  // the running maximum may lag by 2^8 before O 
 // memory and stores them back, so each key is read once and written once.
 //
 // Warps: 0-3 softmax of tile 0; 4-7 softmax of tile 1 (NT = 2) or the keys' update (NT = 1); 8
-// allocates TMEM and issues the MMAs; 9 streams the pages.
+// allocates TMEM and issues the MMAs; 9 streams the pages. (NT = 2 has two more warps without
+// a role, so that the last warpgroup can give registers to the softmax.)
 // Positions past the sequence's n and those on bad pages: the streaming warp zeroes their rows
 // after the copy, and the softmax masks them.
 template <int NT, int D>
-struct CachedSmem {
+struct CachedCfg {
     static constexpr uint32_t tile = 128 * D * 2, atom = 128 * 128;
     static constexpr uint32_t X = 0, M = X + NT * tile, mbytes = NT == 1 ? 2 * D * D * 2 : 0;
     // slots: what fits beside; for NT = 1 and D = 64 so that two CTAs share an SM
     static constexpr int slots = NT == 1 ? 4 : (D == 64 ? 8 : 5);
     static constexpr uint32_t ring = M + mbytes, bars = ring + slots * tile;
-    static constexpr int FULL = 0, EMPTY = slots, XF = 2 * slots, SF = XF + 1, PR = SF + 2, FIN = PR + 2,
-                         DF = FIN + 1, DE = DF + 1, TMP = DE + 1, count = TMP + 1;
+    static constexpr int FULL = 0, EMPTY = slots, XF = 2 * slots, XE = XF + 1, SF = XE + 1, PR = SF + 2, FIN = PR + 2,
+                         DF = FIN + 2, DE = DF + 1, TMP = DE + 1, END = TMP + 1, count = END + 1;
     static constexpr uint32_t bytes = bars + count * 8 + 16, alloc = bytes + 1024;
+    static constexpr int threads = NT == 2 ? 384 : 320;
+    static constexpr int ctas_per_sm = NT == 1 && D == 64 ? 2 : 1;
+    // registers after the split (NT = 2: launched with 168 each)
+    static constexpr int reg_row = 208, reg_other = 80;
+    // TMEM columns: per row tile S 128 (the weights over it) and O; NT = 1: the update's product
+    static constexpr uint32_t cS = 0, cO = 128, per_tile = 256, cD = 128 + D;
+    static constexpr uint32_t cols = NT == 1 && D == 64 ? 256 : 512;
 };
+static_assert(CachedCfg<1, 128>::alloc <= 227 * 1024 && CachedCfg<2, 128>::alloc <= 227 * 1024, "shared memory");
+static_assert(256 * CachedCfg<2, 64>::reg_row + 128 * CachedCfg<2, 64>::reg_other <= 384 * 168, "registers");
 
-template <int NT, int D>
-struct CachedTmem {
-    static constexpr uint32_t S = 0, O = 128, per_tile = 256, Dt = O + D;  // Dt: NT = 1 only
-    static constexpr uint32_t cols = NT == 2 ? 512 : (D == 64 ? 256 : 512);
-};
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
 
-constexpr int kCachedThr = 320;
+// Whether all boxes of a key tile lie on good pages below n: `have` one bit per box of
+// 1 << box_shift rows.
+__device__ __forceinline__ bool tile_whole(int pos0, int n, unsigned have, int box_shift) {
+    return pos0 + 128 <= n && have == (1u << (128 >> box_shift)) - 1u;
+}
 
 template <int NT, int D, bool FOX>
-__global__ void __launch_bounds__(kCachedThr, (NT == 1 && D == 64) ? 2 : 1)
+__global__ void __launch_bounds__(CachedCfg<NT, D>::threads, CachedCfg<NT, D>::ctas_per_sm)
 tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap tm_x,
                  const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
-    using L = CachedSmem<NT, D>;
-    using C = CachedTmem<NT, D>;
+    using L = CachedCfg<NT, D>;
     constexpr int NA = D / 64, NS = L::slots;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -143,17 +161,11 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
     uint32_t *const tslot = reinterpret_cast<uint32_t *>(sm + L::bars + 8 * L::count);
     volatile uint32_t *const abort_f = tslot + 1;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y, G = a.c.G;
-    int b, ti;
-    Seq s;
-    if (!tile_of(a, blockIdx.x, 128 * NT, b, ti, s)) return;
-    const int rows_all = s.T * G;
-    if ((rows_all <= 128) != (NT == 1)) return;  // the other kernel's
-    const int ktiles = (s.n + 127) / 128, per = (ktiles + y.splits - 1) / y.splits;
-    const int k0 = blockIdx.z * per, k1 = min(ktiles, k0 + per), steps = k1 - k0;
-    if (steps <= 0) return;
-    const int row0 = 128 * NT * ti;                                // first row within the sequence
-    const bool two = NT == 2 && row0 + 128 < rows_all;             // the second tile has rows
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.c.G;
+    const Plan plan = y.plan[NT - 1];
+    const long long all = plan.units[a.c.seqs], per = plan_per(plan, a.c.seqs);
+    const long long u_begin = (long long)blockIdx.x * per, u_end = u_begin + per < all ? u_begin + per : all;
+    if (u_begin >= u_end) return;
     const Wait wait{abort_f, a.status, limit_ns};
 
     if (tid == 0) {
@@ -162,335 +174,392 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
         fence_mbar_init();
     }
     if (warp == 8) {
-        tmem_alloc(smem_u32(tslot), C::cols);
+        tmem_alloc(smem_u32(tslot), L::cols);
         tmem_relinquish();
         tc_fence_before();
     }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    auto slot_at = [&](int u) { return base + L::ring + (uint32_t)(u % NS) * L::tile; };
-    // Ring use u: keys of step j at u = 2 j, its values at u = 2 j + 1.
+    // Ring use u: keys of step j at u = 2 j, its values at u = 2 j + 1, j counted over all
+    // stretches of the CTA.
+    auto slot_at = [&](uint32_t u) { return base + L::ring + (u % NS) * L::tile; };
+    auto second = [&](const Stretch &t) { return NT == 2 && t.tile * 256 + 128 < t.s.T * G; };
+    const int page = a.c.page, box_shift = min(a.c.page_shift, 7), box = 1 << box_shift, nbox = 128 >> box_shift;
 
-    if (warp == 9) {
-        // ============================================================ pages into the ring
-        int issued = 0;
-        bool ok = true;
-        if (lane == 0) {
-            const int xr = (int)((long long)s.first * G) + row0;
-            mbar_arrive_expect_tx(bar(L::XF), (two ? 2 : 1) * L::tile + L::mbytes);
-            for (int t = 0; t < (two ? 2 : 1); ++t)
-                for (int x = 0; x < NA; ++x)
-                    tma_load_3d(base + L::X + t * L::tile + x * L::atom, &tm_x, bar(L::XF), 64 * x, xr + 128 * t, h);
-            if (NT == 1)
-                for (int p = 0; p < 2; ++p)
-                    for (int x = 0; x < NA; ++x)
-                        tma_load_3d(base + L::M + (uint32_t)(p * NA + x) * D * 128, &tm_m, bar(L::XF), 64 * x, 0,
-                                    (b * a.c.Hkv + h) * 2 + p);
-        }
-        const int page = a.c.page, box_shift = min(a.c.page_shift, 7), box = 1 << box_shift, nbox = 128 / box;
-        uint32_t tmp_phase = 0;
-        for (int u = 0; ok && u < 2 * steps; ++u) {
-            const bool keys = (u & 1) == 0;
-            const int pos0 = (k0 + (u >> 1)) * 128;
-            // lane i < nbox: the page of box i, -1 past the end or where it is bad
-            int id = -1;
-            if (lane < nbox && pos0 + lane * box < s.n)
-                id = page_of(a, keys ? a.c.k_table : a.c.v_table, b, (pos0 + lane * box) >> a.c.page_shift,
-                             keys ? a.c.nk : a.c.nv);
-            const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
-            const int valid = min(128, s.n - pos0);
-            const bool whole = valid == 128 && have == (1u << nbox) - 1u;
-            if (u >= NS && !(ok = wait.warp(bar(L::EMPTY + u % NS), ((u / NS) & 1) ^ 1))) break;
-            const uint32_t dst = slot_at(u);
-            const uint32_t full = bar(L::FULL + u % NS), target = whole ? full : bar(L::TMP);
-            if (lane == 0) mbar_arrive_expect_tx(target, (uint32_t)__popc(have) * box * D * 2);
-            __syncwarp();
-            if (id >= 0)
-#pragma unroll
-                for (int x = 0; x < NA; ++x)
-                    tma_load_3d(dst + x * L::atom + lane * box * 128, keys ? &tm_k : &tm_v, target, 64 * x,
-                                (pos0 + lane * box) & (page - 1), id * a.c.Hkv + h);
-            if (!whole) {
-                // zero the rows that hold no cached position, then hand the slot on
-                if (!(ok = wait.warp(bar(L::TMP), tmp_phase))) break;
-                tmp_phase ^= 1;
-                uint8_t *const rowp = sm + (dst - base);
-                for (int r = 0; r < 128; ++r) {
-                    if (r < valid && ((have >> (r >> box_shift)) & 1u)) continue;
-                    if (lane < NA * 8)
-                        *reinterpret_cast<uint4 *>(rowp + (lane >> 3) * L::atom + r * 128 + (lane & 7) * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
+    if (warp >= 8) {
+        if (NT == 2) reg_dec<L::reg_other>();
+        if (warp == 9) {
+            // ======================================================== pages into the ring
+            uint32_t u = 0, seg = 0, tmp_phase = 0;
+            bool ok = true;
+            for (long long at = u_begin; ok && at < u_end; ++seg) {
+                const Stretch t = stretch_at(a, plan, NT, at, u_end);
+                at += t.steps;
+                // the rows' tile (and the update's product) once the last stretch's are read
+                if (seg > 0 && !(ok = wait.warp(bar(L::XE), (seg - 1) & 1))) break;
+                if (lane == 0) {
+                    const int nx = second(t) ? 2 : 1, xr = t.s.first * G + 128 * NT * t.tile;
+                    mbar_arrive_expect_tx(bar(L::XF), nx * L::tile + L::mbytes);
+                    for (int i = 0; i < nx; ++i)
+                        for (int x = 0; x < NA; ++x)
+                            tma_load_3d(base + L::X + i * L::tile + x * L::atom, &tm_x, bar(L::XF), 64 * x,
+                                        xr + 128 * i, t.h);
+                    if (NT == 1)
+                        for (int p = 0; p < 2; ++p)
+                            for (int x = 0; x < NA; ++x)
+                                tma_load_3d(base + L::M + (uint32_t)(p * NA + x) * D * 128, &tm_m, bar(L::XF), 64 * x,
+                                            0, (t.b * a.c.Hkv + t.h) * 2 + p);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full);
+                for (int i = 0; ok && i < 2 * t.steps; ++i, ++u) {
+                    const bool keys = (i & 1) == 0;
+                    const int pos0 = (t.k0 + (i >> 1)) * 128;
+                    // lane i < nbox: the page of box i, -1 past the end or where it is bad
+                    int id = -1;
+                    if (lane < nbox && pos0 + lane * box < t.s.n)
+                        id = page_of(a, keys ? a.c.k_table : a.c.v_table, t.b, (pos0 + lane * box) >> a.c.page_shift,
+                                     keys ? a.c.nk : a.c.nv);
+                    const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
+                    const int valid = min(128, t.s.n - pos0);
+                    const bool whole = tile_whole(pos0, t.s.n, have, box_shift);
+                    if (u >= NS && !(ok = wait.warp(bar(L::EMPTY + u % NS), ((u / NS) & 1) ^ 1))) break;
+                    const uint32_t dst = slot_at(u);
+                    const uint32_t full = bar(L::FULL + u % NS), target = whole ? full : bar(L::TMP);
+                    if (lane == 0) mbar_arrive_expect_tx(target, (uint32_t)__popc(have) * box * D * 2);
+                    __syncwarp();
+                    if (id >= 0)
+#pragma unroll
+                        for (int x = 0; x < NA; ++x)
+                            tma_load_3d(dst + x * L::atom + lane * box * 128, keys ? &tm_k : &tm_v, target, 64 * x,
+                                        (pos0 + lane * box) & (page - 1), id * a.c.Hkv + t.h);
+                    if (!whole) {
+                        // zero the rows that hold no cached position, then hand the slot on
+                        if (!(ok = wait.warp(bar(L::TMP), tmp_phase))) break;
+                        tmp_phase ^= 1;
+                        uint8_t *const rowp = sm + (dst - base);
+                        for (int r = 0; r < 128; ++r) {
+                            if (r < valid && ((have >> (r >> box_shift)) & 1u)) continue;
+                            if (lane < NA * 8)
+                                *reinterpret_cast<uint4 *>(rowp + (lane >> 3) * L::atom + r * 128 + (lane & 7) * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full);
+                    }
+                }
             }
-            issued = u + 1;
-        }
-        // on an abort: no copy may land after the CTA is gone
-        if (!ok) {
-            const int from = issued > NS ? issued - NS : 0;
-            for (int u = from; u < issued; ++u) mbar_wait(bar(L::FULL + u % NS), (u / NS) & 1, limit_ns);
-            mbar_wait(bar(L::XF), 0, limit_ns);
-        }
-    } else if (warp == 8) {
-        // ============================================================ MMA issue
-        if (lane == 0) {
+            // on an abort: no copy may land after the CTA is gone. The slots' last uses, the one
+            // that broke off among them (its copies signal TMP or FULL, or were never sent)
+            if (!ok) {
+                for (uint32_t v = u > NS ? u - NS : 0; v < u; ++v)
+                    mbar_wait(bar(L::FULL + v % NS), (v / NS) & 1, limit_ns);
+                mbar_wait(bar(L::XF), seg & 1, limit_ns);
+            }
+        } else if (warp == 8 && lane == 0) {
+            // ======================================================== MMA issue
             constexpr uint32_t ID_S = idesc_b16(128, 128, false), ID_O = idesc_b16(128, D, true);
-            bool ok = wait(bar(L::XF), 0);
-            auto issue_s = [&](int t, int j) {
-                const uint32_t kb = slot_at(2 * j);
+            uint32_t j = 0, j1 = 0, seg = 0;  // steps of the first and of the second row tile
+            bool ok = true;
+            auto issue_s = [&](int t, uint32_t js) {
+                const uint32_t kb = slot_at(2 * js);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16(tmem + C::per_tile * t + C::S,
+                    umma_bf16(tmem + L::per_tile * t + L::cS,
                               sdesc_sw128(base + L::X + t * L::tile + (kk >> 2) * L::atom, 16, 1024) + 2 * (kk & 3),
                               sdesc_sw128(kb + (kk >> 2) * L::atom, 16, 1024) + 2 * (kk & 3), ID_S, kk > 0);
                 umma_commit(bar(L::SF + t));
             };
-            auto issue_pv = [&](int t, int j) {
-                const uint64_t v = sdesc_sw128(slot_at(2 * j + 1), L::atom, 1024);
+            auto issue_pv = [&](int t, uint32_t js, bool first) {
+                const uint64_t v = sdesc_sw128(slot_at(2 * js + 1), L::atom, 1024);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    umma_tA(tmem + C::per_tile * t + C::O, tmem + C::per_tile * t + C::S + 8 * kk, v + 128 * kk, ID_O,
-                            j > 0 || kk > 0);
+                    umma_tA(tmem + L::per_tile * t + L::cO, tmem + L::per_tile * t + L::cS + 8 * kk, v + 128 * kk,
+                            ID_O, !first || kk > 0);
             };
-            auto keys_ready = [&](int j) { return wait(bar(L::FULL + (2 * j) % NS), ((2 * j) / NS) & 1); };
-            auto issue_update = [&](int j) {  // K (P - I): the keys are the A operand
-                if (j > 0 && !wait(bar(L::DE), (j - 1) & 1)) return false;
+            auto keys_ready = [&](uint32_t js) { return wait(bar(L::FULL + (2 * js) % NS), ((2 * js) / NS) & 1); };
+            auto issue_update = [&](uint32_t js) {  // K (P - I): the keys are the A operand
+                if (js > 0 && !wait(bar(L::DE), (js - 1) & 1)) return false;
                 tc_fence_after();
-                const uint32_t kb = slot_at(2 * j);
+                const uint32_t kb = slot_at(2 * js);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     const uint64_t m = sdesc_sw128(base + L::M + p * NA * D * 128, D * 128, 1024);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        umma_bf16(tmem + C::Dt, sdesc_sw128(kb + (kk >> 2) * L::atom, 16, 1024) + 2 * (kk & 3),
+                        umma_bf16(tmem + L::cD, sdesc_sw128(kb + (kk >> 2) * L::atom, 16, 1024) + 2 * (kk & 3),
                                   m + 128 * kk, ID_O, p > 0 || kk > 0);
                 }
                 umma_commit(bar(L::DF));
                 return true;
             };
-            if (ok && (ok = keys_ready(0))) {
+            // the keys' products of step js (the caller has seen the keys arrive); last of a stretch:
+            // the rows' tile is free behind them
+            auto after_s = [&](uint32_t js, bool last) {
+                bool fine = true;
+                if (NT == 1) fine = issue_update(js);
+                else umma_commit(bar(L::EMPTY + (2 * js) % NS));
+                if (last) umma_commit(bar(L::XE));
+                return fine;
+            };
+            for (long long at = u_begin; ok && at < u_end; ++seg) {
+                const Stretch t = stretch_at(a, plan, NT, at, u_end);
+                at += t.steps;
+                const bool two = second(t);
+                if (!(ok = wait(bar(L::XF), seg & 1)) || !(ok = keys_ready(j))) break;
                 tc_fence_after();
-                issue_s(0, 0);
-                if (two) issue_s(1, 0);
-                if (NT == 1) ok = issue_update(0);
-                else umma_commit(bar(L::EMPTY + 0));
-            }
-            for (int j = 0; ok && j < steps; ++j) {
-                const int vs = (2 * j + 1) % NS;
-                if (!(ok = wait(bar(L::FULL + vs), ((2 * j + 1) / NS) & 1))) break;
-                for (int t = 0; t < (two ? 2 : 1); ++t) {
-                    if (!(ok = wait(bar(L::PR + t), j & 1))) break;
-                    tc_fence_after();
-                    issue_pv(t, j);
-                    if (t == (two ? 1 : 0)) umma_commit(bar(L::EMPTY + vs));
-                    if (j + 1 < steps) {
-                        if (t == 0 && !(ok = keys_ready(j + 1))) break;
-                        if (t == 0) tc_fence_after();
-                        issue_s(t, j + 1);
+                issue_s(0, j);
+                if (two) issue_s(1, j);
+                ok = after_s(j, t.steps == 1);
+                for (int i = 0; ok && i < t.steps; ++i, ++j) {
+                    const uint32_t vs = (2 * j + 1) % NS;
+                    if (!(ok = wait(bar(L::FULL + vs), ((2 * j + 1) / NS) & 1))) break;
+                    for (int q = 0; q < (two ? 2 : 1); ++q) {
+                        if (!(ok = wait(bar(L::PR + q), (q ? j1 : j) & 1))) break;
+                        tc_fence_after();
+                        issue_pv(q, j, i == 0);
+                        if (q == (two ? 1 : 0)) umma_commit(bar(L::EMPTY + vs));
+                        if (i + 1 < t.steps) {
+                            if (q == 0 && !(ok = keys_ready(j + 1))) break;
+                            if (q == 0) tc_fence_after();
+                            issue_s(q, j + 1);
+                        }
                     }
+                    if (!ok) break;
+                    j1 += two;
+                    if (i + 1 < t.steps) ok = after_s(j + 1, i + 2 == t.steps);
                 }
-                if (!ok) break;
-                if (j + 1 < steps) {
-                    if (NT == 1) ok = issue_update(j + 1);
-                    else umma_commit(bar(L::EMPTY + (2 * j + 2) % NS));
-                }
+                // a barrier per row tile: the second has a phase only where it has rows, so neither
+                // can run ahead of the warps that wait for it
+                umma_commit(bar(L::FIN));
+                if (two) umma_commit(bar(L::FIN + 1));
             }
-            umma_commit(bar(L::FIN));
-            mbar_wait(bar(L::FIN), 0, limit_ns);
+            // every product has completed before TMEM is freed
+            umma_commit(bar(L::END));
+            mbar_wait(bar(L::END), 0, limit_ns);
         }
     } else if (NT == 1 && warp >= 4) {
         // ============================================================ the keys' update
         const int r = tid - 128;
-        const uint32_t tm = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + C::Dt;
-        const int page = a.c.page, box_shift = min(a.c.page_shift, 7), box = 1 << box_shift, nbox = 128 / box;
+        const uint32_t tm = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + L::cD;
         bool ok = true;
-        for (int j = 0; j < steps; ++j) {
-            const int pos0 = (k0 + j) * 128;
-            int id = -1;
-            if (lane < nbox && pos0 + lane * box < s.n)
-                id = page_of(a, a.c.k_table, b, (pos0 + lane * box) >> a.c.page_shift, a.c.nk);
-            const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
-            const bool whole = pos0 + 128 <= s.n && have == (1u << nbox) - 1u;
-            const int mine = __shfl_sync(0xffffffffu, id, r >> box_shift);
-            if (!(ok = wait.warp(bar(L::DF), j & 1))) break;
-            tc_fence_after();
-            uint8_t *const kt = sm + (slot_at(2 * j) - base);
-            bf *const dst = mine >= 0 && pos0 + r < s.n
-                                ? static_cast<bf *>(a.c.k_pages) +
-                                      ((((size_t)mine * a.c.Hkv + h) << a.c.page_shift) + ((pos0 + r) & (page - 1))) * D
-                                : nullptr;
+        uint32_t j = 0;
+        for (long long at = u_begin; ok && at < u_end;) {
+            const Stretch t = stretch_at(a, plan, NT, at, u_end);
+            at += t.steps;
+            for (int i = 0; i < t.steps; ++i, ++j) {
+                const int pos0 = (t.k0 + i) * 128;
+                int id = -1;
+                if (lane < nbox && pos0 + lane * box < t.s.n)
+                    id = page_of(a, a.c.k_table, t.b, (pos0 + lane * box) >> a.c.page_shift, a.c.nk);
+                const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
+                const bool whole = tile_whole(pos0, t.s.n, have, box_shift);
+                const int mine = __shfl_sync(0xffffffffu, id, r >> box_shift);
+                if (!(ok = wait.warp(bar(L::DF), j & 1))) break;
+                tc_fence_after();
+                uint8_t *const kt = sm + (slot_at(2 * j) - base);
+                bf *const dst = mine >= 0 && pos0 + r < t.s.n
+                                    ? static_cast<bf *>(a.c.k_pages) +
+                                          ((((size_t)mine * a.c.Hkv + t.h) << a.c.page_shift) +
+                                           ((pos0 + r) & (page - 1))) * D
+                                    : nullptr;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float x[32];
-                tld32(tm + c, x);
+                for (int c = 0; c < D; c += 32) {
+                    float x[32];
+                    tld32(tm + c, x);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint4 *at = reinterpret_cast<uint4 *>(kt + (c >> 6) * L::atom + sw128_offset(r, ((c & 63) >> 3) + q));
-                    const uint4 k4 = *at;
-                    const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
-                    uint32_t o[4];
+                    for (int q = 0; q < 4; ++q) {
+                        uint4 *p4 =
+                            reinterpret_cast<uint4 *>(kt + (c >> 6) * L::atom + sw128_offset(r, ((c & 63) >> 3) + q));
+                        const uint4 k4 = *p4;
+                        const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+                        uint32_t o[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 k2 = unpack_bf16x2(w[e]);
-                        o[e] = pack_bf16x2(k2.x + x[8 * q + 2 * e], k2.y + x[8 * q + 2 * e + 1]);
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 k2 = unpack_bf16x2(w[e]);
+                            o[e] = pack_bf16x2(k2.x + x[8 * q + 2 * e], k2.y + x[8 * q + 2 * e + 1]);
+                        }
+                        const uint4 v = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (whole) *p4 = v;
+                        else if (dst) *reinterpret_cast<uint4 *>(dst + c + 8 * q) = v;
                     }
-                    const uint4 v = make_uint4(o[0], o[1], o[2], o[3]);
-                    if (whole) *at = v;
-                    else if (dst) *reinterpret_cast<uint4 *>(dst + c + 8 * q) = v;
                 }
-            }
-            tc_fence_before();
-            mbar_arrive_warp(bar(L::DE));
-            fence_proxy_async_smem();
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (warp == 4) {
-                if (whole && id >= 0) {
+                tc_fence_before();
+                mbar_arrive_warp(bar(L::DE));
+                fence_proxy_async_smem();
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (warp == 4) {
+                    if (whole && id >= 0) {
 #pragma unroll
-                    for (int x = 0; x < NA; ++x)
-                        tma_store_3d(&tm_k, slot_at(2 * j) + x * L::atom + lane * box * 128, 64 * x,
-                                     (pos0 + lane * box) & (page - 1), id * a.c.Hkv + h);
-                    bulk_wait_read();
+                        for (int x = 0; x < NA; ++x)
+                            tma_store_3d(&tm_k, slot_at(2 * j) + x * L::atom + lane * box * 128, 64 * x,
+                                         (pos0 + lane * box) & (page - 1), id * a.c.Hkv + t.h);
+                        bulk_wait_read();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::EMPTY + (2 * j) % NS));
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::EMPTY + (2 * j) % NS));
             }
         }
         if (warp == 4) bulk_wait_all();
-    } else if (warp < 4 || two) {
+    } else {
         // ============================================================ softmax
-        const int t = warp >> 2, r = 128 * t + (tid & 127);
-        const uint32_t tm = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C::per_tile * t;
-        const bool live = row0 + r < rows_all;
-        const bool warp_live = row0 + 128 * t + 32 * (warp & 3) < rows_all;
-        const size_t row = (size_t)h * y.R + (size_t)s.first * G + row0 + r;
-        const int hq = h * G + (live ? (row0 + r) % G : 0);
-        const float gq = FOX && live ? y.gq[row] * kLog2e : 0.f;
+        if (NT == 2) reg_inc<L::reg_row>();
         constexpr bool kTwice = NT == 1 || FOX;
-        const int page = a.c.page, box_shift = min(a.c.page_shift, 7), box = 1 << box_shift, nbox = 128 / box;
-        float m_run = -INFINITY, l_run = 0.f;
+        const int w = warp >> 2, r = tid & 127;  // row tile and row in it
+        const uint32_t tm = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + L::per_tile * w;
         bool ok = true;
-        for (int j = 0; j < steps; ++j) {
-            const int pos0 = (k0 + j) * 128;
-            int id = -1;
-            bool good = false;
-            if (lane < nbox && pos0 + lane * box < s.n) {
-                const int sl = (pos0 + lane * box) >> a.c.page_shift;
-                const size_t at = (size_t)b * a.c.max_pages + sl;
-                id = __ldg(a.c.k_table + at);
-                good = (unsigned)id < (unsigned)a.c.nk && (unsigned)__ldg(a.c.v_table + at) < (unsigned)a.c.nv;
-            }
-            const unsigned have = __ballot_sync(0xffffffffu, good);
-            const int valid = min(128, s.n - pos0);
-            const bool whole = valid == 128 && have == (1u << nbox) - 1u;
-            if (!(ok = wait.warp(bar(L::SF + t), j & 1))) break;
-            tc_fence_after();
-            if (warp_live) {
-                // 32 logits of the row from column c: scaled, gated and masked
-                auto logits = [&](int c, float *x) {
-                    uint32_t u[32];
-                    tmem_ld32(tm + C::S + c, u);
-                    tmem_ld_wait();
+        uint32_t j = 0, seg = 0;  // steps and stretches that this row tile takes part in
+        for (long long at = u_begin; ok && at < u_end;) {
+            const Stretch t = stretch_at(a, plan, NT, at, u_end);
+            at += t.steps;
+            if (w == 1 && !second(t)) continue;
+            const int rows_all = t.s.T * G, row0 = 128 * (NT * t.tile + w);
+            const bool live = row0 + r < rows_all, warp_live = row0 + 32 * (warp & 3) < rows_all;
+            const int hq = t.h * G + (live ? (row0 + r) % G : 0);
+            const float gq =
+                FOX && live ? y.gq[(size_t)t.h * y.R + (size_t)t.s.first * G + row0 + r] * kLog2e : 0.f;
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int i = 0; i < t.steps; ++i, ++j) {
+                const int pos0 = (t.k0 + i) * 128;
+                int id = -1;
+                bool good = false;
+                if (lane < nbox && pos0 + lane * box < t.s.n) {
+                    const size_t e = (size_t)t.b * a.c.max_pages + ((pos0 + lane * box) >> a.c.page_shift);
+                    id = __ldg(a.c.k_table + e);
+                    good = (unsigned)id < (unsigned)a.c.nk && (unsigned)__ldg(a.c.v_table + e) < (unsigned)a.c.nv;
+                }
+                const unsigned have = __ballot_sync(0xffffffffu, good);
+                const int valid = min(128, t.s.n - pos0);
+                const bool whole = tile_whole(pos0, t.s.n, have, box_shift);
+                if (!(ok = wait.warp(bar(L::SF + w), j & 1))) break;
+                tc_fence_after();
+                if (warp_live) {
+                    // gates and mask of 32 logits of the row from column c
+                    auto gate = [&](int c, float *x) {
+                        if (FOX) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(u[e]) * a.scale_log2;
-                    if (FOX) {
+                            for (int e = 0; e < 32; e += 16) {  // 16 positions lie in one page
+                                const int bx = (c + e) >> box_shift;
+                                const int pid = __shfl_sync(0xffffffffu, id, bx);
+                                const bool in = (have >> bx) & 1u;
+                                const float4 *gp = reinterpret_cast<const float4 *>(
+                                    a.c.g_pages + (((size_t)(in ? pid : 0) * a.c.Hq + hq) << a.c.page_shift) +
+                                    ((pos0 + c + e) & (page - 1)));
 #pragma unroll
-                        for (int e = 0; e < 32; e += 16) {  // 16 positions lie in one page
-                            const int bx = (c + e) >> box_shift;
-                            const int pid = __shfl_sync(0xffffffffu, id, bx);
-                            const bool in = (have >> bx) & 1u;
-                            const float4 *gp = reinterpret_cast<const float4 *>(
-                                a.c.g_pages + (((size_t)(in ? pid : 0) * a.c.Hq + hq) << a.c.page_shift) +
-                                ((pos0 + c + e) & (page - 1)));
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const float4 g4 = in ? __ldg(gp + q) : make_float4(0.f, 0.f, 0.f, 0.f);
-                                float *v = x + e + 4 * q;
-                                v[0] = fmaf(g4.x, kLog2e, v[0] + gq);
-                                v[1] = fmaf(g4.y, kLog2e, v[1] + gq);
-                                v[2] = fmaf(g4.z, kLog2e, v[2] + gq);
-                                v[3] = fmaf(g4.w, kLog2e, v[3] + gq);
+                                for (int q = 0; q < 4; ++q) {
+                                    const float4 g4 = in ? __ldg(gp + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                                    float *v = x + e + 4 * q;
+                                    v[0] = fmaf(g4.x, kLog2e, v[0] + gq);
+                                    v[1] = fmaf(g4.y, kLog2e, v[1] + gq);
+                                    v[2] = fmaf(g4.z, kLog2e, v[2] + gq);
+                                    v[3] = fmaf(g4.w, kLog2e, v[3] + gq);
+                                }
                             }
                         }
-                    }
-                    if (!whole) {
+                        if (!whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 16) {
-                            const int last = ((have >> ((c + e) >> box_shift)) & 1u) ? valid - c - e : 0;
+                            for (int e = 0; e < 32; e += 16) {
+                                const int last = ((have >> ((c + e) >> box_shift)) & 1u) ? valid - c - e : 0;
 #pragma unroll
-                            for (int q = 0; q < 16; ++q) x[e + q] = q < last ? x[e + q] : -INFINITY;
+                                for (int q = 0; q < 16; ++q) x[e + q] = q < last ? x[e + q] : -INFINITY;
+                            }
+                        }
+                    };
+                    // the logits once in registers, or (where registers are short) read twice
+                    float x[kTwice ? 32 : 128];
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto max32 = [&](const float *v) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) mx[q] = fmax3(mx[q], v[e + 2 * q], v[e + 2 * q + 1]);
+                    };
+                    if (kTwice) {
+#pragma unroll
+                        for (int c = 0; c < 128; c += 32) {
+                            tld32(tm + L::cS + c, x);
+                            gate(c, x);
+                            max32(x);
+                        }
+                    } else {
+                        uint32_t(*u)[32] = reinterpret_cast<uint32_t(*)[32]>(x);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld32(tm + L::cS + 32 * c, u[c]);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 128; c += 32) {
+                            gate(c, x + (kTwice ? 0 : c));
+                            max32(x + (kTwice ? 0 : c));
                         }
                     }
-                };
-                // the logits once in registers, or (where registers are short) read twice
-                float x[kTwice ? 32 : 128];
-                float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    float *v = x + (kTwice ? 0 : c);
-                    logits(c, v);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) mx = fmax3(mx, v[e], v[e + 1]);
-                }
-                float alpha = 1.f;
-                if (mx > m_run + kRescale || (m_run == -INFINITY && mx > -INFINITY)) {
-                    alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - mx);
-                    m_run = mx;
-                }
-                // S of this step is complete, so the previous P V is too: O may be rescaled
-                const bool resc = alpha != 1.f && l_run > 0.f;
-                if (__any_sync(0xffffffffu, resc)) tmem_scale<D>(tm + C::O, resc ? alpha : 1.f);
-                l_run *= alpha;
-                const float use = m_run == -INFINITY ? 0.f : m_run;
-                float sum = 0.f;
-#pragma unroll
-                for (int c = 0; c < 128; c += 64) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int half = 0; half < 64; half += 32) {
-                        float *v = x + (kTwice ? 0 : c + half);
-                        if (kTwice) logits(c + half, v);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float p0 = ex2_approx(v[e] - use), p1 = ex2_approx(v[e + 1] - use);
-                            sum += p0 + p1;
-                            p[(half + e) / 2] = pack_bf16x2(p0, p1);
-                        }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    float alpha = 1.f;
+                    if (top > m_run + kRescale || (m_run == -INFINITY && top > -INFINITY)) {
+                        alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - top);
+                        m_run = top;
                     }
-                    // the weights of columns c .. c + 63 take 32 columns of S that have been read
-                    tmem_st32(tm + C::S + c / 2, p);
+                    // S of this step is complete, so the previous P V is too: O may be rescaled
+                    const bool resc = alpha != 1.f && l_run > 0.f;
+                    if (__any_sync(0xffffffffu, resc)) tmem_scale<D>(tm + L::cO, resc ? alpha : 1.f);
+                    l_run *= alpha;
+                    const float use = m_run == -INFINITY ? 0.f : -m_run;
+                    const float2 use2 = make_float2(use, use);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < 128; c += 64) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int half = 0; half < 64; half += 32) {
+                            float *v = x + (kTwice ? 0 : c + half);
+                            if (kTwice) {
+                                tld32(tm + L::cS + c + half, v);
+                                gate(c + half, v);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                const float2 z = fadd2(make_float2(v[e], v[e + 1]), use2);
+                                const float2 q = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+                                sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], q);
+                                p[(half + e) / 2] = pack_bf16x2(q.x, q.y);
+                            }
+                        }
+                        // the weights of columns c .. c + 63 take 32 columns of S that have been read
+                        tmem_st32(tm + L::cS + c / 2, p);
+                    }
+                    l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    tmem_st_wait();
                 }
-                l_run += sum;
-                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive_warp(bar(L::PR + w));
+            }
+            if (!ok || !(ok = wait.warp(bar(L::FIN + w), seg & 1))) break;
+            ++seg;
+            tc_fence_after();
+            if (warp_live) {
+                // the part's place: its CTA and item; a row whose keys were all absent leaves a sum of 0
+                const size_t e = ((size_t)(blockIdx.x + t.item) * NT + w) * 128 + r;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tld32(tm + L::cO + c, o);
+                    if (live) {
+                        float4 *dst = reinterpret_cast<float4 *>(y.so[NT - 1] + e * D + c);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    }
+                }
+                if (live) y.sml[NT - 1][e] = make_float2(m_run, l_run);
             }
             tc_fence_before();
-            mbar_arrive_warp(bar(L::PR + t));
-        }
-        if (ok) ok = wait.warp(bar(L::FIN), 0);
-        if (ok && warp_live) {
-            tc_fence_after();
-            const size_t at = (size_t)(1 + blockIdx.z) * a.c.Hkv * y.R + row;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tld32(tm + C::O + c, o);
-                if (live) {
-                    // a row whose keys were all absent has weights of nothing: its sum is 0
-                    float4 *dst = reinterpret_cast<float4 *>(y.po + at * D + c);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-                }
-            }
-            if (live) y.pml[at] = make_float2(m_run, l_run);
         }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 8) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::cols);
+        tmem_dealloc(tmem, L::cols);
     }
 }
 
@@ -678,15 +747,12 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
                         const float4 g4 = __ldg(gt + q);
-                        x[4 * q] = fmaf(g4.x, kLog2e, fmaf(x[4 * q], a.scale_log2, bias));
-                        x[4 * q + 1] = fmaf(g4.y, kLog2e, fmaf(x[4 * q + 1], a.scale_log2, bias));
-                        x[4 * q + 2] = fmaf(g4.z, kLog2e, fmaf(x[4 * q + 2], a.scale_log2, bias));
-                        x[4 * q + 3] = fmaf(g4.w, kLog2e, fmaf(x[4 * q + 3], a.scale_log2, bias));
+                        x[4 * q] = fmaf(g4.x, kLog2e, x[4 * q] + bias);
+                        x[4 * q + 1] = fmaf(g4.y, kLog2e, x[4 * q + 1] + bias);
+                        x[4 * q + 2] = fmaf(g4.z, kLog2e, x[4 * q + 2] + bias);
+                        x[4 * q + 3] = fmaf(g4.w, kLog2e, x[4 * q + 3] + bias);
                     }
                     between += y.gtot[(size_t)ks * a.c.Hq + hq];
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) x[c] *= a.scale_log2;
                 }
             }
             // P and O are free once the previous P V has completed
@@ -843,11 +909,11 @@ cudaError_t launch_cached(const Step &a, const TcWs &y, uint64_t limit_ns, cudaS
         !make_map(&tk, a.c.k_pages, D, a.c.page, (long long)a.c.nk * a.c.Hkv, a.c.page < 128 ? a.c.page : 128) ||
         !make_map(&tv, a.c.v_pages, D, a.c.page, (long long)a.c.nv * a.c.Hkv, a.c.page < 128 ? a.c.page : 128))
         return cudaErrorInvalidValue;
+    using L = CachedCfg<NT, D>;
     auto kern = tc_cached_kernel<NT, D, FOX>;
-    const cudaError_t e = big_smem(kern, CachedSmem<NT, D>::alloc);
+    const cudaError_t e = big_smem(kern, L::alloc);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(tile_slots(a.N, a.c.G, a.c.seqs, 128 * NT), a.c.Hkv, y.splits), kCachedThr, CachedSmem<NT, D>::alloc,
-           stream>>>(a, y, tx, tm, tk, tv, limit_ns);
+    kern<<<y.plan[NT - 1].ctas, L::threads, L::alloc, stream>>>(a, y, tx, tm, tk, tv, limit_ns);
     return cudaGetLastError();
 }
 
@@ -892,33 +958,35 @@ cudaError_t launch_all(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStre
 }
 
 struct TcLayout {
-    int splits;
-    size_t qt, po, pml, gq, gt, gtot, mt, kh, kl, vb, total;
+    int ctas[2];
+    size_t qt, po, pml, so[2], sml[2], units[2], items[2], gq, gt, gtot, mt, kh, kl, vb, total;
 };
 
-// Splits of the cached keys, for two CTAs per SM. The parts are sized by a bound that does not
-// fall as the step grows, so that a workspace for many tokens serves smaller steps.
+// The regions depend on the sizes in ways that do not fall as the step grows, so that a workspace
+// for many tokens serves smaller steps.
 TcLayout tc_layout(const Cache &c, int N, int max_chunk, int d, bool fox) {
     TcLayout y;
-    const size_t slots = slots_of(N, c.seqs), R = (size_t)N * c.G;
-    const long long cap = (long long)c.max_pages << c.page_shift;
-    const long long tiles = (long long)tile_slots(N, c.G, c.seqs, 128) * c.Hkv;
-    const long long want = 2 * 152 / tiles + 1, most = (cap + 511) / 512;
-    y.splits = (int)(want < most ? want : most);
-    if (y.splits < 1) y.splits = 1;
+    const size_t slots = slots_of(N, c.seqs), rows = (size_t)N * c.G * c.Hkv;
     size_t off = 256;
     auto take = [&](size_t bytes) {
         const size_t at = off;
         off = align256(off + bytes);
         return at;
     };
-    const size_t rows = R * c.Hkv;
-    // (1 + splits) rows <= 2 rows + 304 / tiles * rows, and rows <= 128 tiles
-    const size_t by_want = 2 * rows + 304 * 128, by_most = rows * (1 + (size_t)(most < 1 ? 1 : most));
-    const size_t parts = by_want < by_most ? by_want : by_most;
     y.qt = take(rows * d * 2);
-    y.po = take(parts * d * 4);
-    y.pml = take(parts * 8);
+    y.po = take(rows * d * 4);
+    y.pml = take(rows * 8);
+    for (int p = 0; p < 2; ++p) {
+        // one CTA per SM, or two: every SM of the part (152) has its share of the units
+        y.ctas[p] = 152 * (p == 0 && d == 64 ? CachedCfg<1, 64>::ctas_per_sm : 1);
+        const bool used = p == 0 || (long long)max_chunk * c.G > 128;
+        const size_t tile = 128 * (p + 1);
+        const size_t parts = used ? y.ctas[p] + (size_t)tile_slots(N, c.G, c.seqs, (int)tile) * c.Hkv : 0;
+        y.so[p] = take(parts * tile * d * 4);
+        y.sml[p] = take(parts * tile * 8);
+        y.units[p] = take(((size_t)c.seqs + 1) * 8);
+        y.items[p] = take(((size_t)c.seqs + 1) * 8);
+    }
     y.gq = take(fox ? rows * 4 : 0);
     y.gt = take(fox ? slots * c.Hq * kC * 4 : 0);
     y.gtot = take(fox ? slots * c.Hq * 8 : 0);
@@ -943,9 +1011,24 @@ cudaError_t launch_tc(const Step &a, int d, void *ws, uint64_t limit_ns, cudaStr
     char *w = static_cast<char *>(ws);
     auto b16 = [&](size_t off) { return reinterpret_cast<bf *>(w + off); };
     auto f32 = [&](size_t off) { return reinterpret_cast<float *>(w + off); };
-    const TcWs y{b16(f.qt), b16(f.mt), b16(f.kh), b16(f.kl), b16(f.vb), f32(f.po),
-                 reinterpret_cast<float2 *>(w + f.pml), f32(f.gq), f32(f.gt),
-                 reinterpret_cast<double *>(w + f.gtot), f.splits, (long long)a.N * a.c.G};
+    TcWs y;
+    y.qt = b16(f.qt);
+    y.mt = b16(f.mt);
+    y.kh = b16(f.kh);
+    y.kl = b16(f.kl);
+    y.vb = b16(f.vb);
+    y.po = f32(f.po);
+    y.pml = reinterpret_cast<float2 *>(w + f.pml);
+    for (int p = 0; p < 2; ++p) {
+        y.so[p] = f32(f.so[p]);
+        y.sml[p] = reinterpret_cast<float2 *>(w + f.sml[p]);
+        y.plan[p] = Plan{reinterpret_cast<long long *>(w + f.units[p]),
+                         reinterpret_cast<long long *>(w + f.items[p]), f.ctas[p]};
+    }
+    y.gq = f32(f.gq);
+    y.gt = f32(f.gt);
+    y.gtot = reinterpret_cast<double *>(w + f.gtot);
+    y.R = (long long)a.N * a.c.G;
     if (d == 64)
         return fox ? launch_all<64, true>(a, y, limit_ns, stream) : launch_all<64, false>(a, y, limit_ns, stream);
     return fox ? launch_all<128, true>(a, y, limit_ns, stream) : launch_all<128, false>(a, y, limit_ns, stream);

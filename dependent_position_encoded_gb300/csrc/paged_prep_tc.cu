@@ -118,6 +118,46 @@ __device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid) 
     }
 }
 
+// Units and items of cached-key work before each sequence (one CTA, both plans).
+__device__ __forceinline__ void make_plans(const Step &a, const TcWs &y, long long *sums) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long run[4] = {0, 0, 0, 0};
+    for (int base = 0; base <= a.c.seqs; base += kThr) {
+        const int b = base + tid;
+        long long v[4] = {0, 0, 0, 0};
+        if (b < a.c.seqs) {
+            const Seq s = seq_of(a, b);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                int tiles, kt;
+                plan_of(s, a.c.G, p + 1, tiles, kt);
+                v[2 * p + 1] = kt > 0 ? (long long)tiles * a.c.Hkv : 0;
+                v[2 * p] = v[2 * p + 1] * kt;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            long long x = v[q];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += t;
+            }
+            __syncthreads();
+            if (lane == 31) sums[warp] = x;
+            __syncthreads();
+            long long before = run[q], all = 0;
+#pragma unroll
+            for (int i = 0; i < kThr / 32; ++i) {
+                if (i < warp) before += sums[i];
+                all += sums[i];
+            }
+            if (b <= a.c.seqs) (q & 1 ? y.plan[q >> 1].items : y.plan[q >> 1].units)[b] = before + x - v[q];
+            run[q] += all;
+        }
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const Step a, const TcWs y) {
     using S = PrepSmem<D>;
@@ -137,6 +177,10 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
     const int G = a.c.G;
     int b, c;
     Seq s;
+    if ((int)blockIdx.x == gridDim.x - 1) {  // the CTA behind the slots
+        if (h == 0) make_plans(a, y, reinterpret_cast<long long *>(smem));
+        return;
+    }
     if (!block_of(a, slot, b, c, s)) return;
     const int rows = min(kC, s.T - c * kC), nt = (rows + 15) >> 4;
     const bool single = s.T <= kC;
@@ -350,7 +394,9 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
                 if (i >= rows) return;
                 const float2 q2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(Q + i * LDD + j));
-                *reinterpret_cast<uint32_t *>(y.qt + row_of(i) * D + j) = pack_bf16x2(q2.x - p, q2.y - q);
+                // scaled here once, so that the attention's logits need no factor
+                *reinterpret_cast<uint32_t *>(y.qt + row_of(i) * D + j) =
+                    pack_bf16x2((q2.x - p) * a.scale_log2, (q2.y - q) * a.scale_log2);
             });
         }
         {  // the block's logits Q K^T - (Lq A) R^T
@@ -589,45 +635,75 @@ __global__ void __launch_bounds__(kThr) tc_gates_kernel(const Step a, const TcWs
 }
 
 // ---------------------------------------------------------------- combine
-// Positions of split sp of n cached ones, in tiles of 128; how many splits have any.
-__device__ __forceinline__ int used_splits(int n, int splits) {
-    const int tiles = (n + 127) / 128, per = (tiles + splits - 1) / splits;
-    return per > 0 ? (tiles + per - 1) / per : 0;
-}
-
-// One warp per row: joins its softmax parts. grid (slots, key heads).
+// One warp per row (of a key head): joins the part of the step's own tokens and those of the
+// cached keys. Lane p holds the maximum and sum of part p (further parts in turns of 31).
 template <int D>
 __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const TcWs y) {
     constexpr int E = D / 32;
-    const int slot = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = a.c.G;
-    int b, c;
-    Seq s;
-    if (!block_of(a, slot, b, c, s)) return;
-    const int rows = min(kC, s.T - c * kC) * G, parts = 1 + used_splits(s.n, y.splits);
-    const size_t stride = (size_t)a.c.Hkv * y.R;
-    for (int i = warp; i < rows; i += kThr / 32) {
-        const long long tok = s.first + c * kC + i / G;
-        const int hq = h * G + i % G;
-        const size_t row = (size_t)h * y.R + tok * G + i % G;
-        float M = -INFINITY, L = 0.f, O[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) O[e] = 0.f;
-        for (int p = 0; p < parts; ++p) M = fmaxf(M, y.pml[row + p * stride].x);
-        for (int p = 0; p < parts; ++p) {
-            const float2 ml = y.pml[row + p * stride];
-            if (ml.x == -INFINITY) continue;
-            const float f = exp2f(ml.x - M);
-            L = fmaf(ml.y, f, L);
-            const float *o = y.po + (row + p * stride) * D + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; ++e) O[e] = fmaf(o[e], f, O[e]);
-        }
-        bf *dst = static_cast<bf *>(a.out) + tok * a.so.tok + hq * a.so.head + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16x2(O[e] / L, O[e + 1] / L);
+    const int G = a.c.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
+    const long long r = (long long)blockIdx.x * (kThr / 32) + warp;
+    if (r >= y.R) return;
+    const int tok = (int)(r / G), hq = h * G + (int)(r - (long long)tok * G);
+    int lo = 0, hi = a.c.seqs - 1;  // the last sequence that begins at or before the token
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(a.cu + mid) <= tok) lo = mid;
+        else hi = mid - 1;
     }
+    const Seq s = seq_of(a, lo);
+    if (tok < s.first || tok >= s.first + s.T) return;
+    const size_t row = (size_t)h * y.R + r;
+    const int own = (int)(r - (long long)s.first * G);  // the row within its sequence
+    int NT = 1, tiles, kt;
+    plan_of(s, G, 1, tiles, kt);
+    if (tiles == 0) {
+        NT = 2;
+        plan_of(s, G, 2, tiles, kt);
+    }
+    const Plan &p = NT == 1 ? y.plan[0] : y.plan[1];
+    const int it = h * tiles + own / (128 * NT);
+    long long first = 0, number = 0;  // the first part's number and how many there are
+    if (kt > 0) {
+        const long long per = plan_per(p, a.c.seqs), u = p.units[lo] + (long long)it * kt;
+        first = u / per + p.items[lo] + it;
+        number = (u + kt - 1) / per - u / per + 1;
+    }
+    const float *so = NT == 1 ? y.so[0] : y.so[1];
+    const float2 *sml = NT == 1 ? y.sml[0] : y.sml[1];
+    const int at = own % (128 * NT), tile = 128 * NT;
+    const float2 z = y.pml[row];
+    float M = z.x, L = z.y, O[E];
+    {
+        const float *o = y.po + row * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) O[e] = o[e];
+    }
+    for (long long p0 = 0; p0 < number; p0 += 32) {
+        const int n = number - p0 < 32 ? (int)(number - p0) : 32;
+        const float2 ml = lane < n ? sml[(first + p0 + lane) * tile + at] : make_float2(-INFINITY, 0.f);
+        float m = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float nm = fmaxf(M, m), f0 = exp2f(M - nm), f = exp2f(ml.x - nm);  // M is never -inf
+        float l = ml.x == -INFINITY ? 0.f : ml.y * f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        M = nm;
+        L = fmaf(L, f0, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) O[e] *= f0;
+        const float *o = so + ((first + p0) * tile + at) * D + lane * E;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float w = __shfl_sync(0xffffffffu, f, i);
+            if (w == 0.f) continue;  // absent keys alone, or nothing beside the others
+#pragma unroll
+            for (int e = 0; e < E; ++e) O[e] = fmaf(o[(size_t)i * tile * D + e], w, O[e]);
+        }
+    }
+    bf *dst = static_cast<bf *>(a.out) + (long long)tok * a.so.tok + hq * a.so.head + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16x2(O[e] / L, O[e + 1] / L);
 }
 
 template <typename K>
@@ -641,7 +717,7 @@ template <int D>
 cudaError_t launch_tc_prep(const Step &a, const TcWs &y, cudaStream_t stream) {
     const cudaError_t e = big_smem(tc_prep_kernel<D>, PrepSmem<D>::bytes);
     if (e != cudaSuccess) return e;
-    tc_prep_kernel<D><<<dim3(slots_of(a.N, a.c.seqs), a.c.Hkv), kThr, PrepSmem<D>::bytes, stream>>>(a, y);
+    tc_prep_kernel<D><<<dim3(slots_of(a.N, a.c.seqs) + 1, a.c.Hkv), kThr, PrepSmem<D>::bytes, stream>>>(a, y);
     return cudaGetLastError();
 }
 
@@ -660,9 +736,8 @@ cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
 // tile_rows rows, the gate sums.
 template <int D>
 cudaError_t launch_tc_finish(const Step &a, const TcWs &y, int tile_rows, cudaStream_t stream) {
-    const int nslots = slots_of(a.N, a.c.seqs);
     const long long cap = (long long)a.c.max_pages << a.c.page_shift;
-    tc_combine_kernel<D><<<dim3(nslots, a.c.Hkv), kThr, 0, stream>>>(a, y);
+    tc_combine_kernel<D><<<dim3((unsigned)((y.R + kThr / 32 - 1) / (kThr / 32)), a.c.Hkv), kThr, 0, stream>>>(a, y);
     cudaError_t e;
     if ((long long)a.max_chunk * a.c.G > tile_rows) {
         const size_t bytes = CarrySmem<D>::Yh + (size_t)128 * CarrySmem<D>::LDD * 2;

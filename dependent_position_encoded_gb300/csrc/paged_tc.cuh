@@ -11,10 +11,23 @@
 namespace path {
 namespace paged {
 
+// Work on cached keys. A unit is one tile of 128 NT rows against one tile of 128 cached
+// positions; an item is a row tile with all its key tiles. Items are ordered by sequence, key
+// head and row tile, and their units numbered through; each of `ctas` resident CTAs takes `per`
+// consecutive units, whatever the sequences' lengths, so the load is even and only items that
+// reach over a border have several parts. Sequences whose rows fit one tile go with NT = 1, the
+// others with NT = 2.
+struct Plan {
+    long long *units, *items;  // (seqs + 1): units and items before each sequence
+    int ctas;
+};
+
 // Workspace of the bf16 block path, behind the 256-byte status header:
-//   qt   (Hkv, R, D) bf16       queries carried to the chunk's start
-//   po   (1 + splits, Hkv, R, D) fp32, pml (1 + splits, Hkv, R) fp32 pairs: unnormalised softmax
-//        parts and their (maximum in log2 units, sum): 0 the step's own tokens, then the splits
+//   qt   (Hkv, R, D) bf16       queries carried to the chunk's start, times scale log2(e)
+//   po   (Hkv, R, D) fp32, pml (Hkv, R) fp32 pairs: the step's own tokens' unnormalised softmax
+//        part and its (maximum in log2 units, sum)
+//   so, sml per NT: (ctas + items, 128 NT, D) fp32 and (.., 128 NT) pairs, the parts of the
+//        cached keys: the part that CTA c has of item i is number c + i
 //   gq   (Hkv, R) fp32          PaTH-FoX: gate sum of a row from the chunk's start
 //   gt   (slots, Hq, 64) fp32   PaTH-FoX: gate sum behind a key to its block's end
 //   gtot (slots, Hq) fp64       PaTH-FoX: gate sum of a block
@@ -26,11 +39,55 @@ struct TcWs {
     __nv_bfloat16 *qt, *mt, *kh, *kl, *vb;
     float *po;
     float2 *pml;
+    float *so[2];
+    float2 *sml[2];
+    Plan plan[2];
     float *gq, *gt;
     double *gtot;
-    int splits;
     long long R;
 };
+
+// Row tiles and key tiles of a sequence in the plan of NT (0 where it goes with the other).
+__device__ __forceinline__ void plan_of(const Seq &s, int G, int NT, int &tiles, int &ktiles) {
+    const int rows = s.T * G;  // T G <= N G, which the host keeps within an int
+    ktiles = (s.n + 127) / 128;
+    tiles = (rows <= 128) == (NT == 1) ? (rows + 128 * NT - 1) / (128 * NT) : 0;
+}
+
+// Units per CTA: at least two, so that a part is worth its join.
+__device__ __forceinline__ long long plan_per(const Plan &p, int seqs) {
+    const long long all = p.units[seqs], per = (all + p.ctas - 1) / p.ctas;
+    return per < 2 ? 2 : per;
+}
+
+// The stretch of units from u on that lies in one item and below `end`.
+struct Stretch {
+    Seq s;
+    int b, h, tile, k0, steps;
+    long long item;  // over all sequences
+};
+__device__ __forceinline__ Stretch stretch_at(const Step &a, const Plan &p, int NT, long long u, long long end) {
+    int lo = 0, hi = a.c.seqs - 1;  // the last sequence with units[b] <= u: it has units
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.units[mid] <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    Stretch t;
+    t.b = lo;
+    t.s = seq_of(a, lo);
+    int tiles, kt;
+    plan_of(t.s, a.c.G, NT, tiles, kt);
+    const long long rem = u - p.units[lo];
+    const int it = (int)(rem / kt);
+    t.k0 = (int)(rem - (long long)it * kt);
+    t.h = it / tiles;
+    t.tile = it - t.h * tiles;
+    t.item = p.items[lo] + it;
+    const long long left = end - u;
+    t.steps = kt - t.k0 < left ? kt - t.k0 : (int)left;
+    return t;
+}
 
 // Rows of `rows` per tile over all sequences: tile i of sequence b is slot
 // cu[b] G / rows + b + i (as slots_of).

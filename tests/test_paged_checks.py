@@ -123,7 +123,7 @@ def _extend(so, cache, fox=True, **kw):
 def _strides(**kw):
     a = {n: (64, 64) for n in ("q", "k", "v", "w", "beta", "log_f", "out")}
     a.update(kw)
-    return ctypes.byref(pa._CPagedStrides(*[(ctypes.c_int64 * 2)(*a[n]) for n in a]))
+    return (ctypes.c_int64 * 14)(*[x for n in a for x in a[n]])
 
 
 @no_gpu
