@@ -211,14 +211,27 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                                 tma_load_3d(base + L::M + (uint32_t)(p * NA + x) * D * 128, &tm_m, bar(L::XF), 64 * x,
                                             0, (t.b * a.c.Hkv + t.h) * 2 + p);
                 }
+                // lane i < nbox: the pages of box i of a key tile, -1 past the end or where it is bad;
+                // looked up one tile ahead
+                int kid = -1, vid = -1, kid1, vid1;
+                auto look_up = [&](int pos0) {
+                    kid1 = vid1 = -1;
+                    if (lane < nbox && pos0 + lane * box < t.s.n) {
+                        const int sl = (pos0 + lane * box) >> a.c.page_shift;
+                        kid1 = page_of(a, a.c.k_table, t.b, sl, a.c.nk);
+                        vid1 = page_of(a, a.c.v_table, t.b, sl, a.c.nv);
+                    }
+                };
+                look_up(t.k0 * 128);
                 for (int i = 0; ok && i < 2 * t.steps; ++i, ++u) {
                     const bool keys = (i & 1) == 0;
                     const int pos0 = (t.k0 + (i >> 1)) * 128;
-                    // lane i < nbox: the page of box i, -1 past the end or where it is bad
-                    int id = -1;
-                    if (lane < nbox && pos0 + lane * box < t.s.n)
-                        id = page_of(a, keys ? a.c.k_table : a.c.v_table, t.b, (pos0 + lane * box) >> a.c.page_shift,
-                                     keys ? a.c.nk : a.c.nv);
+                    if (keys) {
+                        kid = kid1;
+                        vid = vid1;
+                        if (i + 2 < 2 * t.steps) look_up(pos0 + 128);
+                    }
+                    const int id = keys ? kid : vid;
                     const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
                     const int valid = min(128, t.s.n - pos0);
                     const bool whole = tile_whole(pos0, t.s.n, have, box_shift);
@@ -347,11 +360,16 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
         for (long long at = u_begin; ok && at < u_end;) {
             const Stretch t = stretch_at(a, plan, NT, at, u_end);
             at += t.steps;
-            for (int i = 0; i < t.steps; ++i, ++j) {
-                const int pos0 = (t.k0 + i) * 128;
-                int id = -1;
+            int next;  // the key pages of the next tile's boxes
+            auto look_up = [&](int pos0) {
+                next = -1;
                 if (lane < nbox && pos0 + lane * box < t.s.n)
-                    id = page_of(a, a.c.k_table, t.b, (pos0 + lane * box) >> a.c.page_shift, a.c.nk);
+                    next = page_of(a, a.c.k_table, t.b, (pos0 + lane * box) >> a.c.page_shift, a.c.nk);
+            };
+            look_up(t.k0 * 128);
+            for (int i = 0; i < t.steps; ++i, ++j) {
+                const int pos0 = (t.k0 + i) * 128, id = next;
+                if (i + 1 < t.steps) look_up(pos0 + 128);
                 const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
                 const bool whole = tile_whole(pos0, t.s.n, have, box_shift);
                 const int mine = __shfl_sync(0xffffffffu, id, r >> box_shift);
@@ -420,15 +438,20 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             const float gq =
                 FOX && live ? y.gq[(size_t)t.h * y.R + (size_t)t.s.first * G + row0 + r] * kLog2e : 0.f;
             float m_run = -INFINITY, l_run = 0.f;
-            for (int i = 0; i < t.steps; ++i, ++j) {
-                const int pos0 = (t.k0 + i) * 128;
-                int id = -1;
-                bool good = false;
+            int kid1, vid1;  // the pages of the next tile's boxes
+            auto look_up = [&](int pos0) {
+                kid1 = vid1 = -1;
                 if (lane < nbox && pos0 + lane * box < t.s.n) {
                     const size_t e = (size_t)t.b * a.c.max_pages + ((pos0 + lane * box) >> a.c.page_shift);
-                    id = __ldg(a.c.k_table + e);
-                    good = (unsigned)id < (unsigned)a.c.nk && (unsigned)__ldg(a.c.v_table + e) < (unsigned)a.c.nv;
+                    kid1 = __ldg(a.c.k_table + e);
+                    vid1 = __ldg(a.c.v_table + e);
                 }
+            };
+            look_up(t.k0 * 128);
+            for (int i = 0; i < t.steps; ++i, ++j) {
+                const int pos0 = (t.k0 + i) * 128, id = kid1;
+                const bool good = (unsigned)id < (unsigned)a.c.nk && (unsigned)vid1 < (unsigned)a.c.nv;
+                if (i + 1 < t.steps) look_up(pos0 + 128);
                 const unsigned have = __ballot_sync(0xffffffffu, good);
                 const int valid = min(128, t.s.n - pos0);
                 const bool whole = tile_whole(pos0, t.s.n, have, box_shift);
@@ -959,7 +982,7 @@ cudaError_t launch_all(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStre
 
 struct TcLayout {
     int ctas[2];
-    size_t qt, po, pml, so[2], sml[2], units[2], items[2], gq, gt, gtot, mt, kh, kl, vb, total;
+    size_t qt, po, pml, so[2], sml[2], units[2], items[2], gq, gt, gtot, mt, kh, kl, vb, ch, cl, gp, total;
 };
 
 // The regions depend on the sizes in ways that do not fall as the step grows, so that a workspace
@@ -995,6 +1018,10 @@ TcLayout tc_layout(const Cache &c, int N, int max_chunk, int d, bool fox) {
     y.kh = take(blocks ? slots * c.Hkv * (kC + d) * d * 2 : 0);
     y.kl = take(blocks ? slots * c.Hkv * (kC + d) * d * 2 : 0);
     y.vb = take(blocks ? slots * c.Hkv * kC * d * 2 : 0);
+    const bool groups = max_chunk > kC * 8;
+    y.ch = take(groups ? slots * c.Hkv * kC * d * 2 : 0);
+    y.cl = take(groups ? slots * c.Hkv * kC * d * 2 : 0);
+    y.gp = take(groups ? (slots / 8 + c.seqs + 1) * c.Hkv * 2 * d * d * 2 : 0);
     y.total = off;
     return y;
 }
@@ -1017,6 +1044,9 @@ cudaError_t launch_tc(const Step &a, int d, void *ws, uint64_t limit_ns, cudaStr
     y.kh = b16(f.kh);
     y.kl = b16(f.kl);
     y.vb = b16(f.vb);
+    y.ch = b16(f.ch);
+    y.cl = b16(f.cl);
+    y.gp = b16(f.gp);
     y.po = f32(f.po);
     y.pml = reinterpret_cast<float2 *>(w + f.pml);
     for (int p = 0; p < 2; ++p) {

@@ -30,33 +30,43 @@ struct PrepSmem {
     static constexpr size_t Ah = 4 * big, Al = Ah + sml, Rh = Al + sml, Rl = Rh + sml, Lh = Rl + sml,
                             Ll = Lh + sml, Th = Ll + sml, Tl = Th + sml, F = Th;
     // fp32 64 x 68 (E, the logits) lies in [Th, Tl]; the pair Lh, Ll holds Lq and R A^T, then P
-    static constexpr size_t vec = Tl + sml;  // beta, m, l: 64 floats each; cum: 64 doubles
-    static constexpr size_t bytes = vec + 3 * kC * 4 + kC * 8;
+    // beta, row maxima and sums, the gates' prefix sums as float pairs: 64 floats each; 16 pages
+    static constexpr size_t vec = Tl + sml, bytes = vec + 5 * kC * 4 + 16 * 4;
 };
 
-// 64 tokens (rows past `rows` zero) of one head into a shared tile
+// 64 tokens (rows past `rows` zero) of one head into registers, and from there into a shared
+// tile: the loads of several tiles are in flight together
 template <int D>
-__device__ __forceinline__ void load_block(bf *dst, const void *src, Stride st, long long first, int head,
-                                           int rows) {
-    constexpr int LDD = D + 8, PER = D / 8;
-    const bf *p = static_cast<const bf *>(src) + head * st.head;
-    for (int e = threadIdx.x; e < kC * PER; e += kThr) {
-        const int r = e / PER, c = e % PER * 8;
-        const uint4 x = r < rows ? *reinterpret_cast<const uint4 *>(p + (first + r) * st.tok + c)
-                                 : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4 *>(dst + r * LDD + c) = x;
+struct Block {
+    static constexpr int LDD = D + 8, PER = D / 8, IT = kC * PER / kThr;
+    uint4 x[IT];
+    __device__ __forceinline__ void load(const void *src, Stride st, long long first, int head, int rows) {
+        const bf *p = static_cast<const bf *>(src) + head * st.head;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int e = threadIdx.x + i * kThr, r = e / PER, c = e % PER * 8;
+            x[i] = r < rows ? *reinterpret_cast<const uint4 *>(p + (first + r) * st.tok + c)
+                            : make_uint4(0u, 0u, 0u, 0u);
+        }
     }
-}
+    __device__ __forceinline__ void put(bf *dst) const {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int e = threadIdx.x + i * kThr, r = e / PER, c = e % PER * 8;
+            *reinterpret_cast<uint4 *>(dst + r * LDD + c) = x[i];
+        }
+    }
+};
 
 __device__ __forceinline__ void put2(bf *t, int ld, int r, int c, uint32_t v) {
     *reinterpret_cast<uint32_t *>(t + r * ld + c) = v;
 }
 
-// (I + E)^{-1} D in fp32 for a strictly lower triangular E (shared, stride 68): the four 16 x
-// 16 diagonal blocks by substitution (one column per thread), then X21 = -X22 E21 X11 for the
-// 16- and the 32-blocks; every factor is bounded (products of contractions), so nothing
-// grows. `Y`: 32 x 36 floats of scratch. The columns are scaled by beta at the end.
-__device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid) {
+// (I + E)^{-1} in fp32 for a strictly lower triangular E (shared, stride 68): the four 16 x 16
+// diagonal blocks by substitution (one column per thread), then X21 = -X22 E21 X11 for the 16-
+// and the 32-blocks; every factor is bounded (products of contractions), so nothing grows.
+// `Y`: 32 x 36 floats of scratch; nt: the 16-row tiles in use (the others are the identity).
+__device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid, int nt) {
     constexpr int LD = 68, YL = 36;
     const int b0 = (tid >> 4) << 4, lu = tid & 15;
     float x[16];
@@ -73,6 +83,7 @@ __device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid) 
 #pragma unroll
         for (int l = 0; l < 16; ++l) E[(b0 + l) * LD + tid] = x[l];
     __syncthreads();
+    if (nt <= 1) return;
     // level 1: two 32-blocks at o, X21 (16 x 16)
     for (int pass = 0; pass < 2; ++pass) {
         float v[2];
@@ -95,6 +106,7 @@ __device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid) 
         }
         __syncthreads();
     }
+    if (nt <= 2) return;
     // level 2: X21 (32 x 32)
     for (int pass = 0; pass < 2; ++pass) {
         float v[4];
@@ -171,14 +183,15 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
        *const Ll = reinterpret_cast<bf *>(smem + S::Ll), *const Th = reinterpret_cast<bf *>(smem + S::Th),
        *const Tl = reinterpret_cast<bf *>(smem + S::Tl);
     float *const F = reinterpret_cast<float *>(smem + S::F);
-    float *const beta = reinterpret_cast<float *>(smem + S::vec), *const rm = beta + kC, *const rl = rm + kC;
-    double *const cum = reinterpret_cast<double *>(rl + kC);
+    float *const beta = reinterpret_cast<float *>(smem + S::vec), *const rm = beta + kC, *const rl = rm + kC,
+                 *const cumh = rl + kC, *const cuml = cumh + kC;
+    int *const kpage = reinterpret_cast<int *>(cuml + kC), *const vpage = kpage + 8;
     const int slot = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.c.G;
     int b, c;
     Seq s;
     if ((int)blockIdx.x == gridDim.x - 1) {  // the CTA behind the slots
-        if (h == 0) make_plans(a, y, reinterpret_cast<long long *>(smem));
+        if (h == 0 && blockIdx.z == 0) make_plans(a, y, reinterpret_cast<long long *>(smem));
         return;
     }
     if (!block_of(a, slot, b, c, s)) return;
@@ -186,8 +199,29 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
     const bool single = s.T <= kC;
     const long long first = s.first + c * kC;
     const size_t bh = (size_t)slot * a.c.Hkv + h;
-    load_block<D>(W, a.w, a.sw, first, h, rows);
-    load_block<D>(K, a.k, a.sk, first, h, rows);
+    // this CTA's query heads of the key head; the first CTA writes what they share
+    const int g0 = G * (int)blockIdx.z / (int)gridDim.z, g1 = G * ((int)blockIdx.z + 1) / (int)gridDim.z;
+    const bool lead = blockIdx.z == 0;
+    const int pos0 = s.n + c * kC, slot0 = pos0 >> a.c.page_shift;  // where the block goes in the cache
+    Block<D> vb, qb;
+    {
+        Block<D> wb, kb;
+        wb.load(a.w, a.sw, first, h, rows);
+        kb.load(a.k, a.sk, first, h, rows);
+        qb.load(a.q, a.sq, first, h * G + g0, rows);
+        vb.load(a.v, a.sv, first, h, rows);
+        wb.put(W);
+        kb.put(K);
+    }
+    if (tid < 8 && tid <= ((pos0 + rows - 1) >> a.c.page_shift) - slot0) {
+        kpage[tid] = page_of(a, a.c.k_table, b, slot0 + tid, a.c.nk);
+        vpage[tid] = page_of(a, a.c.v_table, b, slot0 + tid, a.c.nv);
+    }
+    // the place of the block's row i on its page (-1: the page is bad)
+    auto place = [&](const int *pages, int i, int heads, int head) -> long long {
+        const int pos = pos0 + i, id = pages[(pos >> a.c.page_shift) - slot0];
+        return id < 0 ? -1 : (((long long)id * heads + head) << a.c.page_shift) + (pos & (a.c.page - 1));
+    };
     if (tid < kC) beta[tid] = tid < rows ? a.beta[(first + tid) * a.sb.tok + h * a.sb.head] : 0.f;
     __syncthreads();
     // a warp's 16 x 32 piece of a 64 x 64 product
@@ -213,7 +247,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
         });
     }
     __syncthreads();
-    unit_lower_inverse(F, reinterpret_cast<float *>(Lh), tid);
+    unit_lower_inverse(F, reinterpret_cast<float *>(Lh), tid, nt);
     for (int e = tid; e < kC * kC / 2; e += kThr) {
         const int i = e / 32, j = 2 * (e % 32);
         uint32_t hi, lo;
@@ -256,7 +290,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
     }
     __syncthreads();
     // P_b - I = -U^T W (D x D): to the chunk's product or the block's factors
-    {
+    if (lead) {
         bf *const mh = single ? y.mt + ((size_t)b * a.c.Hkv + h) * 2 * D * D : y.kh + (bh * (kC + D) + kC) * D;
         bf *const ml = single ? mh + (size_t)D * D : y.kl + (bh * (kC + D) + kC) * D;
 #pragma unroll 1
@@ -277,7 +311,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
     // k~ = K - (R A^T) W: into the pages (the chunk's only block) or the block's factors
 #pragma unroll
     for (int x = 0; x < NH; ++x) {
-        if (single && (warp & 3) >= nt) break;
+        if (!lead || (single && (warp & 3) >= nt)) break;
         float u[4][4];
         zero_acc(u);
         warp_mma<4, false, true>(u, Lh, LDS, m0, W, LDD, 64 * x + n0, nt);
@@ -287,13 +321,9 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             p = k2.x - p;
             q = k2.y - q;
             if (single) {
-                if (i >= rows) return;
-                const int pos = s.n + i, id = page_of(a, a.c.k_table, b, pos >> a.c.page_shift, a.c.nk);
-                if (id >= 0)
-                    *reinterpret_cast<uint32_t *>(
-                        static_cast<bf *>(a.c.k_pages) +
-                        ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) + (pos & (a.c.page - 1))) * D + j) =
-                        pack_bf16x2(p, q);
+                const long long at = i < rows ? place(kpage, i, a.c.Hkv, h) : -1;
+                if (at >= 0)
+                    *reinterpret_cast<uint32_t *>(static_cast<bf *>(a.c.k_pages) + at * D + j) = pack_bf16x2(p, q);
             } else {
                 uint32_t hi, lo;
                 split2(p, q, hi, lo);
@@ -302,59 +332,58 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             }
         });
     }
-    __syncthreads();
-    load_block<D>(V, a.v, a.sv, first, h, rows);
-    __syncthreads();
     // the block's values: into the pages, and beside the factors for the scan
-    for (int e = tid; e < kC * D / 8; e += kThr) {
-        const int r = e / (D / 8), q = e % (D / 8) * 8;
-        const uint4 x = *reinterpret_cast<const uint4 *>(V + r * LDD + q);
-        if (!single) *reinterpret_cast<uint4 *>(y.vb + (bh * kC + r) * D + q) = x;
-        if (r >= rows) continue;
-        const int pos = s.n + c * kC + r, id = page_of(a, a.c.v_table, b, pos >> a.c.page_shift, a.c.nv);
-        if (id >= 0)
-            *reinterpret_cast<uint4 *>(
-                static_cast<bf *>(a.c.v_pages) +
-                ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) + (pos & (a.c.page - 1))) * D + q) = x;
-    }
-    for (int g = 0; g < G; ++g) {
+    if (lead)
+#pragma unroll
+        for (int i = 0; i < Block<D>::IT; ++i) {
+            const int e = tid + i * kThr, r = e / Block<D>::PER, q = e % Block<D>::PER * 8;
+            if (!single) *reinterpret_cast<uint4 *>(y.vb + (bh * kC + r) * D + q) = vb.x[i];
+            const long long at = r < rows ? place(vpage, r, a.c.Hkv, h) : -1;
+            if (at >= 0) *reinterpret_cast<uint4 *>(static_cast<bf *>(a.c.v_pages) + at * D + q) = vb.x[i];
+        }
+    __syncthreads();
+    vb.put(V);
+    for (int g = g0; g < g1; ++g) {
         const int hq = h * G + g;
         const size_t bq = (size_t)slot * a.c.Hq + hq;
         // the row of token t: its place in the step's packed rows
         auto row_of = [&](int t) { return (size_t)h * y.R + (first + t) * G + g; };
         __syncthreads();
-        load_block<D>(Q, a.q, a.sq, first, hq, rows);
+        qb.put(Q);
+        if (g + 1 < g1) qb.load(a.q, a.sq, first, hq + 1, rows);
         if (a.log_f != nullptr && warp == 0) {
-            // inclusive prefix sums of the 64 gates
-            double p = 0.0;
+            // inclusive prefix sums of the 64 gates, in fp64: lane t holds those of t and t + 32.
+            // Shared as two floats each: a difference of two is then right to an fp32 rounding of
+            // itself, however large the sums are
+            double x[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int t = 32 * half + lane;
-                double x = t < rows ? (double)a.log_f[(first + t) * a.sf.tok + hq * a.sf.head] : 0.0;
+                x[half] = t < rows ? (double)a.log_f[(first + t) * a.sf.tok + hq * a.sf.head] : 0.0;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const double z = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += z;
+                    const double z = __shfl_up_sync(0xffffffffu, x[half], o);
+                    if (lane >= o) x[half] += z;
                 }
-                cum[t] = p + x;
-                p += __shfl_sync(0xffffffffu, x, 31);
             }
-            if (lane == 0) y.gtot[bq] = p;
+            x[1] += __shfl_sync(0xffffffffu, x[0], 31);
+            const double all = __shfl_sync(0xffffffffu, x[1], 31);
+            if (lane == 0) y.gtot[bq] = all;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int t = 32 * half + lane;
+                const float hi = (float)x[half], behind = (float)(all - x[half]);
+                cumh[t] = hi;
+                cuml[t] = (float)(x[half] - (double)hi);
+                y.gt[bq * kC + t] = behind;
+                if (t < rows) {
+                    y.gq[row_of(t)] = hi;
+                    const long long at = single ? place(kpage, t, a.c.Hq, hq) : -1;
+                    if (at >= 0) a.c.g_pages[at] = behind;
+                }
+            }
         }
         __syncthreads();
-        if (a.log_f != nullptr && tid < kC) {
-            const float behind = (float)(cum[kC - 1] - cum[tid]);
-            y.gt[bq * kC + tid] = behind;
-            if (tid < rows) {
-                y.gq[row_of(tid)] = (float)cum[tid];
-                if (single) {
-                    const int pos = s.n + tid, id = page_of(a, a.c.k_table, b, pos >> a.c.page_shift, a.c.nk);
-                    if (id >= 0)
-                        a.c.g_pages[(((size_t)id * a.c.Hq + hq) << a.c.page_shift) + (pos & (a.c.page - 1))] =
-                            behind;
-                }
-            }
-        }
         {  // Lq = tril(Q W^T)
             float u[4][4];
             zero_acc(u);
@@ -416,26 +445,39 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             __syncthreads();  // Lq A has been read; the logits take its place
             each_pair(u, m0, n0, [&](int i, int j, float p, float q) {
                 if (a.log_f != nullptr) {
-                    if (j < i) p = fmaf((float)(cum[i] - cum[j]), kLog2e, p);
-                    if (j + 1 < i) q = fmaf((float)(cum[i] - cum[j + 1]), kLog2e, q);
+                    if (j < i) p = fmaf((cumh[i] - cumh[j]) + (cuml[i] - cuml[j]), kLog2e, p);
+                    if (j + 1 < i) q = fmaf((cumh[i] - cumh[j + 1]) + (cuml[i] - cuml[j + 1]), kLog2e, q);
                 }
                 F[i * LDF + j] = j <= i ? p : -INFINITY;
                 F[i * LDF + j + 1] = j + 1 <= i ? q : -INFINITY;
             });
         }
         __syncthreads();
-        // row maxima and sums; the weights, rounded to bf16, for the product with the values
-        for (int i = warp; i < 16 * nt; i += kThr / 32) {
-            const float x0 = F[i * LDF + 2 * lane], x1 = F[i * LDF + 2 * lane + 1];
-            float m = fmaxf(x0, x1);
+        // row maxima and sums; the weights, rounded to bf16, for the product with the values: eight
+        // lanes per row, eight columns each
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float p0 = exp2f(x0 - m), p1 = exp2f(x1 - m);  // the row's own key is never masked
-            float l = p0 + p1;
+        for (int pass = 0; pass < 2; ++pass) {
+            const int i = 8 * warp + 4 * pass + (lane >> 3), j = 8 * (lane & 7);
+            const float4 u = *reinterpret_cast<const float4 *>(F + i * LDF + j);
+            const float4 v = *reinterpret_cast<const float4 *>(F + i * LDF + j + 4);
+            float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+            float m = x[0];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            put2(Lh, LDS, i, 2 * lane, pack_bf16x2(p0, p1));
-            if (lane == 0) {
+            for (int e = 1; e < 8; ++e) m = fmaxf(m, x[e]);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float l = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[e] = exp2f(x[e] - m);  // the row's own key is never masked
+                l += x[e];
+            }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            *reinterpret_cast<uint4 *>(Lh + i * LDS + j) =
+                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                           pack_bf16x2(x[6], x[7]));
+            if ((lane & 7) == 0) {
                 rm[i] = m;
                 rl[i] = l;
             }
@@ -459,7 +501,12 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
 // Chunks of several blocks: the new keys of a block through the later ones, Y <- Y P_b for
 // b = c + 1 .. last, into their pages; and the identity through all blocks, which gives the
 // chunk's own product. Y is split into 16-bit pairs at every step, its sum stays in fp32
-// registers (Y + Y (P_b - I)), four warps of 16 rows each.
+// registers (Y + Y (P_b - I)), four warps of 16 rows each. A chain of all blocks would be as
+// long as the chunk, so it goes in two passes over groups of kGroup blocks: to the group's
+// end (and the group's product), then over the later groups' products. Each step waits for
+// 2 D^2 bf16 from L2 and for its MMAs, two CTAs to an SM.
+constexpr int kGroup = 8;
+
 template <int D>
 struct CarrySmem {
     static constexpr int LDD = D + 8;
@@ -467,54 +514,78 @@ struct CarrySmem {
                             bytes = Yl + (size_t)kC * LDD * 2;
 };
 
-template <int D>
-__global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs y) {
+// Groups of all sequences share one numbering: group i of a sequence whose first block is slot
+// f is number f / kGroup + b + i.
+__device__ __forceinline__ int group_of(const Seq &s, int b, int i) { return slot_of(s, b, 0) / kGroup + b + i; }
+
+__device__ __forceinline__ void cp16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// PASS 1: within the group; PASS 2: over the groups behind. grid.x: (seqs x groups x D / 64)
+// row tiles of the identity, then the slots. A chunk of one group is done after pass 1.
+template <int D, int PASS>
+__global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs y, int max_groups) {
     using S = CarrySmem<D>;
     constexpr int LDD = S::LDD, NT = D / 8, PER = D / 8;
     extern __shared__ __align__(16) uint8_t smem[];
     bf *const Mh = reinterpret_cast<bf *>(smem + S::Mh), *const Ml = reinterpret_cast<bf *>(smem + S::Ml),
        *const Yh = reinterpret_cast<bf *>(smem + S::Yh), *const Yl = reinterpret_cast<bf *>(smem + S::Yl);
-    const int h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, m0 = 16 * warp;
-    const bool ident = (int)blockIdx.x < a.c.seqs * (D / 64);  // the longest ways first
-    int b, c = -1, tile = 0;
+    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, m0 = 16 * warp;
+    const int per_seq = (PASS == 1 ? max_groups : 1) * (D / 64), idents = a.c.seqs * per_seq;
+    const bool ident = (int)blockIdx.x < idents;
+    int b, c = 0, tile = 0, grp = 0, slot = 0;
     Seq s;
     float acc[NT][4];
+    zero_acc(acc);
     if (ident) {
-        b = blockIdx.x / (D / 64);
+        b = blockIdx.x / per_seq;
         tile = blockIdx.x % (D / 64);
+        grp = blockIdx.x % per_seq / (D / 64);
         s = seq_of(a, b);
-        if (s.T <= kC || s.n == 0) return;
-        zero_acc(acc);
-        const int lane = tid & 31, r = 64 * tile + m0 + (lane >> 2), q = 2 * (lane & 3);
+    } else {
+        slot = blockIdx.x - idents;
+        if (!block_of(a, slot, b, c, s)) return;
+        grp = c / kGroup;
+    }
+    const int nb = (s.T + kC - 1) / kC, ng = (nb + kGroup - 1) / kGroup;
+    if (s.T <= kC || grp >= ng || (PASS == 2 && ng == 1)) return;
+    if (ident) {
+        // the chunk's product is for the cached keys, a group's for the groups before it too
+        if (s.n == 0 && (ng == 1 || PASS == 2 || grp == 0)) return;
+        const int r = 64 * tile + m0 + (lane >> 2), q = 2 * (lane & 3);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[n][i] = (8 * n + q + (i & 1) == r + 8 * (i >> 1)) ? 1.f : 0.f;
     } else {
-        const int slot = blockIdx.x - a.c.seqs * (D / 64);
-        if (!block_of(a, slot, b, c, s) || s.T <= kC) return;
-        const size_t base = ((size_t)slot * a.c.Hkv + h) * (kC + D);
-        zero_acc(acc);
-        const int lane = tid & 31;
+        const size_t bh = (size_t)slot * a.c.Hkv + h, base = PASS == 1 ? bh * (kC + D) : bh * kC;
+        const bf *const ph = PASS == 1 ? y.kh : y.ch, *const pl = PASS == 1 ? y.kl : y.cl;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const size_t at = (base + m0 + (lane >> 2) + 8 * i) * D + 8 * n + 2 * (lane & 3);
-                const float2 p = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(y.kh + at));
-                const float2 q = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(y.kl + at));
+                const float2 p = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(ph + at));
+                const float2 q = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(pl + at));
                 acc[n][2 * i] = p.x + q.x;
                 acc[n][2 * i + 1] = p.y + q.y;
             }
     }
-    const int nb = (s.T + kC - 1) / kC;
-    for (int kb = c + 1; kb < nb; ++kb) {
-        const size_t base = (((size_t)slot_of(s, b, kb) * a.c.Hkv + h) * (kC + D) + kC) * D;
+    // the factors: blocks of the group, or groups
+    const int from = PASS == 1 ? (ident ? grp * kGroup : c + 1) : (ident ? 0 : grp + 1);
+    const int to = PASS == 1 ? min(nb, (grp + 1) * kGroup) : ng;
+    for (int k = from; k < to; ++k) {
+        const size_t at = PASS == 1 ? (((size_t)slot_of(s, b, k) * a.c.Hkv + h) * (kC + D) + kC) * D
+                                    : ((size_t)group_of(s, b, k) * a.c.Hkv + h) * 2 * D * D;
+        const bf *const ph = PASS == 1 ? y.kh + at : y.gp + at, *const pl = PASS == 1 ? y.kl + at : ph + D * D;
         __syncthreads();
+#pragma unroll 4
         for (int e = tid; e < D * PER; e += 128) {
             const int r = e / PER, q = e % PER * 8;
-            *reinterpret_cast<uint4 *>(Mh + r * LDD + q) = *reinterpret_cast<const uint4 *>(y.kh + base + (size_t)r * D + q);
-            *reinterpret_cast<uint4 *>(Ml + r * LDD + q) = *reinterpret_cast<const uint4 *>(y.kl + base + (size_t)r * D + q);
+            cp16(Mh + r * LDD + q, ph + (size_t)r * D + q);
+            cp16(Ml + r * LDD + q, pl + (size_t)r * D + q);
         }
         each_pair(acc, m0, 0, [&](int i, int j, float p, float q) {
             uint32_t hi, lo;
@@ -522,13 +593,17 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
             put2(Yh, LDD, i, j, hi);
             put2(Yl, LDD, i, j, lo);
         });
+        cp_wait_all();
         __syncthreads();
         warp_mma<NT, false, true>(acc, Yh, LDD, m0, Mh, LDD, 0, D / 16);
         warp_mma<NT, false, true>(acc, Yl, LDD, m0, Mh, LDD, 0, D / 16);
         warp_mma<NT, false, true>(acc, Yh, LDD, m0, Ml, LDD, 0, D / 16);
     }
+    const bool done = PASS == 2 || ng == 1;
     if (ident) {
-        bf *const mh = y.mt + ((size_t)b * a.c.Hkv + h) * 2 * D * D, *const ml = mh + (size_t)D * D;
+        bf *const mh = done ? y.mt + ((size_t)b * a.c.Hkv + h) * 2 * D * D
+                            : y.gp + ((size_t)group_of(s, b, grp) * a.c.Hkv + h) * 2 * D * D;
+        bf *const ml = mh + (size_t)D * D;
         each_pair(acc, 64 * tile + m0, 0, [&](int i, int j, float p, float q) {
             uint32_t hi, lo;
             split2(p - (i == j), q - (i == j + 1), hi, lo);
@@ -537,6 +612,17 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
         });
         return;
     }
+    if (!done && grp + 1 < ng) {
+        const size_t base = ((size_t)slot * a.c.Hkv + h) * kC;
+        each_pair(acc, m0, 0, [&](int i, int j, float p, float q) {
+            uint32_t hi, lo;
+            split2(p, q, hi, lo);
+            *reinterpret_cast<uint32_t *>(y.ch + (base + i) * D + j) = hi;
+            *reinterpret_cast<uint32_t *>(y.cl + (base + i) * D + j) = lo;
+        });
+        return;
+    }
+    if (PASS == 2 && grp + 1 == ng) return;  // the last group's keys went to the pages in pass 1
     const int rows = min(kC, s.T - c * kC);
     each_pair(acc, m0, 0, [&](int i, int j, float p, float q) {
         if (i >= rows) return;
@@ -547,8 +633,7 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
                 ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) + (pos & (a.c.page - 1))) * D + j) =
                 pack_bf16x2(p, q);
     });
-    if (a.log_f != nullptr) {
-        const int slot = blockIdx.x - a.c.seqs * (D / 64);
+    if (a.log_f != nullptr)
         for (int e = tid; e < rows * a.c.G; e += 128) {
             const int r = e % rows, hq = h * a.c.G + e / rows, pos = s.n + c * kC + r;
             double g = y.gt[((size_t)slot * a.c.Hq + hq) * kC + r];
@@ -557,64 +642,119 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
             if (id >= 0)
                 a.c.g_pages[(((size_t)id * a.c.Hq + hq) << a.c.page_shift) + (pos & (a.c.page - 1))] = (float)g;
         }
-    }
 }
 
 // ---------------------------------------------------------------- transform
 // K <- K + K (P - I) in place for sequences whose rows fill several tiles (with one tile the
-// attention pass does it on the keys that it has loaded). Bound by HBM: a key is read and
-// written once. grid (parts, key heads, sequences), a CTA keeps P - I in shared memory.
+// attention pass does it on the keys that it has loaded). A key is read and written once; the
+// two products of P - I's parts keep the warp-level tensor path busy for longer than HBM at
+// D = 128. A warp takes 32 positions at a time, so that a fragment of P - I serves two row
+// tiles, and loads the next 32 meanwhile. grid (parts, key heads, sequences), a CTA keeps
+// P - I in shared memory.
+template <int D>
+struct TransformSmem {
+    static constexpr int LDD = D + 8;
+    static constexpr size_t Mh = 0, Ml = (size_t)D * LDD * 2, K = 2 * Ml, strip = (size_t)32 * LDD * 2,
+                            bytes = K + 8 * 2 * strip;
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, const TcWs y, int tile_rows) {
-    using S = CarrySmem<D>;
+    using S = TransformSmem<D>;
     constexpr int LDD = S::LDD, NT = D / 8, PER = D / 8;
     extern __shared__ __align__(16) uint8_t smem[];
-    bf *const Mh = reinterpret_cast<bf *>(smem + S::Mh), *const Ml = reinterpret_cast<bf *>(smem + S::Ml),
-       *const Kt = reinterpret_cast<bf *>(smem + S::Yh);  // 16 rows per warp: 128 in all
+    bf *const Mh = reinterpret_cast<bf *>(smem + S::Mh), *const Ml = reinterpret_cast<bf *>(smem + S::Ml);
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Seq s = seq_of(a, b);
-    if ((long long)s.T * a.c.G <= tile_rows || (int)blockIdx.x * 128 >= s.n) return;
+    const int strips = (s.n + 31) / 32, per = (strips + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int first = (int)blockIdx.x * per, last = min(strips, first + per);
+    if ((long long)s.T * a.c.G <= tile_rows || first >= last) return;
     const bf *const m = y.mt + ((size_t)b * a.c.Hkv + h) * 2 * D * D;
+#pragma unroll 4
     for (int e = tid; e < D * PER; e += kThr) {
         const int r = e / PER, q = e % PER * 8;
-        *reinterpret_cast<uint4 *>(Mh + r * LDD + q) = *reinterpret_cast<const uint4 *>(m + (size_t)r * D + q);
-        *reinterpret_cast<uint4 *>(Ml + r * LDD + q) = *reinterpret_cast<const uint4 *>(m + (size_t)(D + r) * D + q);
+        cp16(Mh + r * LDD + q, m + (size_t)r * D + q);
+        cp16(Ml + r * LDD + q, m + (size_t)(D + r) * D + q);
     }
-    __syncthreads();
-    bf *const mine = Kt + warp * 16 * LDD;
     bf *const pool = static_cast<bf *>(a.c.k_pages);
-    for (int j0 = (blockIdx.x * 8 + warp) * 16; j0 < s.n; j0 += gridDim.x * 128) {
-        // 16 positions of one page (pages are multiples of 16)
-        const int id = page_of(a, a.c.k_table, b, j0 >> a.c.page_shift, a.c.nk);
-        if (id < 0) continue;  // the same for the warp
-        const int left = min(16, s.n - j0);
-        bf *const src = pool + ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) + (j0 & (a.c.page - 1))) * D;
-        __syncwarp();
+    bf *const mine = reinterpret_cast<bf *>(smem + S::K + warp * 2 * S::strip);
+    // where 16 positions from j lie (pages are multiples of 16); null past the end or on a bad page
+    auto rows_at = [&](int j) -> bf * {
+        if (j >= s.n) return nullptr;
+        const int id = page_of(a, a.c.k_table, b, j >> a.c.page_shift, a.c.nk);
+        return id < 0 ? nullptr
+                      : pool + ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) + (j & (a.c.page - 1))) * D;
+    };
+    auto fetch = [&](int strip, int buf) {
+        bf *const dst = mine + buf * 32 * LDD;
 #pragma unroll
-        for (int e = lane; e < 16 * PER; e += 32) {
-            const int r = e / PER, q = e % PER * 8;
-            *reinterpret_cast<uint4 *>(mine + r * LDD + q) =
-                r < left ? *reinterpret_cast<const uint4 *>(src + (size_t)r * D + q) : make_uint4(0u, 0u, 0u, 0u);
+        for (int half = 0; half < 2; ++half) {
+            const bf *src = rows_at(32 * strip + 16 * half);
+#pragma unroll
+            for (int e = lane; e < 16 * PER; e += 32) {
+                const int r = e / PER, q = e % PER * 8;
+                if (src != nullptr) cp16(dst + (16 * half + r) * LDD + q, src + (size_t)r * D + q);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int buf = 0;
+    if (first + warp < last) fetch(first + warp, 0);
+    cp_wait_all();
+    __syncthreads();
+    for (int strip = first + warp; strip < last; strip += 8, buf ^= 1) {
+        if (strip + 8 < last) {
+            fetch(strip + 8, buf ^ 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            cp_wait_all();
         }
         __syncwarp();
-        float acc[NT][4];
-        zero_acc(acc);
-        warp_mma<NT, false, true>(acc, mine, LDD, 0, Mh, LDD, 0, D / 16);
-        warp_mma<NT, false, true>(acc, mine, LDD, 0, Ml, LDD, 0, D / 16);
-        __syncwarp();
-        each_pair(acc, 0, 0, [&](int i, int j, float p, float q) {
-            uint32_t *at = reinterpret_cast<uint32_t *>(mine + i * LDD + j);
-            const float2 k2 = unpack_bf16x2(*at);
-            *at = pack_bf16x2(k2.x + p, k2.y + q);
-        });
+        bf *const k = mine + buf * 32 * LDD;
+        float acc[2][NT][4];
+        zero_acc(acc[0]);
+        zero_acc(acc[1]);
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            const bf *const M = part == 0 ? Mh : Ml;
+#pragma unroll 2
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint32_t a0[4], a1[4];
+                frag_a(a0, k, LDD, 0, 16 * kk);
+                frag_a(a1, k, LDD, 16, 16 * kk);
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t f[4];
+                    frag_b(f, M, LDD, 8 * n, 16 * kk);
+                    mma_bf16(acc[0][n], a0, f[0], f[1]);
+                    mma_bf16(acc[0][n + 1], a0, f[2], f[3]);
+                    mma_bf16(acc[1][n], a1, f[0], f[1]);
+                    mma_bf16(acc[1][n + 1], a1, f[2], f[3]);
+                }
+            }
+        }
         __syncwarp();
 #pragma unroll
-        for (int e = lane; e < 16 * PER; e += 32) {
-            const int r = e / PER, q = e % PER * 8;
-            if (r < left)
-                *reinterpret_cast<uint4 *>(src + (size_t)r * D + q) =
-                    *reinterpret_cast<const uint4 *>(mine + r * LDD + q);
+        for (int half = 0; half < 2; ++half)
+            each_pair(acc[half], 16 * half, 0, [&](int i, int j, float p, float q) {
+                uint32_t *at = reinterpret_cast<uint32_t *>(k + i * LDD + j);
+                const float2 k2 = unpack_bf16x2(*at);
+                *at = pack_bf16x2(k2.x + p, k2.y + q);
+            });
+        __syncwarp();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int j = 32 * strip + 16 * half, left = min(16, s.n - j);
+            bf *const dst = rows_at(j);
+#pragma unroll
+            for (int e = lane; e < 16 * PER; e += 32) {
+                const int r = e / PER, q = e % PER * 8;
+                if (dst != nullptr && r < left)
+                    *reinterpret_cast<uint4 *>(dst + (size_t)r * D + q) =
+                        *reinterpret_cast<const uint4 *>(k + (16 * half + r) * LDD + q);
+            }
         }
+        __syncwarp();
     }
 }
 
@@ -717,7 +857,11 @@ template <int D>
 cudaError_t launch_tc_prep(const Step &a, const TcWs &y, cudaStream_t stream) {
     const cudaError_t e = big_smem(tc_prep_kernel<D>, PrepSmem<D>::bytes);
     if (e != cudaSuccess) return e;
-    tc_prep_kernel<D><<<dim3(slots_of(a.N, a.c.seqs) + 1, a.c.Hkv), kThr, PrepSmem<D>::bytes, stream>>>(a, y);
+    // a CTA takes all query heads of a key head, or fewer while CTAs would be idle (what they
+    // share is then formed by each: the step waits for the slowest CTA, not for the sum)
+    const int slots = slots_of(a.N, a.c.seqs), room = 152 * (D == 64 ? 2 : 1) / (slots * a.c.Hkv);
+    const int z = room < 1 ? 1 : room < a.c.G ? room : a.c.G;
+    tc_prep_kernel<D><<<dim3(slots + 1, a.c.Hkv, z), kThr, PrepSmem<D>::bytes, stream>>>(a, y);
     return cudaGetLastError();
 }
 
@@ -725,10 +869,16 @@ cudaError_t launch_tc_prep(const Step &a, const TcWs &y, cudaStream_t stream) {
 // attention, which takes those of short sequences).
 template <int D>
 cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
-    const cudaError_t e = big_smem(tc_carry_kernel<D>, CarrySmem<D>::bytes);
-    if (e != cudaSuccess) return e;
-    tc_carry_kernel<D><<<dim3(a.c.seqs * (D / 64) + slots_of(a.N, a.c.seqs), a.c.Hkv), 128, CarrySmem<D>::bytes,
-                         stream>>>(a, y);
+    cudaError_t e;
+    if ((e = big_smem(tc_carry_kernel<D, 1>, CarrySmem<D>::bytes)) != cudaSuccess ||
+        (e = big_smem(tc_carry_kernel<D, 2>, CarrySmem<D>::bytes)) != cudaSuccess)
+        return e;
+    const int slots = slots_of(a.N, a.c.seqs), groups = (a.max_chunk + kC * kGroup - 1) / (kC * kGroup);
+    tc_carry_kernel<D, 1><<<dim3(a.c.seqs * groups * (D / 64) + slots, a.c.Hkv), 128, CarrySmem<D>::bytes, stream>>>(
+        a, y, groups);
+    if (groups > 1)
+        tc_carry_kernel<D, 2><<<dim3(a.c.seqs * (D / 64) + slots, a.c.Hkv), 128, CarrySmem<D>::bytes, stream>>>(
+            a, y, groups);
     return cudaGetLastError();
 }
 
@@ -739,12 +889,17 @@ cudaError_t launch_tc_finish(const Step &a, const TcWs &y, int tile_rows, cudaSt
     const long long cap = (long long)a.c.max_pages << a.c.page_shift;
     tc_combine_kernel<D><<<dim3((unsigned)((y.R + kThr / 32 - 1) / (kThr / 32)), a.c.Hkv), kThr, 0, stream>>>(a, y);
     cudaError_t e;
+    if (cap == 0) return cudaGetLastError();  // no sequence has room for a token
     if ((long long)a.max_chunk * a.c.G > tile_rows) {
-        const size_t bytes = CarrySmem<D>::Yh + (size_t)128 * CarrySmem<D>::LDD * 2;
+        const size_t bytes = TransformSmem<D>::bytes;
         if ((e = big_smem(tc_transform_kernel<D>, bytes)) != cudaSuccess) return e;
-        const long long tiles = (cap + 127) / 128;  // four per CTA: P is loaded once for 512 keys
-        tc_transform_kernel<D><<<dim3((unsigned)((tiles + 3) / 4), a.c.Hkv, a.c.seqs), kThr, bytes, stream>>>(
-            a, y, tile_rows);
+        // CTAs per key head: one wave over the key heads' long sequences, of which there are at
+        // most N G / tile_rows, and at least 256 positions each
+        const long long longs = (long long)a.N * a.c.G / tile_rows;
+        const long long heads = a.c.Hkv * (longs < a.c.seqs ? (longs < 1 ? 1 : longs) : a.c.seqs);
+        long long parts = (152 + heads - 1) / heads;
+        if (parts > (cap + 255) / 256) parts = (cap + 255) / 256;
+        tc_transform_kernel<D><<<dim3((unsigned)parts, a.c.Hkv, a.c.seqs), kThr, bytes, stream>>>(a, y, tile_rows);
     }
     if (a.log_f != nullptr)
         tc_gates_kernel<<<dim3((unsigned)((cap + 4 * kThr - 1) / (4 * kThr)), a.c.Hq, a.c.seqs), kThr, 0, stream>>>(

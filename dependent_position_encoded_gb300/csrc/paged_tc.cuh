@@ -35,8 +35,11 @@ struct Plan {
 // and, where a chunk may have several blocks of 64 tokens:
 //   kh, kl (slots, Hkv, 64 + D, D) bf16 high and low parts of [k~; P_b - I]
 //   vb   (slots, Hkv, 64, D) bf16 the block's values, zero past its tokens
+// and, where it may have several groups of blocks (paged_prep_tc.cu):
+//   ch, cl (slots, Hkv, 64, D) bf16 high and low parts of the new keys at their group's end
+//   gp   (groups, Hkv, 2, D, D) bf16 high and low parts of the groups' products less I
 struct TcWs {
-    __nv_bfloat16 *qt, *mt, *kh, *kl, *vb;
+    __nv_bfloat16 *qt, *mt, *kh, *kl, *vb, *ch, *cl, *gp;
     float *po;
     float2 *pml;
     float *so[2];
