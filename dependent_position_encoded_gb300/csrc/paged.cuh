@@ -84,5 +84,31 @@ __device__ __forceinline__ bool block_of(const Step &a, int slot, int &b, int &c
     return c >= 0 && c * kC < s.T;
 }
 
+// The kernels of one call follow each other as programmatic dependents: the next one's CTAs
+// may come up (barriers, tensor memory) while the last ones of the one before still run, and
+// wait here before they touch memory. Every CTA waits before anything else that counts, so a
+// kernel's end implies the ends of all before it.
+__device__ __forceinline__ void grid_wait() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Launch behind another kernel of the same call (first: behind whatever the stream holds).
+template <typename... P, typename... A>
+cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, bool first,
+                   A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = first ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 }  // namespace paged
 }  // namespace path

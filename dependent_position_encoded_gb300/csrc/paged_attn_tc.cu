@@ -73,6 +73,15 @@ __device__ __forceinline__ void tst32(uint32_t taddr, const float *x) {
     tmem_st32(taddr, u);
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 // multiplies N fp32 columns of the thread's row by f
 template <int N>
 __device__ __forceinline__ void tmem_scale(uint32_t taddr, float f) {
@@ -93,8 +102,8 @@ constexpr float kRescale = 8.f;  // the running maximum may lag by 2^8 before O 
 // ================================================================ cached keys
 // Persistent: a CTA walks its stretches of units (paged_tc.cuh), each of them one item: NT tiles
 // of 128 rows of one sequence and key head against consecutive key tiles of 128 positions. Keys
-// and values stream through one ring of shared-memory slots (TMA, one box per page; a slot
-// holds 128 rows of D bf16 in 128-byte-swizzled atoms of 64 columns), which runs on from
+// and values stream through two rings of shared-memory slots (TMA, one box per page; a slot
+// holds 128 rows of D bf16 in 128-byte-swizzled atoms of 64 columns), which run on from
 // stretch to stretch, as every barrier's phase does. Per key tile and row tile: S = X K^T (N =
 // 128) into TMEM, softmax by the 128 threads of a warpgroup, one row each, which write the
 // weights as bf16 over S, and O += P V with the weights as the A operand in TMEM. With NT = 2
@@ -106,31 +115,43 @@ constexpr float kRescale = 8.f;  // the running maximum may lag by 2^8 before O 
 // (P - I split into two bf16 parts), and the second warpgroup adds it to the keys in shared
 // memory and stores them back, so each key is read once and written once.
 //
+// With NT = 1 and at most 64 (32) rows, the tile holds two (four) copies of them and each copy's
+// softmax takes a half (quarter) of the key tile's columns, with weights of 0 in the others: the
+// warps share the row's softmax, and the copies' sums are parts to join like any others.
+//
 // Warps: 0-3 softmax of tile 0; 4-7 softmax of tile 1 (NT = 2) or the keys' update (NT = 1); 8
-// allocates TMEM and issues the MMAs; 9 streams the pages. (NT = 2 has two more warps without
-// a role, so that the last warpgroup can give registers to the softmax.)
+// allocates TMEM and issues the MMAs; 9 and 10 stream the key and the value pages. (Warp 11 has
+// no role: the last warpgroup gives registers to the softmax.)
 // Positions past the sequence's n and those on bad pages: the streaming warp zeroes their rows
 // after the copy, and the softmax masks them.
 template <int NT, int D>
 struct CachedCfg {
     static constexpr uint32_t tile = 128 * D * 2, atom = 128 * 128;
     static constexpr uint32_t X = 0, M = X + NT * tile, mbytes = NT == 1 ? 2 * D * D * 2 : 0;
-    // slots: what fits beside; for NT = 1 and D = 64 so that two CTAs share an SM
-    static constexpr int slots = NT == 1 ? 4 : (D == 64 ? 8 : 5);
-    static constexpr uint32_t ring = M + mbytes, bars = ring + slots * tile;
-    static constexpr int FULL = 0, EMPTY = slots, XF = 2 * slots, XE = XF + 1, SF = XE + 1, PR = SF + 2, FIN = PR + 2,
-                         DF = FIN + 2, DE = DF + 1, TMP = DE + 1, END = TMP + 1, count = END + 1;
-    static constexpr uint32_t bytes = bars + count * 8 + 16, alloc = bytes + 1024;
-    static constexpr int threads = NT == 2 ? 384 : 320;
+    // slots of keys and of values: what fits beside; for NT = 1 and D = 64 so that two CTAs share
+    // an SM. With NT = 1 a key slot is held until the updated keys have left it.
+    static constexpr int NK = NT == 1 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 2);
+    static constexpr int NV = NT == 1 ? 2 : (D == 64 ? 4 : 3);
+    static constexpr uint32_t K = M + mbytes, V = K + NK * tile, bars = V + NV * tile;
+    static constexpr int KF = 0, KE = NK, VF = 2 * NK, VE = VF + NV, XF = VE + NV, XE = XF + 1, SF = XE + 1, PR = SF + 2, FIN = PR + 2,
+                         DF = FIN + 2, DE = DF + 1, TMP = DE + 1, END = TMP + 2, count = END + 1;
+    static constexpr uint32_t bytes = bars + count * 8 + 16;  // from a 1024-byte boundary
+    static constexpr int threads = 384;
     static constexpr int ctas_per_sm = NT == 1 && D == 64 ? 2 : 1;
-    // registers after the split (NT = 2: launched with 168 each)
-    static constexpr int reg_row = 208, reg_other = 80;
+    // registers after the split of what the CTA is launched with (NT = 2: 168 for each thread; NT = 1
+    // with two CTAs per SM: 80): the softmax's warpgroups, the update's and the last one
+    static constexpr bool split = NT == 2 || D == 64;
+    static constexpr int reg_row = NT == 2 ? 208 : 104, reg_update = 72, reg_other = NT == 2 ? 80 : 64;
     // TMEM columns: per row tile S 128 (the weights over it) and O; NT = 1: the update's product
     static constexpr uint32_t cS = 0, cO = 128, per_tile = 256, cD = 128 + D;
     static constexpr uint32_t cols = NT == 1 && D == 64 ? 256 : 512;
 };
-static_assert(CachedCfg<1, 128>::alloc <= 227 * 1024 && CachedCfg<2, 128>::alloc <= 227 * 1024, "shared memory");
+static_assert(CachedCfg<1, 128>::bytes <= 227 * 1024 && CachedCfg<2, 128>::bytes <= 227 * 1024 &&
+                  2 * (CachedCfg<1, 64>::bytes + 1024) <= 228 * 1024,
+              "shared memory");
 static_assert(256 * CachedCfg<2, 64>::reg_row + 128 * CachedCfg<2, 64>::reg_other <= 384 * 168, "registers");
+static_assert(128 * (CachedCfg<1, 64>::reg_row + CachedCfg<1, 64>::reg_update + CachedCfg<1, 64>::reg_other) <= 384 * 80,
+              "registers");
 
 template <int N>
 __device__ __forceinline__ void reg_inc() {
@@ -153,15 +174,19 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                  const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
     using L = CachedCfg<NT, D>;
-    constexpr int NA = D / 64, NS = L::slots;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    uint8_t *const sm = smem_raw + (base - raw);
+    constexpr int NA = D / 64, NK = L::NK, NV = L::NV;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t base = smem_u32(sm);
     auto bar = [&](int i) { return base + L::bars + 8u * (uint32_t)i; };
     uint32_t *const tslot = reinterpret_cast<uint32_t *>(sm + L::bars + 8 * L::count);
     volatile uint32_t *const abort_f = tslot + 1;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.c.G;
+    grid_wait();
+    if (base & 1023u) {  // the swizzle's atoms need it; the kernel has no other shared memory
+        report_status(a.status, kStatusTimeout);
+        return;
+    }
     const Plan plan = y.plan[NT - 1];
     const long long all = plan.units[a.c.seqs], per = plan_per(plan, a.c.seqs);
     const long long u_begin = (long long)blockIdx.x * per, u_end = u_begin + per < all ? u_begin + per : all;
@@ -181,63 +206,66 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    // Ring use u: keys of step j at u = 2 j, its values at u = 2 j + 1, j counted over all
-    // stretches of the CTA.
-    auto slot_at = [&](uint32_t u) { return base + L::ring + (u % NS) * L::tile; };
+    // Step j of the CTA (counted over all its stretches) uses key slot j % NK and value slot j % NV;
+    // each ring has one producing warp, which waits for every release of its slots in turn.
+    auto key_slot = [&](uint32_t j) { return base + L::K + (j % NK) * L::tile; };
+    auto value_slot = [&](uint32_t j) { return base + L::V + (j % NV) * L::tile; };
     auto second = [&](const Stretch &t) { return NT == 2 && t.tile * 256 + 128 < t.s.T * G; };
+    // log2 of the copies of the rows
+    auto copies = [&](const Stretch &t) { return NT == 2 ? 0 : t.s.T * G <= 32 ? 2 : t.s.T * G <= 64 ? 1 : 0; };
     const int page = a.c.page, box_shift = min(a.c.page_shift, 7), box = 1 << box_shift, nbox = 128 >> box_shift;
 
     if (warp >= 8) {
-        if (NT == 2) reg_dec<L::reg_other>();
-        if (warp == 9) {
+        if (L::split) reg_dec<L::reg_other>();
+        if (warp == 9 || warp == 10) {
             // ======================================================== pages into the ring
-            uint32_t u = 0, seg = 0, tmp_phase = 0;
+            const bool keys = warp == 9;
+            const int *const table = keys ? a.c.k_table : a.c.v_table;
+            const int npool = keys ? a.c.nk : a.c.nv;
+            const uint32_t tmp = bar(L::TMP + (keys ? 0 : 1));
+            const uint32_t ring = keys ? NK : NV, full0 = keys ? L::KF : L::VF, empty0 = keys ? L::KE : L::VE;
+            uint32_t j = 0, seg = 0, tmp_phase = 0;
             bool ok = true;
             for (long long at = u_begin; ok && at < u_end; ++seg) {
                 const Stretch t = stretch_at(a, plan, NT, at, u_end);
                 at += t.steps;
-                // the rows' tile (and the update's product) once the last stretch's are read
-                if (seg > 0 && !(ok = wait.warp(bar(L::XE), (seg - 1) & 1))) break;
-                if (lane == 0) {
-                    const int nx = second(t) ? 2 : 1, xr = t.s.first * G + 128 * NT * t.tile;
-                    mbar_arrive_expect_tx(bar(L::XF), nx * L::tile + L::mbytes);
-                    for (int i = 0; i < nx; ++i)
-                        for (int x = 0; x < NA; ++x)
-                            tma_load_3d(base + L::X + i * L::tile + x * L::atom, &tm_x, bar(L::XF), 64 * x,
-                                        xr + 128 * i, t.h);
-                    if (NT == 1)
-                        for (int p = 0; p < 2; ++p)
+                if (keys) {
+                    // the rows' tile (and the update's product) once the last stretch's are read
+                    if (seg > 0 && !(ok = wait.warp(bar(L::XE), (seg - 1) & 1))) break;
+                    if (lane == 0) {
+                        const int xr = t.s.first * G + 128 * NT * t.tile;
+                        const int nx = second(t) ? 8 : 4, mask = (128 * NT >> copies(t)) - 1;  // boxes of 32 rows
+                        mbar_arrive_expect_tx(bar(L::XF), nx * (L::tile / 4) + L::mbytes);
+                        for (int i = 0; i < nx; ++i)
                             for (int x = 0; x < NA; ++x)
-                                tma_load_3d(base + L::M + (uint32_t)(p * NA + x) * D * 128, &tm_m, bar(L::XF), 64 * x,
-                                            0, (t.b * a.c.Hkv + t.h) * 2 + p);
-                }
-                // lane i < nbox: the pages of box i of a key tile, -1 past the end or where it is bad;
-                // looked up one tile ahead
-                int kid = -1, vid = -1, kid1, vid1;
-                auto look_up = [&](int pos0) {
-                    kid1 = vid1 = -1;
-                    if (lane < nbox && pos0 + lane * box < t.s.n) {
-                        const int sl = (pos0 + lane * box) >> a.c.page_shift;
-                        kid1 = page_of(a, a.c.k_table, t.b, sl, a.c.nk);
-                        vid1 = page_of(a, a.c.v_table, t.b, sl, a.c.nv);
+                                tma_load_3d(base + L::X + (i >> 2) * L::tile + x * L::atom + (i & 3) * 32 * 128, &tm_x,
+                                            bar(L::XF), 64 * x, xr + ((32 * i) & mask), t.h);
+                        if (NT == 1)
+                            for (int p = 0; p < 2; ++p)
+                                for (int x = 0; x < NA; ++x)
+                                    tma_load_3d(base + L::M + (uint32_t)(p * NA + x) * D * 128, &tm_m, bar(L::XF),
+                                                64 * x, 0, (t.b * a.c.Hkv + t.h) * 2 + p);
                     }
+                }
+                // lane i < nbox: the page of box i of a key tile, -1 past the end or where it is bad;
+                // looked up one tile ahead
+                int next;
+                auto look_up = [&](int pos0) {
+                    next = -1;
+                    if (lane < nbox && pos0 + lane * box < t.s.n)
+                        next = page_of(a, table, t.b, (pos0 + lane * box) >> a.c.page_shift, npool);
                 };
                 look_up(t.k0 * 128);
-                for (int i = 0; ok && i < 2 * t.steps; ++i, ++u) {
-                    const bool keys = (i & 1) == 0;
-                    const int pos0 = (t.k0 + (i >> 1)) * 128;
-                    if (keys) {
-                        kid = kid1;
-                        vid = vid1;
-                        if (i + 2 < 2 * t.steps) look_up(pos0 + 128);
-                    }
-                    const int id = keys ? kid : vid;
+                for (int i = 0; ok && i < t.steps; ++i, ++j) {
+                    const int pos0 = (t.k0 + i) * 128, id = next;
+                    if (i + 1 < t.steps) look_up(pos0 + 128);
                     const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
                     const int valid = min(128, t.s.n - pos0);
                     const bool whole = tile_whole(pos0, t.s.n, have, box_shift);
-                    if (u >= NS && !(ok = wait.warp(bar(L::EMPTY + u % NS), ((u / NS) & 1) ^ 1))) break;
-                    const uint32_t dst = slot_at(u);
-                    const uint32_t full = bar(L::FULL + u % NS), target = whole ? full : bar(L::TMP);
+                    const uint32_t sl = j % ring, turn = j / ring;
+                    if (turn > 0 && !(ok = wait.warp(bar(empty0 + sl), (turn - 1) & 1))) break;
+                    const uint32_t dst = keys ? key_slot(j) : value_slot(j);
+                    const uint32_t full = bar(full0 + sl), target = whole ? full : tmp;
                     if (lane == 0) mbar_arrive_expect_tx(target, (uint32_t)__popc(have) * box * D * 2);
                     __syncwarp();
                     if (id >= 0)
@@ -247,14 +275,19 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                                         (pos0 + lane * box) & (page - 1), id * a.c.Hkv + t.h);
                     if (!whole) {
                         // zero the rows that hold no cached position, then hand the slot on
-                        if (!(ok = wait.warp(bar(L::TMP), tmp_phase))) break;
+                        if (!(ok = wait.warp(tmp, tmp_phase))) break;
                         tmp_phase ^= 1;
                         uint8_t *const rowp = sm + (dst - base);
-                        for (int r = 0; r < 128; ++r) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int r = 32 * q + lane;
                             if (r < valid && ((have >> (r >> box_shift)) & 1u)) continue;
-                            if (lane < NA * 8)
-                                *reinterpret_cast<uint4 *>(rowp + (lane >> 3) * L::atom + r * 128 + (lane & 7) * 16) =
-                                    make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                            for (int x = 0; x < NA; ++x)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    *reinterpret_cast<uint4 *>(rowp + x * L::atom + sw128_offset(r, c)) =
+                                        make_uint4(0u, 0u, 0u, 0u);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -262,12 +295,12 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                     }
                 }
             }
-            // on an abort: no copy may land after the CTA is gone. The slots' last uses, the one
-            // that broke off among them (its copies signal TMP or FULL, or were never sent)
+            // on an abort: no copy may land after the CTA is gone (those that may still be on their way
+            // are the last ones of the ring's slots)
             if (!ok) {
-                for (uint32_t v = u > NS ? u - NS : 0; v < u; ++v)
-                    mbar_wait(bar(L::FULL + v % NS), (v / NS) & 1, limit_ns);
-                mbar_wait(bar(L::XF), seg & 1, limit_ns);
+                for (uint32_t v = j > ring ? j - ring : 0; v < j; ++v)
+                    mbar_wait(bar(full0 + v % ring), (v / ring) & 1, limit_ns);
+                if (keys) mbar_wait(bar(L::XF), seg & 1, limit_ns);
             }
         } else if (warp == 8 && lane == 0) {
             // ======================================================== MMA issue
@@ -275,7 +308,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             uint32_t j = 0, j1 = 0, seg = 0;  // steps of the first and of the second row tile
             bool ok = true;
             auto issue_s = [&](int t, uint32_t js) {
-                const uint32_t kb = slot_at(2 * js);
+                const uint32_t kb = key_slot(js);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     umma_bf16(tmem + L::per_tile * t + L::cS,
@@ -284,17 +317,17 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 umma_commit(bar(L::SF + t));
             };
             auto issue_pv = [&](int t, uint32_t js, bool first) {
-                const uint64_t v = sdesc_sw128(slot_at(2 * js + 1), L::atom, 1024);
+                const uint64_t v = sdesc_sw128(value_slot(js), L::atom, 1024);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                     umma_tA(tmem + L::per_tile * t + L::cO, tmem + L::per_tile * t + L::cS + 8 * kk, v + 128 * kk,
                             ID_O, !first || kk > 0);
             };
-            auto keys_ready = [&](uint32_t js) { return wait(bar(L::FULL + (2 * js) % NS), ((2 * js) / NS) & 1); };
+            auto keys_ready = [&](uint32_t js) { return wait(bar(L::KF + js % NK), (js / NK) & 1); };
             auto issue_update = [&](uint32_t js) {  // K (P - I): the keys are the A operand
                 if (js > 0 && !wait(bar(L::DE), (js - 1) & 1)) return false;
                 tc_fence_after();
-                const uint32_t kb = slot_at(2 * js);
+                const uint32_t kb = key_slot(js);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     const uint64_t m = sdesc_sw128(base + L::M + p * NA * D * 128, D * 128, 1024);
@@ -311,7 +344,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             auto after_s = [&](uint32_t js, bool last) {
                 bool fine = true;
                 if (NT == 1) fine = issue_update(js);
-                else umma_commit(bar(L::EMPTY + (2 * js) % NS));
+                else umma_commit(bar(L::KE + js % NK));
                 if (last) umma_commit(bar(L::XE));
                 return fine;
             };
@@ -325,13 +358,12 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 if (two) issue_s(1, j);
                 ok = after_s(j, t.steps == 1);
                 for (int i = 0; ok && i < t.steps; ++i, ++j) {
-                    const uint32_t vs = (2 * j + 1) % NS;
-                    if (!(ok = wait(bar(L::FULL + vs), ((2 * j + 1) / NS) & 1))) break;
+                    if (!(ok = wait(bar(L::VF + j % NV), (j / NV) & 1))) break;
                     for (int q = 0; q < (two ? 2 : 1); ++q) {
                         if (!(ok = wait(bar(L::PR + q), (q ? j1 : j) & 1))) break;
                         tc_fence_after();
                         issue_pv(q, j, i == 0);
-                        if (q == (two ? 1 : 0)) umma_commit(bar(L::EMPTY + vs));
+                        if (q == (two ? 1 : 0)) umma_commit(bar(L::VE + j % NV));
                         if (i + 1 < t.steps) {
                             if (q == 0 && !(ok = keys_ready(j + 1))) break;
                             if (q == 0) tc_fence_after();
@@ -353,6 +385,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
         }
     } else if (NT == 1 && warp >= 4) {
         // ============================================================ the keys' update
+        if (L::split) reg_dec<L::reg_update>();
         const int r = tid - 128;
         const uint32_t tm = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + L::cD;
         bool ok = true;
@@ -375,7 +408,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 const int mine = __shfl_sync(0xffffffffu, id, r >> box_shift);
                 if (!(ok = wait.warp(bar(L::DF), j & 1))) break;
                 tc_fence_after();
-                uint8_t *const kt = sm + (slot_at(2 * j) - base);
+                uint8_t *const kt = sm + (key_slot(j) - base);
                 bf *const dst = mine >= 0 && pos0 + r < t.s.n
                                     ? static_cast<bf *>(a.c.k_pages) +
                                           ((((size_t)mine * a.c.Hkv + t.h) << a.c.page_shift) +
@@ -410,19 +443,19 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                     if (whole && id >= 0) {
 #pragma unroll
                         for (int x = 0; x < NA; ++x)
-                            tma_store_3d(&tm_k, slot_at(2 * j) + x * L::atom + lane * box * 128, 64 * x,
+                            tma_store_3d(&tm_k, key_slot(j) + x * L::atom + lane * box * 128, 64 * x,
                                          (pos0 + lane * box) & (page - 1), id * a.c.Hkv + t.h);
                         bulk_wait_read();
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(L::EMPTY + (2 * j) % NS));
+                    if (lane == 0) mbar_arrive(bar(L::KE + j % NK));
                 }
             }
         }
         if (warp == 4) bulk_wait_all();
     } else {
         // ============================================================ softmax
-        if (NT == 2) reg_inc<L::reg_row>();
+        if (L::split) reg_inc<L::reg_row>();
         constexpr bool kTwice = NT == 1 || FOX;
         const int w = warp >> 2, r = tid & 127;  // row tile and row in it
         const uint32_t tm = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + L::per_tile * w;
@@ -432,11 +465,13 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             const Stretch t = stretch_at(a, plan, NT, at, u_end);
             at += t.steps;
             if (w == 1 && !second(t)) continue;
-            const int rows_all = t.s.T * G, row0 = 128 * (NT * t.tile + w);
-            const bool live = row0 + r < rows_all, warp_live = row0 + 32 * (warp & 3) < rows_all;
-            const int hq = t.h * G + (live ? (row0 + r) % G : 0);
+            // the row of this thread, and the columns of the key tiles that its copy takes
+            const int rows_all = t.s.T * G, cp = copies(t), rw = r & ((128 >> cp) - 1);
+            const int row0 = 128 * (NT * t.tile + w), cols = 128 >> cp, c_begin = (r >> (7 - cp)) * cols;
+            const bool live = row0 + rw < rows_all, warp_live = row0 + (rw & ~31) < rows_all;
+            const int hq = t.h * G + (live ? (row0 + rw) % G : 0);
             const float gq =
-                FOX && live ? y.gq[(size_t)t.h * y.R + (size_t)t.s.first * G + row0 + r] * kLog2e : 0.f;
+                FOX && live ? y.gq[(size_t)t.h * y.R + (size_t)t.s.first * G + row0 + rw] * kLog2e : 0.f;
             float m_run = -INFINITY, l_run = 0.f;
             int kid1, vid1;  // the pages of the next tile's boxes
             auto look_up = [&](int pos0) {
@@ -489,66 +524,89 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                             }
                         }
                     };
-                    // the logits once in registers, or (where registers are short) read twice
-                    float x[kTwice ? 32 : 128];
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float top;
                     auto max32 = [&](const float *v) {
+                        float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
+                        for (int e = 4; e < 28; e += 8)
 #pragma unroll
                             for (int q = 0; q < 4; ++q) mx[q] = fmax3(mx[q], v[e + 2 * q], v[e + 2 * q + 1]);
+                        return fmax3(fmax3(mx[0], mx[1], mx[2]), mx[3], fmax3(fmaxf(v[28], v[29]), v[30], v[31]));
+                    };
+                    // the running maximum of the row; O follows it when it has risen by 2^8. (S of this
+                    // step is complete, so the previous P V is too.)
+                    float use;
+                    auto raise = [&]() {
+                        float alpha = 1.f;
+                        if (top > m_run + kRescale || (m_run == -INFINITY && top > -INFINITY)) {
+                            alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - top);
+                            m_run = top;
+                        }
+                        const bool resc = alpha != 1.f && l_run > 0.f;
+                        if (__any_sync(0xffffffffu, resc)) tmem_scale<D>(tm + L::cO, resc ? alpha : 1.f);
+                        l_run *= alpha;
+                        use = m_run == -INFINITY ? 0.f : -m_run;
+                    };
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    // 32 weights as 16 bf16 pairs
+                    auto weigh = [&](const float *v, uint32_t *p) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float2 z = fadd2(make_float2(v[e], v[e + 1]), make_float2(use, use));
+                            const float2 q = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+                            sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], q);
+                            p[e / 2] = pack_bf16x2(q.x, q.y);
+                        }
                     };
                     if (kTwice) {
-#pragma unroll
-                        for (int c = 0; c < 128; c += 32) {
+                        // registers are short: the logits of more than 32 columns are read twice. The
+                        // weights of columns c .. c + 31 take the 16 columns from c / 2, whose logits
+                        // have been read or are another copy's
+                        float x[32];
+                        top = -INFINITY;
+#pragma unroll 1
+                        for (int c = c_begin; c < c_begin + cols; c += 32) {
                             tld32(tm + L::cS + c, x);
                             gate(c, x);
-                            max32(x);
+                            top = fmaxf(top, max32(x));
                         }
+                        raise();
+                        uint32_t p[16];
+#pragma unroll 1
+                        for (int c = c_begin; c < c_begin + cols; c += 32) {
+                            if (cols > 32) {
+                                tld32(tm + L::cS + c, x);
+                                gate(c, x);
+                            }
+                            weigh(x, p);
+                            tmem_st16(tm + L::cS + c / 2, p);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) p[e] = 0u;
+#pragma unroll 1
+                        for (int c = 0; c < 128; c += 32)
+                            if (c < c_begin || c >= c_begin + cols) tmem_st16(tm + L::cS + c / 2, p);
                     } else {
+                        float x[128];
                         uint32_t(*u)[32] = reinterpret_cast<uint32_t(*)[32]>(x);
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tmem_ld32(tm + L::cS + 32 * c, u[c]);
                         tmem_ld_wait();
+                        float mx[4];
 #pragma unroll
-                        for (int c = 0; c < 128; c += 32) {
-                            gate(c, x + (kTwice ? 0 : c));
-                            max32(x + (kTwice ? 0 : c));
+                        for (int c = 0; c < 4; ++c) {
+                            gate(32 * c, x + 32 * c);
+                            mx[c] = max32(x + 32 * c);
                         }
-                    }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    float alpha = 1.f;
-                    if (top > m_run + kRescale || (m_run == -INFINITY && top > -INFINITY)) {
-                        alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - top);
-                        m_run = top;
-                    }
-                    // S of this step is complete, so the previous P V is too: O may be rescaled
-                    const bool resc = alpha != 1.f && l_run > 0.f;
-                    if (__any_sync(0xffffffffu, resc)) tmem_scale<D>(tm + L::cO, resc ? alpha : 1.f);
-                    l_run *= alpha;
-                    const float use = m_run == -INFINITY ? 0.f : -m_run;
-                    const float2 use2 = make_float2(use, use);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        raise();
 #pragma unroll
-                    for (int c = 0; c < 128; c += 64) {
-                        uint32_t p[32];
-#pragma unroll
-                        for (int half = 0; half < 64; half += 32) {
-                            float *v = x + (kTwice ? 0 : c + half);
-                            if (kTwice) {
-                                tld32(tm + L::cS + c + half, v);
-                                gate(c + half, v);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const float2 z = fadd2(make_float2(v[e], v[e + 1]), use2);
-                                const float2 q = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-                                sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], q);
-                                p[(half + e) / 2] = pack_bf16x2(q.x, q.y);
-                            }
+                        for (int c = 0; c < 128; c += 64) {
+                            uint32_t p[32];
+                            weigh(x + c, p);
+                            weigh(x + c + 32, p + 16);
+                            tmem_st32(tm + L::cS + c / 2, p);
                         }
-                        // the weights of columns c .. c + 63 take 32 columns of S that have been read
-                        tmem_st32(tm + L::cS + c / 2, p);
                     }
                     l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_st_wait();
@@ -627,6 +685,7 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y, G = a.c.G;
     int b, ti;
     Seq s;
+    grid_wait();
     // later rows walk further: the last tiles first
     if (!tile_of(a, gridDim.x - 1 - blockIdx.x, 128, b, ti, s)) return;
     const int row0 = 128 * ti, rows_all = s.T * G, per_block = kC * G;
@@ -927,17 +986,16 @@ cudaError_t big_smem(K kern, size_t bytes) {
 template <int NT, int D, bool FOX>
 cudaError_t launch_cached(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream) {
     CUtensorMap tx, tm, tk, tv;
-    if (!make_map(&tx, y.qt, D, y.R, a.c.Hkv, 128) ||
+    if (!make_map(&tx, y.qt, D, y.R, a.c.Hkv, 32) ||
         !make_map(&tm, y.mt, D, D, (long long)a.c.seqs * a.c.Hkv * 2, D) ||
         !make_map(&tk, a.c.k_pages, D, a.c.page, (long long)a.c.nk * a.c.Hkv, a.c.page < 128 ? a.c.page : 128) ||
         !make_map(&tv, a.c.v_pages, D, a.c.page, (long long)a.c.nv * a.c.Hkv, a.c.page < 128 ? a.c.page : 128))
         return cudaErrorInvalidValue;
     using L = CachedCfg<NT, D>;
     auto kern = tc_cached_kernel<NT, D, FOX>;
-    const cudaError_t e = big_smem(kern, L::alloc);
+    const cudaError_t e = big_smem(kern, L::bytes);
     if (e != cudaSuccess) return e;
-    kern<<<y.plan[NT - 1].ctas, L::threads, L::alloc, stream>>>(a, y, tx, tm, tk, tv, limit_ns);
-    return cudaGetLastError();
+    return launch(kern, dim3(y.plan[NT - 1].ctas), L::threads, L::bytes, stream, false, a, y, tx, tm, tk, tv, limit_ns);
 }
 
 template <int D, bool FOX>
@@ -949,9 +1007,8 @@ cudaError_t launch_scan(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStr
     auto kern = tc_scan_kernel<D, FOX>;
     const cudaError_t e = big_smem(kern, ScanSmem<D>::alloc);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(tile_slots(a.N, a.c.G, a.c.seqs, 128), a.c.Hkv), kScanThr, ScanSmem<D>::alloc, stream>>>(a, y, tr, tv,
-                                                                                                        limit_ns);
-    return cudaGetLastError();
+    return launch(kern, dim3(tile_slots(a.N, a.c.G, a.c.seqs, 128), a.c.Hkv), kScanThr, ScanSmem<D>::alloc, stream,
+                  false, a, y, tr, tv, limit_ns);
 }
 
 }  // namespace

@@ -75,6 +75,7 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
     __shared__ float sm_o[G][SLOTS][D];
 
     const int sp = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    grid_wait();  // the first of the call: it only lets the merge come up
     const Seq s = seq_of(a, b);
     const int j0 = sp * chunk, j1 = min(j0 + chunk, s.n);
     if (s.T == 0 || j0 >= j1) return;  // the merge skips the splits past n
@@ -277,6 +278,7 @@ __global__ void __launch_bounds__(D)
 paged_decode_merge(const Step a, int chunk, int nsplit, const float *__restrict__ part) {
     __shared__ float red[D / 32];
     const int hq = blockIdx.x, b = blockIdx.y, c = threadIdx.x;
+    grid_wait();
     const Seq s = seq_of(a, b);
     if (s.T == 0) return;
     const int h = hq / a.c.G;
@@ -322,13 +324,12 @@ paged_decode_merge(const Step a, int chunk, int nsplit, const float *__restrict_
 template <typename T, bool FOX, int D, int G>
 cudaError_t launch_g(const Step &a, int chunk, int nsplit, float *part, cudaStream_t stream) {
     if (nsplit > 0) {
-        paged_decode_split<T, FOX, D, G><<<dim3(nsplit, a.c.Hkv, a.c.seqs), kThreads, 0, stream>>>(
-            a, chunk, nsplit, part);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch(paged_decode_split<T, FOX, D, G>, dim3(nsplit, a.c.Hkv, a.c.seqs), kThreads, 0,
+                                     stream, true, a, chunk, nsplit, part);
         if (e != cudaSuccess) return e;
     }
-    paged_decode_merge<T, FOX, D><<<dim3(a.c.Hq, a.c.seqs), D, 0, stream>>>(a, chunk, nsplit, part);
-    return cudaGetLastError();
+    return launch(paged_decode_merge<T, FOX, D>, dim3(a.c.Hq, a.c.seqs), D, 0, stream, nsplit == 0, a, chunk, nsplit,
+                  part);
 }
 
 template <typename T, bool FOX, int D>

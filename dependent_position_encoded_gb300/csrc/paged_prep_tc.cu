@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
     const int G = a.c.G;
     int b, c;
     Seq s;
+    grid_wait();  // the first of the call: it only lets the next one come up
     if ((int)blockIdx.x == gridDim.x - 1) {  // the CTA behind the slots
         if (h == 0 && blockIdx.z == 0) make_plans(a, y, reinterpret_cast<long long *>(smem));
         return;
@@ -537,6 +538,7 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
     const bool ident = (int)blockIdx.x < idents;
     int b, c = 0, tile = 0, grp = 0, slot = 0;
     Seq s;
+    grid_wait();
     float acc[NT][4];
     zero_acc(acc);
     if (ident) {
@@ -665,6 +667,7 @@ __global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, con
     extern __shared__ __align__(16) uint8_t smem[];
     bf *const Mh = reinterpret_cast<bf *>(smem + S::Mh), *const Ml = reinterpret_cast<bf *>(smem + S::Ml);
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_wait();
     const Seq s = seq_of(a, b);
     const int strips = (s.n + 31) / 32, per = (strips + (int)gridDim.x - 1) / (int)gridDim.x;
     const int first = (int)blockIdx.x * per, last = min(strips, first + per);
@@ -761,6 +764,7 @@ __global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, con
 // PaTH-FoX: every cached key's gate sums advance by the chunk's. grid (parts, Hq, seqs).
 __global__ void __launch_bounds__(kThr) tc_gates_kernel(const Step a, const TcWs y) {
     const int hq = blockIdx.y, b = blockIdx.z;
+    grid_wait();
     const Seq s = seq_of(a, b);
     if (s.T == 0 || (int)blockIdx.x * kThr >= s.n) return;
     const int nb = (s.T + kC - 1) / kC;
@@ -782,6 +786,7 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
     constexpr int E = D / 32;
     const int G = a.c.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
     const long long r = (long long)blockIdx.x * (kThr / 32) + warp;
+    grid_wait();
     if (r >= y.R) return;
     const int tok = (int)(r / G), hq = h * G + (int)(r - (long long)tok * G);
     int lo = 0, hi = a.c.seqs - 1;  // the last sequence that begins at or before the token
@@ -810,7 +815,11 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
     }
     const float *so = NT == 1 ? y.so[0] : y.so[1];
     const float2 *sml = NT == 1 ? y.sml[0] : y.sml[1];
-    const int at = own % (128 * NT), tile = 128 * NT;
+    // short sequences' tiles hold copies of their rows, each a part of its own
+    const int rows_all = s.T * G, cp = NT == 2 ? 0 : rows_all <= 32 ? 2 : rows_all <= 64 ? 1 : 0;
+    const int at = own % (128 * NT), tile = 128 * NT, cp_rows = 128 >> cp;
+    number <<= cp;
+    auto part_at = [&](long long p) { return (first + (p >> cp)) * tile + (p & ((1 << cp) - 1)) * cp_rows + at; };
     const float2 z = y.pml[row];
     float M = z.x, L = z.y, O[E];
     {
@@ -820,7 +829,7 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
     }
     for (long long p0 = 0; p0 < number; p0 += 32) {
         const int n = number - p0 < 32 ? (int)(number - p0) : 32;
-        const float2 ml = lane < n ? sml[(first + p0 + lane) * tile + at] : make_float2(-INFINITY, 0.f);
+        const float2 ml = lane < n ? sml[part_at(p0 + lane)] : make_float2(-INFINITY, 0.f);
         float m = ml.x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -832,13 +841,13 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
         L = fmaf(L, f0, l);
 #pragma unroll
         for (int e = 0; e < E; ++e) O[e] *= f0;
-        const float *o = so + ((first + p0) * tile + at) * D + lane * E;
 #pragma unroll 4
         for (int i = 0; i < n; ++i) {
             const float w = __shfl_sync(0xffffffffu, f, i);
             if (w == 0.f) continue;  // absent keys alone, or nothing beside the others
+            const float *o = so + part_at(p0 + i) * D + lane * E;
 #pragma unroll
-            for (int e = 0; e < E; ++e) O[e] = fmaf(o[(size_t)i * tile * D + e], w, O[e]);
+            for (int e = 0; e < E; ++e) O[e] = fmaf(o[e], w, O[e]);
         }
     }
     bf *dst = static_cast<bf *>(a.out) + (long long)tok * a.so.tok + hq * a.so.head + lane * E;
@@ -861,8 +870,7 @@ cudaError_t launch_tc_prep(const Step &a, const TcWs &y, cudaStream_t stream) {
     // share is then formed by each: the step waits for the slowest CTA, not for the sum)
     const int slots = slots_of(a.N, a.c.seqs), room = 152 * (D == 64 ? 2 : 1) / (slots * a.c.Hkv);
     const int z = room < 1 ? 1 : room < a.c.G ? room : a.c.G;
-    tc_prep_kernel<D><<<dim3(slots + 1, a.c.Hkv, z), kThr, PrepSmem<D>::bytes, stream>>>(a, y);
-    return cudaGetLastError();
+    return launch(tc_prep_kernel<D>, dim3(slots + 1, a.c.Hkv, z), kThr, PrepSmem<D>::bytes, stream, true, a, y);
 }
 
 // Chunks of several blocks: new keys into the pages and the chunks' products (before the
@@ -874,12 +882,12 @@ cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
         (e = big_smem(tc_carry_kernel<D, 2>, CarrySmem<D>::bytes)) != cudaSuccess)
         return e;
     const int slots = slots_of(a.N, a.c.seqs), groups = (a.max_chunk + kC * kGroup - 1) / (kC * kGroup);
-    tc_carry_kernel<D, 1><<<dim3(a.c.seqs * groups * (D / 64) + slots, a.c.Hkv), 128, CarrySmem<D>::bytes, stream>>>(
-        a, y, groups);
-    if (groups > 1)
-        tc_carry_kernel<D, 2><<<dim3(a.c.seqs * (D / 64) + slots, a.c.Hkv), 128, CarrySmem<D>::bytes, stream>>>(
-            a, y, groups);
-    return cudaGetLastError();
+    e = launch(tc_carry_kernel<D, 1>, dim3(a.c.seqs * groups * (D / 64) + slots, a.c.Hkv), 128, CarrySmem<D>::bytes,
+               stream, false, a, y, groups);
+    if (e == cudaSuccess && groups > 1)
+        e = launch(tc_carry_kernel<D, 2>, dim3(a.c.seqs * (D / 64) + slots, a.c.Hkv), 128, CarrySmem<D>::bytes, stream,
+                   false, a, y, groups);
+    return e;
 }
 
 // The rest of a step after its attention: outputs, the cached keys of sequences with more than
@@ -887,9 +895,9 @@ cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_tc_finish(const Step &a, const TcWs &y, int tile_rows, cudaStream_t stream) {
     const long long cap = (long long)a.c.max_pages << a.c.page_shift;
-    tc_combine_kernel<D><<<dim3((unsigned)((y.R + kThr / 32 - 1) / (kThr / 32)), a.c.Hkv), kThr, 0, stream>>>(a, y);
-    cudaError_t e;
-    if (cap == 0) return cudaGetLastError();  // no sequence has room for a token
+    cudaError_t e = launch(tc_combine_kernel<D>, dim3((unsigned)((y.R + kThr / 32 - 1) / (kThr / 32)), a.c.Hkv), kThr, 0,
+                           stream, false, a, y);
+    if (e != cudaSuccess || cap == 0) return e;  // no sequence has room for a token
     if ((long long)a.max_chunk * a.c.G > tile_rows) {
         const size_t bytes = TransformSmem<D>::bytes;
         if ((e = big_smem(tc_transform_kernel<D>, bytes)) != cudaSuccess) return e;
@@ -899,12 +907,14 @@ cudaError_t launch_tc_finish(const Step &a, const TcWs &y, int tile_rows, cudaSt
         const long long heads = a.c.Hkv * (longs < a.c.seqs ? (longs < 1 ? 1 : longs) : a.c.seqs);
         long long parts = (152 + heads - 1) / heads;
         if (parts > (cap + 255) / 256) parts = (cap + 255) / 256;
-        tc_transform_kernel<D><<<dim3((unsigned)parts, a.c.Hkv, a.c.seqs), kThr, bytes, stream>>>(a, y, tile_rows);
+        e = launch(tc_transform_kernel<D>, dim3((unsigned)parts, a.c.Hkv, a.c.seqs), kThr, bytes, stream, false, a, y,
+                   tile_rows);
+        if (e != cudaSuccess) return e;
     }
     if (a.log_f != nullptr)
-        tc_gates_kernel<<<dim3((unsigned)((cap + 4 * kThr - 1) / (4 * kThr)), a.c.Hq, a.c.seqs), kThr, 0, stream>>>(
-            a, y);
-    return cudaGetLastError();
+        e = launch(tc_gates_kernel, dim3((unsigned)((cap + 4 * kThr - 1) / (4 * kThr)), a.c.Hq, a.c.seqs), kThr, 0,
+                   stream, false, a, y);
+    return e;
 }
 
 template cudaError_t launch_tc_prep<64>(const Step &, const TcWs &, cudaStream_t);

@@ -69,9 +69,8 @@ def make(lens, chunks, Hq, Hkv, d, page, dtype, fox, seed=0, head_major=False, s
 def put(pool, table, start, rows):
     """rows (tokens, H[, d]) at positions start .. of the sequence with this table row."""
     page = pool.shape[2]
-    for i in range(0, rows.shape[0]):
-        p = start + i
-        pool[int(table[p // page]), :, p % page] = rows[i]
+    p = torch.arange(start, start + rows.shape[0], device=pool.device)
+    pool[table[(p // page).long()].long(), :, p % page] = rows
 
 
 def rows_of(pool, table, n):
@@ -180,8 +179,8 @@ def check(x, before, out, scale=None):
                     err = (got - Gs[s]).abs() - Gs[s].abs() * 2.0 ** -22
                     assert float(err.max()) <= 1e-6
             lo = n if name == "v_pages" else (0 if T else n)
-            for p in range(lo, n + T):
-                same[int(table[s, p // x["page"]]), p % x["page"]] = False
+            p = torch.arange(lo, n + T, device=same.device)
+            same[table[s][p // x["page"]].long(), p % x["page"]] = False
         keep = same[:, None].expand(x[name].shape[:3]) if x[name].dim() == 4 else \
             same[:, None].expand(x[name].shape)
         a, b = x[name][keep], before[name][keep]

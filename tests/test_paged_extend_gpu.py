@@ -263,6 +263,17 @@ def test_a_workspace_for_chunks_serves_smaller_steps(lib):
     assert lib.path_check_workspace(ws) == lib.OK
 
 
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("fox", [False, True])
+@pytest.mark.parametrize("Hq,chunk", [(16, 3), (32, 25), (64, 40)])
+def test_many_key_tiles(lib, d, page, fox, Hq, chunk):
+    """Long caches: many key tiles for every resident CTA, so that its rings and barriers turn
+    many times, and stretches that begin and end inside an item; 3, 50 and 160 rows a key
+    head."""
+    x = pc.make([20000, 3000], [chunk, 1], Hq, 16, d, page, BF, fox, seed=16)
+    run(lib, x)
+
+
 def test_long_cache_offsets_past_32_bits(lib):
     """Pages whose byte and element offsets pass 2^31 and 2^32."""
     pages, page, H, d = 36000, 64, 16, 128  # 4.7e9 elements a pool
