@@ -83,13 +83,24 @@ path_status check_workspace(const void *ws, size_t bytes, size_t need) {
     return bytes < need ? PATH_ERR_WORKSPACE : PATH_OK;
 }
 
-// The step's kernels: one token per sequence at most takes the one-pass kernel where it has
-// the query heads per key head, everything else the block kernels of the type.
-bool one_pass(const Cache &c, int max_chunk) { return max_chunk == 1 && paged::decode_takes(c.G); }
+// The step's kernels. One token per sequence at most, and a few query heads per key head: the
+// one-pass kernel on the CUDA cores scores them from registers and needs one launch more for
+// the join, where the block kernels need three; but it does G products per key on the CUDA cores.
+// Measured for bf16 (us, one-pass / block kernels), by query heads x cached positions of the
+// whole cache: 2,400 at G = 1: 10 / 17; 2^18 at G = 1: 27 / 29; 2^18 at G = 4: 32 / 29; 2^20 at
+// G = 4: 69 / 50; 2^22 at G = 1: 240 / 221; 2^23 at G = 4 with gates: 536 / 283. With gates and
+// G = 1 the one-pass kernel leaves most value rows unread: 240 / 252 at 2^22. fp32 has no tensor
+// path: one-pass wherever it takes G.
+bool one_pass(const Cache &c, int max_chunk, bool bf16, bool fox) {
+    if (max_chunk != 1 || !paged::decode_takes(c.G)) return false;
+    if (!bf16 || (fox && c.G == 1)) return true;
+    const long long positions = ((long long)c.max_pages << c.page_shift) * c.seqs * c.Hq;
+    return positions <= (1 << 18);
+}
 
 size_t step_ws_bytes(const path_paged_cache *p, int N, int max_chunk, bool fox) {
     const Cache c = to_cache(p);
-    if (one_pass(c, max_chunk)) return 256 + align256(paged::decode_part_bytes(c, p->d));
+    if (one_pass(c, max_chunk, p->dtype == PATH_BF16, fox)) return 256 + align256(paged::decode_part_bytes(c, p->d));
     if (p->dtype == PATH_BF16) return paged::tc_ws_bytes(c, N, max_chunk, p->d, fox);
     return paged::f32_ws_bytes(c, N, p->d, fox);
 }
@@ -144,7 +155,7 @@ path_status extend(const path_paged_cache *p, const void *q, const void *k, cons
                         stride_of(strides ? strides->out : nullptr, p->Hq, p->d),
                         cu_tokens, N, max_chunk, scale * kLog2e, static_cast<uint32_t *>(ws)};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (one_pass(c, max_chunk))
+    if (one_pass(c, max_chunk, p->dtype == PATH_BF16, fox))
         return cuda_status(paged::launch_decode(a, p->d, p->dtype == PATH_BF16,
                                                 reinterpret_cast<float *>(static_cast<char *>(ws) + 256), s));
     if (p->dtype == PATH_BF16) return cuda_status(paged::launch_tc(a, p->d, ws, kWaitLimitNs, s));
@@ -179,12 +190,13 @@ size_t path_paged_workspace_bytes(const path_paged_cache *cache, int num_tokens,
         return 0;
     size_t n = paged::pages_ws_bytes(to_cache(cache));
     if (num_tokens > 0) {
-        // with gates: at least what a step without them needs; a step of single tokens too, so
-        // that a workspace for chunks serves the steps between them
-        for (int chunk : {max_chunk, 1}) {
-            const size_t s = step_ws_bytes(cache, num_tokens, chunk, true);
-            n = s > n ? s : n;
-        }
+        // with and without gates, and a step of single tokens too, so that a workspace for chunks
+        // serves the steps between them
+        for (int chunk : {max_chunk, 1})
+            for (bool fox : {false, true}) {
+                const size_t s = step_ws_bytes(cache, num_tokens, chunk, fox);
+                n = s > n ? s : n;
+            }
     }
     return n;
 }

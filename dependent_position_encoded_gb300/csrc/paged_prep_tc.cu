@@ -170,6 +170,87 @@ __device__ __forceinline__ void make_plans(const Step &a, const TcWs &y, long lo
     }
 }
 
+// A sequence's only token: H = I - beta w w^T, q~ = q - beta (w . q) w, and the token's own key
+// and value enter the cache as they are. A warp per query head in turns; all threads form the
+// product less I, -beta w w^T.
+template <int D>
+__device__ __forceinline__ void prep_single(const Step &a, const TcWs &y, const Seq &s, int b, int slot, int h,
+                                            float *buf) {
+    constexpr int E = D / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.c.G, kw = kThr / 32;
+    const float beta = a.beta[(long long)s.first * a.sb.tok + h * a.sb.head];
+    auto row = [&](const void *p, Stride st, int head) {
+        return static_cast<const bf *>(p) + (long long)s.first * st.tok + (long long)head * st.head + lane * E;
+    };
+    const bf *const wp = row(a.w, a.sw, h), *const kp = row(a.k, a.sk, h), *const vp = row(a.v, a.sv, h);
+    float w[E], k[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        w[e] = __bfloat162float(wp[e]);
+        k[e] = __bfloat162float(kp[e]);
+    }
+    if (warp == 0)
+#pragma unroll
+        for (int e = 0; e < E; ++e) buf[lane * E + e] = w[e];
+    const int pos = s.n, sl = pos >> a.c.page_shift, off = pos & (a.c.page - 1);
+    const int kid = page_of(a, a.c.k_table, b, sl, a.c.nk), vid = page_of(a, a.c.v_table, b, sl, a.c.nv);
+    if (warp == kw - 1) {
+        if (kid >= 0)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                static_cast<bf *>(a.c.k_pages)[((((size_t)kid * a.c.Hkv + h) << a.c.page_shift) + off) * D + lane * E +
+                                               e] = kp[e];
+        if (vid >= 0)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                static_cast<bf *>(a.c.v_pages)[((((size_t)vid * a.c.Hkv + h) << a.c.page_shift) + off) * D + lane * E +
+                                               e] = vp[e];
+    }
+    for (int g = warp; g < G; g += kw) {
+        const int hq = h * G + g;
+        const bf *const qp = row(a.q, a.sq, hq);
+        float q[E], wq = 0.f, kq = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            q[e] = __bfloat162float(qp[e]);
+            wq = fmaf(w[e], q[e], wq);
+            kq = fmaf(k[e], q[e], kq);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            wq += __shfl_xor_sync(0xffffffffu, wq, o);
+            kq += __shfl_xor_sync(0xffffffffu, kq, o);
+        }
+        const size_t r = (size_t)h * y.R + (size_t)s.first * G + g;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            y.qt[r * D + lane * E + e] = __float2bfloat16_rn(fmaf(-beta * wq, w[e], q[e]) * a.scale_log2);
+            y.po[r * D + lane * E + e] = __bfloat162float(vp[e]);
+        }
+        if (lane == 0) {
+            y.pml[r] = make_float2(kq * a.scale_log2, 1.f);
+            if (a.log_f != nullptr) {
+                const float f = a.log_f[(long long)s.first * a.sf.tok + (long long)hq * a.sf.head];
+                y.gq[r] = f;
+                y.gtot[(size_t)slot * a.c.Hq + hq] = f;
+                if (kid >= 0) a.c.g_pages[(((size_t)kid * a.c.Hq + hq) << a.c.page_shift) + off] = 0.f;
+            }
+        }
+    }
+    if (s.n == 0) return;  // no cached key takes the product
+    __syncthreads();
+    bf *const mh = y.mt + ((size_t)b * a.c.Hkv + h) * 2 * D * D, *const ml = mh + (size_t)D * D;
+    for (int e = tid; e < D * D / 8; e += kThr) {
+        const int i = e / (D / 8), j = e % (D / 8) * 8;
+        const float f = -beta * buf[i];
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) split2(f * buf[j + 2 * q], f * buf[j + 2 * q + 1], hi[q], lo[q]);
+        *reinterpret_cast<uint4 *>(mh + (size_t)i * D + j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(ml + (size_t)i * D + j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const Step a, const TcWs y) {
     using S = PrepSmem<D>;
@@ -196,6 +277,10 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
         return;
     }
     if (!block_of(a, slot, b, c, s)) return;
+    if (s.T == 1) {
+        if (blockIdx.z == 0) prep_single<D>(a, y, s, b, slot, h, reinterpret_cast<float *>(smem));
+        return;
+    }
     const int rows = min(kC, s.T - c * kC), nt = (rows + 15) >> 4;
     const bool single = s.T <= kC;
     const long long first = s.first + c * kC;
@@ -841,13 +926,31 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
         L = fmaf(L, f0, l);
 #pragma unroll
         for (int e = 0; e < E; ++e) O[e] *= f0;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float w = __shfl_sync(0xffffffffu, f, i);
-            if (w == 0.f) continue;  // absent keys alone, or nothing beside the others
-            const float *o = so + part_at(p0 + i) * D + lane * E;
+        // eight parts' rows in flight at a time (an absent part's weight is 0 and its row 0)
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            float v[8][E], w[8];
 #pragma unroll
-            for (int e = 0; e < E; ++e) O[e] = fmaf(o[e], w, O[e]);
+            for (int i = 0; i < 8; ++i) {
+                const int q = min(i0 + i, n - 1);
+                w[i] = __shfl_sync(0xffffffffu, f, q);
+                if (i0 + i >= n) w[i] = 0.f;
+                const float *o = so + part_at(p0 + q) * D + lane * E;
+                if (E == 2) {
+                    const float2 t = *reinterpret_cast<const float2 *>(o);
+                    v[i][0] = t.x;
+                    v[i][1] = t.y;
+                } else {
+                    const float4 t = *reinterpret_cast<const float4 *>(o);
+                    v[i][0] = t.x;
+                    v[i][1] = t.y;
+                    v[i][E - 2] = t.z;
+                    v[i][E - 1] = t.w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < E; ++e) O[e] = fmaf(v[i][e], w[i], O[e]);
         }
     }
     bf *dst = static_cast<bf *>(a.out) + (long long)tok * a.so.tok + hq * a.so.head + lane * E;
