@@ -542,58 +542,72 @@ _I32_FIELDS = ("k_table", "v_table", "lens", "k_ref", "v_ref")
 def _paged_cache(cache, counts=False, Hq=None, on_gpu=True):
     """Checks the cache's tensors and returns its C form. Shapes and dtypes are checked before
     devices (on_gpu=False: the caller checks those with _paged_devices), so that every size
-    error is raised before any call."""
+    error is raised before any call. What is usual is tested in one expression (a step's host
+    time is a few microseconds); what fails it goes through _paged_cache_errors."""
     torch = _torch()
-    if not isinstance(cache, PathPagedCache):
-        raise TypeError("cache must be a PathPagedCache")
-    kp, vp, gp = cache.k_pages, cache.v_pages, cache.g_pages
-    ints = (cache.k_table, cache.v_table, cache.lens, cache.k_ref, cache.v_ref)
-    used = 5 if counts or ints[3] is not None or ints[4] is not None else 3
-    Tensor, i32 = torch.Tensor, torch.int32
-    if not isinstance(kp, Tensor) or not isinstance(vp, Tensor):
-        raise TypeError("k_pages and v_pages must be tensors")
-    for t, n in zip(ints[:used], _I32_FIELDS):
-        if not isinstance(t, Tensor):
-            raise TypeError("%s must be a tensor" % n)
-        if t.dtype != i32:
-            raise TypeError("%s must be %s, got %s" % (n, i32, t.dtype))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % n)
-    ks, vs = kp.shape, vp.shape
-    if len(ks) != 4 or len(vs) != 4 or ks[1:] != vs[1:]:
-        raise ValueError("k_pages and v_pages must be (pages, Hkv, page, d) of equal pages")
-    if vp.dtype != kp.dtype:
-        raise TypeError("v_pages must be %s, got %s" % (kp.dtype, vp.dtype))
-    dt = _dtype_code(kp)
-    nk, Hkv, page, d = ks
-    ts = ints[0].shape
-    if len(ts) != 2 or ints[1].shape != ts:
-        raise ValueError("k_table and v_table must be (seqs, max_pages) of equal shape")
-    seqs, max_pages = ts
-    if ints[2].shape != (seqs,):
-        raise ValueError("lens must be (seqs,)")
-    if used == 5 and (ints[3].shape != (nk,) or ints[4].shape != (vs[0],)):
-        raise ValueError("k_ref and v_ref must hold one count per page")
-    if gp is not None:
-        if not isinstance(gp, Tensor):
-            raise TypeError("g_pages must be a tensor")
-        if gp.dtype != torch.float32:
-            raise TypeError("g_pages must be %s, got %s" % (torch.float32, gp.dtype))
-        gs = gp.shape
-        if len(gs) != 3 or gs[0] != nk or gs[2] != page or (Hq is not None and gs[1] != Hq):
-            raise ValueError("g_pages must be (K pages, Hq, page)")
-        if not gp.is_contiguous():
-            raise ValueError("g_pages must be contiguous")
-        Hq = gs[1]
-    if not kp.is_contiguous() or not vp.is_contiguous():
-        raise ValueError("k_pages and v_pages must be contiguous")
+    i32 = torch.int32
+    try:
+        kp, vp, gp, kt, vt = cache.k_pages, cache.v_pages, cache.g_pages, cache.k_table, cache.v_table
+        ln, kr, vr = cache.lens, cache.k_ref, cache.v_ref
+        ks, vs, ts, dtype = kp.shape, vp.shape, kt.shape, kp.dtype
+        nk, Hkv, page, d = ks
+        seqs, max_pages = ts
+        refs = counts or kr is not None or vr is not None
+        fine = (ks[1:] == vs[1:] and vp.dtype == dtype and kt.dtype == i32 and vt.dtype == i32
+                and ln.dtype == i32 and vt.shape == ts and ln.shape == (seqs,) and kp.is_contiguous()
+                and vp.is_contiguous() and kt.is_contiguous() and vt.is_contiguous()
+                and ln.is_contiguous())
+        if fine and refs:
+            fine = (kr.dtype == i32 and vr.dtype == i32 and kr.shape == (nk,)
+                    and vr.shape == (vs[0],) and kr.is_contiguous() and vr.is_contiguous())
+        if fine and gp is not None:
+            if Hq is None:
+                Hq = gp.shape[1]
+            fine = (gp.dtype == torch.float32 and gp.shape == (nk, Hq, page)
+                    and gp.is_contiguous())
+    except (AttributeError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine or type(cache) is not PathPagedCache:
+        _paged_cache_errors(cache, counts, Hq)
+    code = _dtype_code_of(dtype)
     if on_gpu:
         _paged_devices(cache)
     return _CPagedCache(kp.data_ptr(), vp.data_ptr(), None if gp is None else gp.data_ptr(),
-                        *[t.data_ptr() for t in ints[:2]],
-                        *([t.data_ptr() for t in ints[3:]] if used == 5 else (None, None)),
-                        ints[2].data_ptr(), seqs, max_pages, page, nk, vs[0],
-                        Hkv if Hq is None else Hq, Hkv, d, dt)
+                        kt.data_ptr(), vt.data_ptr(), kr.data_ptr() if refs else None,
+                        vr.data_ptr() if refs else None, ln.data_ptr(), seqs, max_pages, page, nk,
+                        vs[0], Hkv if Hq is None else Hq, Hkv, d, code)
+
+
+def _paged_cache_errors(cache, counts, Hq):
+    """Raises what is wrong with the cache."""
+    torch = _torch()
+    if type(cache) is not PathPagedCache:
+        raise TypeError("cache must be a PathPagedCache")
+    kp, vp, gp = cache.k_pages, cache.v_pages, cache.g_pages
+    named = [("k_table", cache.k_table), ("v_table", cache.v_table), ("lens", cache.lens)]
+    if counts or cache.k_ref is not None or cache.v_ref is not None:
+        named += [("k_ref", cache.k_ref), ("v_ref", cache.v_ref)]
+    for n, t in [("k_pages", kp), ("v_pages", vp)] + named + ([("g_pages", gp)] if gp is not None else []):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a tensor" % n)
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % n)
+    for n, t in named:
+        if t.dtype != torch.int32:
+            raise TypeError("%s must be %s, got %s" % (n, torch.int32, t.dtype))
+    if kp.dim() != 4 or vp.dim() != 4 or kp.shape[1:] != vp.shape[1:]:
+        raise ValueError("k_pages and v_pages must be (pages, Hkv, page, d) of equal pages")
+    if vp.dtype != kp.dtype:
+        raise TypeError("v_pages must be %s, got %s" % (kp.dtype, vp.dtype))
+    if cache.k_table.dim() != 2 or cache.v_table.shape != cache.k_table.shape:
+        raise ValueError("k_table and v_table must be (seqs, max_pages) of equal shape")
+    if cache.lens.shape != (cache.k_table.shape[0],):
+        raise ValueError("lens must be (seqs,)")
+    if gp is not None:
+        if gp.dtype != torch.float32:
+            raise TypeError("g_pages must be %s, got %s" % (torch.float32, gp.dtype))
+        raise ValueError("g_pages must be (K pages, Hq, page), k_ref and v_ref one count per page")
+    raise ValueError("k_ref and v_ref must hold one count per page")
 
 
 def _paged_devices(cache, *more):
@@ -650,46 +664,42 @@ def new_paged_workspace(cache, num_tokens=0, max_chunk=0, Hq=None):
 def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, scale, out,
                   workspace, stream):
     torch = _torch()
-    Tensor, f32 = torch.Tensor, torch.float32
-    kp = cache.k_pages if isinstance(cache, PathPagedCache) else None
-    if not isinstance(q, Tensor) or not isinstance(kp, Tensor):
-        raise TypeError("q must be a tensor and cache a PathPagedCache of tensors")
-    if q.dim() != 3:
-        raise ValueError("q must be (tokens, Hq, d)")
-    if kp.dim() != 4:
-        raise ValueError("k_pages must be (pages, Hkv, page, d)")
-    qs = q.shape
-    N, Hq, d = qs
-    Hkv, dt, dev = kp.shape[1], kp.dtype, kp.device
+    f32 = torch.float32
+    try:
+        kp = cache.k_pages
+        dt, dev, Hkv = kp.dtype, kp.device, kp.shape[1]
+        qs = q.shape
+        N, Hq, d = qs
+        rows, heads = (N, Hkv, d), (N, Hkv)
+        q0, k0, v0, w0 = q.stride(), k.stride(), v.stride(), w.stride()
+        b0 = beta.stride()
+        f0 = (0, 0) if log_f is None else log_f.stride()
+        o0 = (Hq * d, d, 1) if out is None else out.stride()
+        fine = (q.dtype == dt and k.dtype == dt and v.dtype == dt and w.dtype == dt
+                and beta.dtype == f32 and cu_tokens.dtype == torch.int32 and k.shape == rows
+                and v.shape == rows and w.shape == rows and beta.shape == heads
+                and cu_tokens.dim() == 1 and cu_tokens.is_contiguous()
+                and q0[2] == 1 and k0[2] == 1 and v0[2] == 1 and w0[2] == 1 and o0[2] == 1
+                and (log_f is None or (log_f.dtype == f32 and log_f.shape == qs[:2]))
+                and (out is None or (out.dtype == dt and out.shape == qs)))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        fine = False
+    if not fine:
+        _paged_extend_errors(q, k, v, w, beta, log_f, cu_tokens, cache, out)
     c = _paged_cache(cache, Hq=Hq, on_gpu=False)
-    ks, bs = (N, Hkv, d), (N, Hkv)
-    st = []
-    for t, n, shape, want in ((q, "q", qs, dt), (k, "k", ks, dt), (v, "v", ks, dt), (w, "w", ks, dt),
-                              (beta, "beta", bs, f32), (log_f, "log_f", qs[:2], f32),
-                              (out, "out", qs, dt)):
-        if t is None and (n == "log_f" or n == "out"):
-            st += (0, 0) if n == "log_f" else (Hq * d, d)
-            continue
-        if not isinstance(t, Tensor):
-            raise TypeError("%s must be a tensor" % n)
-        if t.dtype != want:
-            raise TypeError("%s must be %s, got %s" % (n, want, t.dtype))
-        if t.shape != shape:
-            raise ValueError("%s must have shape %s, got %s" % (n, tuple(shape), tuple(t.shape)))
-        s = t.stride()
-        if len(s) == 3 and s[2] != 1:
-            raise ValueError("the last axis of %s must be contiguous" % n)
-        # the stride of an axis of one element says nothing
-        st += (s[0] if N > 1 else 0, s[1] if shape[1] > 1 else 0)
-    if not isinstance(cu_tokens, Tensor) or cu_tokens.dtype != torch.int32:
-        raise TypeError("cu_tokens must be an int32 tensor")
-    if cu_tokens.shape != (c.seqs + 1,) or not cu_tokens.is_contiguous():
-        raise ValueError("cu_tokens must be (seqs + 1,), contiguous")
+    if cu_tokens.shape[0] != c.seqs + 1:
+        raise ValueError("cu_tokens must be (seqs + 1,)")
     if d != c.d:
         raise ValueError("q has head size %d, the cache %d" % (d, c.d))
-    if out is not None and out.numel() and (N > 1 and st[12] == 0 or Hq > 1 and st[13] == 0):
+    if out is not None and (N > 1 and o0[0] == 0 or Hq > 1 and o0[1] == 0):
         raise ValueError("out must not repeat its own memory")
     _paged_devices(cache, q, k, v, w, beta, log_f, out, cu_tokens)
+    st = (q0[0], q0[1], k0[0], k0[1], v0[0], v0[1], w0[0], w0[1], b0[0], b0[1], f0[0], f0[1], o0[0],
+          o0[1])
+    if N <= 1 or Hkv <= 1:  # the stride of an axis of one element says nothing
+        one = (N <= 1, Hq <= 1, N <= 1, Hkv <= 1)
+        st = [0 if one[(i & 1) + (0 if i in (0, 1, 10, 11, 12, 13) else 2)] else x
+              for i, x in enumerate(st)]
     gate = () if log_f is None else (log_f.data_ptr(),)
     with _on(dev, stream):
         if out is None:
@@ -702,6 +712,35 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
             out.data_ptr(), _C14(*st), None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel(), _stream(stream, dev)), name)
     return out
+
+
+def _paged_extend_errors(q, k, v, w, beta, log_f, cu_tokens, cache, out):
+    """Raises what is wrong with a step's tensors (or with the cache)."""
+    torch = _torch()
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a tensor")
+    if q.dim() != 3:
+        raise ValueError("q must be (tokens, Hq, d)")
+    N, Hq, d = q.shape
+    _paged_cache(cache, Hq=Hq, on_gpu=False)
+    Hkv, dt = cache.k_pages.shape[1], cache.k_pages.dtype
+    for t, n, shape, want in ((q, "q", (N, Hq, d), dt), (k, "k", (N, Hkv, d), dt),
+                              (v, "v", (N, Hkv, d), dt), (w, "w", (N, Hkv, d), dt),
+                              (beta, "beta", (N, Hkv), torch.float32),
+                              (log_f, "log_f", (N, Hq), torch.float32), (out, "out", (N, Hq, d), dt)):
+        if t is None and n in ("log_f", "out"):
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a tensor" % n)
+        if t.dtype != want:
+            raise TypeError("%s must be %s, got %s" % (n, want, t.dtype))
+        if tuple(t.shape) != shape:
+            raise ValueError("%s must have shape %s, got %s" % (n, shape, tuple(t.shape)))
+        if len(shape) == 3 and t.stride()[2] != 1:
+            raise ValueError("the last axis of %s must be contiguous" % n)
+    if not isinstance(cu_tokens, torch.Tensor) or cu_tokens.dtype != torch.int32:
+        raise TypeError("cu_tokens must be an int32 tensor")
+    raise ValueError("cu_tokens must be (seqs + 1,), contiguous")
 
 
 def path_paged_extend(q, k, v, w, beta, cu_tokens, cache, max_chunk, scale=None, out=None,

@@ -82,17 +82,27 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-// multiplies N fp32 columns of the thread's row by f
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// multiplies N fp32 columns of the thread's row by f (16 at a time: the row's logits are in
+// registers beside it)
 template <int N>
 __device__ __forceinline__ void tmem_scale(uint32_t taddr, float f) {
 #pragma unroll 1
-    for (int c = 0; c < N; c += 32) {
-        uint32_t u[32];
-        tmem_ld32(taddr + c, u);
+    for (int c = 0; c < N; c += 16) {
+        uint32_t u[16];
+        tmem_ld16(taddr + c, u);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * f);
-        tmem_st32(taddr + c, u);
+        for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) * f);
+        tmem_st16(taddr + c, u);
     }
     tmem_st_wait();
 }
@@ -490,29 +500,53 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 const unsigned have = __ballot_sync(0xffffffffu, good);
                 const int valid = min(128, t.s.n - pos0);
                 const bool whole = tile_whole(pos0, t.s.n, have, box_shift);
+                // gate sums of 32 keys from column c for the row's query head
+                auto gates_of = [&](int c, float4 *v) {
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {  // 16 positions lie in one page
+                        const int bx = (c + 4 * e) >> box_shift;
+                        const int pid = __shfl_sync(0xffffffffu, id, bx);
+                        const bool in = (have >> bx) & 1u;
+                        const float4 *gp = reinterpret_cast<const float4 *>(
+                            a.c.g_pages + (((size_t)(in ? pid : 0) * a.c.Hq + hq) << a.c.page_shift) +
+                            ((pos0 + c + 4 * e) & (page - 1)));
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v[e + q] = in ? __ldg(gp + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                };
+                // on their way while the product runs: in registers where there are enough for the 32
+                // columns of a copy, else into L1
+                constexpr bool kAhead = FOX && NT == 1 && D == 128;
+                float4 ahead[kAhead ? 8 : 1];
+                const bool early = kAhead && cols == 32;
+                if (early) {
+                    gates_of(c_begin, ahead);
+                } else if (FOX) {
+#pragma unroll 1
+                    for (int c = c_begin; c < c_begin + cols; c += 16) {
+                        const int bx = c >> box_shift, pid = __shfl_sync(0xffffffffu, id, bx);
+                        if ((have >> bx) & 1u)
+                            asm volatile("prefetch.global.L1 [%0];" ::"l"(
+                                a.c.g_pages + (((size_t)pid * a.c.Hq + hq) << a.c.page_shift) +
+                                ((pos0 + c) & (page - 1))));
+                    }
+                }
                 if (!(ok = wait.warp(bar(L::SF + w), j & 1))) break;
                 tc_fence_after();
                 if (warp_live) {
                     // gates and mask of 32 logits of the row from column c
                     auto gate = [&](int c, float *x) {
                         if (FOX) {
+                            float4 own[8];
+                            if (!early) gates_of(c, own);
 #pragma unroll
-                            for (int e = 0; e < 32; e += 16) {  // 16 positions lie in one page
-                                const int bx = (c + e) >> box_shift;
-                                const int pid = __shfl_sync(0xffffffffu, id, bx);
-                                const bool in = (have >> bx) & 1u;
-                                const float4 *gp = reinterpret_cast<const float4 *>(
-                                    a.c.g_pages + (((size_t)(in ? pid : 0) * a.c.Hq + hq) << a.c.page_shift) +
-                                    ((pos0 + c + e) & (page - 1)));
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const float4 g4 = in ? __ldg(gp + q) : make_float4(0.f, 0.f, 0.f, 0.f);
-                                    float *v = x + e + 4 * q;
-                                    v[0] = fmaf(g4.x, kLog2e, v[0] + gq);
-                                    v[1] = fmaf(g4.y, kLog2e, v[1] + gq);
-                                    v[2] = fmaf(g4.z, kLog2e, v[2] + gq);
-                                    v[3] = fmaf(g4.w, kLog2e, v[3] + gq);
-                                }
+                            for (int q = 0; q < 8; ++q) {
+                                const float4 g4 = early ? ahead[kAhead ? q : 0] : own[q];
+                                float *v = x + 4 * q;
+                                v[0] = fmaf(g4.x, kLog2e, v[0] + gq);
+                                v[1] = fmaf(g4.y, kLog2e, v[1] + gq);
+                                v[2] = fmaf(g4.z, kLog2e, v[2] + gq);
+                                v[3] = fmaf(g4.w, kLog2e, v[3] + gq);
                             }
                         }
                         if (!whole) {
@@ -652,22 +686,25 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
 // The state is the fp32 accumulator itself in TMEM; each step's products take a bf16 copy
 // of it (rows that do not take part yet have a zero copy and so keep their state). At the
 // end the state is the query carried to the chunk's start.
-// Warps: 0-3 softmax, one row per thread; 4-7 the bf16 copy of the state; 8 allocates TMEM,
-// issues the MMAs and streams [k~_b; P_b - I] and V_b.
+// Per step the logits go first, so that the softmax runs beside the state's product and copy,
+// which are the chain from step to step.
+// Warps: 0-3 softmax, one row per thread; 4-7 the bf16 copy of the state; 8 allocates TMEM and
+// issues the MMAs; 9 streams [k~_b; P_b - I] and V_b.
 template <int D>
 struct ScanSmem {
     static constexpr int NR = 3, NV = 2;
     static constexpr uint32_t xtile = 128 * D * 2, xatom = 128 * 128, ratom = (64 + D) * 128, rtile = ratom * (D / 64),
                               vatom = 64 * 128, vtile = vatom * (D / 64);
     static constexpr uint32_t X = 0, R = X + xtile, V = R + NR * rtile, bars = V + NV * vtile;
-    static constexpr int RF = 0, RE = RF + NR, VF = RE + NR, VE = VF + NV, SX = VE + NV, XR = SX + 1, SFREE = XR + 1,
+    static constexpr int RF = 0, RE = RF + NR, VF = RE + NR, VE = VF + NV, SD = VE + NV, XD = SD + 1, XR = XD + 1,
+                         SFREE = XR + 1,
                          PR = SFREE + 1, PV = PR + 1, FIN = PV + 1, count = FIN + 1;
     static constexpr uint32_t bytes = bars + count * 8 + 16, alloc = bytes + 1024;
     // TMEM columns
     static constexpr uint32_t cS = 0, cP = 64, cX = 128, cO = 128 + D, cols = D == 64 ? 256 : 512;
 };
 
-constexpr int kScanThr = 288;
+constexpr int kScanThr = 320;
 
 template <int D, bool FOX>
 __global__ void __launch_bounds__(kScanThr, D == 64 ? 2 : 1)
@@ -713,49 +750,51 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
     const size_t row = (size_t)h * y.R + (size_t)s.first * G + row0 + r;
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
 
-    if (warp == 8) {
+    if (warp == 9) {
+        // ============================================================ factors and values
         if (lane == 0) {
-            int r_iss = 0, v_iss = 0, r_done = 0, v_done = 0;
-            auto load_r = [&](int st) {
-                const int kb = hi - 1 - st, i = st % L::NR, head = slot_of(s, b, kb) * a.c.Hkv + h;
+            int r = 0, v = 0;
+            bool ok = true;
+            for (int st = 0; ok && st < steps; ++st) {
+                const int head = slot_of(s, b, hi - 1 - st) * a.c.Hkv + h, i = st % L::NR, q = st % L::NV;
+                if (st >= L::NR && !(ok = wait(bar(L::RE + i), (st / L::NR - 1) & 1))) break;
                 mbar_arrive_expect_tx(bar(L::RF + i), L::rtile);
                 for (int x = 0; x < NA; ++x)
                     tma_load_3d(base + L::R + i * L::rtile + x * L::ratom, &tm_r, bar(L::RF + i), 64 * x, 0, head);
-                ++r_iss;
-            };
-            auto load_v = [&](int st) {
-                const int kb = hi - 1 - st, i = st % L::NV, head = slot_of(s, b, kb) * a.c.Hkv + h;
-                mbar_arrive_expect_tx(bar(L::VF + i), L::vtile);
+                ++r;
+                if (st >= L::NV && !(ok = wait(bar(L::VE + q), (st / L::NV - 1) & 1))) break;
+                mbar_arrive_expect_tx(bar(L::VF + q), L::vtile);
                 for (int x = 0; x < NA; ++x)
-                    tma_load_3d(base + L::V + i * L::vtile + x * L::vatom, &tm_v, bar(L::VF + i), 64 * x, 0, head);
-                ++v_iss;
-            };
-            for (int st = 0; st < steps && st < L::NR; ++st) load_r(st);
-            for (int st = 0; st < steps && st < L::NV; ++st) load_v(st);
+                    tma_load_3d(base + L::V + q * L::vtile + x * L::vatom, &tm_v, bar(L::VF + q), 64 * x, 0, head);
+                ++v;
+            }
+            if (!ok) {  // an abort: no copy may land after the CTA is gone
+                for (int st = r > L::NR ? r - L::NR : 0; st < r; ++st)
+                    mbar_wait(bar(L::RF + st % L::NR), (st / L::NR) & 1, limit_ns);
+                for (int st = v > L::NV ? v - L::NV : 0; st < v; ++st)
+                    mbar_wait(bar(L::VF + st % L::NV), (st / L::NV) & 1, limit_ns);
+            }
+        }
+    } else if (warp == 8) {
+        // ============================================================ MMA issue
+        if (lane == 0) {
             constexpr uint32_t ID_S = idesc_b16(128, 64, false), ID_X = idesc_b16(128, D, false),
                                ID_O = idesc_b16(128, D, true);
             bool ok = true;
             auto issue_pv = [&](int st) -> bool {
                 const int i = st % L::NV;
-                if (!wait(bar(L::VF + i), (st / L::NV) & 1)) return false;
-                ++v_done;
-                if (!wait(bar(L::PR), st & 1)) return false;
+                if (!wait(bar(L::VF + i), (st / L::NV) & 1) || !wait(bar(L::PR), st & 1)) return false;
                 tc_fence_after();
                 const uint64_t v = sdesc_sw128(base + L::V + i * L::vtile, L::vatom, 1024);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) umma_tA(tmem + L::cO, tmem + L::cP + 8 * kk, v + 128 * kk, ID_O, 1);
                 umma_commit(bar(L::PV));
                 umma_commit(bar(L::VE + i));
-                if (st + L::NV < steps) {
-                    if (!wait(bar(L::VE + i), (st / L::NV) & 1)) return false;
-                    load_v(st + L::NV);
-                }
                 return true;
             };
             for (int st = 0; ok && st < steps; ++st) {
                 const int i = st % L::NR;
                 if (!(ok = wait(bar(L::RF + i), (st / L::NR) & 1))) break;
-                ++r_done;
                 if (!(ok = wait(bar(L::XR), st & 1))) break;                       // the copy of the state
                 if (st > 0 && !(ok = wait(bar(L::SFREE), (st - 1) & 1))) break;    // the last logits read
                 tc_fence_after();
@@ -764,26 +803,19 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
                 for (int kk = 0; kk < D / 16; ++kk)
                     umma_bf16(tmem + L::cS, sdesc_sw128(base + L::X + (kk >> 2) * L::xatom, 16, 1024) + 2 * (kk & 3),
                               sdesc_sw128(rs + (kk >> 2) * L::ratom, 16, 1024) + 2 * (kk & 3), ID_S, kk > 0);
+                umma_commit(bar(L::SD));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     umma_bf16(tmem + L::cX, sdesc_sw128(base + L::X + (kk >> 2) * L::xatom, 16, 1024) + 2 * (kk & 3),
                               sdesc_sw128(rs + 64 * 128 + (kk >> 2) * L::ratom, 16, 1024) + 2 * (kk & 3), ID_X, 1);
-                umma_commit(bar(L::SX));
+                umma_commit(bar(L::XD));
                 umma_commit(bar(L::RE + i));
-                // P V of the previous step behind this step's products; then the slot of the step
-                // before refills
+                // P V of the previous step behind this step's products
                 if (st > 0 && !(ok = issue_pv(st - 1))) break;
-                if (st > 0 && st - 1 + L::NR < steps) {
-                    const int pi = (st - 1) % L::NR;
-                    if (!(ok = wait(bar(L::RE + pi), ((st - 1) / L::NR) & 1))) break;
-                    load_r(st - 1 + L::NR);
-                }
             }
             if (ok) ok = issue_pv(steps - 1);
             umma_commit(bar(L::FIN));
             mbar_wait(bar(L::FIN), 0, limit_ns);
-            for (; r_done < r_iss; ++r_done) mbar_wait(bar(L::RF + r_done % L::NR), (r_done / L::NR) & 1, limit_ns);
-            for (; v_done < v_iss; ++v_done) mbar_wait(bar(L::VF + v_done % L::NV), (v_done / L::NV) & 1, limit_ns);
         }
     } else if (warp < 4) {
         // ============================================================ softmax
@@ -812,39 +844,50 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
         for (int st = 0; st < steps; ++st) {
             const int kb = hi - 1 - st;
             const bool part = kb < own;  // the same for the warp
-            if (!(ok = wait.warp(bar(L::SX), st & 1))) break;
+            const int ks = slot_of(s, b, kb);
+            const float4 *const gt =
+                FOX ? reinterpret_cast<const float4 *>(y.gt + ((size_t)ks * a.c.Hq + hq) * kC) : nullptr;
+            float bias = 0.f;
+            double block = 0.0;
+            if (FOX && part) {  // on their way while the product runs
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(gt));
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(gt + 8));
+                block = y.gtot[(size_t)ks * a.c.Hq + hq];
+                bias = (float)((double)gq + between) * kLog2e;
+            }
+            if (!(ok = wait.warp(bar(L::SD), st & 1))) break;
             tc_fence_after();
             float x[64];
-            if (part) {
-                tld32(tmem + lane_off + L::cS, x);
-                tld32(tmem + lane_off + L::cS + 32, x + 32);
+            {
+                uint32_t(*u)[32] = reinterpret_cast<uint32_t(*)[32]>(x);
+                tmem_ld32(tmem + lane_off + L::cS, u[0]);
+                tmem_ld32(tmem + lane_off + L::cS + 32, u[1]);
+                tmem_ld_wait();
             }
             tc_fence_before();
             mbar_arrive_warp(bar(L::SFREE));
-            if (part) {
-                const int ks = slot_of(s, b, kb);
-                if (FOX) {
-                    const float bias = (float)((double)gq + between) * kLog2e;
-                    const float4 *gt = reinterpret_cast<const float4 *>(y.gt + ((size_t)ks * a.c.Hq + hq) * kC);
+            if (FOX && part) {
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const float4 g4 = __ldg(gt + q);
-                        x[4 * q] = fmaf(g4.x, kLog2e, x[4 * q] + bias);
-                        x[4 * q + 1] = fmaf(g4.y, kLog2e, x[4 * q + 1] + bias);
-                        x[4 * q + 2] = fmaf(g4.z, kLog2e, x[4 * q + 2] + bias);
-                        x[4 * q + 3] = fmaf(g4.w, kLog2e, x[4 * q + 3] + bias);
-                    }
-                    between += y.gtot[(size_t)ks * a.c.Hq + hq];
+                for (int q = 0; q < 16; ++q) {
+                    const float4 g4 = __ldg(gt + q);
+                    x[4 * q] = fmaf(g4.x, kLog2e, x[4 * q] + bias);
+                    x[4 * q + 1] = fmaf(g4.y, kLog2e, x[4 * q + 1] + bias);
+                    x[4 * q + 2] = fmaf(g4.z, kLog2e, x[4 * q + 2] + bias);
+                    x[4 * q + 3] = fmaf(g4.w, kLog2e, x[4 * q + 3] + bias);
                 }
+                between += block;
             }
             // P and O are free once the previous P V has completed
             if (st > 0 && !(ok = wait.warp(bar(L::PV), (st - 1) & 1))) break;
             tc_fence_after();
-            uint32_t p[32];
+            uint32_t p[16];
             if (part) {
-                float mx = -INFINITY;
+                float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int c = 0; c < 64; c += 2) mx = fmax3(mx, x[c], x[c + 1]);
+                for (int c = 4; c < 60; c += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) m4[q] = fmax3(m4[q], x[c + 2 * q], x[c + 2 * q + 1]);
+                const float mx = fmax3(fmax3(m4[0], m4[1], m4[2]), fmax3(m4[3], x[60], x[61]), fmaxf(x[62], x[63]));
                 float alpha = 1.f;
                 if (mx > m_run + kRescale) {
                     alpha = ex2_approx(m_run - mx);
@@ -853,20 +896,27 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
                 if (!live) alpha = 1.f;
                 if (__any_sync(0xffffffffu, alpha != 1.f)) tmem_scale<D>(tmem + lane_off + L::cO, alpha);
                 l_run *= alpha;
-                const float use = m_run == -INFINITY ? 0.f : m_run;
-                float sum = 0.f;
+                // rows past the sequence's end weigh as they will: nobody reads their sums
+                const float use = m_run == -INFINITY ? 0.f : -m_run;
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int c = 0; c < 64; c += 2) {
-                    const float p0 = live ? ex2_approx(x[c] - use) : 0.f, p1 = live ? ex2_approx(x[c + 1] - use) : 0.f;
-                    sum += p0 + p1;
-                    p[c / 2] = pack_bf16x2(p0, p1);
+                for (int half = 0; half < 64; half += 32) {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        const float2 z = fadd2(make_float2(x[half + c], x[half + c + 1]), make_float2(use, use));
+                        const float2 q = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+                        sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], q);
+                        p[c / 2] = pack_bf16x2(q.x, q.y);
+                    }
+                    tmem_st16(tmem + lane_off + L::cP + half / 2, p);
                 }
-                l_run += sum;
+                l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             } else {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) p[c] = 0u;
+                for (int c = 0; c < 16; ++c) p[c] = 0u;
+                tmem_st16(tmem + lane_off + L::cP, p);
+                tmem_st16(tmem + lane_off + L::cP + 16, p);
             }
-            tmem_st32(tmem + lane_off + L::cP, p);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive_warp(bar(L::PR));
@@ -889,7 +939,7 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
                 if (FOX) y.gq[row] = (float)((double)gq + between);
             }
         }
-    } else {
+    } else if (warp < 8) {
         // ============================================================ the state's bf16 copy
         bool ok = true;
         uint8_t *const xs = sm + L::X;
@@ -926,7 +976,7 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
         tc_fence_before();
         mbar_arrive_warp(bar(L::XR));
         for (int st = 1; st < steps; ++st) {
-            if (!(ok = wait.warp(bar(L::SX), (st - 1) & 1))) break;
+            if (!(ok = wait.warp(bar(L::XD), (st - 1) & 1))) break;
             tc_fence_after();
             const bool take = hi - 1 - st < own;
 #pragma unroll 1

@@ -24,13 +24,13 @@ using bf = __nv_bfloat16;
 // every product is cut to those (a step of a few tokens costs a few tiles).
 template <int D>
 struct PrepSmem {
-    static constexpr int LDD = D + 8, LDS = 72, LDF = 68;  // row strides: 16-byte phases differ
+    static constexpr int LDD = D + 8, LDS = 72, LDF = 72;  // row strides: 16-byte phases differ
     static constexpr size_t big = (size_t)kC * LDD * 2, sml = (size_t)kC * LDS * 2;
     static constexpr size_t W = 0, K = big, Q = 2 * big, V = 3 * big;  // U (hi, lo) lies in Q, V
     static constexpr size_t Ah = 4 * big, Al = Ah + sml, Rh = Al + sml, Rl = Rh + sml, Lh = Rl + sml,
                             Ll = Lh + sml, Th = Ll + sml, Tl = Th + sml, F = Th;
-    // fp32 64 x 68 (E, the logits) lies in [Th, Tl]; the pair Lh, Ll holds Lq and R A^T, then P
-    // beta, row maxima and sums, the gates' prefix sums as float pairs: 64 floats each; 16 pages
+    // fp32 64 x 72 (E, the logits) lies in [Th, Tl]; the pair Lh, Ll holds Lq and R A^T, then P
+    // beta, row maxima and sums: 64 floats each; the gates' prefix sums as float pairs; 16 pages
     static constexpr size_t vec = Tl + sml, bytes = vec + 5 * kC * 4 + 16 * 4;
 };
 
@@ -62,12 +62,12 @@ __device__ __forceinline__ void put2(bf *t, int ld, int r, int c, uint32_t v) {
     *reinterpret_cast<uint32_t *>(t + r * ld + c) = v;
 }
 
-// (I + E)^{-1} in fp32 for a strictly lower triangular E (shared, stride 68): the four 16 x 16
+// (I + E)^{-1} in fp32 for a strictly lower triangular E (shared, stride 72): the four 16 x 16
 // diagonal blocks by substitution (one column per thread), then X21 = -X22 E21 X11 for the 16-
 // and the 32-blocks; every factor is bounded (products of contractions), so nothing grows.
 // `Y`: 32 x 36 floats of scratch; nt: the 16-row tiles in use (the others are the identity).
 __device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid, int nt) {
-    constexpr int LD = 68, YL = 36;
+    constexpr int LD = 72, YL = 36;
     const int b0 = (tid >> 4) << 4, lu = tid & 15;
     float x[16];
     if (tid < kC) {
@@ -264,9 +264,9 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
        *const Ll = reinterpret_cast<bf *>(smem + S::Ll), *const Th = reinterpret_cast<bf *>(smem + S::Th),
        *const Tl = reinterpret_cast<bf *>(smem + S::Tl);
     float *const F = reinterpret_cast<float *>(smem + S::F);
-    float *const beta = reinterpret_cast<float *>(smem + S::vec), *const rm = beta + kC, *const rl = rm + kC,
-                 *const cumh = rl + kC, *const cuml = cumh + kC;
-    int *const kpage = reinterpret_cast<int *>(cuml + kC), *const vpage = kpage + 8;
+    float *const beta = reinterpret_cast<float *>(smem + S::vec), *const rm = beta + kC, *const rl = rm + kC;
+    float2 *const cum = reinterpret_cast<float2 *>(rl + kC);
+    int *const kpage = reinterpret_cast<int *>(cum + kC), *const vpage = kpage + 8;
     const int slot = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.c.G;
     int b, c;
@@ -322,8 +322,8 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             warp_mma<4, false, false>(r, K, LDD, m0, W, LDD, n0, D / 16);
         }
         each_pair(e, m0, n0, [&](int i, int j, float x, float z) {
-            F[i * LDF + j] = j < i ? beta[i] * x : 0.f;
-            F[i * LDF + j + 1] = j + 1 < i ? beta[i] * z : 0.f;
+            *reinterpret_cast<float2 *>(F + i * LDF + j) =
+                make_float2(j < i ? beta[i] * x : 0.f, j + 1 < i ? beta[i] * z : 0.f);
         });
         each_pair(r, m0, n0, [&](int i, int j, float x, float z) {
             uint32_t hi, lo;
@@ -349,8 +349,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
         float u[4][4];
         zero_acc(u);
         if ((warp & 3) < nt) {
-            warp_mma<4, false, true>(u, Ah, LDS, m0, W, LDD, 64 * x + n0, nt);
-            warp_mma<4, false, true>(u, Al, LDS, m0, W, LDD, 64 * x + n0, nt);
+            warp_mma_a2<4, false, true>(u, Ah, Al, LDS, m0, W, LDD, 64 * x + n0, nt);
         }
         each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
             uint32_t hi, lo;
@@ -363,9 +362,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
         float r[4][4];
         zero_acc(r);
         if (live) {
-            warp_mma<4, false, false>(r, Rh, LDS, m0, Ah, LDS, n0, nt);
-            warp_mma<4, false, false>(r, Rl, LDS, m0, Ah, LDS, n0, nt);
-            warp_mma<4, false, false>(r, Rh, LDS, m0, Al, LDS, n0, nt);
+            warp_mma_3<4, false>(r, Rh, Rl, LDS, m0, Ah, Al, LDS, n0, nt);
         }
         each_pair(r, m0, n0, [&](int i, int j, float p, float q) {
             uint32_t hi, lo;
@@ -384,8 +381,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             const int r0 = 16 * (t % (D / 16)), c0 = 32 * (t / (D / 16));
             float u[4][4];
             zero_acc(u);
-            warp_mma<4, true, true>(u, Uh, LDD, r0, W, LDD, c0, nt);
-            warp_mma<4, true, true>(u, Ul, LDD, r0, W, LDD, c0, nt);
+            warp_mma_a2<4, true, true>(u, Uh, Ul, LDD, r0, W, LDD, c0, nt);
             each_pair(u, r0, c0, [&](int i, int j, float p, float q) {
                 uint32_t hi, lo;
                 split2(-p, -q, hi, lo);
@@ -400,8 +396,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
         if (!lead || (single && (warp & 3) >= nt)) break;
         float u[4][4];
         zero_acc(u);
-        warp_mma<4, false, true>(u, Lh, LDS, m0, W, LDD, 64 * x + n0, nt);
-        warp_mma<4, false, true>(u, Ll, LDS, m0, W, LDD, 64 * x + n0, nt);
+        warp_mma_a2<4, false, true>(u, Lh, Ll, LDS, m0, W, LDD, 64 * x + n0, nt);
         each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
             const float2 k2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(K + i * LDD + j));
             p = k2.x - p;
@@ -459,8 +454,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             for (int half = 0; half < 2; ++half) {
                 const int t = 32 * half + lane;
                 const float hi = (float)x[half], behind = (float)(all - x[half]);
-                cumh[t] = hi;
-                cuml[t] = (float)(x[half] - (double)hi);
+                cum[t] = make_float2(hi, (float)(x[half] - (double)hi));
                 y.gt[bq * kC + t] = behind;
                 if (t < rows) {
                     y.gq[row_of(t)] = hi;
@@ -486,9 +480,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             float u[4][4];
             zero_acc(u);
             if (live) {
-                warp_mma<4, false, true>(u, Lh, LDS, m0, Ah, LDS, n0, nt);
-                warp_mma<4, false, true>(u, Ll, LDS, m0, Ah, LDS, n0, nt);
-                warp_mma<4, false, true>(u, Lh, LDS, m0, Al, LDS, n0, nt);
+                warp_mma_3<4, true>(u, Lh, Ll, LDS, m0, Ah, Al, LDS, n0, nt);
             }
             each_pair(u, m0, n0, [&](int i, int j, float p, float q) {
                 uint32_t hi, lo;
@@ -504,8 +496,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             if ((warp & 3) >= nt) break;
             float u[4][4];
             zero_acc(u);
-            warp_mma<4, false, true>(u, Th, LDS, m0, W, LDD, 64 * x + n0, nt);
-            warp_mma<4, false, true>(u, Tl, LDS, m0, W, LDD, 64 * x + n0, nt);
+            warp_mma_a2<4, false, true>(u, Th, Tl, LDS, m0, W, LDD, 64 * x + n0, nt);
             each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
                 if (i >= rows) return;
                 const float2 q2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(Q + i * LDD + j));
@@ -520,9 +511,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             zero_acc(z);
             if (live) {
                 warp_mma<4, false, false>(u, Q, LDD, m0, K, LDD, n0, D / 16);
-                warp_mma<4, false, false>(z, Th, LDS, m0, Rh, LDS, n0, nt);
-                warp_mma<4, false, false>(z, Tl, LDS, m0, Rh, LDS, n0, nt);
-                warp_mma<4, false, false>(z, Th, LDS, m0, Rl, LDS, n0, nt);
+                warp_mma_3<4, false>(z, Th, Tl, LDS, m0, Rh, Rl, LDS, n0, nt);
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -531,11 +520,13 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             __syncthreads();  // Lq A has been read; the logits take its place
             each_pair(u, m0, n0, [&](int i, int j, float p, float q) {
                 if (a.log_f != nullptr) {
-                    if (j < i) p = fmaf((cumh[i] - cumh[j]) + (cuml[i] - cuml[j]), kLog2e, p);
-                    if (j + 1 < i) q = fmaf((cumh[i] - cumh[j + 1]) + (cuml[i] - cuml[j + 1]), kLog2e, q);
+                    const float2 ci = cum[i];
+                    const float4 cj = *reinterpret_cast<const float4 *>(cum + j);
+                    if (j < i) p = fmaf((ci.x - cj.x) + (ci.y - cj.y), kLog2e, p);
+                    if (j + 1 < i) q = fmaf((ci.x - cj.z) + (ci.y - cj.w), kLog2e, q);
                 }
-                F[i * LDF + j] = j <= i ? p : -INFINITY;
-                F[i * LDF + j + 1] = j + 1 <= i ? q : -INFINITY;
+                *reinterpret_cast<float2 *>(F + i * LDF + j) =
+                    make_float2(j <= i ? p : -INFINITY, j + 1 <= i ? q : -INFINITY);
             });
         }
         __syncthreads();
@@ -682,9 +673,7 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
         });
         cp_wait_all();
         __syncthreads();
-        warp_mma<NT, false, true>(acc, Yh, LDD, m0, Mh, LDD, 0, D / 16);
-        warp_mma<NT, false, true>(acc, Yl, LDD, m0, Mh, LDD, 0, D / 16);
-        warp_mma<NT, false, true>(acc, Yh, LDD, m0, Ml, LDD, 0, D / 16);
+        warp_mma_3<NT, true>(acc, Yh, Yl, LDD, m0, Mh, Ml, LDD, 0, D / 16);
     }
     const bool done = PASS == 2 || ng == 1;
     if (ident) {
@@ -846,20 +835,31 @@ __global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, con
     }
 }
 
-// PaTH-FoX: every cached key's gate sums advance by the chunk's. grid (parts, Hq, seqs).
+// PaTH-FoX: every cached key's gate sums advance by the chunk's, four positions a thread (the
+// pool's rows of 16 or more positions are 16-byte aligned). grid (parts, Hq, seqs).
 __global__ void __launch_bounds__(kThr) tc_gates_kernel(const Step a, const TcWs y) {
     const int hq = blockIdx.y, b = blockIdx.z;
     grid_wait();
     const Seq s = seq_of(a, b);
-    if (s.T == 0 || (int)blockIdx.x * kThr >= s.n) return;
+    if (s.T == 0 || (int)blockIdx.x * kThr * 4 >= s.n) return;
     const int nb = (s.T + kC - 1) / kC;
-    double t = 0.0;
-    for (int kb = 0; kb < nb; ++kb) t += y.gtot[(size_t)slot_of(s, b, kb) * a.c.Hq + hq];
-    for (int j = blockIdx.x * kThr + threadIdx.x; j < s.n; j += gridDim.x * kThr) {
+    double sum = 0.0;
+    for (int kb = 0; kb < nb; ++kb) sum += y.gtot[(size_t)slot_of(s, b, kb) * a.c.Hq + hq];
+    const float t = (float)sum;
+    for (int j = (blockIdx.x * kThr + threadIdx.x) * 4; j < s.n; j += gridDim.x * kThr * 4) {
         const int id = page_of(a, a.c.k_table, b, j >> a.c.page_shift, a.c.nk);
         if (id < 0) continue;
         float *g = a.c.g_pages + (((size_t)id * a.c.Hq + hq) << a.c.page_shift) + (j & (a.c.page - 1));
-        *g = (float)((double)*g + t);
+        if (j + 4 <= s.n) {
+            float4 v = *reinterpret_cast<const float4 *>(g);
+            v.x += t;
+            v.y += t;
+            v.z += t;
+            v.w += t;
+            *reinterpret_cast<float4 *>(g) = v;
+        } else {
+            for (int i = 0; j + i < s.n; ++i) g[i] += t;
+        }
     }
 }
 
@@ -931,9 +931,14 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
             float v[8][E], w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int q = min(i0 + i, n - 1);
-                w[i] = __shfl_sync(0xffffffffu, f, q);
-                if (i0 + i >= n) w[i] = 0.f;
+                const int q = i0 + i;
+                w[i] = __shfl_sync(0xffffffffu, f, q & 31);
+                if (q >= n) {  // the same for the warp
+                    w[i] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+                    continue;
+                }
                 const float *o = so + part_at(p0 + q) * D + lane * E;
                 if (E == 2) {
                     const float2 t = *reinterpret_cast<const float2 *>(o);

@@ -169,6 +169,62 @@ __device__ __forceinline__ void warp_mma(float (&acc)[NT][4], const __nv_bfloat1
     }
 }
 
+// As warp_mma with split operands, fragments shared between the products: A = Ah + Al with B as
+// it is, or with B = Bh + Bl (low x low left out).
+template <int NT, bool AT, bool BN>
+__device__ __forceinline__ void warp_mma_a2(float (&acc)[NT][4], const __nv_bfloat16 *Ah, const __nv_bfloat16 *Al,
+                                            int lda, int m0, const __nv_bfloat16 *B, int ldb, int n0, int ksteps) {
+#pragma unroll 2
+    for (int k = 0; k < ksteps; ++k) {
+        uint32_t a[4], c[4];
+        if (AT) {
+            frag_at(a, Ah, lda, m0, 16 * k);
+            frag_at(c, Al, lda, m0, 16 * k);
+        } else {
+            frag_a(a, Ah, lda, m0, 16 * k);
+            frag_a(c, Al, lda, m0, 16 * k);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+            uint32_t b[4];
+            if (BN) frag_b(b, B, ldb, n0 + 8 * n, 16 * k);
+            else frag_bt(b, B, ldb, n0 + 8 * n, 16 * k);
+            mma_bf16(acc[n], a, b[0], b[1]);
+            mma_bf16(acc[n + 1], a, b[2], b[3]);
+            mma_bf16(acc[n], c, b[0], b[1]);
+            mma_bf16(acc[n + 1], c, b[2], b[3]);
+        }
+    }
+}
+template <int NT, bool BN>
+__device__ __forceinline__ void warp_mma_3(float (&acc)[NT][4], const __nv_bfloat16 *Ah, const __nv_bfloat16 *Al,
+                                           int lda, int m0, const __nv_bfloat16 *Bh, const __nv_bfloat16 *Bl,
+                                           int ldb, int n0, int ksteps) {
+#pragma unroll 1
+    for (int k = 0; k < ksteps; ++k) {
+        uint32_t a[4], c[4];
+        frag_a(a, Ah, lda, m0, 16 * k);
+        frag_a(c, Al, lda, m0, 16 * k);
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+            uint32_t b[4], l[4];
+            if (BN) {
+                frag_b(b, Bh, ldb, n0 + 8 * n, 16 * k);
+                frag_b(l, Bl, ldb, n0 + 8 * n, 16 * k);
+            } else {
+                frag_bt(b, Bh, ldb, n0 + 8 * n, 16 * k);
+                frag_bt(l, Bl, ldb, n0 + 8 * n, 16 * k);
+            }
+            mma_bf16(acc[n], a, b[0], b[1]);
+            mma_bf16(acc[n + 1], a, b[2], b[3]);
+            mma_bf16(acc[n], c, b[0], b[1]);
+            mma_bf16(acc[n + 1], c, b[2], b[3]);
+            mma_bf16(acc[n], a, l[0], l[1]);
+            mma_bf16(acc[n + 1], a, l[2], l[3]);
+        }
+    }
+}
+
 template <int NT>
 __device__ __forceinline__ void zero_acc(float (&acc)[NT][4]) {
 #pragma unroll
