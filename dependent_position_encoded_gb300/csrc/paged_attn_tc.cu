@@ -143,7 +143,8 @@ struct CachedCfg {
     static constexpr int NK = NT == 1 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 2);
     static constexpr int NV = NT == 1 ? 2 : (D == 64 ? 4 : 3);
     static constexpr uint32_t K = M + mbytes, V = K + NK * tile, bars = V + NV * tile;
-    static constexpr int KF = 0, KE = NK, VF = 2 * NK, VE = VF + NV, XF = VE + NV, XE = XF + 1, SF = XE + 1, PR = SF + 2, FIN = PR + 2,
+    static constexpr int KF = 0, KE = NK, VF = 2 * NK, VE = VF + NV, XF = VE + NV, XE = XF + 1, SF = XE + 1, PR = SF + 2,
+                         FIN = PR + 4,  // PR: weights of columns 0-63 and 64-127, per row tile
                          DF = FIN + 2, DE = DF + 1, TMP = DE + 1, END = TMP + 2, count = END + 1;
     static constexpr uint32_t bytes = bars + count * 8 + 16;  // from a 1024-byte boundary
     static constexpr int threads = 384;
@@ -326,12 +327,13 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                               sdesc_sw128(kb + (kk >> 2) * L::atom, 16, 1024) + 2 * (kk & 3), ID_S, kk > 0);
                 umma_commit(bar(L::SF + t));
             };
-            auto issue_pv = [&](int t, uint32_t js, bool first) {
-                const uint64_t v = sdesc_sw128(value_slot(js), L::atom, 1024);
+            // half 0 or 1 of the key tile: the second half's weights are still formed while the first's
+            // product runs
+            auto issue_pv = [&](int t, uint32_t js, bool first, int half) {
+                const uint64_t v = sdesc_sw128(value_slot(js), L::atom, 1024) + 512 * half;
+                const uint32_t o = tmem + L::per_tile * t + L::cO, w = tmem + L::per_tile * t + L::cS + 32 * half;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    umma_tA(tmem + L::per_tile * t + L::cO, tmem + L::per_tile * t + L::cS + 8 * kk, v + 128 * kk,
-                            ID_O, !first || kk > 0);
+                for (int kk = 0; kk < 4; ++kk) umma_tA(o, w + 8 * kk, v + 128 * kk, ID_O, !first || half > 0 || kk > 0);
             };
             auto keys_ready = [&](uint32_t js) { return wait(bar(L::KF + js % NK), (js / NK) & 1); };
             auto issue_update = [&](uint32_t js) {  // K (P - I): the keys are the A operand
@@ -370,9 +372,13 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 for (int i = 0; ok && i < t.steps; ++i, ++j) {
                     if (!(ok = wait(bar(L::VF + j % NV), (j / NV) & 1))) break;
                     for (int q = 0; q < (two ? 2 : 1); ++q) {
-                        if (!(ok = wait(bar(L::PR + q), (q ? j1 : j) & 1))) break;
+                        const uint32_t parity = (q ? j1 : j) & 1;
+                        if (!(ok = wait(bar(L::PR + 2 * q), parity))) break;
                         tc_fence_after();
-                        issue_pv(q, j, i == 0);
+                        issue_pv(q, j, i == 0, 0);
+                        if (!(ok = wait(bar(L::PR + 2 * q + 1), parity))) break;
+                        tc_fence_after();
+                        issue_pv(q, j, i == 0, 1);
                         if (q == (two ? 1 : 0)) umma_commit(bar(L::VE + j % NV));
                         if (i + 1 < t.steps) {
                             if (q == 0 && !(ok = keys_ready(j + 1))) break;
@@ -640,13 +646,19 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                             weigh(x + c, p);
                             weigh(x + c + 32, p + 16);
                             tmem_st32(tm + L::cS + c / 2, p);
+                            if (c == 0) {
+                                tmem_st_wait();
+                                tc_fence_before();
+                                mbar_arrive_warp(bar(L::PR + 2 * w));
+                            }
                         }
                     }
                     l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_st_wait();
                 }
                 tc_fence_before();
-                mbar_arrive_warp(bar(L::PR + w));
+                if (kTwice || !warp_live) mbar_arrive_warp(bar(L::PR + 2 * w));
+                mbar_arrive_warp(bar(L::PR + 2 * w + 1));
             }
             if (!ok || !(ok = wait.warp(bar(L::FIN + w), seg & 1))) break;
             ++seg;

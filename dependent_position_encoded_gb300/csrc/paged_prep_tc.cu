@@ -864,103 +864,119 @@ __global__ void __launch_bounds__(kThr) tc_gates_kernel(const Step a, const TcWs
 }
 
 // ---------------------------------------------------------------- combine
-// One warp per row (of a key head): joins the part of the step's own tokens and those of the
-// cached keys. Lane p holds the maximum and sum of part p (further parts in turns of 31).
+// A warp joins `rows` consecutive rows of a key head, each the part of the step's own tokens and
+// those of the cached keys. Lane p holds the maximum and sum of part p (32 at a time). What the
+// rows of a tile share (their sequence and the numbers of their parts) is looked up once.
 template <int D>
-__global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const TcWs y) {
+__global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const TcWs y, int rows) {
     constexpr int E = D / 32;
     const int G = a.c.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
-    const long long r = (long long)blockIdx.x * (kThr / 32) + warp;
+    const long long r0 = ((long long)blockIdx.x * (kThr / 32) + warp) * rows;
+    const long long r1 = r0 + rows < y.R ? r0 + rows : y.R;
     grid_wait();
-    if (r >= y.R) return;
-    const int tok = (int)(r / G), hq = h * G + (int)(r - (long long)tok * G);
-    int lo = 0, hi = a.c.seqs - 1;  // the last sequence that begins at or before the token
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(a.cu + mid) <= tok) lo = mid;
-        else hi = mid - 1;
-    }
-    const Seq s = seq_of(a, lo);
-    if (tok < s.first || tok >= s.first + s.T) return;
-    const size_t row = (size_t)h * y.R + r;
-    const int own = (int)(r - (long long)s.first * G);  // the row within its sequence
-    int NT = 1, tiles, kt;
-    plan_of(s, G, 1, tiles, kt);
-    if (tiles == 0) {
-        NT = 2;
-        plan_of(s, G, 2, tiles, kt);
-    }
-    const Plan &p = NT == 1 ? y.plan[0] : y.plan[1];
-    const int it = h * tiles + own / (128 * NT);
-    long long first = 0, number = 0;  // the first part's number and how many there are
-    if (kt > 0) {
-        const long long per = plan_per(p, a.c.seqs), u = p.units[lo] + (long long)it * kt;
-        first = u / per + p.items[lo] + it;
-        number = (u + kt - 1) / per - u / per + 1;
-    }
-    const float *so = NT == 1 ? y.so[0] : y.so[1];
-    const float2 *sml = NT == 1 ? y.sml[0] : y.sml[1];
-    // short sequences' tiles hold copies of their rows, each a part of its own
-    const int rows_all = s.T * G, cp = NT == 2 ? 0 : rows_all <= 32 ? 2 : rows_all <= 64 ? 1 : 0;
-    const int at = own % (128 * NT), tile = 128 * NT, cp_rows = 128 >> cp;
-    number <<= cp;
-    auto part_at = [&](long long p) { return (first + (p >> cp)) * tile + (p & ((1 << cp) - 1)) * cp_rows + at; };
-    const float2 z = y.pml[row];
-    float M = z.x, L = z.y, O[E];
-    {
-        const float *o = y.po + row * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) O[e] = o[e];
-    }
-    for (long long p0 = 0; p0 < number; p0 += 32) {
-        const int n = number - p0 < 32 ? (int)(number - p0) : 32;
-        const float2 ml = lane < n ? sml[part_at(p0 + lane)] : make_float2(-INFINITY, 0.f);
-        float m = ml.x;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float nm = fmaxf(M, m), f0 = exp2f(M - nm), f = exp2f(ml.x - nm);  // M is never -inf
-        float l = ml.x == -INFINITY ? 0.f : ml.y * f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        M = nm;
-        L = fmaf(L, f0, l);
-#pragma unroll
-        for (int e = 0; e < E; ++e) O[e] *= f0;
-        // eight parts' rows in flight at a time (an absent part's weight is 0 and its row 0)
-        for (int i0 = 0; i0 < n; i0 += 8) {
-            float v[8][E], w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int q = i0 + i;
-                w[i] = __shfl_sync(0xffffffffu, f, q & 31);
-                if (q >= n) {  // the same for the warp
-                    w[i] = 0.f;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) v[i][e] = 0.f;
-                    continue;
-                }
-                const float *o = so + part_at(p0 + q) * D + lane * E;
-                if (E == 2) {
-                    const float2 t = *reinterpret_cast<const float2 *>(o);
-                    v[i][0] = t.x;
-                    v[i][1] = t.y;
-                } else {
-                    const float4 t = *reinterpret_cast<const float4 *>(o);
-                    v[i][0] = t.x;
-                    v[i][1] = t.y;
-                    v[i][E - 2] = t.z;
-                    v[i][E - 1] = t.w;
-                }
+    long long known = -1;  // rows below it are of the tile looked up last
+    Seq s{0, 0, 0};
+    long long first = 0, number = 0;
+    int NT = 1, cp = 0;
+    for (long long r = r0; r < r1; ++r) {
+        const int tok = (int)(r / G), hq = h * G + (int)(r - (long long)tok * G);
+        if (r >= known) {
+            int lo = 0, hi = a.c.seqs - 1;  // the last sequence that begins at or before the token
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (__ldg(a.cu + mid) <= tok) lo = mid;
+                else hi = mid - 1;
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int e = 0; e < E; ++e) O[e] = fmaf(v[i][e], w[i], O[e]);
+            s = seq_of(a, lo);
+            if (tok < s.first || tok >= s.first + s.T) continue;
+            const int rows_all = s.T * G, own = (int)(r - (long long)s.first * G);
+            int tiles, kt;
+            NT = 1;
+            plan_of(s, G, 1, tiles, kt);
+            if (tiles == 0) {
+                NT = 2;
+                plan_of(s, G, 2, tiles, kt);
+            }
+            const Plan &p = NT == 1 ? y.plan[0] : y.plan[1];
+            const int tile = own / (128 * NT), it = h * tiles + tile;
+            // the first part's number and how many there are
+            first = number = 0;
+            if (kt > 0) {
+                const long long per = plan_per(p, a.c.seqs), u = p.units[lo] + (long long)it * kt, c0 = u / per;
+                first = c0 + p.items[lo] + it;
+                number = (u + kt - 1) / per - c0 + 1;
+            }
+            // short sequences' tiles hold copies of their rows, each a part of its own
+            cp = NT == 2 ? 0 : rows_all <= 32 ? 2 : rows_all <= 64 ? 1 : 0;
+            number <<= cp;
+            const int end = min(rows_all, (tile + 1) * 128 * NT);
+            known = (long long)s.first * G + end;
         }
-    }
-    bf *dst = static_cast<bf *>(a.out) + (long long)tok * a.so.tok + hq * a.so.head + lane * E;
+        const float *so = NT == 1 ? y.so[0] : y.so[1];
+        const float2 *sml = NT == 1 ? y.sml[0] : y.sml[1];
+        const int at = (int)(r - (long long)s.first * G) % (128 * NT), cp_rows = 128 >> cp;
+        auto part_at = [&](long long p) {
+            return (first + (p >> cp)) * (128 * NT) + (p & ((1 << cp) - 1)) * cp_rows + at;
+        };
+        const size_t row = (size_t)h * y.R + r;
+        const float2 z = y.pml[row];
+        float M = z.x, L = z.y, O[E];
+        {
+            const float *o = y.po + row * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16x2(O[e] / L, O[e + 1] / L);
+            for (int e = 0; e < E; ++e) O[e] = o[e];
+        }
+        for (long long p0 = 0; p0 < number; p0 += 32) {
+            const int n = number - p0 < 32 ? (int)(number - p0) : 32;
+            const float2 ml = lane < n ? sml[part_at(p0 + lane)] : make_float2(-INFINITY, 0.f);
+            float m = ml.x;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float nm = fmaxf(M, m), f0 = exp2f(M - nm), f = exp2f(ml.x - nm);  // M is never -inf
+            float l = ml.x == -INFINITY ? 0.f : ml.y * f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            M = nm;
+            L = fmaf(L, f0, l);
+#pragma unroll
+            for (int e = 0; e < E; ++e) O[e] *= f0;
+            // eight parts' rows in flight at a time (an absent part's weight is 0 and its row 0)
+            for (int i0 = 0; i0 < n; i0 += 8) {
+                float v[8][E], w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int q = i0 + i;
+                    w[i] = __shfl_sync(0xffffffffu, f, q & 31);
+                    if (q >= n) {  // the same for the warp
+                        w[i] = 0.f;
+#pragma unroll
+                        for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+                        continue;
+                    }
+                    const float *o = so + part_at(p0 + q) * D + lane * E;
+                    if (E == 2) {
+                        const float2 t = *reinterpret_cast<const float2 *>(o);
+                        v[i][0] = t.x;
+                        v[i][1] = t.y;
+                    } else {
+                        const float4 t = *reinterpret_cast<const float4 *>(o);
+                        v[i][0] = t.x;
+                        v[i][1] = t.y;
+                        v[i][E - 2] = t.z;
+                        v[i][E - 1] = t.w;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) O[e] = fmaf(v[i][e], w[i], O[e]);
+            }
+        }
+        bf *dst = static_cast<bf *>(a.out) + (long long)tok * a.so.tok + hq * a.so.head + lane * E;
+        const float inv = 1.f / L;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16x2(O[e] * inv, O[e + 1] * inv);
+    }
 }
 
 template <typename K>
@@ -1003,8 +1019,11 @@ cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_tc_finish(const Step &a, const TcWs &y, int tile_rows, cudaStream_t stream) {
     const long long cap = (long long)a.c.max_pages << a.c.page_shift;
-    cudaError_t e = launch(tc_combine_kernel<D>, dim3((unsigned)((y.R + kThr / 32 - 1) / (kThr / 32)), a.c.Hkv), kThr, 0,
-                           stream, false, a, y);
+    // rows per warp: one while that leaves warps idle, at most eight
+    const long long fill = y.R * a.c.Hkv / (152 * 32);
+    const int rows = fill < 1 ? 1 : fill > 8 ? 8 : (int)fill, per = kThr / 32 * rows;
+    cudaError_t e = launch(tc_combine_kernel<D>, dim3((unsigned)((y.R + per - 1) / per), a.c.Hkv), kThr, 0, stream, false,
+                           a, y, rows);
     if (e != cudaSuccess || cap == 0) return e;  // no sequence has room for a token
     if ((long long)a.max_chunk * a.c.G > tile_rows) {
         const size_t bytes = TransformSmem<D>::bytes;
