@@ -130,8 +130,10 @@ constexpr float kRescale = 8.f;  // the running maximum may lag by 2^8 before O 
 // warps share the row's softmax, and the copies' sums are parts to join like any others.
 //
 // Warps: 0-3 softmax of tile 0; 4-7 softmax of tile 1 (NT = 2) or the keys' update (NT = 1); 8
-// allocates TMEM and issues the MMAs; 9 and 10 stream the key and the value pages. (Warp 11 has
-// no role: the last warpgroup gives registers to the softmax.)
+// allocates TMEM and issues the MMAs of S and P V; 11 those of the update (NT = 1); 9 and 10
+// stream the key and the value pages. One thread issues both row tiles' MMAs: two of them, whose
+// products mix on the tensor core, were a sixth slower (n = 32768, T = 2048, D = 128: 1,420 us a
+// step against 1,200), and so were weights handed over in two halves (1,243).
 // Positions past the sequence's n and those on bad pages: the streaming warp zeroes their rows
 // after the copy, and the softmax masks them.
 template <int NT, int D>
@@ -143,16 +145,15 @@ struct CachedCfg {
     static constexpr int NK = NT == 1 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 2);
     static constexpr int NV = NT == 1 ? 2 : (D == 64 ? 4 : 3);
     static constexpr uint32_t K = M + mbytes, V = K + NK * tile, bars = V + NV * tile;
-    static constexpr int KF = 0, KE = NK, VF = 2 * NK, VE = VF + NV, XF = VE + NV, XE = XF + 1, SF = XE + 1, PR = SF + 2,
-                         FIN = PR + 4,  // PR: weights of columns 0-63 and 64-127, per row tile
-                         DF = FIN + 2, DE = DF + 1, TMP = DE + 1, END = TMP + 2, count = END + 1;
+    static constexpr int KF = 0, KE = NK, VF = 2 * NK, VE = VF + NV, XF = VE + NV, XE = XF + 1, SF = XE + 1, PR = SF + 2, FIN = PR + 2,
+                         DF = FIN + 2, DE = DF + NK, TMP = DE + 1, END = TMP + 2, count = END + 2;
     static constexpr uint32_t bytes = bars + count * 8 + 16;  // from a 1024-byte boundary
     static constexpr int threads = 384;
     static constexpr int ctas_per_sm = NT == 1 && D == 64 ? 2 : 1;
     // registers after the split of what the CTA is launched with (NT = 2: 168 for each thread; NT = 1
     // with two CTAs per SM: 80): the softmax's warpgroups, the update's and the last one
     static constexpr bool split = NT == 2 || D == 64;
-    static constexpr int reg_row = NT == 2 ? 208 : 104, reg_update = 72, reg_other = NT == 2 ? 80 : 64;
+    static constexpr int reg_row = NT == 2 ? 200 : 104, reg_update = 72, reg_other = NT == 2 ? 104 : 64;
     // TMEM columns: per row tile S 128 (the weights over it) and O; NT = 1: the update's product
     static constexpr uint32_t cS = 0, cO = 128, per_tile = 256, cD = 128 + D;
     static constexpr uint32_t cols = NT == 1 && D == 64 ? 256 : 512;
@@ -172,6 +173,18 @@ template <int N>
 __device__ __forceinline__ void reg_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
+
+// A ring's running slot and the parity of its use.
+template <int N>
+struct Ring {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 // Whether all boxes of a key tile lie on good pages below n: `have` one bit per box of
 // 1 << box_shift rows.
@@ -206,7 +219,13 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
 
     if (tid == 0) {
         *abort_f = 0u;
-        for (int i = 0; i < L::count; ++i) mbar_init(bar(i), (i >= L::PR && i < L::FIN) || i == L::DE ? 4u : 1u);
+        // four warps: weights written, update's product read; both issuing threads (NT = 1): rows' tile
+        // free, keys read by their products
+        for (int i = 0; i < L::count; ++i) {
+            const bool four = (i >= L::PR && i < L::FIN) || i == L::DE;
+            const bool both = NT == 1 && (i == L::XE || (i >= L::DF && i < L::DE));
+            mbar_init(bar(i), four ? 4u : both ? 2u : 1u);
+        }
         fence_mbar_init();
     }
     if (warp == 8) {
@@ -313,82 +332,66 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                     mbar_wait(bar(full0 + v % ring), (v / ring) & 1, limit_ns);
                 if (keys) mbar_wait(bar(L::XF), seg & 1, limit_ns);
             }
-        } else if (warp == 8 && lane == 0) {
-            // ======================================================== MMA issue
+        } else if (lane == 0 && warp == 8) {
+            // ======================================================== S and P V
+            // A lone thread's instructions follow each other slowly, and two tiles' MMAs keep the
+            // tensor core busy only if little stands between them: slots and phases run along,
+            // descriptors are sums.
             constexpr uint32_t ID_S = idesc_b16(128, 128, false), ID_O = idesc_b16(128, D, true);
-            uint32_t j = 0, j1 = 0, seg = 0;  // steps of the first and of the second row tile
+            constexpr uint64_t kAtom = L::atom >> 4, kTile = L::tile >> 4;
+            const uint64_t x_desc = sdesc_sw128(base + L::X, 16, 1024), k_desc = sdesc_sw128(base + L::K, 16, 1024),
+                           v_desc = sdesc_sw128(base + L::V, L::atom, 1024);
+            Ring<NK> k;
+            Ring<NV> v;
+            uint32_t seg = 0, parity[2] = {0, 0};
             bool ok = true;
-            auto issue_s = [&](int t, uint32_t js) {
-                const uint32_t kb = key_slot(js);
+            auto issue_s = [&](int q) {
+                const uint64_t xd = x_desc + q * kTile, kd = k_desc + k.slot * kTile;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16(tmem + L::per_tile * t + L::cS,
-                              sdesc_sw128(base + L::X + t * L::tile + (kk >> 2) * L::atom, 16, 1024) + 2 * (kk & 3),
-                              sdesc_sw128(kb + (kk >> 2) * L::atom, 16, 1024) + 2 * (kk & 3), ID_S, kk > 0);
-                umma_commit(bar(L::SF + t));
+                    umma_bf16(tmem + L::per_tile * q + L::cS, xd + (kk >> 2) * kAtom + 2 * (kk & 3),
+                              kd + (kk >> 2) * kAtom + 2 * (kk & 3), ID_S, kk > 0);
+                umma_commit(bar(L::SF + q));
             };
-            // half 0 or 1 of the key tile: the second half's weights are still formed while the first's
-            // product runs
-            auto issue_pv = [&](int t, uint32_t js, bool first, int half) {
-                const uint64_t v = sdesc_sw128(value_slot(js), L::atom, 1024) + 512 * half;
-                const uint32_t o = tmem + L::per_tile * t + L::cO, w = tmem + L::per_tile * t + L::cS + 32 * half;
+            auto issue_pv = [&](int q, bool first) {
+                const uint64_t vd = v_desc + v.slot * kTile;
+                const uint32_t tm = tmem + L::per_tile * q;
+                umma_tA(tm + L::cO, tm + L::cS, vd, ID_O, !first);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) umma_tA(o, w + 8 * kk, v + 128 * kk, ID_O, !first || half > 0 || kk > 0);
+                for (int kk = 1; kk < 8; ++kk) umma_tA(tm + L::cO, tm + L::cS + 8 * kk, vd + 128 * kk, ID_O, 1);
             };
-            auto keys_ready = [&](uint32_t js) { return wait(bar(L::KF + js % NK), (js / NK) & 1); };
-            auto issue_update = [&](uint32_t js) {  // K (P - I): the keys are the A operand
-                if (js > 0 && !wait(bar(L::DE), (js - 1) & 1)) return false;
-                tc_fence_after();
-                const uint32_t kb = key_slot(js);
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const uint64_t m = sdesc_sw128(base + L::M + p * NA * D * 128, D * 128, 1024);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        umma_bf16(tmem + L::cD, sdesc_sw128(kb + (kk >> 2) * L::atom, 16, 1024) + 2 * (kk & 3),
-                                  m + 128 * kk, ID_O, p > 0 || kk > 0);
-                }
-                umma_commit(bar(L::DF));
-                return true;
-            };
-            // the keys' products of step js (the caller has seen the keys arrive); last of a stretch:
-            // the rows' tile is free behind them
-            auto after_s = [&](uint32_t js, bool last) {
-                bool fine = true;
-                if (NT == 1) fine = issue_update(js);
-                else umma_commit(bar(L::KE + js % NK));
+            // the keys of the ring's slot have been multiplied; last of a stretch: the rows' tile is free
+            auto after_s = [&](bool last) {
+                umma_commit(bar((NT == 2 ? L::KE : L::DF) + k.slot));
                 if (last) umma_commit(bar(L::XE));
-                return fine;
+                k.next();
             };
             for (long long at = u_begin; ok && at < u_end; ++seg) {
                 const Stretch t = stretch_at(a, plan, NT, at, u_end);
                 at += t.steps;
                 const bool two = second(t);
-                if (!(ok = wait(bar(L::XF), seg & 1)) || !(ok = keys_ready(j))) break;
+                if (!(ok = wait(bar(L::XF), seg & 1)) || !(ok = wait(bar(L::KF + k.slot), k.phase))) break;
                 tc_fence_after();
-                issue_s(0, j);
-                if (two) issue_s(1, j);
-                ok = after_s(j, t.steps == 1);
-                for (int i = 0; ok && i < t.steps; ++i, ++j) {
-                    if (!(ok = wait(bar(L::VF + j % NV), (j / NV) & 1))) break;
-                    for (int q = 0; q < (two ? 2 : 1); ++q) {
-                        const uint32_t parity = (q ? j1 : j) & 1;
-                        if (!(ok = wait(bar(L::PR + 2 * q), parity))) break;
+                issue_s(0);
+                if (two) issue_s(1);
+                after_s(t.steps == 1);
+                for (int i = 0; i < t.steps; ++i) {
+                    const bool more = i + 1 < t.steps;
+                    if (!(ok = wait(bar(L::VF + v.slot), v.phase))) break;
+                    if (more && !(ok = wait(bar(L::KF + k.slot), k.phase))) break;
+#pragma unroll
+                    for (int q = 0; q < NT; ++q) {
+                        if (q == 1 && !two) break;
+                        if (!(ok = wait(bar(L::PR + q), parity[q]))) break;
                         tc_fence_after();
-                        issue_pv(q, j, i == 0, 0);
-                        if (!(ok = wait(bar(L::PR + 2 * q + 1), parity))) break;
-                        tc_fence_after();
-                        issue_pv(q, j, i == 0, 1);
-                        if (q == (two ? 1 : 0)) umma_commit(bar(L::VE + j % NV));
-                        if (i + 1 < t.steps) {
-                            if (q == 0 && !(ok = keys_ready(j + 1))) break;
-                            if (q == 0) tc_fence_after();
-                            issue_s(q, j + 1);
-                        }
+                        issue_pv(q, i == 0);
+                        if (more) issue_s(q);
+                        parity[q] ^= 1;
                     }
                     if (!ok) break;
-                    j1 += two;
-                    if (i + 1 < t.steps) ok = after_s(j + 1, i + 2 == t.steps);
+                    umma_commit(bar(L::VE + v.slot));
+                    v.next();
+                    if (more) after_s(i + 2 == t.steps);
                 }
                 // a barrier per row tile: the second has a phase only where it has rows, so neither
                 // can run ahead of the warps that wait for it
@@ -398,6 +401,36 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             // every product has completed before TMEM is freed
             umma_commit(bar(L::END));
             mbar_wait(bar(L::END), 0, limit_ns);
+        } else if (NT == 1 && lane == 0 && warp == 11) {
+            // ======================================================== K (P - I), NT = 1
+            constexpr uint32_t ID_D = idesc_b16(128, D, true);
+            constexpr uint64_t kAtom = L::atom >> 4, kTile = L::tile >> 4, kPart = (NA * D * 128) >> 4;
+            const uint64_t k_desc = sdesc_sw128(base + L::K, 16, 1024), m_desc = sdesc_sw128(base + L::M, D * 128, 1024);
+            Ring<NK> k;
+            uint32_t j = 0, seg = 0;
+            bool ok = true;
+            for (long long at = u_begin; ok && at < u_end; ++seg) {
+                const Stretch t = stretch_at(a, plan, NT, at, u_end);
+                at += t.steps;
+                if (!(ok = wait(bar(L::XF), seg & 1))) break;
+                for (int i = 0; i < t.steps; ++i, ++j) {
+                    if (!(ok = wait(bar(L::KF + k.slot), k.phase))) break;
+                    if (j > 0 && !(ok = wait(bar(L::DE), (j - 1) & 1))) break;
+                    tc_fence_after();
+                    const uint64_t kd = k_desc + k.slot * kTile;  // the keys are the A operand
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            umma_bf16(tmem + L::cD, kd + (kk >> 2) * kAtom + 2 * (kk & 3), m_desc + p * kPart + 128 * kk,
+                                      ID_D, p > 0 || kk > 0);
+                    umma_commit(bar(L::DF + k.slot));
+                    if (i + 1 == t.steps) umma_commit(bar(L::XE));
+                    k.next();
+                }
+            }
+            umma_commit(bar(L::END + 1));
+            mbar_wait(bar(L::END + 1), 0, limit_ns);
         }
     } else if (NT == 1 && warp >= 4) {
         // ============================================================ the keys' update
@@ -422,7 +455,8 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
                 const bool whole = tile_whole(pos0, t.s.n, have, box_shift);
                 const int mine = __shfl_sync(0xffffffffu, id, r >> box_shift);
-                if (!(ok = wait.warp(bar(L::DF), j & 1))) break;
+                // the product is there, and the logits' product has read the keys too
+                if (!(ok = wait.warp(bar(L::DF + j % NK), (j / NK) & 1))) break;
                 tc_fence_after();
                 uint8_t *const kt = sm + (key_slot(j) - base);
                 bf *const dst = mine >= 0 && pos0 + r < t.s.n
@@ -646,19 +680,13 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                             weigh(x + c, p);
                             weigh(x + c + 32, p + 16);
                             tmem_st32(tm + L::cS + c / 2, p);
-                            if (c == 0) {
-                                tmem_st_wait();
-                                tc_fence_before();
-                                mbar_arrive_warp(bar(L::PR + 2 * w));
-                            }
                         }
                     }
                     l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_st_wait();
                 }
                 tc_fence_before();
-                if (kTwice || !warp_live) mbar_arrive_warp(bar(L::PR + 2 * w));
-                mbar_arrive_warp(bar(L::PR + 2 * w + 1));
+                mbar_arrive_warp(bar(L::PR + w));
             }
             if (!ok || !(ok = wait.warp(bar(L::FIN + w), seg & 1))) break;
             ++seg;
