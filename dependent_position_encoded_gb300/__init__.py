@@ -674,7 +674,7 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
         q0, k0, v0, w0 = q.stride(), k.stride(), v.stride(), w.stride()
         b0 = beta.stride()
         f0 = (0, 0) if log_f is None else log_f.stride()
-        o0 = (Hq * d, d, 1) if out is None else out.stride()
+        o0 = q0 if out is None else out.stride()
         fine = (q.dtype == dt and k.dtype == dt and v.dtype == dt and w.dtype == dt
                 and beta.dtype == f32 and cu_tokens.dtype == torch.int32 and k.shape == rows
                 and v.shape == rows and w.shape == rows and beta.shape == heads
@@ -694,22 +694,18 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
     if out is not None and (N > 1 and o0[0] == 0 or Hq > 1 and o0[1] == 0):
         raise ValueError("out must not repeat its own memory")
     _paged_devices(cache, q, k, v, w, beta, log_f, out, cu_tokens)
-    st = (q0[0], q0[1], k0[0], k0[1], v0[0], v0[1], w0[0], w0[1], b0[0], b0[1], f0[0], f0[1], o0[0],
-          o0[1])
-    if N <= 1 or Hkv <= 1:  # the stride of an axis of one element says nothing
-        one = (N <= 1, Hq <= 1, N <= 1, Hkv <= 1)
-        st = [0 if one[(i & 1) + (0 if i in (0, 1, 10, 11, 12, 13) else 2)] else x
-              for i, x in enumerate(st)]
     gate = () if log_f is None else (log_f.data_ptr(),)
     with _on(dev, stream):
         if out is None:
-            out = torch.empty(qs, dtype=dt, device=dev)
+            out = torch.empty_like(q)
+            o0 = out.stride()
         if workspace is None and N > 0 and c.seqs > 0:
             workspace = new_paged_workspace(cache, N, max_chunk, Hq)
         _check(getattr(_load(), name)(
             ctypes.byref(c), q.data_ptr(), k.data_ptr(), v.data_ptr(), w.data_ptr(),
             beta.data_ptr(), *gate, cu_tokens.data_ptr(), N, int(max_chunk), _scale(scale, d),
-            out.data_ptr(), _C14(*st), None if workspace is None else workspace.data_ptr(),
+            out.data_ptr(), _C14(q0[0], q0[1], k0[0], k0[1], v0[0], v0[1], w0[0], w0[1], b0[0], b0[1],
+                                 f0[0], f0[1], o0[0], o0[1]), None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel(), _stream(stream, dev)), name)
     return out
 

@@ -84,6 +84,75 @@ __device__ __forceinline__ bool block_of(const Step &a, int slot, int &b, int &c
     return c >= 0 && c * kC < s.T;
 }
 
+// (I + E)^{-1} in fp32 for a strictly lower triangular E (shared, stride LD): the four 16 x 16
+// diagonal blocks by substitution (one column per thread), then X21 = -X22 E21 X11 for the 16-
+// and the 32-blocks; every factor is bounded (products of contractions), so nothing grows.
+// 256 threads. `Y`: 32 x 36 floats of scratch; nt: the 16-row tiles in use (the others are the identity).
+template <int LD>
+__device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid, int nt) {
+    constexpr int YL = 36, kThr = 256;
+    const int b0 = (tid >> 4) << 4, lu = tid & 15;
+    float x[16];
+    if (tid < kC) {
+#pragma unroll
+        for (int l = 0; l < 16; ++l) x[l] = l == lu ? 1.f : 0.f;
+#pragma unroll
+        for (int m = 0; m < 15; ++m)
+#pragma unroll
+            for (int l = m + 1; l < 16; ++l) x[l] = fmaf(-E[(b0 + l) * LD + b0 + m], x[m], x[l]);
+    }
+    __syncthreads();
+    if (tid < kC)
+#pragma unroll
+        for (int l = 0; l < 16; ++l) E[(b0 + l) * LD + tid] = x[l];
+    __syncthreads();
+    if (nt <= 1) return;
+    // level 1: two 32-blocks at o, X21 (16 x 16)
+    for (int pass = 0; pass < 2; ++pass) {
+        float v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = tid + i * kThr, o = 32 * (e >> 8), r = (e >> 4) & 15, c = e & 15;
+            float t = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                t = pass == 0 ? fmaf(E[(o + 16 + r) * LD + o + k], E[(o + k) * LD + o + c], t)
+                              : fmaf(E[(o + 16 + r) * LD + o + 16 + k], Y[((o >> 1) + k) * YL + c], t);
+            v[i] = t;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = tid + i * kThr, o = 32 * (e >> 8), r = (e >> 4) & 15, c = e & 15;
+            if (pass == 0) Y[((o >> 1) + r) * YL + c] = v[i];
+            else E[(o + 16 + r) * LD + o + c] = -v[i];
+        }
+        __syncthreads();
+    }
+    if (nt <= 2) return;
+    // level 2: X21 (32 x 32)
+    for (int pass = 0; pass < 2; ++pass) {
+        float v[4];
+        const int r = tid >> 3, c0 = (tid & 7) * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) {
+            const float l = pass == 0 ? E[(32 + r) * LD + k] : E[(32 + r) * LD + 32 + k];
+            const float4 q = *reinterpret_cast<const float4 *>(pass == 0 ? E + k * LD + c0 : Y + k * YL + c0);
+            v[0] = fmaf(l, q.x, v[0]);
+            v[1] = fmaf(l, q.y, v[1]);
+            v[2] = fmaf(l, q.z, v[2]);
+            v[3] = fmaf(l, q.w, v[3]);
+        }
+        __syncthreads();
+        float *dst = pass == 0 ? Y + r * YL + c0 : E + (32 + r) * LD + c0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = pass == 0 ? v[i] : -v[i];
+        __syncthreads();
+    }
+}
+
 // The kernels of one call follow each other as programmatic dependents: the next one's CTAs
 // may come up (barriers, tensor memory) while the last ones of the one before still run, and
 // wait here before they touch memory. Every CTA waits before anything else that counts, so a

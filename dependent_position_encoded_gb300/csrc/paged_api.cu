@@ -18,9 +18,9 @@ size_t tc_ws_bytes(const Cache &c, int N, int max_chunk, int d, bool fox);
 cudaError_t launch_tc(const Step &a, int d, void *ws, uint64_t limit_ns, cudaStream_t stream);
 size_t pages_ws_bytes(const Cache &c);
 cudaError_t launch_reserve(const Cache &c, const int *extra, void *ws, cudaStream_t stream);
-cudaError_t launch_fork(const Cache &c, const Rows &src, const Rows &dst, int row_bytes, void *ws,
-                        cudaStream_t stream);
-cudaError_t launch_free(const Cache &c, const Rows &rows, void *ws, cudaStream_t stream);
+cudaError_t launch_fork(const Cache &c, const Rows<kMaxRows> &src, const Rows<kMaxRows> &dst, int row_bytes,
+                        void *ws, cudaStream_t stream);
+cudaError_t launch_free(const Cache &c, const Rows<kMaxRows> &rows, void *ws, cudaStream_t stream);
 cudaError_t launch_compact(const Cache &c, int row_bytes, void *ws, cudaStream_t stream);
 }  // namespace paged
 }  // namespace path
@@ -29,7 +29,7 @@ namespace {
 
 using namespace path;
 using paged::Cache;
-using paged::Rows;
+using Rows = paged::Rows<paged::kMaxRows>;
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bounded waits of the tensor-core kernels
 
@@ -113,9 +113,14 @@ path_status check_step_sizes(const path_paged_cache *p, int N, int max_chunk) {
     return PATH_OK;
 }
 
-// (token, head) strides of a (N, H, inner) tensor: packed where st is null
-paged::Stride stride_of(const int64_t *st, int H, int inner) {
-    return st ? paged::Stride{st[0], st[1]} : paged::Stride{(long long)H * inner, inner};
+// (token, head) strides of a (N, H, inner) tensor: packed where st is null. The stride of an axis
+// of one element says nothing.
+paged::Stride stride_of(const int64_t *st, int N, int H, int inner) {
+    if (!st) return paged::Stride{(long long)H * inner, inner};
+    return paged::Stride{N > 1 ? st[0] : 0, H > 1 ? st[1] : 0};
+}
+bool bad_stride(const paged::Stride &s, int bytes) {
+    return s.tok < 0 || s.head < 0 || s.tok * bytes % 16 != 0 || s.head * bytes % 16 != 0;
 }
 
 path_status extend(const path_paged_cache *p, const void *q, const void *k, const void *v,
@@ -134,25 +139,21 @@ path_status extend(const path_paged_cache *p, const void *q, const void *k, cons
     for (const void *x : al16)
         if (!is_aligned(x, 16)) return PATH_ERR_ALIGN;
     if (!is_aligned(beta, 4) || !is_aligned(log_f, 4) || !is_aligned(cu_tokens, 4)) return PATH_ERR_ALIGN;
-    if (strides) {
-        const int64_t *rows[] = {strides->q, strides->k, strides->v, strides->w, strides->out};
-        for (const int64_t *r : rows)
-            if (r[0] < 0 || r[1] < 0 || r[0] * elt_size(p) % 16 != 0 || r[1] * elt_size(p) % 16 != 0)
-                return PATH_ERR_ALIGN;
-        const int64_t *flat[] = {strides->beta, strides->log_f};
-        for (const int64_t *r : flat)
-            if (r[0] < 0 || r[1] < 0) return PATH_ERR_ALIGN;
-    }
+    const paged::Stride sq = stride_of(strides ? strides->q : nullptr, N, p->Hq, p->d),
+                        sk = stride_of(strides ? strides->k : nullptr, N, p->Hkv, p->d),
+                        sv = stride_of(strides ? strides->v : nullptr, N, p->Hkv, p->d),
+                        sw = stride_of(strides ? strides->w : nullptr, N, p->Hkv, p->d),
+                        sb = stride_of(strides ? strides->beta : nullptr, N, p->Hkv, 1),
+                        sf = stride_of(strides ? strides->log_f : nullptr, N, p->Hq, 1),
+                        so = stride_of(strides ? strides->out : nullptr, N, p->Hq, p->d);
+    for (const paged::Stride &r : {sq, sk, sv, sw, so})
+        if (bad_stride(r, elt_size(p))) return PATH_ERR_ALIGN;
+    for (const paged::Stride &r : {sb, sf})
+        if (r.tok < 0 || r.head < 0) return PATH_ERR_ALIGN;
     if ((st = check_workspace(ws, ws_bytes, step_ws_bytes(p, N, max_chunk, fox))) != PATH_OK) return st;
     const Cache c = to_cache(p);
     const paged::Step a{c, q, k, v, w, beta, fox ? log_f : nullptr, out,
-                        stride_of(strides ? strides->q : nullptr, p->Hq, p->d),
-                        stride_of(strides ? strides->k : nullptr, p->Hkv, p->d),
-                        stride_of(strides ? strides->v : nullptr, p->Hkv, p->d),
-                        stride_of(strides ? strides->w : nullptr, p->Hkv, p->d),
-                        stride_of(strides ? strides->beta : nullptr, p->Hkv, 1),
-                        stride_of(strides ? strides->log_f : nullptr, p->Hq, 1),
-                        stride_of(strides ? strides->out : nullptr, p->Hq, p->d),
+                        sq, sk, sv, sw, sb, sf, so,
                         cu_tokens, N, max_chunk, scale * kLog2e, static_cast<uint32_t *>(ws)};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (one_pass(c, max_chunk, p->dtype == PATH_BF16, fox))

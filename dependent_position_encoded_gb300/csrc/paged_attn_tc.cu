@@ -142,8 +142,8 @@ struct CachedCfg {
     static constexpr uint32_t X = 0, M = X + NT * tile, mbytes = NT == 1 ? 2 * D * D * 2 : 0;
     // slots of keys and of values: what fits beside; for NT = 1 and D = 64 so that two CTAs share
     // an SM. With NT = 1 a key slot is held until the updated keys have left it.
-    static constexpr int NK = NT == 1 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 2);
-    static constexpr int NV = NT == 1 ? 2 : (D == 64 ? 4 : 3);
+    static constexpr int NK = NT == 1 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3);
+    static constexpr int NV = NT == 1 ? 2 : (D == 64 ? 4 : 2);
     static constexpr uint32_t K = M + mbytes, V = K + NK * tile, bars = V + NV * tile;
     static constexpr int KF = 0, KE = NK, VF = 2 * NK, VE = VF + NV, XF = VE + NV, XE = XF + 1, SF = XE + 1, PR = SF + 2, FIN = PR + 2,
                          DF = FIN + 2, DE = DF + NK, TMP = DE + 1, END = TMP + 2, count = END + 2;
@@ -220,10 +220,11 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
     if (tid == 0) {
         *abort_f = 0u;
         // four warps: weights written, update's product read; both issuing threads (NT = 1): rows' tile
-        // free, keys read by their products
+        // free, keys read by their products; both row tiles (NT = 2): keys and values read
         for (int i = 0; i < L::count; ++i) {
             const bool four = (i >= L::PR && i < L::FIN) || i == L::DE;
-            const bool both = NT == 1 && (i == L::XE || (i >= L::DF && i < L::DE));
+            const bool both = NT == 1 ? i == L::XE || (i >= L::DF && i < L::DE)
+                                      : (i >= L::KE && i < L::VF) || (i >= L::VE && i < L::XF);
             mbar_init(bar(i), four ? 4u : both ? 2u : 1u);
         }
         fence_mbar_init();
@@ -360,9 +361,10 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
 #pragma unroll
                 for (int kk = 1; kk < 8; ++kk) umma_tA(tm + L::cO, tm + L::cS + 8 * kk, vd + 128 * kk, ID_O, 1);
             };
-            // the keys of the ring's slot have been multiplied; last of a stretch: the rows' tile is free
+            // behind the products of the ring's keys; last of a stretch: the rows' tile is free. (Slots are
+            // handed back by the softmax's warps, which learn of the products' ends anyway.)
             auto after_s = [&](bool last) {
-                umma_commit(bar((NT == 2 ? L::KE : L::DF) + k.slot));
+                if (NT == 1) umma_commit(bar(L::DF + k.slot));
                 if (last) umma_commit(bar(L::XE));
                 k.next();
             };
@@ -378,18 +380,21 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 for (int i = 0; i < t.steps; ++i) {
                     const bool more = i + 1 < t.steps;
                     if (!(ok = wait(bar(L::VF + v.slot), v.phase))) break;
-                    if (more && !(ok = wait(bar(L::KF + k.slot), k.phase))) break;
-#pragma unroll
-                    for (int q = 0; q < NT; ++q) {
-                        if (q == 1 && !two) break;
-                        if (!(ok = wait(bar(L::PR + q), parity[q]))) break;
-                        tc_fence_after();
-                        issue_pv(q, i == 0);
-                        if (more) issue_s(q);
-                        parity[q] ^= 1;
+                    if (!(ok = wait(bar(L::PR), parity[0]))) break;
+                    tc_fence_after();
+                    issue_pv(0, i == 0);
+                    if (more) {
+                        if (!(ok = wait(bar(L::KF + k.slot), k.phase))) break;
+                        issue_s(0);
                     }
-                    if (!ok) break;
-                    umma_commit(bar(L::VE + v.slot));
+                    parity[0] ^= 1;
+                    if (NT == 2 && two) {
+                        if (!(ok = wait(bar(L::PR + 1), parity[1]))) break;
+                        tc_fence_after();
+                        issue_pv(1, i == 0);
+                        if (more) issue_s(1);
+                        parity[1] ^= 1;
+                    }
                     v.next();
                     if (more) after_s(i + 2 == t.steps);
                 }
@@ -510,11 +515,18 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
         const int w = warp >> 2, r = tid & 127;  // row tile and row in it
         const uint32_t tm = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + L::per_tile * w;
         bool ok = true;
-        uint32_t j = 0, seg = 0;  // steps and stretches that this row tile takes part in
+        // One thread of a row tile hands slots back: the logits' product of step j has read its keys, and
+        // it ends behind the values' product of step j - 1. (NT = 1: the update's warps release keys.)
+        const bool releases = (warp & 3) == 0 && lane == 0;
+        uint32_t j = 0, seg = 0, step = 0;  // steps and stretches with rows in this tile; steps of the CTA
         for (long long at = u_begin; ok && at < u_end;) {
             const Stretch t = stretch_at(a, plan, NT, at, u_end);
             at += t.steps;
-            if (w == 1 && !second(t)) continue;
+            if (w == 1 && !second(t)) {
+                step += t.steps;
+                continue;
+            }
+            const bool alone = NT == 2 && !second(t);  // no other tile: its part of the releases too
             // the row of this thread, and the columns of the key tiles that its copy takes
             const int rows_all = t.s.T * G, cp = copies(t), rw = r & ((128 >> cp) - 1);
             const int row0 = 128 * (NT * t.tile + w), cols = 128 >> cp, c_begin = (r >> (7 - cp)) * cols;
@@ -533,7 +545,11 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 }
             };
             look_up(t.k0 * 128);
-            for (int i = 0; i < t.steps; ++i, ++j) {
+            auto release = [&](int empty, uint32_t slot) {
+                mbar_arrive(bar(empty + slot));
+                if (alone) mbar_arrive(bar(empty + slot));
+            };
+            for (int i = 0; i < t.steps; ++i, ++j, ++step) {
                 const int pos0 = (t.k0 + i) * 128, id = kid1;
                 const bool good = (unsigned)id < (unsigned)a.c.nk && (unsigned)vid1 < (unsigned)a.c.nv;
                 if (i + 1 < t.steps) look_up(pos0 + 128);
@@ -573,6 +589,10 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 }
                 if (!(ok = wait.warp(bar(L::SF + w), j & 1))) break;
                 tc_fence_after();
+                if (releases) {
+                    if (NT == 2) release(L::KE, step % NK);
+                    if (i > 0) release(L::VE, (step - 1) % NV);
+                }
                 if (warp_live) {
                     // gates and mask of 32 logits of the row from column c
                     auto gate = [&](int c, float *x) {
@@ -691,6 +711,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             if (!ok || !(ok = wait.warp(bar(L::FIN + w), seg & 1))) break;
             ++seg;
             tc_fence_after();
+            if (releases) release(L::VE, (step - 1) % NV);
             if (warp_live) {
                 // the part's place: its CTA and item; a row whose keys were all absent leaves a sum of 0
                 const size_t e = ((size_t)(blockIdx.x + t.item) * NT + w) * 128 + r;

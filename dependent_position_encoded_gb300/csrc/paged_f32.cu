@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y
     const int ty = tid >> 4, tx = tid & 15;
     int b, c;
     Seq s;
+    grid_wait();
     if (!block_of(a, slot, b, c, s)) return;
     const int i0 = c * kC, rows = min(kC, s.T - i0);
     const long long first = s.first + i0;
@@ -267,20 +268,9 @@ __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y
             R[r * LD + q] = q > r ? c0[i][j] : 0.f;
         }
     __syncthreads();
-    // A = (I + E)^{-1} D, one column per thread by forward substitution
-    float x[kC];
-    if (tid < kC) {
-#pragma unroll
-        for (int t = 0; t < kC; ++t) x[t] = t == tid ? beta[t] : 0.f;
-#pragma unroll
-        for (int t = 0; t < kC - 1; ++t)
-#pragma unroll
-            for (int r = t + 1; r < kC; ++r) x[r] = fmaf(-A[r * LD + t], x[t], x[r]);
-    }
-    __syncthreads();
-    if (tid < kC)
-#pragma unroll
-        for (int t = 0; t < kC; ++t) A[t * LD + tid] = x[t];
+    // A = (I + E)^{-1} D
+    unit_lower_inverse<LD>(A, L, tid, 4);
+    for (int e = tid; e < kC * kC; e += kThr) A[(e >> 6) * LD + (e & 63)] *= beta[e & 63];
     __syncthreads();
 #pragma unroll 1
     for (int x2 = 0; x2 < NH; ++x2) {
@@ -325,13 +315,23 @@ __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y
         const size_t bq = (size_t)slot * a.c.Hq + hq;
         __syncthreads();
         load_tokens<D>(Q, a.q, a.sq, first, hq, rows);
-        if (a.log_f != nullptr && tid == 0) {
-            double t = 0.0;
-            for (int i = 0; i < kC; ++i) {
-                if (i < rows) t += (double)a.log_f[(first + i) * a.sf.tok + hq * a.sf.head];
-                cum[i] = t;
+        if (a.log_f != nullptr && tid < 32) {
+            // inclusive prefix sums: lane i holds those of tokens i and i + 32
+            double t[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int i = 32 * half + tid;
+                t[half] = i < rows ? (double)a.log_f[(first + i) * a.sf.tok + hq * a.sf.head] : 0.0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double z = __shfl_up_sync(0xffffffffu, t[half], o);
+                    if (tid >= o) t[half] += z;
+                }
             }
-            y.gtot[bq] = t;
+            t[1] += __shfl_sync(0xffffffffu, t[0], 31);
+            cum[tid] = t[0];
+            cum[tid + 32] = t[1];
+            if (tid == 31) y.gtot[bq] = t[1];
         }
         if (tid < kC) {
             m[tid] = -INFINITY;
@@ -413,6 +413,7 @@ __global__ void __launch_bounds__(kThr) f32_scan_kernel(const Step a, const Ws y
     const int ty = tid >> 4, tx = tid & 15;
     int b, c;
     Seq s;
+    grid_wait();
     if (!block_of(a, slot, b, c, s) || c == 0) return;
     const size_t bq = (size_t)slot * a.c.Hq + hq;
     float *const part = y.part + bq * (1 + y.splits) * kPart<D>;
@@ -508,6 +509,7 @@ __global__ void __launch_bounds__(kThr) f32_cached_kernel(const Step a, const Ws
     const int ty = tid >> 4, tx = tid & 15;
     int b, c, j0, j1;
     Seq s;
+    grid_wait();
     if (!block_of(a, slot, b, c, s)) return;
     split_range(s.n, y.splits, sp, j0, j1);
     if (j0 >= j1) return;
@@ -565,30 +567,55 @@ __global__ void __launch_bounds__(kThr) f32_cached_kernel(const Step a, const Ws
 }
 
 // ---------------------------------------------------------------- combine
+// One warp per row, eight parts' rows in flight at a time; grid (slots, Hq, 8).
 template <int D>
 __global__ void __launch_bounds__(kThr) f32_combine_kernel(const Step a, const Ws y) {
-    const int slot = blockIdx.x, hq = blockIdx.y;
+    constexpr int E = D / 32;
+    const int slot = blockIdx.x, hq = blockIdx.y, lane = threadIdx.x & 31;
+    const int r = blockIdx.z * 8 + (threadIdx.x >> 5);
     int b, c;
     Seq s;
-    if (!block_of(a, slot, b, c, s)) return;
-    const int rows = min(kC, s.T - c * kC);
+    grid_wait();
+    if (!block_of(a, slot, b, c, s) || r >= s.T - c * kC) return;
     const int tiles = (s.n + kC - 1) / kC, per = (tiles + y.splits - 1) / y.splits;
     const int used = 1 + (per > 0 ? (tiles + per - 1) / per : 0);
     const float *p0 = y.part + ((size_t)slot * a.c.Hq + hq) * (1 + y.splits) * kPart<D>;
-    for (int e = threadIdx.x; e < rows * D; e += kThr) {
-        const int r = e / D, q = e % D;
-        float M = -INFINITY, Ls = 0.f, O = 0.f;
-        for (int i = 0; i < used; ++i) M = fmaxf(M, p0[i * kPart<D> + kC * D + r]);
-        for (int i = 0; i < used; ++i) {
-            const float *p = p0 + i * kPart<D>;
-            const float mi = p[kC * D + r];
-            if (mi == -INFINITY) continue;
-            const float f = exp2f(mi - M);
-            Ls = fmaf(p[kC * D + kC + r], f, Ls);
-            O = fmaf(p[r * D + q], f, O);
+    float M = -INFINITY, L = 0.f, O[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) O[e] = 0.f;
+    for (int i0 = 0; i0 < used; i0 += 8) {
+        float m[8], l[8], v[8][E], top = M;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+            if (i0 + i < used) {
+                const float *p = p0 + (i0 + i) * kPart<D>;
+                m[i] = p[kC * D + r];
+                l[i] = p[kC * D + kC + r];
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[i][e] = p[r * D + lane * E + e];
+            }
+            top = fmaxf(top, m[i]);
         }
-        static_cast<float *>(a.out)[(long long)(s.first + c * kC + r) * a.so.tok + hq * a.so.head + q] = O / Ls;
+        const float f0 = exp2f(M - top);  // 0 at first; part 0 holds the row's own key
+        M = top;
+        L *= f0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) O[e] *= f0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float f = exp2f(m[i] - top);
+            L = fmaf(l[i], f, L);
+#pragma unroll
+            for (int e = 0; e < E; ++e) O[e] = fmaf(v[i][e], f, O[e]);
+        }
     }
+    float *dst = static_cast<float *>(a.out) + (long long)(s.first + c * kC + r) * a.so.tok + hq * a.so.head + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) dst[e] = O[e] / L;
 }
 
 // ---------------------------------------------------------------- carry
@@ -605,6 +632,7 @@ __global__ void __launch_bounds__(kThr) f32_carry_kernel(const Step a, const Ws 
     const bool ident = (int)blockIdx.x >= nslots;
     int b, c = -1;
     Seq s;
+    grid_wait();
     int tile = 0;
     if (ident) {
         b = ((int)blockIdx.x - nslots) / NH;
@@ -684,6 +712,7 @@ __global__ void __launch_bounds__(kThr) f32_transform_kernel(const Step a, const
     float *K = sm, *P = K + NH * TILE;
     int *kid = reinterpret_cast<int *>(P + NH * NH * TILE);
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    grid_wait();
     const Seq s = seq_of(a, b);
     if (s.T == 0 || (int)blockIdx.x * kC >= s.n) return;
     const int nb = (s.T + kC - 1) / kC;
@@ -741,17 +770,24 @@ cudaError_t launch_d(const Step &a, const Ws &y, cudaStream_t stream) {
         (e = big_smem(f32_carry_kernel<D>, carry_smem<D>())) != cudaSuccess ||
         (e = big_smem(f32_transform_kernel<D>, transform_smem<D>())) != cudaSuccess)
         return e;
-    f32_prep_kernel<D><<<dim3(nslots, Hkv), kThr, prep_smem<D>(), stream>>>(a, y);
-    if (a.max_chunk > kC)
-        f32_scan_kernel<D><<<dim3(nslots, Hq), kThr, scan_smem<D>(), stream>>>(a, y);
-    f32_cached_kernel<D><<<dim3(nslots, Hq, y.splits), kThr, cached_smem<D>(), stream>>>(a, y);
-    f32_combine_kernel<D><<<dim3(nslots, Hq), kThr, 0, stream>>>(a, y);
-    f32_carry_kernel<D><<<dim3(nslots + a.c.seqs * (D / 64), Hkv), kThr, carry_smem<D>(), stream>>>(
-        a, y, nslots);
     const long long cap = (long long)a.c.max_pages << a.c.page_shift;
-    const int parts = (int)((cap + 4 * kC - 1) / (4 * kC));
-    f32_transform_kernel<D><<<dim3(parts, Hkv, a.c.seqs), kThr, transform_smem<D>(), stream>>>(a, y);
-    return cudaGetLastError();
+    e = launch(f32_prep_kernel<D>, dim3(nslots, Hkv), kThr, prep_smem<D>(), stream, true, a, y);
+    if (e == cudaSuccess && a.max_chunk > kC)
+        e = launch(f32_scan_kernel<D>, dim3(nslots, Hq), kThr, scan_smem<D>(), stream, false, a, y);
+    if (e == cudaSuccess)
+        e = launch(f32_cached_kernel<D>, dim3(nslots, Hq, y.splits), kThr, cached_smem<D>(), stream, false, a, y);
+    if (e == cudaSuccess)
+        e = launch(f32_combine_kernel<D>, dim3(nslots, Hq, kC / 8), kThr, 0, stream, false, a, y);
+    if (e == cudaSuccess)
+        e = launch(f32_carry_kernel<D>, dim3(nslots + a.c.seqs * (D / 64), Hkv), kThr, carry_smem<D>(), stream, false,
+                   a, y, nslots);
+    // CTAs of 64 cached keys, or of several where that makes more than four to an SM
+    long long parts = 4 * 152 / ((long long)Hkv * a.c.seqs) + 1;
+    if (parts > (cap + kC - 1) / kC) parts = (cap + kC - 1) / kC;
+    if (e == cudaSuccess && parts > 0)
+        e = launch(f32_transform_kernel<D>, dim3((unsigned)parts, Hkv, a.c.seqs), kThr, transform_smem<D>(), stream,
+                   false, a, y);
+    return e;
 }
 
 struct F32Layout {
@@ -759,12 +795,12 @@ struct F32Layout {
     size_t qt, kt, pb, part, gq, gt, gtot, ptot, total;
 };
 
-// Splits of the cached keys: enough CTAs for every SM twice, none below 512 positions.
+// Splits of the cached keys: enough CTAs for every SM four times, none below 64 positions.
 F32Layout f32_layout(const Cache &c, int N, int d, bool fox) {
     F32Layout y;
     const size_t slots = slots_of(N, c.seqs);
     const long long cap = (long long)c.max_pages << c.page_shift;
-    const long long want = 304 / (long long)(slots * c.Hq) + 1, most = (cap + 511) / 512;
+    const long long want = 608 / (long long)(slots * c.Hq) + 1, most = (cap + 63) / 64;
     y.splits = (int)(want < most ? want : most);
     if (y.splits < 1) y.splits = 1;
     size_t off = 256;
@@ -778,7 +814,7 @@ F32Layout f32_layout(const Cache &c, int N, int d, bool fox) {
     y.pb = take(slots * c.Hkv * d * d * 4);
     // parts: (1 + splits) per row block, taken as a bound that does not fall as slots rises, so
     // that a workspace for many tokens serves steps of fewer
-    const size_t blocks = slots * c.Hq, by_want = 2 * blocks + 304, by_most = blocks * (1 + (size_t)most);
+    const size_t blocks = slots * c.Hq, by_want = 2 * blocks + 608, by_most = blocks * (1 + (size_t)most);
     const size_t parts = most < 1 ? 2 * blocks : (by_want < by_most ? by_want : by_most);
     y.part = take(parts * kC * (d + 2) * 4);
     y.gq = take(fox ? slots * c.Hq * kC * 4 : 0);

@@ -173,13 +173,15 @@ __global__ void __launch_bounds__(kPlanThr) reserve_kernel(const Cache c, const 
 }
 
 // ---------------------------------------------------------------- fork
-__global__ void __launch_bounds__(kPlanThr) fork_plan_kernel(const Cache c, const Rows src, const Rows dst,
+template <int N>
+__global__ void __launch_bounds__(kPlanThr) fork_plan_kernel(const Cache c, const Rows<N> src, const Rows<N> dst,
                                                              const PagesWs y) {
     __shared__ int sums[32];
     const int tid = threadIdx.x, half = tid / kHalf, t = tid & (kHalf - 1), warp = t >> 5, lane = tid & 31;
     const Pool p = pool_of(c, y, half);
     const int pairs = src.n;
     bool bad = false;
+    grid_wait();  // the first of the call: it only lets the copies come up
     if (tid == 0) y.go[0] = 0;
     for (int i = warp; i < pairs; i += kHalfWarps) {
         const int n = c.lens[src.row[i]];
@@ -257,8 +259,10 @@ __device__ __forceinline__ void copy_page(char *dst, const char *src, int heads,
 
 // grid (slots, pairs): the key page (and its gate sums) of a slot, or the value page that is
 // not shared
-__global__ void __launch_bounds__(256) fork_copy_kernel(const Cache c, const Rows src, const Rows dst,
+template <int N>
+__global__ void __launch_bounds__(256) fork_copy_kernel(const Cache c, const Rows<N> src, const Rows<N> dst,
                                                         int row_bytes, const PagesWs y) {
+    grid_wait();
     if (y.go[0] == 0) return;
     const int s = blockIdx.x, i = blockIdx.y;
     const int n = c.lens[src.row[i]], rows = min(c.page, n - (s << c.page_shift));
@@ -283,7 +287,8 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const Cache c, const Row
 
 // ---------------------------------------------------------------- free
 // grid (rows, pools)
-__global__ void __launch_bounds__(256) free_kernel(const Cache c, const Rows rows, const PagesWs y) {
+template <int N>
+__global__ void __launch_bounds__(256) free_kernel(const Cache c, const Rows<N> rows, const PagesWs y) {
     const int s = rows.row[blockIdx.x];
     const Pool p = pool_of(c, y, blockIdx.y);
     for (int i = threadIdx.x; i < c.max_pages; i += 256) {
@@ -306,6 +311,7 @@ __global__ void __launch_bounds__(kPlanThr) compact_plan_kernel(const Cache c, c
     const Pool p = pool_of(c, y, half);
     const int most = max(c.nk, c.nv);
     int live = 0;
+    grid_wait();  // the first of the call: it only lets the moves come up
     for (long long base = 0; base < most; base += kHalf * kItems) {
         int r[kItems];
         load_counts(p, base + t * kItems, r);
@@ -351,6 +357,7 @@ __global__ void __launch_bounds__(kPlanThr) compact_plan_kernel(const Cache c, c
 // CTAs below `table_ctas` renumber the tables' entries, the others move pages.
 __global__ void __launch_bounds__(256) compact_move_kernel(const Cache c, int row_bytes, int table_ctas,
                                                            const PagesWs y) {
+    grid_wait();
     if ((int)blockIdx.x < table_ctas) {
         const long long per = (long long)c.seqs * c.max_pages;
         for (long long i = blockIdx.x * 256ll + threadIdx.x; i < 2 * per; i += table_ctas * 256ll) {
@@ -420,33 +427,47 @@ cudaError_t launch_reserve(const Cache &c, const int *extra, void *ws, cudaStrea
     return cudaGetLastError();
 }
 
-cudaError_t launch_fork(const Cache &c, const Rows &src, const Rows &dst, int row_bytes, void *ws,
-                        cudaStream_t stream) {
-    const PagesWs y = pages_ws(c, ws, nullptr);
-    fork_plan_kernel<<<1, kPlanThr, 0, stream>>>(c, src, dst, y);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    fork_copy_kernel<<<dim3(c.max_pages, src.n), 256, 0, stream>>>(c, src, dst, row_bytes, y);
-    return cudaGetLastError();
+// A list as a smaller one: most calls name a few rows, and a launch copies its parameters.
+constexpr int kFewRows = 32;
+Rows<kFewRows> few_rows(const Rows<kMaxRows> &a) {
+    Rows<kFewRows> r;
+    r.n = a.n;
+    for (int i = 0; i < a.n; ++i) r.row[i] = a.row[i];
+    return r;
 }
 
-cudaError_t launch_free(const Cache &c, const Rows &rows, void *ws, cudaStream_t stream) {
-    free_kernel<<<dim3(rows.n, 2), 256, 0, stream>>>(c, rows, pages_ws(c, ws, nullptr));
-    return cudaGetLastError();
+template <int N>
+cudaError_t launch_fork_n(const Cache &c, const Rows<N> &src, const Rows<N> &dst, int row_bytes, const PagesWs &y,
+                          cudaStream_t stream) {
+    const cudaError_t e = launch(fork_plan_kernel<N>, dim3(1), kPlanThr, 0, stream, true, c, src, dst, y);
+    if (e != cudaSuccess) return e;
+    return launch(fork_copy_kernel<N>, dim3(c.max_pages, src.n), 256, 0, stream, false, c, src, dst, row_bytes, y);
+}
+
+cudaError_t launch_fork(const Cache &c, const Rows<kMaxRows> &src, const Rows<kMaxRows> &dst, int row_bytes,
+                        void *ws, cudaStream_t stream) {
+    const PagesWs y = pages_ws(c, ws, nullptr);
+    return src.n <= kFewRows ? launch_fork_n(c, few_rows(src), few_rows(dst), row_bytes, y, stream)
+                             : launch_fork_n(c, src, dst, row_bytes, y, stream);
+}
+
+cudaError_t launch_free(const Cache &c, const Rows<kMaxRows> &rows, void *ws, cudaStream_t stream) {
+    const PagesWs y = pages_ws(c, ws, nullptr);
+    return rows.n <= kFewRows
+               ? launch(free_kernel<kFewRows>, dim3(rows.n, 2), 256, 0, stream, true, c, few_rows(rows), y)
+               : launch(free_kernel<kMaxRows>, dim3(rows.n, 2), 256, 0, stream, true, c, rows, y);
 }
 
 cudaError_t launch_compact(const Cache &c, int row_bytes, void *ws, cudaStream_t stream) {
     const PagesWs y = pages_ws(c, ws, nullptr);
-    compact_plan_kernel<<<1, kPlanThr, 0, stream>>>(c, y);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch(compact_plan_kernel, dim3(1), kPlanThr, 0, stream, true, c, y);
     if (e != cudaSuccess) return e;
     const long long entries = 2ll * c.seqs * c.max_pages;
     const int table_ctas = (int)(entries / 2048 < 64 ? entries / 2048 + 1 : 64);
     // at most min(nk, nv) + ... / 2 pages move; eight CTAs per SM keep the copies in flight
     const long long most = ((long long)c.nk + c.nv) / 2 + 1;
     const int movers = (int)(most < 8 * 152 ? most : 8 * 152);
-    compact_move_kernel<<<table_ctas + movers, 256, 0, stream>>>(c, row_bytes, table_ctas, y);
-    return cudaGetLastError();
+    return launch(compact_move_kernel, dim3(table_ctas + movers), 256, 0, stream, false, c, row_bytes, table_ctas, y);
 }
 
 }  // namespace paged

@@ -6,9 +6,10 @@ namespace path {
 namespace paged {
 
 constexpr int kMaxRows = 1024;
+template <int N>
 struct Rows {
     int n;
-    int row[kMaxRows];
+    int row[N];
 };
 
 }  // namespace paged

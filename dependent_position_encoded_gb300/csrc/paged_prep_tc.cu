@@ -62,74 +62,6 @@ __device__ __forceinline__ void put2(bf *t, int ld, int r, int c, uint32_t v) {
     *reinterpret_cast<uint32_t *>(t + r * ld + c) = v;
 }
 
-// (I + E)^{-1} in fp32 for a strictly lower triangular E (shared, stride 72): the four 16 x 16
-// diagonal blocks by substitution (one column per thread), then X21 = -X22 E21 X11 for the 16-
-// and the 32-blocks; every factor is bounded (products of contractions), so nothing grows.
-// `Y`: 32 x 36 floats of scratch; nt: the 16-row tiles in use (the others are the identity).
-__device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid, int nt) {
-    constexpr int LD = 72, YL = 36;
-    const int b0 = (tid >> 4) << 4, lu = tid & 15;
-    float x[16];
-    if (tid < kC) {
-#pragma unroll
-        for (int l = 0; l < 16; ++l) x[l] = l == lu ? 1.f : 0.f;
-#pragma unroll
-        for (int m = 0; m < 15; ++m)
-#pragma unroll
-            for (int l = m + 1; l < 16; ++l) x[l] = fmaf(-E[(b0 + l) * LD + b0 + m], x[m], x[l]);
-    }
-    __syncthreads();
-    if (tid < kC)
-#pragma unroll
-        for (int l = 0; l < 16; ++l) E[(b0 + l) * LD + tid] = x[l];
-    __syncthreads();
-    if (nt <= 1) return;
-    // level 1: two 32-blocks at o, X21 (16 x 16)
-    for (int pass = 0; pass < 2; ++pass) {
-        float v[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int e = tid + i * kThr, o = 32 * (e >> 8), r = (e >> 4) & 15, c = e & 15;
-            float t = 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-                t = pass == 0 ? fmaf(E[(o + 16 + r) * LD + o + k], E[(o + k) * LD + o + c], t)
-                              : fmaf(E[(o + 16 + r) * LD + o + 16 + k], Y[((o >> 1) + k) * YL + c], t);
-            v[i] = t;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int e = tid + i * kThr, o = 32 * (e >> 8), r = (e >> 4) & 15, c = e & 15;
-            if (pass == 0) Y[((o >> 1) + r) * YL + c] = v[i];
-            else E[(o + 16 + r) * LD + o + c] = -v[i];
-        }
-        __syncthreads();
-    }
-    if (nt <= 2) return;
-    // level 2: X21 (32 x 32)
-    for (int pass = 0; pass < 2; ++pass) {
-        float v[4];
-        const int r = tid >> 3, c0 = (tid & 7) * 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = 0.f;
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-            const float l = pass == 0 ? E[(32 + r) * LD + k] : E[(32 + r) * LD + 32 + k];
-            const float4 q = *reinterpret_cast<const float4 *>(pass == 0 ? E + k * LD + c0 : Y + k * YL + c0);
-            v[0] = fmaf(l, q.x, v[0]);
-            v[1] = fmaf(l, q.y, v[1]);
-            v[2] = fmaf(l, q.z, v[2]);
-            v[3] = fmaf(l, q.w, v[3]);
-        }
-        __syncthreads();
-        float *dst = pass == 0 ? Y + r * YL + c0 : E + (32 + r) * LD + c0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = pass == 0 ? v[i] : -v[i];
-        __syncthreads();
-    }
-}
-
 // Units and items of cached-key work before each sequence (one CTA, both plans).
 __device__ __forceinline__ void make_plans(const Step &a, const TcWs &y, long long *sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -333,7 +265,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
         });
     }
     __syncthreads();
-    unit_lower_inverse(F, reinterpret_cast<float *>(Lh), tid, nt);
+    unit_lower_inverse<LDF>(F, reinterpret_cast<float *>(Lh), tid, nt);
     for (int e = tid; e < kC * kC / 2; e += kThr) {
         const int i = e / 32, j = 2 * (e % 32);
         uint32_t hi, lo;
@@ -865,21 +797,33 @@ __global__ void __launch_bounds__(kThr) tc_gates_kernel(const Step a, const TcWs
 
 // ---------------------------------------------------------------- combine
 // A warp joins `rows` consecutive rows of a key head, each the part of the step's own tokens and
-// those of the cached keys. Lane p holds the maximum and sum of part p (32 at a time). What the
-// rows of a tile share (their sequence and the numbers of their parts) is looked up once.
-template <int D>
+// those of the cached keys, P of them at a time. What the rows of a tile share (their sequence
+// and the numbers of their parts) is looked up once. Bound by the latency of the look-up and of
+// the parts' rows: two or four rows joined together, or sixteen a warp, took longer.
+template <int D, int P>
 __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const TcWs y, int rows) {
     constexpr int E = D / 32;
     const int G = a.c.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
-    const long long r0 = ((long long)blockIdx.x * (kThr / 32) + warp) * rows;
-    const long long r1 = r0 + rows < y.R ? r0 + rows : y.R;
+    const int r0 = (blockIdx.x * (kThr / 32) + warp) * rows, r1 = min(r0 + rows, (int)y.R);  // R <= INT_MAX / 2
     grid_wait();
-    long long known = -1;  // rows below it are of the tile looked up last
-    Seq s{0, 0, 0};
-    long long first = 0, number = 0;
-    int NT = 1, cp = 0;
-    for (long long r = r0; r < r1; ++r) {
-        const int tok = (int)(r / G), hq = h * G + (int)(r - (long long)tok * G);
+    auto load = [&](const float *p, float (&v)[E]) {
+        if (E == 2) {
+            const float2 t = *reinterpret_cast<const float2 *>(p + lane * E);
+            v[0] = t.x;
+            v[1] = t.y;
+        } else {
+            const float4 t = *reinterpret_cast<const float4 *>(p + lane * E);
+            v[0] = t.x;
+            v[1] = t.y;
+            v[E - 2] = t.z;
+            v[E - 1] = t.w;
+        }
+    };
+    // of the row looked up last: rows below `known` are of the same tile
+    long long first = 0;
+    int known = -1, start = 0, number = 0, cp = 0, tile = 128;
+    for (int r = r0; r < r1; ++r) {
+        const int tok = r / G, hq = h * G + (r - tok * G);
         if (r >= known) {
             int lo = 0, hi = a.c.seqs - 1;  // the last sequence that begins at or before the token
             while (lo < hi) {
@@ -887,89 +831,67 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
                 if (__ldg(a.cu + mid) <= tok) lo = mid;
                 else hi = mid - 1;
             }
-            s = seq_of(a, lo);
+            const Seq s = seq_of(a, lo);
             if (tok < s.first || tok >= s.first + s.T) continue;
-            const int rows_all = s.T * G, own = (int)(r - (long long)s.first * G);
-            int tiles, kt;
-            NT = 1;
+            const int rows_all = s.T * G;
+            start = s.first * G;
+            int NT = 1, tiles, kt;
             plan_of(s, G, 1, tiles, kt);
             if (tiles == 0) {
                 NT = 2;
                 plan_of(s, G, 2, tiles, kt);
             }
+            tile = 128 * NT;
             const Plan &p = NT == 1 ? y.plan[0] : y.plan[1];
-            const int tile = own / (128 * NT), it = h * tiles + tile;
+            const int ti = (r - start) / tile, it = h * tiles + ti;
             // the first part's number and how many there are
             first = number = 0;
             if (kt > 0) {
                 const long long per = plan_per(p, a.c.seqs), u = p.units[lo] + (long long)it * kt, c0 = u / per;
                 first = c0 + p.items[lo] + it;
-                number = (u + kt - 1) / per - c0 + 1;
+                number = (int)((u + kt - 1) / per - c0) + 1;
             }
             // short sequences' tiles hold copies of their rows, each a part of its own
             cp = NT == 2 ? 0 : rows_all <= 32 ? 2 : rows_all <= 64 ? 1 : 0;
             number <<= cp;
-            const int end = min(rows_all, (tile + 1) * 128 * NT);
-            known = (long long)s.first * G + end;
+            known = start + min(rows_all, (ti + 1) * tile);
         }
-        const float *so = NT == 1 ? y.so[0] : y.so[1];
-        const float2 *sml = NT == 1 ? y.sml[0] : y.sml[1];
-        const int at = (int)(r - (long long)s.first * G) % (128 * NT), cp_rows = 128 >> cp;
-        auto part_at = [&](long long p) {
-            return (first + (p >> cp)) * (128 * NT) + (p & ((1 << cp) - 1)) * cp_rows + at;
-        };
         const size_t row = (size_t)h * y.R + r;
+        const long long at0 = first * tile + (r - start) % tile;
+        const float *const so = tile == 128 ? y.so[0] : y.so[1];
+        const float2 *const sml = tile == 128 ? y.sml[0] : y.sml[1];
         const float2 z = y.pml[row];
-        float M = z.x, L = z.y, O[E];
-        {
-            const float *o = y.po + row * D + lane * E;
+        float M = z.x, L = z.y, O[E];  // M is never -inf: a row has its own key
+        load(y.po + row * D, O);
+        for (int p0 = 0; p0 < number; p0 += P) {
+            float2 ml[P];
+            float v[P][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) O[e] = o[e];
-        }
-        for (long long p0 = 0; p0 < number; p0 += 32) {
-            const int n = number - p0 < 32 ? (int)(number - p0) : 32;
-            const float2 ml = lane < n ? sml[part_at(p0 + lane)] : make_float2(-INFINITY, 0.f);
-            float m = ml.x;
+            for (int j = 0; j < P; ++j) {
+                const int q = p0 + j;
+                ml[j] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float nm = fmaxf(M, m), f0 = exp2f(M - nm), f = exp2f(ml.x - nm);  // M is never -inf
-            float l = ml.x == -INFINITY ? 0.f : ml.y * f;
+                for (int e = 0; e < E; ++e) v[j][e] = 0.f;
+                if (q < number) {
+                    const size_t at = at0 + (size_t)(q >> cp) * tile + (q & ((1 << cp) - 1)) * (128 >> cp);
+                    ml[j] = sml[at];
+                    load(so + at * D, v[j]);
+                }
+            }
+            float m = M;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            M = nm;
-            L = fmaf(L, f0, l);
+            for (int j = 0; j < P; ++j) m = fmaxf(m, ml[j].x);
+            const float f0 = exp2f(M - m);
+            M = m;
+            L *= f0;
 #pragma unroll
             for (int e = 0; e < E; ++e) O[e] *= f0;
-            // eight parts' rows in flight at a time (an absent part's weight is 0 and its row 0)
-            for (int i0 = 0; i0 < n; i0 += 8) {
-                float v[8][E], w[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int q = i0 + i;
-                    w[i] = __shfl_sync(0xffffffffu, f, q & 31);
-                    if (q >= n) {  // the same for the warp
-                        w[i] = 0.f;
+            for (int j = 0; j < P; ++j) {
+                const float f = exp2f(ml[j].x - m);  // absent keys alone: 0, and their row 0
+                L = fmaf(ml[j].y, f, L);
 #pragma unroll
-                        for (int e = 0; e < E; ++e) v[i][e] = 0.f;
-                        continue;
-                    }
-                    const float *o = so + part_at(p0 + q) * D + lane * E;
-                    if (E == 2) {
-                        const float2 t = *reinterpret_cast<const float2 *>(o);
-                        v[i][0] = t.x;
-                        v[i][1] = t.y;
-                    } else {
-                        const float4 t = *reinterpret_cast<const float4 *>(o);
-                        v[i][0] = t.x;
-                        v[i][1] = t.y;
-                        v[i][E - 2] = t.z;
-                        v[i][E - 1] = t.w;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int e = 0; e < E; ++e) O[e] = fmaf(v[i][e], w[i], O[e]);
+                for (int e = 0; e < E; ++e) O[e] = fmaf(v[j][e], f, O[e]);
             }
         }
         bf *dst = static_cast<bf *>(a.out) + (long long)tok * a.so.tok + hq * a.so.head + lane * E;
@@ -1019,20 +941,19 @@ cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_tc_finish(const Step &a, const TcWs &y, int tile_rows, cudaStream_t stream) {
     const long long cap = (long long)a.c.max_pages << a.c.page_shift;
-    // rows per warp: one while that leaves warps idle, at most eight
-    const long long fill = y.R * a.c.Hkv / (152 * 32);
-    const int rows = fill < 1 ? 1 : fill > 8 ? 8 : (int)fill, per = kThr / 32 * rows;
-    cudaError_t e = launch(tc_combine_kernel<D>, dim3((unsigned)((y.R + per - 1) / per), a.c.Hkv), kThr, 0, stream, false,
-                           a, y, rows);
+    // few rows: a warp for each, its parts eight at a time; many (whose sequences have few parts):
+    // four a warp
+    const bool few = y.R * a.c.Hkv < 8 * 152 * 24;
+    const int rows = few ? 1 : 4, per = kThr / 32 * rows;
+    cudaError_t e = launch(few ? tc_combine_kernel<D, 8> : tc_combine_kernel<D, 2>,
+                           dim3((unsigned)((y.R + per - 1) / per), a.c.Hkv), kThr, 0, stream, false, a, y, rows);
     if (e != cudaSuccess || cap == 0) return e;  // no sequence has room for a token
     if ((long long)a.max_chunk * a.c.G > tile_rows) {
         const size_t bytes = TransformSmem<D>::bytes;
         if ((e = big_smem(tc_transform_kernel<D>, bytes)) != cudaSuccess) return e;
-        // CTAs per key head: one wave over the key heads' long sequences, of which there are at
-        // most N G / tile_rows, and at least 256 positions each
-        const long long longs = (long long)a.N * a.c.G / tile_rows;
-        const long long heads = a.c.Hkv * (longs < a.c.seqs ? (longs < 1 ? 1 : longs) : a.c.seqs);
-        long long parts = (152 + heads - 1) / heads;
+        // one wave for one long sequence, at least 256 positions a CTA (further long sequences take
+        // further waves, the others' CTAs leave at once)
+        long long parts = (152 + a.c.Hkv - 1) / a.c.Hkv;
         if (parts > (cap + 255) / 256) parts = (cap + 255) / 256;
         e = launch(tc_transform_kernel<D>, dim3((unsigned)parts, a.c.Hkv, a.c.seqs), kThr, bytes, stream, false, a, y,
                    tile_rows);
