@@ -139,14 +139,19 @@ constexpr float kRescale = 8.f;  // the running maximum may lag by 2^8 before O 
 template <int NT, int D>
 struct CachedCfg {
     static constexpr uint32_t tile = 128 * D * 2, atom = 128 * 128;
-    static constexpr uint32_t X = 0, M = X + NT * tile, mbytes = NT == 1 ? 2 * D * D * 2 : 0;
+    // The rows' tiles, their high parts and then (keeps_low) their low ones; for NT = 1 at D = 128,
+    // where the update's product takes 64 KB, they lie in tensor memory instead.
+    static constexpr bool rows_in_tmem = NT == 1 && D == 128, low = keeps_low(NT, D);
+    static constexpr uint32_t X = 0, xbytes = rows_in_tmem ? 0 : NT * (low ? 2 : 1) * tile;
+    static constexpr uint32_t M = X + xbytes, mbytes = NT == 1 ? 2 * D * D * 2 : 0;
     // slots of keys and of values: what fits beside; for NT = 1 and D = 64 so that two CTAs share
     // an SM. With NT = 1 a key slot is held until the updated keys have left it.
-    static constexpr int NK = NT == 1 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3);
+    static constexpr int NK = NT == 1 ? (D == 64 ? 2 : 3) : (D == 64 ? 4 : 3);
     static constexpr int NV = NT == 1 ? 2 : (D == 64 ? 4 : 2);
     static constexpr uint32_t K = M + mbytes, V = K + NK * tile, bars = V + NV * tile;
     static constexpr int KF = 0, KE = NK, VF = 2 * NK, VE = VF + NV, XF = VE + NV, XE = XF + 1, SF = XE + 1, PR = SF + 2, FIN = PR + 2,
-                         DF = FIN + 2, DE = DF + NK, TMP = DE + 1, END = TMP + 2, count = END + 2;
+                         DF = FIN + 2, DE = DF + NK, TMP = DE + 1, END = TMP + 2,
+                         XT = END + 2, count = XT + 1;
     static constexpr uint32_t bytes = bars + count * 8 + 16;  // from a 1024-byte boundary
     static constexpr int threads = 384;
     static constexpr int ctas_per_sm = NT == 1 && D == 64 ? 2 : 1;
@@ -155,7 +160,7 @@ struct CachedCfg {
     static constexpr bool split = NT == 2 || D == 64;
     static constexpr int reg_row = NT == 2 ? 200 : 104, reg_update = 72, reg_other = NT == 2 ? 104 : 64;
     // TMEM columns: per row tile S 128 (the weights over it) and O; NT = 1: the update's product
-    static constexpr uint32_t cS = 0, cO = 128, per_tile = 256, cD = 128 + D;
+    static constexpr uint32_t cS = 0, cO = 128, per_tile = 256, cD = 128 + D, cX = 384;
     static constexpr uint32_t cols = NT == 1 && D == 64 ? 256 : 512;
 };
 static_assert(CachedCfg<1, 128>::bytes <= 227 * 1024 && CachedCfg<2, 128>::bytes <= 227 * 1024 &&
@@ -195,7 +200,7 @@ __device__ __forceinline__ bool tile_whole(int pos0, int n, unsigned have, int b
 template <int NT, int D, bool FOX>
 __global__ void __launch_bounds__(CachedCfg<NT, D>::threads, CachedCfg<NT, D>::ctas_per_sm)
 tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap tm_x,
-                 const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_l, const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
     using L = CachedCfg<NT, D>;
     constexpr int NA = D / 64, NK = L::NK, NV = L::NV;
@@ -222,8 +227,8 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
         // four warps: weights written, update's product read; both issuing threads (NT = 1): rows' tile
         // free, keys read by their products; both row tiles (NT = 2): keys and values read
         for (int i = 0; i < L::count; ++i) {
-            const bool four = (i >= L::PR && i < L::FIN) || i == L::DE;
-            const bool both = NT == 1 ? i == L::XE || (i >= L::DF && i < L::DE)
+            const bool four = (i >= L::PR && i < L::FIN) || i == L::DE || i == L::XT;
+            const bool both = NT == 1 ? (i == L::XE && !L::rows_in_tmem) || (i >= L::DF && i < L::DE)
                                       : (i >= L::KE && i < L::VF) || (i >= L::VE && i < L::XF);
             mbar_init(bar(i), four ? 4u : both ? 2u : 1u);
         }
@@ -265,12 +270,16 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                     if (seg > 0 && !(ok = wait.warp(bar(L::XE), (seg - 1) & 1))) break;
                     if (lane == 0) {
                         const int xr = t.s.first * G + 128 * NT * t.tile;
-                        const int nx = second(t) ? 8 : 4, mask = (128 * NT >> copies(t)) - 1;  // boxes of 32 rows
-                        mbar_arrive_expect_tx(bar(L::XF), nx * (L::tile / 4) + L::mbytes);
-                        for (int i = 0; i < nx; ++i)
-                            for (int x = 0; x < NA; ++x)
-                                tma_load_3d(base + L::X + (i >> 2) * L::tile + x * L::atom + (i & 3) * 32 * 128, &tm_x,
-                                            bar(L::XF), 64 * x, xr + ((32 * i) & mask), t.h);
+                        // boxes of 32 rows
+                        const int nx = L::rows_in_tmem ? 0 : second(t) ? 8 : 4, parts = L::low ? 2 : 1;
+                        const int mask = (128 * NT >> copies(t)) - 1;
+                        mbar_arrive_expect_tx(bar(L::XF), nx * parts * (L::tile / 4) + L::mbytes);
+                        for (int part = 0; part < parts; ++part)
+                            for (int i = 0; i < nx; ++i)
+                                for (int x = 0; x < NA; ++x)
+                                    tma_load_3d(base + L::X + (part * NT + (i >> 2)) * L::tile + x * L::atom +
+                                                    (i & 3) * 32 * 128,
+                                                part ? &tm_l : &tm_x, bar(L::XF), 64 * x, xr + ((32 * i) & mask), t.h);
                         if (NT == 1)
                             for (int p = 0; p < 2; ++p)
                                 for (int x = 0; x < NA; ++x)
@@ -349,9 +358,17 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             auto issue_s = [&](int q) {
                 const uint64_t xd = x_desc + q * kTile, kd = k_desc + k.slot * kTile;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16(tmem + L::per_tile * q + L::cS, xd + (kk >> 2) * kAtom + 2 * (kk & 3),
-                              kd + (kk >> 2) * kAtom + 2 * (kk & 3), ID_S, kk > 0);
+                for (int part = 0; part < (L::low ? 2 : 1); ++part)  // the rows' high and low parts
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t b = kd + (kk >> 2) * kAtom + 2 * (kk & 3);
+                        if (L::rows_in_tmem)
+                            umma_tA(tmem + L::cS, tmem + L::cX + part * (D / 2) + 8 * kk, b, ID_S, part > 0 || kk > 0);
+                        else
+                            umma_bf16(tmem + L::per_tile * q + L::cS,
+                                      xd + part * NT * kTile + (kk >> 2) * kAtom + 2 * (kk & 3), b, ID_S,
+                                      part > 0 || kk > 0);
+                    }
                 umma_commit(bar(L::SF + q));
             };
             auto issue_pv = [&](int q, bool first) {
@@ -365,14 +382,15 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             // handed back by the softmax's warps, which learn of the products' ends anyway.)
             auto after_s = [&](bool last) {
                 if (NT == 1) umma_commit(bar(L::DF + k.slot));
-                if (last) umma_commit(bar(L::XE));
+                if (last && !L::rows_in_tmem) umma_commit(bar(L::XE));
                 k.next();
             };
             for (long long at = u_begin; ok && at < u_end; ++seg) {
                 const Stretch t = stretch_at(a, plan, NT, at, u_end);
                 at += t.steps;
                 const bool two = second(t);
-                if (!(ok = wait(bar(L::XF), seg & 1)) || !(ok = wait(bar(L::KF + k.slot), k.phase))) break;
+                if (!(ok = wait(bar(L::rows_in_tmem ? L::XT : L::XF), seg & 1))) break;
+                if (!(ok = wait(bar(L::KF + k.slot), k.phase))) break;
                 tc_fence_after();
                 issue_s(0);
                 if (two) issue_s(1);
@@ -534,6 +552,30 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             const int hq = t.h * G + (live ? (row0 + rw) % G : 0);
             const float gq =
                 FOX && live ? y.gq[(size_t)t.h * y.R + (size_t)t.s.first * G + row0 + rw] * kLog2e : 0.f;
+            if (L::rows_in_tmem) {
+                // the row's two parts (the last stretch's products have ended)
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int c = 0; c < D / 2; c += 32) {  // 32 columns of two elements
+                        const uint4 *src = reinterpret_cast<const uint4 *>(
+                            (part ? y.ql : y.qt) +
+                            ((size_t)t.h * y.R + (size_t)t.s.first * G + row0 + (live ? rw : 0)) * D + 2 * c);
+                        uint32_t u[32];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const uint4 v = live ? src[q] : make_uint4(0u, 0u, 0u, 0u);
+                            u[4 * q] = v.x;
+                            u[4 * q + 1] = v.y;
+                            u[4 * q + 2] = v.z;
+                            u[4 * q + 3] = v.w;
+                        }
+                        tmem_st32(tm + L::cX + part * (D / 2) + c, u);
+                    }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive_warp(bar(L::XT));
+            }
             float m_run = -INFINITY, l_run = 0.f;
             int kid1, vid1;  // the pages of the next tile's boxes
             auto look_up = [&](int pos0) {
@@ -1003,6 +1045,7 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
     } else if (warp < 8) {
         // ============================================================ the state's bf16 copy
         bool ok = true;
+        const bool low = keeps_low(rows_all <= 128 ? 1 : 2, D);  // the state's second part
         uint8_t *const xs = sm + L::X;
         auto put = [&](int c, const float *x, bool take) {  // 32 columns from c
 #pragma unroll
@@ -1019,14 +1062,15 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
             float x[32];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint4 u = live ? *reinterpret_cast<const uint4 *>(y.qt + row * D + c + 8 * q)
-                                     : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+                const uint4 u = live ? *reinterpret_cast<const uint4 *>(y.qt + row * D + c + 8 * q) : none;
+                const uint4 z = live && low ? *reinterpret_cast<const uint4 *>(y.ql + row * D + c + 8 * q) : none;
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w}, wl[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 f = unpack_bf16x2(w[e]);
-                    x[8 * q + 2 * e] = f.x;
-                    x[8 * q + 2 * e + 1] = f.y;
+                    const float2 f = unpack_bf16x2(w[e]), g = unpack_bf16x2(wl[e]);
+                    x[8 * q + 2 * e] = f.x + g.x;
+                    x[8 * q + 2 * e + 1] = f.y + g.y;
                 }
             }
             tst32(tmem + lane_off + L::cX + c, x);
@@ -1058,12 +1102,15 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
                 float x[32];
                 tld32(tmem + lane_off + L::cX + c, x);
                 if (live) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(y.qt + row * D + c);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        dst[q] = make_uint4(pack_bf16x2(x[8 * q], x[8 * q + 1]), pack_bf16x2(x[8 * q + 2], x[8 * q + 3]),
-                                            pack_bf16x2(x[8 * q + 4], x[8 * q + 5]),
-                                            pack_bf16x2(x[8 * q + 6], x[8 * q + 7]));
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) split2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], lo[e]);
+                        const size_t at = row * D + c + 8 * q;
+                        *reinterpret_cast<uint4 *>(y.qt + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        if (low) *reinterpret_cast<uint4 *>(y.ql + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
                 }
             }
         }
@@ -1096,8 +1143,8 @@ cudaError_t big_smem(K kern, size_t bytes) {
 
 template <int NT, int D, bool FOX>
 cudaError_t launch_cached(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream) {
-    CUtensorMap tx, tm, tk, tv;
-    if (!make_map(&tx, y.qt, D, y.R, a.c.Hkv, 32) ||
+    CUtensorMap tx, tl, tm, tk, tv;
+    if (!make_map(&tx, y.qt, D, y.R, a.c.Hkv, 32) || !make_map(&tl, y.ql, D, y.R, a.c.Hkv, 32) ||
         !make_map(&tm, y.mt, D, D, (long long)a.c.seqs * a.c.Hkv * 2, D) ||
         !make_map(&tk, a.c.k_pages, D, a.c.page, (long long)a.c.nk * a.c.Hkv, a.c.page < 128 ? a.c.page : 128) ||
         !make_map(&tv, a.c.v_pages, D, a.c.page, (long long)a.c.nv * a.c.Hkv, a.c.page < 128 ? a.c.page : 128))
@@ -1106,7 +1153,8 @@ cudaError_t launch_cached(const Step &a, const TcWs &y, uint64_t limit_ns, cudaS
     auto kern = tc_cached_kernel<NT, D, FOX>;
     const cudaError_t e = big_smem(kern, L::bytes);
     if (e != cudaSuccess) return e;
-    return launch(kern, dim3(y.plan[NT - 1].ctas), L::threads, L::bytes, stream, false, a, y, tx, tm, tk, tv, limit_ns);
+    return launch(kern, dim3(y.plan[NT - 1].ctas), L::threads, L::bytes, stream, false, a, y, tx, tl, tm, tk, tv,
+                  limit_ns);
 }
 
 template <int D, bool FOX>
@@ -1150,7 +1198,7 @@ cudaError_t launch_all(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStre
 
 struct TcLayout {
     int ctas[2];
-    size_t qt, po, pml, so[2], sml[2], units[2], items[2], gq, gt, gtot, mt, kh, kl, vb, ch, cl, gp, total;
+    size_t qt, ql, po, pml, so[2], sml[2], units[2], items[2], gq, gt, gtot, mt, kh, kl, vb, ch, cl, gp, total;
 };
 
 // The regions depend on the sizes in ways that do not fall as the step grows, so that a workspace
@@ -1165,6 +1213,7 @@ TcLayout tc_layout(const Cache &c, int N, int max_chunk, int d, bool fox) {
         return at;
     };
     y.qt = take(rows * d * 2);
+    y.ql = take(rows * d * 2);
     y.po = take(rows * d * 4);
     y.pml = take(rows * 8);
     for (int p = 0; p < 2; ++p) {
@@ -1208,6 +1257,7 @@ cudaError_t launch_tc(const Step &a, int d, void *ws, uint64_t limit_ns, cudaStr
     auto f32 = [&](size_t off) { return reinterpret_cast<float *>(w + off); };
     TcWs y;
     y.qt = b16(f.qt);
+    y.ql = b16(f.ql);
     y.mt = b16(f.mt);
     y.kh = b16(f.kh);
     y.kl = b16(f.kl);

@@ -7,8 +7,9 @@
 // Precision. The inputs are bf16; what is computed from them (A, U, Lq A, R A^T, P_b) enters
 // further products as a high and a low bf16 part (16 bits of significand, see split2), so
 // carried keys and transitions are exact to 2^-16 before the cache rounds the keys to bf16.
-// The factor A = (I + D N)^{-1} D is solved in fp32. Only the carried queries, the softmax
-// weights and, in the scan over a chunk's blocks, keys and transitions are rounded to bf16.
+// The factor A = (I + D N)^{-1} D is solved in fp32. Rounded to bf16 are the softmax weights,
+// in the scan over a chunk's blocks keys and transitions, and the carried queries (keeps_low says
+// where these have a second part).
 #include "paged_tc.cuh"
 
 namespace path {
@@ -156,7 +157,10 @@ __device__ __forceinline__ void prep_single(const Step &a, const TcWs &y, const 
         const size_t r = (size_t)h * y.R + (size_t)s.first * G + g;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            y.qt[r * D + lane * E + e] = __float2bfloat16_rn(fmaf(-beta * wq, w[e], q[e]) * a.scale_log2);
+            const float x = fmaf(-beta * wq, w[e], q[e]) * a.scale_log2;
+            const bf xh = __float2bfloat16_rn(x);
+            y.qt[r * D + lane * E + e] = xh;
+            if (keeps_low(G <= 128 ? 1 : 2, D)) y.ql[r * D + lane * E + e] = __float2bfloat16_rn(x - __bfloat162float(xh));
             y.po[r * D + lane * E + e] = __bfloat162float(vp[e]);
         }
         if (lane == 0) {
@@ -433,8 +437,10 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
                 if (i >= rows) return;
                 const float2 q2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(Q + i * LDD + j));
                 // scaled here once, so that the attention's logits need no factor
-                *reinterpret_cast<uint32_t *>(y.qt + row_of(i) * D + j) =
-                    pack_bf16x2((q2.x - p) * a.scale_log2, (q2.y - q) * a.scale_log2);
+                uint32_t hi, lo;
+                split2((q2.x - p) * a.scale_log2, (q2.y - q) * a.scale_log2, hi, lo);
+                *reinterpret_cast<uint32_t *>(y.qt + row_of(i) * D + j) = hi;
+                if (keeps_low(s.T * G <= 128 ? 1 : 2, D)) *reinterpret_cast<uint32_t *>(y.ql + row_of(i) * D + j) = lo;
             });
         }
         {  // the block's logits Q K^T - (Lq A) R^T

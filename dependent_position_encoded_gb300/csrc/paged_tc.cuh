@@ -22,8 +22,17 @@ struct Plan {
     int ctas;
 };
 
+// Whether a carried query enters the cached keys' logits as a high and a low bf16 part. Rounded
+// once to bf16 it adds as much error to the output as the weights' and the output's own rounding
+// do: 2.9e-3 of the norm against 2.3e-3 with the second part and 1.7e-3 for the output's rounding
+// alone. The second product costs 4 to 6% where the cache's bytes bound the pass (NT = 1: 207 ->
+// 215 us for 32 sequences of 8192 at D = 64) and little beside the exponentials at D = 64; at
+// D = 128 with several row tiles shared memory has no room for the parts.
+__host__ __device__ constexpr bool keeps_low(int NT, int D) { return NT == 1 || D == 64; }
+
 // Workspace of the bf16 block path, behind the 256-byte status header:
 //   qt   (Hkv, R, D) bf16       queries carried to the chunk's start, times scale log2(e)
+//   ql   (Hkv, R, D) bf16       what that rounding left, where keeps_low
 //   po   (Hkv, R, D) fp32, pml (Hkv, R) fp32 pairs: the step's own tokens' unnormalised softmax
 //        part and its (maximum in log2 units, sum)
 //   so, sml per NT: (ctas + items, 128 NT, D) fp32 and (.., 128 NT) pairs, the parts of the
@@ -39,7 +48,7 @@ struct Plan {
 //   ch, cl (slots, Hkv, 64, D) bf16 high and low parts of the new keys at their group's end
 //   gp   (groups, Hkv, 2, D, D) bf16 high and low parts of the groups' products less I
 struct TcWs {
-    __nv_bfloat16 *qt, *mt, *kh, *kl, *vb, *ch, *cl, *gp;
+    __nv_bfloat16 *qt, *ql, *mt, *kh, *kl, *vb, *ch, *cl, *gp;
     float *po;
     float2 *pml;
     float *so[2];
