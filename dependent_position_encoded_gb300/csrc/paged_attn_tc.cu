@@ -8,6 +8,8 @@
 // the pages, for whatever number of new tokens. Only the keys' own update needs the chunk's
 // product, K <- K + K (P - I) (review "거리에서 경로로, PaTH Attention" §9; technical summary
 // "技術要約: PaTH Attention" §3 "推論").
+#include <algorithm>
+
 #include "paged_tc.cuh"
 
 namespace path {
@@ -284,7 +286,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                             for (int p = 0; p < 2; ++p)
                                 for (int x = 0; x < NA; ++x)
                                     tma_load_3d(base + L::M + (uint32_t)(p * NA + x) * D * 128, &tm_m, bar(L::XF),
-                                                64 * x, 0, (t.b * a.c.Hkv + t.h) * 2 + p);
+                                                64 * x, 0, ((int)mt_row(a, t.s, t.b) * a.c.Hkv + t.h) * 2 + p);
                     }
                 }
                 // lane i < nbox: the page of box i of a key tile, -1 past the end or where it is bad;
@@ -1145,7 +1147,7 @@ template <int NT, int D, bool FOX>
 cudaError_t launch_cached(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream) {
     CUtensorMap tx, tl, tm, tk, tv;
     if (!make_map(&tx, y.qt, D, y.R, a.c.Hkv, 32) || !make_map(&tl, y.ql, D, y.R, a.c.Hkv, 32) ||
-        !make_map(&tm, y.mt, D, D, (long long)a.c.seqs * a.c.Hkv * 2, D) ||
+        !make_map(&tm, y.mt, D, D, (long long)std::min(a.c.seqs, a.N) * a.c.Hkv * 2, D) ||
         !make_map(&tk, a.c.k_pages, D, a.c.page, (long long)a.c.nk * a.c.Hkv, a.c.page < 128 ? a.c.page : 128) ||
         !make_map(&tv, a.c.v_pages, D, a.c.page, (long long)a.c.nv * a.c.Hkv, a.c.page < 128 ? a.c.page : 128))
         return cudaErrorInvalidValue;
@@ -1221,7 +1223,8 @@ TcLayout tc_layout(const Cache &c, int N, int max_chunk, int d, bool fox) {
         y.ctas[p] = 152 * (p == 0 && d == 64 ? CachedCfg<1, 64>::ctas_per_sm : 1);
         const bool used = p == 0 || (long long)max_chunk * c.G > 128;
         const size_t tile = 128 * (p + 1);
-        const size_t parts = used ? y.ctas[p] + (size_t)tile_slots(N, c.G, c.seqs, (int)tile) * c.Hkv : 0;
+        const size_t parts =
+            used ? y.ctas[p] + (size_t)tile_slots(N, c.G, std::min(c.seqs, N), (int)tile) * c.Hkv : 0;
         y.so[p] = take(parts * tile * d * 4);
         y.sml[p] = take(parts * tile * 8);
         y.units[p] = take(((size_t)c.seqs + 1) * 8);
@@ -1230,15 +1233,15 @@ TcLayout tc_layout(const Cache &c, int N, int max_chunk, int d, bool fox) {
     y.gq = take(fox ? rows * 4 : 0);
     y.gt = take(fox ? slots * c.Hq * kC * 4 : 0);
     y.gtot = take(fox ? slots * c.Hq * 8 : 0);
-    y.mt = take((size_t)c.seqs * c.Hkv * 2 * d * d * 2);
+    y.mt = take((size_t)std::min(c.seqs, N) * c.Hkv * 2 * d * d * 2);
     const bool blocks = max_chunk > kC;
     y.kh = take(blocks ? slots * c.Hkv * (kC + d) * d * 2 : 0);
     y.kl = take(blocks ? slots * c.Hkv * (kC + d) * d * 2 : 0);
     y.vb = take(blocks ? slots * c.Hkv * kC * d * 2 : 0);
-    const bool groups = max_chunk > kC * 8;
+    const bool groups = max_chunk > kC * 8;  // kGroup blocks
     y.ch = take(groups ? slots * c.Hkv * kC * d * 2 : 0);
     y.cl = take(groups ? slots * c.Hkv * kC * d * 2 : 0);
-    y.gp = take(groups ? (slots / 8 + c.seqs + 1) * c.Hkv * 2 * d * d * 2 : 0);
+    y.gp = take(groups ? (slots / 8 + c.seqs) * c.Hkv * 2 * d * d * 2 : 0);
     y.total = off;
     return y;
 }

@@ -63,14 +63,35 @@ __device__ __forceinline__ void put2(bf *t, int ld, int r, int c, uint32_t v) {
     *reinterpret_cast<uint32_t *>(t + r * ld + c) = v;
 }
 
-// Units and items of cached-key work before each sequence (one CTA, both plans).
+// Units and items of cached-key work before each sequence (one CTA, both plans). The parts'
+// buffers hold what sequences without common tokens can need, so one that begins before an
+// earlier one's begin or end (cu_tokens falls somewhere, which the falling sequence reports) gets
+// no work: with m the largest cu_tokens so far, a sequence counts where cu_tokens = m.
 __device__ __forceinline__ void make_plans(const Step &a, const TcWs &y, long long *sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int *const tops = reinterpret_cast<int *>(sums + kThr / 32);
     long long run[4] = {0, 0, 0, 0};
+    int top = 0;
     for (int base = 0; base <= a.c.seqs; base += kThr) {
         const int b = base + tid;
+        const int begin = b < a.c.seqs ? __ldg(a.cu + b) : 0;
+        int m = begin;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, m, o);
+            if (lane >= o) m = max(m, t);
+        }
+        __syncthreads();
+        if (lane == 31) tops[warp] = m;
+        __syncthreads();
+        m = max(m, top);
+#pragma unroll
+        for (int i = 0; i < kThr / 32; ++i) {
+            if (i < warp) m = max(m, tops[i]);
+            top = max(top, tops[i]);
+        }
         long long v[4] = {0, 0, 0, 0};
-        if (b < a.c.seqs) {
+        if (b < a.c.seqs && begin == m) {
             const Seq s = seq_of(a, b);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
@@ -175,7 +196,7 @@ __device__ __forceinline__ void prep_single(const Step &a, const TcWs &y, const 
     }
     if (s.n == 0) return;  // no cached key takes the product
     __syncthreads();
-    bf *const mh = y.mt + ((size_t)b * a.c.Hkv + h) * 2 * D * D, *const ml = mh + (size_t)D * D;
+    bf *const mh = y.mt + (mt_row(a, s, b) * a.c.Hkv + h) * 2 * D * D, *const ml = mh + (size_t)D * D;
     for (int e = tid; e < D * D / 8; e += kThr) {
         const int i = e / (D / 8), j = e % (D / 8) * 8;
         const float f = -beta * buf[i];
@@ -310,7 +331,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
     __syncthreads();
     // P_b - I = -U^T W (D x D): to the chunk's product or the block's factors
     if (lead) {
-        bf *const mh = single ? y.mt + ((size_t)b * a.c.Hkv + h) * 2 * D * D : y.kh + (bh * (kC + D) + kC) * D;
+        bf *const mh = single ? y.mt + (mt_row(a, s, b) * a.c.Hkv + h) * 2 * D * D : y.kh + (bh * (kC + D) + kC) * D;
         bf *const ml = single ? mh + (size_t)D * D : y.kl + (bh * (kC + D) + kC) * D;
 #pragma unroll 1
         for (int t = warp; t < D / 16 * (D / 32); t += kThr / 32) {
@@ -532,36 +553,52 @@ struct CarrySmem {
 // Groups of all sequences share one numbering: group i of a sequence whose first block is slot
 // f is number f / kGroup + b + i.
 __device__ __forceinline__ int group_of(const Seq &s, int b, int i) { return slot_of(s, b, 0) / kGroup + b + i; }
+// The (sequence, group) of a number, as block_of.
+__device__ __forceinline__ bool group_at(const Step &a, int number, int &b, int &i, Seq &s) {
+    int lo = 0, hi = a.c.seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((__ldg(a.cu + mid) / kC + mid) / kGroup + mid <= number) lo = mid;
+        else hi = mid - 1;
+    }
+    b = lo;
+    s = seq_of(a, b);
+    i = number - group_of(s, b, 0);
+    return i >= 0 && i * kGroup * kC < s.T;
+}
 
 __device__ __forceinline__ void cp16(void *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// PASS 1: within the group; PASS 2: over the groups behind. grid.x: (seqs x groups x D / 64)
-// row tiles of the identity, then the slots. A chunk of one group is done after pass 1.
+// PASS 1: within the group; PASS 2: over the groups behind. grid.x: D / 64 row tiles of the
+// identity for each of `idents` groups (pass 2: sequences), then the slots. A chunk of one group
+// is done after pass 1.
 template <int D, int PASS>
-__global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs y, int max_groups) {
+__global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs y, int idents) {
     using S = CarrySmem<D>;
     constexpr int LDD = S::LDD, NT = D / 8, PER = D / 8;
     extern __shared__ __align__(16) uint8_t smem[];
     bf *const Mh = reinterpret_cast<bf *>(smem + S::Mh), *const Ml = reinterpret_cast<bf *>(smem + S::Ml),
        *const Yh = reinterpret_cast<bf *>(smem + S::Yh), *const Yl = reinterpret_cast<bf *>(smem + S::Yl);
     const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, m0 = 16 * warp;
-    const int per_seq = (PASS == 1 ? max_groups : 1) * (D / 64), idents = a.c.seqs * per_seq;
-    const bool ident = (int)blockIdx.x < idents;
+    const bool ident = (int)blockIdx.x < idents * (D / 64);
     int b, c = 0, tile = 0, grp = 0, slot = 0;
     Seq s;
     grid_wait();
     float acc[NT][4];
     zero_acc(acc);
     if (ident) {
-        b = blockIdx.x / per_seq;
         tile = blockIdx.x % (D / 64);
-        grp = blockIdx.x % per_seq / (D / 64);
-        s = seq_of(a, b);
+        if (PASS == 1) {
+            if (!group_at(a, blockIdx.x / (D / 64), b, grp, s)) return;
+        } else {
+            b = blockIdx.x / (D / 64);
+            s = seq_of(a, b);
+        }
     } else {
-        slot = blockIdx.x - idents;
+        slot = blockIdx.x - idents * (D / 64);
         if (!block_of(a, slot, b, c, s)) return;
         grp = c / kGroup;
     }
@@ -615,7 +652,7 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
     }
     const bool done = PASS == 2 || ng == 1;
     if (ident) {
-        bf *const mh = done ? y.mt + ((size_t)b * a.c.Hkv + h) * 2 * D * D
+        bf *const mh = done ? y.mt + (mt_row(a, s, b) * a.c.Hkv + h) * 2 * D * D
                             : y.gp + ((size_t)group_of(s, b, grp) * a.c.Hkv + h) * 2 * D * D;
         bf *const ml = mh + (size_t)D * D;
         each_pair(acc, 64 * tile + m0, 0, [&](int i, int j, float p, float q) {
@@ -684,7 +721,7 @@ __global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, con
     const int strips = (s.n + 31) / 32, per = (strips + (int)gridDim.x - 1) / (int)gridDim.x;
     const int first = (int)blockIdx.x * per, last = min(strips, first + per);
     if ((long long)s.T * a.c.G <= tile_rows || first >= last) return;
-    const bf *const m = y.mt + ((size_t)b * a.c.Hkv + h) * 2 * D * D;
+    const bf *const m = y.mt + (mt_row(a, s, b) * a.c.Hkv + h) * 2 * D * D;
 #pragma unroll 4
     for (int e = tid; e < D * PER; e += kThr) {
         const int r = e / PER, q = e % PER * 8;
@@ -850,9 +887,9 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
             tile = 128 * NT;
             const Plan &p = NT == 1 ? y.plan[0] : y.plan[1];
             const int ti = (r - start) / tile, it = h * tiles + ti;
-            // the first part's number and how many there are
+            // the first part's number and how many there are (none where the sequence has no work)
             first = number = 0;
-            if (kt > 0) {
+            if (kt > 0 && p.items[lo + 1] > p.items[lo]) {
                 const long long per = plan_per(p, a.c.seqs), u = p.units[lo] + (long long)it * kt, c0 = u / per;
                 first = c0 + p.items[lo] + it;
                 number = (int)((u + kt - 1) / per - c0) + 1;
@@ -933,12 +970,12 @@ cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
     if ((e = big_smem(tc_carry_kernel<D, 1>, CarrySmem<D>::bytes)) != cudaSuccess ||
         (e = big_smem(tc_carry_kernel<D, 2>, CarrySmem<D>::bytes)) != cudaSuccess)
         return e;
-    const int slots = slots_of(a.N, a.c.seqs), groups = (a.max_chunk + kC * kGroup - 1) / (kC * kGroup);
-    e = launch(tc_carry_kernel<D, 1>, dim3(a.c.seqs * groups * (D / 64) + slots, a.c.Hkv), 128, CarrySmem<D>::bytes,
-               stream, false, a, y, groups);
-    if (e == cudaSuccess && groups > 1)
+    const int slots = slots_of(a.N, a.c.seqs), groups = slots / kGroup + a.c.seqs;
+    e = launch(tc_carry_kernel<D, 1>, dim3(groups * (D / 64) + slots, a.c.Hkv), 128, CarrySmem<D>::bytes, stream, false,
+               a, y, groups);
+    if (e == cudaSuccess && a.max_chunk > kC * kGroup)
         e = launch(tc_carry_kernel<D, 2>, dim3(a.c.seqs * (D / 64) + slots, a.c.Hkv), 128, CarrySmem<D>::bytes, stream,
-                   false, a, y, groups);
+                   false, a, y, a.c.seqs);
     return e;
 }
 

@@ -40,7 +40,7 @@ __host__ __device__ constexpr bool keeps_low(int NT, int D) { return NT == 1 || 
 //   gq   (Hkv, R) fp32          PaTH-FoX: gate sum of a row from the chunk's start
 //   gt   (slots, Hq, 64) fp32   PaTH-FoX: gate sum behind a key to its block's end
 //   gtot (slots, Hq) fp64       PaTH-FoX: gate sum of a block
-//   mt   (seqs, Hkv, 2, D, D)   bf16 high and low parts of (H_1 ... H_T) - I of the whole chunk
+//   mt   (min(seqs, N), Hkv, 2, D, D) bf16 high and low parts of (H_1 ... H_T) - I of the chunk
 // and, where a chunk may have several blocks of 64 tokens:
 //   kh, kl (slots, Hkv, 64 + D, D) bf16 high and low parts of [k~; P_b - I]
 //   vb   (slots, Hkv, 64, D) bf16 the block's values, zero past its tokens
@@ -58,6 +58,11 @@ struct TcWs {
     double *gtot;
     long long R;
 };
+
+// A sequence's row of mt: with more sequences than tokens (most of them idle) its first token.
+__device__ __forceinline__ size_t mt_row(const Step &a, const Seq &s, int b) {
+    return a.N < a.c.seqs ? s.first : b;
+}
 
 // Row tiles and key tiles of a sequence in the plan of NT (0 where it goes with the other).
 __device__ __forceinline__ void plan_of(const Seq &s, int G, int NT, int &tiles, int &ktiles) {

@@ -363,8 +363,10 @@ size_t path_paged_workspace_bytes(const path_paged_cache *cache, int num_tokens,
  * The same as T calls of one token each but for the roundings of the cached keys between them.
  *   q, out : (num_tokens, Hq, d) dtype; k, v, w : (num_tokens, Hkv, d) dtype; beta :
  *            (num_tokens, Hkv) fp32; strides NULL for packed tensors
- *   cu_tokens : (seqs + 1) int32 on the device, from 0, not falling; tokens at or past
- *            cu_tokens[seqs] are not read and their out rows are left as they are
+ *   cu_tokens : (seqs + 1) int32 on the device, from 0, not falling (where it falls,
+ *            PATH_ERR_CACHE, and what the step's own sequences hold and give is then undefined);
+ *            tokens at or past cu_tokens[seqs] are not read and their out rows are left as they
+ *            are
  *   max_chunk : the most new tokens of a sequence, 1 .. num_tokens (a sequence with more is
  *            left out, with PATH_ERR_CACHE)
  *   ws     : path_paged_workspace_bytes(cache, num_tokens, max_chunk) bytes

@@ -248,6 +248,56 @@ def test_pages_outside_the_pool_are_absent(lib, dtype, chunks):
         assert torch.equal(x["k_pages"][i].nan_to_num(nan=7.0), before["k_pages"][i].nan_to_num(nan=7.0))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fox", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,d,new", [
+    (3, 1, 64, {0: 1, 17: 1, 39: 1}),       # single tokens
+    (8, 1, 128, {3: 2, 38: 20}),            # more rows than a tile of 128: the key update's own pass
+    (2, 2, 64, {20: 1}),                    # one token in all
+])
+def test_more_sequences_than_tokens(lib, dtype, fox, Hq, Hkv, d, new):
+    """Most sequences idle, so that the step has fewer tokens than the cache sequences."""
+    lens = [(37 * s) % 300 for s in range(40)]
+    x = pc.make(lens, [new.get(s, 0) for s in range(40)], Hq, Hkv, d, 16, dtype, fox, seed=17)
+    run(lib, x)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fox", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,chunks,cu", [
+    (8, 2, [100, 0, 100, 100], [0, 200, 100, 300, 300]),
+    (2, 2, [1] * 6, [0, 5, 1, 6, 2, 7, 3]),
+    (4, 2, [700, 20], [300, 0, 720]),
+    (2, 1, [64] * 12, [0, 768] * 6 + [768]),  # the same tokens for every other sequence
+])
+def test_token_ranges_that_fall(lib, dtype, fox, Hq, Hkv, chunks, cu):
+    """cu_tokens that falls is reported, only the step's own sequences' pages and rows change,
+    and the next step is right."""
+    lens = [(130 * s) % 400 for s in range(len(chunks))]
+    N, most = max(cu), max(max(chunks), max(b - a for a, b in zip(cu, cu[1:])))
+    width = max(-(-(n + most) // 16) for n in lens)
+    x = pc.make(lens, chunks, Hq, Hkv, 64, 16, dtype, fox, seed=18, tail=N + 5 - sum(chunks), width=width)
+    cache = pc.cache_of(lib, x)
+    before, tables = pc.snapshot(x), [x[n].clone() for n in ("k_table", "v_table", "lens")]
+    ws = lib.new_paged_workspace(cache, x["q"].shape[0], most, Hq=Hq)
+    args = [x[n] for n in ("q", "k", "v", "w", "beta")] + ([x["log_f"]] if fox else [])
+    call = lib.path_fox_paged_extend if fox else lib.path_paged_extend
+    out = torch.full_like(x["q"], 3.0)
+    call(*args, torch.tensor(cu, dtype=torch.int32, device="cuda"), cache, most, out=out, workspace=ws)
+    assert lib.path_check_workspace(ws) == lib.ERR_CACHE
+    assert (out[N:] == 3).all()
+    for n, t in (("k_pages", "k_table"), ("v_pages", "v_table"), ("g_pages", "k_table")):
+        if x[n] is not None:
+            spare = torch.ones(x[n].shape[0], dtype=torch.bool, device="cuda")
+            spare[x[t][x[t] >= 0].long()] = False
+            assert torch.equal(x[n][spare].nan_to_num(nan=7.0), before[n][spare].nan_to_num(nan=7.0))
+            x[n].copy_(before[n])
+    assert all(torch.equal(a, x[n]) for a, n in zip(tables, ("k_table", "v_table", "lens")))
+    got = pc.step(lib, x, cache, workspace=ws)
+    assert lib.path_check_workspace(ws) == lib.OK
+    pc.check(x, before, got)
+
+
 def test_a_workspace_for_chunks_serves_smaller_steps(lib):
     x = pc.make([200, 100], [300, 20], 2, 2, 64, 16, BF, True, seed=13)
     cache = pc.cache_of(lib, x)
