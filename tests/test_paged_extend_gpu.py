@@ -63,6 +63,72 @@ def test_other_scales(lib, chunks):
         run(lib, x, scale=scale)
 
 
+@pytest.mark.parametrize("chunks", [[1, 1], [150, 40]])
+@pytest.mark.parametrize("G", [1, 3])
+def test_scales_that_turn_the_order(lib, chunks, G):
+    """Logits of unit size, as the bar of bf16 supposes, and none."""
+    for scale in (0.0, -0.125):
+        x = pc.make([90, 340], chunks, 2 * G, 2, 64, 64, BF, G == 3, seed=4)
+        run(lib, x, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fox", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,d,page,chunks", [
+    (5, 1, 128, 256, [1, 9, 40]),
+    (16, 2, 64, 256, [1, 1, 1]),
+    (128, 1, 128, 16, [1, 0, 1]),   # a tile's rows are one token's
+    (256, 1, 64, 32, [1, 1, 0]),    # more rows for one token than a tile has
+    (200, 2, 128, 64, [2, 1, 70]),
+])
+def test_many_heads_to_a_key(lib, dtype, fox, Hq, Hkv, d, page, chunks):
+    x = pc.make([700, 0, 255], chunks, Hq, Hkv, d, page, dtype, fox, seed=19)
+    run(lib, x)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("chunks", [[1, 1], [70, 3]])
+def test_inputs_broadcast_over_heads_and_nan_behind(lib, dtype, chunks):
+    """One transition and gate for all heads, given with a stride of 0; NaN in the rows behind
+    the last sequence."""
+    x = pc.make([50, 300], chunks, 4, 2, 64, 16, dtype, True, seed=20, tail=3)
+    for n in ("w", "beta", "log_f"):
+        x[n] = x[n][:, :1].expand(x[n].shape)
+    for n in ("q", "k", "v"):
+        x[n][sum(chunks):] = float("nan")
+    run(lib, x)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("chunks", [[1, 1], [70, 3]])
+def test_two_streams_at_once(lib, dtype, chunks):
+    """Two caches stepped on two streams, each with its own workspace, give what they give one
+    after the other."""
+    xs = [pc.make([900, 130], chunks, 4, 2, 64, 16, dtype, True, seed=21 + i) for i in range(2)]
+    caches = [pc.cache_of(lib, x) for x in xs]
+    ws = [lib.new_paged_workspace(c, sum(chunks), max(chunks), Hq=4) for c in caches]
+    starts = [pc.snapshot(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    ends = []
+    for apart in (True, False):
+        for x, s in zip(xs, starts):
+            for n in s:
+                x[n].copy_(s[n])
+        outs = [[], []]
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for i, x in enumerate(xs):
+                with torch.cuda.stream(streams[i]):
+                    outs[i].append(pc.step(lib, x, caches[i], workspace=ws[i]))
+                if apart:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        ends.append([t.clone() for o in outs for t in o] +
+                    [x[n].nan_to_num(nan=7.0) for x in xs for n in starts[0]])
+    assert all(torch.equal(a, b) for a, b in zip(*ends))
+    assert all(lib.path_check_workspace(w) == lib.OK for w in ws)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("fox", [False, True])
 def test_beta_zero_and_two(lib, dtype, fox):

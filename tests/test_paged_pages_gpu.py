@@ -267,3 +267,47 @@ def test_captured_page_calls(lib):
     assert int(c.k_ref.sum()) == 8
     g.replay()  # 65 tokens do not fit four pages of 16
     assert lib.path_check_workspace(ws) == lib.ERR_CAPACITY
+
+
+def test_captured_fork_free_and_compact(lib):
+    """One graph that forks a sequence twice, steps all three, drops the first fork and packs the
+    pools; each replay leaves what the calls made one by one leave, and the lists of rows may
+    change after the capture."""
+    def fresh():
+        c = cache(lib, [40, 0, 0, 90], page=16, Hq=4, Hkv=2, d=64, dtype=torch.bfloat16, fox=True, spare=40, seed=5)
+        return c, lib.new_paged_workspace(c, 16, 8, Hq=4)
+
+    x = pc.make([0] * 4, [3, 1, 8, 4], 4, 2, 64, 16, torch.bfloat16, True, seed=6)
+    extra = x["cu"][1:] - x["cu"][:-1]
+    src, dst, gone = [0, 3], [1, 2], [1, 2]
+
+    def turn(c, ws):
+        lib.path_paged_fork(src, dst, c, workspace=ws)
+        lib.path_paged_reserve(extra, c, workspace=ws)
+        out = pc.step(lib, x, c, workspace=ws)
+        c.lens += extra
+        lib.path_paged_free(gone, c, workspace=ws)
+        lib.path_paged_compact(c, workspace=ws)
+        return out
+
+    def contents(c):
+        live_k, live_v = c.k_ref > 0, c.v_ref > 0
+        return [c.k_table, c.v_table, c.k_ref, c.v_ref, c.lens, c.k_pages[live_k].nan_to_num(nan=7.0),
+                c.v_pages[live_v].nan_to_num(nan=7.0), c.g_pages[live_k].nan_to_num(nan=7.0)]
+
+    a, wa = fresh()
+    outs = [turn(a, wa) for _ in range(3)]
+    b, wb = fresh()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        got = turn(b, wb)
+    for lists in (src, dst, gone):
+        lists[:] = [0, 0]
+    for out in outs:
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, out)
+    assert lib.path_check_workspace(wa) == lib.OK and lib.path_check_workspace(wb) == lib.OK
+    assert all(torch.equal(p, q) for p, q in zip(contents(a), contents(b)))
