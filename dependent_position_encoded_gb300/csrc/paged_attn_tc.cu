@@ -110,6 +110,9 @@ __device__ __forceinline__ void tmem_scale(uint32_t taddr, float f) {
 }
 
 constexpr float kRescale = 8.f;  // the running maximum may lag by 2^8 before O is rescaled
+// PaTH-FoX: how far (a power of two) below a row's maximum a weight counts for nothing, and how far
+// above its gates a logit is not expected (only what is fetched early goes by that)
+constexpr float kNothing = 64.f, kGuess = 32.f;
 
 // ================================================================ cached keys
 // Persistent: a CTA walks its stretches of units (paged_tc.cuh), each of them one item: NT tiles
@@ -804,6 +807,8 @@ struct ScanSmem {
     static constexpr int RF = 0, RE = RF + NR, VF = RE + NR, VE = VF + NV, SD = VE + NV, XD = SD + 1, XR = XD + 1,
                          SFREE = XR + 1,
                          PR = SFREE + 1, PV = PR + 1, FIN = PV + 1, count = FIN + 1;
+    // behind the barriers: TMEM's address, the abort flag, the last step whose values count (need)
+    static constexpr int need = 2;
     static constexpr uint32_t bytes = bars + count * 8 + 16, alloc = bytes + 1024;
     // TMEM columns
     static constexpr uint32_t cS = 0, cP = 64, cX = 128, cO = 128 + D, cols = D == 64 ? 256 : 512;
@@ -822,7 +827,7 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
     uint8_t *const sm = smem_raw + (base - raw);
     auto bar = [&](int i) { return base + L::bars + 8u * (uint32_t)i; };
     uint32_t *const tslot = reinterpret_cast<uint32_t *>(sm + L::bars + 8 * L::count);
-    volatile uint32_t *const abort_f = tslot + 1;
+    volatile uint32_t *const abort_f = tslot + 1, *const need = tslot + L::need;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y, G = a.c.G;
     int b, ti;
@@ -835,7 +840,7 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
     if (steps <= 0) return;
     const Wait wait{abort_f, a.status, limit_ns};
     if (tid == 0) {
-        *abort_f = 0u;
+        *abort_f = *need = 0u;
         for (int i = 0; i < L::count; ++i)
             mbar_init(bar(i), i == L::XR || i == L::SFREE || i == L::PR ? 4u : 1u);
         fence_mbar_init();
@@ -891,8 +896,9 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
                 if (!wait(bar(L::VF + i), (st / L::NV) & 1) || !wait(bar(L::PR), st & 1)) return false;
                 tc_fence_after();
                 const uint64_t v = sdesc_sw128(base + L::V + i * L::vtile, L::vatom, 1024);
+                if (!FOX || *need == st + 1u)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) umma_tA(tmem + L::cO, tmem + L::cP + 8 * kk, v + 128 * kk, ID_O, 1);
+                    for (int kk = 0; kk < 4; ++kk) umma_tA(tmem + L::cO, tmem + L::cP + 8 * kk, v + 128 * kk, ID_O, 1);
                 umma_commit(bar(L::PV));
                 umma_commit(bar(L::VE + i));
                 return true;
@@ -932,7 +938,7 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
             l_run = ml.y;
         }
         const float gq = FOX && live ? y.gq[row] : 0.f;
-        double between = 0.0;
+        float between = 0.f;  // gates of the blocks passed (where they matter the sum is small: fp32 will do)
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             float o[32];
@@ -952,13 +958,16 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
             const int ks = slot_of(s, b, kb);
             const float4 *const gt =
                 FOX ? reinterpret_cast<const float4 *>(y.gt + ((size_t)ks * a.c.Hq + hq) * kC) : nullptr;
+            // the block's gates: their sum, and the largest sum behind a key
+            float2 block = make_float2(0.f, 0.f);
             float bias = 0.f;
-            double block = 0.0;
-            if (FOX && part) {  // on their way while the product runs
-                asm volatile("prefetch.global.L1 [%0];" ::"l"(gt));
-                asm volatile("prefetch.global.L1 [%0];" ::"l"(gt + 8));
-                block = y.gtot[(size_t)ks * a.c.Hq + hq];
-                bias = (float)((double)gq + between) * kLog2e;
+            if (FOX && part) {
+                block = y.gblk[(size_t)ks * a.c.Hq + hq];
+                bias = (gq + between) * kLog2e;
+                if (bias > m_run - kNothing - kGuess) {  // on their way while the product runs
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(gt));
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(gt + 8));
+                }
             }
             if (!(ok = wait.warp(bar(L::SD), st & 1))) break;
             tc_fence_after();
@@ -971,7 +980,22 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
             }
             tc_fence_before();
             mbar_arrive_warp(bar(L::SFREE));
-            if (FOX && part) {
+            auto top64 = [&]() {
+                float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int c = 4; c < 60; c += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) m4[q] = fmax3(m4[q], x[c + 2 * q], x[c + 2 * q + 1]);
+                return fmax3(fmax3(m4[0], m4[1], m4[2]), fmax3(m4[3], x[60], x[61]), fmaxf(x[62], x[63]));
+            };
+            // PaTH-FoX: a block whose logits all lie below 2^-64 of what a row has is left out (2^22 keys
+            // of those move a sum by less than 2^-42 of itself), its values' product too if that
+            // holds for all rows
+            bool counts = part;
+            if (FOX && part)
+                counts = __any_sync(0xffffffffu,
+                                    live && !(top64() + fmaf(block.y, kLog2e, bias) < m_run - kNothing)) != 0;
+            if (FOX && counts) {
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     const float4 g4 = __ldg(gt + q);
@@ -980,19 +1004,15 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
                     x[4 * q + 2] = fmaf(g4.z, kLog2e, x[4 * q + 2] + bias);
                     x[4 * q + 3] = fmaf(g4.w, kLog2e, x[4 * q + 3] + bias);
                 }
-                between += block;
             }
+            if (FOX) between += block.x;
             // P and O are free once the previous P V has completed
             if (st > 0 && !(ok = wait.warp(bar(L::PV), (st - 1) & 1))) break;
             tc_fence_after();
+            if (FOX && counts && lane == 0) *need = st + 1;  // the last step's has been read
             uint32_t p[16];
-            if (part) {
-                float m4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                for (int c = 4; c < 60; c += 8)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) m4[q] = fmax3(m4[q], x[c + 2 * q], x[c + 2 * q + 1]);
-                const float mx = fmax3(fmax3(m4[0], m4[1], m4[2]), fmax3(m4[3], x[60], x[61]), fmaxf(x[62], x[63]));
+            if (counts) {
+                const float mx = top64();
                 float alpha = 1.f;
                 if (mx > m_run + kRescale) {
                     alpha = ex2_approx(m_run - mx);
@@ -1041,7 +1061,7 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
             }
             if (live) {
                 y.pml[row] = make_float2(m_run, l_run);
-                if (FOX) y.gq[row] = (float)((double)gq + between);
+                if (FOX) y.gq[row] = gq + between;
             }
         }
     } else if (warp < 8) {
@@ -1200,7 +1220,7 @@ cudaError_t launch_all(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStre
 
 struct TcLayout {
     int ctas[2];
-    size_t qt, ql, po, pml, so[2], sml[2], units[2], items[2], gq, gt, gtot, mt, kh, kl, vb, ch, cl, gp, total;
+    size_t qt, ql, po, pml, so[2], sml[2], units[2], items[2], gq, gt, gtot, gblk, mt, kh, kl, vb, ch, cl, gp, total;
 };
 
 // The regions depend on the sizes in ways that do not fall as the step grows, so that a workspace
@@ -1233,6 +1253,7 @@ TcLayout tc_layout(const Cache &c, int N, int max_chunk, int d, bool fox) {
     y.gq = take(fox ? rows * 4 : 0);
     y.gt = take(fox ? slots * c.Hq * kC * 4 : 0);
     y.gtot = take(fox ? slots * c.Hq * 8 : 0);
+    y.gblk = take(fox ? slots * c.Hq * 8 : 0);
     y.mt = take((size_t)std::min(c.seqs, N) * c.Hkv * 2 * d * d * 2);
     const bool blocks = max_chunk > kC;
     y.kh = take(blocks ? slots * c.Hkv * (kC + d) * d * 2 : 0);
@@ -1279,6 +1300,7 @@ cudaError_t launch_tc(const Step &a, int d, void *ws, uint64_t limit_ns, cudaStr
     y.gq = f32(f.gq);
     y.gt = f32(f.gt);
     y.gtot = reinterpret_cast<double *>(w + f.gtot);
+    y.gblk = reinterpret_cast<float2 *>(w + f.gblk);
     y.R = (long long)a.N * a.c.G;
     if (d == 64)
         return fox ? launch_all<64, true>(a, y, limit_ns, stream) : launch_all<64, false>(a, y, limit_ns, stream);

@@ -406,18 +406,25 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             }
             x[1] += __shfl_sync(0xffffffffu, x[0], 31);
             const double all = __shfl_sync(0xffffffffu, x[1], 31);
-            if (lane == 0) y.gtot[bq] = all;
+            float most = -INFINITY;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int t = 32 * half + lane;
                 const float hi = (float)x[half], behind = (float)(all - x[half]);
                 cum[t] = make_float2(hi, (float)(x[half] - (double)hi));
                 y.gt[bq * kC + t] = behind;
+                most = fmaxf(most, behind);
                 if (t < rows) {
                     y.gq[row_of(t)] = hi;
                     const long long at = single ? place(kpage, t, a.c.Hq, hq) : -1;
                     if (at >= 0) a.c.g_pages[at] = behind;
                 }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            if (lane == 0) {
+                y.gtot[bq] = all;
+                y.gblk[bq] = make_float2((float)all, most);
             }
         }
         __syncthreads();

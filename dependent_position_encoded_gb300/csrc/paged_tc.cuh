@@ -40,6 +40,7 @@ __host__ __device__ constexpr bool keeps_low(int NT, int D) { return NT == 1 || 
 //   gq   (Hkv, R) fp32          PaTH-FoX: gate sum of a row from the chunk's start
 //   gt   (slots, Hq, 64) fp32   PaTH-FoX: gate sum behind a key to its block's end
 //   gtot (slots, Hq) fp64       PaTH-FoX: gate sum of a block
+//   gblk (slots, Hq, 2) fp32    PaTH-FoX: the same rounded, and the largest of the block's gt
 //   mt   (min(seqs, N), Hkv, 2, D, D) bf16 high and low parts of (H_1 ... H_T) - I of the chunk
 // and, where a chunk may have several blocks of 64 tokens:
 //   kh, kl (slots, Hkv, 64 + D, D) bf16 high and low parts of [k~; P_b - I]
@@ -56,6 +57,7 @@ struct TcWs {
     Plan plan[2];
     float *gq, *gt;
     double *gtot;
+    float2 *gblk;
     long long R;
 };
 

@@ -150,6 +150,58 @@ def test_gates_that_close(lib, dtype, chunks):
     run(lib, x)
 
 
+def far_key(lens, chunks, at, Hq, Hkv, d, page, dtype=BF):
+    """Steps whose gates close fast, exp(-0.35) a token, so that nothing a few hundred positions
+    back should count, but one key far back points along every query with a logit of 260: at
+    most 180 of gates lie on it, so it takes all the weight (the logits of the others are of
+    unit size). `at`: its position per sequence."""
+    x = pc.make(lens, chunks, Hq, Hkv, d, page, dtype, True, seed=22)
+    q = torch.randn(d, device="cuda")
+    q = (q * d ** 0.5 / q.norm()).to(dtype)
+    x["q"][:] = q
+    x["beta"].zero_()
+    x["log_f"].fill_(-0.35)
+    first = 0
+    for s, (n, T, j) in enumerate(zip(lens, chunks, at)):
+        dist = torch.arange(n - 1, -1, -1, device="cuda", dtype=torch.float32)
+        pc.put(x["g_pages"], x["k_table"][s], 0, (-0.35 * dist)[:, None].expand(n, Hq).contiguous())
+        key = (q.double() * 260 / d ** 0.5).to(dtype)[None, None].expand(1, Hkv, d)
+        if j is not None and j < n:
+            pc.put(x["k_pages"], x["k_table"][s], j, key.contiguous())
+        elif j is not None:
+            x["k"][first + j - n] = key[0]
+        first += T
+    return x
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (8, 2), (3, 1)])
+@pytest.mark.parametrize("lens,chunks,at", [
+    ([900, 600, 300], [1, 1, 1], [500, 100, None]),      # single tokens; far keys of two of them
+    ([700, 200, 400], [30, 3, 65], [280, None, 5]),      # one row tile, or two
+    ([500, 0], [190, 3], [300, None]),                   # the chunk's own blocks, and cached keys
+    ([0, 0], [450, 500], [10, 63]),                      # a chunk's first block
+])
+def test_far_keys_behind_closed_gates(lib, d, page, Hq, Hkv, lens, chunks, at):
+    x = far_key(lens, chunks, at, Hq, Hkv, d, page)
+    run(lib, x)
+
+
+@pytest.mark.parametrize("Hq,chunk", [(2, 1), (8, 40)])
+def test_far_key_beside_an_absent_page(lib, Hq, chunk):
+    x = far_key([900], [chunk], [550], Hq, 2, 64, 16)
+    ids = x["v_table"][0]
+    want = x["v_pages"][int(ids[550 // 16]), :, 550 % 16].float()
+    ids[550 // 16 + 1] = -1
+    x["k_table"][0, 550 // 16 - 1] = 1 << 20
+    cache = pc.cache_of(lib, x)
+    ws = lib.new_paged_workspace(cache, chunk, chunk, Hq=Hq)
+    out = pc.step(lib, x, cache, workspace=ws)
+    assert lib.path_check_workspace(ws) == lib.ERR_CACHE
+    # all the weight is the far key's, and its value is a bf16 number already
+    assert torch.equal(out.float(), want.repeat_interleave(Hq // 2, 0).expand(chunk, Hq, 64))
+
+
 def test_one_call_equals_single_steps(lib):
     """A chunk and its tokens one by one end in the same cache and outputs, in fp32 within the
     roundings of either."""
