@@ -4,7 +4,7 @@
 // 64 x 64 x d or the pass is bound by memory, and none of them is worth a tensor-memory
 // pipeline; the attention itself is in paged_attn_tc.cu.
 //
-// Precision. The inputs are bf16; what is computed from them (A, U, Lq A, R A^T, P_b) enters
+// Precision. The inputs are bf16; what is computed from them (A, U, Lq, R A^T, P_b) enters
 // further products as a high and a low bf16 part (16 bits of significand, see split2), so
 // carried keys and transitions are exact to 2^-16 before the cache rounds the keys to bf16.
 // The factor A = (I + D N)^{-1} D is solved in fp32. Rounded to bf16 are the softmax weights,
@@ -27,13 +27,17 @@ template <int D>
 struct PrepSmem {
     static constexpr int LDD = D + 8, LDS = 72, LDF = 72;  // row strides: 16-byte phases differ
     static constexpr size_t big = (size_t)kC * LDD * 2, sml = (size_t)kC * LDS * 2;
-    static constexpr size_t W = 0, K = big, Q = 2 * big, V = 3 * big;  // U (hi, lo) lies in Q, V
-    static constexpr size_t Ah = 4 * big, Al = Ah + sml, Rh = Al + sml, Rl = Rh + sml, Lh = Rl + sml,
-                            Ll = Lh + sml, Th = Ll + sml, Tl = Th + sml, F = Th;
-    // fp32 64 x 72 (E, the logits) lies in [Th, Tl]; the pair Lh, Ll holds Lq and R A^T, then P
-    // beta, row maxima and sums: 64 floats each; the gates' prefix sums as float pairs; 16 pages
-    static constexpr size_t vec = Tl + sml, bytes = vec + 5 * kC * 4 + 16 * 4;
+    // pairs (hi, lo): U; S = R A^T; A, in its place Lq and then P; R in the places of Q and V
+    static constexpr size_t W = 0, K = big, Q = 2 * big, V = 3 * big, Uh = 4 * big, Ul = 5 * big, Ah = 6 * big,
+                            Al = Ah + sml, Sh = Al + sml, Sl = Sh + sml, Rh = Q, Rl = V;
+    static constexpr size_t F = Sl + sml;  // fp32 64 x 72: E and its inverse, then the logits
+    // beta, row maxima and sums: 64 floats each; 16 pages; the gates' prefix sums of kHeads query
+    // heads as float pairs
+    static constexpr int kHeads = 8;
+    static constexpr size_t vec = F + kC * LDF * 4, cum = vec + 3 * kC * 4 + 16 * 4, bytes = cum + kHeads * kC * 8;
 };
+static_assert(PrepSmem<64>::kHeads == kThr / 32, "a warp per head");
+static_assert(2 * (PrepSmem<64>::bytes + 1024) <= 228 * 1024 && PrepSmem<128>::bytes <= 227 * 1024, "shared memory");
 
 // 64 tokens (rows past `rows` zero) of one head into registers, and from there into a shared
 // tile: the loads of several tiles are in flight together
@@ -213,17 +217,15 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
     using S = PrepSmem<D>;
     constexpr int LDD = S::LDD, LDS = S::LDS, LDF = S::LDF, NH = D / 64;
     extern __shared__ __align__(16) uint8_t smem[];
-    bf *const W = reinterpret_cast<bf *>(smem + S::W), *const K = reinterpret_cast<bf *>(smem + S::K),
-       *const Q = reinterpret_cast<bf *>(smem + S::Q), *const V = reinterpret_cast<bf *>(smem + S::V),
-       *const Uh = Q, *const Ul = V, *const Ah = reinterpret_cast<bf *>(smem + S::Ah),
-       *const Al = reinterpret_cast<bf *>(smem + S::Al), *const Rh = reinterpret_cast<bf *>(smem + S::Rh),
-       *const Rl = reinterpret_cast<bf *>(smem + S::Rl), *const Lh = reinterpret_cast<bf *>(smem + S::Lh),
-       *const Ll = reinterpret_cast<bf *>(smem + S::Ll), *const Th = reinterpret_cast<bf *>(smem + S::Th),
-       *const Tl = reinterpret_cast<bf *>(smem + S::Tl);
+    auto tile = [&](size_t at) { return reinterpret_cast<bf *>(smem + at); };
+    bf *const W = tile(S::W), *const K = tile(S::K), *const Q = tile(S::Q), *const V = tile(S::V),
+       *const Uh = tile(S::Uh), *const Ul = tile(S::Ul), *const Ah = tile(S::Ah), *const Al = tile(S::Al),
+       *const Sh = tile(S::Sh), *const Sl = tile(S::Sl), *const Rh = tile(S::Rh), *const Rl = tile(S::Rl),
+       *const Lh = Ah, *const Ll = Al, *const P = Ah;
     float *const F = reinterpret_cast<float *>(smem + S::F);
     float *const beta = reinterpret_cast<float *>(smem + S::vec), *const rm = beta + kC, *const rl = rm + kC;
-    float2 *const cum = reinterpret_cast<float2 *>(rl + kC);
-    int *const kpage = reinterpret_cast<int *>(cum + kC), *const vpage = kpage + 8;
+    int *const kpage = reinterpret_cast<int *>(rl + kC), *const vpage = kpage + 8;
+    float2 *const cums = reinterpret_cast<float2 *>(smem + S::cum);
     const int slot = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.c.G;
     int b, c;
@@ -270,14 +272,16 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
     // a warp's 16 x 32 piece of a 64 x 64 product
     const int m0 = 16 * (warp & 3), n0 = 32 * (warp >> 2);
     const bool live = (warp & 3) < nt && n0 < 16 * nt;  // the piece has rows and columns
+    // and entries at or below the diagonal, or above it. A lower triangle's rows m0 .. m0 + 15 end in
+    // column tile m_end - 1, an upper one's begin in column tile m0 / 16
+    const bool lower = live && n0 <= m0, upper = live && m0 < n0 + 32;
+    const int m_end = min(nt, (warp & 3) + 1);
     {
         float e[4][4], r[4][4];
         zero_acc(e);
         zero_acc(r);
-        if (live) {
-            warp_mma<4, false, false>(e, W, LDD, m0, W, LDD, n0, D / 16);
-            warp_mma<4, false, false>(r, K, LDD, m0, W, LDD, n0, D / 16);
-        }
+        if (lower) warp_mma<4, false, false>(e, W, LDD, m0, W, LDD, n0, D / 16);
+        if (upper) warp_mma<4, false, false>(r, K, LDD, m0, W, LDD, n0, D / 16);
         each_pair(e, m0, n0, [&](int i, int j, float x, float z) {
             *reinterpret_cast<float2 *>(F + i * LDF + j) =
                 make_float2(j < i ? beta[i] * x : 0.f, j + 1 < i ? beta[i] * z : 0.f);
@@ -290,7 +294,53 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
         });
     }
     __syncthreads();
-    unit_lower_inverse<LDF>(F, reinterpret_cast<float *>(Lh), tid, nt);
+    // PaTH-FoX, a warp per query head: inclusive prefix sums of the block's 64 gates, in fp64: lane t
+    // holds those of t and t + 32. Shared as two floats each: a difference of two is then right to
+    // an fp32 rounding of itself, however large the sums are
+    auto gates = [&](int g, float2 *cum) {
+        const int hq = h * G + g;
+        const size_t bq = (size_t)slot * a.c.Hq + hq;
+        double x[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int t = 32 * half + lane;
+            x[half] = t < rows ? (double)a.log_f[(first + t) * a.sf.tok + hq * a.sf.head] : 0.0;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const double z = __shfl_up_sync(0xffffffffu, x[half], o);
+                if (lane >= o) x[half] += z;
+            }
+        }
+        x[1] += __shfl_sync(0xffffffffu, x[0], 31);
+        const double all = __shfl_sync(0xffffffffu, x[1], 31);
+        float most = -INFINITY;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int t = 32 * half + lane;
+            const float hi = (float)x[half], behind = (float)(all - x[half]);
+            cum[t] = make_float2(hi, (float)(x[half] - (double)hi));
+            y.gt[bq * kC + t] = behind;
+            most = fmaxf(most, behind);
+            if (t < rows) {
+                y.gq[(size_t)h * y.R + (first + t) * G + g] = hi;
+                const long long at = single ? place(kpage, t, a.c.Hq, hq) : -1;
+                if (at >= 0) a.c.g_pages[at] = behind;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        if (lane == 0) {
+            y.gtot[bq] = all;
+            y.gblk[bq] = make_float2((float)all, most);
+        }
+    };
+    // those of the first heads, by the warps that the inverse's first part leaves idle
+    if (a.log_f != nullptr && warp >= 2)
+        for (int g = g0 + warp - 2; g < min(g1, g0 + S::kHeads); g += kThr / 32 - 2) gates(g, cums + (g - g0) * kC);
+    unit_lower_inverse<LDF>(F, reinterpret_cast<float *>(Sh), tid, nt);
     for (int e = tid; e < kC * kC / 2; e += kThr) {
         const int i = e / 32, j = 2 * (e % 32);
         uint32_t hi, lo;
@@ -300,14 +350,12 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
         put2(Al, LDS, i, j, lo);
     }
     __syncthreads();
-    // U = A W (64 x D) and R A^T (64 x 64)
+    // U = A W (64 x D) and S = R A^T (64 x 64, strictly upper)
 #pragma unroll
     for (int x = 0; x < NH; ++x) {
         float u[4][4];
         zero_acc(u);
-        if ((warp & 3) < nt) {
-            warp_mma_a2<4, false, true>(u, Ah, Al, LDS, m0, W, LDD, 64 * x + n0, nt);
-        }
+        if ((warp & 3) < nt) warp_mma_a2<4, false, true>(u, Ah, Al, LDS, m0, W, LDD, 64 * x + n0, m_end);
         each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
             uint32_t hi, lo;
             split2(p, q, hi, lo);
@@ -318,14 +366,12 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
     {
         float r[4][4];
         zero_acc(r);
-        if (live) {
-            warp_mma_3<4, false>(r, Rh, Rl, LDS, m0, Ah, Al, LDS, n0, nt);
-        }
+        if (upper) warp_mma_3<4, false>(r, Rh, Rl, LDS, m0, Ah, Al, LDS, n0, min(nt, n0 / 16 + 2), m0 / 16);
         each_pair(r, m0, n0, [&](int i, int j, float p, float q) {
             uint32_t hi, lo;
             split2(p, q, hi, lo);
-            put2(Lh, LDS, i, j, hi);
-            put2(Ll, LDS, i, j, lo);
+            put2(Sh, LDS, i, j, hi);
+            put2(Sl, LDS, i, j, lo);
         });
     }
     __syncthreads();
@@ -347,13 +393,13 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             });
         }
     }
-    // k~ = K - (R A^T) W: into the pages (the chunk's only block) or the block's factors
+    // k~ = K - S W: into the pages (the chunk's only block) or the block's factors
 #pragma unroll
     for (int x = 0; x < NH; ++x) {
         if (!lead || (single && (warp & 3) >= nt)) break;
         float u[4][4];
         zero_acc(u);
-        warp_mma_a2<4, false, true>(u, Lh, Ll, LDS, m0, W, LDD, 64 * x + n0, nt);
+        warp_mma_a2<4, false, true>(u, Sh, Sl, LDS, m0, W, LDD, 64 * x + n0, nt, m0 / 16);
         each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
             const float2 k2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(K + i * LDD + j));
             p = k2.x - p;
@@ -379,60 +425,27 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             const long long at = r < rows ? place(vpage, r, a.c.Hkv, h) : -1;
             if (at >= 0) *reinterpret_cast<uint4 *>(static_cast<bf *>(a.c.v_pages) + at * D + q) = vb.x[i];
         }
-    __syncthreads();
-    vb.put(V);
+    vb.put(V);  // R has been read
     for (int g = g0; g < g1; ++g) {
         const int hq = h * G + g;
-        const size_t bq = (size_t)slot * a.c.Hq + hq;
         // the row of token t: its place in the step's packed rows
         auto row_of = [&](int t) { return (size_t)h * y.R + (first + t) * G + g; };
-        __syncthreads();
+        const float2 *const cum = cums + (g - g0) % S::kHeads * kC;
         qb.put(Q);
         if (g + 1 < g1) qb.load(a.q, a.sq, first, hq + 1, rows);
-        if (a.log_f != nullptr && warp == 0) {
-            // inclusive prefix sums of the 64 gates, in fp64: lane t holds those of t and t + 32.
-            // Shared as two floats each: a difference of two is then right to an fp32 rounding of
-            // itself, however large the sums are
-            double x[2];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int t = 32 * half + lane;
-                x[half] = t < rows ? (double)a.log_f[(first + t) * a.sf.tok + hq * a.sf.head] : 0.0;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double z = __shfl_up_sync(0xffffffffu, x[half], o);
-                    if (lane >= o) x[half] += z;
-                }
-            }
-            x[1] += __shfl_sync(0xffffffffu, x[0], 31);
-            const double all = __shfl_sync(0xffffffffu, x[1], 31);
-            float most = -INFINITY;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int t = 32 * half + lane;
-                const float hi = (float)x[half], behind = (float)(all - x[half]);
-                cum[t] = make_float2(hi, (float)(x[half] - (double)hi));
-                y.gt[bq * kC + t] = behind;
-                most = fmaxf(most, behind);
-                if (t < rows) {
-                    y.gq[row_of(t)] = hi;
-                    const long long at = single ? place(kpage, t, a.c.Hq, hq) : -1;
-                    if (at >= 0) a.c.g_pages[at] = behind;
-                }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-            if (lane == 0) {
-                y.gtot[bq] = all;
-                y.gblk[bq] = make_float2((float)all, most);
-            }
-        }
+        if (a.log_f != nullptr && g > g0 && (g - g0) % S::kHeads == 0 && g + warp < g1)
+            gates(g + warp, cums + warp * kC);  // the next heads'
         __syncthreads();
-        {  // Lq = tril(Q W^T)
-            float u[4][4];
-            zero_acc(u);
-            if (live) warp_mma<4, false, false>(u, Q, LDD, m0, W, LDD, n0, D / 16);
-            each_pair(u, m0, n0, [&](int i, int j, float p, float q) {
+        float u[4][4];
+        zero_acc(u);
+        {  // Lq = tril(Q W^T), and Q K^T
+            float z[4][4];
+            zero_acc(z);
+            if (lower) {
+                warp_mma<4, false, false>(z, Q, LDD, m0, W, LDD, n0, D / 16);
+                warp_mma<4, false, false>(u, Q, LDD, m0, K, LDD, n0, D / 16);
+            }
+            each_pair(z, m0, n0, [&](int i, int j, float p, float q) {
                 uint32_t hi, lo;
                 split2(j <= i ? p : 0.f, j + 1 <= i ? q : 0.f, hi, lo);
                 put2(Lh, LDS, i, j, hi);
@@ -440,50 +453,14 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             });
         }
         __syncthreads();
-        {  // Lq A
-            float u[4][4];
-            zero_acc(u);
-            if (live) {
-                warp_mma_3<4, true>(u, Lh, Ll, LDS, m0, Ah, Al, LDS, n0, nt);
-            }
-            each_pair(u, m0, n0, [&](int i, int j, float p, float q) {
-                uint32_t hi, lo;
-                split2(p, q, hi, lo);
-                put2(Th, LDS, i, j, hi);
-                put2(Tl, LDS, i, j, lo);
-            });
-        }
-        __syncthreads();
-        // q~ = Q - (Lq A) W
-#pragma unroll
-        for (int x = 0; x < NH; ++x) {
-            if ((warp & 3) >= nt) break;
-            float u[4][4];
-            zero_acc(u);
-            warp_mma_a2<4, false, true>(u, Th, Tl, LDS, m0, W, LDD, 64 * x + n0, nt);
-            each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
-                if (i >= rows) return;
-                const float2 q2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(Q + i * LDD + j));
-                // scaled here once, so that the attention's logits need no factor
-                uint32_t hi, lo;
-                split2((q2.x - p) * a.scale_log2, (q2.y - q) * a.scale_log2, hi, lo);
-                *reinterpret_cast<uint32_t *>(y.qt + row_of(i) * D + j) = hi;
-                if (keeps_low(s.T * G <= 128 ? 1 : 2, D)) *reinterpret_cast<uint32_t *>(y.ql + row_of(i) * D + j) = lo;
-            });
-        }
-        {  // the block's logits Q K^T - (Lq A) R^T
-            float u[4][4], z[4][4];
-            zero_acc(u);
+        {  // the block's logits Q K^T - Lq S^T
+            float z[4][4];
             zero_acc(z);
-            if (live) {
-                warp_mma<4, false, false>(u, Q, LDD, m0, K, LDD, n0, D / 16);
-                warp_mma_3<4, false>(z, Th, Tl, LDS, m0, Rh, Rl, LDS, n0, nt);
-            }
+            if (lower) warp_mma_3<4, false>(z, Lh, Ll, LDS, m0, Sh, Sl, LDS, n0, m_end, n0 / 16);
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) u[n][i] = (u[n][i] - z[n][i]) * a.scale_log2;
-            __syncthreads();  // Lq A has been read; the logits take its place
             each_pair(u, m0, n0, [&](int i, int j, float p, float q) {
                 if (a.log_f != nullptr) {
                     const float2 ci = cum[i];
@@ -493,6 +470,23 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
                 }
                 *reinterpret_cast<float2 *>(F + i * LDF + j) =
                     make_float2(j <= i ? p : -INFINITY, j + 1 <= i ? q : -INFINITY);
+            });
+        }
+        // q~ = Q - Lq U
+#pragma unroll
+        for (int x = 0; x < NH; ++x) {
+            if ((warp & 3) >= nt) break;
+            float v[4][4];
+            zero_acc(v);
+            warp_mma_3<4, true>(v, Lh, Ll, LDS, m0, Uh, Ul, LDD, 64 * x + n0, m_end);
+            each_pair(v, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
+                if (i >= rows) return;
+                const float2 q2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(Q + i * LDD + j));
+                // scaled here once, so that the attention's logits need no factor
+                uint32_t hi, lo;
+                split2((q2.x - p) * a.scale_log2, (q2.y - q) * a.scale_log2, hi, lo);
+                *reinterpret_cast<uint32_t *>(y.qt + row_of(i) * D + j) = hi;
+                if (keeps_low(s.T * G <= 128 ? 1 : 2, D)) *reinterpret_cast<uint32_t *>(y.ql + row_of(i) * D + j) = lo;
             });
         }
         __syncthreads();
@@ -517,7 +511,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             }
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            *reinterpret_cast<uint4 *>(Lh + i * LDS + j) =
+            *reinterpret_cast<uint4 *>(P + i * LDS + j) =
                 make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                            pack_bf16x2(x[6], x[7]));
             if ((lane & 7) == 0) {
@@ -530,10 +524,10 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
 #pragma unroll
         for (int x = 0; x < NH; ++x) {
             if ((warp & 3) >= nt) break;
-            float u[4][4];
-            zero_acc(u);
-            warp_mma<4, false, true>(u, Lh, LDS, m0, V, LDD, 64 * x + n0, nt);
-            each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
+            float v[4][4];
+            zero_acc(v);
+            warp_mma<4, false, true>(v, P, LDS, m0, V, LDD, 64 * x + n0, m_end);
+            each_pair(v, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
                 if (i < rows) *reinterpret_cast<float2 *>(y.po + row_of(i) * D + j) = make_float2(p, q);
             });
         }

@@ -168,9 +168,10 @@ __device__ __forceinline__ void frag_b(uint32_t (&r)[4], const __nv_bfloat16 *t,
 // 2 (lane % 4), + 1; acc[n][2..3]: row + 8.
 template <int NT, bool AT, bool BN>
 __device__ __forceinline__ void warp_mma(float (&acc)[NT][4], const __nv_bfloat16 *A, int lda, int m0,
-                                         const __nv_bfloat16 *B, int ldb, int n0, int ksteps) {
+                                         const __nv_bfloat16 *B, int ldb, int n0, int ksteps,
+                                         int k0 = 0) {
 #pragma unroll 2
-    for (int k = 0; k < ksteps; ++k) {
+    for (int k = k0; k < ksteps; ++k) {
         uint32_t a[4];
         if (AT) frag_at(a, A, lda, m0, 16 * k);
         else frag_a(a, A, lda, m0, 16 * k);
@@ -189,9 +190,10 @@ __device__ __forceinline__ void warp_mma(float (&acc)[NT][4], const __nv_bfloat1
 // it is, or with B = Bh + Bl (low x low left out).
 template <int NT, bool AT, bool BN>
 __device__ __forceinline__ void warp_mma_a2(float (&acc)[NT][4], const __nv_bfloat16 *Ah, const __nv_bfloat16 *Al,
-                                            int lda, int m0, const __nv_bfloat16 *B, int ldb, int n0, int ksteps) {
+                                            int lda, int m0, const __nv_bfloat16 *B, int ldb, int n0, int ksteps,
+                                         int k0 = 0) {
 #pragma unroll 2
-    for (int k = 0; k < ksteps; ++k) {
+    for (int k = k0; k < ksteps; ++k) {
         uint32_t a[4], c[4];
         if (AT) {
             frag_at(a, Ah, lda, m0, 16 * k);
@@ -215,9 +217,10 @@ __device__ __forceinline__ void warp_mma_a2(float (&acc)[NT][4], const __nv_bflo
 template <int NT, bool BN>
 __device__ __forceinline__ void warp_mma_3(float (&acc)[NT][4], const __nv_bfloat16 *Ah, const __nv_bfloat16 *Al,
                                            int lda, int m0, const __nv_bfloat16 *Bh, const __nv_bfloat16 *Bl,
-                                           int ldb, int n0, int ksteps) {
+                                           int ldb, int n0, int ksteps,
+                                         int k0 = 0) {
 #pragma unroll 1
-    for (int k = 0; k < ksteps; ++k) {
+    for (int k = k0; k < ksteps; ++k) {
         uint32_t a[4], c[4];
         frag_a(a, Ah, lda, m0, 16 * k);
         frag_a(c, Al, lda, m0, 16 * k);
