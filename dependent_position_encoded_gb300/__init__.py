@@ -15,6 +15,7 @@ Entry points keep the C names: ``path_attn_fwd``, ``path_fox_fwd``,
 """
 import ctypes
 import dataclasses
+import functools
 import math
 import os
 
@@ -613,28 +614,34 @@ def _paged_cache_errors(cache, counts, Hq):
 def _paged_devices(cache, *more):
     """Every tensor on the GPU that holds k_pages; `more`: tensors or None."""
     dev = cache.k_pages.get_device()
-    for t in (cache.k_pages, cache.v_pages, cache.g_pages, cache.k_table, cache.v_table,
-              cache.lens, cache.k_ref, cache.v_ref) + more:
-        if t is not None and (t.get_device() != dev or not t.is_cuda):
-            if not t.is_cuda:
-                raise TypeError("the cache and the step's tensors must be CUDA tensors")
-            raise ValueError("the cache and the step's tensors must be on one device")
+    all_of = [t for t in (cache.k_pages, cache.v_pages, cache.g_pages, cache.k_table, cache.v_table,
+                          cache.lens, cache.k_ref, cache.v_ref, *more) if t is not None]
+    if dev < 0 or not cache.k_pages.is_cuda or [t.get_device() for t in all_of].count(dev) != len(all_of):
+        if not all(t.is_cuda for t in all_of):
+            raise TypeError("the cache and the step's tensors must be CUDA tensors")
+        raise ValueError("the cache and the step's tensors must be on one device")
+    return dev
 
 
 class _on:
-    """The device and, where one is given, the stream of a call, as torch's current ones: what is
-    allocated inside belongs to the stream that the call runs on."""
-    __slots__ = ("guards",)
+    """The device (its index) and, where one is given, the stream of a call, as torch's current
+    ones: what is allocated inside belongs to the stream that the call runs on, whose handle it
+    gives."""
+    __slots__ = ("guards", "dev")
 
     def __init__(self, dev, stream):
         cuda = _torch().cuda
-        self.guards = [] if dev.index == cuda.current_device() else [cuda.device(dev)]
+        self.dev = dev
+        self.guards = [] if dev == cuda.current_device() else [cuda.device(dev)]
         if stream is not None:
+            if stream.device.index != dev:
+                raise ValueError("stream must be on the cache's device")
             self.guards.append(cuda.stream(stream))
 
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
+        return _torch()._C._cuda_getCurrentRawStream(self.dev)
 
     def __exit__(self, *e):
         for g in reversed(self.guards):
@@ -667,7 +674,7 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
     f32 = torch.float32
     try:
         kp = cache.k_pages
-        dt, dev, Hkv = kp.dtype, kp.device, kp.shape[1]
+        dt, Hkv = kp.dtype, kp.shape[1]
         qs = q.shape
         N, Hq, d = qs
         rows, heads = (N, Hkv, d), (N, Hkv)
@@ -693,9 +700,9 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
         raise ValueError("q has head size %d, the cache %d" % (d, c.d))
     if out is not None and (N > 1 and o0[0] == 0 or Hq > 1 and o0[1] == 0):
         raise ValueError("out must not repeat its own memory")
-    _paged_devices(cache, q, k, v, w, beta, log_f, out, cu_tokens)
+    dev = _paged_devices(cache, q, k, v, w, beta, log_f, out, cu_tokens)
     gate = () if log_f is None else (log_f.data_ptr(),)
-    with _on(dev, stream):
+    with _on(dev, stream) as on_stream:
         if out is None:
             out = torch.empty_like(q)
             o0 = out.stride()
@@ -706,7 +713,7 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
             beta.data_ptr(), *gate, cu_tokens.data_ptr(), N, int(max_chunk), _scale(scale, d),
             out.data_ptr(), _C14(q0[0], q0[1], k0[0], k0[1], v0[0], v0[1], w0[0], w0[1], b0[0], b0[1],
                                  f0[0], f0[1], o0[0], o0[1]), None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel(), _stream(stream, dev)), name)
+            0 if workspace is None else workspace.numel(), on_stream), name)
     return out
 
 
@@ -764,18 +771,22 @@ def path_fox_paged_extend(q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, 
 
 
 def _paged_call(name, cache, workspace, stream, *args):
-    c = _paged_cache(cache, counts=True)
-    dev = cache.k_pages.device
-    with _on(dev, stream):
+    c = _paged_cache(cache, counts=True, on_gpu=False)
+    with _on(_paged_devices(cache), stream) as on_stream:
         if workspace is None:
             workspace = new_paged_workspace(cache)
         _check(getattr(_load(), name)(ctypes.byref(c), *args, workspace.data_ptr(),
-                                      workspace.numel(), _stream(stream, dev)), name)
+                                      workspace.numel(), on_stream), name)
+
+
+@functools.lru_cache(maxsize=64)
+def _row_list(n):
+    return ctypes.c_int * n
 
 
 def _rows(rows):
     rows = [int(r) for r in rows]
-    return (ctypes.c_int * max(len(rows), 1))(*rows), len(rows)
+    return _row_list(max(len(rows), 1))(*rows), len(rows)
 
 
 def path_paged_reserve(extra, cache, workspace=None, stream=None):
@@ -787,10 +798,10 @@ def path_paged_reserve(extra, cache, workspace=None, stream=None):
         raise TypeError("extra must be a tensor")
     if extra.dtype != torch.int32:
         raise TypeError("extra must be torch.int32, got %s" % extra.dtype)
-    if isinstance(cache, PathPagedCache) and tuple(extra.shape) != tuple(cache.lens.shape):
+    if isinstance(cache, PathPagedCache) and extra.shape != cache.lens.shape:
         raise ValueError("extra must be (seqs,)")
     _cuda_tensor(extra, "extra")
-    if isinstance(cache, PathPagedCache) and extra.device != cache.k_pages.device:
+    if isinstance(cache, PathPagedCache) and extra.get_device() != cache.k_pages.get_device():
         raise ValueError("extra must be on %s" % cache.k_pages.device)
     _paged_call("path_paged_reserve", cache, workspace, stream, extra.data_ptr())
 
