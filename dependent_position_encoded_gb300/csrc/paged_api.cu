@@ -87,15 +87,16 @@ path_status check_workspace(const void *ws, size_t bytes, size_t need) {
 // one-pass kernel on the CUDA cores scores them from registers and needs one launch more for
 // the join, where the block kernels need three; but it does G products per key on the CUDA cores.
 // Measured for bf16 (us, one-pass / block kernels), by query heads x cached positions of the
-// whole cache: 2,400 at G = 1: 10 / 17; 2^18 at G = 1: 27 / 29; 2^18 at G = 4: 32 / 29; 2^20 at
-// G = 4: 69 / 50; 2^22 at G = 1: 240 / 221; 2^23 at G = 4 with gates: 536 / 283. With gates and
-// G = 1 the one-pass kernel leaves most value rows unread: 240 / 252 at 2^22. fp32 has no tensor
-// path: one-pass wherever it takes G.
+// whole cache. G = 1: 2,400: 8.5 / 16.5; 2^18: 27 / 31 (d = 64), 43 / 50 (d = 128); 2^19: 45 / 48,
+// 80 / 80; 2^20: 77 / 75; 2^22: 238 / 216. G = 4: 2^15: 12.5 / 16.5; 2^16: 16.5 / 23; 2^17: 23 / 21,
+// 23 / 27; 2^18: 33 / 25; 2^20: 68 / 51. G = 4 with gates: 2^17: 41 / 29; 2^23: 529 / 256. With
+// gates and G = 1 the one-pass kernel leaves most value rows unread: 17 / 23 at 2^15, 237 / 242 at
+// 2^22. fp32 has no tensor path: one-pass wherever it takes G.
 bool one_pass(const Cache &c, int max_chunk, bool bf16, bool fox) {
     if (max_chunk != 1 || !paged::decode_takes(c.G)) return false;
     if (!bf16 || (fox && c.G == 1)) return true;
     const long long positions = ((long long)c.max_pages << c.page_shift) * c.seqs * c.Hq;
-    return positions <= (1 << 18);
+    return positions <= (c.G == 1 ? 1 << 18 : fox ? 1 << 16 : 1 << 17);
 }
 
 size_t step_ws_bytes(const path_paged_cache *p, int N, int max_chunk, bool fox) {
