@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
 // Chunks of several blocks: the new keys of a block through the later ones, Y <- Y P_b for
 // b = c + 1 .. last, into their pages; and the identity through all blocks, which gives the
 // chunk's own product. Y is split into 16-bit pairs at every step, its sum stays in fp32
-// registers (Y + Y (P_b - I)), four warps of 16 rows each. A chain of all blocks would be as
+// registers (Y + Y (P_b - I)), eight warps of 16 rows and half of the columns each. A chain of all blocks would be as
 // long as the chunk, so it goes in two passes over groups of kGroup blocks: to the group's
 // end (and the group's product), then over the later groups' products. Each step waits for
 // 2 D^2 bf16 from L2 and for its MMAs, two CTAs to an SM: 46 + 27 us for 2,048 tokens of 8 key
@@ -587,13 +587,14 @@ __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;
 // identity for each of `idents` groups (pass 2: sequences), then the slots. A chunk of one group
 // is done after pass 1.
 template <int D, int PASS>
-__global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs y, int idents) {
+__global__ void __launch_bounds__(kThr) tc_carry_kernel(const Step a, const TcWs y, int idents) {
     using S = CarrySmem<D>;
-    constexpr int LDD = S::LDD, NT = D / 8, PER = D / 8;
+    constexpr int LDD = S::LDD, NT = D / 16, PER = D / 8;
     extern __shared__ __align__(16) uint8_t smem[];
     bf *const Mh = reinterpret_cast<bf *>(smem + S::Mh), *const Ml = reinterpret_cast<bf *>(smem + S::Ml),
        *const Yh = reinterpret_cast<bf *>(smem + S::Yh), *const Yl = reinterpret_cast<bf *>(smem + S::Yl);
-    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, m0 = 16 * warp;
+    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int m0 = 16 * (warp & 3), n0 = D / 2 * (warp >> 2);  // the warp's 16 rows and half of the columns
     const bool ident = (int)blockIdx.x < idents * (D / 64);
     int b, c = 0, tile = 0, grp = 0, slot = 0;
     Seq s;
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = (8 * n + q + (i & 1) == r + 8 * (i >> 1)) ? 1.f : 0.f;
+            for (int i = 0; i < 4; ++i) acc[n][i] = (n0 + 8 * n + q + (i & 1) == r + 8 * (i >> 1)) ? 1.f : 0.f;
     } else {
         const size_t bh = (size_t)slot * a.c.Hkv + h, base = PASS == 1 ? bh * (kC + D) : bh * kC;
         const bf *const ph = PASS == 1 ? y.kh : y.ch, *const pl = PASS == 1 ? y.kl : y.cl;
@@ -630,7 +631,7 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const size_t at = (base + m0 + (lane >> 2) + 8 * i) * D + 8 * n + 2 * (lane & 3);
+                const size_t at = (base + m0 + (lane >> 2) + 8 * i) * D + n0 + 8 * n + 2 * (lane & 3);
                 const float2 p = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(ph + at));
                 const float2 q = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(pl + at));
                 acc[n][2 * i] = p.x + q.x;
@@ -646,12 +647,12 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
         const bf *const ph = PASS == 1 ? y.kh + at : y.gp + at, *const pl = PASS == 1 ? y.kl + at : ph + D * D;
         __syncthreads();
 #pragma unroll 4
-        for (int e = tid; e < D * PER; e += 128) {
+        for (int e = tid; e < D * PER; e += kThr) {
             const int r = e / PER, q = e % PER * 8;
             cp16(Mh + r * LDD + q, ph + (size_t)r * D + q);
             cp16(Ml + r * LDD + q, pl + (size_t)r * D + q);
         }
-        each_pair(acc, m0, 0, [&](int i, int j, float p, float q) {
+        each_pair(acc, m0, n0, [&](int i, int j, float p, float q) {
             uint32_t hi, lo;
             split2(p, q, hi, lo);
             put2(Yh, LDD, i, j, hi);
@@ -659,14 +660,14 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
         });
         cp_wait_all();
         __syncthreads();
-        warp_mma_3<NT, true>(acc, Yh, Yl, LDD, m0, Mh, Ml, LDD, 0, D / 16);
+        warp_mma_3<NT, true>(acc, Yh, Yl, LDD, m0, Mh, Ml, LDD, n0, D / 16);
     }
     const bool done = PASS == 2 || ng == 1;
     if (ident) {
         bf *const mh = done ? y.mt + (mt_row(a, s, b) * a.c.Hkv + h) * 2 * D * D
                             : y.gp + ((size_t)group_of(s, b, grp) * a.c.Hkv + h) * 2 * D * D;
         bf *const ml = mh + (size_t)D * D;
-        each_pair(acc, 64 * tile + m0, 0, [&](int i, int j, float p, float q) {
+        each_pair(acc, 64 * tile + m0, n0, [&](int i, int j, float p, float q) {
             uint32_t hi, lo;
             split2(p - (i == j), q - (i == j + 1), hi, lo);
             *reinterpret_cast<uint32_t *>(mh + (size_t)i * D + j) = hi;
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
     }
     if (!done && grp + 1 < ng) {
         const size_t base = ((size_t)slot * a.c.Hkv + h) * kC;
-        each_pair(acc, m0, 0, [&](int i, int j, float p, float q) {
+        each_pair(acc, m0, n0, [&](int i, int j, float p, float q) {
             uint32_t hi, lo;
             split2(p, q, hi, lo);
             *reinterpret_cast<uint32_t *>(y.ch + (base + i) * D + j) = hi;
@@ -686,7 +687,7 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
     }
     if (PASS == 2 && grp + 1 == ng) return;  // the last group's keys went to the pages in pass 1
     const int rows = min(kC, s.T - c * kC);
-    each_pair(acc, m0, 0, [&](int i, int j, float p, float q) {
+    each_pair(acc, m0, n0, [&](int i, int j, float p, float q) {
         if (i >= rows) return;
         const int pos = s.n + c * kC + i, id = page_of(a, a.c.k_table, b, pos >> a.c.page_shift, a.c.nk);
         if (id >= 0)
@@ -696,7 +697,7 @@ __global__ void __launch_bounds__(128) tc_carry_kernel(const Step a, const TcWs 
                 pack_bf16x2(p, q);
     });
     if (a.log_f != nullptr)
-        for (int e = tid; e < rows * a.c.G; e += 128) {
+        for (int e = tid; e < rows * a.c.G; e += kThr) {
             const int r = e % rows, hq = h * a.c.G + e / rows, pos = s.n + c * kC + r;
             double g = y.gt[((size_t)slot * a.c.Hq + hq) * kC + r];
             for (int kb = c + 1; kb < nb; ++kb) g += y.gtot[(size_t)slot_of(s, b, kb) * a.c.Hq + hq];
@@ -986,10 +987,10 @@ cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
         (e = big_smem(tc_carry_kernel<D, 2>, CarrySmem<D>::bytes)) != cudaSuccess)
         return e;
     const int slots = slots_of(a.N, a.c.seqs), groups = slots / kGroup + a.c.seqs;
-    e = launch(tc_carry_kernel<D, 1>, dim3(groups * (D / 64) + slots, a.c.Hkv), 128, CarrySmem<D>::bytes, stream, false,
+    e = launch(tc_carry_kernel<D, 1>, dim3(groups * (D / 64) + slots, a.c.Hkv), kThr, CarrySmem<D>::bytes, stream, false,
                a, y, groups);
     if (e == cudaSuccess && a.max_chunk > kC * kGroup)
-        e = launch(tc_carry_kernel<D, 2>, dim3(a.c.seqs * (D / 64) + slots, a.c.Hkv), 128, CarrySmem<D>::bytes, stream,
+        e = launch(tc_carry_kernel<D, 2>, dim3(a.c.seqs * (D / 64) + slots, a.c.Hkv), kThr, CarrySmem<D>::bytes, stream,
                    false, a, y, a.c.seqs);
     return e;
 }

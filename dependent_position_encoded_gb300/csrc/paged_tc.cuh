@@ -203,14 +203,16 @@ __device__ __forceinline__ void warp_mma_a2(float (&acc)[NT][4], const __nv_bflo
             frag_a(c, Al, lda, m0, 16 * k);
         }
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-            uint32_t b[4];
-            if (BN) frag_b(b, B, ldb, n0 + 8 * n, 16 * k);
-            else frag_bt(b, B, ldb, n0 + 8 * n, 16 * k);
-            mma_bf16(acc[n], a, b[0], b[1]);
-            mma_bf16(acc[n + 1], a, b[2], b[3]);
-            mma_bf16(acc[n], c, b[0], b[1]);
-            mma_bf16(acc[n + 1], c, b[2], b[3]);
+        for (int n = 0; n < NT; n += 4) {  // products of one accumulator four apart
+            uint32_t b[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (BN) frag_b(b[i], B, ldb, n0 + 8 * n + 16 * i, 16 * k);
+                else frag_bt(b[i], B, ldb, n0 + 8 * n + 16 * i, 16 * k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_bf16(acc[n + i], a, b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_bf16(acc[n + i], c, b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
         }
     }
 }
@@ -225,21 +227,23 @@ __device__ __forceinline__ void warp_mma_3(float (&acc)[NT][4], const __nv_bfloa
         frag_a(a, Ah, lda, m0, 16 * k);
         frag_a(c, Al, lda, m0, 16 * k);
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-            uint32_t b[4], l[4];
-            if (BN) {
-                frag_b(b, Bh, ldb, n0 + 8 * n, 16 * k);
-                frag_b(l, Bl, ldb, n0 + 8 * n, 16 * k);
-            } else {
-                frag_bt(b, Bh, ldb, n0 + 8 * n, 16 * k);
-                frag_bt(l, Bl, ldb, n0 + 8 * n, 16 * k);
-            }
-            mma_bf16(acc[n], a, b[0], b[1]);
-            mma_bf16(acc[n + 1], a, b[2], b[3]);
-            mma_bf16(acc[n], c, b[0], b[1]);
-            mma_bf16(acc[n + 1], c, b[2], b[3]);
-            mma_bf16(acc[n], a, l[0], l[1]);
-            mma_bf16(acc[n + 1], a, l[2], l[3]);
+        for (int n = 0; n < NT; n += 4) {  // products of one accumulator four apart
+            uint32_t b[2][4], l[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (BN) {
+                    frag_b(b[i], Bh, ldb, n0 + 8 * n + 16 * i, 16 * k);
+                    frag_b(l[i], Bl, ldb, n0 + 8 * n + 16 * i, 16 * k);
+                } else {
+                    frag_bt(b[i], Bh, ldb, n0 + 8 * n + 16 * i, 16 * k);
+                    frag_bt(l[i], Bl, ldb, n0 + 8 * n + 16 * i, 16 * k);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_bf16(acc[n + i], a, b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_bf16(acc[n + i], c, b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_bf16(acc[n + i], a, l[i >> 1][2 * (i & 1)], l[i >> 1][2 * (i & 1) + 1]);
         }
     }
 }
