@@ -838,12 +838,12 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
     uint32_t *const tslot = reinterpret_cast<uint32_t *>(sm + L::bars + 8 * L::count);
     volatile uint32_t *const abort_f = tslot + 1, *const need = tslot + L::need;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y, G = a.c.G;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.x % a.c.Hkv, G = a.c.G;
     int b, ti;
     Seq s;
     grid_wait();
-    // later rows walk further: the last tiles first
-    if (!tile_of(a, gridDim.x - 1 - blockIdx.x, 128, b, ti, s)) return;
+    // later rows walk further: the last tiles first, those of all key heads
+    if (!tile_of(a, (int)((gridDim.x - 1 - blockIdx.x) / a.c.Hkv), 128, b, ti, s)) return;
     const int row0 = 128 * ti, rows_all = s.T * G, per_block = kC * G;
     const int hi = (min(row0 + 128, rows_all) - 1) / per_block, steps = hi;
     if (steps <= 0) return;
@@ -1197,7 +1197,7 @@ cudaError_t launch_scan(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStr
     auto kern = tc_scan_kernel<D, FOX>;
     const cudaError_t e = big_smem(kern, ScanSmem<D>::alloc);
     if (e != cudaSuccess) return e;
-    return launch(kern, dim3(tile_slots(a.N, a.c.G, a.c.seqs, 128), a.c.Hkv), kScanThr, ScanSmem<D>::alloc, stream,
+    return launch(kern, dim3(tile_slots(a.N, a.c.G, a.c.seqs, 128) * a.c.Hkv), kScanThr, ScanSmem<D>::alloc, stream,
                   false, a, y, tr, tv, limit_ns);
 }
 

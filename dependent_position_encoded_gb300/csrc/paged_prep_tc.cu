@@ -583,9 +583,9 @@ __device__ __forceinline__ void cp16(void *dst, const void *src) {
 }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// PASS 1: within the group; PASS 2: over the groups behind. grid.x: D / 64 row tiles of the
-// identity for each of `idents` groups (pass 2: sequences), then the slots. A chunk of one group
-// is done after pass 1.
+// PASS 1: within the group; PASS 2: over the groups behind. The grid, key heads within: D / 64 row
+// tiles of the identity for each of `idents` groups (pass 2: sequences), the longest chains, then
+// the slots. A chunk of one group is done after pass 1.
 template <int D, int PASS>
 __global__ void __launch_bounds__(kThr) tc_carry_kernel(const Step a, const TcWs y, int idents) {
     using S = CarrySmem<D>;
@@ -593,24 +593,25 @@ __global__ void __launch_bounds__(kThr) tc_carry_kernel(const Step a, const TcWs
     extern __shared__ __align__(16) uint8_t smem[];
     bf *const Mh = reinterpret_cast<bf *>(smem + S::Mh), *const Ml = reinterpret_cast<bf *>(smem + S::Ml),
        *const Yh = reinterpret_cast<bf *>(smem + S::Yh), *const Yl = reinterpret_cast<bf *>(smem + S::Yl);
-    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.x % a.c.Hkv, at = blockIdx.x / a.c.Hkv;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int m0 = 16 * (warp & 3), n0 = D / 2 * (warp >> 2);  // the warp's 16 rows and half of the columns
-    const bool ident = (int)blockIdx.x < idents * (D / 64);
+    const bool ident = at < idents * (D / 64);
     int b, c = 0, tile = 0, grp = 0, slot = 0;
     Seq s;
     grid_wait();
     float acc[NT][4];
     zero_acc(acc);
     if (ident) {
-        tile = blockIdx.x % (D / 64);
+        tile = at % (D / 64);
         if (PASS == 1) {
-            if (!group_at(a, blockIdx.x / (D / 64), b, grp, s)) return;
+            if (!group_at(a, at / (D / 64), b, grp, s)) return;
         } else {
-            b = blockIdx.x / (D / 64);
+            b = at / (D / 64);
             s = seq_of(a, b);
         }
     } else {
-        slot = blockIdx.x - idents * (D / 64);
+        slot = at - idents * (D / 64);
         if (!block_of(a, slot, b, c, s)) return;
         grp = c / kGroup;
     }
@@ -987,11 +988,11 @@ cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
         (e = big_smem(tc_carry_kernel<D, 2>, CarrySmem<D>::bytes)) != cudaSuccess)
         return e;
     const int slots = slots_of(a.N, a.c.seqs), groups = slots / kGroup + a.c.seqs;
-    e = launch(tc_carry_kernel<D, 1>, dim3(groups * (D / 64) + slots, a.c.Hkv), kThr, CarrySmem<D>::bytes, stream, false,
-               a, y, groups);
+    e = launch(tc_carry_kernel<D, 1>, dim3((groups * (D / 64) + slots) * a.c.Hkv), kThr, CarrySmem<D>::bytes, stream,
+               false, a, y, groups);
     if (e == cudaSuccess && a.max_chunk > kC * kGroup)
-        e = launch(tc_carry_kernel<D, 2>, dim3(a.c.seqs * (D / 64) + slots, a.c.Hkv), kThr, CarrySmem<D>::bytes, stream,
-                   false, a, y, a.c.seqs);
+        e = launch(tc_carry_kernel<D, 2>, dim3((a.c.seqs * (D / 64) + slots) * a.c.Hkv), kThr, CarrySmem<D>::bytes,
+                   stream, false, a, y, a.c.seqs);
     return e;
 }
 
