@@ -802,9 +802,10 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
 // end the state is the query carried to the chunk's start.
 // Per step the logits go first, so that the softmax runs beside the state's product and copy,
 // which are the chain from step to step. Bound by that chain and the softmax (3,000 cycles a step
-// with gates at D = 64): 113 us for 2,048 tokens of 32 heads at
-// D = 128 (0.59 PFLOP/s), 70 us for four chunks of up to 1,500 tokens, 16 heads, D = 64, gates (91
-// without leaving out the blocks whose gates have closed).
+// with gates at D = 64): 102 us for 2,048 tokens of 32 heads at
+// D = 128 (0.65 PFLOP/s; 113 with the tiles of one key head after the other's), 65 us for four
+// chunks of up to 1,500 tokens, 16 heads, D = 64, gates (91 before the blocks whose gates have
+// closed were left out, 70 head by head).
 // Warps: 0-3 softmax, one row per thread; 4-7 the bf16 copy of the state; 8 allocates TMEM and
 // issues the MMAs; 9 streams [k~_b; P_b - I] and V_b.
 template <int D>

@@ -550,8 +550,8 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
 // registers (Y + Y (P_b - I)), eight warps of 16 rows and half of the columns each. A chain of all blocks would be as
 // long as the chunk, so it goes in two passes over groups of kGroup blocks: to the group's
 // end (and the group's product), then over the later groups' products. Each step waits for
-// 2 D^2 bf16 from L2 and for its MMAs, two CTAs to an SM: 46 + 27 us for 2,048 tokens of 8 key
-// heads at D = 128, 29 + 17 us for four chunks of up to 1,500 at D = 64.
+// 2 D^2 bf16 from L2 and for its MMAs, two CTAs to an SM: 47 + 21 us for 2,048 tokens of 8 key
+// heads at D = 128, 25 + 14 us for four chunks of up to 1,500 at D = 64.
 constexpr int kGroup = 8;
 
 template <int D>
