@@ -154,13 +154,13 @@ __device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid, 
 }
 
 // The kernels of one call follow each other as programmatic dependents: the next one's CTAs
-// may come up (barriers, tensor memory) while the last ones of the one before still run, and
-// wait here before they touch memory. Every CTA waits before anything else that counts, so a
-// kernel's end implies the ends of all before it.
-__device__ __forceinline__ void grid_wait() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
+// may come up (barriers, tensor memory) while the last ones of the one before still run. Up to
+// grid_wait they read only what the caller gave (cu_tokens, lengths, tables, the step's own
+// tensors: complete since before the call's first kernel, which is launched as any other) and
+// write nothing that an earlier kernel of the call reads or writes. Every CTA waits, also those
+// without work, so a kernel's end implies the ends of all before it.
+__device__ __forceinline__ void grid_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Launch behind another kernel of the same call (first: behind whatever the stream holds).
 template <typename... P, typename... A>

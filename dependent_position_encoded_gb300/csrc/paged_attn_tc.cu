@@ -222,6 +222,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
     volatile uint32_t *const abort_f = tslot + 1;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.c.G;
+    grid_begin();
     grid_wait();
     if (base & 1023u) {  // the swizzle's atoms need it; the kernel has no other shared memory
         report_status(a.status, kStatusTimeout);
@@ -842,9 +843,11 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.x % a.c.Hkv, G = a.c.G;
     int b, ti;
     Seq s;
-    grid_wait();
+    grid_begin();
     // later rows walk further: the last tiles first, those of all key heads
-    if (!tile_of(a, (int)((gridDim.x - 1 - blockIdx.x) / a.c.Hkv), 128, b, ti, s)) return;
+    const bool mine = tile_of(a, (int)((gridDim.x - 1 - blockIdx.x) / a.c.Hkv), 128, b, ti, s);
+    grid_wait();
+    if (!mine) return;
     const int row0 = 128 * ti, rows_all = s.T * G, per_block = kC * G;
     const int hi = (min(row0 + 128, rows_all) - 1) / per_block, steps = hi;
     if (steps <= 0) return;

@@ -77,7 +77,7 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
     __shared__ float sm_o[G][SLOTS][D];
 
     const int sp = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-    grid_wait();  // the first of the call: it only lets the merge come up
+    grid_begin();  // the first of the call: nothing to wait for
     const Seq s = seq_of(a, b);
     const int j0 = sp * chunk, j1 = min(j0 + chunk, s.n);
     if (s.T == 0 || j0 >= j1) return;  // the merge skips the splits past n
@@ -280,9 +280,13 @@ __global__ void __launch_bounds__(D)
 paged_decode_merge(const Step a, int chunk, int nsplit, const float *__restrict__ part) {
     __shared__ float red[D / 32];
     const int hq = blockIdx.x, b = blockIdx.y, c = threadIdx.x;
-    grid_wait();
+    grid_begin();
     const Seq s = seq_of(a, b);
-    if (s.T == 0) return;
+    if (s.T == 0) {
+        grid_wait();
+        return;
+    }
+    // the new token's own part, while the splits still run (they read nothing from position n on)
     const int h = hq / a.c.G;
     const T kt = static_cast<const T *>(a.k)[s.first * a.sk.tok + h * a.sk.head + c];
     const T vt = static_cast<const T *>(a.v)[s.first * a.sv.tok + h * a.sv.head + c];
@@ -307,6 +311,7 @@ paged_decode_merge(const Step a, int chunk, int nsplit, const float *__restrict_
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) dsum += red[i];
     const float x_new = dsum * a.scale_log2;
+    grid_wait();
     const int used = (s.n + chunk - 1) / chunk;
     const float *pp = part + ((size_t)b * a.c.Hq + hq) * nsplit * (D + 2);
     float M = x_new;

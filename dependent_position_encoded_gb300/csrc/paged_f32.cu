@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y
     const int ty = tid >> 4, tx = tid & 15;
     int b, c;
     Seq s;
-    grid_wait();
+    grid_begin();  // the first of the call: nothing to wait for
     if (!block_of(a, slot, b, c, s)) return;
     const int i0 = c * kC, rows = min(kC, s.T - i0);
     const long long first = s.first + i0;
@@ -417,8 +417,10 @@ __global__ void __launch_bounds__(kThr) f32_scan_kernel(const Step a, const Ws y
     const int ty = tid >> 4, tx = tid & 15;
     int b, c;
     Seq s;
+    grid_begin();
+    const bool mine = block_of(a, slot, b, c, s) && c > 0;
     grid_wait();
-    if (!block_of(a, slot, b, c, s) || c == 0) return;
+    if (!mine) return;
     const size_t bq = (size_t)slot * a.c.Hq + hq;
     float *const part = y.part + bq * (1 + y.splits) * kPart<D>;
     load_rows<D>(X, y.qt + bq * kC * D);
@@ -513,8 +515,10 @@ __global__ void __launch_bounds__(kThr) f32_cached_kernel(const Step a, const Ws
     const int ty = tid >> 4, tx = tid & 15;
     int b, c, j0, j1;
     Seq s;
+    grid_begin();
+    const bool mine = block_of(a, slot, b, c, s);
     grid_wait();
-    if (!block_of(a, slot, b, c, s)) return;
+    if (!mine) return;
     split_range(s.n, y.splits, sp, j0, j1);
     if (j0 >= j1) return;
     const size_t bq = (size_t)slot * a.c.Hq + hq;
@@ -579,8 +583,10 @@ __global__ void __launch_bounds__(kThr) f32_combine_kernel(const Step a, const W
     const int r = blockIdx.z * 8 + (threadIdx.x >> 5);
     int b, c;
     Seq s;
+    grid_begin();
+    const bool mine = block_of(a, slot, b, c, s) && r < s.T - c * kC;
     grid_wait();
-    if (!block_of(a, slot, b, c, s) || r >= s.T - c * kC) return;
+    if (!mine) return;
     const int tiles = (s.n + kC - 1) / kC, per = (tiles + y.splits - 1) / y.splits;
     const int used = 1 + (per > 0 ? (tiles + per - 1) / per : 0);
     const float *p0 = y.part + ((size_t)slot * a.c.Hq + hq) * (1 + y.splits) * kPart<D>;
@@ -636,6 +642,7 @@ __global__ void __launch_bounds__(kThr) f32_carry_kernel(const Step a, const Ws 
     const bool ident = (int)blockIdx.x >= nslots;
     int b, c = -1;
     Seq s;
+    grid_begin();
     grid_wait();
     int tile = 0;
     if (ident) {
@@ -716,8 +723,9 @@ __global__ void __launch_bounds__(kThr) f32_transform_kernel(const Step a, const
     float *K = sm, *P = K + NH * TILE;
     int *kid = reinterpret_cast<int *>(P + NH * NH * TILE);
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    grid_wait();
+    grid_begin();
     const Seq s = seq_of(a, b);
+    grid_wait();
     if (s.T == 0 || (int)blockIdx.x * kC >= s.n) return;
     const int nb = (s.T + kC - 1) / kC;
 #pragma unroll

@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kPlanThr) fork_plan_kernel(const Cache c, cons
     const Pool p = pool_of(c, y, half);
     const int pairs = src.n;
     bool bad = false;
-    grid_wait();  // the first of the call: it only lets the copies come up
+    grid_begin();  // the first of the call: nothing to wait for
     if (tid == 0) y.go[0] = 0;
     for (int i = warp; i < pairs; i += kHalfWarps) {
         const int n = c.lens[src.row[i]];
@@ -266,6 +266,7 @@ __device__ __forceinline__ void copy_page(char *dst, const char *src, int heads,
 template <int N>
 __global__ void __launch_bounds__(256) fork_copy_kernel(const Cache c, const Rows<N> src, const Rows<N> dst,
                                                         int row_bytes, const PagesWs y) {
+    grid_begin();
     grid_wait();
     if (y.go[0] == 0) return;
     const int s = blockIdx.x, i = blockIdx.y;
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kPlanThr) compact_plan_kernel(const Cache c, c
     const Pool p = pool_of(c, y, half);
     const int most = max(c.nk, c.nv);
     int live = 0;
-    grid_wait();  // the first of the call: it only lets the moves come up
+    grid_begin();  // the first of the call: nothing to wait for
     for (long long base = 0; base < most; base += kHalf * kItems) {
         int r[kItems];
         load_counts(p, base + t * kItems, r);
@@ -361,6 +362,7 @@ __global__ void __launch_bounds__(kPlanThr) compact_plan_kernel(const Cache c, c
 // CTAs below `table_ctas` renumber the tables' entries, the others move pages.
 __global__ void __launch_bounds__(256) compact_move_kernel(const Cache c, int row_bytes, int table_ctas,
                                                            const PagesWs y) {
+    grid_begin();
     grid_wait();
     if ((int)blockIdx.x < table_ctas) {
         const long long per = (long long)c.seqs * c.max_pages;

@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
     const int G = a.c.G;
     int b, c;
     Seq s;
-    grid_wait();  // the first of the call: it only lets the next one come up
+    grid_begin();  // the first of the call: nothing to wait for
     if ((int)blockIdx.x == gridDim.x - 1) {  // the CTA behind the slots
         if (h == 0 && blockIdx.z == 0) make_plans(a, y, reinterpret_cast<long long *>(smem));
         return;
@@ -599,22 +599,25 @@ __global__ void __launch_bounds__(kThr) tc_carry_kernel(const Step a, const TcWs
     const bool ident = at < idents * (D / 64);
     int b, c = 0, tile = 0, grp = 0, slot = 0;
     Seq s;
-    grid_wait();
+    bool mine = true;
+    grid_begin();
     float acc[NT][4];
     zero_acc(acc);
     if (ident) {
         tile = at % (D / 64);
         if (PASS == 1) {
-            if (!group_at(a, at / (D / 64), b, grp, s)) return;
+            mine = group_at(a, at / (D / 64), b, grp, s);
         } else {
             b = at / (D / 64);
             s = seq_of(a, b);
         }
     } else {
         slot = at - idents * (D / 64);
-        if (!block_of(a, slot, b, c, s)) return;
+        mine = block_of(a, slot, b, c, s);
         grp = c / kGroup;
     }
+    grid_wait();
+    if (!mine) return;
     const int nb = (s.T + kC - 1) / kC, ng = (nb + kGroup - 1) / kGroup;
     if (s.T <= kC || grp >= ng || (PASS == 2 && ng == 1)) return;
     if (ident) {
@@ -730,8 +733,9 @@ __global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, con
     extern __shared__ __align__(16) uint8_t smem[];
     bf *const Mh = reinterpret_cast<bf *>(smem + S::Mh), *const Ml = reinterpret_cast<bf *>(smem + S::Ml);
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    grid_wait();
+    grid_begin();
     const Seq s = seq_of(a, b);
+    grid_wait();
     const int strips = (s.n + 31) / 32, per = (strips + (int)gridDim.x - 1) / (int)gridDim.x;
     const int first = (int)blockIdx.x * per, last = min(strips, first + per);
     if ((long long)s.T * a.c.G <= tile_rows || first >= last) return;
@@ -829,8 +833,9 @@ __global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, con
 // sequences of 16,384 positions and 32 heads (67 MB: 4.4 TB/s).
 __global__ void __launch_bounds__(kThr) tc_gates_kernel(const Step a, const TcWs y) {
     const int hq = blockIdx.y, b = blockIdx.z;
-    grid_wait();
+    grid_begin();
     const Seq s = seq_of(a, b);
+    grid_wait();
     if (s.T == 0 || (int)blockIdx.x * kThr * 4 >= s.n) return;
     const int nb = (s.T + kC - 1) / kC;
     double sum = 0.0;
@@ -865,6 +870,19 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
     constexpr int E = D / 32;
     const int G = a.c.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
     const int r0 = (blockIdx.x * (kThr / 32) + warp) * rows, r1 = min(r0 + rows, (int)y.R);  // R <= INT_MAX / 2
+    grid_begin();
+    // the last sequence that begins at or before a token
+    int lo = 0;
+    auto find = [&](int tok) {
+        lo = 0;
+        for (int hi = a.c.seqs - 1; lo < hi;) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (__ldg(a.cu + mid) <= tok) lo = mid;
+            else hi = mid - 1;
+        }
+        return seq_of(a, lo);
+    };
+    Seq s = find(r0 / G);
     grid_wait();
     auto load = [&](const float *p, float (&v)[E]) {
         if (E == 2) {
@@ -885,13 +903,7 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
     for (int r = r0; r < r1; ++r) {
         const int tok = r / G, hq = h * G + (r - tok * G);
         if (r >= known) {
-            int lo = 0, hi = a.c.seqs - 1;  // the last sequence that begins at or before the token
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (__ldg(a.cu + mid) <= tok) lo = mid;
-                else hi = mid - 1;
-            }
-            const Seq s = seq_of(a, lo);
+            if (r > r0) s = find(tok);
             if (tok < s.first || tok >= s.first + s.T) continue;
             const int rows_all = s.T * G;
             start = s.first * G;
