@@ -20,7 +20,7 @@
 //   combine    the softmax parts of a row joined.
 // For results in full precision, not for speed: at two chunks of up to 130 tokens on 1,000
 // cached, 4 heads, D = 64, too few blocks to fill the machine, it is bound by the latency of
-// each kernel's chain of products (prep 43 us, scan 32, cached 21, carry 16, transform 11,
+// each kernel's chain of products (prep 35 us, scan 33, cached 21, carry 16, transform 11,
 // combine 9).
 #include "paged.cuh"
 
@@ -246,6 +246,12 @@ __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y
     if (!block_of(a, slot, b, c, s)) return;
     const int i0 = c * kC, rows = min(kC, s.T - i0);
     const long long first = s.first + i0;
+    // what this CTA forms: the keys' factors, and its query heads' part; one of them, where the
+    // blocks are too few for the machine
+    const int parts = gridDim.z - 1, z = blockIdx.z - 1;
+    const bool keys = blockIdx.z == 0;
+    const int g0 = parts == 0 ? 0 : keys ? 0 : a.c.G * z / parts,
+              g1 = parts == 0 ? a.c.G : keys ? 0 : a.c.G * (z + 1) / parts;
     load_tokens<D>(W, a.w, a.sw, first, h, rows);
     load_tokens<D>(K, a.k, a.sk, first, h, rows);
     if (tid < kC) beta[tid] = tid < rows ? a.beta[(first + tid) * a.sb.tok + h * a.sb.head] : 0.f;
@@ -276,19 +282,21 @@ __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y
     unit_lower_inverse<LD>(A, L, tid, 4);
     for (int e = tid; e < kC * kC; e += kThr) A[(e >> 6) * LD + (e & 63)] *= beta[e & 63];
     __syncthreads();
-#pragma unroll 1
-    for (int x2 = 0; x2 < NH; ++x2) {
-        zero(c0);
-        mm_nn(A, W + x2 * TILE, c0);
-        put_nn(U + x2 * TILE, c0);
-    }
-    zero(c0);
-    mm_nt(R, A, c0);
-    put_nt(S, c0);
-    __syncthreads();
     const size_t bh = (size_t)slot * a.c.Hkv + h;
+    if (keys) {
 #pragma unroll 1
-    for (int x2 = 0; x2 < NH; ++x2) {
+        for (int x2 = 0; x2 < NH; ++x2) {
+            zero(c0);
+            mm_nn(A, W + x2 * TILE, c0);
+            put_nn(U + x2 * TILE, c0);
+        }
+        zero(c0);
+        mm_nt(R, A, c0);
+        put_nt(S, c0);
+        __syncthreads();
+    }
+#pragma unroll 1
+    for (int x2 = 0; x2 < (keys ? NH : 0); ++x2) {
         zero(c0);
         mm_nn(S, W + x2 * TILE, c0);
 #pragma unroll
@@ -311,10 +319,11 @@ __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y
             }
         }
     }
+    if (g0 == g1) return;
     __syncthreads();
     float *V = U;
     load_tokens<D>(V, a.v, a.sv, first, h, rows);
-    for (int g = 0; g < a.c.G; ++g) {
+    for (int g = g0; g < g1; ++g) {
         const int hq = h * a.c.G + g;
         const size_t bq = (size_t)slot * a.c.Hq + hq;
         __syncthreads();
@@ -783,7 +792,9 @@ cudaError_t launch_d(const Step &a, const Ws &y, cudaStream_t stream) {
         (e = big_smem(f32_transform_kernel<D>, transform_smem<D>())) != cudaSuccess)
         return e;
     const long long cap = (long long)a.c.max_pages << a.c.page_shift;
-    e = launch(f32_prep_kernel<D>, dim3(nslots, Hkv), kThr, prep_smem<D>(), stream, true, a, y);
+    // while half of the SMs would be idle, a CTA for the keys and others for the query heads
+    const int room = 152 / (nslots * Hkv), z = room < 2 ? 1 : 1 + (room - 1 < a.c.G ? room - 1 : a.c.G);
+    e = launch(f32_prep_kernel<D>, dim3(nslots, Hkv, z), kThr, prep_smem<D>(), stream, true, a, y);
     if (e == cudaSuccess && a.max_chunk > kC)
         e = launch(f32_scan_kernel<D>, dim3(nslots, Hq), kThr, scan_smem<D>(), stream, false, a, y);
     if (e == cudaSuccess)
