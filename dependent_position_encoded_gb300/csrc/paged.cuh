@@ -84,13 +84,10 @@ __device__ __forceinline__ bool block_of(const Step &a, int slot, int &b, int &c
     return c >= 0 && c * kC < s.T;
 }
 
-// (I + E)^{-1} in fp32 for a strictly lower triangular E (shared, stride LD): the four 16 x 16
-// diagonal blocks by substitution (one column per thread), then X21 = -X22 E21 X11 for the 16-
-// and the 32-blocks; every factor is bounded (products of contractions), so nothing grows.
-// 256 threads. `Y`: 32 x 36 floats of scratch; nt: the 16-row tiles in use (the others are the identity).
+// The four 16 x 16 diagonal blocks of (I + E)^{-1} for a strictly lower triangular E (64 x 64,
+// shared, stride LD), by substitution (one column per thread of the first 64), in place.
 template <int LD>
-__device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid, int nt) {
-    constexpr int YL = 36, kThr = 256;
+__device__ __forceinline__ void diagonal_inverses(float *E, int tid) {
     const int b0 = (tid >> 4) << 4, lu = tid & 15;
     float x[16];
     if (tid < kC) {
@@ -106,6 +103,15 @@ __device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid, 
 #pragma unroll
         for (int l = 0; l < 16; ++l) E[(b0 + l) * LD + tid] = x[l];
     __syncthreads();
+}
+
+// (I + E)^{-1} in fp32: the diagonal blocks, then X21 = -X22 E21 X11 for the 16- and the
+// 32-blocks; every factor is bounded (products of contractions), so nothing grows.
+// 256 threads. `Y`: 32 x 36 floats of scratch; nt: the 16-row tiles in use (the others are the identity).
+template <int LD>
+__device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid, int nt) {
+    constexpr int YL = 36, kThr = 256;
+    diagonal_inverses<LD>(E, tid);
     if (nt <= 1) return;
     // level 1: two 32-blocks at o, X21 (16 x 16)
     for (int pass = 0; pass < 2; ++pass) {

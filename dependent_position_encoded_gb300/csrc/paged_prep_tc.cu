@@ -7,9 +7,9 @@
 // Precision. The inputs are bf16; what is computed from them (A, U, Lq, R A^T, P_b) enters
 // further products as a high and a low bf16 part (16 bits of significand, see split2), so
 // carried keys and transitions are exact to 2^-16 before the cache rounds the keys to bf16.
-// The factor A = (I + D N)^{-1} D is solved in fp32. Rounded to bf16 are the softmax weights,
-// in the scan over a chunk's blocks keys and transitions, and the carried queries (keeps_low says
-// where these have a second part).
+// The 16 x 16 diagonal blocks of A = (I + D N)^{-1} D are solved in fp32. Rounded to bf16 are the
+// softmax weights, in the scan over a chunk's blocks keys and transitions, and the carried
+// queries (keeps_low says where these have a second part).
 #include "paged_tc.cuh"
 
 namespace path {
@@ -221,6 +221,96 @@ __device__ __forceinline__ void prep_single(const Step &a, const TcWs &y, const 
     }
 }
 
+// (I + E)^{-1} as unit_lower_inverse forms it, but with the products behind the diagonal blocks on
+// the warp-level tensor path, their factors as two bf16 parts (what A enters further products
+// with has no more): a factor of the shared fp32 matrix is split as it is loaded, and the first
+// product's sums are the second one's A operand as they lie in registers.
+template <int LD>
+__device__ __forceinline__ void unit_lower_inverse_mma(float *E, int tid, int nt) {
+    diagonal_inverses<LD>(E, tid);
+    if (nt <= 1) return;
+    const int warp = tid >> 5, g = (tid & 31) >> 2, t2 = 2 * (tid & 3);
+    struct A {
+        uint32_t h[4], l[4];
+    };
+    auto a_of = [&](int r0, int k0) {  // 16 x 16 from (r0, k0)
+        A f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v =
+                *reinterpret_cast<const float2 *>(E + (r0 + g + 8 * (i & 1)) * LD + k0 + t2 + 8 * (i >> 1));
+            split2(v.x, v.y, f.h[i], f.l[i]);
+        }
+        return f;
+    };
+    // acc (16 x 8) += a E[k0 .. k0 + 15][n0 .. n0 + 7]
+    auto product = [&](float (&acc)[4], const A &a, int k0, int n0) {
+        uint32_t h[2], l[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float *const p = E + (k0 + t2 + 8 * i) * LD + n0 + g;
+            split2(p[0], p[LD], h[i], l[i]);
+        }
+        mma_bf16(acc, a.h, h[0], h[1]);
+        mma_bf16(acc, a.l, h[0], h[1]);
+        mma_bf16(acc, a.h, l[0], l[1]);
+    };
+    auto a_from = [&](const float (&x)[4], const float (&y)[4]) {  // two 16 x 8 sums side by side
+        A f;
+        split2(x[0], x[1], f.h[0], f.l[0]);
+        split2(x[2], x[3], f.h[1], f.l[1]);
+        split2(y[0], y[1], f.h[2], f.l[2]);
+        split2(y[2], y[3], f.h[3], f.l[3]);
+        return f;
+    };
+    auto put_minus = [&](const float (&x)[4], int r0, int n0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float2 *>(E + (r0 + g + 8 * i) * LD + n0 + t2) = make_float2(-x[2 * i], -x[2 * i + 1]);
+    };
+    if (warp < 2) {  // a warp for the 16-blocks of each 32-block, at o
+        const int o = 32 * warp;
+        const A x22 = a_of(o + 16, o + 16);
+        float t[2][4], x[2][4];
+        zero_acc(t);
+        zero_acc(x);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) product(t[n], x22, o + 16, o + 8 * n);
+        const A ta = a_from(t[0], t[1]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) product(x[n], ta, o, o + 8 * n);
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < 2; ++n) put_minus(x[n], o + 16, o + 8 * n);
+    }
+    __syncthreads();
+    if (nt <= 2) return;
+    // the 32-blocks: a warp for 16 rows and 16 columns
+    const int i0 = 16 * (warp & 1), j0 = 16 * (warp >> 1);
+    float x[2][4];
+    zero_acc(x);
+    if (warp < 4) {
+        float t[4][4];
+        zero_acc(t);
+#pragma unroll 1
+        for (int k = 0; k <= i0; k += 16) {  // X22 is lower triangular
+            const A x22 = a_of(32 + i0, 32 + k);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) product(t[n], x22, 32 + k, 8 * n);
+        }
+        for (int k = j0; k < 32; k += 16) {  // and so is X11
+            const A ta = k == 0 ? a_from(t[0], t[1]) : a_from(t[2], t[3]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) product(x[n], ta, k, j0 + 8 * n);
+        }
+    }
+    __syncthreads();
+    if (warp < 4)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) put_minus(x[n], 32 + i0, j0 + 8 * n);
+    __syncthreads();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const Step a, const TcWs y) {
     using S = PrepSmem<D>;
@@ -349,7 +439,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
     // those of the first heads, by the warps that the inverse's first part leaves idle
     if (a.log_f != nullptr && warp >= 2)
         for (int g = g0 + warp - 2; g < min(g1, g0 + S::kHeads); g += kThr / 32 - 2) gates(g, cums + (g - g0) * kC);
-    unit_lower_inverse<LDF>(F, reinterpret_cast<float *>(Sh), tid, nt);
+    unit_lower_inverse_mma<LDF>(F, tid, nt);
     for (int e = tid; e < kC * kC / 2; e += kThr) {
         const int i = e / 32, j = 2 * (e % 32);
         uint32_t hi, lo;
