@@ -484,12 +484,16 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             float u[4][4];
             zero_acc(u);
             warp_mma_a2<4, true, true>(u, Uh, Ul, LDD, r0, W, LDD, c0, nt);
-            each_pair(u, r0, c0, [&](int i, int j, float p, float q) {
-                uint32_t hi, lo;
-                split2(-p, -q, hi, lo);
-                *reinterpret_cast<uint32_t *>(mh + (size_t)i * D + j) = hi;
-                *reinterpret_cast<uint32_t *>(ml + (size_t)i * D + j) = lo;
-            });
+            each_eight(
+                u, r0, c0,
+                [](int, int, float &p, float &q) {
+                    p = -p;
+                    q = -q;
+                },
+                [&](int i, int j, uint4 hi, uint4 lo) {
+                    *reinterpret_cast<uint4 *>(mh + (size_t)i * D + j) = hi;
+                    *reinterpret_cast<uint4 *>(ml + (size_t)i * D + j) = lo;
+                });
         }
     }
     // k~ = K - S W: into the pages (the chunk's only block) or the block's factors
@@ -499,21 +503,22 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
         float u[4][4];
         zero_acc(u);
         warp_mma_a2<4, false, true>(u, Sh, Sl, LDS, m0, W, LDD, 64 * x + n0, nt, m0 / 16);
-        each_pair(u, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
-            const float2 k2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(K + i * LDD + j));
-            p = k2.x - p;
-            q = k2.y - q;
-            if (single) {
-                const long long at = i < rows ? place(kpage, i, a.c.Hkv, h) : -1;
-                if (at >= 0)
-                    *reinterpret_cast<uint32_t *>(static_cast<bf *>(a.c.k_pages) + at * D + j) = pack_bf16x2(p, q);
-            } else {
-                uint32_t hi, lo;
-                split2(p, q, hi, lo);
-                *reinterpret_cast<uint32_t *>(y.kh + (bh * (kC + D) + i) * D + j) = hi;
-                *reinterpret_cast<uint32_t *>(y.kl + (bh * (kC + D) + i) * D + j) = lo;
-            }
-        });
+        each_eight(
+            u, m0, 64 * x + n0,
+            [&](int i, int j, float &p, float &q) {
+                const float2 k2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(K + i * LDD + j));
+                p = k2.x - p;
+                q = k2.y - q;
+            },
+            [&](int i, int j, uint4 hi, uint4 lo) {
+                if (single) {
+                    const long long at = i < rows ? place(kpage, i, a.c.Hkv, h) : -1;
+                    if (at >= 0) *reinterpret_cast<uint4 *>(static_cast<bf *>(a.c.k_pages) + at * D + j) = hi;
+                } else {
+                    *reinterpret_cast<uint4 *>(y.kh + (bh * (kC + D) + i) * D + j) = hi;
+                    *reinterpret_cast<uint4 *>(y.kl + (bh * (kC + D) + i) * D + j) = lo;
+                }
+            });
     }
     // the block's values: into the pages, and beside the factors for the scan
     if (lead)
@@ -578,15 +583,19 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             float v[4][4];
             zero_acc(v);
             warp_mma_3<4, true>(v, Lh, Ll, LDS, m0, Uh, Ul, LDD, 64 * x + n0, m_end);
-            each_pair(v, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
-                if (i >= rows) return;
-                const float2 q2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(Q + i * LDD + j));
-                // scaled here once, so that the attention's logits need no factor
-                uint32_t hi, lo;
-                split2((q2.x - p) * a.scale_log2, (q2.y - q) * a.scale_log2, hi, lo);
-                *reinterpret_cast<uint32_t *>(y.qt + row_of(i) * D + j) = hi;
-                if (keeps_low(s.T * G <= 128 ? 1 : 2, D)) *reinterpret_cast<uint32_t *>(y.ql + row_of(i) * D + j) = lo;
-            });
+            const bool low = keeps_low(s.T * G <= 128 ? 1 : 2, D);
+            each_eight(
+                v, m0, 64 * x + n0,
+                [&](int i, int j, float &p, float &q) {  // scaled here once: the attention's logits need no factor
+                    const float2 q2 = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(Q + i * LDD + j));
+                    p = (q2.x - p) * a.scale_log2;
+                    q = (q2.y - q) * a.scale_log2;
+                },
+                [&](int i, int j, uint4 hi, uint4 lo) {
+                    if (i >= rows) return;
+                    *reinterpret_cast<uint4 *>(y.qt + row_of(i) * D + j) = hi;
+                    if (low) *reinterpret_cast<uint4 *>(y.ql + row_of(i) * D + j) = lo;
+                });
         }
         __syncthreads();
         // row maxima and sums; the weights, rounded to bf16, for the product with the values: eight
@@ -626,9 +635,22 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             float v[4][4];
             zero_acc(v);
             warp_mma<4, false, true>(v, P, LDS, m0, V, LDD, 64 * x + n0, m_end);
-            each_pair(v, m0, 64 * x + n0, [&](int i, int j, float p, float q) {
-                if (i < rows) *reinterpret_cast<float2 *>(y.po + row_of(i) * D + j) = make_float2(p, q);
-            });
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // eight consecutive columns a lane, as each_eight
+                uint32_t p[4], q[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    p[n] = __float_as_uint(v[n][2 * half]);
+                    q[n] = __float_as_uint(v[n][2 * half + 1]);
+                }
+                quad_turn(p);
+                quad_turn(q);
+                const int i = m0 + (lane >> 2) + 8 * half;
+                if (i >= rows) continue;
+                uint4 *const dst = reinterpret_cast<uint4 *>(y.po + row_of(i) * D + 64 * x + n0 + 8 * (lane & 3));
+                dst[0] = make_uint4(p[0], q[0], p[1], q[1]);
+                dst[1] = make_uint4(p[2], q[2], p[3], q[3]);
+            }
         }
     }
 }
@@ -761,35 +783,41 @@ __global__ void __launch_bounds__(kThr) tc_carry_kernel(const Step a, const TcWs
         bf *const mh = done ? y.mt + (mt_row(a, s, b) * a.c.Hkv + h) * 2 * D * D
                             : y.gp + ((size_t)group_of(s, b, grp) * a.c.Hkv + h) * 2 * D * D;
         bf *const ml = mh + (size_t)D * D;
-        each_pair(acc, 64 * tile + m0, n0, [&](int i, int j, float p, float q) {
-            uint32_t hi, lo;
-            split2(p - (i == j), q - (i == j + 1), hi, lo);
-            *reinterpret_cast<uint32_t *>(mh + (size_t)i * D + j) = hi;
-            *reinterpret_cast<uint32_t *>(ml + (size_t)i * D + j) = lo;
-        });
+        each_eight(
+            acc, 64 * tile + m0, n0,
+            [](int i, int j, float &p, float &q) {
+                p -= i == j;
+                q -= i == j + 1;
+            },
+            [&](int i, int j, uint4 hi, uint4 lo) {
+                *reinterpret_cast<uint4 *>(mh + (size_t)i * D + j) = hi;
+                *reinterpret_cast<uint4 *>(ml + (size_t)i * D + j) = lo;
+            });
         return;
     }
     if (!done && grp + 1 < ng) {
         const size_t base = ((size_t)slot * a.c.Hkv + h) * kC;
-        each_pair(acc, m0, n0, [&](int i, int j, float p, float q) {
-            uint32_t hi, lo;
-            split2(p, q, hi, lo);
-            *reinterpret_cast<uint32_t *>(y.ch + (base + i) * D + j) = hi;
-            *reinterpret_cast<uint32_t *>(y.cl + (base + i) * D + j) = lo;
-        });
+        each_eight(
+            acc, m0, n0, [](int, int, float &, float &) {},
+            [&](int i, int j, uint4 hi, uint4 lo) {
+                *reinterpret_cast<uint4 *>(y.ch + (base + i) * D + j) = hi;
+                *reinterpret_cast<uint4 *>(y.cl + (base + i) * D + j) = lo;
+            });
         return;
     }
     if (PASS == 2 && grp + 1 == ng) return;  // the last group's keys went to the pages in pass 1
     const int rows = min(kC, s.T - c * kC);
-    each_pair(acc, m0, n0, [&](int i, int j, float p, float q) {
-        if (i >= rows) return;
-        const int pos = s.n + c * kC + i, id = page_of(a, a.c.k_table, b, pos >> a.c.page_shift, a.c.nk);
-        if (id >= 0)
-            *reinterpret_cast<uint32_t *>(
-                static_cast<bf *>(a.c.k_pages) +
-                ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) + (pos & (a.c.page - 1))) * D + j) =
-                pack_bf16x2(p, q);
-    });
+    each_eight(
+        acc, m0, n0, [](int, int, float &, float &) {},
+        [&](int i, int j, uint4 hi, uint4) {
+            if (i >= rows) return;
+            const int pos = s.n + c * kC + i, id = page_of(a, a.c.k_table, b, pos >> a.c.page_shift, a.c.nk);
+            if (id >= 0)
+                *reinterpret_cast<uint4 *>(static_cast<bf *>(a.c.k_pages) +
+                                           ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) + (pos & (a.c.page - 1))) *
+                                               D +
+                                           j) = hi;
+        });
     if (a.log_f != nullptr)
         for (int e = tid; e < rows * a.c.G; e += kThr) {
             const int r = e % rows, hq = h * a.c.G + e / rows, pos = s.n + c * kC + r;

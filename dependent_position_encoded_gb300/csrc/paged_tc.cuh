@@ -264,6 +264,55 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = pack_bf16x2(x - h.x, y - h.y);
 }
 
+// Lane t of a quad holds v[n] of four things n; afterwards those of thing t by all four lanes.
+__device__ __forceinline__ void quad_turn(uint32_t (&v)[4]) {
+    const int t = threadIdx.x & 3;
+    uint32_t a = __shfl_xor_sync(0xffffffffu, t & 1 ? v[0] : v[1], 1);
+    uint32_t b = __shfl_xor_sync(0xffffffffu, t & 1 ? v[2] : v[3], 1);
+    if (t & 1) {
+        v[0] = a;
+        v[2] = b;
+    } else {
+        v[1] = a;
+        v[3] = b;
+    }
+    a = __shfl_xor_sync(0xffffffffu, t & 2 ? v[0] : v[2], 2);
+    b = __shfl_xor_sync(0xffffffffu, t & 2 ? v[1] : v[3], 2);
+    if (t & 2) {
+        v[0] = a;
+        v[1] = b;
+    } else {
+        v[2] = a;
+        v[3] = b;
+    }
+}
+
+// A warp's accumulator tile to global memory, eight consecutive columns a lane (a store of a lane's
+// pair of columns instead touches as many lines for a quarter of the bytes, which bounded the
+// preparation): value(row, column, x, y) changes a pair in place, put(row, column, high, low) takes
+// eight columns as split2 gives them. All lanes of the warp take part.
+template <int NT, typename V, typename P>
+__device__ __forceinline__ void each_eight(const float (&acc)[NT][4], int m0, int n0, V value, P put) {
+    const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int r = m0 + (lane >> 2) + 8 * half;
+#pragma unroll
+        for (int n = 0; n < NT; n += 4) {
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x = acc[n + i][2 * half], y = acc[n + i][2 * half + 1];
+                value(r, n0 + 8 * (n + i) + 2 * t, x, y);
+                split2(x, y, h[i], l[i]);
+            }
+            quad_turn(h);
+            quad_turn(l);
+            put(r, n0 + 8 * (n + t), make_uint4(h[0], h[1], h[2], h[3]), make_uint4(l[0], l[1], l[2], l[3]));
+        }
+    }
+}
+
 // fn(row, column, value, value of the next column) over a warp's accumulator tile
 template <int NT, typename F>
 __device__ __forceinline__ void each_pair(float (&acc)[NT][4], int m0, int n0, F fn) {
