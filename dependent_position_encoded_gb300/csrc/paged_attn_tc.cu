@@ -872,6 +872,10 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
     const int own = min(row0 + (r & ~31), rows_all - 1) / per_block;
     const size_t row = (size_t)h * y.R + (size_t)s.first * G + row0 + r;
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    // the four rows of this thread's quad in (Hkv, R, D): null past the sequence's end
+    auto quad = [&](auto *p, int c) {
+        return [=](int i) { return row0 + (r & ~3) + i < rows_all ? p + (row - (r & 3) + i) * D + c : nullptr; };
+    };
 
     if (warp == 9) {
         // ============================================================ factors and values
@@ -954,14 +958,10 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
         float between = 0.f;  // gates of the blocks passed (where they matter the sum is small: fp32 will do)
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
-            float o[32];
+            uint4 u[2][4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float4 v = live ? *reinterpret_cast<const float4 *>(y.po + row * D + c + 4 * q)
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-                o[4 * q] = v.x; o[4 * q + 1] = v.y; o[4 * q + 2] = v.z; o[4 * q + 3] = v.w;
-            }
-            tst32(tmem + lane_off + L::cO + c, o);
+            for (int q = 0; q < 2; ++q) load_quad_rows(u[q], quad(y.po, c + 16 * q));
+            tmem_st32(tmem + lane_off + L::cO + c, reinterpret_cast<uint32_t(&)[32]>(u));
         }
         tmem_st_wait();
         bool ok = true;
@@ -1066,10 +1066,14 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
             for (int c = 0; c < D; c += 32) {
                 float o[32];
                 tld32(tmem + lane_off + L::cO + c, o);
-                if (live) {
-                    float4 *dst = reinterpret_cast<float4 *>(y.po + row * D + c);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                for (int q = 0; q < 2; ++q) {
+                    uint4 u[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        u[e] = make_uint4(__float_as_uint(o[16 * q + 4 * e]), __float_as_uint(o[16 * q + 4 * e + 1]),
+                                          __float_as_uint(o[16 * q + 4 * e + 2]), __float_as_uint(o[16 * q + 4 * e + 3]));
+                    store_quad_rows(u, quad(y.po, c + 16 * q));
                 }
             }
             if (live) {
@@ -1095,12 +1099,12 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             float x[32];
+            uint4 u[4], z[4] = {};
+            load_quad_rows(u, quad(y.qt, c));
+            if (low) load_quad_rows(z, quad(y.ql, c));
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-                const uint4 u = live ? *reinterpret_cast<const uint4 *>(y.qt + row * D + c + 8 * q) : none;
-                const uint4 z = live && low ? *reinterpret_cast<const uint4 *>(y.ql + row * D + c + 8 * q) : none;
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w}, wl[4] = {z.x, z.y, z.z, z.w};
+                const uint32_t w[4] = {u[q].x, u[q].y, u[q].z, u[q].w}, wl[4] = {z[q].x, z[q].y, z[q].z, z[q].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 f = unpack_bf16x2(w[e]), g = unpack_bf16x2(wl[e]);
@@ -1136,17 +1140,17 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
             for (int c = 0; c < D; c += 32) {
                 float x[32];
                 tld32(tmem + lane_off + L::cX + c, x);
-                if (live) {
+                uint4 u[4], z[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t hi[4], lo[4];
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) split2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], lo[e]);
-                        const size_t at = row * D + c + 8 * q;
-                        *reinterpret_cast<uint4 *>(y.qt + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        if (low) *reinterpret_cast<uint4 *>(y.ql + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
+                    for (int e = 0; e < 4; ++e) split2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], lo[e]);
+                    u[q] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    z[q] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
+                store_quad_rows(u, quad(y.qt, c));
+                if (low) store_quad_rows(z, quad(y.ql, c));
             }
         }
     }

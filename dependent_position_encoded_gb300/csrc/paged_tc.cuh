@@ -287,6 +287,45 @@ __device__ __forceinline__ void quad_turn(uint32_t (&v)[4]) {
     }
 }
 
+__device__ __forceinline__ void turn_quad_rows(uint4 (&v)[4]) {
+    uint32_t a[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a[0][i] = v[i].x;
+        a[1][i] = v[i].y;
+        a[2][i] = v[i].z;
+        a[3][i] = v[i].w;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) quad_turn(a[e]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_uint4(a[0][i], a[1][i], a[2][i], a[3][i]);
+}
+
+// 64 bytes of each row, a row per lane: a quad's lanes load (store) 16 bytes each of one of its four
+// rows after the other, so that a load touches eight lines instead of 32. `at(i)`: where lane i of
+// the quad has its bytes, null to leave the row out (zeros). All lanes of the warp take part.
+template <typename F>
+__device__ __forceinline__ void load_quad_rows(uint4 (&v)[4], F at) {
+    const int t = threadIdx.x & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(at(i));
+        v[i] = p != nullptr ? p[t] : make_uint4(0u, 0u, 0u, 0u);
+    }
+    turn_quad_rows(v);
+}
+template <typename F>
+__device__ __forceinline__ void store_quad_rows(uint4 (&v)[4], F at) {
+    const int t = threadIdx.x & 3;
+    turn_quad_rows(v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint4 *p = reinterpret_cast<uint4 *>(at(i));
+        if (p != nullptr) p[t] = v[i];
+    }
+}
+
 // A warp's accumulator tile to global memory, eight consecutive columns a lane (a store of a lane's
 // pair of columns instead touches as many lines for a quarter of the bytes, which bounded the
 // preparation): value(row, column, x, y) changes a pair in place, put(row, column, high, low) takes
