@@ -773,11 +773,19 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
                     tld32(tm + L::cO + c, o);
-                    if (live) {
-                        float4 *dst = reinterpret_cast<float4 *>(y.so[NT - 1] + e * D + c);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    for (int q = 0; q < 2; ++q) {
+                        uint4 u[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            u[i] = make_uint4(__float_as_uint(o[16 * q + 4 * i]), __float_as_uint(o[16 * q + 4 * i + 1]),
+                                              __float_as_uint(o[16 * q + 4 * i + 2]),
+                                              __float_as_uint(o[16 * q + 4 * i + 3]));
+                        store_quad_rows(u, [&](int i) {
+                            return row0 + (rw & ~3) + i < rows_all
+                                       ? y.so[NT - 1] + (e - (r & 3) + i) * D + c + 16 * q
+                                       : nullptr;
+                        });
                     }
                 }
                 if (live) y.sml[NT - 1][e] = make_float2(m_run, l_run);
