@@ -202,6 +202,17 @@ struct Ring {
     }
 };
 
+// How many of a key tile's 128 columns have the weights' second bf16 part (in the columns of the
+// logits that the first leaves free): a weight's rounding is the largest error of an output, 1.4e-3 of
+// the norm beside 1.66e-3 for the output's own, and for longer chunks the carried queries' and the
+// scan's come to it. Behind 1,000 cached keys with T = 300, without and with the second part: D = 64
+// 2.66e-3 and 2.18e-3; D = 128, where the tensor core bounds the pass, so that only half of the columns
+// have it, 2.59e-3 and 2.37e-3 (a quarter: 2.48e-3). It costs 6% at D = 64 (one chunk of 512 in a
+// batch of 32: 232 -> 246 us a step) and 20% of a long chunk at D = 128 (2,048 behind 32,768: 1,143 ->
+// 1,370 us). NT = 1, whose queries have fewer steps behind them, stays at 2.2e-3 without; with
+// gates few keys count: below 2.0e-3.
+__host__ __device__ constexpr int low_weights(int NT, int D, bool fox) { return NT == 1 || fox ? 0 : D == 64 ? 128 : 64; }
+
 // Whether all boxes of a key tile lie on good pages below n: `have` one bit per box of
 // 1 << box_shift rows.
 __device__ __forceinline__ bool tile_whole(int pos0, int n, unsigned have, int box_shift) {
@@ -214,7 +225,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                  const __grid_constant__ CUtensorMap tm_l, const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
     using L = CachedCfg<NT, D>;
-    constexpr int NA = D / 64, NK = L::NK, NV = L::NV;
+    constexpr int NA = D / 64, NK = L::NK, NV = L::NV, kLow = low_weights(NT, D, FOX);
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t base = smem_u32(sm);
     auto bar = [&](int i) { return base + L::bars + 8u * (uint32_t)i; };
@@ -275,7 +286,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             uint32_t j = 0, seg = 0, tmp_phase = 0;
             bool ok = true;
             for (long long at = u_begin; ok && at < u_end; ++seg) {
-                const Stretch t = stretch_at(a, plan, NT, at, u_end);
+                const Stretch t = stretch_at(a, plan, D, NT, at, u_end);
                 at += t.steps;
                 if (keys) {
                     // the rows' tile (and the update's product) once the last stretch's are read
@@ -389,6 +400,10 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 umma_tA(tm + L::cO, tm + L::cS, vd, ID_O, !first);
 #pragma unroll
                 for (int kk = 1; kk < 8; ++kk) umma_tA(tm + L::cO, tm + L::cS + 8 * kk, vd + 128 * kk, ID_O, 1);
+                if (kLow > 0)
+#pragma unroll
+                    for (int kk = 0; kk < kLow / 16; ++kk)
+                        umma_tA(tm + L::cO, tm + L::cS + 64 + 8 * kk, vd + 128 * kk, ID_O, 1);
             };
             // behind the products of the ring's keys; last of a stretch: the rows' tile is free. (Slots are
             // handed back by the softmax's warps, which learn of the products' ends anyway.)
@@ -398,7 +413,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 k.next();
             };
             for (long long at = u_begin; ok && at < u_end; ++seg) {
-                const Stretch t = stretch_at(a, plan, NT, at, u_end);
+                const Stretch t = stretch_at(a, plan, D, NT, at, u_end);
                 at += t.steps;
                 const bool two = second(t);
                 if (!(ok = wait(bar(L::rows_in_tmem ? L::XT : L::XF), seg & 1))) break;
@@ -445,7 +460,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             uint32_t j = 0, seg = 0;
             bool ok = true;
             for (long long at = u_begin; ok && at < u_end; ++seg) {
-                const Stretch t = stretch_at(a, plan, NT, at, u_end);
+                const Stretch t = stretch_at(a, plan, D, NT, at, u_end);
                 at += t.steps;
                 if (!(ok = wait(bar(L::XF), seg & 1))) break;
                 for (int i = 0; i < t.steps; ++i, ++j) {
@@ -475,7 +490,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
         bool ok = true;
         uint32_t j = 0;
         for (long long at = u_begin; ok && at < u_end;) {
-            const Stretch t = stretch_at(a, plan, NT, at, u_end);
+            const Stretch t = stretch_at(a, plan, D, NT, at, u_end);
             at += t.steps;
             int next;  // the key pages of the next tile's boxes
             auto look_up = [&](int pos0) {
@@ -550,7 +565,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
         const bool releases = (warp & 3) == 0 && lane == 0;
         uint32_t j = 0, seg = 0, step = 0;  // steps and stretches with rows in this tile; steps of the CTA
         for (long long at = u_begin; ok && at < u_end;) {
-            const Stretch t = stretch_at(a, plan, NT, at, u_end);
+            const Stretch t = stretch_at(a, plan, D, NT, at, u_end);
             at += t.steps;
             if (w == 1 && !second(t)) {
                 step += t.steps;
@@ -696,14 +711,15 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                         use = m_run == -INFINITY ? 0.f : -m_run;
                     };
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    // 32 weights as 16 bf16 pairs
-                    auto weigh = [&](const float *v, uint32_t *p) {
+                    // 32 weights as 16 bf16 pairs, and what the rounding left as others
+                    auto weigh = [&](const float *v, uint32_t *p, uint32_t *low, bool both) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             const float2 z = fadd2(make_float2(v[e], v[e + 1]), make_float2(use, use));
                             const float2 q = make_float2(ex2_approx(z.x), ex2_approx(z.y));
                             sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], q);
-                            p[e / 2] = pack_bf16x2(q.x, q.y);
+                            if (both) split2(q.x, q.y, p[e / 2], low[e / 2]);
+                            else p[e / 2] = pack_bf16x2(q.x, q.y);
                         }
                     };
                     if (kTwice) {
@@ -726,7 +742,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                                 tld32(tm + L::cS + c, x);
                                 gate(c, x);
                             }
-                            weigh(x, p);
+                            weigh(x, p, p, false);
                             tmem_st16(tm + L::cS + c / 2, p);
                         }
 #pragma unroll
@@ -749,11 +765,11 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                         top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                         raise();
 #pragma unroll
-                        for (int c = 0; c < 128; c += 64) {
-                            uint32_t p[32];
-                            weigh(x + c, p);
-                            weigh(x + c + 32, p + 16);
-                            tmem_st32(tm + L::cS + c / 2, p);
+                        for (int c = 0; c < 128; c += 32) {
+                            uint32_t p[16], l[16];
+                            weigh(x + c, p, l, c < kLow);
+                            tmem_st16(tm + L::cS + c / 2, p);
+                            if (c < kLow) tmem_st16(tm + L::cS + 64 + c / 2, l);
                         }
                     }
                     l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -817,15 +833,24 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
 // closed were left out, 70 head by head).
 // Warps: 0-3 softmax, one row per thread; 4-7 the bf16 copy of the state; 8 allocates TMEM and
 // issues the MMAs; 9 streams [k~_b; P_b - I] and V_b.
-template <int D>
+//
+// LOW: the copy of the state and its own product's factor P_b - I have a second bf16 part. Their
+// roundings gather from step to step in the queries that go on to the cached keys; without gates
+// and at D = 128, where these then are rounded once more, an output's error behind 1,000 cached
+// keys is 2.91e-3 of its norm without, 2.59e-3 with (T = 300; the plain 1.66e-3 is the output's own
+// rounding). The scan takes 94 us without and 180 with for 2,048 tokens of 32 heads. At D = 64 the
+// weights' second part (low_weights) does more for less.
+template <int D, bool LOW>
 struct ScanSmem {
-    static constexpr int NR = 3, NV = 2;
+    // slots of [k~_b; P_b - I], of P_b - I's low part and of values
+    static constexpr int NR = LOW ? 2 : 3, NL = LOW ? 1 : 0, NV = 2;
     static constexpr uint32_t xtile = 128 * D * 2, xatom = 128 * 128, ratom = (64 + D) * 128, rtile = ratom * (D / 64),
-                              vatom = 64 * 128, vtile = vatom * (D / 64);
-    static constexpr uint32_t X = 0, R = X + xtile, V = R + NR * rtile, bars = V + NV * vtile;
-    static constexpr int RF = 0, RE = RF + NR, VF = RE + NR, VE = VF + NV, SD = VE + NV, XD = SD + 1, XR = XD + 1,
-                         SFREE = XR + 1,
-                         PR = SFREE + 1, PV = PR + 1, FIN = PV + 1, count = FIN + 1;
+                              latom = D * 128, ltile = latom * (D / 64), vatom = 64 * 128, vtile = vatom * (D / 64);
+    static constexpr uint32_t X = 0, R = X + (LOW ? 2 : 1) * xtile, P = R + NR * rtile, V = P + NL * ltile,
+                              bars = V + NV * vtile;
+    static constexpr int RF = 0, RE = RF + NR, LF = RE + NR, LE = LF + NL, VF = LE + NL, VE = VF + NV, SD = VE + NV,
+                         XD = SD + 1, XR = XD + 1, SFREE = XR + 1, PR = SFREE + 1, PV = PR + 1, FIN = PV + 1,
+                         count = FIN + 1;
     // behind the barriers: TMEM's address, the abort flag, the last step whose values count (need)
     static constexpr int need = 2;
     static constexpr uint32_t bytes = bars + count * 8 + 16, alloc = bytes + 1024;
@@ -833,13 +858,16 @@ struct ScanSmem {
     static constexpr uint32_t cS = 0, cP = 64, cX = 128, cO = 128 + D, cols = D == 64 ? 256 : 512;
 };
 
+static_assert(ScanSmem<128, true>::alloc <= 227 * 1024, "shared memory");
+__host__ __device__ constexpr bool scan_low(int D, bool fox) { return D == 128 && !fox; }
 constexpr int kScanThr = 320;
 
 template <int D, bool FOX>
 __global__ void __launch_bounds__(kScanThr, D == 64 ? 2 : 1)
 tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap tm_r,
-               const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
-    using L = ScanSmem<D>;
+               const __grid_constant__ CUtensorMap tm_l, const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
+    constexpr bool LOW = scan_low(D, FOX);
+    using L = ScanSmem<D, LOW>;
     constexpr int NA = D / 64;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -888,7 +916,7 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
     if (warp == 9) {
         // ============================================================ factors and values
         if (lane == 0) {
-            int r = 0, v = 0;
+            int r = 0, l = 0, v = 0;
             bool ok = true;
             for (int st = 0; ok && st < steps; ++st) {
                 const int head = slot_of(s, b, hi - 1 - st) * a.c.Hkv + h, i = st % L::NR, q = st % L::NV;
@@ -897,6 +925,13 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
                 for (int x = 0; x < NA; ++x)
                     tma_load_3d(base + L::R + i * L::rtile + x * L::ratom, &tm_r, bar(L::RF + i), 64 * x, 0, head);
                 ++r;
+                if (LOW) {
+                    if (st >= L::NL && !(ok = wait(bar(L::LE), (st - 1) & 1))) break;
+                    mbar_arrive_expect_tx(bar(L::LF), L::ltile);
+                    for (int x = 0; x < NA; ++x)
+                        tma_load_3d(base + L::P + x * L::latom, &tm_l, bar(L::LF), 64 * x, 64, head);
+                    ++l;
+                }
                 if (st >= L::NV && !(ok = wait(bar(L::VE + q), (st / L::NV - 1) & 1))) break;
                 mbar_arrive_expect_tx(bar(L::VF + q), L::vtile);
                 for (int x = 0; x < NA; ++x)
@@ -906,6 +941,7 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
             if (!ok) {  // an abort: no copy may land after the CTA is gone
                 for (int st = r > L::NR ? r - L::NR : 0; st < r; ++st)
                     mbar_wait(bar(L::RF + st % L::NR), (st / L::NR) & 1, limit_ns);
+                if (l > 0) mbar_wait(bar(L::LF), (l - 1) & 1, limit_ns);
                 for (int st = v > L::NV ? v - L::NV : 0; st < v; ++st)
                     mbar_wait(bar(L::VF + st % L::NV), (st / L::NV) & 1, limit_ns);
             }
@@ -935,15 +971,24 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
                 if (st > 0 && !(ok = wait(bar(L::SFREE), (st - 1) & 1))) break;    // the last logits read
                 tc_fence_after();
                 const uint32_t rs = base + L::R + i * L::rtile;
+                // a part of the state with a factor's tile
+                auto product = [&](uint32_t d, int part, uint32_t b, uint32_t batom, uint32_t id, bool first) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16(tmem + L::cS, sdesc_sw128(base + L::X + (kk >> 2) * L::xatom, 16, 1024) + 2 * (kk & 3),
-                              sdesc_sw128(rs + (kk >> 2) * L::ratom, 16, 1024) + 2 * (kk & 3), ID_S, kk > 0);
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        umma_bf16(d, sdesc_sw128(base + L::X + part * L::xtile + (kk >> 2) * L::xatom, 16, 1024) + 2 * (kk & 3),
+                                  sdesc_sw128(b + (kk >> 2) * batom, 16, 1024) + 2 * (kk & 3), id, !first || kk > 0);
+                };
+                product(tmem + L::cS, 0, rs, L::ratom, ID_S, true);
+                if (LOW) product(tmem + L::cS, 1, rs, L::ratom, ID_S, false);
                 umma_commit(bar(L::SD));
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16(tmem + L::cX, sdesc_sw128(base + L::X + (kk >> 2) * L::xatom, 16, 1024) + 2 * (kk & 3),
-                              sdesc_sw128(rs + 64 * 128 + (kk >> 2) * L::ratom, 16, 1024) + 2 * (kk & 3), ID_X, 1);
+                product(tmem + L::cX, 0, rs + 64 * 128, L::ratom, ID_X, false);
+                if (LOW) {
+                    product(tmem + L::cX, 1, rs + 64 * 128, L::ratom, ID_X, false);
+                    if (!(ok = wait(bar(L::LF), st & 1))) break;
+                    tc_fence_after();
+                    product(tmem + L::cX, 0, base + L::P, L::latom, ID_X, false);
+                    umma_commit(bar(L::LE));
+                }
                 umma_commit(bar(L::XD));
                 umma_commit(bar(L::RE + i));
                 // P V of the previous step behind this step's products
@@ -1092,24 +1137,29 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
     } else if (warp < 8) {
         // ============================================================ the state's bf16 copy
         bool ok = true;
-        const bool low = keeps_low(rows_all <= 128 ? 1 : 2, D);  // the state's second part
+        const bool low = keeps_low(one_tile(s.T, G, D, FOX) ? 1 : 2, D);  // of what goes on to the cached keys
         uint8_t *const xs = sm + L::X;
         auto put = [&](int c, const float *x, bool take) {  // 32 columns from c
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float *v = x + 8 * q;
-                *reinterpret_cast<uint4 *>(xs + (c >> 6) * L::xatom + sw128_offset(r, ((c & 63) >> 3) + q)) =
-                    take ? make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                      pack_bf16x2(v[6], v[7]))
-                         : make_uint4(0u, 0u, 0u, 0u);
+                uint32_t hi[4] = {}, lo[4] = {};
+                if (take)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (LOW) split2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1], hi[e], lo[e]);
+                        else hi[e] = pack_bf16x2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1]);
+                uint4 *const at =
+                    reinterpret_cast<uint4 *>(xs + (c >> 6) * L::xatom + sw128_offset(r, ((c & 63) >> 3) + q));
+                at[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                if (LOW) at[L::xtile / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         };
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             float x[32];
-            uint4 u[4], z[4] = {};
+            uint4 u[4], z[4];
             load_quad_rows(u, quad(y.qt, c));
-            if (low) load_quad_rows(z, quad(y.ql, c));
+            load_quad_rows(z, quad(y.ql, c));
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint32_t w[4] = {u[q].x, u[q].y, u[q].z, u[q].w}, wl[4] = {z[q].x, z[q].y, z[q].z, z[q].w};
@@ -1206,15 +1256,17 @@ cudaError_t launch_cached(const Step &a, const TcWs &y, uint64_t limit_ns, cudaS
 
 template <int D, bool FOX>
 cudaError_t launch_scan(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream) {
-    CUtensorMap tr, tv;
+    CUtensorMap tr, tl, tv;
     const long long heads = (long long)slots_of(a.N, a.c.seqs) * a.c.Hkv;
-    if (!make_map(&tr, y.kh, D, 64 + D, heads, 64 + D) || !make_map(&tv, y.vb, D, 64, heads, 64))
+    if (!make_map(&tr, y.kh, D, 64 + D, heads, 64 + D) || !make_map(&tl, y.kl, D, 64 + D, heads, D) ||
+        !make_map(&tv, y.vb, D, 64, heads, 64))
         return cudaErrorInvalidValue;
+    using L = ScanSmem<D, scan_low(D, FOX)>;
     auto kern = tc_scan_kernel<D, FOX>;
-    const cudaError_t e = big_smem(kern, ScanSmem<D>::alloc);
+    const cudaError_t e = big_smem(kern, L::alloc);
     if (e != cudaSuccess) return e;
-    return launch(kern, dim3(tile_slots(a.N, a.c.G, a.c.seqs, 128) * a.c.Hkv), kScanThr, ScanSmem<D>::alloc, stream,
-                  false, a, y, tr, tv, limit_ns);
+    return launch(kern, dim3(tile_slots(a.N, a.c.G, a.c.seqs, 128) * a.c.Hkv), kScanThr, L::alloc, stream, false, a, y,
+                  tr, tl, tv, limit_ns);
 }
 
 }  // namespace
@@ -1224,7 +1276,7 @@ cudaError_t launch_tc_prep(const Step &a, const TcWs &y, cudaStream_t stream);
 template <int D>
 cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream);
 template <int D>
-cudaError_t launch_tc_finish(const Step &a, const TcWs &y, int tile_rows, cudaStream_t stream);
+cudaError_t launch_tc_finish(const Step &a, const TcWs &y, cudaStream_t stream);
 
 namespace {
 
@@ -1237,9 +1289,9 @@ cudaError_t launch_all(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStre
     }
     if (a.c.max_pages > 0 && a.c.nk > 0 && a.c.nv > 0) {
         if (e == cudaSuccess) e = launch_cached<1, D, FOX>(a, y, limit_ns, stream);
-        if (e == cudaSuccess && (long long)a.max_chunk * a.c.G > 128) e = launch_cached<2, D, FOX>(a, y, limit_ns, stream);
+        if (e == cudaSuccess && !one_tile(a.max_chunk, a.c.G, D, FOX)) e = launch_cached<2, D, FOX>(a, y, limit_ns, stream);
     }
-    if (e == cudaSuccess) e = launch_tc_finish<D>(a, y, 128, stream);
+    if (e == cudaSuccess) e = launch_tc_finish<D>(a, y, stream);
     return e;
 }
 
@@ -1266,7 +1318,7 @@ TcLayout tc_layout(const Cache &c, int N, int max_chunk, int d, bool fox) {
     for (int p = 0; p < 2; ++p) {
         // one CTA per SM, or two: every SM of the part (152) has its share of the units
         y.ctas[p] = 152 * (p == 0 && d == 64 ? CachedCfg<1, 64>::ctas_per_sm : 1);
-        const bool used = p == 0 || (long long)max_chunk * c.G > 128;
+        const bool used = p == 0 || !one_tile(max_chunk, c.G, d, fox);
         const size_t tile = 128 * (p + 1);
         const size_t parts =
             used ? y.ctas[p] + (size_t)tile_slots(N, c.G, std::min(c.seqs, N), (int)tile) * c.Hkv : 0;

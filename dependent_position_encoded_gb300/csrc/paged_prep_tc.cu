@@ -8,7 +8,7 @@
 // further products as a high and a low bf16 part (16 bits of significand, see split2), so
 // carried keys and transitions are exact to 2^-16 before the cache rounds the keys to bf16.
 // The 16 x 16 diagonal blocks of A = (I + D N)^{-1} D are solved in fp32. Rounded to bf16 are the
-// softmax weights, in the scan over a chunk's blocks keys and transitions, and the carried
+// softmax weights, in the scan over a chunk's blocks keys and (but for D = 128 without gates) transitions, and the carried
 // queries (keeps_low says where these have a second part).
 #include "paged_tc.cuh"
 
@@ -80,6 +80,7 @@ __device__ __forceinline__ void put2(bf *t, int ld, int r, int c, uint32_t v) {
 // buffers hold what sequences without common tokens can need, so one that begins before an
 // earlier one's begin or end (cu_tokens falls somewhere, which the falling sequence reports) gets
 // no work: with m the largest cu_tokens so far, a sequence counts where cu_tokens = m.
+template <int D>
 __device__ __forceinline__ void make_plans(const Step &a, const TcWs &y, long long *sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int *const tops = reinterpret_cast<int *>(sums + kThr / 32);
@@ -109,7 +110,7 @@ __device__ __forceinline__ void make_plans(const Step &a, const TcWs &y, long lo
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 int tiles, kt;
-                plan_of(s, a.c.G, p + 1, tiles, kt);
+                plan_of(a, s, D, p + 1, tiles, kt);
                 v[2 * p + 1] = kt > 0 ? (long long)tiles * a.c.Hkv : 0;
                 v[2 * p] = v[2 * p + 1] * kt;
             }
@@ -194,7 +195,7 @@ __device__ __forceinline__ void prep_single(const Step &a, const TcWs &y, const 
             const float x = fmaf(-beta * wq, w[e], q[e]) * a.scale_log2;
             const bf xh = __float2bfloat16_rn(x);
             y.qt[r * D + lane * E + e] = xh;
-            if (keeps_low(G <= 128 ? 1 : 2, D)) y.ql[r * D + lane * E + e] = __float2bfloat16_rn(x - __bfloat162float(xh));
+            if (keeps_low(one_tile(1, G, D, a.log_f != nullptr) ? 1 : 2, D)) y.ql[r * D + lane * E + e] = __float2bfloat16_rn(x - __bfloat162float(xh));
             y.po[r * D + lane * E + e] = __bfloat162float(vp[e]);
         }
         if (lane == 0) {
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
     Seq s;
     grid_begin();  // the first of the call: nothing to wait for
     if ((int)blockIdx.x == gridDim.x - 1) {  // the CTA behind the slots
-        if (h == 0 && blockIdx.z == 0) make_plans(a, y, reinterpret_cast<long long *>(smem));
+        if (h == 0 && blockIdx.z == 0) make_plans<D>(a, y, reinterpret_cast<long long *>(smem));
         return;
     }
     if (!block_of(a, slot, b, c, s)) return;
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             float v[4][4];
             zero_acc(v);
             warp_mma_3<4, true>(v, Lh, Ll, LDS, m0, Uh, Ul, LDD, 64 * x + n0, m_end);
-            const bool low = keeps_low(s.T * G <= 128 ? 1 : 2, D);
+            const bool low = !single || keeps_low(one_tile(s.T, G, D, a.log_f != nullptr) ? 1 : 2, D);  // the scan starts from both
             each_eight(
                 v, m0, 64 * x + n0,
                 [&](int i, int j, float &p, float &q) {  // scaled here once: the attention's logits need no factor
@@ -845,7 +846,7 @@ struct TransformSmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, const TcWs y, int tile_rows) {
+__global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, const TcWs y) {
     using S = TransformSmem<D>;
     constexpr int LDD = S::LDD, NT = D / 8, PER = D / 8;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -856,7 +857,7 @@ __global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, con
     grid_wait();
     const int strips = (s.n + 31) / 32, per = (strips + (int)gridDim.x - 1) / (int)gridDim.x;
     const int first = (int)blockIdx.x * per, last = min(strips, first + per);
-    if ((long long)s.T * a.c.G <= tile_rows || first >= last) return;
+    if (one_tile(s.T, a.c.G, D, a.log_f != nullptr) || first >= last) return;
     const bf *const m = y.mt + (mt_row(a, s, b) * a.c.Hkv + h) * 2 * D * D;
 #pragma unroll 4
     for (int e = tid; e < D * PER; e += kThr) {
@@ -1026,10 +1027,10 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
             const int rows_all = s.T * G;
             start = s.first * G;
             int NT = 1, tiles, kt;
-            plan_of(s, G, 1, tiles, kt);
+            plan_of(a, s, D, 1, tiles, kt);
             if (tiles == 0) {
                 NT = 2;
-                plan_of(s, G, 2, tiles, kt);
+                plan_of(a, s, D, 2, tiles, kt);
             }
             tile = 128 * NT;
             const Plan &p = NT == 1 ? y.plan[0] : y.plan[1];
@@ -1126,10 +1127,10 @@ cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
     return e;
 }
 
-// The rest of a step after its attention: outputs, the cached keys of sequences with more than
-// tile_rows rows, the gate sums.
+// The rest of a step after its attention: outputs, the cached keys of sequences of more than one
+// tile, the gate sums.
 template <int D>
-cudaError_t launch_tc_finish(const Step &a, const TcWs &y, int tile_rows, cudaStream_t stream) {
+cudaError_t launch_tc_finish(const Step &a, const TcWs &y, cudaStream_t stream) {
     const long long cap = (long long)a.c.max_pages << a.c.page_shift;
     // few rows: a warp for each, its parts eight at a time; many (whose sequences have few parts):
     // four a warp
@@ -1138,15 +1139,14 @@ cudaError_t launch_tc_finish(const Step &a, const TcWs &y, int tile_rows, cudaSt
     cudaError_t e = launch(few ? tc_combine_kernel<D, 8> : tc_combine_kernel<D, 2>,
                            dim3((unsigned)((y.R + per - 1) / per), a.c.Hkv), kThr, 0, stream, false, a, y, rows);
     if (e != cudaSuccess || cap == 0) return e;  // no sequence has room for a token
-    if ((long long)a.max_chunk * a.c.G > tile_rows) {
+    if (!one_tile(a.max_chunk, a.c.G, D, a.log_f != nullptr)) {
         const size_t bytes = TransformSmem<D>::bytes;
         if ((e = big_smem(tc_transform_kernel<D>, bytes)) != cudaSuccess) return e;
         // one wave for one long sequence, at least 256 positions a CTA (further long sequences take
         // further waves, the others' CTAs leave at once)
         long long parts = (152 + a.c.Hkv - 1) / a.c.Hkv;
         if (parts > (cap + 255) / 256) parts = (cap + 255) / 256;
-        e = launch(tc_transform_kernel<D>, dim3((unsigned)parts, a.c.Hkv, a.c.seqs), kThr, bytes, stream, false, a, y,
-                   tile_rows);
+        e = launch(tc_transform_kernel<D>, dim3((unsigned)parts, a.c.Hkv, a.c.seqs), kThr, bytes, stream, false, a, y);
         if (e != cudaSuccess) return e;
     }
     if (a.log_f != nullptr)
@@ -1159,8 +1159,8 @@ template cudaError_t launch_tc_prep<64>(const Step &, const TcWs &, cudaStream_t
 template cudaError_t launch_tc_prep<128>(const Step &, const TcWs &, cudaStream_t);
 template cudaError_t launch_tc_carry<64>(const Step &, const TcWs &, cudaStream_t);
 template cudaError_t launch_tc_carry<128>(const Step &, const TcWs &, cudaStream_t);
-template cudaError_t launch_tc_finish<64>(const Step &, const TcWs &, int, cudaStream_t);
-template cudaError_t launch_tc_finish<128>(const Step &, const TcWs &, int, cudaStream_t);
+template cudaError_t launch_tc_finish<64>(const Step &, const TcWs &, cudaStream_t);
+template cudaError_t launch_tc_finish<128>(const Step &, const TcWs &, cudaStream_t);
 
 }  // namespace paged
 }  // namespace path

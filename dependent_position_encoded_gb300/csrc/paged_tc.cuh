@@ -16,7 +16,7 @@ namespace paged {
 // head and row tile, and their units numbered through; each of `ctas` resident CTAs takes `per`
 // consecutive units, whatever the sequences' lengths, so the load is even and only items that
 // reach over a border have several parts. Sequences whose rows fit one tile go with NT = 1, the
-// others with NT = 2.
+// others with NT = 2 (one_tile).
 struct Plan {
     long long *units, *items;  // (seqs + 1): units and items before each sequence
     int ctas;
@@ -25,7 +25,7 @@ struct Plan {
 // Whether a carried query enters the cached keys' logits as a high and a low bf16 part. Rounded
 // once to bf16 it adds as much error to the output as the weights' and the output's own rounding
 // do: 2.9e-3 of the norm against 2.3e-3 with the second part and 1.7e-3 for the output's rounding
-// alone. The second product costs 4 to 6% where the cache's bytes bound the pass (NT = 1: 207 ->
+// alone, for single tokens. The second product costs 4 to 6% where the cache's bytes bound the pass (NT = 1: 207 ->
 // 215 us for 32 sequences of 8192 at D = 64) and little beside the exponentials at D = 64; at
 // D = 128 with several row tiles shared memory has no room for the parts.
 __host__ __device__ constexpr bool keeps_low(int NT, int D) { return NT == 1 || D == 64; }
@@ -66,11 +66,18 @@ __device__ __forceinline__ size_t mt_row(const Step &a, const Seq &s, int b) {
     return a.N < a.c.seqs ? s.first : b;
 }
 
+// Whether a sequence goes with NT = 1. At D = 64 without gates one of several blocks does not: its
+// queries have been through the scan's roundings, and there only the pass of NT = 2 makes up for
+// that with the weights' second part (low_weights).
+__host__ __device__ __forceinline__ bool one_tile(int T, int G, int D, bool fox) {
+    return (T <= kC || D == 128 || fox) && (long long)T * G <= 128;
+}
+
 // Row tiles and key tiles of a sequence in the plan of NT (0 where it goes with the other).
-__device__ __forceinline__ void plan_of(const Seq &s, int G, int NT, int &tiles, int &ktiles) {
-    const int rows = s.T * G;  // T G <= N G, which the host keeps within an int
+__device__ __forceinline__ void plan_of(const Step &a, const Seq &s, int D, int NT, int &tiles, int &ktiles) {
+    const int G = a.c.G, rows = s.T * G;  // T G <= N G, which the host keeps within an int
     ktiles = (s.n + 127) / 128;
-    tiles = (rows <= 128) == (NT == 1) ? (rows + 128 * NT - 1) / (128 * NT) : 0;
+    tiles = one_tile(s.T, G, D, a.log_f != nullptr) == (NT == 1) ? (rows + 128 * NT - 1) / (128 * NT) : 0;
 }
 
 // Units per CTA: at least two, so that a part is worth its join.
@@ -85,7 +92,8 @@ struct Stretch {
     int b, h, tile, k0, steps;
     long long item;  // over all sequences
 };
-__device__ __forceinline__ Stretch stretch_at(const Step &a, const Plan &p, int NT, long long u, long long end) {
+__device__ __forceinline__ Stretch stretch_at(const Step &a, const Plan &p, int D, int NT, long long u,
+                                              long long end) {
     int lo = 0, hi = a.c.seqs - 1;  // the last sequence with units[b] <= u: it has units
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -96,7 +104,7 @@ __device__ __forceinline__ Stretch stretch_at(const Step &a, const Plan &p, int 
     t.b = lo;
     t.s = seq_of(a, lo);
     int tiles, kt;
-    plan_of(t.s, a.c.G, NT, tiles, kt);
+    plan_of(a, t.s, D, NT, tiles, kt);
     const long long rem = u - p.units[lo];
     const int it = (int)(rem / kt);
     t.k0 = (int)(rem - (long long)it * kt);
