@@ -142,11 +142,12 @@ constexpr float kNothing = 64.f, kGuess = 32.f;
 // Positions past the sequence's n and those on bad pages: the streaming warp zeroes their rows
 // after the copy, and the softmax masks them.
 //
-// NT = 1 is bound by the bytes of keys (read and written) and values: 200 us for 1.17 GB of them
-// (32 sequences of up to 8,192, 16 heads, D = 64, one token each: 5.8 TB/s), 226 us for 1.2 GB (16
+// NT = 1 is bound by the bytes of keys (read and written) and values: 194 us for 1.17 GB of them
+// (32 sequences of up to 8,192, 16 heads, D = 64, one token each: 6.0 TB/s), 226 us for 1.2 GB (16
 // of up to 16,384, 8 key heads of four query heads, D = 128, gates: 5.4 TB/s). NT = 2 by the
-// tensor core: 780 us for 2,048 tokens of 32 heads against 32,768 keys at D = 128 (1.41 PFLOP/s,
-// its instructions taking 77 to 85 cycles of the 64 that they need alone).
+// tensor core: 976 us for 2,048 tokens of 32 heads against 32,768 keys at D = 128, a quarter of it
+// the weights' second part (755 us and 1.46 PFLOP/s without; instructions take 77 to 85 cycles of the
+// 64 that they need alone).
 template <int NT, int D>
 struct CachedCfg {
     static constexpr uint32_t tile = 128 * D * 2, atom = 128 * 128;
@@ -827,10 +828,10 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
 // end the state is the query carried to the chunk's start.
 // Per step the logits go first, so that the softmax runs beside the state's product and copy,
 // which are the chain from step to step. Bound by that chain and the softmax (3,000 cycles a step
-// with gates at D = 64): 102 us for 2,048 tokens of 32 heads at
-// D = 128 (0.65 PFLOP/s; 113 with the tiles of one key head after the other's), 65 us for four
-// chunks of up to 1,500 tokens, 16 heads, D = 64, gates (91 before the blocks whose gates have
-// closed were left out, 70 head by head).
+// with gates at D = 64): 176 us for 2,048 tokens of 32 heads at
+// D = 128 (94 with one part of the state), 57 us for four chunks of up to 1,500 tokens, 16 heads,
+// D = 64, gates (91 before the blocks whose gates have closed were left out, 70 with the tiles of
+// one key head after the other's, 65 with a row's loads by one lane).
 // Warps: 0-3 softmax, one row per thread; 4-7 the bf16 copy of the state; 8 allocates TMEM and
 // issues the MMAs; 9 streams [k~_b; P_b - I] and V_b.
 //

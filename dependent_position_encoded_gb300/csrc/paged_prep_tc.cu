@@ -8,8 +8,8 @@
 // further products as a high and a low bf16 part (16 bits of significand, see split2), so
 // carried keys and transitions are exact to 2^-16 before the cache rounds the keys to bf16.
 // The 16 x 16 diagonal blocks of A = (I + D N)^{-1} D are solved in fp32. Rounded to bf16 are the
-// softmax weights, in the scan over a chunk's blocks keys and (but for D = 128 without gates) transitions, and the carried
-// queries (keeps_low says where these have a second part).
+// softmax weights, in the scan over a chunk's blocks keys, state and transitions, and the carried
+// queries (low_weights, scan_low and keeps_low say where these have a second part).
 #include "paged_tc.cuh"
 
 namespace path {
@@ -27,11 +27,12 @@ using bf = __nv_bfloat16;
 //   A = (I + D N)^{-1} D, U = A W, S = R A^T with R the part t > j of K W^T;
 //   P_b - I = -U^T W, k~ = K - S W; per query head, with Lq = tril(Q W^T):
 //   q~ = Q - Lq U and the block's own logits Q K^T - Lq S^T.
-// Bound by the latency of that chain of small products between barriers (the warp-level tensor
-// path is busy a quarter of the time): 77 us for four first chunks of up to 1,500 tokens, 8 key
-// heads of two query heads, D = 64 (two CTAs per SM, 1.7 waves; 88 with the products (Lq A) W
-// and (Lq A) R^T in place of those with U and S, and the gates in line), 79 us for 2,048 tokens
-// of 8 key heads of four, D = 128 (84), 9 us for 32 single tokens of 16 heads, D = 64.
+// Bound by the latency of that chain of small products between barriers, each of them run for the
+// first time by most CTAs (the warp-level tensor path is busy an eighth to a quarter of the time):
+// 66 us for four first chunks of up to 1,500 tokens, 8 key heads of two query heads, D = 64 (two
+// CTAs per SM, 1.7 waves; 88 with the products (Lq A) W and (Lq A) R^T in place of those with U and
+// S, the gates in line, the inverse on the CUDA cores and stores of a lane's pairs), 76 us for
+// 2,048 tokens of 8 key heads of four, D = 128 (84), 9 us for 32 single tokens of 16 heads, D = 64.
 template <int D>
 struct PrepSmem {
     static constexpr int LDD = D + 8, LDS = 72, LDF = 72;  // row strides: 16-byte phases differ
@@ -663,8 +664,8 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
 // registers (Y + Y (P_b - I)), eight warps of 16 rows and half of the columns each. A chain of all blocks would be as
 // long as the chunk, so it goes in two passes over groups of kGroup blocks: to the group's
 // end (and the group's product), then over the later groups' products. Each step waits for
-// 2 D^2 bf16 from L2 and for its MMAs, two CTAs to an SM: 47 + 21 us for 2,048 tokens of 8 key
-// heads at D = 128, 25 + 14 us for four chunks of up to 1,500 at D = 64.
+// 2 D^2 bf16 from L2 and for its MMAs, two CTAs to an SM: 44 + 19 us for 2,048 tokens of 8 key
+// heads at D = 128, 23 + 14 us for four chunks of up to 1,500 at D = 64.
 constexpr int kGroup = 8;
 
 template <int D>
@@ -836,7 +837,7 @@ __global__ void __launch_bounds__(kThr) tc_carry_kernel(const Step a, const TcWs
 // two products of P - I's parts keep the warp-level tensor path busy for longer than HBM at
 // D = 128. A warp takes 32 positions at a time, so that a fragment of P - I serves two row
 // tiles, and loads the next 32 meanwhile. grid (parts, key heads, sequences), a CTA keeps
-// P - I in shared memory. 52 us for 32,768 positions of 8 heads at D = 128: 2.6 TB/s of keys,
+// P - I in shared memory. 51 us for 32,768 positions of 8 heads at D = 128: 2.6 TB/s of keys,
 // 0.33 PFLOP/s.
 template <int D>
 struct TransformSmem {
