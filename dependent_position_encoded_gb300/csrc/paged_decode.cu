@@ -1,4 +1,5 @@
-// One new token per sequence over a paged cache (PaTH and PaTH-FoX), in one pass over it.
+// One new token per sequence over a paged cache (PaTH and PaTH-FoX), in one pass over it;
+// sequences with none or several are left out.
 //
 // The new token's transition H = I - beta w w^T is applied to every cached key in place,
 // k <- k - beta (w . k) w, and the attention of the token's query runs over the updated keys
@@ -80,7 +81,7 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
     grid_begin();  // the first of the call: nothing to wait for
     const Seq s = seq_of(a, b);
     const int j0 = sp * chunk, j1 = min(j0 + chunk, s.n);
-    if (s.T == 0 || j0 >= j1) return;  // the merge skips the splits past n
+    if (s.T != 1 || j0 >= j1) return;  // the merge skips the splits past n
     const int shift = a.c.page_shift, pmask = a.c.page - 1;
     const int slot0 = j0 >> shift;
     for (int i = threadIdx.x; i <= ((j1 - 1) >> shift) - slot0; i += kThreads) {
@@ -282,7 +283,7 @@ paged_decode_merge(const Step a, int chunk, int nsplit, const float *__restrict_
     const int hq = blockIdx.x, b = blockIdx.y, c = threadIdx.x;
     grid_begin();
     const Seq s = seq_of(a, b);
-    if (s.T == 0) {
+    if (s.T != 1) {
         grid_wait();
         return;
     }

@@ -223,6 +223,8 @@ struct Ws {
     float *qt, *kt, *pb, *part, *gq, *gt, *ptot;
     double *gtot;
     int splits;
+    bool singles;  // sequences of one token go to the one-pass kernels
+    __device__ __forceinline__ bool takes(const Seq &s) const { return !(singles && s.T == 1); }
 };
 template <int D> constexpr size_t kPart = (size_t)kC * (D + 2);
 
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y
     int b, c;
     Seq s;
     grid_begin();  // the first of the call: nothing to wait for
-    if (!block_of(a, slot, b, c, s)) return;
+    if (!block_of(a, slot, b, c, s) || !y.takes(s)) return;
     const int i0 = c * kC, rows = min(kC, s.T - i0);
     const long long first = s.first + i0;
     // what this CTA forms: the keys' factors, and its query heads' part; one of them, where the
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(kThr) f32_cached_kernel(const Step a, const Ws
     int b, c, j0, j1;
     Seq s;
     grid_begin();
-    const bool mine = block_of(a, slot, b, c, s);
+    const bool mine = block_of(a, slot, b, c, s) && y.takes(s);
     grid_wait();
     if (!mine) return;
     split_range(s.n, y.splits, sp, j0, j1);
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(kThr) f32_combine_kernel(const Step a, const W
     int b, c;
     Seq s;
     grid_begin();
-    const bool mine = block_of(a, slot, b, c, s) && r < s.T - c * kC;
+    const bool mine = block_of(a, slot, b, c, s) && r < s.T - c * kC && y.takes(s);
     grid_wait();
     if (!mine) return;
     const int tiles = (s.n + kC - 1) / kC, per = (tiles + y.splits - 1) / y.splits;
@@ -658,13 +660,13 @@ __global__ void __launch_bounds__(kThr) f32_carry_kernel(const Step a, const Ws 
         b = ((int)blockIdx.x - nslots) / NH;
         tile = ((int)blockIdx.x - nslots) % NH;
         s = seq_of(a, b);
-        if (s.T == 0 || s.n == 0) return;
+        if (s.T == 0 || s.n == 0 || !y.takes(s)) return;
         for (int e = tid; e < kC * D; e += kThr) {
             const int r = e / D, q = e % D;
             Y[(q >> 6) * TILE + r * LD + (q & 63)] = (q == 64 * tile + r) ? 1.f : 0.f;
         }
     } else {
-        if (!block_of(a, blockIdx.x, b, c, s)) return;
+        if (!block_of(a, blockIdx.x, b, c, s) || !y.takes(s)) return;
         load_rows<D>(Y, y.kt + ((size_t)blockIdx.x * a.c.Hkv + h) * kC * D);
     }
     const int nb = (s.T + kC - 1) / kC;
@@ -735,7 +737,7 @@ __global__ void __launch_bounds__(kThr) f32_transform_kernel(const Step a, const
     grid_begin();
     const Seq s = seq_of(a, b);
     grid_wait();
-    if (s.T == 0 || (int)blockIdx.x * kC >= s.n) return;
+    if (s.T == 0 || (int)blockIdx.x * kC >= s.n || !y.takes(s)) return;
     const int nb = (s.T + kC - 1) / kC;
 #pragma unroll
     for (int x = 0; x < NH; ++x)
@@ -850,14 +852,29 @@ F32Layout f32_layout(const Cache &c, int N, int d, bool fox) {
 
 }  // namespace
 
-size_t f32_ws_bytes(const Cache &c, int N, int d, bool fox) { return f32_layout(c, N, d, fox).total; }
+bool decode_takes(int G);
+size_t decode_part_bytes(const Cache &c, int d);
+cudaError_t launch_decode(const Step &a, int d, bool bf16, float *part, cudaStream_t stream);
+
+size_t f32_ws_bytes(const Cache &c, int N, int d, bool fox) {
+    return f32_layout(c, N, d, fox).total + (decode_takes(c.G) ? align256(decode_part_bytes(c, d)) : 0);
+}
 
 cudaError_t launch_f32(const Step &a, int d, void *ws, cudaStream_t stream) {
     const F32Layout f = f32_layout(a.c, a.N, d, a.log_f != nullptr);
     char *w = static_cast<char *>(ws);
     auto at = [&](size_t off) { return reinterpret_cast<float *>(w + off); };
+    // A sequence of one token takes a whole block of 64 rows here. Where all but the longest chunk bring
+    // under four tokens on average, those of one go to the one-pass kernels first, which is two
+    // launches more (8 us where there are none): one chunk of 3 tokens among 35 single ones behind
+    // 1,050, 32 / 8 heads, D = 128: 2,202 us without, 646 with.
+    const bool singles = decode_takes(a.c.G) && a.c.seqs > 1 && a.N - a.max_chunk < 4 * (a.c.seqs - 1);
     const Ws y{at(f.qt), at(f.kt), at(f.pb), at(f.part), at(f.gq), at(f.gt), at(f.ptot),
-               reinterpret_cast<double *>(w + f.gtot), f.splits};
+               reinterpret_cast<double *>(w + f.gtot), f.splits, singles};
+    if (singles) {
+        const cudaError_t e = launch_decode(a, d, false, at(f.total), stream);
+        if (e != cudaSuccess) return e;
+    }
     return d == 64 ? launch_d<64>(a, y, stream) : launch_d<128>(a, y, stream);
 }
 

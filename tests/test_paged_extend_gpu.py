@@ -431,6 +431,15 @@ def test_a_workspace_for_chunks_serves_smaller_steps(lib):
     assert lib.path_check_workspace(ws) == lib.OK
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fox", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 4, 64), (4, 1, 128), (3, 1, 64)])
+@pytest.mark.parametrize("chunks", [[3, 1, 1, 0, 1, 2], [1, 1, 70, 1, 1, 1, 1, 1], [1, 2]])
+def test_single_tokens_among_chunks(lib, dtype, fox, Hq, Hkv, d, chunks):
+    x = pc.make([(90 * s) % 400 for s in range(len(chunks))], chunks, Hq, Hkv, d, 16, dtype, fox, seed=23)
+    run(lib, x)
+
+
 @pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
 @pytest.mark.parametrize("fox", [False, True])
 @pytest.mark.parametrize("Hq,chunk", [(16, 3), (32, 25), (64, 40)])
