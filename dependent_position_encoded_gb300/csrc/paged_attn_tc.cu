@@ -161,8 +161,8 @@ struct CachedCfg {
     static constexpr int NK = NT == 1 ? (D == 64 ? 2 : 3) : (D == 64 ? 4 : 3);
     static constexpr int NV = NT == 1 ? 2 : (D == 64 ? 4 : 2);
     static constexpr uint32_t K = M + mbytes, V = K + NK * tile, bars = V + NV * tile;
-    static constexpr int KF = 0, KE = NK, VF = 2 * NK, VE = VF + NV, XF = VE + NV, XE = XF + 1, SF = XE + 1, PR = SF + 2, FIN = PR + 2,
-                         DF = FIN + 2, DE = DF + NK, TMP = DE + 1, END = TMP + 2,
+    static constexpr int KF = 0, KE = NK, VF = 2 * NK, VE = VF + NV, XF = VE + NV, XE = XF + 1, SF = XE + 1,
+                         PR = SF + 2, FIN = PR + 2, DF = FIN + 2, DE = DF + NK, TMP = DE + 1, END = TMP + 2,
                          XT = END + 2, count = XT + 1;
     static constexpr uint32_t bytes = bars + count * 8 + 16;  // from a 1024-byte boundary
     static constexpr int threads = 384;
@@ -212,7 +212,9 @@ struct Ring {
 // batch of 32: 232 -> 246 us a step) and 20% of a long chunk at D = 128 (2,048 behind 32,768: 1,143 ->
 // 1,370 us). NT = 1, whose queries have fewer steps behind them, stays at 2.2e-3 without; with
 // gates few keys count: below 2.0e-3.
-__host__ __device__ constexpr int low_weights(int NT, int D, bool fox) { return NT == 1 || fox ? 0 : D == 64 ? 128 : 64; }
+__host__ __device__ constexpr int low_weights(int NT, int D, bool fox) {
+    return NT == 1 || fox ? 0 : D == 64 ? 128 : 64;
+}
 
 // Whether all boxes of a key tile lie on good pages below n: `have` one bit per box of
 // 1 << box_shift rows.
@@ -223,8 +225,8 @@ __device__ __forceinline__ bool tile_whole(int pos0, int n, unsigned have, int b
 template <int NT, int D, bool FOX>
 __global__ void __launch_bounds__(CachedCfg<NT, D>::threads, CachedCfg<NT, D>::ctas_per_sm)
 tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap tm_x,
-                 const __grid_constant__ CUtensorMap tm_l, const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
+                 const __grid_constant__ CUtensorMap tm_l, const __grid_constant__ CUtensorMap tm_m,
+                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
     using L = CachedCfg<NT, D>;
     constexpr int NA = D / 64, NK = L::NK, NV = L::NV, kLow = low_weights(NT, D, FOX);
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -976,7 +978,9 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
                 auto product = [&](uint32_t d, int part, uint32_t b, uint32_t batom, uint32_t id, bool first) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
-                        umma_bf16(d, sdesc_sw128(base + L::X + part * L::xtile + (kk >> 2) * L::xatom, 16, 1024) + 2 * (kk & 3),
+                        umma_bf16(d,
+                                  sdesc_sw128(base + L::X + part * L::xtile + (kk >> 2) * L::xatom, 16, 1024) +
+                                      2 * (kk & 3),
                                   sdesc_sw128(b + (kk >> 2) * batom, 16, 1024) + 2 * (kk & 3), id, !first || kk > 0);
                 };
                 product(tmem + L::cS, 0, rs, L::ratom, ID_S, true);
@@ -1290,7 +1294,8 @@ cudaError_t launch_all(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStre
     }
     if (a.c.max_pages > 0 && a.c.nk > 0 && a.c.nv > 0) {
         if (e == cudaSuccess) e = launch_cached<1, D, FOX>(a, y, limit_ns, stream);
-        if (e == cudaSuccess && !one_tile(a.max_chunk, a.c.G, D, FOX)) e = launch_cached<2, D, FOX>(a, y, limit_ns, stream);
+        if (e == cudaSuccess && !one_tile(a.max_chunk, a.c.G, D, FOX))
+            e = launch_cached<2, D, FOX>(a, y, limit_ns, stream);
     }
     if (e == cudaSuccess) e = launch_tc_finish<D>(a, y, stream);
     return e;

@@ -196,7 +196,8 @@ __device__ __forceinline__ void prep_single(const Step &a, const TcWs &y, const 
             const float x = fmaf(-beta * wq, w[e], q[e]) * a.scale_log2;
             const bf xh = __float2bfloat16_rn(x);
             y.qt[r * D + lane * E + e] = xh;
-            if (keeps_low(one_tile(1, G, D, a.log_f != nullptr) ? 1 : 2, D)) y.ql[r * D + lane * E + e] = __float2bfloat16_rn(x - __bfloat162float(xh));
+            if (keeps_low(one_tile(1, G, D, a.log_f != nullptr) ? 1 : 2, D))
+                y.ql[r * D + lane * E + e] = __float2bfloat16_rn(x - __bfloat162float(xh));
             y.po[r * D + lane * E + e] = __bfloat162float(vp[e]);
         }
         if (lane == 0) {
@@ -585,7 +586,8 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             float v[4][4];
             zero_acc(v);
             warp_mma_3<4, true>(v, Lh, Ll, LDS, m0, Uh, Ul, LDD, 64 * x + n0, m_end);
-            const bool low = !single || keeps_low(one_tile(s.T, G, D, a.log_f != nullptr) ? 1 : 2, D);  // the scan starts from both
+            // the scan starts from both parts
+            const bool low = !single || keeps_low(one_tile(s.T, G, D, a.log_f != nullptr) ? 1 : 2, D);
             each_eight(
                 v, m0, 64 * x + n0,
                 [&](int i, int j, float &p, float &q) {  // scaled here once: the attention's logits need no factor
