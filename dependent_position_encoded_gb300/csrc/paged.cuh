@@ -84,6 +84,68 @@ __device__ __forceinline__ bool block_of(const Step &a, int slot, int &b, int &c
     return c >= 0 && c * kC < s.T;
 }
 
+// PaTH-FoX: sums of a block's 64 gates, formed by one warp in fp64; lane t holds those of tokens t
+// and t + 32.
+//   before  f_0 + ... + f_t
+//   behind  f_{t+1} + ... + f_63
+//   pair    as `before`, but fit for differences: pair_i - pair_j is the sum of the gates behind j up
+//           to i
+// A difference loses what lies below 2^-53 of the sums, so a gate that closes for good (-1e30, the
+// type's lowest value) would take the block's other gates with it. Where a gate is as large as
+// kClosed, it counts as kClosed in `pair`: the sums then stay within 2^30 and a difference is right to
+// 2^-22, and a key behind such a gate has no weight either way (logits in fp32 are whole numbers
+// apart there). `behind` is then summed from the end; else it is the block's sum less `before`.
+struct GateSums {
+    double before[2], behind[2], pair[2], all;
+};
+constexpr double kClosed = 16777216.0;  // 2^24
+
+__device__ __forceinline__ void gate_prefix(double (&x)[2], int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const double z = __shfl_up_sync(0xffffffffu, x[half], o);
+            if (lane >= o) x[half] += z;
+        }
+    x[1] += __shfl_sync(0xffffffffu, x[0], 31);
+}
+
+__device__ __forceinline__ GateSums gate_sums(double f0, double f1, int lane) {
+    GateSums g;
+    g.before[0] = f0;
+    g.before[1] = f1;
+    gate_prefix(g.before, lane);
+    g.all = __shfl_sync(0xffffffffu, g.before[1], 31);
+    if (!__any_sync(0xffffffffu, fmax(fabs(f0), fabs(f1)) >= kClosed)) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            g.pair[half] = g.before[half];
+            g.behind[half] = g.all - g.before[half];
+        }
+        return g;
+    }
+    g.pair[0] = fmin(fmax(f0, -kClosed), kClosed);
+    g.pair[1] = fmin(fmax(f1, -kClosed), kClosed);
+    gate_prefix(g.pair, lane);
+    double s[2] = {f0, f1};  // sums of a half from its lane on
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const double z = __shfl_down_sync(0xffffffffu, s[half], o);
+            if (lane + o < 32) s[half] += z;
+        }
+    const double upper = __shfl_sync(0xffffffffu, s[1], 0);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const double z = __shfl_down_sync(0xffffffffu, s[half], 1);
+        g.behind[half] = lane < 31 ? z : 0.0;
+    }
+    g.behind[0] += upper;
+    return g;
+}
+
 // The four 16 x 16 diagonal blocks of (I + E)^{-1} for a strictly lower triangular E (64 x 64,
 // shared, stride LD), by substitution (one column per thread of the first 64), in place.
 template <int LD>

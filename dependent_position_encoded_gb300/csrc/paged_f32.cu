@@ -331,32 +331,27 @@ __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y
         __syncthreads();
         load_tokens<D>(Q, a.q, a.sq, first, hq, rows);
         if (a.log_f != nullptr && tid < 32) {
-            // inclusive prefix sums: lane i holds those of tokens i and i + 32
-            double t[2];
+            double f[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int i = 32 * half + tid;
-                t[half] = i < rows ? (double)a.log_f[(first + i) * a.sf.tok + hq * a.sf.head] : 0.0;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double z = __shfl_up_sync(0xffffffffu, t[half], o);
-                    if (tid >= o) t[half] += z;
-                }
+                f[half] = i < rows ? (double)a.log_f[(first + i) * a.sf.tok + hq * a.sf.head] : 0.0;
             }
-            t[1] += __shfl_sync(0xffffffffu, t[0], 31);
-            cum[tid] = t[0];
-            cum[tid + 32] = t[1];
-            if (tid == 31) y.gtot[bq] = t[1];
+            const GateSums sums = gate_sums(f[0], f[1], tid);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int i = 32 * half + tid;
+                cum[i] = sums.pair[half];
+                y.gq[bq * kC + i] = (float)sums.before[half];
+                y.gt[bq * kC + i] = (float)sums.behind[half];
+            }
+            if (tid == 0) y.gtot[bq] = sums.all;
         }
         if (tid < kC) {
             m[tid] = -INFINITY;
             l[tid] = 0.f;
         }
         __syncthreads();
-        if (a.log_f != nullptr && tid < kC) {
-            y.gq[bq * kC + tid] = (float)cum[tid];
-            y.gt[bq * kC + tid] = (float)(cum[kC - 1] - cum[tid]);
-        }
         zero(c0);
 #pragma unroll
         for (int x2 = 0; x2 < NH; ++x2) mm_nt(Q + x2 * TILE, W + x2 * TILE, c0);

@@ -396,38 +396,29 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
         });
     }
     __syncthreads();
-    // PaTH-FoX, a warp per query head: inclusive prefix sums of the block's 64 gates, in fp64: lane t
-    // holds those of t and t + 32. Shared as two floats each: a difference of two is then right to
-    // an fp32 rounding of itself, however large the sums are
+    // PaTH-FoX, a warp per query head: sums of the block's 64 gates (gate_sums), lane t those of tokens
+    // t and t + 32. Those for differences are shared as two floats each: a difference of two is
+    // right to 2^-47 of the sums
     auto gates = [&](int g, float2 *cum) {
         const int hq = h * G + g;
         const size_t bq = (size_t)slot * a.c.Hq + hq;
-        double x[2];
+        double f[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int t = 32 * half + lane;
-            x[half] = t < rows ? (double)a.log_f[(first + t) * a.sf.tok + hq * a.sf.head] : 0.0;
+            f[half] = t < rows ? (double)a.log_f[(first + t) * a.sf.tok + hq * a.sf.head] : 0.0;
         }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const double z = __shfl_up_sync(0xffffffffu, x[half], o);
-                if (lane >= o) x[half] += z;
-            }
-        }
-        x[1] += __shfl_sync(0xffffffffu, x[0], 31);
-        const double all = __shfl_sync(0xffffffffu, x[1], 31);
+        const GateSums sums = gate_sums(f[0], f[1], lane);
         float most = -INFINITY;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int t = 32 * half + lane;
-            const float hi = (float)x[half], behind = (float)(all - x[half]);
-            cum[t] = make_float2(hi, (float)(x[half] - (double)hi));
+            const float hi = (float)sums.pair[half], behind = (float)sums.behind[half];
+            cum[t] = make_float2(hi, (float)(sums.pair[half] - (double)hi));
             y.gt[bq * kC + t] = behind;
             most = fmaxf(most, behind);
             if (t < rows) {
-                y.gq[(size_t)h * y.R + (first + t) * G + g] = hi;
+                y.gq[(size_t)h * y.R + (first + t) * G + g] = (float)sums.before[half];
                 const long long at = single ? place(kpage, t, a.c.Hq, hq) : -1;
                 if (at >= 0) a.c.g_pages[at] = behind;
             }
@@ -435,8 +426,8 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
         if (lane == 0) {
-            y.gtot[bq] = all;
-            y.gblk[bq] = make_float2((float)all, most);
+            y.gtot[bq] = sums.all;
+            y.gblk[bq] = make_float2((float)sums.all, most);
         }
     };
     // those of the first heads, by the warps that the inverse's first part leaves idle
