@@ -16,6 +16,8 @@
 // pages of 64 positions 174 us for 1.13 GB (6.5 TB/s). The plans are bound by the latency of their
 // rounds: 9 us (fork of 3 rows), 13 (16 rows), 7 to 12 (reserve), 10 (compact, 300 pages), 20
 // (9,000).
+#include <climits>
+
 #include "paged.cuh"
 #include "paged_pages.cuh"
 
@@ -110,19 +112,20 @@ __device__ __forceinline__ Pool pool_of(const Cache &c, const PagesWs &y, int ha
 }
 
 // Where the wanted pages of item i begin in the half's list: exclusive sums of cnt[0 .. n)
-// in place. Returns the sum. Every thread of the CTA calls it.
+// in place. Returns the sum, INT_MAX where it is larger (65,535 sequences of 2^18 slots pass an int; no
+// pool has as many pages, so the places are not used then). Every thread of the CTA calls it.
 __device__ __forceinline__ int scan_counts(int *cnt, int n, int *sums) {
     const int t = threadIdx.x & (kHalf - 1);
-    int run = 0;
+    long long run = 0;
     for (int base = 0; base < n; base += kHalf) {
         const int v = base + t < n ? cnt[base + t] : 0;
         int total;
-        const int at = run + half_scan(v, sums, total);
-        if (base + t < n) cnt[base + t] = at;
+        const long long at = run + half_scan(v, sums, total);
+        if (base + t < n) cnt[base + t] = (int)at;
         run += total;
     }
     __syncthreads();
-    return run;
+    return run < INT_MAX ? (int)run : INT_MAX;
 }
 
 // ---------------------------------------------------------------- reserve
