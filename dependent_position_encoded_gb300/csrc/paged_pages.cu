@@ -252,12 +252,12 @@ __device__ __forceinline__ void copy16(uint4 *dst, const uint4 *src, int n) {
 // The first `rows` token rows of every head of a page; row_bytes = d * element size.
 __device__ __forceinline__ void copy_page(char *dst, const char *src, int heads, int page, int rows,
                                           int row_bytes) {
+    // in 16-byte words: a page's bytes may pass an int, its words do not (65,535 heads of 256 rows)
+    const int per = rows * row_bytes / 16, pitch = page * row_bytes / 16;
     if (rows == page) {
-        copy16(reinterpret_cast<uint4 *>(dst), reinterpret_cast<const uint4 *>(src),
-               heads * page * row_bytes / 16);
+        copy16(reinterpret_cast<uint4 *>(dst), reinterpret_cast<const uint4 *>(src), heads * pitch);
         return;
     }
-    const int per = rows * row_bytes / 16, pitch = page * row_bytes / 16;
     for (int i = threadIdx.x; i < heads * per; i += blockDim.x) {
         const int h = i / per, e = h * pitch + i % per;
         __stcs(reinterpret_cast<uint4 *>(dst) + e, __ldcs(reinterpret_cast<const uint4 *>(src) + e));
