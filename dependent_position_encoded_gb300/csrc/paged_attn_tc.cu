@@ -1246,10 +1246,12 @@ cudaError_t big_smem(K kern, size_t bytes) {
 template <int NT, int D, bool FOX>
 cudaError_t launch_cached(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream) {
     CUtensorMap tx, tl, tm, tk, tv;
+    // a map has no empty axis; of an empty pool nothing is loaded, every page number is outside it
+    auto heads = [&](int pages) { return (long long)std::max(pages, 1) * a.c.Hkv; };
     if (!make_map(&tx, y.qt, D, y.R, a.c.Hkv, 32) || !make_map(&tl, y.ql, D, y.R, a.c.Hkv, 32) ||
         !make_map(&tm, y.mt, D, D, (long long)std::min(a.c.seqs, a.N) * a.c.Hkv * 2, D) ||
-        !make_map(&tk, a.c.k_pages, D, a.c.page, (long long)a.c.nk * a.c.Hkv, a.c.page < 128 ? a.c.page : 128) ||
-        !make_map(&tv, a.c.v_pages, D, a.c.page, (long long)a.c.nv * a.c.Hkv, a.c.page < 128 ? a.c.page : 128))
+        !make_map(&tk, a.c.k_pages, D, a.c.page, heads(a.c.nk), a.c.page < 128 ? a.c.page : 128) ||
+        !make_map(&tv, a.c.v_pages, D, a.c.page, heads(a.c.nv), a.c.page < 128 ? a.c.page : 128))
         return cudaErrorInvalidValue;
     using L = CachedCfg<NT, D>;
     auto kern = tc_cached_kernel<NT, D, FOX>;
@@ -1292,7 +1294,7 @@ cudaError_t launch_all(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStre
         if (e == cudaSuccess) e = launch_tc_carry<D>(a, y, stream);
         if (e == cudaSuccess) e = launch_scan<D, FOX>(a, y, limit_ns, stream);
     }
-    if (a.c.max_pages > 0 && a.c.nk > 0 && a.c.nv > 0) {
+    if (a.c.max_pages > 0) {
         if (e == cudaSuccess) e = launch_cached<1, D, FOX>(a, y, limit_ns, stream);
         if (e == cudaSuccess && !one_tile(a.max_chunk, a.c.G, D, FOX))
             e = launch_cached<2, D, FOX>(a, y, limit_ns, stream);
