@@ -623,6 +623,19 @@ def _paged_devices(cache, *more):
     return dev
 
 
+def _paged_workspace(ws):
+    """Refuses what is no workspace (`ws`: a tensor or None); its device is checked with the cache's."""
+    torch = _torch()
+    if ws is None or (isinstance(ws, torch.Tensor) and ws.dtype == torch.uint8 and ws.is_cuda
+                      and ws.is_contiguous()):
+        return
+    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8:
+        raise TypeError("workspace must be a uint8 tensor (new_paged_workspace)")
+    if not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    raise TypeError("workspace must be a CUDA tensor")
+
+
 class _on:
     """The device (its index) and, where one is given, the stream of a call, as torch's current
     ones: what is allocated inside belongs to the stream that the call runs on, whose handle it
@@ -700,7 +713,8 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
         raise ValueError("q has head size %d, the cache %d" % (d, c.d))
     if out is not None and (N > 1 and o0[0] == 0 or Hq > 1 and o0[1] == 0):
         raise ValueError("out must not repeat its own memory")
-    dev = _paged_devices(cache, q, k, v, w, beta, log_f, out, cu_tokens)
+    _paged_workspace(workspace)
+    dev = _paged_devices(cache, q, k, v, w, beta, log_f, out, cu_tokens, workspace)
     gate = () if log_f is None else (log_f.data_ptr(),)
     with _on(dev, stream) as on_stream:
         if out is None:
@@ -772,7 +786,8 @@ def path_fox_paged_extend(q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, 
 
 def _paged_call(name, cache, workspace, stream, *args):
     c = _paged_cache(cache, counts=True, on_gpu=False)
-    with _on(_paged_devices(cache), stream) as on_stream:
+    _paged_workspace(workspace)
+    with _on(_paged_devices(cache, workspace), stream) as on_stream:
         if workspace is None:
             workspace = new_paged_workspace(cache)
         _check(getattr(_load(), name)(ctypes.byref(c), *args, workspace.data_ptr(),
