@@ -178,6 +178,14 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _ws(workspace, device):
+    """A workspace's address and size: a contiguous tensor on the call's device."""
+    _cuda_tensor(workspace, "workspace")
+    if workspace.device != device:
+        raise ValueError("workspace must be on %s" % device)
+    return _ptr(workspace), workspace.numel()
+
+
 def _scale(scale, d):
     return 1.0 / math.sqrt(d) if scale is None else float(scale)
 
@@ -234,8 +242,9 @@ def path_attn_fwd(q, k, v, w, beta, out=None, lse=True, scale=None, workspace=No
     if workspace is None:
         workspace = new_workspace(OP_FWD, B, H, L, dt, q.device, d=d)
     _check(_load().path_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(w), _ptr(beta), _ptr(out),
-                                 _ptr(lse), B, H, L, d, dt, _scale(scale, d), _ptr(workspace),
-                                 workspace.numel(), _stream(stream, q.device)), "path_attn_fwd")
+                                 _ptr(lse), B, H, L, d, dt, _scale(scale, d),
+                                 *_ws(workspace, q.device), _stream(stream, q.device)),
+           "path_attn_fwd")
     return out, lse
 
 
@@ -276,7 +285,7 @@ def path_attn_bwd(q, k, v, w, beta, out, lse, d_out, scale=None, grads=None, wor
     _check(_load().path_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(w), _ptr(beta), _ptr(out),
                                  _ptr(lse), _ptr(d_out), B, H, L, d, dt, _scale(scale, d),
                                  _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dw"]),
-                                 _ptr(g["dbeta"]), _ptr(workspace), workspace.numel(),
+                                 _ptr(g["dbeta"]), *_ws(workspace, q.device),
                                  _stream(stream, q.device)), "path_attn_bwd")
     return g
 
@@ -298,7 +307,7 @@ def path_fox_bwd(q, k, v, w, beta, log_f, out, lse, d_out, scale=None, grads=Non
                                 _ptr(out), _ptr(lse), _ptr(d_out), B, H, L, d, dt,
                                 _scale(scale, d), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]),
                                 _ptr(g["dw"]), _ptr(g["dbeta"]), _ptr(g["dlog_f"]),
-                                _ptr(workspace), workspace.numel(), _stream(stream, q.device)),
+                                *_ws(workspace, q.device), _stream(stream, q.device)),
            "path_fox_bwd")
     return g
 
@@ -316,7 +325,7 @@ def path_fox_fwd(q, k, v, w, beta, log_f, out=None, lse=True, scale=None, worksp
         workspace = new_workspace(OP_FOX_FWD, B, H, L, dt, q.device, d=d)
     _check(_load().path_fox_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(w), _ptr(beta), _ptr(log_f),
                                 _ptr(out), _ptr(lse), B, H, L, d, dt, _scale(scale, d),
-                                _ptr(workspace), workspace.numel(), _stream(stream, q.device)),
+                                *_ws(workspace, q.device), _stream(stream, q.device)),
            "path_fox_fwd")
     return out, lse
 
@@ -328,7 +337,7 @@ def path_fwd_prepare(q, k, w, beta, workspace, log_f=None, scale=None, stream=No
     if log_f is not None:
         _cuda_tensor(log_f, "log_f", torch.float32)
     _check(_load().path_fwd_prepare(_ptr(q), _ptr(k), _ptr(w), _ptr(beta), _ptr(log_f), B, H, L,
-                                    d, dt, _scale(scale, d), _ptr(workspace), workspace.numel(),
+                                    d, dt, _scale(scale, d), *_ws(workspace, q.device),
                                     _stream(stream, q.device)), "path_fwd_prepare")
 
 
@@ -339,7 +348,7 @@ def path_fwd_scan(v, workspace, out=None, lse=True, fox=False, scale=None, strea
     dt = _dtype_code(v)
     out, lse = _outputs(v, out, lse, B, H, L)
     _check(_load().path_fwd_scan(_ptr(v), _ptr(out), _ptr(lse), int(bool(fox)), B, H, L, d, dt,
-                                 _scale(scale, d), _ptr(workspace), workspace.numel(),
+                                 _scale(scale, d), *_ws(workspace, v.device),
                                  _stream(stream, v.device)), "path_fwd_scan")
     return out, lse
 
@@ -352,7 +361,7 @@ def path_fox_first_blocks(workspace, B, H, L, dtype, stream=None, d=HEAD_DIM):
     torch = _torch()
     nq = (L + 63) // 64
     first = torch.empty((B, H, nq), dtype=torch.int32, device=workspace.device)
-    _check(_load().path_fox_first_blocks(_ptr(workspace), workspace.numel(), B, H, L, int(d),
+    _check(_load().path_fox_first_blocks(*_ws(workspace, workspace.device), B, H, L, int(d),
                                          _dtype_code_of(dtype), _ptr(first),
                                          _stream(stream, workspace.device)),
            "path_fox_first_blocks")
@@ -404,8 +413,9 @@ def path_decode_step(q, k, v, w, beta, k_cache, v_cache, cache_len, scale=None, 
     _check(_load().path_decode_step(_ptr(ins[0]), _ptr(ins[1]), _ptr(ins[2]), _ptr(ins[3]),
                                     _ptr(beta), _ptr(k_cache), _ptr(v_cache), B, H,
                                     int(cache_len), cap, d, _dtype_code(k_cache),
-                                    _scale(scale, d), _ptr(out), _ptr(workspace),
-                                    workspace.numel(), _stream(stream, k_cache.device)),
+                                    _scale(scale, d), _ptr(out),
+                                    *_ws(workspace, k_cache.device),
+                                    _stream(stream, k_cache.device)),
            "path_decode_step")
     return out
 
@@ -430,7 +440,7 @@ def path_fox_decode_step(q, k, v, w, beta, log_f, k_cache, v_cache, g_cache, cac
                                         _ptr(beta), _ptr(log_f), _ptr(k_cache), _ptr(v_cache),
                                         _ptr(g_cache), B, H, int(cache_len), cap, d,
                                         _dtype_code(k_cache), _scale(scale, d), _ptr(out),
-                                        _ptr(workspace), workspace.numel(),
+                                        *_ws(workspace, k_cache.device),
                                         _stream(stream, k_cache.device)),
            "path_fox_decode_step")
     return out
@@ -492,7 +502,7 @@ def path_wbeta_produce(x, w_down, w_up, conv, u, bias, beta_max=2.0, w_out=None,
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
     _check(_load().path_wbeta_produce(_ptr(x), _ptr(w_down), _ptr(w_up), _ptr(conv), _ptr(u),
                                       _ptr(bias), float(beta_max), _ptr(w_out), _ptr(beta_out), B,
-                                      L, D, R, H, d, BF16, _ptr(workspace), workspace.numel(),
+                                      L, D, R, H, d, BF16, *_ws(workspace, x.device),
                                       _stream(stream, x.device)),
            "path_wbeta_produce")
     return w_out, beta_out
