@@ -646,6 +646,13 @@ def _paged_workspace(ws):
     raise TypeError("workspace must be a CUDA tensor")
 
 
+def _paged_found(name, ws, on_stream):
+    """Of a workspace that the caller does not hold: waits for the call and raises what its kernels
+    found wrong (in a capture there is nothing to wait for)."""
+    if not _torch().cuda.is_current_stream_capturing():
+        _check(_load().path_check_workspace(ws.data_ptr(), on_stream), name)
+
+
 class _on:
     """The device (its index) and, where one is given, the stream of a call, as torch's current
     ones: what is allocated inside belongs to the stream that the call runs on, whose handle it
@@ -730,7 +737,8 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
         if out is None:
             out = torch.empty_like(q)
             o0 = out.stride()
-        if workspace is None and N > 0 and c.seqs > 0:
+        own = workspace is None and N > 0 and c.seqs > 0
+        if own:
             workspace = new_paged_workspace(cache, N, max_chunk, Hq)
         _check(getattr(_load(), name)(
             ctypes.byref(c), q.data_ptr(), k.data_ptr(), v.data_ptr(), w.data_ptr(),
@@ -738,6 +746,8 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
             out.data_ptr(), _C14(q0[0], q0[1], k0[0], k0[1], v0[0], v0[1], w0[0], w0[1], b0[0], b0[1],
                                  f0[0], f0[1], o0[0], o0[1]), None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel(), on_stream), name)
+        if own:
+            _paged_found(name, workspace, on_stream)
     return out
 
 
@@ -776,7 +786,11 @@ def path_paged_extend(q, k, v, w, beta, cu_tokens, cache, max_chunk, scale=None,
     and the new tokens' entry into the cache; returns out (tokens, Hq, d). q: (tokens, Hq, d);
     k, v, w: (tokens, Hkv, d); beta: (tokens, Hkv); any strides with a contiguous last axis.
     cu_tokens: (seqs + 1) int32, where each sequence's tokens begin; max_chunk: the most of one
-    sequence. The pages must be mapped (path_paged_reserve); the caller advances cache.lens."""
+    sequence. The pages must be mapped (path_paged_reserve); the caller advances cache.lens.
+
+    What the kernels find wrong (lengths that do not fit, pages that are not mapped) is in the
+    status word of `workspace`, for path_check_workspace. Without a workspace the call makes one,
+    waits for its end and raises PathError (in a capture it cannot: give a workspace)."""
     return _paged_extend("path_paged_extend", q, k, v, w, beta, None, cu_tokens, cache, max_chunk,
                          scale, out, workspace, stream)
 
@@ -798,10 +812,14 @@ def _paged_call(name, cache, workspace, stream, *args):
     c = _paged_cache(cache, counts=True, on_gpu=False)
     _paged_workspace(workspace)
     with _on(_paged_devices(cache, workspace), stream) as on_stream:
-        if workspace is None:
+        own = workspace is None
+        if own:
             workspace = new_paged_workspace(cache)
         _check(getattr(_load(), name)(ctypes.byref(c), *args, workspace.data_ptr(),
                                       workspace.numel(), on_stream), name)
+        if own:
+            _paged_found(name, workspace, on_stream)
+    return workspace
 
 
 @functools.lru_cache(maxsize=64)
@@ -817,7 +835,11 @@ def _rows(rows):
 def path_paged_reserve(extra, cache, workspace=None, stream=None):
     """Maps the lowest free pages so that every sequence can hold lens + extra tokens (extra:
     (seqs) int32 on the device). Nothing changes if the pages run out: the workspace's status
-    word says so (path_check_workspace)."""
+    word says so (path_check_workspace). Returns the workspace.
+
+    As every page call: without a workspace it makes one, waits for its end and raises PathError
+    if something was wrong; in a capture it does not wait, and the workspace that it returns has
+    the status of the last replay."""
     torch = _torch()
     if not isinstance(extra, torch.Tensor):
         raise TypeError("extra must be a tensor")
@@ -828,24 +850,26 @@ def path_paged_reserve(extra, cache, workspace=None, stream=None):
     _cuda_tensor(extra, "extra")
     if isinstance(cache, PathPagedCache) and extra.get_device() != cache.k_pages.get_device():
         raise ValueError("extra must be on %s" % cache.k_pages.device)
-    _paged_call("path_paged_reserve", cache, workspace, stream, extra.data_ptr())
+    return _paged_call("path_paged_reserve", cache, workspace, stream, extra.data_ptr())
 
 
 def path_paged_fork(src, dst, cache, workspace=None, stream=None):
     """Rows dst (empty) become copies of rows src (lists of ints): keys copied, full value
-    pages shared, a value page that still fills copied."""
+    pages shared, a value page that still fills copied. Workspaces as in path_paged_reserve."""
     (a, n), (b, m) = _rows(src), _rows(dst)
     if n != m:
         raise ValueError("src and dst must be equally long")
-    _paged_call("path_paged_fork", cache, workspace, stream, a, b, n)
+    return _paged_call("path_paged_fork", cache, workspace, stream, a, b, n)
 
 
 def path_paged_free(rows, cache, workspace=None, stream=None):
-    """Empties rows (a list of ints): their pages go back, their lengths become 0."""
+    """Empties rows (a list of ints): their pages go back, their lengths become 0.
+    Workspaces as in path_paged_reserve."""
     a, n = _rows(rows)
-    _paged_call("path_paged_free", cache, workspace, stream, a, n)
+    return _paged_call("path_paged_free", cache, workspace, stream, a, n)
 
 
 def path_paged_compact(cache, workspace=None, stream=None):
-    """Moves the pages in use to the front of each pool; the tables follow."""
-    _paged_call("path_paged_compact", cache, workspace, stream)
+    """Moves the pages in use to the front of each pool; the tables follow. Workspaces as in
+    path_paged_reserve."""
+    return _paged_call("path_paged_compact", cache, workspace, stream)
