@@ -109,6 +109,13 @@ __device__ __forceinline__ void tmem_scale(uint32_t taddr, float f) {
     tmem_st_wait();
 }
 
+// as fmax3, but NaN where an operand is
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 constexpr float kRescale = 8.f;  // the running maximum may lag by 2^8 before O is rescaled
 // PaTH-FoX: how far (a power of two) below a row's maximum a weight counts for nothing, and how far
 // above its gates a logit is not expected (only what is fetched early goes by that)
@@ -1051,13 +1058,15 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
             }
             tc_fence_before();
             mbar_arrive_warp(bar(L::SFREE));
+            // NaN if one of them is, which then counts below and makes its row's sums NaN
             auto top64 = [&]() {
                 float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
                 for (int c = 4; c < 60; c += 8)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) m4[q] = fmax3(m4[q], x[c + 2 * q], x[c + 2 * q + 1]);
-                return fmax3(fmax3(m4[0], m4[1], m4[2]), fmax3(m4[3], x[60], x[61]), fmaxf(x[62], x[63]));
+                    for (int q = 0; q < 4; ++q) m4[q] = fmax3_nan(m4[q], x[c + 2 * q], x[c + 2 * q + 1]);
+                return fmax3_nan(fmax3_nan(m4[0], m4[1], m4[2]), fmax3_nan(m4[3], x[60], x[61]),
+                                 fmax3_nan(x[62], x[63], x[63]));
             };
             // PaTH-FoX: a block whose logits all lie below 2^-64 of what a row has is left out (2^22 keys
             // of those move a sum by less than 2^-42 of itself), its values' product too if that

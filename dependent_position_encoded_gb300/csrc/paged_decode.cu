@@ -159,7 +159,7 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
         if (FOX) {
             bool any = false;
 #pragma unroll
-            for (int g = 0; g < G; ++g) any |= x[g] >= thr[g];
+            for (int g = 0; g < G; ++g) any |= !(x[g] < thr[g]);  // NaN counts
             if (!any) return;  // the same for all lanes of the key
             vraw = ld16(vp + vrow + e0);
         }
@@ -174,7 +174,7 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
 #pragma unroll
                 for (int e = 0; e < E; ++e) o[g][e] *= sc;
             }
-            const float p = (m[g] == -INFINITY) ? 0.f : exp2f(x[g] - m[g]);
+            const float p = (x[g] == -INFINITY) ? 0.f : exp2f(x[g] - m[g]);
             l[g] += p;
 #pragma unroll
             for (int e = 0; e < E; ++e) o[g][e] = fmaf(p, vv[e], o[g][e]);
@@ -259,12 +259,13 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
         const int g = i / D, c = i % D;
         float M = -INFINITY, Ls = 0.f, Oc = 0.f;
         for (int t = 0; t < SLOTS; ++t) M = fmaxf(M, sm_m[g][t]);
-        if (M != -INFINITY)
-            for (int t = 0; t < SLOTS; ++t) {
-                const float f = exp2f(sm_m[g][t] - M);
-                Ls += sm_l[g][t] * f;
-                Oc += sm_o[g][t][c] * f;
-            }
+        // a slot without a key has a sum of 0 under its -inf, one whose keys are NaN a sum of NaN
+        const float use = M == -INFINITY ? 0.f : M;
+        for (int t = 0; t < SLOTS; ++t) {
+            const float f = exp2f(sm_m[g][t] - use);
+            Ls += sm_l[g][t] * f;
+            Oc += sm_o[g][t][c] * f;
+        }
         float *dst = part + (((size_t)b * a.c.Hq + h * G + g) * nsplit + sp) * (D + 2);
         dst[2 + c] = Oc;
         if (c == 0) {
@@ -320,9 +321,7 @@ paged_decode_merge(const Step a, int chunk, int nsplit, const float *__restrict_
     const float f_new = exp2f(x_new - M);
     float Ls = f_new, Oc = f_new * Elt<T>::to_f(vt);
     for (int i = 0; i < used; ++i) {
-        const float ms = pp[i * (D + 2)];
-        if (ms == -INFINITY) continue;
-        const float f = exp2f(ms - M);
+        const float f = exp2f(pp[i * (D + 2)] - M);  // M is at least the new token's logit
         Ls += pp[i * (D + 2) + 1] * f;
         Oc += pp[i * (D + 2) + 2 + c] * f;
     }

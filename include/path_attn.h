@@ -387,6 +387,8 @@ path_status path_paged_extend(const path_paged_cache *cache, const void *q, cons
  * tokens. g_pages holds every cached key's sum up to the last cached token; it is advanced
  * like the keys (cached: + the whole chunk's sum; new key j: the sum behind j).
  *   log_f : (num_tokens, Hq) fp32, any finite value
+ * A logit that is NaN makes its row NaN, as without gates. Of keys whose weight lies below 2^-64 of
+ * the row's largest the values need not be read, so a NaN there need not show.
  */
 path_status path_fox_paged_extend(const path_paged_cache *cache, const void *q, const void *k,
                                   const void *v, const void *w, const float *beta,
