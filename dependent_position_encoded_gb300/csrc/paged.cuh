@@ -222,11 +222,14 @@ __device__ __forceinline__ void unit_lower_inverse(float *E, float *Y, int tid, 
 }
 
 // The kernels of one call follow each other as programmatic dependents: the next one's CTAs
-// may come up (barriers, tensor memory) while the last ones of the one before still run. Up to
+// may come up while the last ones of the one before still run, and look up there which sequence and
+// block they have; the kernels with barriers and tensor memory set these up behind grid_wait. Up to
 // grid_wait they read only what the caller gave (cu_tokens, lengths, tables, the step's own
 // tensors: complete since before the call's first kernel, which is launched as any other) and
-// write nothing that an earlier kernel of the call reads or writes. Every CTA waits, also those
-// without work, so a kernel's end implies the ends of all before it.
+// write nothing that an earlier kernel of the call reads or writes. What a kernel of the call writes
+// is read by plain loads (not __ldg, no __restrict__, which promise that nobody writes it while the
+// reader lives). Every CTA waits, also those without work, so a kernel's end implies the ends of all
+// before it.
 __device__ __forceinline__ void grid_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

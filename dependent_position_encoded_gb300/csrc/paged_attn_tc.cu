@@ -646,7 +646,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                             a.c.g_pages + (((size_t)(in ? pid : 0) * a.c.Hq + hq) << a.c.page_shift) +
                             ((pos0 + c + 4 * e) & (page - 1)));
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) v[e + q] = in ? __ldg(gp + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int q = 0; q < 4; ++q) v[e + q] = in ? gp[q] : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
                 };
                 // on their way while the product runs: in registers where there are enough for the 32
@@ -1078,7 +1078,7 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
             if (FOX && counts) {
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
-                    const float4 g4 = __ldg(gt + q);
+                    const float4 g4 = gt[q];
                     x[4 * q] = fmaf(g4.x, kLog2e, x[4 * q] + bias);
                     x[4 * q + 1] = fmaf(g4.y, kLog2e, x[4 * q + 1] + bias);
                     x[4 * q + 2] = fmaf(g4.z, kLog2e, x[4 * q + 2] + bias);

@@ -279,7 +279,7 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
 // first query head of a key head, append the new key and value.
 template <typename T, bool FOX, int D>
 __global__ void __launch_bounds__(D)
-paged_decode_merge(const Step a, int chunk, int nsplit, const float *__restrict__ part) {
+paged_decode_merge(const Step a, int chunk, int nsplit, const float *part) {
     __shared__ float red[D / 32];
     const int hq = blockIdx.x, b = blockIdx.y, c = threadIdx.x;
     grid_begin();
