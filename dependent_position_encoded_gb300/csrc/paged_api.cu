@@ -86,17 +86,31 @@ path_status check_workspace(const void *ws, size_t bytes, size_t need) {
 // The step's kernels. One token per sequence at most, and a few query heads per key head: the
 // one-pass kernel on the CUDA cores scores them from registers and needs one launch more for
 // the join, where the block kernels need three; but it does G products per key on the CUDA cores.
-// Measured for bf16 (us, one-pass / block kernels), by query heads x cached positions of the
-// whole cache. G = 1: 2,400: 8.5 / 16.5; 2^18: 27 / 31 (d = 64), 43 / 50 (d = 128); 2^19: 45 / 48,
-// 80 / 80; 2^20: 77 / 75; 2^22: 238 / 216. G = 4: 2^15: 12.5 / 16.5; 2^16: 16.5 / 23; 2^17: 23 / 21,
-// 23 / 27; 2^18: 33 / 25; 2^20: 68 / 51. G = 4 with gates: 2^17: 41 / 29; 2^23: 529 / 256. With
-// gates and G = 1 the one-pass kernel leaves most value rows unread: 17 / 23 at 2^15, 237 / 242 at
-// 2^22. fp32 has no tensor path: one-pass wherever it takes G.
+// The rule goes by what the tables can hold (query heads x positions of the whole cache), not by the
+// lengths, which only the device knows. Measured for bf16 with tables that are full (us, one-pass /
+// block kernels; 8 key heads, 1 to 8 sequences):
+//                        2^14       2^15       2^16       2^17       2^18       2^19       2^20      2^22
+//   G = 1, d =  64    12.5/18.5  18.6/22.6  29.7/28.5  26.0/28.7  32.8/35.5  44.3/47.5  78/73   248/210
+//              128    14.5/23.1  22.6/28.8  34.9/34.4  34.4/38.5  61.4/57.6  79.6/79.9  141/128 468/412
+//   G = 2, d =  64    10.3/16.5  14.4/18.5  20.6/20.9  23.1/23.3  30.7/28.7  30.9/30.9  53/49   159/114
+//              128    12.3/21.9  16.3/24.2  24.7/28.7  28.7/30.8  41.5/37.4  53.4/52.6  95/80   298/214
+//   G = 4, d =  64    10.4/16.5  10.4/18.1  14.5/18.6  18.5/20.6  29.2/24.6  32.6/26.9  43/31   122/73
+//              128    12.3/21.3  12.4/22.6  16.5/24.8  22.4/26.8  34.9/32.3  43.1/36.9  72/53   223/127
+// with gates
+//   G = 1, d =  64    16.4/22.6  26.3/24.7  39.0/32.4  32.8/32.9  34.8/43.1  38.5/55.4  72/82   242/235
+//              128    22.6/26.7  35.0/32.9  53.4/39.0  47.2/44.0  53.6/67.0  81.3/92.4  147/142 503/457
+//   G = 2, d =  64    14.9/20.5  19.6/22.5  29.6/24.7  34.3/28.8  41.2/34.9  37.5/39.0  60/59   203/132
+//              128    22.6/24.8  26.8/27.0  43.1/32.8  48.3/35.0  61.8/45.1  62.3/63.9  127/94  413/245
+//   G = 4, d =  64    16.5/20.5  18.5/22.0  22.6/22.6  28.7/24.6  43.3/29.0  43.0/33.0  47/39   143/88
+//              128    24.6/24.7  26.5/26.5  30.8/28.8  43.2/30.8  64.5/38.1  67.3/42.1  79/61   294/151
+// With gates and G = 1 the one-pass kernel leaves most value rows unread and takes every size: behind at
+// 2^16 and from 2^21 on, ahead between. Its weights are fp32 where the block kernels' are bf16, so
+// equal times go to it. fp32 inputs have no tensor path: one-pass wherever it takes G.
 bool one_pass(const Cache &c, int max_chunk, bool bf16, bool fox) {
     if (max_chunk != 1 || !paged::decode_takes(c.G)) return false;
     if (!bf16 || (fox && c.G == 1)) return true;
     const long long positions = ((long long)c.max_pages << c.page_shift) * c.seqs * c.Hq;
-    return positions <= (c.G == 1 ? 1 << 18 : fox ? 1 << 16 : 1 << 17);
+    return positions <= (c.G == 1 ? 1 << 19 : fox ? 1 << 15 : 1 << 17);
 }
 
 size_t step_ws_bytes(const path_paged_cache *p, int N, int max_chunk, bool fox) {
