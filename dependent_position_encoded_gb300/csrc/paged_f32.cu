@@ -16,8 +16,8 @@
 //              logit with the chunk's transitions is k_j . (H_1 ... H_i q_i)), in splits;
 //   carry      the new keys, k~_b P_{b+1} ... P_last, into their pages with their values,
 //              and the whole chunk's product P = P_1 ... P_last;
-//   transform  the cached keys in place, K <- K P, after the cached pass has read them;
-//   combine    the softmax parts of a row joined.
+//   combine    the softmax parts of a row joined;
+//   transform  the cached keys in place, K <- K P, after the cached pass has read them.
 // For results in full precision, not for speed: at two chunks of up to 130 tokens on 1,000
 // cached, 4 heads, D = 64, too few blocks to fill the machine, it is bound by the latency of
 // each kernel's chain of products (prep 35 us, scan 33, cached 21, carry 16, transform 11,
@@ -797,10 +797,11 @@ cudaError_t launch_d(const Step &a, const Ws &y, cudaStream_t stream) {
     if (e == cudaSuccess)
         e = launch(f32_cached_kernel<D>, dim3(nslots, Hq, y.splits), kThr, cached_smem<D>(), stream, false, a, y);
     if (e == cudaSuccess)
-        e = launch(f32_combine_kernel<D>, dim3(nslots, Hq, kC / 8), kThr, 0, stream, false, a, y);
-    if (e == cudaSuccess)
         e = launch(f32_carry_kernel<D>, dim3(nslots + a.c.seqs * (D / 64), Hkv), kThr, carry_smem<D>(), stream, false,
                    a, y, nslots);
+    // behind the last kernel that reads the step's own tensors: `out` may be one of them
+    if (e == cudaSuccess)
+        e = launch(f32_combine_kernel<D>, dim3(nslots, Hq, kC / 8), kThr, 0, stream, false, a, y);
     // CTAs of 64 cached keys, or of several where that makes more than four to an SM
     long long parts = 4 * 152 / ((long long)Hkv * a.c.seqs) + 1;
     if (parts > (cap + kC - 1) / kC) parts = (cap + kC - 1) / kC;

@@ -363,6 +363,7 @@ size_t path_paged_workspace_bytes(const path_paged_cache *cache, int num_tokens,
  * The same as T calls of one token each but for the roundings of the cached keys between them.
  *   q, out : (num_tokens, Hq, d) dtype; k, v, w : (num_tokens, Hkv, d) dtype; beta :
  *            (num_tokens, Hkv) fp32; strides NULL for packed tensors
+ *            (out may be q itself, or where Hq = Hkv one of k, v, w)
  *   cu_tokens : (seqs + 1) int32 on the device, from 0, not falling (where it falls,
  *            PATH_ERR_CACHE, and what the step's own sequences hold and give is then undefined);
  *            tokens at or past cu_tokens[seqs] are not read and their out rows are left as they
