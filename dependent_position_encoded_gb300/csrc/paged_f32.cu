@@ -8,15 +8,15 @@
 //   prep       per block: P_b = I - U^T W; queries carried to the block's start,
 //              q~ = Q - (Lq A) W with Lq = tril(Q W^T); keys carried to its end,
 //              k~ = K - (R A^T) W with R the part t > j of K W^T; the block's own logits
-//              Q K^T - (Lq A) R^T and their softmax part;
+//              Q K^T - (Lq A) R^T and their softmax part; the new values into their pages;
 //   scan       chunks of several blocks: a query block visits the earlier blocks of its
 //              chunk right to left, logits X k~_b^T, X <- X P_b^T, and so arrives at the
 //              chunk's start;
 //   cached     the carried queries against the cached keys as they are (a cached key's
 //              logit with the chunk's transitions is k_j . (H_1 ... H_i q_i)), in splits;
-//   carry      the new keys, k~_b P_{b+1} ... P_last, into their pages with their values,
-//              and the whole chunk's product P = P_1 ... P_last;
 //   combine    the softmax parts of a row joined;
+//   carry      the new keys, k~_b P_{b+1} ... P_last, into their pages, and the whole chunk's
+//              product P = P_1 ... P_last;
 //   transform  the cached keys in place, K <- K P, after the cached pass has read them.
 // For results in full precision, not for speed: at two chunks of up to 130 tokens on 1,000
 // cached, 4 heads, D = 64, too few blocks to fill the machine, it is bound by the latency of
@@ -286,6 +286,16 @@ __global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y
     __syncthreads();
     const size_t bh = (size_t)slot * a.c.Hkv + h;
     if (keys) {
+        // the values go to their pages here: nothing reads the step's own tensors behind the kernel that
+        // writes `out`, which may be one of them
+        for (int e = tid; e < rows * D / 4; e += kThr) {
+            const int r = 4 * e / D, q = 4 * e % D, pos = s.n + i0 + r;
+            const int vid = page_of(a, a.c.v_table, b, pos >> a.c.page_shift, a.c.nv);
+            if (vid >= 0)
+                set4(static_cast<float *>(a.c.v_pages) +
+                         ((((size_t)vid * a.c.Hkv + h) << a.c.page_shift) + (pos & (a.c.page - 1))) * D + q,
+                     get4(static_cast<const float *>(a.v) + (first + r) * a.sv.tok + h * a.sv.head + q));
+        }
 #pragma unroll 1
         for (int x2 = 0; x2 < NH; ++x2) {
             zero(c0);
@@ -691,19 +701,15 @@ __global__ void __launch_bounds__(kThr) f32_carry_kernel(const Step a, const Ws 
         }
         return;
     }
-    // the block's keys and values into their pages, and the keys' gate sums
+    // the block's keys into their pages, and the keys' gate sums
     const int rows = min(kC, s.T - c * kC);
     for (int e = tid; e < rows * D / 4; e += kThr) {
         const int r = 4 * e / D, q = 4 * e % D, pos = s.n + c * kC + r;
-        const int sl = pos >> a.c.page_shift, off = pos & (a.c.page - 1);
-        const int kid = page_of(a, a.c.k_table, b, sl, a.c.nk), vid = page_of(a, a.c.v_table, b, sl, a.c.nv);
+        const int kid = page_of(a, a.c.k_table, b, pos >> a.c.page_shift, a.c.nk);
         if (kid >= 0)
-            set4(static_cast<float *>(a.c.k_pages) + ((((size_t)kid * a.c.Hkv + h) << a.c.page_shift) + off) * D + q,
+            set4(static_cast<float *>(a.c.k_pages) +
+                     ((((size_t)kid * a.c.Hkv + h) << a.c.page_shift) + (pos & (a.c.page - 1))) * D + q,
                  *reinterpret_cast<const float4 *>(Y + (q >> 6) * TILE + r * LD + (q & 63)));
-        if (vid >= 0)
-            set4(static_cast<float *>(a.c.v_pages) + ((((size_t)vid * a.c.Hkv + h) << a.c.page_shift) + off) * D + q,
-                 get4(static_cast<const float *>(a.v) + (long long)(s.first + c * kC + r) * a.sv.tok +
-                      h * a.sv.head + q));
     }
     if (a.log_f != nullptr)
         for (int e = tid; e < rows * a.c.G; e += kThr) {
@@ -797,11 +803,10 @@ cudaError_t launch_d(const Step &a, const Ws &y, cudaStream_t stream) {
     if (e == cudaSuccess)
         e = launch(f32_cached_kernel<D>, dim3(nslots, Hq, y.splits), kThr, cached_smem<D>(), stream, false, a, y);
     if (e == cudaSuccess)
+        e = launch(f32_combine_kernel<D>, dim3(nslots, Hq, kC / 8), kThr, 0, stream, false, a, y);
+    if (e == cudaSuccess)
         e = launch(f32_carry_kernel<D>, dim3(nslots + a.c.seqs * (D / 64), Hkv), kThr, carry_smem<D>(), stream, false,
                    a, y, nslots);
-    // behind the last kernel that reads the step's own tensors: `out` may be one of them
-    if (e == cudaSuccess)
-        e = launch(f32_combine_kernel<D>, dim3(nslots, Hq, kC / 8), kThr, 0, stream, false, a, y);
     // CTAs of 64 cached keys, or of several where that makes more than four to an SM
     long long parts = 4 * 152 / ((long long)Hkv * a.c.seqs) + 1;
     if (parts > (cap + kC - 1) / kC) parts = (cap + kC - 1) / kC;
