@@ -1,5 +1,5 @@
 // A step of several new tokens per sequence over a paged cache, on the CUDA cores: fp32
-// inputs, every product and sum in fp32 (gate prefix sums in fp64).
+// inputs, every product and sum in fp32 (gate sums in fp64).
 //
 // With u_t = beta_t (w_t - sum_{s<t} (w_s . w_t) u_s) a product of transitions is
 // H_1 ... H_i = I - sum_{s<=i} u_s w_s^T (the UT form; technical summary "技術要約: PaTH
@@ -20,8 +20,8 @@
 //   transform  the cached keys in place, K <- K P, after the cached pass has read them.
 // For results in full precision, not for speed: at two chunks of up to 130 tokens on 1,000
 // cached, 4 heads, D = 64, too few blocks to fill the machine, it is bound by the latency of
-// each kernel's chain of products (prep 35 us, scan 33, cached 21, carry 16, transform 11,
-// combine 9).
+// each kernel's chain of products (prep 37 us, scan 32, cached 21, combine 9, carry 14,
+// transform 11).
 #include "paged.cuh"
 
 namespace path {
@@ -868,7 +868,7 @@ cudaError_t launch_f32(const Step &a, int d, void *ws, cudaStream_t stream) {
     // A sequence of one token takes a whole block of 64 rows here. Where all but the longest chunk bring
     // under four tokens on average, those of one go to the one-pass kernels first, which is two
     // launches more (8 us where there are none): one chunk of 3 tokens among 35 single ones behind
-    // 1,050, 32 / 8 heads, D = 128: 2,202 us without, 646 with.
+    // 1,050, 32 / 8 heads, D = 128: 2,202 us without, 639 with.
     const bool singles = decode_takes(a.c.G) && a.c.seqs > 1 && a.N - a.max_chunk < 4 * (a.c.seqs - 1);
     const Ws y{at(f.qt), at(f.kt), at(f.pb), at(f.part), at(f.gq), at(f.gt), at(f.ptot),
                reinterpret_cast<double *>(w + f.gtot), f.splits, singles};

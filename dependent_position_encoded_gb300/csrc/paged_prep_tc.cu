@@ -29,7 +29,7 @@ using bf = __nv_bfloat16;
 //   q~ = Q - Lq U and the block's own logits Q K^T - Lq S^T.
 // Bound by the latency of that chain of small products between barriers, each of them run for the
 // first time by most CTAs (the warp-level tensor path is busy an eighth to a quarter of the time):
-// 66 us for four first chunks of up to 1,500 tokens, 8 key heads of two query heads, D = 64 (two
+// 69 us for four first chunks of up to 1,500 tokens, 8 key heads of two query heads, D = 64 (two
 // CTAs per SM, 1.7 waves; 88 with the products (Lq A) W and (Lq A) R^T in place of those with U and
 // S, the gates in line, the inverse on the CUDA cores and stores of a lane's pairs), 76 us for
 // 2,048 tokens of 8 key heads of four, D = 128 (84), 9 us for 32 single tokens of 16 heads, D = 64.

@@ -387,7 +387,7 @@ path_status path_paged_extend(const path_paged_cache *cache, const void *q, cons
  * PaTH-FoX"): the logit of key j at query i gains sum_{s=j+1..i} log f_s, over cached and new
  * tokens. g_pages holds every cached key's sum up to the last cached token; it is advanced
  * like the keys (cached: + the whole chunk's sum; new key j: the sum behind j).
- *   log_f : (num_tokens, Hq) fp32, any finite value
+ *   log_f : (num_tokens, Hq) fp32, any finite value (sums below fp32's range become -inf)
  * A logit that is NaN makes its row NaN, as without gates. Of keys whose weight lies below 2^-64 of
  * the row's largest the values need not be read, so a NaN there need not show.
  */
