@@ -100,8 +100,10 @@ struct GateSums {
 };
 constexpr double kClosed = 16777216.0;  // 2^24
 
+// (UNROLL 1 for the rare form: what a CTA seldom runs stays short; unrolled it cost first chunks 1 us)
+template <int UNROLL>
 __device__ __forceinline__ void gate_prefix(double (&x)[2], int lane) {
-#pragma unroll
+#pragma unroll UNROLL
     for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -115,7 +117,7 @@ __device__ __forceinline__ GateSums gate_sums(double f0, double f1, int lane) {
     GateSums g;
     g.before[0] = f0;
     g.before[1] = f1;
-    gate_prefix(g.before, lane);
+    gate_prefix<5>(g.before, lane);
     g.all = __shfl_sync(0xffffffffu, g.before[1], 31);
     if (!__any_sync(0xffffffffu, fmax(fabs(f0), fabs(f1)) >= kClosed)) {
 #pragma unroll
@@ -127,9 +129,9 @@ __device__ __forceinline__ GateSums gate_sums(double f0, double f1, int lane) {
     }
     g.pair[0] = fmin(fmax(f0, -kClosed), kClosed);
     g.pair[1] = fmin(fmax(f1, -kClosed), kClosed);
-    gate_prefix(g.pair, lane);
+    gate_prefix<1>(g.pair, lane);
     double s[2] = {f0, f1};  // sums of a half from its lane on
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
