@@ -594,7 +594,8 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
         }
         __syncthreads();
         // row maxima and sums; the weights, rounded to bf16, for the product with the values: eight
-        // lanes per row, eight columns each
+        // lanes per row, eight columns each. (One part: 64 keys of a row at most, and with nothing else
+        // the output's error is 2.05e-3 of its norm, its own rounding alone 1.65e-3.)
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
             const int i = 8 * warp + 4 * pass + (lane >> 3), j = 8 * (lane & 7);
