@@ -10,7 +10,8 @@ CUDA device every call raises.
 Entry points keep the C names: ``path_attn_fwd``, ``path_fox_fwd``,
 ``path_fwd_prepare``, ``path_fwd_scan``, ``path_decode_step``, ``path_fox_decode_step``,
 ``path_wbeta_produce``, ``path_paged_extend``, ``path_fox_paged_extend``,
-``path_paged_reserve``, ``path_paged_fork``, ``path_paged_free``, ``path_paged_compact`` (on a
+``path_paged_window_extend``, ``path_fox_paged_window_extend``, ``path_paged_reserve``,
+``path_paged_fork``, ``path_paged_free``, ``path_paged_trim``, ``path_paged_compact`` (on a
 ``PathPagedCache``), ``path_workspace_bytes``, ``path_check_workspace``, ``path_status_string``.
 """
 import ctypes
@@ -34,7 +35,8 @@ EXPORTED = ("path_workspace_bytes", "path_attn_fwd", "path_fox_fwd", "path_fwd_p
             "path_wbeta_workspace_bytes", "path_wbeta_produce", "path_attn_bwd",
             "path_fox_bwd", "path_paged_workspace_bytes", "path_paged_extend",
             "path_fox_paged_extend", "path_paged_reserve", "path_paged_fork", "path_paged_free",
-            "path_paged_compact")
+            "path_paged_compact", "path_paged_window_extend", "path_fox_paged_window_extend",
+            "path_paged_trim")
 
 _lib = None
 
@@ -111,6 +113,12 @@ def _load():
     lib.path_paged_extend.restype = I
     lib.path_fox_paged_extend.argtypes = [C, P, P, P, P, P, P, P, I, I, F, P, T, P, S, P]
     lib.path_fox_paged_extend.restype = I
+    lib.path_paged_window_extend.argtypes = [C, P, P, P, P, P, P, I, I, I, I, F, P, T, P, S, P]
+    lib.path_paged_window_extend.restype = I
+    lib.path_fox_paged_window_extend.argtypes = [C, P, P, P, P, P, P, P, I, I, I, I, F, P, T, P, S, P]
+    lib.path_fox_paged_window_extend.restype = I
+    lib.path_paged_trim.argtypes = [C, I, I, P, S, P]
+    lib.path_paged_trim.restype = I
     lib.path_paged_reserve.argtypes = [C, P, P, S, P]
     lib.path_paged_reserve.restype = I
     lib.path_paged_fork.argtypes = [C, P, P, I, P, S, P]
@@ -699,7 +707,7 @@ def new_paged_workspace(cache, num_tokens=0, max_chunk=0, Hq=None):
 
 
 def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, scale, out,
-                  workspace, stream):
+                  workspace, stream, more=()):
     torch = _torch()
     f32 = torch.float32
     try:
@@ -742,7 +750,7 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
             workspace = new_paged_workspace(cache, N, max_chunk, Hq)
         _check(getattr(_load(), name)(
             ctypes.byref(c), q.data_ptr(), k.data_ptr(), v.data_ptr(), w.data_ptr(),
-            beta.data_ptr(), *gate, cu_tokens.data_ptr(), N, int(max_chunk), _scale(scale, d),
+            beta.data_ptr(), *gate, cu_tokens.data_ptr(), N, int(max_chunk), *more, _scale(scale, d),
             out.data_ptr(), _C14(q0[0], q0[1], k0[0], k0[1], v0[0], v0[1], w0[0], w0[1], b0[0], b0[1],
                                  f0[0], f0[1], o0[0], o0[1]), None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel(), on_stream), name)
@@ -799,13 +807,34 @@ def path_fox_paged_extend(q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, 
                           out=None, workspace=None, stream=None):
     """path_paged_extend with the forget gates of PaTH-FoX: log_f (tokens, Hq) fp32, and
     cache.g_pages advanced like the keys."""
-    torch = _torch()
-    if not isinstance(log_f, torch.Tensor):
+    _paged_gates(log_f, cache)
+    return _paged_extend("path_fox_paged_extend", q, k, v, w, beta, log_f, cu_tokens, cache,
+                         max_chunk, scale, out, workspace, stream)
+
+
+def path_paged_window_extend(q, k, v, w, beta, cu_tokens, cache, max_chunk, window, sinks=0,
+                             scale=None, out=None, workspace=None, stream=None):
+    """path_paged_extend through a sliding window: every new token sees the last `window`
+    positions of its sequence, its own among them, and the first `sinks` ones. max_chunk must not
+    be larger than the window. Cached keys that no new token sees are neither read nor advanced;
+    path_paged_trim gives their pages back."""
+    return _paged_extend("path_paged_window_extend", q, k, v, w, beta, None, cu_tokens, cache,
+                         max_chunk, scale, out, workspace, stream, (int(window), int(sinks)))
+
+
+def path_fox_paged_window_extend(q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, window,
+                                 sinks=0, scale=None, out=None, workspace=None, stream=None):
+    """path_paged_window_extend with the forget gates of path_fox_paged_extend."""
+    _paged_gates(log_f, cache)
+    return _paged_extend("path_fox_paged_window_extend", q, k, v, w, beta, log_f, cu_tokens, cache,
+                         max_chunk, scale, out, workspace, stream, (int(window), int(sinks)))
+
+
+def _paged_gates(log_f, cache):
+    if not isinstance(log_f, _torch().Tensor):
         raise TypeError("log_f must be a tensor")
     if isinstance(cache, PathPagedCache) and cache.g_pages is None:
         raise TypeError("cache.g_pages must be a tensor")
-    return _paged_extend("path_fox_paged_extend", q, k, v, w, beta, log_f, cu_tokens, cache,
-                         max_chunk, scale, out, workspace, stream)
 
 
 def _paged_call(name, cache, workspace, stream, *args):
@@ -867,6 +896,12 @@ def path_paged_free(rows, cache, workspace=None, stream=None):
     Workspaces as in path_paged_reserve."""
     a, n = _rows(rows)
     return _paged_call("path_paged_free", cache, workspace, stream, a, n)
+
+
+def path_paged_trim(cache, window, sinks=0, workspace=None, stream=None):
+    """Gives back the pages that no later step through this window reaches: the slots behind them
+    move down and cache.lens falls by their tokens. Workspaces as in path_paged_reserve."""
+    return _paged_call("path_paged_trim", cache, workspace, stream, int(window), int(sinks))
 
 
 def path_paged_compact(cache, workspace=None, stream=None):

@@ -34,6 +34,7 @@ struct Step {
     int N, max_chunk;
     float scale_log2;
     uint32_t *status;
+    int window, sinks;  // window 0: every new token sees every position before it
 };
 
 // Sequence b's tokens: first .. first + T - 1 of the packed step, behind n cached ones.
@@ -52,6 +53,45 @@ __device__ __forceinline__ Seq seq_of(const Step &a, int b) {
         s.T = 0;
     }
     return s;
+}
+
+// A step with a window: new token t of a sequence (position n + t) sees the positions above
+// n + t - window and those below `sinks`. Of the cached ones the first new token sees the most, those
+// below `ends` and from `lo` on; the step reads and advances these and leaves the others as they are.
+// (Without a window: 0 and 0, and everything is seen.)
+struct Sight {
+    int ends, lo;
+    __device__ __forceinline__ bool sees(int j) const { return j >= lo || j < ends; }
+    __device__ __forceinline__ bool any(int j, int count) const { return j + count > lo || j < ends; }
+    __device__ __forceinline__ bool all(int j, int count) const { return j >= lo || j + count <= ends; }
+    // the positions in sight, numbered through
+    __device__ __forceinline__ int count(int n) const { return ends + n - lo; }
+    __device__ __forceinline__ int position(int i) const { return i < ends ? i : lo + (i - ends); }
+    // the tiles of `size` positions that hold any of them: those of the first positions, then those
+    // from lo's on
+    __device__ __forceinline__ int skip_from(int n, int size) const {
+        const int first = lo < n ? lo / size : (n + size - 1) / size, head = (ends + size - 1) / size;
+        return head < first ? head : first;
+    }
+    __device__ __forceinline__ int skip_to(int n, int size) const {
+        return lo < n ? lo / size : (n + size - 1) / size;
+    }
+    __device__ __forceinline__ int tiles(int n, int size) const {
+        return skip_from(n, size) + (n + size - 1) / size - skip_to(n, size);
+    }
+    __device__ __forceinline__ int tile(int i, int n, int size) const {
+        const int from = skip_from(n, size);
+        return i < from ? i : i + skip_to(n, size) - from;
+    }
+};
+__device__ __forceinline__ Sight sight_of(const Step &a, const Seq &s) {
+    const int lo = a.window > 0 && s.n >= a.window ? s.n + 1 - a.window : 0;
+    return Sight{a.sinks < lo ? a.sinks : lo, lo};
+}
+// Positions of a sequence that a step can have in sight, at most.
+inline long long most_seen(const Step &a) {
+    const long long cap = (long long)a.c.max_pages << a.c.page_shift, seen = (long long)a.window - 1 + a.sinks;
+    return a.window > 0 && seen < cap ? seen : cap;
 }
 
 // Page number of a sequence's slot, -1 (and the status word set) if it is outside the pool.

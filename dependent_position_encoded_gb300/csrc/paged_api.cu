@@ -22,6 +22,7 @@ cudaError_t launch_fork(const Cache &c, const Rows<kMaxRows> &src, const Rows<kM
                         void *ws, cudaStream_t stream);
 cudaError_t launch_free(const Cache &c, const Rows<kMaxRows> &rows, void *ws, cudaStream_t stream);
 cudaError_t launch_compact(const Cache &c, int row_bytes, void *ws, cudaStream_t stream);
+cudaError_t launch_trim(const Cache &c, int window, int sinks, void *ws, cudaStream_t stream);
 }  // namespace paged
 }  // namespace path
 
@@ -86,8 +87,8 @@ path_status check_workspace(const void *ws, size_t bytes, size_t need) {
 // The step's kernels. One token per sequence at most, and a few query heads per key head: the
 // one-pass kernel on the CUDA cores scores them from registers and needs one launch more for
 // the join, where the block kernels need three; but it does G products per key on the CUDA cores.
-// The rule goes by what the tables can hold (query heads x positions of the whole cache), not by the
-// lengths, which only the device knows. Measured for bf16 with tables that are full (us, one-pass /
+// The rule goes by what the tables can hold (query heads x positions of the whole cache, or of the
+// window and the sinks), not by the lengths, which only the device knows. Measured for bf16 with tables that are full (us, one-pass /
 // block kernels; 8 key heads, 1 to 8 sequences):
 //                        2^14       2^15       2^16       2^17       2^18       2^19       2^20      2^22
 //   G = 1, d =  64    12.5/18.5  18.6/22.6  29.7/28.5  26.0/28.7  32.8/35.5  44.3/47.5  78/73   248/210
@@ -106,16 +107,18 @@ path_status check_workspace(const void *ws, size_t bytes, size_t need) {
 // With gates and G = 1 the one-pass kernel leaves most value rows unread and takes every size: behind at
 // 2^16 and from 2^21 on, ahead between. Its weights are fp32 where the block kernels' are bf16, so
 // equal times go to it. fp32 inputs have no tensor path: one-pass wherever it takes G.
-bool one_pass(const Cache &c, int max_chunk, bool bf16, bool fox) {
+bool one_pass(const Cache &c, long long seen, int max_chunk, bool bf16, bool fox) {
     if (max_chunk != 1 || !paged::decode_takes(c.G)) return false;
     if (!bf16 || (fox && c.G == 1)) return true;
-    const long long positions = ((long long)c.max_pages << c.page_shift) * c.seqs * c.Hq;
+    const long long positions = seen * c.seqs * c.Hq;
     return positions <= (c.G == 1 ? 1 << 19 : fox ? 1 << 15 : 1 << 17);
 }
 
-size_t step_ws_bytes(const path_paged_cache *p, int N, int max_chunk, bool fox) {
+// seen: the positions that a sequence's step can have in sight (most_seen)
+size_t step_ws_bytes(const path_paged_cache *p, long long seen, int N, int max_chunk, bool fox) {
     const Cache c = to_cache(p);
-    if (one_pass(c, max_chunk, p->dtype == PATH_BF16, fox)) return 256 + align256(paged::decode_part_bytes(c, p->d));
+    if (one_pass(c, seen, max_chunk, p->dtype == PATH_BF16, fox))
+        return 256 + align256(paged::decode_part_bytes(c, p->d));
     if (p->dtype == PATH_BF16) return paged::tc_ws_bytes(c, N, max_chunk, p->d, fox);
     return paged::f32_ws_bytes(c, N, p->d, fox);
 }
@@ -141,7 +144,8 @@ bool bad_stride(const paged::Stride &s, int bytes) {
 path_status extend(const path_paged_cache *p, const void *q, const void *k, const void *v,
                    const void *w, const float *beta, const float *log_f, bool fox,
                    const int *cu_tokens, int N, int max_chunk, float scale, void *out,
-                   const path_paged_strides *strides, void *ws, size_t ws_bytes, void *stream) {
+                   const path_paged_strides *strides, void *ws, size_t ws_bytes, void *stream,
+                   int window = 0, int sinks = 0) {
     path_status st = check_cache_sizes(p);
     if (st == PATH_OK) st = check_step_sizes(p, N, max_chunk);
     if (st != PATH_OK) return st;
@@ -165,17 +169,33 @@ path_status extend(const path_paged_cache *p, const void *q, const void *k, cons
         if (bad_stride(r, elt_size(p))) return PATH_ERR_ALIGN;
     for (const paged::Stride &r : {sb, sf})
         if (r.tok < 0 || r.head < 0) return PATH_ERR_ALIGN;
-    if ((st = check_workspace(ws, ws_bytes, step_ws_bytes(p, N, max_chunk, fox))) != PATH_OK) return st;
     const Cache c = to_cache(p);
     const paged::Step a{c, q, k, v, w, beta, fox ? log_f : nullptr, out,
                         sq, sk, sv, sw, sb, sf, so,
-                        cu_tokens, N, max_chunk, scale * kLog2e, static_cast<uint32_t *>(ws)};
+                        cu_tokens, N, max_chunk, scale * kLog2e, static_cast<uint32_t *>(ws), window, sinks};
+    const long long seen = paged::most_seen(a);
+    if ((st = check_workspace(ws, ws_bytes, step_ws_bytes(p, seen, N, max_chunk, fox))) != PATH_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (one_pass(c, max_chunk, p->dtype == PATH_BF16, fox))
+    if (one_pass(c, seen, max_chunk, p->dtype == PATH_BF16, fox))
         return cuda_status(paged::launch_decode(a, p->d, p->dtype == PATH_BF16,
                                                 reinterpret_cast<float *>(static_cast<char *>(ws) + 256), s));
     if (p->dtype == PATH_BF16) return cuda_status(paged::launch_tc(a, p->d, ws, kWaitLimitNs, s));
     return cuda_status(paged::launch_f32(a, p->d, ws, s));
+}
+
+path_status check_window(int window, int sinks) {
+    return window < 1 || window > PATH_MAX_LEN || sinks < 0 || sinks > PATH_MAX_LEN ? PATH_ERR_ARG : PATH_OK;
+}
+
+path_status window_extend(const path_paged_cache *p, const void *q, const void *k, const void *v,
+                          const void *w, const float *beta, const float *log_f, bool fox,
+                          const int *cu_tokens, int N, int max_chunk, int window, int sinks,
+                          float scale, void *out, const path_paged_strides *strides, void *ws,
+                          size_t ws_bytes, void *stream) {
+    // with longer chunks the new tokens would hide one another
+    if (check_window(window, sinks) != PATH_OK || max_chunk > window) return PATH_ERR_ARG;
+    return extend(p, q, k, v, w, beta, log_f, fox, cu_tokens, N, max_chunk, scale, out, strides, ws,
+                  ws_bytes, stream, window, sinks);
 }
 
 // A list of sequence rows from the host: in range, none twice.
@@ -204,15 +224,18 @@ extern "C" {
 size_t path_paged_workspace_bytes(const path_paged_cache *cache, int num_tokens, int max_chunk) {
     if (check_cache_sizes(cache) != PATH_OK || check_step_sizes(cache, num_tokens, max_chunk) != PATH_OK)
         return 0;
-    size_t n = paged::pages_ws_bytes(to_cache(cache));
+    const Cache c = to_cache(cache);
+    size_t n = paged::pages_ws_bytes(c);
     if (num_tokens > 0) {
-        // with and without gates, and a step of single tokens too, so that a workspace for chunks
-        // serves the steps between them
+        // with and without gates, a step of single tokens too, so that a workspace for chunks serves the
+        // steps between them, and one that sees the least, which may go with the one-pass kernels where
+        // the others do not
         for (int chunk : {max_chunk, 1})
-            for (bool fox : {false, true}) {
-                const size_t s = step_ws_bytes(cache, num_tokens, chunk, fox);
-                n = s > n ? s : n;
-            }
+            for (bool fox : {false, true})
+                for (long long seen : {(long long)c.max_pages << c.page_shift, 0ll}) {
+                    const size_t s = step_ws_bytes(cache, seen, num_tokens, chunk, fox);
+                    n = s > n ? s : n;
+                }
     }
     return n;
 }
@@ -234,6 +257,39 @@ path_status path_fox_paged_extend(const path_paged_cache *cache, const void *q, 
                                   void *stream) {
     return extend(cache, q, k, v, w, beta, log_f, true, cu_tokens, num_tokens, max_chunk, scale, out,
                   strides, ws, ws_bytes, stream);
+}
+
+path_status path_paged_window_extend(const path_paged_cache *cache, const void *q, const void *k,
+                                     const void *v, const void *w, const float *beta,
+                                     const int *cu_tokens, int num_tokens, int max_chunk, int window,
+                                     int sinks, float scale, void *out,
+                                     const path_paged_strides *strides, void *ws, size_t ws_bytes,
+                                     void *stream) {
+    return window_extend(cache, q, k, v, w, beta, nullptr, false, cu_tokens, num_tokens, max_chunk,
+                         window, sinks, scale, out, strides, ws, ws_bytes, stream);
+}
+
+path_status path_fox_paged_window_extend(const path_paged_cache *cache, const void *q, const void *k,
+                                         const void *v, const void *w, const float *beta,
+                                         const float *log_f, const int *cu_tokens, int num_tokens,
+                                         int max_chunk, int window, int sinks, float scale, void *out,
+                                         const path_paged_strides *strides, void *ws, size_t ws_bytes,
+                                         void *stream) {
+    return window_extend(cache, q, k, v, w, beta, log_f, true, cu_tokens, num_tokens, max_chunk, window,
+                         sinks, scale, out, strides, ws, ws_bytes, stream);
+}
+
+path_status path_paged_trim(const path_paged_cache *cache, int window, int sinks, void *ws,
+                            size_t ws_bytes, void *stream) {
+    path_status st = check_cache_sizes(cache);
+    if (st != PATH_OK) return st;
+    if ((st = check_window(window, sinks)) != PATH_OK) return st;
+    if (cache->seqs == 0) return PATH_OK;
+    if ((st = check_cache(cache, true)) != PATH_OK) return st;
+    const Cache c = to_cache(cache);
+    if ((st = check_workspace(ws, ws_bytes, paged::pages_ws_bytes(c))) != PATH_OK) return st;
+    if (c.max_pages == 0) return PATH_OK;
+    return cuda_status(paged::launch_trim(c, window, sinks, ws, static_cast<cudaStream_t>(stream)));
 }
 
 path_status path_paged_reserve(const path_paged_cache *cache, const int *extra, void *ws,

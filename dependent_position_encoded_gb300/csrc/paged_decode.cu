@@ -30,7 +30,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxChunk = 1024;
-constexpr int kMaxIds = kMaxChunk / 16 + 1;
+constexpr int kMaxIds = kMaxChunk / 16 + 3;  // a window: two stretches of pages
 
 template <typename T> struct Row;
 template <> struct Row<__nv_bfloat16> {
@@ -66,7 +66,8 @@ __device__ __forceinline__ uint4 ld16(const T *p) {
     return *reinterpret_cast<const uint4 *>(p);
 }
 
-template <typename T, bool FOX, int D, int G>
+// WIN: the splits' positions are those in sight, numbered through (Sight::position).
+template <typename T, bool FOX, int D, int G, bool WIN>
 __global__ void __launch_bounds__(kThreads, G == 4 ? 2 : 3)
 paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part) {
     constexpr int E = Row<T>::E;
@@ -80,14 +81,22 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
     const int sp = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     grid_begin();  // the first of the call: nothing to wait for
     const Seq s = seq_of(a, b);
-    const int j0 = sp * chunk, j1 = min(j0 + chunk, s.n);
-    if (s.T != 1 || j0 >= j1) return;  // the merge skips the splits past n
+    const Sight seen = WIN ? sight_of(a, s) : Sight{0, 0};
+    const int j0 = sp * chunk, j1 = min(j0 + chunk, WIN ? seen.count(s.n) : s.n);
+    if (s.T != 1 || j0 >= j1) return;  // the merge skips the splits past the end
     const int shift = a.c.page_shift, pmask = a.c.page - 1;
-    const int slot0 = j0 >> shift;
-    for (int i = threadIdx.x; i <= ((j1 - 1) >> shift) - slot0; i += kThreads) {
-        kid[i] = page_of(a, a.c.k_table, b, slot0 + i, a.c.nk);
-        vid[i] = page_of(a, a.c.v_table, b, slot0 + i, a.c.nv);
+    // the split's slots: those of its first positions (a window's sinks), then those from slot1 on
+    const int slot0 = j0 >> shift, lead = WIN && j0 < seen.ends ? ((min(j1, seen.ends) - 1) >> shift) + 1 - slot0 : 0;
+    const int slot1 = WIN ? seen.position(max(j0, seen.ends)) >> shift : slot0;
+    const int last = WIN ? seen.position(j1 - 1) : j1 - 1;
+    const int pages = WIN && j1 <= seen.ends ? lead : lead + (last >> shift) + 1 - slot1;
+    for (int i = threadIdx.x; i < pages; i += kThreads) {
+        const int sl = WIN && i < lead ? slot0 + i : slot1 + i - lead;
+        kid[i] = page_of(a, a.c.k_table, b, sl, a.c.nk);
+        vid[i] = page_of(a, a.c.v_table, b, sl, a.c.nv);
     }
+    auto place_of = [&](int j) { return WIN ? seen.position(j) : j; };
+    auto index_of = [&](int j) { return (place_of(j) >> shift) - (WIN && j < seen.ends ? slot0 : slot1 - lead); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grp = lane / TPK, e0 = (lane % TPK) * E;
     float qv[G][E], wv[E], thr[G], m[G], l[G], o[G][E];
@@ -128,9 +137,9 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
     // row of position j in its page, or -1 past the split's end or where the page is bad
     auto place = [&](int j, const int *ids) -> long long {
         if (j >= j1) return -1;
-        const int id = ids[(j >> shift) - slot0];
+        const int id = ids[index_of(j)];
         if (id < 0) return -1;
-        return ((((long long)id * a.c.Hkv + h) << shift) + (j & pmask)) * D;
+        return ((((long long)id * a.c.Hkv + h) << shift) + (place_of(j) & pmask)) * D;
     };
     // One cached key whose row is in registers: update it in place, score it for the G heads
     // and fold it into their softmax. Every lane calls it (the shuffles are warp-wide).
@@ -211,8 +220,8 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
         for (int rb = j0 + warp * 32; rb < j1; rb += kWarps * 32) {
             const int jl = rb + lane;
             float gl[G];
-            const int id = jl < j1 ? kid[(jl >> shift) - slot0] : -1;
-            float *gp = a.c.g_pages + ((((long long)id * a.c.Hq + h * G)) << shift) + (jl & pmask);
+            const int id = jl < j1 ? kid[index_of(jl)] : -1;
+            float *gp = a.c.g_pages + ((((long long)id * a.c.Hq + h * G)) << shift) + (place_of(jl) & pmask);
 #pragma unroll
             for (int g = 0; g < G; ++g) gl[g] = id >= 0 ? gp[(long long)g << shift] : 0.f;
 #pragma unroll
@@ -314,7 +323,7 @@ paged_decode_merge(const Step a, int chunk, int nsplit, const float *part) {
     for (int i = 0; i < D / 32; ++i) dsum += red[i];
     const float x_new = dsum * a.scale_log2;
     grid_wait();
-    const int used = (s.n + chunk - 1) / chunk;
+    const int used = (sight_of(a, s).count(s.n) + chunk - 1) / chunk;
     const float *pp = part + ((size_t)b * a.c.Hq + hq) * nsplit * (D + 2);
     float M = x_new;
     for (int i = 0; i < used; ++i) M = fmaxf(M, pp[i * (D + 2)]);
@@ -331,8 +340,9 @@ paged_decode_merge(const Step a, int chunk, int nsplit, const float *part) {
 template <typename T, bool FOX, int D, int G>
 cudaError_t launch_g(const Step &a, int chunk, int nsplit, float *part, cudaStream_t stream) {
     if (nsplit > 0) {
-        const cudaError_t e = launch(paged_decode_split<T, FOX, D, G>, dim3(nsplit, a.c.Hkv, a.c.seqs), kThreads, 0,
-                                     stream, true, a, chunk, nsplit, part);
+        const cudaError_t e = launch(a.window > 0 ? paged_decode_split<T, FOX, D, G, true>
+                                                  : paged_decode_split<T, FOX, D, G, false>,
+                                     dim3(nsplit, a.c.Hkv, a.c.seqs), kThreads, 0, stream, true, a, chunk, nsplit, part);
         if (e != cudaSuccess) return e;
     }
     return launch(paged_decode_merge<T, FOX, D>, dim3(a.c.Hq, a.c.seqs), D, 0, stream, nsplit == 0, a, chunk, nsplit,
@@ -356,22 +366,24 @@ bool decode_takes(int G) { return G == 1 || G == 2 || G == 4; }
 // Cached positions per CTA: the most that still gives every SM six CTAs (two rounds of the
 // three that are resident), so that short caches spread over the machine and long ones have
 // few parts to merge.
-int decode_chunk(const Cache &c) {
-    const long long cap = (long long)c.max_pages << c.page_shift;
+int decode_chunk(const Cache &c, long long cap) {
     int chunk = kMaxChunk;
     while (chunk > 64 && (cap + chunk - 1) / chunk * c.Hkv * c.seqs < 6 * 152) chunk >>= 1;
     return chunk;
 }
 
+// For any number of positions in sight up to the cache's: splits of kMaxChunk, or no more than make
+// twice the CTAs that decode_chunk asks for.
 size_t decode_part_bytes(const Cache &c, int d) {
-    const long long cap = (long long)c.max_pages << c.page_shift;
-    const int chunk = decode_chunk(c);
-    return (size_t)c.seqs * c.Hq * ((cap + chunk - 1) / chunk) * (d + 2) * sizeof(float);
+    const long long cap = (long long)c.max_pages << c.page_shift, ctas = 12 * 152 / ((long long)c.Hkv * c.seqs) + 1;
+    long long splits = (cap + 63) / 64 < ctas ? (cap + 63) / 64 : ctas;
+    if (splits < (cap + kMaxChunk - 1) / kMaxChunk) splits = (cap + kMaxChunk - 1) / kMaxChunk;
+    return (size_t)c.seqs * c.Hq * splits * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode(const Step &a, int d, bool bf16, float *part, cudaStream_t stream) {
-    const long long cap = (long long)a.c.max_pages << a.c.page_shift;
-    const int chunk = decode_chunk(a.c), nsplit = (int)((cap + chunk - 1) / chunk);
+    const long long cap = most_seen(a);
+    const int chunk = decode_chunk(a.c, cap), nsplit = (int)((cap + chunk - 1) / chunk);
     const bool fox = a.log_f != nullptr;
     auto pick = [&](auto t) {
         using T = decltype(t);

@@ -22,6 +22,8 @@
 // cached, 4 heads, D = 64, too few blocks to fill the machine, it is bound by the latency of
 // each kernel's chain of products (prep 37 us, scan 32, cached 21, combine 9, carry 14,
 // transform 11).
+#include <climits>
+
 #include "paged.cuh"
 
 namespace path {
@@ -146,14 +148,24 @@ __device__ __forceinline__ void load_tokens(float *dst, const void *src, Stride 
     }
 }
 
-// 64 cached positions from j0 of one key head into shared tiles; positions at or past n and
-// those of bad pages are zero. ids: page numbers of the positions' slots from slot0.
+// The page numbers of the slots of 64 cached positions from j0 (-1: bad, or nothing there is in
+// sight); returns the first slot.
+__device__ __forceinline__ int find_pages(const Step &a, int *ids, const int *table, int pool, int b, int j0, int n,
+                                          const Sight &seen) {
+    const int slot0 = j0 >> a.c.page_shift, last = (min(j0 + kC, n) - 1) >> a.c.page_shift, i = threadIdx.x;
+    if (i <= last - slot0)
+        ids[i] = seen.any((slot0 + i) << a.c.page_shift, a.c.page) ? page_of(a, table, b, slot0 + i, pool) : -1;
+    return slot0;
+}
+
+// 64 cached positions from j0 of one key head into shared tiles; positions at or past n, out of sight
+// and those of bad pages are zero. ids: page numbers of the positions' slots from slot0.
 template <int D>
 __device__ __forceinline__ void load_cached(float *dst, const void *pages, const Cache &c, const int *ids,
-                                            int slot0, int h, int j0, int n) {
+                                            int slot0, int h, int j0, int n, const Sight &seen) {
     for (int e = threadIdx.x; e < kC * D / 4; e += kThr) {
         const int r = 4 * e / D, col = 4 * e % D, j = j0 + r;
-        const int id = j < n ? ids[(j >> c.page_shift) - slot0] : -1;
+        const int id = j < n && seen.sees(j) ? ids[(j >> c.page_shift) - slot0] : -1;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (id >= 0)
             x = get4(static_cast<const float *>(pages) +
@@ -510,11 +522,11 @@ __global__ void __launch_bounds__(kThr) f32_scan_kernel(const Step a, const Ws y
 }
 
 // ---------------------------------------------------------------- cached keys
-// Positions of split sp of n cached ones: whole tiles of 64.
-__device__ __forceinline__ void split_range(int n, int splits, int sp, int &j0, int &j1) {
-    const int tiles = (n + kC - 1) / kC, per = (tiles + splits - 1) / splits;
-    j0 = min(n, sp * per * kC);
-    j1 = min(n, j0 + per * kC);
+// Tiles of 64 positions of split sp of so many in sight.
+__device__ __forceinline__ void split_range(int tiles, int splits, int sp, int &t0, int &t1) {
+    const int per = (tiles + splits - 1) / splits;
+    t0 = min(tiles, sp * per);
+    t1 = min(tiles, t0 + per);
 }
 
 template <int D>
@@ -529,14 +541,15 @@ __global__ void __launch_bounds__(kThr) f32_cached_kernel(const Step a, const Ws
     int *kid = reinterpret_cast<int *>(gj + kC), *vid = kid + 8;
     const int slot = blockIdx.x, hq = blockIdx.y, sp = blockIdx.z, h = hq / a.c.G, tid = threadIdx.x;
     const int ty = tid >> 4, tx = tid & 15;
-    int b, c, j0, j1;
+    int b, c, t0, t1;
     Seq s;
     grid_begin();
     const bool mine = block_of(a, slot, b, c, s) && y.takes(s);
     grid_wait();
     if (!mine) return;
-    split_range(s.n, y.splits, sp, j0, j1);
-    if (j0 >= j1) return;
+    const Sight seen = sight_of(a, s);
+    split_range(seen.tiles(s.n, kC), y.splits, sp, t0, t1);
+    if (t0 >= t1) return;
     const size_t bq = (size_t)slot * a.c.Hq + hq;
     load_rows<D>(X, y.qt + bq * kC * D);
     if (tid < kC) {
@@ -549,20 +562,20 @@ __global__ void __launch_bounds__(kThr) f32_cached_kernel(const Step a, const Ws
     Acc o[NH];
 #pragma unroll
     for (int x = 0; x < NH; ++x) zero(o[x]);
-    for (int j = j0; j < j1; j += kC) {
-        const int slot0 = j >> a.c.page_shift, last = (min(j + kC, j1) - 1) >> a.c.page_shift;
+    // a window: row i of the block sees the positions from `from` + i on, and the sinks
+    const int from = s.n + c * kC + 1 - a.window, past = a.window > 0 ? a.sinks : INT_MAX;
+    for (int t = t0; t < t1; ++t) {
+        const int j = kC * seen.tile(t, s.n, kC);
         __syncthreads();
-        if (tid <= last - slot0) {
-            kid[tid] = page_of(a, a.c.k_table, b, slot0 + tid, a.c.nk);
-            vid[tid] = page_of(a, a.c.v_table, b, slot0 + tid, a.c.nv);
-        }
+        const int slot0 = find_pages(a, kid, a.c.k_table, a.c.nk, b, j, s.n, seen);
+        find_pages(a, vid, a.c.v_table, a.c.nv, b, j, s.n, seen);
         __syncthreads();
-        load_cached<D>(K, a.c.k_pages, a.c, kid, slot0, h, j, j1);
-        load_cached<D>(V, a.c.v_pages, a.c, vid, slot0, h, j, j1);
+        load_cached<D>(K, a.c.k_pages, a.c, kid, slot0, h, j, s.n, seen);
+        load_cached<D>(V, a.c.v_pages, a.c, vid, slot0, h, j, s.n, seen);
         if (tid < kC) {
             // the key's gate sum; -inf where there is no such key
             const int jj = j + tid, sl = (jj >> a.c.page_shift) - slot0;
-            const bool in = jj < j1 && kid[sl] >= 0 && vid[sl] >= 0;
+            const bool in = jj < s.n && kid[sl] >= 0 && vid[sl] >= 0;
             float g = in ? 0.f : -INFINITY;
             if (in && a.log_f != nullptr)
                 g = a.c.g_pages[(((size_t)kid[sl] * a.c.Hq + hq) << a.c.page_shift) + (jj & (a.c.page - 1))];
@@ -578,7 +591,9 @@ __global__ void __launch_bounds__(kThr) f32_cached_kernel(const Step a, const Ws
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 S[(ty + 16 * i) * LD + tx + 16 * q] =
-                    fmaf(gq[i] + gj[tx + 16 * q], kLog2e, c0[i][q] * a.scale_log2);
+                    j + tx + 16 * q >= past && j + tx + 16 * q < from + ty + 16 * i
+                        ? -INFINITY
+                        : fmaf(gq[i] + gj[tx + 16 * q], kLog2e, c0[i][q] * a.scale_log2);
         __syncthreads();
         softmax_rows(S, m, l, alpha);
         __syncthreads();
@@ -603,7 +618,7 @@ __global__ void __launch_bounds__(kThr) f32_combine_kernel(const Step a, const W
     const bool mine = block_of(a, slot, b, c, s) && r < s.T - c * kC && y.takes(s);
     grid_wait();
     if (!mine) return;
-    const int tiles = (s.n + kC - 1) / kC, per = (tiles + y.splits - 1) / y.splits;
+    const int tiles = sight_of(a, s).tiles(s.n, kC), per = (tiles + y.splits - 1) / y.splits;
     const int used = 1 + (per > 0 ? (tiles + per - 1) / per : 0);
     const float *p0 = y.part + ((size_t)slot * a.c.Hq + hq) * (1 + y.splits) * kPart<D>;
     float M = -INFINITY, L = 0.f, O[E];
@@ -738,17 +753,19 @@ __global__ void __launch_bounds__(kThr) f32_transform_kernel(const Step a, const
     grid_begin();
     const Seq s = seq_of(a, b);
     grid_wait();
-    if (s.T == 0 || (int)blockIdx.x * kC >= s.n || !y.takes(s)) return;
+    const Sight seen = sight_of(a, s);
+    const int tiles = seen.tiles(s.n, kC);
+    if (s.T == 0 || (int)blockIdx.x >= tiles || !y.takes(s)) return;
     const int nb = (s.T + kC - 1) / kC;
 #pragma unroll
     for (int x = 0; x < NH; ++x)
         load_rows<D>(P + x * NH * TILE, y.ptot + (((size_t)b * a.c.Hkv + h) * D + 64 * x) * D);
-    for (int j = blockIdx.x * kC; j < s.n; j += gridDim.x * kC) {
-        const int slot0 = j >> a.c.page_shift, jend = min(j + kC, s.n), last = (jend - 1) >> a.c.page_shift;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int j = kC * seen.tile(t, s.n, kC), jend = min(j + kC, s.n);
         __syncthreads();
-        if (tid <= last - slot0) kid[tid] = page_of(a, a.c.k_table, b, slot0 + tid, a.c.nk);
+        const int slot0 = find_pages(a, kid, a.c.k_table, a.c.nk, b, j, s.n, seen);
         __syncthreads();
-        load_cached<D>(K, a.c.k_pages, a.c, kid, slot0, h, j, jend);
+        load_cached<D>(K, a.c.k_pages, a.c, kid, slot0, h, j, s.n, seen);
         __syncthreads();
 #pragma unroll
         for (int x1 = 0; x1 < NH; ++x1) {
@@ -759,7 +776,7 @@ __global__ void __launch_bounds__(kThr) f32_transform_kernel(const Step a, const
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int jj = j + ty + 16 * i;
-                const int id = jj < jend ? kid[(jj >> a.c.page_shift) - slot0] : -1;
+                const int id = jj < jend && seen.sees(jj) ? kid[(jj >> a.c.page_shift) - slot0] : -1;
                 if (id >= 0)
                     set4(static_cast<float *>(a.c.k_pages) + ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) +
                                                           (jj & (a.c.page - 1))) * D + 64 * x1 + 4 * tx,
@@ -769,7 +786,7 @@ __global__ void __launch_bounds__(kThr) f32_transform_kernel(const Step a, const
         if (a.log_f != nullptr)
             for (int e = tid; e < kC * a.c.G; e += kThr) {
                 const int jj = j + e % kC, hq = h * a.c.G + e / kC;
-                const int id = jj < jend ? kid[(jj >> a.c.page_shift) - slot0] : -1;
+                const int id = jj < jend && seen.sees(jj) ? kid[(jj >> a.c.page_shift) - slot0] : -1;
                 if (id < 0) continue;
                 double t = 0.0;
                 for (int kb = 0; kb < nb; ++kb) t += y.gtot[(size_t)slot_of(s, b, kb) * a.c.Hq + hq];
@@ -794,7 +811,7 @@ cudaError_t launch_d(const Step &a, const Ws &y, cudaStream_t stream) {
         (e = big_smem(f32_carry_kernel<D>, carry_smem<D>())) != cudaSuccess ||
         (e = big_smem(f32_transform_kernel<D>, transform_smem<D>())) != cudaSuccess)
         return e;
-    const long long cap = (long long)a.c.max_pages << a.c.page_shift;
+    const long long cap = most_seen(a);
     // while half of the SMs would be idle, a CTA for the keys and others for the query heads
     const int room = 152 / (nslots * Hkv), z = room < 2 ? 1 : 1 + (room - 1 < a.c.G ? room - 1 : a.c.G);
     e = launch(f32_prep_kernel<D>, dim3(nslots, Hkv, z), kThr, prep_smem<D>(), stream, true, a, y);

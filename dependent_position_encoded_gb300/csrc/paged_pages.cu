@@ -1,4 +1,4 @@
-// The pages of a paged cache: reserving, forking, freeing and compacting, on the device, so
+// The pages of a paged cache: reserving, forking, freeing, trimming and compacting, on the device, so
 // that a captured step can grow its sequences without the host.
 //
 // Every decode step rewrites every cached key of a sequence (review "거리에서 경로로, PaTH
@@ -310,6 +310,51 @@ __global__ void __launch_bounds__(256) free_kernel(const Cache c, const Rows<N> 
     if (blockIdx.y == 0 && threadIdx.x == 0) c.lens[s] = 0;
 }
 
+// ---------------------------------------------------------------- trim
+// The pages whose every position lies behind the window of the next token and past the sinks leave
+// the sequence. The logits go by distances and no position has a number of its own, so the slots
+// behind them move down and the length falls by as many pages; what a window sees is the same. A
+// CTA per sequence; slots move down in rounds of kTrimThr * kTrimItems, read before they are
+// written.
+constexpr int kTrimThr = 256, kTrimItems = 8;
+
+__global__ void __launch_bounds__(kTrimThr) trim_kernel(const Cache c, int window, int sinks, const PagesWs y) {
+    const int s = blockIdx.x, tid = threadIdx.x, n = c.lens[s];
+    if (n < 0 || n > (long long)c.max_pages << c.page_shift) {
+        if (tid == 0) report_status(y.status, kStatusCache);
+        return;
+    }
+    const int first = (sinks + c.page - 1) >> c.page_shift;
+    const int gone = (n >= window ? (n + 1 - window) >> c.page_shift : 0) - first;
+    if (gone <= 0) return;
+    for (int half = 0; half < 2; ++half) {
+        const Pool p = pool_of(c, y, half);
+        int *const row = p.table + (size_t)s * c.max_pages;
+        for (int i = first + tid; i < first + gone; i += kTrimThr) {
+            const int id = row[i];
+            if (id < 0) continue;
+            if (id < p.pages) atomicSub(p.ref + id, 1);
+            else report_status(y.status, kStatusCache);
+        }
+        for (int i0 = first; i0 < c.max_pages; i0 += kTrimThr * kTrimItems) {
+            int id[kTrimItems];
+#pragma unroll
+            for (int q = 0; q < kTrimItems; ++q) {
+                const int i = i0 + q * kTrimThr + tid;
+                id[q] = i < c.max_pages - gone ? row[i + gone] : -1;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < kTrimItems; ++q) {
+                const int i = i0 + q * kTrimThr + tid;
+                if (i < c.max_pages) row[i] = id[q];
+            }
+            __syncthreads();
+        }
+    }
+    if (tid == 0) c.lens[s] = n - (gone << c.page_shift);  // every thread has read it
+}
+
 // ---------------------------------------------------------------- compact
 // With L live pages, the k-th free page below L takes the k-th live page at or above L: the
 // two sets are as large as each other and disjoint, so the copies may run in any order.
@@ -465,6 +510,10 @@ cudaError_t launch_free(const Cache &c, const Rows<kMaxRows> &rows, void *ws, cu
     return rows.n <= kFewRows
                ? launch(free_kernel<kFewRows>, dim3(rows.n, 2), 256, 0, stream, true, c, few_rows(rows), y)
                : launch(free_kernel<kMaxRows>, dim3(rows.n, 2), 256, 0, stream, true, c, rows, y);
+}
+
+cudaError_t launch_trim(const Cache &c, int window, int sinks, void *ws, cudaStream_t stream) {
+    return launch(trim_kernel, dim3(c.seqs), kTrimThr, 0, stream, true, c, window, sinks, pages_ws(c, ws, nullptr));
 }
 
 cudaError_t launch_compact(const Cache &c, int row_bytes, void *ws, cudaStream_t stream) {

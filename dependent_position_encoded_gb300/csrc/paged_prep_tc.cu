@@ -849,8 +849,9 @@ __global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, con
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_begin();
     const Seq s = seq_of(a, b);
+    const Sight seen = sight_of(a, s);
     grid_wait();
-    const int strips = (s.n + 31) / 32, per = (strips + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int strips = seen.tiles(s.n, 32), per = (strips + (int)gridDim.x - 1) / (int)gridDim.x;
     const int first = (int)blockIdx.x * per, last = min(strips, first + per);
     if (one_tile(s.T, a.c.G, D, a.log_f != nullptr) || first >= last) return;
     const bf *const m = y.mt + (mt_row(a, s, b) * a.c.Hkv + h) * 2 * D * D;
@@ -864,7 +865,7 @@ __global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, con
     bf *const mine = reinterpret_cast<bf *>(smem + S::K + warp * 2 * S::strip);
     // where 16 positions from j lie (pages are multiples of 16); null past the end or on a bad page
     auto rows_at = [&](int j) -> bf * {
-        if (j >= s.n) return nullptr;
+        if (j >= s.n || !seen.any(j, 16)) return nullptr;
         const int id = page_of(a, a.c.k_table, b, j >> a.c.page_shift, a.c.nk);
         return id < 0 ? nullptr
                       : pool + ((((size_t)id * a.c.Hkv + h) << a.c.page_shift) + (j & (a.c.page - 1))) * D;
@@ -873,7 +874,7 @@ __global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, con
         bf *const dst = mine + buf * 32 * LDD;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const bf *src = rows_at(32 * strip + 16 * half);
+            const bf *src = rows_at(32 * seen.tile(strip, s.n, 32) + 16 * half);
 #pragma unroll
             for (int e = lane; e < 16 * PER; e += 32) {
                 const int r = e / PER, q = e % PER * 8;
@@ -928,12 +929,12 @@ __global__ void __launch_bounds__(kThr, 1) tc_transform_kernel(const Step a, con
         __syncwarp();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int j = 32 * strip + 16 * half, left = min(16, s.n - j);
+            const int j = 32 * seen.tile(strip, s.n, 32) + 16 * half, left = min(16, s.n - j);
             bf *const dst = rows_at(j);
 #pragma unroll
             for (int e = lane; e < 16 * PER; e += 32) {
                 const int r = e / PER, q = e % PER * 8;
-                if (dst != nullptr && r < left)
+                if (dst != nullptr && r < left && seen.sees(j + r))
                     *reinterpret_cast<uint4 *>(dst + (size_t)r * D + q) =
                         *reinterpret_cast<const uint4 *>(k + (16 * half + r) * LDD + q);
             }
@@ -949,17 +950,20 @@ __global__ void __launch_bounds__(kThr) tc_gates_kernel(const Step a, const TcWs
     const int hq = blockIdx.y, b = blockIdx.z;
     grid_begin();
     const Seq s = seq_of(a, b);
+    const Sight seen = sight_of(a, s);
+    const int fours = seen.tiles(s.n, 4);
     grid_wait();
-    if (s.T == 0 || (int)blockIdx.x * kThr * 4 >= s.n) return;
+    if (s.T == 0 || (int)blockIdx.x * kThr >= fours) return;
     const int nb = (s.T + kC - 1) / kC;
     double sum = 0.0;
     for (int kb = 0; kb < nb; ++kb) sum += y.gtot[(size_t)slot_of(s, b, kb) * a.c.Hq + hq];
     const float t = (float)sum;
-    for (int j = (blockIdx.x * kThr + threadIdx.x) * 4; j < s.n; j += gridDim.x * kThr * 4) {
+    for (int i4 = blockIdx.x * kThr + threadIdx.x; i4 < fours; i4 += gridDim.x * kThr) {
+        const int j = 4 * seen.tile(i4, s.n, 4);
         const int id = page_of(a, a.c.k_table, b, j >> a.c.page_shift, a.c.nk);
         if (id < 0) continue;
         float *g = a.c.g_pages + (((size_t)id * a.c.Hq + hq) << a.c.page_shift) + (j & (a.c.page - 1));
-        if (j + 4 <= s.n) {
+        if (j + 4 <= s.n && seen.all(j, 4)) {
             float4 v = *reinterpret_cast<const float4 *>(g);
             v.x += t;
             v.y += t;
@@ -967,7 +971,8 @@ __global__ void __launch_bounds__(kThr) tc_gates_kernel(const Step a, const TcWs
             v.w += t;
             *reinterpret_cast<float4 *>(g) = v;
         } else {
-            for (int i = 0; j + i < s.n; ++i) g[i] += t;
+            for (int i = 0; i < 4 && j + i < s.n; ++i)
+                if (seen.sees(j + i)) g[i] += t;
         }
     }
 }
@@ -1126,7 +1131,7 @@ cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
 // tile, the gate sums.
 template <int D>
 cudaError_t launch_tc_finish(const Step &a, const TcWs &y, cudaStream_t stream) {
-    const long long cap = (long long)a.c.max_pages << a.c.page_shift;
+    const long long cap = most_seen(a);
     // few rows: a warp for each, its parts eight at a time; many (whose sequences have few parts):
     // four a warp
     const bool few = y.R * a.c.Hkv < 8 * 152 * 24;

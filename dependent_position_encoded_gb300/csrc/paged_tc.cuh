@@ -22,6 +22,10 @@ struct Plan {
     int ctas;
 };
 
+// What a pass over cached keys does: that of a step over its own cache, the same seen through a
+// window, or one over keys that several sequences share, which stay as they are.
+enum class Pass { step, window, shared };
+
 // Whether a carried query enters the cached keys' logits as a high and a low bf16 part. Rounded
 // once to bf16 it adds as much error to the output as the weights' and the output's own rounding
 // do: 2.9e-3 of the norm against 2.3e-3 with the second part and 1.7e-3 for the output's rounding
@@ -76,7 +80,7 @@ __host__ __device__ __forceinline__ bool one_tile(int T, int G, int D, bool fox)
 // Row tiles and key tiles of a sequence in the plan of NT (0 where it goes with the other).
 __device__ __forceinline__ void plan_of(const Step &a, const Seq &s, int D, int NT, int &tiles, int &ktiles) {
     const int G = a.c.G, rows = s.T * G;  // T G <= N G, which the host keeps within an int
-    ktiles = (s.n + 127) / 128;
+    ktiles = sight_of(a, s).tiles(s.n, 128);
     tiles = one_tile(s.T, G, D, a.log_f != nullptr) == (NT == 1) ? (rows + 128 * NT - 1) / (128 * NT) : 0;
 }
 
@@ -370,6 +374,10 @@ __device__ __forceinline__ void each_pair(float (&acc)[NT][4], int m0, int n0, F
         fn(r + 8, c + 8 * n, acc[n][2], acc[n][3]);
     }
 }
+
+// (paged_cached_tc.cuh)
+template <int NT, int D, bool FOX, Pass M>
+cudaError_t launch_cached(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream);
 
 }  // namespace paged
 }  // namespace path

@@ -317,7 +317,7 @@ path_status path_wbeta_produce(const void *x, const void *w_down, const void *w_
  *   k_table, v_table : (seqs, max_pages) int32: the page of each slot of `page` tokens of a
  *             sequence; -1 where there is none
  *   k_ref, v_ref : (num_k_pages), (num_v_pages) int32: how many table entries hold a page; 0
- *             is a free page. Only the page calls (reserve, fork, free, compact) need them.
+ *             is a free page. Only the page calls (reserve, fork, free, trim, compact) need them.
  *   lens    : (seqs) int32 cached tokens. Sequence s holds its token i in slot i / page.
  * Hq query heads share Hkv key heads, Hq / Hkv to each (query head h uses key head
  * h / (Hq / Hkv)); w and beta go with the key heads, gates with the query heads.
@@ -397,6 +397,45 @@ path_status path_fox_paged_extend(const path_paged_cache *cache, const void *q, 
                                   int max_chunk, float scale, void *out,
                                   const path_paged_strides *strides, void *ws, size_t ws_bytes,
                                   void *stream);
+
+/*
+ * path_paged_extend through a sliding window with sinks: new token i of a sequence, at position
+ * n + i, sees the last `window` positions, its own among them, and the first `sinks` ones of the
+ * sequence. Logits are as in path_paged_extend: a sink's key has taken every transition since.
+ *   window : 1 .. PATH_MAX_LEN, max_chunk <= window (else PATH_ERR_ARG: longer prompts go in
+ *            several steps)
+ *   sinks  : 0 .. PATH_MAX_LEN
+ * The step reads and advances the cached keys that its sequence's first new token sees, positions
+ * j > n - window and j < sinks, and leaves the others as they are, so a step costs no more behind a
+ * long cache than behind a short one; a page that holds only others need not be mapped. What stands
+ * in the others, NaN included, has no influence; but a NaN value that only the first of several new
+ * tokens still see may show in the chunk's later rows. Give every later step of the sequence the
+ * same window and sinks, or smaller ones (keys out of sight have missed transitions).
+ */
+path_status path_paged_window_extend(const path_paged_cache *cache, const void *q, const void *k,
+                                     const void *v, const void *w, const float *beta,
+                                     const int *cu_tokens, int num_tokens, int max_chunk, int window,
+                                     int sinks, float scale, void *out,
+                                     const path_paged_strides *strides, void *ws, size_t ws_bytes,
+                                     void *stream);
+
+/* path_paged_window_extend with the forget gates of path_fox_paged_extend. */
+path_status path_fox_paged_window_extend(const path_paged_cache *cache, const void *q, const void *k,
+                                         const void *v, const void *w, const float *beta,
+                                         const float *log_f, const int *cu_tokens, int num_tokens,
+                                         int max_chunk, int window, int sinks, float scale, void *out,
+                                         const path_paged_strides *strides, void *ws, size_t ws_bytes,
+                                         void *stream);
+
+/*
+ * Gives back the pages that no later window step of their sequence reaches: those whose every
+ * position j has j >= sinks and j <= lens[s] - window. The slots behind them move down and lens[s]
+ * falls by their tokens (logits go by distances, so nothing else changes): a stream's cache
+ * stays within about window + sinks + page tokens. A shared value page's count falls by one. A
+ * sequence whose length does not fit the cache is left as it was (PATH_ERR_CACHE).
+ */
+path_status path_paged_trim(const path_paged_cache *cache, int window, int sinks, void *ws,
+                            size_t ws_bytes, void *stream);
 
 /*
  * Maps free pages so that sequence s can hold lens[s] + extra[s] tokens (extra: (seqs) int32
