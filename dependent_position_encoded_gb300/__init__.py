@@ -10,7 +10,8 @@ CUDA device every call raises.
 Entry points keep the C names: ``path_attn_fwd``, ``path_fox_fwd``,
 ``path_fwd_prepare``, ``path_fwd_scan``, ``path_decode_step``, ``path_fox_decode_step``,
 ``path_wbeta_produce``, ``path_paged_extend``, ``path_fox_paged_extend``,
-``path_paged_window_extend``, ``path_fox_paged_window_extend``, ``path_paged_reserve``,
+``path_paged_window_extend``, ``path_fox_paged_window_extend``, ``path_paged_prefix_extend``,
+``path_fox_paged_prefix_extend``, ``path_paged_reserve``,
 ``path_paged_fork``, ``path_paged_free``, ``path_paged_trim``, ``path_paged_compact`` (on a
 ``PathPagedCache``), ``path_workspace_bytes``, ``path_check_workspace``, ``path_status_string``.
 """
@@ -36,7 +37,8 @@ EXPORTED = ("path_workspace_bytes", "path_attn_fwd", "path_fox_fwd", "path_fwd_p
             "path_fox_bwd", "path_paged_workspace_bytes", "path_paged_extend",
             "path_fox_paged_extend", "path_paged_reserve", "path_paged_fork", "path_paged_free",
             "path_paged_compact", "path_paged_window_extend", "path_fox_paged_window_extend",
-            "path_paged_trim")
+            "path_paged_trim", "path_paged_prefix_workspace_bytes", "path_paged_prefix_extend",
+            "path_fox_paged_prefix_extend")
 
 _lib = None
 
@@ -117,6 +119,12 @@ def _load():
     lib.path_paged_window_extend.restype = I
     lib.path_fox_paged_window_extend.argtypes = [C, P, P, P, P, P, P, P, I, I, I, I, F, P, T, P, S, P]
     lib.path_fox_paged_window_extend.restype = I
+    lib.path_paged_prefix_workspace_bytes.argtypes = [C, I, I]
+    lib.path_paged_prefix_workspace_bytes.restype = S
+    lib.path_paged_prefix_extend.argtypes = [C, P, P, P, P, P, P, I, I, P, P, F, P, T, P, S, P]
+    lib.path_paged_prefix_extend.restype = I
+    lib.path_fox_paged_prefix_extend.argtypes = [C, P, P, P, P, P, P, P, I, I, P, P, P, F, P, T, P, S, P]
+    lib.path_fox_paged_prefix_extend.restype = I
     lib.path_paged_trim.argtypes = [C, I, I, P, S, P]
     lib.path_paged_trim.restype = I
     lib.path_paged_reserve.argtypes = [C, P, P, S, P]
@@ -686,19 +694,19 @@ class _on:
             g.__exit__(*e)
 
 
-def path_paged_workspace_bytes(cache, num_tokens=0, max_chunk=0, Hq=None):
+def path_paged_workspace_bytes(cache, num_tokens=0, max_chunk=0, Hq=None, prefix=False):
     """Workspace bytes of every call on `cache` with up to num_tokens new tokens in all and
-    max_chunk per sequence (0: the page calls alone). Hq: query heads, where the cache has no
-    g_pages to tell (default: the key heads)."""
+    max_chunk per sequence (0: the page calls alone); of those behind a prefix only with
+    prefix=True. Hq: query heads, where the cache has no g_pages to tell (default: the key heads)."""
     c = _paged_cache(cache, Hq=Hq)
-    return int(_load().path_paged_workspace_bytes(ctypes.byref(c), int(num_tokens),
-                                                  int(max_chunk)))
+    call = _load().path_paged_prefix_workspace_bytes if prefix else _load().path_paged_workspace_bytes
+    return int(call(ctypes.byref(c), int(num_tokens), int(max_chunk)))
 
 
-def new_paged_workspace(cache, num_tokens=0, max_chunk=0, Hq=None):
+def new_paged_workspace(cache, num_tokens=0, max_chunk=0, Hq=None, prefix=False):
     """A workspace of path_paged_workspace_bytes, its status word cleared."""
     torch = _torch()
-    n = path_paged_workspace_bytes(cache, num_tokens, max_chunk, Hq)
+    n = path_paged_workspace_bytes(cache, num_tokens, max_chunk, Hq, prefix)
     if n == 0:
         raise PathError(ERR_SHAPE, "path_paged_workspace_bytes")
     ws = torch.empty(n, dtype=torch.uint8, device=cache.k_pages.device)
@@ -707,7 +715,7 @@ def new_paged_workspace(cache, num_tokens=0, max_chunk=0, Hq=None):
 
 
 def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, scale, out,
-                  workspace, stream, more=()):
+                  workspace, stream, more=(), tensors=()):
     torch = _torch()
     f32 = torch.float32
     try:
@@ -739,7 +747,7 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
     if out is not None and (N > 1 and o0[0] == 0 or Hq > 1 and o0[1] == 0):
         raise ValueError("out must not repeat its own memory")
     _paged_workspace(workspace)
-    dev = _paged_devices(cache, q, k, v, w, beta, log_f, out, cu_tokens, workspace)
+    dev = _paged_devices(cache, q, k, v, w, beta, log_f, out, cu_tokens, workspace, *tensors)
     gate = () if log_f is None else (log_f.data_ptr(),)
     with _on(dev, stream) as on_stream:
         if out is None:
@@ -747,10 +755,11 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
             o0 = out.stride()
         own = workspace is None and N > 0 and c.seqs > 0
         if own:
-            workspace = new_paged_workspace(cache, N, max_chunk, Hq)
+            workspace = new_paged_workspace(cache, N, max_chunk, Hq, prefix=len(tensors) > 0)
         _check(getattr(_load(), name)(
             ctypes.byref(c), q.data_ptr(), k.data_ptr(), v.data_ptr(), w.data_ptr(),
-            beta.data_ptr(), *gate, cu_tokens.data_ptr(), N, int(max_chunk), *more, _scale(scale, d),
+            beta.data_ptr(), *gate, cu_tokens.data_ptr(), N, int(max_chunk), *more,
+            *(t.data_ptr() for t in tensors), _scale(scale, d),
             out.data_ptr(), _C14(q0[0], q0[1], k0[0], k0[1], v0[0], v0[1], w0[0], w0[1], b0[0], b0[1],
                                  f0[0], f0[1], o0[0], o0[1]), None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel(), on_stream), name)
@@ -828,6 +837,59 @@ def path_fox_paged_window_extend(q, k, v, w, beta, log_f, cu_tokens, cache, max_
     _paged_gates(log_f, cache)
     return _paged_extend("path_fox_paged_window_extend", q, k, v, w, beta, log_f, cu_tokens, cache,
                          max_chunk, scale, out, workspace, stream, (int(window), int(sinks)))
+
+
+def _prefix_tensors(q, cache, prefix_of, carry, gates=None, fox=False):
+    """Checks prefix_of, carry and (PaTH-FoX) gate_carry against the cache."""
+    torch = _torch()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise (ValueError if isinstance(q, torch.Tensor) else TypeError)("q must be a (tokens, Hq, d) tensor")
+    _paged_cache(cache, Hq=q.shape[1], on_gpu=False)
+    seqs, (_, Hkv, _, d) = cache.lens.shape[0], cache.k_pages.shape
+    named = [(prefix_of, "prefix_of", torch.int32, (seqs,)), (carry, "carry", torch.float32, (seqs, Hkv, d, d))]
+    if fox:
+        named.append((gates, "gate_carry", torch.float32, (seqs, q.shape[1])))
+    for t, n, dt, shape in named:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a tensor" % n)
+        if t.dtype != dt:
+            raise TypeError("%s must be %s, got %s" % (n, dt, t.dtype))
+        if tuple(t.shape) != shape:
+            raise ValueError("%s must have shape %s, got %s" % (n, shape, tuple(t.shape)))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % n)
+    return tuple(t for t, *_ in named)
+
+
+def path_paged_prefix_extend(q, k, v, w, beta, cu_tokens, cache, prefix_of, carry, max_chunk,
+                             scale=None, out=None, workspace=None, stream=None):
+    """path_paged_extend for sequences that continue a prefix. prefix_of (seqs) int32: the row of the
+    cache that a sequence continues, -1 for none; that row brings no tokens and stays as it is, however
+    many sequences continue it. carry (seqs, Hkv, d, d) fp32: the product of the transitions of a
+    sequence's own cached tokens (the identity where it has none, see new_paged_carry), advanced in
+    place. Workspaces: new_paged_workspace(..., prefix=True), or none as in path_paged_extend."""
+    return _paged_extend("path_paged_prefix_extend", q, k, v, w, beta, None, cu_tokens, cache, max_chunk,
+                         scale, out, workspace, stream, (), _prefix_tensors(q, cache, prefix_of, carry))
+
+
+def path_fox_paged_prefix_extend(q, k, v, w, beta, log_f, cu_tokens, cache, prefix_of, carry, gate_carry,
+                                 max_chunk, scale=None, out=None, workspace=None, stream=None):
+    """path_paged_prefix_extend with the forget gates of path_fox_paged_extend: gate_carry (seqs, Hq)
+    fp32 is the sum of the gates of a sequence's own cached tokens, advanced in place."""
+    _paged_gates(log_f, cache)
+    return _paged_extend("path_fox_paged_prefix_extend", q, k, v, w, beta, log_f, cu_tokens, cache,
+                         max_chunk, scale, out, workspace, stream, (),
+                         _prefix_tensors(q, cache, prefix_of, carry, gate_carry, True))
+
+
+def new_paged_carry(cache, Hq=None):
+    """(carry, gate_carry) of sequences without tokens of their own: identities and zeros. To begin
+    a row anew behind a prefix, set carry[row] to the identity and gate_carry[row] to 0."""
+    torch = _torch()
+    c = _paged_cache(cache, Hq=Hq)
+    dev = cache.k_pages.device
+    carry = torch.eye(c.d, device=dev).repeat(c.seqs, c.Hkv, 1, 1)
+    return carry, torch.zeros((c.seqs, c.Hq), device=dev)
 
 
 def _paged_gates(log_f, cache):

@@ -35,6 +35,12 @@ struct Step {
     float scale_log2;
     uint32_t *status;
     int window, sinks;  // window 0: every new token sees every position before it
+    // Sequences that continue a prefix (paged_prefix.cuh): the row that each continues (below 0: none),
+    // and of each row of queries (Hkv, N G) the softmax part of its prefix's keys.
+    const int *prefix_of;
+    const float *px;
+    const float2 *pxml;
+    bool shared;  // the step whose sequences are the prefixes: `cu` is a kernel's of this call
 };
 
 // Sequence b's tokens: first .. first + T - 1 of the packed step, behind n cached ones.
@@ -42,12 +48,28 @@ struct Seq {
     int first, T, n;
 };
 
-// T = 0 (and the status word set) where the lengths do not fit the step or the cache.
+__device__ __forceinline__ int cu_at(const Step &a, int b) { return a.shared ? a.cu[b] : __ldg(a.cu + b); }
+
+// Whether sequence b's row p can be its prefix: a row of the cache without tokens in this step and
+// without a prefix of its own.
+__device__ __forceinline__ bool prefix_fits(const Step &a, int b, int p) {
+    if (p >= a.c.seqs || p == b) return false;
+    const int n = __ldg(a.c.lens + p);
+    return __ldg(a.prefix_of + p) < 0 && __ldg(a.cu + p) == __ldg(a.cu + p + 1) && n >= 0 &&
+           n <= (long long)a.c.max_pages << a.c.page_shift;
+}
+
+// T = 0 (and the status word set) where the lengths do not fit the step or the cache, or the
+// prefix is none.
 __device__ __forceinline__ Seq seq_of(const Step &a, int b) {
-    const int c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1), n = __ldg(a.c.lens + b);
+    const int c0 = cu_at(a, b), c1 = cu_at(a, b + 1), n = __ldg(a.c.lens + b);
     Seq s{c0, c1 - c0, n};
-    const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.N && s.T <= a.max_chunk && n >= 0 &&
-                    (long long)n + s.T <= ((long long)a.c.max_pages << a.c.page_shift);
+    bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.N && s.T <= a.max_chunk && n >= 0 &&
+              (long long)n + (a.shared ? 0 : s.T) <= ((long long)a.c.max_pages << a.c.page_shift);
+    if (a.prefix_of != nullptr && s.T > 0) {
+        const int p = __ldg(a.prefix_of + b);
+        ok = ok && (p < 0 || prefix_fits(a, b, p));
+    }
     if (!ok) {
         report_status(a.status, kStatusCache);
         s.T = 0;
@@ -115,7 +137,7 @@ __device__ __forceinline__ bool block_of(const Step &a, int slot, int &b, int &c
     int lo = 0, hi = a.c.seqs - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(a.cu + mid) / kC + mid <= slot) lo = mid;
+        if (cu_at(a, mid) / kC + mid <= slot) lo = mid;
         else hi = mid - 1;
     }
     b = lo;

@@ -13,9 +13,17 @@ bool decode_takes(int G);
 size_t decode_part_bytes(const Cache &c, int d);
 cudaError_t launch_decode(const Step &a, int d, bool bf16, float *part, cudaStream_t stream);
 size_t f32_ws_bytes(const Cache &c, int N, int d, bool fox);
-cudaError_t launch_f32(const Step &a, int d, void *ws, cudaStream_t stream);
+cudaError_t launch_f32(Step a, int d, void *ws, float *carry, float *gates, void *pws, cudaStream_t stream);
 size_t tc_ws_bytes(const Cache &c, int N, int max_chunk, int d, bool fox);
-cudaError_t launch_tc(const Step &a, int d, void *ws, uint64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_tc(const Step &a, int d, void *ws, float *carry, float *gates, void *pws, uint64_t limit_ns,
+                      cudaStream_t stream);
+struct TcWs;
+size_t prefix_tc_bytes(const Step &a, int d);
+size_t prefix_f32_bytes(const Step &a, int d);
+cudaError_t launch_prefix_tc(Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
+                             uint64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_prefix_f32(Step &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws, bool first,
+                              cudaStream_t stream);
 size_t pages_ws_bytes(const Cache &c);
 cudaError_t launch_reserve(const Cache &c, const int *extra, void *ws, cudaStream_t stream);
 cudaError_t launch_fork(const Cache &c, const Rows<kMaxRows> &src, const Rows<kMaxRows> &dst, int row_bytes,
@@ -141,11 +149,25 @@ bool bad_stride(const paged::Stride &s, int bytes) {
     return s.tok < 0 || s.head < 0 || s.tok * bytes % 16 != 0 || s.head * bytes % 16 != 0;
 }
 
+// What a step has beyond its own tokens and cache: a window (0: none) and its sinks, or prefixes.
+struct More {
+    int window = 0, sinks = 0;
+    const int *prefix_of = nullptr;
+    float *carry = nullptr, *gates = nullptr;
+};
+
+size_t prefix_bytes(const path_paged_cache *p, int N) {
+    paged::Step a{};
+    a.c = to_cache(p);
+    a.N = N;
+    return p->dtype == PATH_BF16 ? paged::prefix_tc_bytes(a, p->d) : paged::prefix_f32_bytes(a, p->d);
+}
+
 path_status extend(const path_paged_cache *p, const void *q, const void *k, const void *v,
                    const void *w, const float *beta, const float *log_f, bool fox,
                    const int *cu_tokens, int N, int max_chunk, float scale, void *out,
                    const path_paged_strides *strides, void *ws, size_t ws_bytes, void *stream,
-                   int window = 0, int sinks = 0) {
+                   const More &more = More{}) {
     path_status st = check_cache_sizes(p);
     if (st == PATH_OK) st = check_step_sizes(p, N, max_chunk);
     if (st != PATH_OK) return st;
@@ -170,17 +192,27 @@ path_status extend(const path_paged_cache *p, const void *q, const void *k, cons
     for (const paged::Stride &r : {sb, sf})
         if (r.tok < 0 || r.head < 0) return PATH_ERR_ALIGN;
     const Cache c = to_cache(p);
-    const paged::Step a{c, q, k, v, w, beta, fox ? log_f : nullptr, out,
+    paged::Step a{c, q, k, v, w, beta, fox ? log_f : nullptr, out,
                         sq, sk, sv, sw, sb, sf, so,
-                        cu_tokens, N, max_chunk, scale * kLog2e, static_cast<uint32_t *>(ws), window, sinks};
+                        cu_tokens, N, max_chunk, scale * kLog2e, static_cast<uint32_t *>(ws),
+                  more.window, more.sinks, more.prefix_of, nullptr, nullptr, false};
+    const bool bf16 = p->dtype == PATH_BF16, prefix = more.prefix_of != nullptr;
     const long long seen = paged::most_seen(a);
-    if ((st = check_workspace(ws, ws_bytes, step_ws_bytes(p, seen, N, max_chunk, fox))) != PATH_OK) return st;
+    const size_t own = align256(step_ws_bytes(p, seen, N, max_chunk, fox));
+    if ((st = check_workspace(ws, ws_bytes, own + (prefix ? prefix_bytes(p, N) : 0))) != PATH_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (one_pass(c, seen, max_chunk, p->dtype == PATH_BF16, fox))
-        return cuda_status(paged::launch_decode(a, p->d, p->dtype == PATH_BF16,
-                                                reinterpret_cast<float *>(static_cast<char *>(ws) + 256), s));
-    if (p->dtype == PATH_BF16) return cuda_status(paged::launch_tc(a, p->d, ws, kWaitLimitNs, s));
-    return cuda_status(paged::launch_f32(a, p->d, ws, s));
+    char *const pws = static_cast<char *>(ws) + own;
+    if (one_pass(c, seen, max_chunk, bf16, fox)) {
+        cudaError_t e = cudaSuccess;
+        if (prefix)
+            e = bf16 ? paged::launch_prefix_tc(a, p->d, more.carry, more.gates, nullptr, pws, true, kWaitLimitNs, s)
+                     : paged::launch_prefix_f32(a, p->d, more.carry, more.gates, nullptr, nullptr, pws, true, s);
+        if (e == cudaSuccess)
+            e = paged::launch_decode(a, p->d, bf16, reinterpret_cast<float *>(static_cast<char *>(ws) + 256), s);
+        return cuda_status(e);
+    }
+    if (bf16) return cuda_status(paged::launch_tc(a, p->d, ws, more.carry, more.gates, pws, kWaitLimitNs, s));
+    return cuda_status(paged::launch_f32(a, p->d, ws, more.carry, more.gates, pws, s));
 }
 
 path_status check_window(int window, int sinks) {
@@ -195,7 +227,23 @@ path_status window_extend(const path_paged_cache *p, const void *q, const void *
     // with longer chunks the new tokens would hide one another
     if (check_window(window, sinks) != PATH_OK || max_chunk > window) return PATH_ERR_ARG;
     return extend(p, q, k, v, w, beta, log_f, fox, cu_tokens, N, max_chunk, scale, out, strides, ws,
-                  ws_bytes, stream, window, sinks);
+                  ws_bytes, stream, More{window, sinks});
+}
+
+path_status prefix_extend(const path_paged_cache *p, const void *q, const void *k, const void *v,
+                          const void *w, const float *beta, const float *log_f, bool fox,
+                          const int *cu_tokens, int N, int max_chunk, const int *prefix_of, float *carry,
+                          float *gate_carry, float scale, void *out, const path_paged_strides *strides,
+                          void *ws, size_t ws_bytes, void *stream) {
+    path_status st = check_cache_sizes(p);
+    if (st == PATH_OK) st = check_step_sizes(p, N, max_chunk);
+    if (st != PATH_OK) return st;
+    if (!std::isfinite(scale)) return PATH_ERR_ARG;
+    if (p->seqs == 0 || N == 0) return PATH_OK;
+    if (!prefix_of || !carry || (fox && !gate_carry)) return PATH_ERR_NULL;
+    if (!is_aligned(prefix_of, 4) || !is_aligned(carry, 16) || !is_aligned(gate_carry, 4)) return PATH_ERR_ALIGN;
+    return extend(p, q, k, v, w, beta, log_f, fox, cu_tokens, N, max_chunk, scale, out, strides, ws,
+                  ws_bytes, stream, More{0, 0, prefix_of, carry, fox ? gate_carry : nullptr});
 }
 
 // A list of sequence rows from the host: in range, none twice.
@@ -277,6 +325,32 @@ path_status path_fox_paged_window_extend(const path_paged_cache *cache, const vo
                                          void *stream) {
     return window_extend(cache, q, k, v, w, beta, log_f, true, cu_tokens, num_tokens, max_chunk, window,
                          sinks, scale, out, strides, ws, ws_bytes, stream);
+}
+
+size_t path_paged_prefix_workspace_bytes(const path_paged_cache *cache, int num_tokens, int max_chunk) {
+    const size_t n = path_paged_workspace_bytes(cache, num_tokens, max_chunk);
+    return n == 0 || num_tokens == 0 ? n : align256(n) + prefix_bytes(cache, num_tokens);
+}
+
+path_status path_paged_prefix_extend(const path_paged_cache *cache, const void *q, const void *k,
+                                     const void *v, const void *w, const float *beta,
+                                     const int *cu_tokens, int num_tokens, int max_chunk,
+                                     const int *prefix_of, float *carry, float scale, void *out,
+                                     const path_paged_strides *strides, void *ws, size_t ws_bytes,
+                                     void *stream) {
+    return prefix_extend(cache, q, k, v, w, beta, nullptr, false, cu_tokens, num_tokens, max_chunk,
+                         prefix_of, carry, nullptr, scale, out, strides, ws, ws_bytes, stream);
+}
+
+path_status path_fox_paged_prefix_extend(const path_paged_cache *cache, const void *q, const void *k,
+                                         const void *v, const void *w, const float *beta,
+                                         const float *log_f, const int *cu_tokens, int num_tokens,
+                                         int max_chunk, const int *prefix_of, float *carry,
+                                         float *gate_carry, float scale, void *out,
+                                         const path_paged_strides *strides, void *ws, size_t ws_bytes,
+                                         void *stream) {
+    return prefix_extend(cache, q, k, v, w, beta, log_f, true, cu_tokens, num_tokens, max_chunk,
+                         prefix_of, carry, gate_carry, scale, out, strides, ws, ws_bytes, stream);
 }
 
 path_status path_paged_trim(const path_paged_cache *cache, int window, int sinks, void *ws,

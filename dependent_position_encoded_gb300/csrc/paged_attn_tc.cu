@@ -342,7 +342,7 @@ tc_scan_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap t
     } else if (warp < 8) {
         // ============================================================ the state's bf16 copy
         bool ok = true;
-        const bool low = keeps_low(one_tile(s.T, G, D, FOX) ? 1 : 2, D);  // of what goes on to the cached keys
+        const bool low = low_queries(a, s.T, D);  // of what goes on to the cached keys
         uint8_t *const xs = sm + L::X;
         auto put = [&](int c, const float *x, bool take) {  // 32 columns from c
 #pragma unroll
@@ -448,16 +448,22 @@ template <int D>
 cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream);
 template <int D>
 cudaError_t launch_tc_finish(const Step &a, const TcWs &y, cudaStream_t stream);
+cudaError_t launch_prefix_tc(Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
+                             uint64_t limit_ns, cudaStream_t stream);
 
 namespace {
 
+// carry: of a step with prefixes (gates, and pws, the workspace's part for them, likewise)
 template <int D, bool FOX>
-cudaError_t launch_all(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream) {
+cudaError_t launch_all(Step a, const TcWs &y, float *carry, float *gates, void *pws, uint64_t limit_ns,
+                       cudaStream_t stream) {
     cudaError_t e = launch_tc_prep<D>(a, y, stream);
     if (a.max_chunk > kC) {
         if (e == cudaSuccess) e = launch_tc_carry<D>(a, y, stream);
         if (e == cudaSuccess) e = launch_scan<D, FOX>(a, y, limit_ns, stream);
     }
+    if (e == cudaSuccess && carry != nullptr)
+        e = launch_prefix_tc(a, D, carry, gates, &y, pws, false, limit_ns, stream);
     if (a.c.max_pages > 0) {
         const bool two = !one_tile(a.max_chunk, a.c.G, D, FOX);
         auto pass = [&](auto one_tiles, auto two_tiles) {
@@ -526,7 +532,8 @@ size_t tc_ws_bytes(const Cache &c, int N, int max_chunk, int d, bool fox) {
     return tc_layout(c, N, max_chunk, d, fox).total;
 }
 
-cudaError_t launch_tc(const Step &a, int d, void *ws, uint64_t limit_ns, cudaStream_t stream) {
+cudaError_t launch_tc(const Step &a, int d, void *ws, float *carry, float *gates, void *pws, uint64_t limit_ns,
+                      cudaStream_t stream) {
     const bool fox = a.log_f != nullptr;
     const TcLayout f = tc_layout(a.c, a.N, a.max_chunk, d, fox);
     char *w = static_cast<char *>(ws);
@@ -555,9 +562,9 @@ cudaError_t launch_tc(const Step &a, int d, void *ws, uint64_t limit_ns, cudaStr
     y.gtot = reinterpret_cast<double *>(w + f.gtot);
     y.gblk = reinterpret_cast<float2 *>(w + f.gblk);
     y.R = (long long)a.N * a.c.G;
-    if (d == 64)
-        return fox ? launch_all<64, true>(a, y, limit_ns, stream) : launch_all<64, false>(a, y, limit_ns, stream);
-    return fox ? launch_all<128, true>(a, y, limit_ns, stream) : launch_all<128, false>(a, y, limit_ns, stream);
+    auto all = [&](auto run) { return run(a, y, carry, gates, pws, limit_ns, stream); };
+    if (d == 64) return fox ? all(launch_all<64, true>) : all(launch_all<64, false>);
+    return fox ? all(launch_all<128, true>) : all(launch_all<128, false>);
 }
 
 }  // namespace paged

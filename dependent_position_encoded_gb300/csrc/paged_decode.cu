@@ -334,6 +334,13 @@ paged_decode_merge(const Step a, int chunk, int nsplit, const float *part) {
         Ls += pp[i * (D + 2) + 1] * f;
         Oc += pp[i * (D + 2) + 2 + c] * f;
     }
+    if (a.px != nullptr && __ldg(a.prefix_of + b) >= 0) {  // the keys of the sequence's prefix
+        const size_t row = ((size_t)h * a.N + s.first) * a.c.G + hq % a.c.G;
+        const float2 ml = a.pxml[row];
+        const float top = fmaxf(M, ml.x), f0 = exp2f(M - top), f1 = exp2f(ml.x - top);
+        Ls = fmaf(ml.y, f1, Ls * f0);
+        Oc = fmaf(a.px[row * D + c], f1, Oc * f0);
+    }
     static_cast<T *>(a.out)[s.first * a.so.tok + hq * a.so.head + c] = Elt<T>::from_f(Oc / Ls);
 }
 

@@ -1,0 +1,270 @@
+// Steps of sequences that continue a prefix: a row of the cache whose keys stay as they were when
+// its last token came, however many sequences continue it.
+//
+// A sequence's carry C (D x D fp32 per key head) is the product of the transitions of its own cached
+// tokens, c (per query head) the sum of their gates. New token i's logit with key j of the prefix is
+//     scale k_j . (C H_1 ... H_i q_i)  (+ g_j + c + sum_{s<=i} log f_s),
+// so all sequences of a prefix ask the same keys, with queries carried to the prefix's end:
+//     plan    counts each prefix's new tokens and gives every sequence its place among them, so that
+//             the queries of one prefix stand one behind the other;
+//     query   C q~_i (q~_i = H_1 ... H_i q_i, from the step's own kernels; a single token's is formed
+//             here, with the carry's update, C - beta (C w) w^T);
+//     pass    the attention of a prefix's queries over its keys, as if it were one sequence with that
+//             many new tokens (Step::shared), each key read once for all of them;
+//     join    the parts of a row into one, which the step's own joining takes up;
+//     carry   C <- C H_1 ... H_T, c <- c + sum log f, of sequences with several tokens.
+#pragma once
+
+#include "paged.cuh"
+
+namespace path {
+namespace paged {
+
+struct Prefix {
+    const int *of;  // (seqs) the row that a sequence continues, below 0: none
+    float *carry;   // (seqs, Hkv, D, D)
+    float *gates;   // (seqs, Hq), PaTH-FoX
+    int *cu;        // (seqs + 1) where each prefix's new tokens begin in their own order
+    int *start;     // (seqs) where a sequence's tokens begin in that order, -1: nowhere
+    float *px;      // (Hkv, N G, D) and pairs: the rows' softmax parts, in the step's order
+    float2 *pxml;
+};
+
+constexpr int kPrefixThr = 256;
+
+// The plan, by one CTA: x.cu and x.start. Sequences take their places in their order, so that no
+// result depends on timing; those with tokens of an earlier one (cu_tokens falls somewhere, which
+// the falling sequence reports) get none, so that no more than N tokens are placed.
+__device__ __forceinline__ void place_tokens(const Step &a, const Prefix &x) {
+    __shared__ int row[kPrefixThr], tokens[kPrefixThr], sums[kPrefixThr / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = a.c.seqs;
+    for (int p = tid; p <= S; p += kPrefixThr) x.cu[p] = 0;
+    int top = 0;
+    for (int base = 0; base < S; base += kPrefixThr) {
+        const int b = base + tid, begin = b < S ? __ldg(a.cu + b) : 0;
+        int m = begin;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, m, o);
+            if (lane >= o) m = max(m, t);
+        }
+        __syncthreads();
+        if (lane == 31) sums[warp] = m;
+        __syncthreads();
+        m = max(m, top);
+#pragma unroll
+        for (int i = 0; i < kPrefixThr / 32; ++i) {
+            if (i < warp) m = max(m, sums[i]);
+            top = max(top, sums[i]);
+        }
+        int p = -1, T = 0;
+        if (b < S && begin == m) {
+            T = seq_of(a, b).T;
+            if (T > 0) p = __ldg(x.of + b);
+        }
+        row[tid] = p;
+        tokens[tid] = T;
+        __syncthreads();
+        // the tokens of the prefix's earlier sequences: of the rounds before, and of this one
+        int before = p >= 0 ? x.cu[p] : 0;
+        if (p >= 0)
+            for (int i = 0; i < tid; ++i) before += row[i] == p ? tokens[i] : 0;
+        __syncthreads();
+        if (p >= 0) atomicAdd(x.cu + p, T);
+        if (b < S) x.start[b] = p >= 0 ? before : -1;
+        __syncthreads();
+    }
+    // counts to where they begin
+    int run = 0;
+    for (int base = 0; base <= S; base += kPrefixThr) {
+        const int p = base + tid, v = p <= S ? x.cu[p] : 0;
+        int t = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += u;
+        }
+        __syncthreads();
+        if (lane == 31) sums[warp] = t;
+        __syncthreads();
+        int before = run;
+#pragma unroll
+        for (int i = 0; i < kPrefixThr / 32; ++i) {
+            if (i < warp) before += sums[i];
+            run += sums[i];
+        }
+        if (p <= S) x.cu[p] = before + t - v;
+    }
+    __syncthreads();
+    for (int b = tid; b < S; b += kPrefixThr)
+        if (x.start[b] >= 0) x.start[b] += x.cu[__ldg(x.of + b)];
+    __syncthreads();
+}
+
+// The step whose sequences are the prefixes.
+inline Step shared_step(const Step &a, const Prefix &x) {
+    Step v = a;
+    v.cu = x.cu;
+    v.max_chunk = a.N;
+    v.window = v.sinks = 0;
+    v.prefix_of = nullptr;
+    v.px = nullptr;
+    v.pxml = nullptr;
+    v.shared = true;
+    return v;
+}
+
+// A sequence's only token, one CTA per key head: its queries carried to the prefix's end and the
+// carry's update from one read of the carry, all in fp32. Eight lanes share a row of C, 16 bytes each at
+// a time. put(g, i, x): entry i of query head g's carried query; gate(g, x): its gates.
+template <typename T, int D, typename P, typename F>
+__device__ __forceinline__ void prefix_single(const Step &a, const Prefix &x, const Seq &s, int b, int h, P put,
+                                              F gate) {
+    constexpr int NC = D / 32, NR = D / 32, kHeads = 16;  // columns / 32 of a row, rows / 32 of C
+    __shared__ __align__(16) float ws[D], qs[kHeads][D], os[kHeads][D];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.c.G;
+    const int sub = lane & 7, r0 = tid >> 3;
+    float4 *const C = reinterpret_cast<float4 *>(x.carry + ((size_t)b * a.c.Hkv + h) * D * D);
+    float4 c[NR][NC];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int k = 0; k < NC; ++k) c[i][k] = C[(r0 + 32 * i) * (D / 4) + 8 * k + sub];
+    const float beta = a.beta[(long long)s.first * a.sb.tok + h * a.sb.head];
+    const T *const wp = static_cast<const T *>(a.w) + (long long)s.first * a.sw.tok + h * a.sw.head;
+    if (tid < D) ws[tid] = Elt<T>::to_f(wp[tid]);
+    __syncthreads();
+    auto dot = [&](const float4 (&u)[NC], const float *v) {
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+            const float4 f = *reinterpret_cast<const float4 *>(v + 32 * k + 4 * sub);
+            t[0] = fmaf(u[k].x, f.x, t[0]);
+            t[1] = fmaf(u[k].y, f.y, t[1]);
+            t[2] = fmaf(u[k].z, f.z, t[2]);
+            t[3] = fmaf(u[k].w, f.w, t[3]);
+        }
+        float z = (t[0] + t[1]) + (t[2] + t[3]);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        return z;
+    };
+    for (int g0 = 0; g0 < G; g0 += kHeads) {
+        const int some = min(kHeads, G - g0);
+        // q~ = q - beta (w . q) w, a warp per head
+        for (int g = warp; g < some; g += kPrefixThr / 32) {
+            const T *const qp = static_cast<const T *>(a.q) + (long long)s.first * a.sq.tok +
+                                (long long)(h * G + g0 + g) * a.sq.head;
+            float q[D / 32], wq = 0.f;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) {
+                q[e] = Elt<T>::to_f(qp[lane + 32 * e]);
+                wq = fmaf(ws[lane + 32 * e], q[e], wq);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) wq += __shfl_xor_sync(0xffffffffu, wq, o);
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) qs[g][lane + 32 * e] = fmaf(-beta * wq, ws[lane + 32 * e], q[e]);
+        }
+        __syncthreads();
+        for (int g = 0; g < some; ++g)
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const float z = dot(c[i], qs[g]);
+                if (sub == 0) os[g][r0 + 32 * i] = z;
+            }
+        __syncthreads();
+        for (int e = tid; e < some * D; e += kPrefixThr) put(g0 + e / D, e % D, os[e / D][e % D]);
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const float z = beta * dot(c[i], ws);
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+            const float4 f = *reinterpret_cast<const float4 *>(ws + 32 * k + 4 * sub);
+            C[(r0 + 32 * i) * (D / 4) + 8 * k + sub] =
+                make_float4(fmaf(-z, f.x, c[i][k].x), fmaf(-z, f.y, c[i][k].y), fmaf(-z, f.z, c[i][k].z),
+                            fmaf(-z, f.w, c[i][k].w));
+        }
+    }
+    if (a.log_f != nullptr)
+        for (int g = tid; g < G; g += kPrefixThr) {
+            float *const p = x.gates + (size_t)b * a.c.Hq + h * G + g;
+            const float t = *p + a.log_f[(long long)s.first * a.sf.tok + (long long)(h * G + g) * a.sf.head];
+            *p = t;
+            gate(g, t);
+        }
+}
+
+// The carries of sequences with several tokens, in fp32 one token after the other: C <- C - beta (C w) w^T.
+// The rows of C do not meet, so a CTA takes 16 of them, eight lanes to a row.
+constexpr int kCarryRows = 16, kCarryThr = 8 * kCarryRows, kCarryTokens = 32;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kCarryThr) prefix_carry_kernel(const Step a, const Prefix x) {
+    constexpr int NC = D / 32;
+    __shared__ __align__(16) float ws[kCarryTokens][D];
+    __shared__ float bs[kCarryTokens];
+    const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, sub = tid & 7, r = blockIdx.x * kCarryRows + (tid >> 3);
+    grid_begin();
+    const Seq s = seq_of(a, b);
+    const bool mine = s.T > 1 && __ldg(x.of + b) >= 0;
+    grid_wait();
+    if (!mine) return;
+    float4 *const C = reinterpret_cast<float4 *>(x.carry + (((size_t)b * a.c.Hkv + h) * D + r) * D);
+    float4 c[NC];
+#pragma unroll
+    for (int k = 0; k < NC; ++k) c[k] = C[8 * k + sub];
+    for (int t0 = 0; t0 < s.T; t0 += kCarryTokens) {
+        const int some = min(kCarryTokens, s.T - t0);
+        __syncthreads();
+        for (int e = tid; e < some * D; e += kCarryThr)
+            ws[e / D][e % D] = Elt<T>::to_f(
+                static_cast<const T *>(a.w)[(long long)(s.first + t0 + e / D) * a.sw.tok + h * a.sw.head + e % D]);
+        if (tid < some) bs[tid] = a.beta[(long long)(s.first + t0 + tid) * a.sb.tok + h * a.sb.head];
+        __syncthreads();
+#pragma unroll 2
+        for (int t = 0; t < some; ++t) {
+            float4 w[NC];
+            float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                w[k] = *reinterpret_cast<const float4 *>(&ws[t][32 * k + 4 * sub]);
+                z[0] = fmaf(c[k].x, w[k].x, z[0]);
+                z[1] = fmaf(c[k].y, w[k].y, z[1]);
+                z[2] = fmaf(c[k].z, w[k].z, z[2]);
+                z[3] = fmaf(c[k].w, w[k].w, z[3]);
+            }
+            float y = (z[0] + z[1]) + (z[2] + z[3]);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+            y *= -bs[t];
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                c[k].x = fmaf(y, w[k].x, c[k].x);
+                c[k].y = fmaf(y, w[k].y, c[k].y);
+                c[k].z = fmaf(y, w[k].z, c[k].z);
+                c[k].w = fmaf(y, w[k].w, c[k].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < NC; ++k) C[8 * k + sub] = c[k];
+    if (a.log_f != nullptr && blockIdx.x == 0)
+        for (int g = tid; g < a.c.G; g += kCarryThr) {
+            float *const p = x.gates + (size_t)b * a.c.Hq + h * a.c.G + g;
+            double sum = *p;
+            for (int t = 0; t < s.T; ++t)
+                sum += a.log_f[(long long)(s.first + t) * a.sf.tok + (long long)(h * a.c.G + g) * a.sf.head];
+            *p = (float)sum;
+        }
+}
+
+template <typename T, int D>
+cudaError_t launch_prefix_carry(const Step &a, const Prefix &x, cudaStream_t stream) {
+    if (a.max_chunk <= 1) return cudaSuccess;
+    return launch(prefix_carry_kernel<T, D>, dim3(D / kCarryRows, a.c.Hkv, a.c.seqs), kCarryThr, 0, stream, false, a, x);
+}
+
+}  // namespace paged
+}  // namespace path

@@ -17,7 +17,6 @@ namespace paged {
 
 namespace {
 
-constexpr int kThr = 256;
 using bf = __nv_bfloat16;
 
 // ---------------------------------------------------------------- prep
@@ -77,68 +76,6 @@ __device__ __forceinline__ void put2(bf *t, int ld, int r, int c, uint32_t v) {
     *reinterpret_cast<uint32_t *>(t + r * ld + c) = v;
 }
 
-// Units and items of cached-key work before each sequence (one CTA, both plans). The parts'
-// buffers hold what sequences without common tokens can need, so one that begins before an
-// earlier one's begin or end (cu_tokens falls somewhere, which the falling sequence reports) gets
-// no work: with m the largest cu_tokens so far, a sequence counts where cu_tokens = m.
-template <int D>
-__device__ __forceinline__ void make_plans(const Step &a, const TcWs &y, long long *sums) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int *const tops = reinterpret_cast<int *>(sums + kThr / 32);
-    long long run[4] = {0, 0, 0, 0};
-    int top = 0;
-    for (int base = 0; base <= a.c.seqs; base += kThr) {
-        const int b = base + tid;
-        const int begin = b < a.c.seqs ? __ldg(a.cu + b) : 0;
-        int m = begin;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, m, o);
-            if (lane >= o) m = max(m, t);
-        }
-        __syncthreads();
-        if (lane == 31) tops[warp] = m;
-        __syncthreads();
-        m = max(m, top);
-#pragma unroll
-        for (int i = 0; i < kThr / 32; ++i) {
-            if (i < warp) m = max(m, tops[i]);
-            top = max(top, tops[i]);
-        }
-        long long v[4] = {0, 0, 0, 0};
-        if (b < a.c.seqs && begin == m) {
-            const Seq s = seq_of(a, b);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                int tiles, kt;
-                plan_of(a, s, D, p + 1, tiles, kt);
-                v[2 * p + 1] = kt > 0 ? (long long)tiles * a.c.Hkv : 0;
-                v[2 * p] = v[2 * p + 1] * kt;
-            }
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            long long x = v[q];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long t = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += t;
-            }
-            __syncthreads();
-            if (lane == 31) sums[warp] = x;
-            __syncthreads();
-            long long before = run[q], all = 0;
-#pragma unroll
-            for (int i = 0; i < kThr / 32; ++i) {
-                if (i < warp) before += sums[i];
-                all += sums[i];
-            }
-            if (b <= a.c.seqs) (q & 1 ? y.plan[q >> 1].items : y.plan[q >> 1].units)[b] = before + x - v[q];
-            run[q] += all;
-        }
-    }
-}
-
 // A sequence's only token: H = I - beta w w^T, q~ = q - beta (w . q) w, and the token's own key
 // and value enter the cache as they are. A warp per query head in turns; all threads form the
 // product less I, -beta w w^T.
@@ -196,7 +133,7 @@ __device__ __forceinline__ void prep_single(const Step &a, const TcWs &y, const 
             const float x = fmaf(-beta * wq, w[e], q[e]) * a.scale_log2;
             const bf xh = __float2bfloat16_rn(x);
             y.qt[r * D + lane * E + e] = xh;
-            if (keeps_low(one_tile(1, G, D, a.log_f != nullptr) ? 1 : 2, D))
+            if (low_queries(a, 1, D))
                 y.ql[r * D + lane * E + e] = __float2bfloat16_rn(x - __bfloat162float(xh));
             y.po[r * D + lane * E + e] = __bfloat162float(vp[e]);
         }
@@ -578,7 +515,7 @@ __global__ void __launch_bounds__(kThr, D == 64 ? 2 : 1) tc_prep_kernel(const St
             zero_acc(v);
             warp_mma_3<4, true>(v, Lh, Ll, LDS, m0, Uh, Ul, LDD, 64 * x + n0, m_end);
             // the scan starts from both parts
-            const bool low = !single || keeps_low(one_tile(s.T, G, D, a.log_f != nullptr) ? 1 : 2, D);
+            const bool low = !single || low_queries(a, s.T, D);
             each_eight(
                 v, m0, 64 * x + n0,
                 [&](int i, int j, float &p, float &q) {  // scaled here once: the attention's logits need no factor
@@ -1054,6 +991,16 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
         const float2 z = y.pml[row];
         float M = z.x, L = z.y, O[E];  // M is never -inf: a row has its own key
         load(y.po + row * D, O);
+        if (a.px != nullptr && __ldg(a.prefix_of + lo) >= 0) {  // the keys of the sequence's prefix
+            const float2 ml = a.pxml[row];
+            float v[E];
+            load(a.px + row * D, v);
+            const float top = fmaxf(M, ml.x), f0 = exp2f(M - top), f1 = exp2f(ml.x - top);
+            M = top;
+            L = fmaf(ml.y, f1, L * f0);
+#pragma unroll
+            for (int e = 0; e < E; ++e) O[e] = fmaf(v[e], f1, O[e] * f0);
+        }
         for (int p0 = 0; p0 < number; p0 += P) {
             float2 ml[P];
             float v[P][E];

@@ -77,11 +77,18 @@ __host__ __device__ __forceinline__ bool one_tile(int T, int G, int D, bool fox)
     return (T <= kC || D == 128 || fox) && (long long)T * G <= 128;
 }
 
+// Whether queries carried to the chunk's start are left in two parts: for the cached keys' pass, or to
+// be carried on to a prefix.
+__device__ __forceinline__ bool low_queries(const Step &a, int T, int D) {
+    return a.prefix_of != nullptr || keeps_low(one_tile(T, a.c.G, D, a.log_f != nullptr) ? 1 : 2, D);
+}
+
 // Row tiles and key tiles of a sequence in the plan of NT (0 where it goes with the other).
 __device__ __forceinline__ void plan_of(const Step &a, const Seq &s, int D, int NT, int &tiles, int &ktiles) {
     const int G = a.c.G, rows = s.T * G;  // T G <= N G, which the host keeps within an int
     ktiles = sight_of(a, s).tiles(s.n, 128);
-    tiles = one_tile(s.T, G, D, a.log_f != nullptr) == (NT == 1) ? (rows + 128 * NT - 1) / (128 * NT) : 0;
+    const bool one = a.shared ? rows <= 128 : one_tile(s.T, G, D, a.log_f != nullptr);
+    tiles = one == (NT == 1) ? (rows + 128 * NT - 1) / (128 * NT) : 0;
 }
 
 // Units per CTA: at least two, so that a part is worth its join.
@@ -118,6 +125,100 @@ __device__ __forceinline__ Stretch stretch_at(const Step &a, const Plan &p, int 
     const long long left = end - u;
     t.steps = kt - t.k0 < left ? kt - t.k0 : (int)left;
     return t;
+}
+
+constexpr int kThr = 256;  // threads of a CTA of the kernels beside the attention's
+
+// Units and items of cached-key work before each sequence (one CTA, both plans). The parts'
+// buffers hold what sequences without common tokens can need, so one that begins before an
+// earlier one's begin or end (cu_tokens falls somewhere, which the falling sequence reports) gets
+// no work: with m the largest cu_tokens so far, a sequence counts where cu_tokens = m.
+template <int D>
+__device__ __forceinline__ void make_plans(const Step &a, const TcWs &y, long long *sums) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int *const tops = reinterpret_cast<int *>(sums + kThr / 32);
+    long long run[4] = {0, 0, 0, 0};
+    int top = 0;
+    for (int base = 0; base <= a.c.seqs; base += kThr) {
+        const int b = base + tid;
+        const int begin = b < a.c.seqs ? cu_at(a, b) : 0;
+        int m = begin;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, m, o);
+            if (lane >= o) m = max(m, t);
+        }
+        __syncthreads();
+        if (lane == 31) tops[warp] = m;
+        __syncthreads();
+        m = max(m, top);
+#pragma unroll
+        for (int i = 0; i < kThr / 32; ++i) {
+            if (i < warp) m = max(m, tops[i]);
+            top = max(top, tops[i]);
+        }
+        long long v[4] = {0, 0, 0, 0};
+        if (b < a.c.seqs && begin == m) {
+            const Seq s = seq_of(a, b);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                int tiles, kt;
+                plan_of(a, s, D, p + 1, tiles, kt);
+                v[2 * p + 1] = kt > 0 ? (long long)tiles * a.c.Hkv : 0;
+                v[2 * p] = v[2 * p + 1] * kt;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            long long x = v[q];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += t;
+            }
+            __syncthreads();
+            if (lane == 31) sums[warp] = x;
+            __syncthreads();
+            long long before = run[q], all = 0;
+#pragma unroll
+            for (int i = 0; i < kThr / 32; ++i) {
+                if (i < warp) before += sums[i];
+                all += sums[i];
+            }
+            if (b <= a.c.seqs) (q & 1 ? y.plan[q >> 1].items : y.plan[q >> 1].units)[b] = before + x - v[q];
+            run[q] += all;
+        }
+    }
+}
+
+// The parts of a row, row `r` of sequence b's and key head h's, that the pass over cached keys left: number
+// of the first, how many, and where they begin (part q at `first` + (q >> copies) * tile + (q & ..) * (128 >> copies)).
+struct RowParts {
+    long long first;
+    int number, copies, tile;
+    const float *so;
+    const float2 *sml;
+    __device__ __forceinline__ size_t at(int q) const {
+        return first + (size_t)(q >> copies) * tile + (q & ((1 << copies) - 1)) * (128 >> copies);
+    }
+};
+__device__ __forceinline__ RowParts parts_of(const Step &a, const TcWs &y, const Seq &s, int b, int h, int r, int D) {
+    int NT = 1, tiles, kt;
+    plan_of(a, s, D, 1, tiles, kt);
+    if (tiles == 0) {
+        NT = 2;
+        plan_of(a, s, D, 2, tiles, kt);
+    }
+    const Plan &p = NT == 1 ? y.plan[0] : y.plan[1];
+    const int rows_all = s.T * a.c.G, ti = r / (128 * NT), it = h * tiles + ti;
+    RowParts x{0, 0, NT == 2 ? 0 : rows_all <= 32 ? 2 : rows_all <= 64 ? 1 : 0, 128 * NT,
+               NT == 1 ? y.so[0] : y.so[1], NT == 1 ? y.sml[0] : y.sml[1]};
+    if (kt > 0 && p.items[b + 1] > p.items[b]) {
+        const long long per = plan_per(p, a.c.seqs), u = p.units[b] + (long long)it * kt, c0 = u / per;
+        x.first = (c0 + p.items[b] + it) * x.tile + r % x.tile;
+        x.number = ((int)((u + kt - 1) / per - c0) + 1) << x.copies;
+    }
+    return x;
 }
 
 // Rows of `rows` per tile over all sequences: tile i of sequence b is slot

@@ -428,6 +428,46 @@ path_status path_fox_paged_window_extend(const path_paged_cache *cache, const vo
                                          void *stream);
 
 /*
+ * path_paged_extend for sequences that continue a prefix: a row of the same cache whose keys and
+ * values lie there once, whatever number of sequences continue it, and stay as they are. (Every
+ * step rewrites its own sequence's cached keys, so copies of a prompt cannot share them; behind a
+ * prefix it is the queries that are carried to the prefix's end instead.)
+ *   prefix_of : (seqs) int32 on the device: the row that a sequence continues, below 0 for none (it
+ *            is then a sequence of path_paged_extend). That row must be another one, have no tokens in
+ *            this step and no prefix of its own (else PATH_ERR_CACHE, and the sequence is left as
+ *            it was). Rows without tokens are not looked at.
+ *   carry  : (seqs, Hkv, d, d) fp32: for a sequence with a prefix C = H_1 ... H_m over its own m cached
+ *            tokens, row-major; the identity where it has none. Advanced in place, C <- C H_1 ... H_T.
+ * New token i's logit with key j of the prefix is scale * k_j^T (C H_1 ... H_i) q_i; the sequence's own
+ * cached and new keys are scored and advanced as in path_paged_extend, and one softmax goes over all of
+ * them. A prefix is a row that steps have filled as any other; it may grow again, once it is nobody's
+ * prefix any more. path_paged_fork copies a sequence's own pages: copy its row of carry with it.
+ *   ws     : path_paged_prefix_workspace_bytes(cache, num_tokens, max_chunk) bytes, which serves every
+ *            other call on the cache too
+ */
+size_t path_paged_prefix_workspace_bytes(const path_paged_cache *cache, int num_tokens, int max_chunk);
+path_status path_paged_prefix_extend(const path_paged_cache *cache, const void *q, const void *k,
+                                     const void *v, const void *w, const float *beta,
+                                     const int *cu_tokens, int num_tokens, int max_chunk,
+                                     const int *prefix_of, float *carry, float scale, void *out,
+                                     const path_paged_strides *strides, void *ws, size_t ws_bytes,
+                                     void *stream);
+
+/*
+ * path_paged_prefix_extend with the forget gates of path_fox_paged_extend: the logit with key j of the
+ * prefix gains g_j + c + sum_{s<=i} log f_s.
+ *   gate_carry : (seqs, Hq) fp32: c, the sum of the gates of the sequence's own cached tokens (0 where it
+ *            has none), advanced in place
+ */
+path_status path_fox_paged_prefix_extend(const path_paged_cache *cache, const void *q, const void *k,
+                                         const void *v, const void *w, const float *beta,
+                                         const float *log_f, const int *cu_tokens, int num_tokens,
+                                         int max_chunk, const int *prefix_of, float *carry,
+                                         float *gate_carry, float scale, void *out,
+                                         const path_paged_strides *strides, void *ws, size_t ws_bytes,
+                                         void *stream);
+
+/*
  * Gives back the pages that no later window step of their sequence reaches: those whose every
  * position j has j >= sinks and j <= lens[s] - window. The slots behind them move down and lens[s]
  * falls by their tokens (logits go by distances, so nothing else changes): a stream's cache
