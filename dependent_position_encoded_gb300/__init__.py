@@ -842,6 +842,16 @@ def path_fox_paged_window_extend(q, k, v, w, beta, log_f, cu_tokens, cache, max_
 def _prefix_tensors(q, cache, prefix_of, carry, gates=None, fox=False):
     """Checks prefix_of, carry and (PaTH-FoX) gate_carry against the cache."""
     torch = _torch()
+    tensors = (prefix_of, carry, gates) if fox else (prefix_of, carry)
+    try:
+        (seqs,), (_, Hkv, _, d), (_, Hq, _) = cache.lens.shape, cache.k_pages.shape, q.shape
+        if (prefix_of.dtype == torch.int32 and carry.dtype == torch.float32 and prefix_of.shape == (seqs,)
+                and carry.shape == (seqs, Hkv, d, d) and prefix_of.is_contiguous() and carry.is_contiguous()
+                and (not fox or (gates.dtype == torch.float32 and gates.shape == (seqs, Hq)
+                                 and gates.is_contiguous()))):
+            return tensors
+    except (AttributeError, TypeError, ValueError):
+        pass
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise (ValueError if isinstance(q, torch.Tensor) else TypeError)("q must be a (tokens, Hq, d) tensor")
     _paged_cache(cache, Hq=q.shape[1], on_gpu=False)
@@ -858,7 +868,7 @@ def _prefix_tensors(q, cache, prefix_of, carry, gates=None, fox=False):
             raise ValueError("%s must have shape %s, got %s" % (n, shape, tuple(t.shape)))
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % n)
-    return tuple(t for t, *_ in named)
+    return tensors
 
 
 def path_paged_prefix_extend(q, k, v, w, beta, cu_tokens, cache, prefix_of, carry, max_chunk,

@@ -3,7 +3,7 @@
 #include <climits>
 #include <cmath>
 
-#include "paged.cuh"
+#include "paged_tc.cuh"
 #include "paged_pages.cuh"
 #include "path_attn.h"
 
@@ -11,17 +11,16 @@ namespace path {
 namespace paged {
 bool decode_takes(int G);
 size_t decode_part_bytes(const Cache &c, int d);
-cudaError_t launch_decode(const Step &a, int d, bool bf16, float *part, cudaStream_t stream);
+cudaError_t launch_decode(const Step &a, int d, bool bf16, const Behind *behind, float *part, cudaStream_t stream);
 size_t f32_ws_bytes(const Cache &c, int N, int d, bool fox);
 cudaError_t launch_f32(Step a, int d, void *ws, float *carry, float *gates, void *pws, cudaStream_t stream);
 size_t tc_ws_bytes(const Cache &c, int N, int max_chunk, int d, bool fox);
 cudaError_t launch_tc(const Step &a, int d, void *ws, float *carry, float *gates, void *pws, uint64_t limit_ns,
                       cudaStream_t stream);
-struct TcWs;
 size_t prefix_tc_bytes(const Step &a, int d);
 size_t prefix_f32_bytes(const Step &a, int d);
-cudaError_t launch_prefix_tc(Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
-                             uint64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_prefix_tc(const Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
+                             uint64_t limit_ns, Behind *behind, cudaStream_t stream);
 cudaError_t launch_prefix_f32(Step &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws, bool first,
                               cudaStream_t stream);
 size_t pages_ws_bytes(const Cache &c);
@@ -204,11 +203,13 @@ path_status extend(const path_paged_cache *p, const void *q, const void *k, cons
     char *const pws = static_cast<char *>(ws) + own;
     if (one_pass(c, seen, max_chunk, bf16, fox)) {
         cudaError_t e = cudaSuccess;
+        paged::Behind behind = {};
         if (prefix)
-            e = bf16 ? paged::launch_prefix_tc(a, p->d, more.carry, more.gates, nullptr, pws, true, kWaitLimitNs, s)
+            e = bf16 ? paged::launch_prefix_tc(a, p->d, more.carry, more.gates, nullptr, pws, true, kWaitLimitNs,
+                                               &behind, s)
                      : paged::launch_prefix_f32(a, p->d, more.carry, more.gates, nullptr, nullptr, pws, true, s);
         if (e == cudaSuccess)
-            e = paged::launch_decode(a, p->d, bf16, reinterpret_cast<float *>(static_cast<char *>(ws) + 256), s);
+            e = paged::launch_decode(a, p->d, bf16, &behind, reinterpret_cast<float *>(static_cast<char *>(ws) + 256), s);
         return cuda_status(e);
     }
     if (bf16) return cuda_status(paged::launch_tc(a, p->d, ws, more.carry, more.gates, pws, kWaitLimitNs, s));

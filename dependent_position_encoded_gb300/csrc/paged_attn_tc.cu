@@ -447,23 +447,24 @@ cudaError_t launch_tc_prep(const Step &a, const TcWs &y, cudaStream_t stream);
 template <int D>
 cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream);
 template <int D>
-cudaError_t launch_tc_finish(const Step &a, const TcWs &y, cudaStream_t stream);
-cudaError_t launch_prefix_tc(Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
-                             uint64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_tc_finish(const Step &a, const TcWs &y, const Behind &x, cudaStream_t stream);
+cudaError_t launch_prefix_tc(const Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
+                             uint64_t limit_ns, Behind *behind, cudaStream_t stream);
 
 namespace {
 
 // carry: of a step with prefixes (gates, and pws, the workspace's part for them, likewise)
 template <int D, bool FOX>
-cudaError_t launch_all(Step a, const TcWs &y, float *carry, float *gates, void *pws, uint64_t limit_ns,
+cudaError_t launch_all(const Step &a, const TcWs &y, float *carry, float *gates, void *pws, uint64_t limit_ns,
                        cudaStream_t stream) {
     cudaError_t e = launch_tc_prep<D>(a, y, stream);
     if (a.max_chunk > kC) {
         if (e == cudaSuccess) e = launch_tc_carry<D>(a, y, stream);
         if (e == cudaSuccess) e = launch_scan<D, FOX>(a, y, limit_ns, stream);
     }
+    Behind behind = {};
     if (e == cudaSuccess && carry != nullptr)
-        e = launch_prefix_tc(a, D, carry, gates, &y, pws, false, limit_ns, stream);
+        e = launch_prefix_tc(a, D, carry, gates, &y, pws, false, limit_ns, &behind, stream);
     if (a.c.max_pages > 0) {
         const bool two = !one_tile(a.max_chunk, a.c.G, D, FOX);
         auto pass = [&](auto one_tiles, auto two_tiles) {
@@ -473,7 +474,7 @@ cudaError_t launch_all(Step a, const TcWs &y, float *carry, float *gates, void *
         if (a.window > 0) pass(launch_cached<1, D, FOX, Pass::window>, launch_cached<2, D, FOX, Pass::window>);
         else pass(launch_cached<1, D, FOX, Pass::step>, launch_cached<2, D, FOX, Pass::step>);
     }
-    if (e == cudaSuccess) e = launch_tc_finish<D>(a, y, stream);
+    if (e == cudaSuccess) e = launch_tc_finish<D>(a, y, behind, stream);
     return e;
 }
 

@@ -20,7 +20,7 @@
 // value row is read only if one of its G logits comes within 2^-64 of the head's own token
 // (a lower bound of the row's maximum): 2^22 keys below that move the sum by less than
 // 2^-42 of itself.
-#include "paged.cuh"
+#include "paged_tc.cuh"
 
 namespace path {
 namespace paged {
@@ -286,9 +286,10 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
 
 // D threads per (query head, sequence): score the new token, merge the splits and, for the
 // first query head of a key head, append the new key and value.
-template <typename T, bool FOX, int D>
+// BEHIND: sequences with prefixes, whose parts are joined too.
+template <typename T, bool FOX, int D, bool BEHIND>
 __global__ void __launch_bounds__(D)
-paged_decode_merge(const Step a, int chunk, int nsplit, const float *part) {
+paged_decode_merge(const Step a, const Behind z, int chunk, int nsplit, const float *part) {
     __shared__ float red[D / 32];
     const int hq = blockIdx.x, b = blockIdx.y, c = threadIdx.x;
     grid_begin();
@@ -334,7 +335,24 @@ paged_decode_merge(const Step a, int chunk, int nsplit, const float *part) {
         Ls += pp[i * (D + 2) + 1] * f;
         Oc += pp[i * (D + 2) + 2 + c] * f;
     }
-    if (a.px != nullptr && __ldg(a.prefix_of + b) >= 0) {  // the keys of the sequence's prefix
+    if (BEHIND && std::is_same<T, __nv_bfloat16>::value && __ldg(z.of + b) >= 0) {
+        // the keys of the sequence's prefix
+        const RowParts x = parts_behind(a, z, b, h, 0, hq % a.c.G);
+        float top = M;
+#pragma unroll 8
+        for (int q = 0; q < x.number; ++q) top = fmaxf(top, x.sml[x.at(q)].x);
+        const float f0 = exp2f(M - top);
+        Ls *= f0;
+        Oc *= f0;
+#pragma unroll 8
+        for (int q = 0; q < x.number; ++q) {
+            const float2 ml = x.sml[x.at(q)];
+            const float f = exp2f(ml.x - top);
+            Ls = fmaf(ml.y, f, Ls);
+            Oc = fmaf(x.so[x.at(q) * D + c], f, Oc);
+        }
+    }
+    if (BEHIND && std::is_same<T, float>::value && __ldg(a.prefix_of + b) >= 0) {
         const size_t row = ((size_t)h * a.N + s.first) * a.c.G + hq % a.c.G;
         const float2 ml = a.pxml[row];
         const float top = fmaxf(M, ml.x), f0 = exp2f(M - top), f1 = exp2f(ml.x - top);
@@ -345,23 +363,23 @@ paged_decode_merge(const Step a, int chunk, int nsplit, const float *part) {
 }
 
 template <typename T, bool FOX, int D, int G>
-cudaError_t launch_g(const Step &a, int chunk, int nsplit, float *part, cudaStream_t stream) {
+cudaError_t launch_g(const Step &a, const Behind &x, int chunk, int nsplit, float *part, cudaStream_t stream) {
     if (nsplit > 0) {
         const cudaError_t e = launch(a.window > 0 ? paged_decode_split<T, FOX, D, G, true>
                                                   : paged_decode_split<T, FOX, D, G, false>,
                                      dim3(nsplit, a.c.Hkv, a.c.seqs), kThreads, 0, stream, true, a, chunk, nsplit, part);
         if (e != cudaSuccess) return e;
     }
-    return launch(paged_decode_merge<T, FOX, D>, dim3(a.c.Hq, a.c.seqs), D, 0, stream, nsplit == 0, a, chunk, nsplit,
-                  part);
+    return launch(a.prefix_of != nullptr ? paged_decode_merge<T, FOX, D, true> : paged_decode_merge<T, FOX, D, false>,
+                  dim3(a.c.Hq, a.c.seqs), D, 0, stream, nsplit == 0, a, x, chunk, nsplit, part);
 }
 
 template <typename T, bool FOX, int D>
-cudaError_t launch_d(const Step &a, int chunk, int nsplit, float *part, cudaStream_t stream) {
+cudaError_t launch_d(const Step &a, const Behind &x, int chunk, int nsplit, float *part, cudaStream_t stream) {
     switch (a.c.G) {
-        case 1: return launch_g<T, FOX, D, 1>(a, chunk, nsplit, part, stream);
-        case 2: return launch_g<T, FOX, D, 2>(a, chunk, nsplit, part, stream);
-        default: return launch_g<T, FOX, D, 4>(a, chunk, nsplit, part, stream);
+        case 1: return launch_g<T, FOX, D, 1>(a, x, chunk, nsplit, part, stream);
+        case 2: return launch_g<T, FOX, D, 2>(a, x, chunk, nsplit, part, stream);
+        default: return launch_g<T, FOX, D, 4>(a, x, chunk, nsplit, part, stream);
     }
 }
 
@@ -388,17 +406,19 @@ size_t decode_part_bytes(const Cache &c, int d) {
     return (size_t)c.seqs * c.Hq * splits * (d + 2) * sizeof(float);
 }
 
-cudaError_t launch_decode(const Step &a, int d, bool bf16, float *part, cudaStream_t stream) {
+// behind: of a bf16 step with prefixes, their parts
+cudaError_t launch_decode(const Step &a, int d, bool bf16, const Behind *behind, float *part, cudaStream_t stream) {
+    const Behind x = behind != nullptr ? *behind : Behind{};
     const long long cap = most_seen(a);
     const int chunk = decode_chunk(a.c, cap), nsplit = (int)((cap + chunk - 1) / chunk);
     const bool fox = a.log_f != nullptr;
     auto pick = [&](auto t) {
         using T = decltype(t);
         if (d == 64)
-            return fox ? launch_d<T, true, 64>(a, chunk, nsplit, part, stream)
-                       : launch_d<T, false, 64>(a, chunk, nsplit, part, stream);
-        return fox ? launch_d<T, true, 128>(a, chunk, nsplit, part, stream)
-                   : launch_d<T, false, 128>(a, chunk, nsplit, part, stream);
+            return fox ? launch_d<T, true, 64>(a, x, chunk, nsplit, part, stream)
+                       : launch_d<T, false, 64>(a, x, chunk, nsplit, part, stream);
+        return fox ? launch_d<T, true, 128>(a, x, chunk, nsplit, part, stream)
+                   : launch_d<T, false, 128>(a, x, chunk, nsplit, part, stream);
     };
     return bf16 ? pick(__nv_bfloat16{}) : pick(0.f);
 }

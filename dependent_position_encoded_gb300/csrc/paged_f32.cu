@@ -589,7 +589,8 @@ F32Layout f32_layout(const Cache &c, int N, int d, bool fox) {
 
 bool decode_takes(int G);
 size_t decode_part_bytes(const Cache &c, int d);
-cudaError_t launch_decode(const Step &a, int d, bool bf16, float *part, cudaStream_t stream);
+struct Behind;
+cudaError_t launch_decode(const Step &a, int d, bool bf16, const Behind *behind, float *part, cudaStream_t stream);
 
 cudaError_t launch_prefix_f32(Step &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws, bool first,
                               cudaStream_t stream);
@@ -616,7 +617,7 @@ cudaError_t launch_f32(Step a, int d, void *ws, float *carry, float *gates, void
         e = blocks();
         if (e == cudaSuccess) e = launch_prefix_f32(a, d, carry, gates, y.qt, y.gq, pws, false, stream);
     }
-    if (e == cudaSuccess && singles) e = launch_decode(a, d, false, at(f.total), stream);
+    if (e == cudaSuccess && singles) e = launch_decode(a, d, false, nullptr, at(f.total), stream);
     if (e == cudaSuccess && carry == nullptr) e = blocks();
     if (e != cudaSuccess) return e;
     return d == 64 ? launch_cache<64>(a, y, stream) : launch_cache<128>(a, y, stream);

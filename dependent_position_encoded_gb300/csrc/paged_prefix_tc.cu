@@ -1,5 +1,5 @@
-// The prefixes of a bf16 step (paged_prefix.cuh): plan, queries, the pass over the shared keys on
-// tcgen05 tensor cores (paged_cached_tc.cuh) and its joining.
+// The prefixes of a bf16 step (paged_prefix.cuh): plan, queries and the pass over the shared keys on
+// tcgen05 tensor cores (paged_cached_tc.cuh).
 #include "paged_cached_tc.cuh"
 #include "paged_prefix.cuh"
 
@@ -12,41 +12,31 @@ namespace {
 
 static_assert(kThr == kPrefixThr, "make_plans");
 
-template <int D>
-__global__ void __launch_bounds__(kThr) prefix_plan_kernel(const Step a, const Step v, const Prefix x, const TcWs y) {
+// ---------------------------------------------------------------- plan and single tokens
+// The first CTA makes the plan, the others carry the single tokens' queries, a sequence and key head
+// each. With up to kFused sequences they find their places by themselves beside it, else by a plan
+// made before (by this kernel, with no sequence).
+constexpr int kFused = 1024;
+
+template <int D, bool FUSED>
+__global__ void __launch_bounds__(kThr) prefix_single_kernel(const Step a, const Step v, const Prefix x, const TcWs z,
+                                                             bool plan) {
     __shared__ long long sums[2 * kThr / 32];
+    const int G = a.c.G;
     grid_begin();
-    place_tokens(a, x);
-    make_plans<D>(v, y, sums);
-    grid_wait();  // what it writes is this call's alone
-}
-
-// ---------------------------------------------------------------- queries
-template <int D>
-struct QuerySmem {
-    static constexpr int LDD = D + 8;
-    static constexpr size_t Ch = 0, Cl = (size_t)D * LDD * 2, Xh = 2 * Cl, Xl = Xh + (size_t)kC * LDD * 2,
-                            bytes = Xl + (size_t)kC * LDD * 2;
-};
-
-// 64 rows of a sequence and key head, X C^T with both in two bf16 parts (16 bits of significand), or
-// its only token's. y: the step's, whose queries have been carried to the chunk's start; z: those of the
-// shared step.
-template <int D>
-__global__ void __launch_bounds__(kThr) prefix_query_kernel(const Step a, const Prefix x, const TcWs y, const TcWs z) {
-    using S = QuerySmem<D>;
-    constexpr int LDD = S::LDD, NT = D / 16, PER = D / 8;
-    extern __shared__ __align__(16) uint8_t smem[];
-    const int h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, G = a.c.G;
-    int b, tile;
-    Seq s;
-    grid_begin();
-    const bool mine = tile_of(a, blockIdx.x, kC, b, tile, s);
-    grid_wait();
-    if (!mine || x.start[b] < 0) return;
-    const size_t from = (size_t)h * y.R + (size_t)s.first * G, to = (size_t)h * y.R + (size_t)x.start[b] * G;
-    if (s.T == 1) {
-        if (tile > 0) return;
+    if (blockIdx.x == 0 && plan) {
+        place_tokens(a, x);
+        make_plans<D>(v, z, sums);
+        grid_wait();  // what it writes is this call's alone
+        return;
+    }
+    const int item = blockIdx.x - (plan ? 1 : 0), h = item % a.c.Hkv, b = item / a.c.Hkv;
+    if (!FUSED) grid_wait();
+    const Seq s = seq_of(a, b);
+    int start = -1;
+    if (s.T == 1 && __ldg(x.of + b) >= 0) start = FUSED ? place_one(a, x, b) : x.start[b];
+    if (start >= 0) {
+        const size_t to = (size_t)h * z.R + (size_t)start * G;
         prefix_single<bf, D>(
             a, x, s, b, h,
             [&](int g, int i, float q) {
@@ -56,128 +46,111 @@ __global__ void __launch_bounds__(kThr) prefix_query_kernel(const Step a, const 
                 z.ql[(to + g) * D + i] = __float2bfloat16_rn(q - __bfloat162float(hi));
             },
             [&](int g, float t) { z.gq[to + g] = t; });
-        return;
     }
-    bf *const Ch = reinterpret_cast<bf *>(smem + S::Ch), *const Cl = reinterpret_cast<bf *>(smem + S::Cl),
-       *const Xh = reinterpret_cast<bf *>(smem + S::Xh), *const Xl = reinterpret_cast<bf *>(smem + S::Xl);
-    const int row0 = kC * tile, rows = min(kC, s.T * G - row0);
-    for (int e = tid; e < kC * PER; e += kThr) {
-        const int r = e / PER, q = e % PER * 8;
-        const size_t at = (from + row0 + r) * D + q;
-        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4 *>(Xh + r * LDD + q) = r < rows ? *reinterpret_cast<const uint4 *>(y.qt + at) : none;
-        *reinterpret_cast<uint4 *>(Xl + r * LDD + q) = r < rows ? *reinterpret_cast<const uint4 *>(y.ql + at) : none;
-    }
-    const float4 *const C = reinterpret_cast<const float4 *>(x.carry + ((size_t)b * a.c.Hkv + h) * D * D);
-#pragma unroll 4
-    for (int e = tid; e < D * D / 4; e += kThr) {
-        const int r = e / (D / 4), q = e % (D / 4) * 4;
-        const float4 c = C[e];
-        uint2 hi, lo;
-        split2(c.x, c.y, hi.x, lo.x);
-        split2(c.z, c.w, hi.y, lo.y);
-        *reinterpret_cast<uint2 *>(Ch + r * LDD + q) = hi;
-        *reinterpret_cast<uint2 *>(Cl + r * LDD + q) = lo;
-    }
-    __syncthreads();
-    const int m0 = 16 * (warp & 3), n0 = D / 2 * (warp >> 2);
-    float acc[NT][4];
-    zero_acc(acc);
-    warp_mma_3<NT, false>(acc, Xh, Xl, LDD, m0, Ch, Cl, LDD, n0, D / 16);
-    each_eight(
-        acc, m0, n0, [](int, int, float &, float &) {},
-        [&](int i, int j, uint4 hi, uint4 lo) {
-            if (i >= rows) return;
-            *reinterpret_cast<uint4 *>(z.qt + (to + row0 + i) * D + j) = hi;
-            *reinterpret_cast<uint4 *>(z.ql + (to + row0 + i) * D + j) = lo;
-        });
-    if (a.log_f != nullptr && tid < rows)
-        z.gq[to + row0 + tid] = y.gq[from + row0 + tid] + x.gates[(size_t)b * a.c.Hq + h * G + (row0 + tid) % G];
+    if (FUSED) grid_wait();  // no kernel before reads or writes what this one does
 }
 
-// ---------------------------------------------------------------- join
-// A warp per row: the parts of its prefix's keys into one, four at a time.
+// ---------------------------------------------------------------- queries of several tokens
+// X C^T over tiles of 64 rows of a sequence and key head, kTiles of them on one load of C, both factors
+// in two bf16 parts (16 bits of significand). y: the step's, whose queries have been carried to the chunk's
+// start; z: those of the shared step.
+constexpr int kTiles = 4;
+
 template <int D>
-__global__ void __launch_bounds__(kThr) prefix_join_kernel(const Step a, const Step v, const Prefix x, const TcWs z) {
-    constexpr int E = D / 32, P = 4;
-    const int G = a.c.G, h = blockIdx.y, lane = threadIdx.x & 31;
-    const long long r = blockIdx.x * (long long)(kThr / 32) + (threadIdx.x >> 5);
+struct QuerySmem {
+    static constexpr int LDD = D + 8;
+    static constexpr size_t Ch = 0, Cl = (size_t)D * LDD * 2, Xh = 2 * Cl, Xl = Xh + (size_t)kC * LDD * 2,
+                            bytes = Xl + (size_t)kC * LDD * 2;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThr, 2) prefix_query_kernel(const Step a, const Prefix x, const TcWs y, const TcWs z) {
+    using S = QuerySmem<D>;
+    constexpr int LDD = S::LDD, NT = D / 16, PER = D / 8, IT = kC * PER / kThr;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, G = a.c.G;
+    int b, part;
+    Seq s;
     grid_begin();
-    // the sequence of the row: the last that begins at or before its token
-    int b = 0;
-    Seq s{0, 0, 0};
-    const int tok = (int)(r / G);
-    if (r < z.R) {
-        for (int hi = a.c.seqs - 1; b < hi;) {
-            const int mid = (b + hi + 1) >> 1;
-            if (__ldg(a.cu + mid) <= tok) b = mid;
-            else hi = mid - 1;
+    const bool mine = tile_of(a, blockIdx.x, kC * kTiles, b, part, s) && s.T > 1;
+    bf *const Ch = reinterpret_cast<bf *>(smem + S::Ch), *const Cl = reinterpret_cast<bf *>(smem + S::Cl),
+       *const Xh = reinterpret_cast<bf *>(smem + S::Xh), *const Xl = reinterpret_cast<bf *>(smem + S::Xl);
+    const bool behind = mine && __ldg(x.of + b) >= 0;
+    if (behind) {
+        const float4 *const C = reinterpret_cast<const float4 *>(x.carry + ((size_t)b * a.c.Hkv + h) * D * D);
+#pragma unroll 4
+        for (int e = tid; e < D * D / 4; e += kThr) {
+            const int r = e / (D / 4), q = e % (D / 4) * 4;
+            const float4 c = C[e];
+            uint2 hi, lo;
+            split2(c.x, c.y, hi.x, lo.x);
+            split2(c.z, c.w, hi.y, lo.y);
+            *reinterpret_cast<uint2 *>(Ch + r * LDD + q) = hi;
+            *reinterpret_cast<uint2 *>(Cl + r * LDD + q) = lo;
         }
-        s = seq_of(a, b);
     }
     grid_wait();
-    if (r >= z.R || tok < s.first || tok >= s.first + s.T || x.start[b] < 0) return;
-    const int p = __ldg(x.of + b);
-    const Seq g = seq_of(v, p);
-    const int row = (x.start[b] - g.first + tok - s.first) * G + (int)(r - (long long)tok * G);
-    const RowParts parts = parts_of(v, z, g, p, h, row, D);
-    float M = -INFINITY, L = 0.f, O[E];
+    if (!behind || x.start[b] < 0) return;
+    const size_t from = (size_t)h * y.R + (size_t)s.first * G, to = (size_t)h * y.R + (size_t)x.start[b] * G;
+    const int rows_all = s.T * G, m0 = 16 * (warp & 3), n0 = D / 2 * (warp >> 2);
+    uint4 xh[IT], xl[IT];
+    auto fetch = [&](int row0) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) O[e] = 0.f;
-    for (int q0 = 0; q0 < parts.number; q0 += P) {
-        float2 ml[P];
-        float w[P][E], m = M;
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-            ml[j] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-            for (int e = 0; e < E; ++e) w[j][e] = 0.f;
-            if (q0 + j < parts.number) {
-                const size_t at = parts.at(q0 + j);
-                ml[j] = parts.sml[at];
-#pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float2 t = *reinterpret_cast<const float2 *>(parts.so + at * D + lane * E + e);
-                    w[j][e] = t.x;
-                    w[j][e + 1] = t.y;
-                }
-            }
-            m = fmaxf(m, ml[j].x);
+        for (int i = 0; i < IT; ++i) {
+            const int e = tid + i * kThr, r = row0 + e / PER;
+            const size_t at = (from + r) * D + e % PER * 8;
+            xh[i] = r < rows_all ? *reinterpret_cast<const uint4 *>(y.qt + at) : make_uint4(0u, 0u, 0u, 0u);
+            xl[i] = r < rows_all ? *reinterpret_cast<const uint4 *>(y.ql + at) : make_uint4(0u, 0u, 0u, 0u);
         }
-        const float use = m == -INFINITY ? 0.f : m, f0 = exp2f(M - use);
-        M = m;
-        L *= f0;
+    };
+    const int first = kC * kTiles * part, last = min(rows_all, first + kC * kTiles);
+    fetch(first);
+    for (int row0 = first; row0 < last; row0 += kC) {
+        __syncthreads();
 #pragma unroll
-        for (int e = 0; e < E; ++e) O[e] *= f0;
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-            const float f = exp2f(ml[j].x - use);  // absent keys alone: 0, and their row 0
-            L = fmaf(ml[j].y, f, L);
-#pragma unroll
-            for (int e = 0; e < E; ++e) O[e] = fmaf(w[j][e], f, O[e]);
+        for (int i = 0; i < IT; ++i) {
+            const int e = tid + i * kThr, at = e / PER * LDD + e % PER * 8;
+            *reinterpret_cast<uint4 *>(Xh + at) = xh[i];
+            *reinterpret_cast<uint4 *>(Xl + at) = xl[i];
         }
+        if (row0 + kC < last) fetch(row0 + kC);
+        __syncthreads();
+        float acc[NT][4];
+        zero_acc(acc);
+        warp_mma_3<NT, false>(acc, Xh, Xl, LDD, m0, Ch, Cl, LDD, n0, D / 16);
+        each_eight(
+            acc, m0, n0, [](int, int, float &, float &) {},
+            [&](int i, int j, uint4 hi, uint4 lo) {
+                if (row0 + i >= rows_all) return;
+                *reinterpret_cast<uint4 *>(z.qt + (to + row0 + i) * D + j) = hi;
+                *reinterpret_cast<uint4 *>(z.ql + (to + row0 + i) * D + j) = lo;
+            });
+        if (a.log_f != nullptr && tid < kC && row0 + tid < rows_all)
+            z.gq[to + row0 + tid] = y.gq[from + row0 + tid] + x.gates[(size_t)b * a.c.Hq + h * G + (row0 + tid) % G];
     }
-    const size_t at = (size_t)h * z.R + r;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<float2 *>(x.px + at * D + lane * E + e) = make_float2(O[e], O[e + 1]);
-    if (lane == 0) x.pxml[at] = make_float2(M, L);
 }
 
 template <int D, bool FOX>
 cudaError_t launch_all(const Step &a, const Prefix &x, const TcWs &y, const TcWs &z, bool first, uint64_t limit_ns,
                        cudaStream_t stream) {
     const Step v = shared_step(a, x);
-    cudaError_t e = launch(prefix_plan_kernel<D>, dim3(1), kThr, 0, stream, first, a, v, x, z);
-    if (e == cudaSuccess) e = big_smem(prefix_query_kernel<D>, QuerySmem<D>::bytes);
-    if (e == cudaSuccess)
-        e = launch(prefix_query_kernel<D>, dim3(tile_slots(a.N, a.c.G, a.c.seqs, kC), a.c.Hkv), kThr,
-                   QuerySmem<D>::bytes, stream, false, a, x, y, z);
+    const int items = a.c.seqs * a.c.Hkv;
+    cudaError_t e;
+    if (a.c.seqs <= kFused) {
+        e = launch(prefix_single_kernel<D, true>, dim3(1 + items), kThr, 0, stream, first, a, v, x, z, true);
+    } else {
+        e = launch(prefix_single_kernel<D, false>, dim3(1), kThr, 0, stream, first, a, v, x, z, true);
+        if (e == cudaSuccess)
+            e = launch(prefix_single_kernel<D, false>, dim3(items), kThr, 0, stream, false, a, v, x, z, false);
+    }
+    if (a.max_chunk > 1) {
+        if (e == cudaSuccess) e = big_smem(prefix_query_kernel<D>, QuerySmem<D>::bytes);
+        if (e == cudaSuccess)
+            e = launch(prefix_query_kernel<D>, dim3(tile_slots(a.N, a.c.G, a.c.seqs, kC * kTiles), a.c.Hkv), kThr,
+                       QuerySmem<D>::bytes, stream, false, a, x, y, z);
+    }
     if (e == cudaSuccess) e = launch_cached<1, D, FOX, Pass::shared>(v, z, limit_ns, stream);
     if (e == cudaSuccess && (long long)a.N * a.c.G > 128) e = launch_cached<2, D, FOX, Pass::shared>(v, z, limit_ns, stream);
-    if (e == cudaSuccess)
-        e = launch(prefix_join_kernel<D>, dim3((unsigned)((z.R + kThr / 32 - 1) / (kThr / 32)), a.c.Hkv), kThr, 0,
-                   stream, false, a, v, x, z);
     if (e == cudaSuccess) e = launch_prefix_carry<bf, D>(a, x, stream);
     return e;
 }
@@ -194,8 +167,6 @@ size_t layout(const Step &a, int d, char *w, Prefix *x, TcWs *z) {
     };
     x->cu = reinterpret_cast<int *>(take(((size_t)c.seqs + 1) * 4));
     x->start = reinterpret_cast<int *>(take((size_t)c.seqs * 4));
-    x->px = reinterpret_cast<float *>(take(rows * d * 4));
-    x->pxml = reinterpret_cast<float2 *>(take(rows * 8));
     z->qt = reinterpret_cast<bf *>(take(rows * d * 2));
     z->ql = reinterpret_cast<bf *>(take(rows * d * 2));
     z->gq = reinterpret_cast<float *>(take(rows * 4));
@@ -222,16 +193,16 @@ size_t prefix_tc_bytes(const Step &a, int d) {
     return layout(a, d, nullptr, &x, &z);
 }
 
-cudaError_t launch_prefix_tc(Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
-                             uint64_t limit_ns, cudaStream_t stream) {
-    Prefix x;
+// behind: what the step's joining takes up
+cudaError_t launch_prefix_tc(const Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
+                             uint64_t limit_ns, Behind *behind, cudaStream_t stream) {
+    Prefix x = {};
     TcWs z = {};
     layout(a, d, static_cast<char *>(ws), &x, &z);
     x.of = a.prefix_of;
     x.carry = carry;
     x.gates = gates;
-    a.px = x.px;
-    a.pxml = x.pxml;
+    *behind = Behind{x.of, x.cu, x.start, {z.so[0], z.so[1]}, {z.sml[0], z.sml[1]}, {z.plan[0], z.plan[1]}};
     TcWs from = y != nullptr ? *y : z;  // (single tokens alone: their queries are formed from the inputs)
     from.R = z.R;
     const bool fox = a.log_f != nullptr;

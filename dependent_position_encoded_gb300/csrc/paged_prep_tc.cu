@@ -921,11 +921,15 @@ __global__ void __launch_bounds__(kThr) tc_gates_kernel(const Step a, const TcWs
 // the parts' rows: two or four rows joined together, sixteen a warp, or own parts loaded before
 // the look-up took longer. 19 us for 79,000 rows without parts at D = 64 (1.6 TB/s, most of it
 // from L2), 7 us for 512 rows of ten parts or so.
-template <int D, int P>
-__global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const TcWs y, int rows) {
+// BEHIND: sequences with prefixes, whose parts are joined too. W: the warps of a row, each with its share
+// of the prefix's parts, of which few rows may have many.
+template <int D, int P, bool BEHIND, int W>
+__global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const TcWs y, const Behind x, int rows) {
     constexpr int E = D / 32;
-    const int G = a.c.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y;
-    const int r0 = (blockIdx.x * (kThr / 32) + warp) * rows, r1 = min(r0 + rows, (int)y.R);  // R <= INT_MAX / 2
+    const int G = a.c.G, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.y, sub = warp % W;
+    const int r0 = (blockIdx.x * (kThr / 32 / W) + warp / W) * rows, r1 = min(r0 + rows, (int)y.R);  // R <= INT_MAX / 2
+    __shared__ float so_all[W > 1 ? kThr / 32 : 1][D];
+    __shared__ float2 ml_all[kThr / 32];
     grid_begin();
     // the last sequence that begins at or before a token
     int lo = 0;
@@ -951,6 +955,41 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
             v[1] = t.y;
             v[E - 2] = t.z;
             v[E - 1] = t.w;
+        }
+    };
+    float M, L, O[E];
+    // the parts from..number in steps of `step`, P at a time; at(q): where part q is
+    auto join = [&](int from, int number, int step, const float *so, const float2 *sml, auto at) {
+        for (int p0 = from; p0 < number; p0 += P * step) {
+            float2 ml[P];
+            float v[P][E];
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const int q = p0 + j * step;
+                ml[j] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[j][e] = 0.f;
+                if (q < number) {
+                    const size_t i = at(q);
+                    ml[j] = sml[i];
+                    load(so + i * D, v[j]);
+                }
+            }
+            float m = M;
+#pragma unroll
+            for (int j = 0; j < P; ++j) m = fmaxf(m, ml[j].x);
+            const float use = W > 1 && m == -INFINITY ? 0.f : m, f0 = exp2f(M - use);
+            M = m;
+            L *= f0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) O[e] *= f0;
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const float f = exp2f(ml[j].x - use);  // absent keys alone: 0, and their row 0
+                L = fmaf(ml[j].y, f, L);
+#pragma unroll
+                for (int e = 0; e < E; ++e) O[e] = fmaf(v[j][e], f, O[e]);
+            }
         }
     };
     // of the row looked up last: rows below `known` are of the same tile
@@ -986,50 +1025,36 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const Step a, const Tc
         }
         const size_t row = (size_t)h * y.R + r;
         const long long at0 = first * tile + (r - start) % tile;
-        const float *const so = tile == 128 ? y.so[0] : y.so[1];
-        const float2 *const sml = tile == 128 ? y.sml[0] : y.sml[1];
-        const float2 z = y.pml[row];
-        float M = z.x, L = z.y, O[E];  // M is never -inf: a row has its own key
-        load(y.po + row * D, O);
-        if (a.px != nullptr && __ldg(a.prefix_of + lo) >= 0) {  // the keys of the sequence's prefix
-            const float2 ml = a.pxml[row];
-            float v[E];
-            load(a.px + row * D, v);
-            const float top = fmaxf(M, ml.x), f0 = exp2f(M - top), f1 = exp2f(ml.x - top);
-            M = top;
-            L = fmaf(ml.y, f1, L * f0);
+        M = -INFINITY;
+        L = 0.f;
+        if (sub == 0) {
+            const float2 z = y.pml[row];
+            M = z.x, L = z.y;  // M is never -inf: a row has its own key
+            load(y.po + row * D, O);
+            join(0, number, 1, tile == 128 ? y.so[0] : y.so[1], tile == 128 ? y.sml[0] : y.sml[1], [&](int q) {
+                return at0 + (size_t)(q >> cp) * tile + (q & ((1 << cp) - 1)) * (128 >> cp);
+            });
+        } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e) O[e] = fmaf(v[e], f1, O[e] * f0);
+            for (int e = 0; e < E; ++e) O[e] = 0.f;
         }
-        for (int p0 = 0; p0 < number; p0 += P) {
-            float2 ml[P];
-            float v[P][E];
+        if (BEHIND && __ldg(x.of + lo) >= 0) {
+            const RowParts behind = parts_behind(a, x, lo, h, tok - s.first, r - tok * G);
+            join(sub, behind.number, W, behind.so, behind.sml, [&](int q) { return behind.at(q); });
+        }
+        if (W > 1) {  // one row a warp: every warp of the CTA comes by
 #pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const int q = p0 + j;
-                ml[j] = make_float2(-INFINITY, 0.f);
+            for (int e = 0; e < E; ++e) so_all[warp][lane * E + e] = O[e];
+            if (lane == 0) ml_all[warp] = make_float2(M, L);
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / W), "r"(32 * W) : "memory");
+            if (sub != 0) return;
+            for (int w = 1; w < W; ++w) {
+                const float2 ml = ml_all[warp + w];
+                const float m = fmaxf(M, ml.x), f0 = exp2f(M - m), f1 = exp2f(ml.x - m);
+                M = m;
+                L = fmaf(ml.y, f1, L * f0);
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[j][e] = 0.f;
-                if (q < number) {
-                    const size_t at = at0 + (size_t)(q >> cp) * tile + (q & ((1 << cp) - 1)) * (128 >> cp);
-                    ml[j] = sml[at];
-                    load(so + at * D, v[j]);
-                }
-            }
-            float m = M;
-#pragma unroll
-            for (int j = 0; j < P; ++j) m = fmaxf(m, ml[j].x);
-            const float f0 = exp2f(M - m);
-            M = m;
-            L *= f0;
-#pragma unroll
-            for (int e = 0; e < E; ++e) O[e] *= f0;
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const float f = exp2f(ml[j].x - m);  // absent keys alone: 0, and their row 0
-                L = fmaf(ml[j].y, f, L);
-#pragma unroll
-                for (int e = 0; e < E; ++e) O[e] = fmaf(v[j][e], f, O[e]);
+                for (int e = 0; e < E; ++e) O[e] = fmaf(so_all[warp + w][lane * E + e], f1, O[e] * f0);
             }
         }
         bf *dst = static_cast<bf *>(a.out) + (long long)tok * a.so.tok + hq * a.so.head + lane * E;
@@ -1077,14 +1102,17 @@ cudaError_t launch_tc_carry(const Step &a, const TcWs &y, cudaStream_t stream) {
 // The rest of a step after its attention: outputs, the cached keys of sequences of more than one
 // tile, the gate sums.
 template <int D>
-cudaError_t launch_tc_finish(const Step &a, const TcWs &y, cudaStream_t stream) {
+cudaError_t launch_tc_finish(const Step &a, const TcWs &y, const Behind &x, cudaStream_t stream) {
     const long long cap = most_seen(a);
     // few rows: a warp for each, its parts eight at a time; many (whose sequences have few parts):
     // four a warp
-    const bool few = y.R * a.c.Hkv < 8 * 152 * 24;
-    const int rows = few ? 1 : 4, per = kThr / 32 * rows;
-    cudaError_t e = launch(few ? tc_combine_kernel<D, 8> : tc_combine_kernel<D, 2>,
-                           dim3((unsigned)((y.R + per - 1) / per), a.c.Hkv), kThr, 0, stream, false, a, y, rows);
+    const bool few = y.R * a.c.Hkv < 8 * 152 * 24, behind = x.of != nullptr;
+    const bool fewer = behind && y.R * a.c.Hkv * 4 <= 152 * 16;
+    const int rows = few ? 1 : 4, per = kThr / 32 / (fewer ? 4 : 1) * rows;
+    auto kern = fewer ? tc_combine_kernel<D, 8, true, 4>
+                : few ? (behind ? tc_combine_kernel<D, 8, true, 1> : tc_combine_kernel<D, 8, false, 1>)
+                      : (behind ? tc_combine_kernel<D, 2, true, 1> : tc_combine_kernel<D, 2, false, 1>);
+    cudaError_t e = launch(kern, dim3((unsigned)((y.R + per - 1) / per), a.c.Hkv), kThr, 0, stream, false, a, y, x, rows);
     if (e != cudaSuccess || cap == 0) return e;  // no sequence has room for a token
     if (!one_tile(a.max_chunk, a.c.G, D, a.log_f != nullptr)) {
         const size_t bytes = TransformSmem<D>::bytes;
@@ -1096,9 +1124,14 @@ cudaError_t launch_tc_finish(const Step &a, const TcWs &y, cudaStream_t stream) 
         e = launch(tc_transform_kernel<D>, dim3((unsigned)parts, a.c.Hkv, a.c.seqs), kThr, bytes, stream, false, a, y);
         if (e != cudaSuccess) return e;
     }
-    if (a.log_f != nullptr)
-        e = launch(tc_gates_kernel, dim3((unsigned)((cap + 4 * kThr - 1) / (4 * kThr)), a.c.Hq, a.c.seqs), kThr, 0,
-                   stream, false, a, y);
+    if (a.log_f != nullptr) {
+        // CTAs of 4 kThr positions, or of several times that where tables are wide and many: most of
+        // these CTAs would find nothing (68 sequences of 200 positions in tables of 17,000, 32 heads: 41 ->
+        // GATES us)
+        const long long parts = (cap + 4 * kThr - 1) / (4 * kThr), room = 8192 / ((long long)a.c.Hq * a.c.seqs) + 1;
+        e = launch(tc_gates_kernel, dim3((unsigned)(parts < room ? parts : room), a.c.Hq, a.c.seqs), kThr, 0, stream,
+                   false, a, y);
+    }
     return e;
 }
 
@@ -1106,8 +1139,8 @@ template cudaError_t launch_tc_prep<64>(const Step &, const TcWs &, cudaStream_t
 template cudaError_t launch_tc_prep<128>(const Step &, const TcWs &, cudaStream_t);
 template cudaError_t launch_tc_carry<64>(const Step &, const TcWs &, cudaStream_t);
 template cudaError_t launch_tc_carry<128>(const Step &, const TcWs &, cudaStream_t);
-template cudaError_t launch_tc_finish<64>(const Step &, const TcWs &, cudaStream_t);
-template cudaError_t launch_tc_finish<128>(const Step &, const TcWs &, cudaStream_t);
+template cudaError_t launch_tc_finish<64>(const Step &, const TcWs &, const Behind &, cudaStream_t);
+template cudaError_t launch_tc_finish<128>(const Step &, const TcWs &, const Behind &, cudaStream_t);
 
 }  // namespace paged
 }  // namespace path

@@ -191,6 +191,15 @@ __device__ __forceinline__ void make_plans(const Step &a, const TcWs &y, long lo
     }
 }
 
+// The parts of the prefixes' pass (paged_prefix.cuh), for the step's joining; of: null where the step has
+// none.
+struct Behind {
+    const int *of, *cu, *start;
+    float *so[2];
+    float2 *sml[2];
+    Plan plan[2];
+};
+
 // The parts of a row, row `r` of sequence b's and key head h's, that the pass over cached keys left: number
 // of the first, how many, and where they begin (part q at `first` + (q >> copies) * tile + (q & ..) * (128 >> copies)).
 struct RowParts {
@@ -202,23 +211,28 @@ struct RowParts {
         return first + (size_t)(q >> copies) * tile + (q & ((1 << copies) - 1)) * (128 >> copies);
     }
 };
-__device__ __forceinline__ RowParts parts_of(const Step &a, const TcWs &y, const Seq &s, int b, int h, int r, int D) {
-    int NT = 1, tiles, kt;
-    plan_of(a, s, D, 1, tiles, kt);
-    if (tiles == 0) {
-        NT = 2;
-        plan_of(a, s, D, 2, tiles, kt);
-    }
-    const Plan &p = NT == 1 ? y.plan[0] : y.plan[1];
-    const int rows_all = s.T * a.c.G, ti = r / (128 * NT), it = h * tiles + ti;
-    RowParts x{0, 0, NT == 2 ? 0 : rows_all <= 32 ? 2 : rows_all <= 64 ? 1 : 0, 128 * NT,
-               NT == 1 ? y.so[0] : y.so[1], NT == 1 ? y.sml[0] : y.sml[1]};
+// rows: those of the sequence and key head; kt: its key tiles; one: whether it goes with NT = 1.
+template <typename Y>
+__device__ __forceinline__ RowParts parts_of(const Y &y, int seqs, int rows, int kt, bool one, int b, int h, int r) {
+    const Plan &p = one ? y.plan[0] : y.plan[1];
+    const int tile = one ? 128 : 256, tiles = (rows + tile - 1) / tile, it = h * tiles + r / tile;
+    RowParts x{0, 0, !one ? 0 : rows <= 32 ? 2 : rows <= 64 ? 1 : 0, tile, one ? y.so[0] : y.so[1],
+               one ? y.sml[0] : y.sml[1]};
+    // (none where the sequence has no work)
     if (kt > 0 && p.items[b + 1] > p.items[b]) {
-        const long long per = plan_per(p, a.c.seqs), u = p.units[b] + (long long)it * kt, c0 = u / per;
-        x.first = (c0 + p.items[b] + it) * x.tile + r % x.tile;
+        const long long per = plan_per(p, seqs), u = p.units[b] + (long long)it * kt, c0 = u / per;
+        x.first = (c0 + p.items[b] + it) * tile + r % tile;
         x.number = ((int)((u + kt - 1) / per - c0) + 1) << x.copies;
     }
     return x;
+}
+// The parts of sequence b's row of new token t and query head g of key head h with its prefix.
+__device__ __forceinline__ RowParts parts_behind(const Step &a, const Behind &x, int b, int h, int t, int g) {
+    const int start = x.start[b];
+    if (start < 0) return RowParts{};
+    const int p = __ldg(x.of + b), first = x.cu[p], rows = (x.cu[p + 1] - first) * a.c.G;
+    return parts_of(x, a.c.seqs, rows, (__ldg(a.c.lens + p) + 127) / 128, rows <= 128, p, h,
+                    (start - first + t) * a.c.G + g);
 }
 
 // Rows of `rows` per tile over all sequences: tile i of sequence b is slot
