@@ -450,6 +450,8 @@ template <int D>
 cudaError_t launch_tc_finish(const Step &a, const TcWs &y, const Behind &x, cudaStream_t stream);
 cudaError_t launch_prefix_tc(const Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
                              uint64_t limit_ns, Behind *behind, cudaStream_t stream);
+cudaError_t launch_singles(const Step &a, int d, const TcWs &y, float *carry, float *gates, void *ws, uint64_t limit_ns,
+                           Behind *behind, cudaStream_t stream);
 
 namespace {
 
@@ -457,12 +459,20 @@ namespace {
 template <int D, bool FOX>
 cudaError_t launch_all(const Step &a, const TcWs &y, float *carry, float *gates, void *pws, uint64_t limit_ns,
                        cudaStream_t stream) {
-    cudaError_t e = launch_tc_prep<D>(a, y, stream);
+    Behind behind = {};
+    cudaError_t e;
+    // single tokens, unless more query heads share a key head than a tile has rows
+    if (a.max_chunk == 1 && a.c.G <= 128 && (a.window > 0 || carry != nullptr)) {
+        TcWs one = y;
+        one.plan[0].ctas = 152 * CachedCfg<1, D, Pass::one>::ctas_per_sm;
+        e = launch_singles(a, D, one, carry, gates, pws, limit_ns, &behind, stream);
+        return e != cudaSuccess ? e : launch_tc_finish<D>(a, one, behind, stream);
+    }
+    e = launch_tc_prep<D>(a, y, stream);
     if (a.max_chunk > kC) {
         if (e == cudaSuccess) e = launch_tc_carry<D>(a, y, stream);
         if (e == cudaSuccess) e = launch_scan<D, FOX>(a, y, limit_ns, stream);
     }
-    Behind behind = {};
     if (e == cudaSuccess && carry != nullptr)
         e = launch_prefix_tc(a, D, carry, gates, &y, pws, false, limit_ns, &behind, stream);
     if (a.c.max_pages > 0) {

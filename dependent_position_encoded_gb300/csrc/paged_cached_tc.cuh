@@ -87,6 +87,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr));
 }
 
+// one column of the thread's row
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float x) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
+    tmem_st_wait();
+}
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+    uint32_t x;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(taddr));
+    tmem_ld_wait();
+    return __uint_as_float(x);
+}
+
 // multiplies N fp32 columns of the thread's row by f (16 at a time: the row's logits are in
 // registers beside it)
 template <int N>
@@ -154,40 +166,53 @@ struct CachedCfg {
     static constexpr uint32_t tile = 128 * D * 2, atom = 128 * 128;
     // The rows' tiles, their high parts and then (keeps_low) their low ones; for NT = 1 at D = 128,
     // where the update's product takes 64 KB, they lie in tensor memory instead.
-    static constexpr bool update = NT == 1 && M != Pass::shared;  // of the keys, in this pass
-    static constexpr bool rows_in_tmem = update && D == 128, low = keeps_low(NT, D);
+    // the keys' update in this pass: by a product with P - I, or (single tokens) on the CUDA cores
+    static constexpr bool update = NT == 1 && M != Pass::shared, single = NT == 1 && M == Pass::one,
+                          matrix = update && !single;
+    // two warpgroups for the softmax of one row tile
+    static constexpr bool duo = NT == 1 && M == Pass::shared;
+    // the next stretch is looked up, and its rows fetched, before the last one's end
+    static constexpr bool ahead = single || duo;
+    static constexpr bool rows_in_tmem = single || (update && D == 128), low = keeps_low(NT, D);
     static constexpr uint32_t X = 0, xbytes = rows_in_tmem ? 0 : NT * (low ? 2 : 1) * tile;
-    static constexpr uint32_t P = X + xbytes, pbytes = update ? 2 * D * D * 2 : 0;
+    static constexpr uint32_t P = X + xbytes, pbytes = matrix ? 2 * D * D * 2 : 0;
     // slots of keys and of values: what fits beside; for NT = 1 and D = 64 so that two CTAs share
     // an SM. With NT = 1 a key slot is held until the updated keys have left it.
-    static constexpr int NK = update ? (D == 64 ? 2 : 3) : NT == 1 ? 3 : (D == 64 ? 4 : 3);
-    static constexpr int NV = NT == 1 ? 2 : (D == 64 ? 4 : 2);
+    static constexpr int NK = matrix ? (D == 64 ? 2 : 3)
+                              : single ? (D == 64 ? 8 : 4)
+                              : NT == 1 ? (D == 64 ? 6 : 3)
+                                        : (D == 64 ? 4 : 3);
+    static constexpr int NV = matrix ? 2 : single ? (D == 64 ? 5 : 3) : NT == 1 ? (D == 64 ? 6 : 2) : (D == 64 ? 4 : 2);
     static constexpr uint32_t K = P + pbytes, V = K + NK * tile, bars = V + NV * tile;
     static constexpr int KF = 0, KE = NK, VF = 2 * NK, VE = VF + NV, XF = VE + NV, XE = XF + 1, SF = XE + 1,
                          PR = SF + 2, FIN = PR + 2, DF = FIN + 2, DE = DF + NK, TMP = DE + 1, END = TMP + 2,
-                         XT = END + 2, count = XT + 1;
-    static constexpr uint32_t bytes = bars + count * 8 + 16;  // from a 1024-byte boundary
+                         XT = END + 2, EX = XT + 1, count = EX + 1;
+    // behind the barriers: TMEM's address and the abort flag; single: the token's w, two of them
+    static constexpr uint32_t W = (bars + count * 8 + 16 + 15) / 16 * 16;  // read 16 bytes at a time
+    static constexpr uint32_t bytes = W + (single ? 2 * D * 4 : 0);  // from a 1024-byte boundary
     static constexpr int threads = 384;
-    static constexpr int ctas_per_sm = NT == 1 && D == 64 ? 2 : 1;
+    static constexpr int ctas_per_sm = matrix && D == 64 ? 2 : 1;
     // registers after the split of what the CTA is launched with (NT = 2: 168 for each thread; NT = 1
     // with two CTAs per SM: 80): the softmax's warpgroups, the update's and the last one
-    static constexpr bool split = NT == 2 || D == 64;
+    static constexpr bool split = NT == 2 || (matrix && D == 64);
     static constexpr int reg_row = NT == 2 ? 200 : 104, reg_update = 72, reg_other = NT == 2 ? 104 : 64;
-    // TMEM columns: per row tile S 128 (the weights over it) and O; NT = 1: the update's product
-    static constexpr uint32_t cS = 0, cO = 128, per_tile = 256, cD = 128 + D, cX = 384;
-    static constexpr uint32_t cols = NT == 1 && D == 64 ? 256 : 512;
+    // TMEM columns: per row tile S 128 (the weights over it) and O; NT = 1: the update's product, or the
+    // rows' two parts, or (duo) what the halves of a row tell each other
+    static constexpr uint32_t cS = 0, cO = 128, per_tile = 256, cD = 128 + D, cX = D == 64 ? 192 : 384;
+    static constexpr uint32_t cols = matrix && D == 64 ? 256 : 512;
 };
 template <Pass M>
 struct CachedFits {
     using A = CachedCfg<1, 64, M>;
     using B = CachedCfg<2, 64, M>;
     static_assert(CachedCfg<1, 128, M>::bytes <= 227 * 1024 && CachedCfg<2, 128, M>::bytes <= 227 * 1024 &&
-                      2 * (A::bytes + 1024) <= 228 * 1024,
+                      A::bytes <= 227 * 1024 && A::ctas_per_sm * (A::bytes + 1024) <= 228 * 1024,
                   "shared memory");
     static_assert(256 * B::reg_row + 128 * B::reg_other <= 384 * 168, "registers");
     static_assert(128 * (A::reg_row + A::reg_update + A::reg_other) <= 384 * 80, "registers");
 };
 template struct CachedFits<Pass::step>;
+template struct CachedFits<Pass::one>;
 template struct CachedFits<Pass::shared>;
 
 template <int N>
@@ -236,7 +261,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                  const __grid_constant__ CUtensorMap tm_l, const __grid_constant__ CUtensorMap tm_m,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
     using L = CachedCfg<NT, D, M>;
-    constexpr bool WIN = M == Pass::window;
+    constexpr bool WIN = M == Pass::window || M == Pass::one;
     constexpr int NA = D / 64, NK = L::NK, NV = L::NV, kLow = low_weights(NT, D, FOX);
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t base = smem_u32(sm);
@@ -259,13 +284,13 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
 
     if (tid == 0) {
         *abort_f = 0u;
-        // four warps: weights written, update's product read; both issuing threads (NT = 1): rows' tile
-        // free, keys read by their products; both row tiles (NT = 2): keys and values read
+        // four warps (duo: eight): weights written, update's product read; both issuing threads (NT = 1):
+        // rows' tile free, keys read by their products; both row tiles (NT = 2): keys and values read
         for (int i = 0; i < L::count; ++i) {
-            const bool four = (i >= L::PR && i < L::FIN) || i == L::DE || i == L::XT;
-            const bool both = NT == 1 ? L::update && ((i == L::XE && !L::rows_in_tmem) || (i >= L::DF && i < L::DE))
+            const bool four = (i >= L::PR && i < L::FIN) || i == L::DE || i == L::XT || i == L::EX;
+            const bool both = NT == 1 ? L::matrix && ((i == L::XE && !L::rows_in_tmem) || (i >= L::DF && i < L::DE))
                                       : (i >= L::KE && i < L::VF) || (i >= L::VE && i < L::XF);
-            mbar_init(bar(i), four ? 4u : both ? 2u : 1u);
+            mbar_init(bar(i), four ? (L::duo ? 8u : 4u) : both ? 2u : 1u);
         }
         fence_mbar_init();
     }
@@ -285,6 +310,9 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
     // log2 of the copies of the rows
     auto copies = [&](const Stretch &t) { return NT == 2 ? 0 : t.s.T * G <= 32 ? 2 : t.s.T * G <= 64 ? 1 : 0; };
     const int page = a.c.page, box_shift = min(a.c.page_shift, 7), box = 1 << box_shift, nbox = 128 >> box_shift;
+    auto stretch_of = [&](Walk &walk, long long at) {
+        return L::ahead ? walk.at(a, plan, D, NT, at, u_end) : Walk().at(a, plan, D, NT, at, u_end);
+    };
     // what the first new token sees, the first position of a stretch's step i, and whether the page of
     // the lane's box at j is wanted
     auto sight = [&](const Stretch &t) { return WIN ? sight_of(a, t.s) : Sight{0, 0}; };
@@ -306,10 +334,11 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             const uint32_t ring = keys ? NK : NV, full0 = keys ? L::KF : L::VF, empty0 = keys ? L::KE : L::VE;
             uint32_t j = 0, seg = 0, tmp_phase = 0;
             bool ok = true;
+            Walk walk;
             for (long long at = u_begin; ok && at < u_end; ++seg) {
-                const Stretch t = stretch_at(a, plan, D, NT, at, u_end);
+                const Stretch t = stretch_of(walk, at);
                 at += t.steps;
-                if (keys) {
+                if (keys && !L::single) {
                     // the rows' tile (and the update's product) once the last stretch's are read
                     if (seg > 0 && !(ok = wait.warp(bar(L::XE), (seg - 1) & 1))) break;
                     if (lane == 0) {
@@ -324,7 +353,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                                     tma_load_3d(base + L::X + (part * NT + (i >> 2)) * L::tile + x * L::atom +
                                                     (i & 3) * 32 * 128,
                                                 part ? &tm_l : &tm_x, bar(L::XF), 64 * x, xr + ((32 * i) & mask), t.h);
-                        if (L::update)
+                        if (L::matrix)
                             for (int p = 0; p < 2; ++p)
                                 for (int x = 0; x < NA; ++x)
                                     tma_load_3d(base + L::P + (uint32_t)(p * NA + x) * D * 128, &tm_m, bar(L::XF),
@@ -387,7 +416,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             if (!ok) {
                 for (uint32_t v = j > ring ? j - ring : 0; v < j; ++v)
                     mbar_wait(bar(full0 + v % ring), (v / ring) & 1, limit_ns);
-                if (keys) mbar_wait(bar(L::XF), seg & 1, limit_ns);
+                if (keys && !L::single) mbar_wait(bar(L::XF), seg & 1, limit_ns);
             }
         } else if (lane == 0 && warp == 8) {
             // ======================================================== S and P V
@@ -436,8 +465,9 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 if (last && !L::rows_in_tmem) umma_commit(bar(L::XE));
                 k.next();
             };
+            Walk walk;
             for (long long at = u_begin; ok && at < u_end; ++seg) {
-                const Stretch t = stretch_at(a, plan, D, NT, at, u_end);
+                const Stretch t = stretch_of(walk, at);
                 at += t.steps;
                 const bool two = second(t);
                 if (!(ok = wait(bar(L::rows_in_tmem ? L::XT : L::XF), seg & 1))) break;
@@ -475,7 +505,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             // every product has completed before TMEM is freed
             umma_commit(bar(L::END));
             mbar_wait(bar(L::END), 0, limit_ns);
-        } else if (L::update && lane == 0 && warp == 11) {
+        } else if (L::matrix && lane == 0 && warp == 11) {
             // ======================================================== K (P - I), NT = 1
             constexpr uint32_t ID_D = idesc_b16(128, D, true);
             constexpr uint64_t kAtom = L::atom >> 4, kTile = L::tile >> 4, kPart = (NA * D * 128) >> 4;
@@ -483,8 +513,9 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             Ring<NK> k;
             uint32_t j = 0, seg = 0;
             bool ok = true;
+            Walk walk;
             for (long long at = u_begin; ok && at < u_end; ++seg) {
-                const Stretch t = stretch_at(a, plan, D, NT, at, u_end);
+                const Stretch t = stretch_of(walk, at);
                 at += t.steps;
                 if (!(ok = wait(bar(L::XF), seg & 1))) break;
                 for (int i = 0; i < t.steps; ++i, ++j) {
@@ -506,16 +537,28 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             umma_commit(bar(L::END + 1));
             mbar_wait(bar(L::END + 1), 0, limit_ns);
         }
-    } else if (NT == 1 && warp >= 4) {
+    } else if (NT == 1 && !L::duo && warp >= 4) {
         // ============================================================ the keys' update
         if (L::split) reg_dec<L::reg_update>();
         const int r = tid - 128;
         const uint32_t tm = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + L::cD;
         bool ok = true;
-        uint32_t j = 0;
-        for (long long at = L::update ? u_begin : u_end; ok && at < u_end;) {
-            const Stretch t = stretch_at(a, plan, D, NT, at, u_end);
+        uint32_t j = 0, seg = 0;
+        Walk walk;
+        for (long long at = L::update ? u_begin : u_end; ok && at < u_end; ++seg) {
+            const Stretch t = stretch_of(walk, at);
             at += t.steps;
+            // single: the token's w and beta. (A stretch's first step has a barrier behind which nobody reads
+            // the w of the stretch before the last.)
+            float *const wv = reinterpret_cast<float *>(sm + L::W) + (seg & 1) * D;
+            float beta = 0.f;
+            if (L::single) {
+                if (r < D)
+                    wv[r] = __bfloat162float(
+                        static_cast<const bf *>(a.w)[(long long)t.s.first * a.sw.tok + t.h * a.sw.head + r]);
+                beta = a.beta[(long long)t.s.first * a.sb.tok + t.h * a.sb.head];
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
             const Sight seen = sight(t);
             int next;  // the key pages of the next tile's boxes
             auto look_up = [&](int pos0) {
@@ -530,17 +573,54 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
                 const bool whole = tile_whole(pos0, t.s.n, have, box_shift) && (!WIN || seen.all(pos0, 128));
                 const int mine = __shfl_sync(0xffffffffu, id, r >> box_shift);
+                uint8_t *const kt = sm + (key_slot(j) - base);
+                uint4 key[L::single ? D / 8 : 1];
+                float al = 0.f;  // -beta (w . k) of the thread's key
+                if (L::single) {
+                    if (!(ok = wait.warp(bar(L::KF + j % NK), (j / NK) & 1))) break;
+                    float2 dot[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        key[c] = *reinterpret_cast<const uint4 *>(kt + (c >> 3) * L::atom + sw128_offset(r, c & 7));
+                        const uint32_t k4[4] = {key[c].x, key[c].y, key[c].z, key[c].w};
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const float4 w4 = *reinterpret_cast<const float4 *>(wv + 8 * c + 2 * e);
+                            dot[0] = ffma2(unpack_bf16x2(k4[e]), make_float2(w4.x, w4.y), dot[0]);
+                            dot[1] = ffma2(unpack_bf16x2(k4[e + 1]), make_float2(w4.z, w4.w), dot[1]);
+                        }
+                    }
+                    al = -beta * ((dot[0].x + dot[0].y) + (dot[1].x + dot[1].y));
+                }
                 // the product is there, and the logits' product has read the keys too
                 if (!(ok = wait.warp(bar(L::DF + j % NK), (j / NK) & 1))) break;
                 tc_fence_after();
-                uint8_t *const kt = sm + (key_slot(j) - base);
                 bf *const dst = mine >= 0 && pos0 + r < t.s.n && (!WIN || seen.sees(pos0 + r))
                                     ? static_cast<bf *>(a.c.k_pages) +
                                           ((((size_t)mine * a.c.Hkv + t.h) << a.c.page_shift) +
                                            ((pos0 + r) & (page - 1))) * D
                                     : nullptr;
+                if (L::single) {
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint32_t k4[4] = {key[c].x, key[c].y, key[c].z, key[c].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const float4 w4 = *reinterpret_cast<const float4 *>(wv + 8 * c + 2 * e);
+                            const float2 lo = ffma2(make_float2(al, al), make_float2(w4.x, w4.y), unpack_bf16x2(k4[e]));
+                            const float2 hi =
+                                ffma2(make_float2(al, al), make_float2(w4.z, w4.w), unpack_bf16x2(k4[e + 1]));
+                            o[e] = pack_bf16x2(lo.x, lo.y);
+                            o[e + 1] = pack_bf16x2(hi.x, hi.y);
+                        }
+                        const uint4 v = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (whole) *reinterpret_cast<uint4 *>(kt + (c >> 3) * L::atom + sw128_offset(r, c & 7)) = v;
+                        else if (dst) *reinterpret_cast<uint4 *>(dst + 8 * c) = v;
+                    }
+                }
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = 0; c < (L::single ? 0 : D); c += 32) {
                     float x[32];
                     tld32(tm + c, x);
 #pragma unroll
@@ -561,7 +641,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                     }
                 }
                 tc_fence_before();
-                mbar_arrive_warp(bar(L::DE));
+                if (!L::single) mbar_arrive_warp(bar(L::DE));
                 fence_proxy_async_smem();
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 if (warp == 4) {
@@ -581,57 +661,83 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
     } else {
         // ============================================================ softmax
         if (L::split) reg_inc<L::reg_row>();
-        constexpr bool kTwice = NT == 1 || FOX;
-        const int w = warp >> 2, r = tid & 127;  // row tile and row in it
+        constexpr bool kTwice = (NT == 1 && !L::duo) || FOX;
+        // row tile and row in it; duo: which half of the columns that the row takes
+        const int w = NT == 1 ? 0 : warp >> 2, r = tid & 127, half = L::duo ? warp >> 2 : 0;
         const uint32_t tm = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + L::per_tile * w;
         bool ok = true;
         // One thread of a row tile hands slots back: the logits' product of step j has read its keys, and
         // it ends behind the values' product of step j - 1. (Keys that the pass updates: its warps do.)
-        const bool releases = (warp & 3) == 0 && lane == 0;
+        const bool releases = (warp & 3) == 0 && lane == 0 && half == 0;
         uint32_t j = 0, seg = 0, step = 0;  // steps and stretches with rows in this tile; steps of the CTA
+        Walk walk;
+        // duo: the other half's x of the row (a step later its column is written again at the earliest), or
+        // (of nothing) until it has read its logits
+        uint32_t turn = 0;
+        auto meet = [&]() {
+            tc_fence_before();
+            mbar_arrive_warp(bar(L::EX));
+            ok = wait.warp(bar(L::EX), turn++ & 1);
+            tc_fence_after();
+        };
+        auto exchange = [&](float x) {
+            const uint32_t at = tm + L::cX + 2 * (turn & 3);
+            tmem_st1(at + half, x);
+            meet();
+            return tmem_ld1(at + 1 - half);
+        };
+        // the row's two parts into tensor memory (the last products of the stretch before have ended)
+        auto load_rows = [&](const Stretch &t) {
+            const int row = 128 * NT * t.tile + (r & ((128 >> copies(t)) - 1));
+            const bool live = row < t.s.T * G;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int c = 0; c < D / 2; c += 32) {  // 32 columns of two elements
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        (part ? y.ql : y.qt) +
+                        ((size_t)t.h * y.R + (size_t)t.s.first * G + (live ? row : 0)) * D + 2 * c);
+                    uint32_t u[32];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint4 v = live ? src[q] : make_uint4(0u, 0u, 0u, 0u);
+                        u[4 * q] = v.x;
+                        u[4 * q + 1] = v.y;
+                        u[4 * q + 2] = v.z;
+                        u[4 * q + 3] = v.w;
+                    }
+                    tmem_st32(tm + L::cX + part * (D / 2) + c, u);
+                }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive_warp(bar(L::XT));
+        };
+        Stretch next;
+        if (L::ahead) next = stretch_of(walk, u_begin);
+        if (L::single) load_rows(next);
         for (long long at = u_begin; ok && at < u_end;) {
-            const Stretch t = stretch_at(a, plan, D, NT, at, u_end);
+            const Stretch t = L::ahead ? next : stretch_of(walk, at);
             at += t.steps;
             if (w == 1 && !second(t)) {
                 step += t.steps;
                 continue;
             }
             const bool alone = NT == 2 && !second(t);  // no other tile: its part of the releases too
-            // the row of this thread, and the columns of the key tiles that its copy takes
+            // the row of this thread, and the columns of the key tiles that its copy takes (duo: that
+            // this half of it takes, none of the second where a copy has 32)
             const int rows_all = t.s.T * G, cp = copies(t), rw = r & ((128 >> cp) - 1);
-            const int row0 = 128 * (NT * t.tile + w), cols = 128 >> cp, c_begin = (r >> (7 - cp)) * cols;
+            const int row0 = 128 * (NT * t.tile + w), c_copy = (r >> (7 - cp)) * (128 >> cp);
+            const bool halves = L::duo && cp < 2, idle = L::duo && cp == 2 && half == 1;
+            const int cols = 128 >> (cp + (halves ? 1 : 0)), c_begin = c_copy + (halves ? half * cols : 0);
             const bool live = row0 + rw < rows_all, warp_live = row0 + (rw & ~31) < rows_all;
             const int hq = t.h * G + (live ? (row0 + rw) % G : 0);
             const float gq =
                 FOX && live ? y.gq[(size_t)t.h * y.R + (size_t)t.s.first * G + row0 + rw] * kLog2e : 0.f;
-            if (L::rows_in_tmem) {
-                // the row's two parts (the last stretch's products have ended)
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int c = 0; c < D / 2; c += 32) {  // 32 columns of two elements
-                        const uint4 *src = reinterpret_cast<const uint4 *>(
-                            (part ? y.ql : y.qt) +
-                            ((size_t)t.h * y.R + (size_t)t.s.first * G + row0 + (live ? rw : 0)) * D + 2 * c);
-                        uint32_t u[32];
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const uint4 v = live ? src[q] : make_uint4(0u, 0u, 0u, 0u);
-                            u[4 * q] = v.x;
-                            u[4 * q + 1] = v.y;
-                            u[4 * q + 2] = v.z;
-                            u[4 * q + 3] = v.w;
-                        }
-                        tmem_st32(tm + L::cX + part * (D / 2) + c, u);
-                    }
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive_warp(bar(L::XT));
-            }
+            if (L::rows_in_tmem && !L::single) load_rows(t);
             // a window: the row sees the keys from `from` on (and the sinks); `edge`: where all rows' do
             const Sight seen = sight(t);
             const int from = WIN ? t.s.n + 1 - a.window + (live ? (row0 + rw) / G : 0) : 0;
-            const int edge = WIN ? t.s.n + t.s.T - a.window : 0;
+            const int edge = WIN && a.window > 0 ? t.s.n + t.s.T - a.window : 0;
             float m_run = -INFINITY, l_run = 0.f;
             int kid1, vid1;  // the pages of the next tile's boxes
             auto look_up = [&](int pos0) {
@@ -691,7 +797,8 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                     if (!L::update) release(L::KE, step % NK);
                     if (i > 0) release(L::VE, (step - 1) % NV);
                 }
-                if (warp_live) {
+                // (duo: every warp meets the other half's)
+                if (warp_live || halves) {
                     // gates and mask of 32 logits of the row from column c
                     auto gate = [&](int c, float *x) {
                         if (FOX) {
@@ -735,12 +842,16 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                     float use;
                     auto raise = [&]() {
                         float alpha = 1.f;
+                        const bool had = L::duo ? m_run > -INFINITY : l_run > 0.f;
                         if (top > m_run + kRescale || (m_run == -INFINITY && top > -INFINITY)) {
                             alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - top);
                             m_run = top;
                         }
-                        const bool resc = alpha != 1.f && l_run > 0.f;
-                        if (__any_sync(0xffffffffu, resc)) tmem_scale<D>(tm + L::cO, resc ? alpha : 1.f);
+                        const bool resc = alpha != 1.f && had;
+                        if (__any_sync(0xffffffffu, resc)) {
+                            if (halves) tmem_scale<D / 2>(tm + L::cO + half * (D / 2), resc ? alpha : 1.f);
+                            else tmem_scale<D>(tm + L::cO, resc ? alpha : 1.f);
+                        }
                         l_run *= alpha;
                         use = m_run == -INFINITY ? 0.f : -m_run;
                     };
@@ -756,7 +867,47 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                             else p[e / 2] = pack_bf16x2(q.x, q.y);
                         }
                     };
-                    if (kTwice) {
+                    if (L::duo) {
+                        // Both halves of a row have the same maximum. A half's weights take columns that may
+                        // hold logits of the other: none is written before both have been read.
+                        float x[32];
+                        top = -INFINITY;
+                        if (warp_live && !idle)
+#pragma unroll 1
+                            for (int c = c_begin; c < c_begin + cols; c += 32) {
+                                tld32(tm + L::cS + c, x);
+                                gate(c, x);
+                                top = fmaxf(top, max32(x));
+                            }
+                        if (halves) top = fmaxf(top, exchange(top));
+                        if (!ok) break;
+                        uint32_t p[16], p2[16];
+                        if (warp_live && !idle) {
+                            raise();
+                            if (cols > 32) {
+                                tld32(tm + L::cS + c_begin, x);
+                                gate(c_begin, x);
+                            }
+                            weigh(x, p, p, false);
+                            if (cols > 32) {
+                                tld32(tm + L::cS + c_begin + 32, x);
+                                gate(c_begin + 32, x);
+                                weigh(x, p2, p2, false);
+                            }
+                        }
+                        if (halves && cols > 32) meet();
+                        if (!ok) break;
+                        if (warp_live && !idle) {
+                            tmem_st16(tm + L::cS + c_begin / 2, p);
+                            if (cols > 32) tmem_st16(tm + L::cS + c_begin / 2 + 16, p2);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) p[e] = 0u;
+#pragma unroll 1
+                            for (int c = 0; c < 128; c += 32)
+                                if (half == 0 && (c < c_copy || c >= c_copy + (128 >> cp)))
+                                    tmem_st16(tm + L::cS + c / 2, p);
+                        }
+                    } else if (kTwice) {
                         // registers are short: the logits of more than 32 columns are read twice. The
                         // weights of columns c .. c + 31 take the 16 columns from c / 2, whose logits
                         // have been read or are another copy's
@@ -806,21 +957,30 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                             if (c < kLow) tmem_st16(tm + L::cS + 64 + c / 2, l);
                         }
                     }
-                    l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    if (!idle) l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_st_wait();
                 }
                 tc_fence_before();
                 mbar_arrive_warp(bar(L::PR + w));
             }
+            // the next stretch's rows while the last product of values runs
+            if (L::ahead && ok && at < u_end) {
+                next = stretch_of(walk, at);
+                if (L::single) load_rows(next);
+            }
             if (!ok || !(ok = wait.warp(bar(L::FIN + w), seg & 1))) break;
             ++seg;
             tc_fence_after();
             if (releases) release(L::VE, (step - 1) % NV);
+            if (halves) {  // the row's sum
+                l_run += exchange(l_run);
+                if (!ok) break;
+            }
             if (warp_live) {
                 // the part's place: its CTA and item; a row whose keys were all absent leaves a sum of 0
                 const size_t e = ((size_t)(blockIdx.x + t.item) * NT + w) * 128 + r;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = L::duo ? half * (D / 2) : 0; c < (L::duo ? (half + 1) * (D / 2) : D); c += 32) {
                     float o[32];
                     tld32(tm + L::cO + c, o);
 #pragma unroll
@@ -838,7 +998,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                         });
                     }
                 }
-                if (live) y.sml[NT - 1][e] = make_float2(m_run, l_run);
+                if (live && half == 0) y.sml[NT - 1][e] = make_float2(m_run, l_run);
             }
             tc_fence_before();
         }
@@ -895,8 +1055,11 @@ cudaError_t launch_cached(const Step &a, const TcWs &y, uint64_t limit_ns, cudaS
 #define PASS(NT, D, FOX, M) \
     template cudaError_t launch_cached<NT, D, FOX, M>(const Step &, const TcWs &, uint64_t, cudaStream_t);
 #define EXTERN_PASS(NT, D, FOX, M) extern PASS(NT, D, FOX, M)
+#define ONE_PASS(WHAT) \
+    WHAT(1, 64, false, Pass::one) WHAT(1, 128, false, Pass::one) WHAT(1, 64, true, Pass::one) WHAT(1, 128, true, Pass::one)
 EACH_PASS(EXTERN_PASS, Pass::window)
 EACH_PASS(EXTERN_PASS, Pass::shared)
+ONE_PASS(EXTERN_PASS)
 
 }  // namespace paged
 }  // namespace path

@@ -1,5 +1,5 @@
 // The prefixes of a bf16 step (paged_prefix.cuh): plan, queries and the pass over the shared keys on
-// tcgen05 tensor cores (paged_cached_tc.cuh).
+// tcgen05 tensor cores (paged_cached_tc.cuh); and steps of single tokens behind them or through a window.
 #include "paged_cached_tc.cuh"
 #include "paged_prefix.cuh"
 
@@ -12,42 +12,63 @@ namespace {
 
 static_assert(kThr == kPrefixThr, "make_plans");
 
-// ---------------------------------------------------------------- plan and single tokens
-// The first CTA makes the plan, the others carry the single tokens' queries, a sequence and key head
-// each. With up to kFused sequences they find their places by themselves beside it, else by a plan
-// made before (by this kernel, with no sequence).
+// ---------------------------------------------------------------- plans and single tokens
+// The first CTA makes the plan of the prefixes, the next one (OWN) that of the step, the others take the
+// single tokens, a sequence and key head each: OWN, of a step that has no others, enter them into
+// the cache and leave their queries and parts; BEHIND, carry their queries to the prefix's end. With up
+// to kFused sequences these find their places by themselves beside the plan, else by one made before
+// (plan: by a launch of this kernel with no sequence).
 constexpr int kFused = 1024;
 
-template <int D, bool FUSED>
-__global__ void __launch_bounds__(kThr) prefix_single_kernel(const Step a, const Step v, const Prefix x, const TcWs z,
-                                                             bool plan) {
+template <int D, bool OWN, bool BEHIND>
+__global__ void __launch_bounds__(kThr) tc_single_kernel(const Step a, const Step v, const Prefix x, const TcWs y,
+                                                         const TcWs z, int plans, bool fused) {
     __shared__ long long sums[2 * kThr / 32];
     const int G = a.c.G;
     grid_begin();
-    if (blockIdx.x == 0 && plan) {
-        place_tokens(a, x);
-        make_plans<D>(v, z, sums);
-        grid_wait();  // what it writes is this call's alone
+    // (no kernel before reads or writes what this one does, but for a plan made before)
+    if ((int)blockIdx.x < plans) {
+        if (BEHIND && blockIdx.x == 0) {
+            place_tokens(a, x);
+            make_plans<D>(v, z, sums);
+        } else if (OWN) {
+            make_plans<D>(a, y, sums);
+        }
+        grid_wait();
         return;
     }
-    const int item = blockIdx.x - (plan ? 1 : 0), h = item % a.c.Hkv, b = item / a.c.Hkv;
-    if (!FUSED) grid_wait();
+    const int item = blockIdx.x - plans, h = item % a.c.Hkv, b = item / a.c.Hkv;
+    if (!fused) grid_wait();
     const Seq s = seq_of(a, b);
-    int start = -1;
-    if (s.T == 1 && __ldg(x.of + b) >= 0) start = FUSED ? place_one(a, x, b) : x.start[b];
-    if (start >= 0) {
-        const size_t to = (size_t)h * z.R + (size_t)start * G;
-        prefix_single<bf, D>(
-            a, x, s, b, h,
-            [&](int g, int i, float q) {
-                q *= a.scale_log2;
-                const bf hi = __float2bfloat16_rn(q);
-                z.qt[(to + g) * D + i] = hi;
-                z.ql[(to + g) * D + i] = __float2bfloat16_rn(q - __bfloat162float(hi));
-            },
-            [&](int g, float t) { z.gq[to + g] = t; });
+    if (s.T == 1) {
+        int start = -1;
+        if (BEHIND && __ldg(x.of + b) >= 0) start = fused ? place_one(a, x, b) : x.start[b];
+        if (OWN) enter_single<D>(a, y, s, b, slot_of(s, b, 0), h);
+        if (BEHIND && start >= 0) {
+            const size_t to = (size_t)h * z.R + (size_t)start * G;
+            prefix_single<bf, D>(
+                a, x, s, b, h,
+                [&](int g, int i, float q) {
+                    q *= a.scale_log2;
+                    const bf hi = __float2bfloat16_rn(q);
+                    z.qt[(to + g) * D + i] = hi;
+                    z.ql[(to + g) * D + i] = __float2bfloat16_rn(q - __bfloat162float(hi));
+                },
+                [&](int g, float t) { z.gq[to + g] = t; });
+        }
     }
-    if (FUSED) grid_wait();  // no kernel before reads or writes what this one does
+    if (fused) grid_wait();
+}
+
+template <int D, bool OWN, bool BEHIND>
+cudaError_t launch_tokens(const Step &a, const Prefix &x, const TcWs &y, const TcWs &z, bool first, cudaStream_t stream) {
+    const Step v = BEHIND ? shared_step(a, x) : a;
+    const int items = a.c.seqs * a.c.Hkv, plans = (OWN ? 1 : 0) + (BEHIND ? 1 : 0);
+    const auto kern = tc_single_kernel<D, OWN, BEHIND>;
+    if (!BEHIND || a.c.seqs <= kFused)
+        return launch(kern, dim3(plans + items), kThr, 0, stream, first, a, v, x, y, z, plans, true);
+    const cudaError_t e = launch(kern, dim3(plans), kThr, 0, stream, first, a, v, x, y, z, plans, true);
+    return e != cudaSuccess ? e : launch(kern, dim3(items), kThr, 0, stream, false, a, v, x, y, z, 0, false);
 }
 
 // ---------------------------------------------------------------- queries of several tokens
@@ -130,28 +151,38 @@ __global__ void __launch_bounds__(kThr, 2) prefix_query_kernel(const Step a, con
     }
 }
 
+// The attention of the prefixes' sequences, behind their queries.
 template <int D, bool FOX>
-cudaError_t launch_all(const Step &a, const Prefix &x, const TcWs &y, const TcWs &z, bool first, uint64_t limit_ns,
-                       cudaStream_t stream) {
+cudaError_t launch_shared(const Step &a, const Prefix &x, const TcWs &z, uint64_t limit_ns, cudaStream_t stream) {
     const Step v = shared_step(a, x);
-    const int items = a.c.seqs * a.c.Hkv;
-    cudaError_t e;
-    if (a.c.seqs <= kFused) {
-        e = launch(prefix_single_kernel<D, true>, dim3(1 + items), kThr, 0, stream, first, a, v, x, z, true);
-    } else {
-        e = launch(prefix_single_kernel<D, false>, dim3(1), kThr, 0, stream, first, a, v, x, z, true);
-        if (e == cudaSuccess)
-            e = launch(prefix_single_kernel<D, false>, dim3(items), kThr, 0, stream, false, a, v, x, z, false);
-    }
+    const cudaError_t e = launch_cached<1, D, FOX, Pass::shared>(v, z, limit_ns, stream);
+    if (e != cudaSuccess || (long long)a.N * a.c.G <= 128) return e;
+    return launch_cached<2, D, FOX, Pass::shared>(v, z, limit_ns, stream);
+}
+
+template <int D, bool FOX>
+cudaError_t launch_all(const Step &a, const Prefix &x, const TcWs *y, const TcWs &z, bool first, uint64_t limit_ns,
+                       cudaStream_t stream) {
+    cudaError_t e = launch_tokens<D, false, true>(a, x, z, z, first, stream);
     if (a.max_chunk > 1) {
         if (e == cudaSuccess) e = big_smem(prefix_query_kernel<D>, QuerySmem<D>::bytes);
         if (e == cudaSuccess)
             e = launch(prefix_query_kernel<D>, dim3(tile_slots(a.N, a.c.G, a.c.seqs, kC * kTiles), a.c.Hkv), kThr,
-                       QuerySmem<D>::bytes, stream, false, a, x, y, z);
+                       QuerySmem<D>::bytes, stream, false, a, x, *y, z);
     }
-    if (e == cudaSuccess) e = launch_cached<1, D, FOX, Pass::shared>(v, z, limit_ns, stream);
-    if (e == cudaSuccess && (long long)a.N * a.c.G > 128) e = launch_cached<2, D, FOX, Pass::shared>(v, z, limit_ns, stream);
+    if (e == cudaSuccess) e = launch_shared<D, FOX>(a, x, z, limit_ns, stream);
     if (e == cudaSuccess) e = launch_prefix_carry<bf, D>(a, x, stream);
+    return e;
+}
+
+// A step of single tokens, through a window or behind prefixes, up to its joining.
+template <int D, bool FOX>
+cudaError_t launch_ones(const Step &a, const Prefix *x, const TcWs &y, const TcWs &z, uint64_t limit_ns,
+                        cudaStream_t stream) {
+    cudaError_t e = x != nullptr ? launch_tokens<D, true, true>(a, *x, y, z, true, stream)
+                                 : launch_tokens<D, true, false>(a, Prefix{}, y, z, true, stream);
+    if (e == cudaSuccess && a.c.max_pages > 0) e = launch_cached<1, D, FOX, Pass::one>(a, y, limit_ns, stream);
+    if (e == cudaSuccess && x != nullptr) e = launch_shared<D, FOX>(a, *x, z, limit_ns, stream);
     return e;
 }
 
@@ -171,7 +202,7 @@ size_t layout(const Step &a, int d, char *w, Prefix *x, TcWs *z) {
     z->ql = reinterpret_cast<bf *>(take(rows * d * 2));
     z->gq = reinterpret_cast<float *>(take(rows * 4));
     for (int p = 0; p < 2; ++p) {
-        const int ctas = 152 * (p == 0 && d == 64 ? CachedCfg<1, 64, Pass::shared>::ctas_per_sm : 1);
+        const int ctas = 152;  // one a SM
         const size_t tile = 128 * (p + 1);
         // (both plans in any case: the sizes must not fall as the step grows)
         const size_t parts = ctas + (size_t)tile_slots(a.N, c.G, c.seqs < a.N ? c.seqs : a.N, (int)tile) * c.Hkv;
@@ -193,24 +224,41 @@ size_t prefix_tc_bytes(const Step &a, int d) {
     return layout(a, d, nullptr, &x, &z);
 }
 
-// behind: what the step's joining takes up
-cudaError_t launch_prefix_tc(const Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
-                             uint64_t limit_ns, Behind *behind, cudaStream_t stream) {
+namespace {
+
+Prefix prefix_at(const Step &a, int d, float *carry, float *gates, void *ws, TcWs *z, Behind *behind) {
     Prefix x = {};
-    TcWs z = {};
-    layout(a, d, static_cast<char *>(ws), &x, &z);
+    layout(a, d, static_cast<char *>(ws), &x, z);
     x.of = a.prefix_of;
     x.carry = carry;
     x.gates = gates;
-    *behind = Behind{x.of, x.cu, x.start, {z.so[0], z.so[1]}, {z.sml[0], z.sml[1]}, {z.plan[0], z.plan[1]}};
-    TcWs from = y != nullptr ? *y : z;  // (single tokens alone: their queries are formed from the inputs)
-    from.R = z.R;
+    *behind = Behind{x.of, x.cu, x.start, {z->so[0], z->so[1]}, {z->sml[0], z->sml[1]}, {z->plan[0], z->plan[1]}};
+    return x;
+}
+
+}  // namespace
+
+// y: the step's workspace, null for single tokens alone, whose queries are formed from the inputs;
+// behind: what the step's joining takes up
+cudaError_t launch_prefix_tc(const Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
+                             uint64_t limit_ns, Behind *behind, cudaStream_t stream) {
+    TcWs z = {};
+    const Prefix x = prefix_at(a, d, carry, gates, ws, &z, behind);
     const bool fox = a.log_f != nullptr;
-    if (d == 64)
-        return fox ? launch_all<64, true>(a, x, from, z, first, limit_ns, stream)
-                   : launch_all<64, false>(a, x, from, z, first, limit_ns, stream);
-    return fox ? launch_all<128, true>(a, x, from, z, first, limit_ns, stream)
-               : launch_all<128, false>(a, x, from, z, first, limit_ns, stream);
+    auto all = [&](auto run) { return run(a, x, y, z, first, limit_ns, stream); };
+    if (d == 64) return fox ? all(launch_all<64, true>) : all(launch_all<64, false>);
+    return fox ? all(launch_all<128, true>) : all(launch_all<128, false>);
+}
+
+cudaError_t launch_singles(const Step &a, int d, const TcWs &y, float *carry, float *gates, void *ws, uint64_t limit_ns,
+                           Behind *behind, cudaStream_t stream) {
+    TcWs z = {};
+    Prefix x = {};
+    if (carry != nullptr) x = prefix_at(a, d, carry, gates, ws, &z, behind);
+    const bool fox = a.log_f != nullptr;
+    auto all = [&](auto run) { return run(a, carry != nullptr ? &x : nullptr, y, z, limit_ns, stream); };
+    if (d == 64) return fox ? all(launch_ones<64, true>) : all(launch_ones<64, false>);
+    return fox ? all(launch_ones<128, true>) : all(launch_ones<128, false>);
 }
 
 }  // namespace paged

@@ -76,77 +76,15 @@ __device__ __forceinline__ void put2(bf *t, int ld, int r, int c, uint32_t v) {
     *reinterpret_cast<uint32_t *>(t + r * ld + c) = v;
 }
 
-// A sequence's only token: H = I - beta w w^T, q~ = q - beta (w . q) w, and the token's own key
-// and value enter the cache as they are. A warp per query head in turns; all threads form the
-// product less I, -beta w w^T.
+// A sequence's only token, and, by all threads, the product less I, -beta w w^T.
 template <int D>
 __device__ __forceinline__ void prep_single(const Step &a, const TcWs &y, const Seq &s, int b, int slot, int h,
                                             float *buf) {
-    constexpr int E = D / 32;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.c.G, kw = kThr / 32;
+    const int tid = threadIdx.x;
+    enter_single<D>(a, y, s, b, slot, h);
     const float beta = a.beta[(long long)s.first * a.sb.tok + h * a.sb.head];
-    auto row = [&](const void *p, Stride st, int head) {
-        return static_cast<const bf *>(p) + (long long)s.first * st.tok + (long long)head * st.head + lane * E;
-    };
-    const bf *const wp = row(a.w, a.sw, h), *const kp = row(a.k, a.sk, h), *const vp = row(a.v, a.sv, h);
-    float w[E], k[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        w[e] = __bfloat162float(wp[e]);
-        k[e] = __bfloat162float(kp[e]);
-    }
-    if (warp == 0)
-#pragma unroll
-        for (int e = 0; e < E; ++e) buf[lane * E + e] = w[e];
-    const int pos = s.n, sl = pos >> a.c.page_shift, off = pos & (a.c.page - 1);
-    const int kid = page_of(a, a.c.k_table, b, sl, a.c.nk), vid = page_of(a, a.c.v_table, b, sl, a.c.nv);
-    if (warp == kw - 1) {
-        if (kid >= 0)
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                static_cast<bf *>(a.c.k_pages)[((((size_t)kid * a.c.Hkv + h) << a.c.page_shift) + off) * D + lane * E +
-                                               e] = kp[e];
-        if (vid >= 0)
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                static_cast<bf *>(a.c.v_pages)[((((size_t)vid * a.c.Hkv + h) << a.c.page_shift) + off) * D + lane * E +
-                                               e] = vp[e];
-    }
-    for (int g = warp; g < G; g += kw) {
-        const int hq = h * G + g;
-        const bf *const qp = row(a.q, a.sq, hq);
-        float q[E], wq = 0.f, kq = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            q[e] = __bfloat162float(qp[e]);
-            wq = fmaf(w[e], q[e], wq);
-            kq = fmaf(k[e], q[e], kq);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            wq += __shfl_xor_sync(0xffffffffu, wq, o);
-            kq += __shfl_xor_sync(0xffffffffu, kq, o);
-        }
-        const size_t r = (size_t)h * y.R + (size_t)s.first * G + g;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float x = fmaf(-beta * wq, w[e], q[e]) * a.scale_log2;
-            const bf xh = __float2bfloat16_rn(x);
-            y.qt[r * D + lane * E + e] = xh;
-            if (low_queries(a, 1, D))
-                y.ql[r * D + lane * E + e] = __float2bfloat16_rn(x - __bfloat162float(xh));
-            y.po[r * D + lane * E + e] = __bfloat162float(vp[e]);
-        }
-        if (lane == 0) {
-            y.pml[r] = make_float2(kq * a.scale_log2, 1.f);
-            if (a.log_f != nullptr) {
-                const float f = a.log_f[(long long)s.first * a.sf.tok + (long long)hq * a.sf.head];
-                y.gq[r] = f;
-                y.gtot[(size_t)slot * a.c.Hq + hq] = f;
-                if (kid >= 0) a.c.g_pages[(((size_t)kid * a.c.Hq + hq) << a.c.page_shift) + off] = 0.f;
-            }
-        }
-    }
+    if (tid < D)
+        buf[tid] = __bfloat162float(static_cast<const bf *>(a.w)[(long long)s.first * a.sw.tok + h * a.sw.head + tid]);
     if (s.n == 0) return;  // no cached key takes the product
     __syncthreads();
     bf *const mh = y.mt + (mt_row(a, s, b) * a.c.Hkv + h) * 2 * D * D, *const ml = mh + (size_t)D * D;

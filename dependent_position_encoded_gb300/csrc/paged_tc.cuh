@@ -23,8 +23,9 @@ struct Plan {
 };
 
 // What a pass over cached keys does: that of a step over its own cache, the same seen through a
-// window, or one over keys that several sequences share, which stay as they are.
-enum class Pass { step, window, shared };
+// window, that of single tokens (a window or none), or one over keys that several sequences share,
+// which stay as they are.
+enum class Pass { step, window, one, shared };
 
 // Whether a carried query enters the cached keys' logits as a high and a low bf16 part. Rounded
 // once to bf16 it adds as much error to the output as the weights' and the output's own rounding
@@ -103,29 +104,41 @@ struct Stretch {
     int b, h, tile, k0, steps;
     long long item;  // over all sequences
 };
-__device__ __forceinline__ Stretch stretch_at(const Step &a, const Plan &p, int D, int NT, long long u,
-                                              long long end) {
-    int lo = 0, hi = a.c.seqs - 1;  // the last sequence with units[b] <= u: it has units
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.units[mid] <= u) lo = mid;
-        else hi = mid - 1;
+// One after the other: the sequence of the last one is kept, since its next key head or row tile mostly
+// comes next, and a look-up is half a dozen loads that wait for each other. (Walk().at(): looked up anew.)
+struct Walk {
+    long long u0 = 0, u1 = -1, items = 0;  // the sequence's units and its first item
+    Seq s;
+    int b, tiles, kt;
+    __device__ __forceinline__ Stretch at(const Step &a, const Plan &p, int D, int NT, long long u, long long end) {
+        if (u >= u1) {
+            int lo = 0, hi = a.c.seqs - 1;  // the last sequence with units[b] <= u: it has units
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (p.units[mid] <= u) lo = mid;
+                else hi = mid - 1;
+            }
+            b = lo;
+            s = seq_of(a, lo);
+            plan_of(a, s, D, NT, tiles, kt);
+            u0 = p.units[lo];
+            u1 = p.units[lo + 1];
+            items = p.items[lo];
+        }
+        Stretch t;
+        t.b = b;
+        t.s = s;
+        const long long rem = u - u0;
+        const int it = (int)(rem / kt);
+        t.k0 = (int)(rem - (long long)it * kt);
+        t.h = it / tiles;
+        t.tile = it - t.h * tiles;
+        t.item = items + it;
+        const long long left = end - u;
+        t.steps = kt - t.k0 < left ? kt - t.k0 : (int)left;
+        return t;
     }
-    Stretch t;
-    t.b = lo;
-    t.s = seq_of(a, lo);
-    int tiles, kt;
-    plan_of(a, t.s, D, NT, tiles, kt);
-    const long long rem = u - p.units[lo];
-    const int it = (int)(rem / kt);
-    t.k0 = (int)(rem - (long long)it * kt);
-    t.h = it / tiles;
-    t.tile = it - t.h * tiles;
-    t.item = p.items[lo] + it;
-    const long long left = end - u;
-    t.steps = kt - t.k0 < left ? kt - t.k0 : (int)left;
-    return t;
-}
+};
 
 constexpr int kThr = 256;  // threads of a CTA of the kernels beside the attention's
 
@@ -187,6 +200,75 @@ __device__ __forceinline__ void make_plans(const Step &a, const TcWs &y, long lo
             }
             if (b <= a.c.seqs) (q & 1 ? y.plan[q >> 1].items : y.plan[q >> 1].units)[b] = before + x - v[q];
             run[q] += all;
+        }
+    }
+}
+
+// A sequence's only token: H = I - beta w w^T, q~ = q - beta (w . q) w, and the token's own key
+// and value enter the cache as they are. A warp per query head in turns.
+template <int D>
+__device__ __forceinline__ void enter_single(const Step &a, const TcWs &y, const Seq &s, int b, int slot, int h) {
+    using bf = __nv_bfloat16;
+    constexpr int E = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.c.G, kw = kThr / 32;
+    const float beta = a.beta[(long long)s.first * a.sb.tok + h * a.sb.head];
+    auto row = [&](const void *p, Stride st, int head) {
+        return static_cast<const bf *>(p) + (long long)s.first * st.tok + (long long)head * st.head + lane * E;
+    };
+    const bf *const wp = row(a.w, a.sw, h), *const kp = row(a.k, a.sk, h), *const vp = row(a.v, a.sv, h);
+    float w[E], k[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        w[e] = __bfloat162float(wp[e]);
+        k[e] = __bfloat162float(kp[e]);
+    }
+    const int pos = s.n, sl = pos >> a.c.page_shift, off = pos & (a.c.page - 1);
+    const int kid = page_of(a, a.c.k_table, b, sl, a.c.nk), vid = page_of(a, a.c.v_table, b, sl, a.c.nv);
+    if (warp == kw - 1) {
+        if (kid >= 0)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                static_cast<bf *>(a.c.k_pages)[((((size_t)kid * a.c.Hkv + h) << a.c.page_shift) + off) * D + lane * E +
+                                               e] = kp[e];
+        if (vid >= 0)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                static_cast<bf *>(a.c.v_pages)[((((size_t)vid * a.c.Hkv + h) << a.c.page_shift) + off) * D + lane * E +
+                                               e] = vp[e];
+    }
+    for (int g = warp; g < G; g += kw) {
+        const int hq = h * G + g;
+        const bf *const qp = row(a.q, a.sq, hq);
+        float q[E], wq = 0.f, kq = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            q[e] = __bfloat162float(qp[e]);
+            wq = fmaf(w[e], q[e], wq);
+            kq = fmaf(k[e], q[e], kq);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            wq += __shfl_xor_sync(0xffffffffu, wq, o);
+            kq += __shfl_xor_sync(0xffffffffu, kq, o);
+        }
+        const size_t r = (size_t)h * y.R + (size_t)s.first * G + g;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float x = fmaf(-beta * wq, w[e], q[e]) * a.scale_log2;
+            const bf xh = __float2bfloat16_rn(x);
+            y.qt[r * D + lane * E + e] = xh;
+            if (low_queries(a, 1, D))
+                y.ql[r * D + lane * E + e] = __float2bfloat16_rn(x - __bfloat162float(xh));
+            y.po[r * D + lane * E + e] = __bfloat162float(vp[e]);
+        }
+        if (lane == 0) {
+            y.pml[r] = make_float2(kq * a.scale_log2, 1.f);
+            if (a.log_f != nullptr) {
+                const float f = a.log_f[(long long)s.first * a.sf.tok + (long long)hq * a.sf.head];
+                y.gq[r] = f;
+                y.gtot[(size_t)slot * a.c.Hq + hq] = f;
+                if (kid >= 0) a.c.g_pages[(((size_t)kid * a.c.Hq + hq) << a.c.page_shift) + off] = 0.f;
+            }
         }
     }
 }
