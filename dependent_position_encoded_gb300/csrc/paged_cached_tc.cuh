@@ -99,6 +99,12 @@ __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
     return __uint_as_float(x);
 }
 
+// Waits until all committed stores but the last N have finished reading shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read_but() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
 // multiplies N fp32 columns of the thread's row by f (16 at a time: the row's logits are in
 // registers beside it)
 template <int N>
@@ -169,29 +175,30 @@ struct CachedCfg {
     // the keys' update in this pass: by a product with P - I, or (single tokens) on the CUDA cores
     static constexpr bool update = NT == 1 && M != Pass::shared, single = NT == 1 && M == Pass::one,
                           matrix = update && !single;
-    // two warpgroups for the softmax of one row tile
-    static constexpr bool duo = NT == 1 && M == Pass::shared;
+    // shared keys at D = 128: two warpgroups for the softmax of one row tile; and, as for single tokens, two
+    // places for its logits, so that the next step's product runs beside it. (Else at D = 64 two CTAs run
+    // beside each other instead.)
+    static constexpr bool duo = NT == 1 && D == 128 && M == Pass::shared, two_s = duo || single;
     // the next stretch is looked up, and its rows fetched, before the last one's end
-    static constexpr bool ahead = single || duo;
+    static constexpr bool ahead = NT == 1 && !matrix;
     static constexpr bool rows_in_tmem = single || (update && D == 128), low = keeps_low(NT, D);
     static constexpr uint32_t X = 0, xbytes = rows_in_tmem ? 0 : NT * (low ? 2 : 1) * tile;
     static constexpr uint32_t P = X + xbytes, pbytes = matrix ? 2 * D * D * 2 : 0;
     // slots of keys and of values: what fits beside; for NT = 1 and D = 64 so that two CTAs share
     // an SM. With NT = 1 a key slot is held until the updated keys have left it.
     static constexpr int NK = matrix ? (D == 64 ? 2 : 3)
-                              : single ? (D == 64 ? 8 : 4)
-                              : NT == 1 ? (D == 64 ? 6 : 3)
-                                        : (D == 64 ? 4 : 3);
-    static constexpr int NV = matrix ? 2 : single ? (D == 64 ? 5 : 3) : NT == 1 ? (D == 64 ? 6 : 2) : (D == 64 ? 4 : 2);
+                              : single ? (D == 64 ? 8 : 4) : NT == 1 ? 3 : (D == 64 ? 4 : 3);
+    static constexpr int NV = single ? (D == 64 ? 5 : 3) : NT == 1 ? 2 : (D == 64 ? 4 : 2);
     static constexpr uint32_t K = P + pbytes, V = K + NK * tile, bars = V + NV * tile;
     static constexpr int KF = 0, KE = NK, VF = 2 * NK, VE = VF + NV, XF = VE + NV, XE = XF + 1, SF = XE + 1,
                          PR = SF + 2, FIN = PR + 2, DF = FIN + 2, DE = DF + NK, TMP = DE + 1, END = TMP + 2,
-                         XT = END + 2, EX = XT + 1, count = EX + 1;
+                         XT = END + 2, EX = XT + 1, PD = EX + 1, count = PD + 1;
     // behind the barriers: TMEM's address and the abort flag; single: the token's w, two of them
     static constexpr uint32_t W = (bars + count * 8 + 16 + 15) / 16 * 16;  // read 16 bytes at a time
     static constexpr uint32_t bytes = W + (single ? 2 * D * 4 : 0);  // from a 1024-byte boundary
-    static constexpr int threads = 384;
-    static constexpr int ctas_per_sm = matrix && D == 64 ? 2 : 1;
+    // warps: those of the rows, the update's, then the others from `other` on
+    static constexpr int other = update || duo || NT == 2 ? 8 : 4, threads = 32 * (other + 4);
+    static constexpr int ctas_per_sm = NT == 1 && D == 64 && !single ? 2 : 1;
     // registers after the split of what the CTA is launched with (NT = 2: 168 for each thread; NT = 1
     // with two CTAs per SM: 80): the softmax's warpgroups, the update's and the last one
     static constexpr bool split = NT == 2 || (matrix && D == 64);
@@ -199,7 +206,8 @@ struct CachedCfg {
     // TMEM columns: per row tile S 128 (the weights over it) and O; NT = 1: the update's product, or the
     // rows' two parts, or (duo) what the halves of a row tell each other
     static constexpr uint32_t cS = 0, cO = 128, per_tile = 256, cD = 128 + D, cX = D == 64 ? 192 : 384;
-    static constexpr uint32_t cols = matrix && D == 64 ? 256 : 512;
+    static constexpr uint32_t cS2 = 256;  // two_s: the odd steps' logits and weights
+    static constexpr uint32_t cols = NT == 1 && D == 64 && !single ? 256 : 512;
 };
 template <Pass M>
 struct CachedFits {
@@ -294,7 +302,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
         }
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == L::other) {
         tmem_alloc(smem_u32(tslot), L::cols);
         tmem_relinquish();
         tc_fence_before();
@@ -323,11 +331,11 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
         return lane < nbox && j < t.s.n && (!WIN || seen.any(j, box));
     };
 
-    if (warp >= 8) {
+    if (warp >= L::other) {
         if (L::split) reg_dec<L::reg_other>();
-        if (warp == 9 || warp == 10) {
+        if (warp == L::other + 1 || warp == L::other + 2) {
             // ======================================================== pages into the ring
-            const bool keys = warp == 9;
+            const bool keys = warp == L::other + 1;
             const int *const table = keys ? a.c.k_table : a.c.v_table;
             const int npool = keys ? a.c.nk : a.c.nv;
             const uint32_t tmp = bar(L::TMP + (keys ? 0 : 1));
@@ -418,7 +426,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                     mbar_wait(bar(full0 + v % ring), (v / ring) & 1, limit_ns);
                 if (keys && !L::single) mbar_wait(bar(L::XF), seg & 1, limit_ns);
             }
-        } else if (lane == 0 && warp == 8) {
+        } else if (lane == 0 && warp == L::other) {
             // ======================================================== S and P V
             // A lone thread's instructions follow each other slowly, and two tiles' MMAs keep the
             // tensor core busy only if little stands between them: slots and phases run along,
@@ -429,19 +437,19 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                            v_desc = sdesc_sw128(base + L::V, L::atom, 1024);
             Ring<NK> k;
             Ring<NV> v;
-            uint32_t seg = 0, parity[2] = {0, 0};
+            uint32_t seg = 0, parity[2] = {0, 0}, turns = 0;  // (turns: the same bits, by place)
             bool ok = true;
-            auto issue_s = [&](int q) {
-                const uint64_t xd = x_desc + q * kTile, kd = k_desc + k.slot * kTile;
+            auto issue_s = [&](int q) {  // of row tile q (two_s: into place q)
+                const uint64_t xd = x_desc + (L::two_s ? 0 : q) * kTile, kd = k_desc + k.slot * kTile;
 #pragma unroll
                 for (int part = 0; part < (L::low ? 2 : 1); ++part)  // the rows' high and low parts
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t b = kd + (kk >> 2) * kAtom + 2 * (kk & 3);
                         if (L::rows_in_tmem)
-                            umma_tA(tmem + L::cS, tmem + L::cX + part * (D / 2) + 8 * kk, b, ID_S, part > 0 || kk > 0);
+                            umma_tA(tmem + L::cS + (L::two_s ? L::cS2 * q : 0), tmem + L::cX + part * (D / 2) + 8 * kk, b, ID_S, part > 0 || kk > 0);
                         else
-                            umma_bf16(tmem + L::per_tile * q + L::cS,
+                            umma_bf16(tmem + (L::two_s ? L::cS2 : L::per_tile) * q + L::cS,
                                       xd + part * NT * kTile + (kk >> 2) * kAtom + 2 * (kk & 3), b, ID_S,
                                       part > 0 || kk > 0);
                     }
@@ -449,10 +457,10 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             };
             auto issue_pv = [&](int q, bool first) {
                 const uint64_t vd = v_desc + v.slot * kTile;
-                const uint32_t tm = tmem + L::per_tile * q;
-                umma_tA(tm + L::cO, tm + L::cS, vd, ID_O, !first);
+                const uint32_t tm = tmem + (L::two_s ? 0 : L::per_tile * q), p = tm + L::cS + (L::two_s ? L::cS2 * q : 0);
+                umma_tA(tm + L::cO, p, vd, ID_O, !first);
 #pragma unroll
-                for (int kk = 1; kk < 8; ++kk) umma_tA(tm + L::cO, tm + L::cS + 8 * kk, vd + 128 * kk, ID_O, 1);
+                for (int kk = 1; kk < 8; ++kk) umma_tA(tm + L::cO, p + 8 * kk, vd + 128 * kk, ID_O, 1);
                 if (kLow > 0)
 #pragma unroll
                     for (int kk = 0; kk < kLow / 16; ++kk)
@@ -462,6 +470,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             // handed back by the softmax's warps, which learn of the products' ends anyway.)
             auto after_s = [&](bool last) {
                 if (L::update) umma_commit(bar(L::DF + k.slot));
+                if (L::duo) umma_commit(bar(L::KE + k.slot));
                 if (last && !L::rows_in_tmem) umma_commit(bar(L::XE));
                 k.next();
             };
@@ -476,7 +485,31 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                 issue_s(0);
                 if (two) issue_s(1);
                 after_s(t.steps == 1);
-                for (int i = 0; i < t.steps; ++i) {
+                if (L::two_s) {
+                    // the logits run a step ahead of the weights
+                    if (t.steps > 1) {
+                        if (!(ok = wait(bar(L::KF + k.slot), k.phase))) break;
+                        issue_s(1);
+                        after_s(t.steps == 2);
+                    }
+                    for (int i = 0; i < t.steps; ++i) {
+                        const int q = i & 1;
+                        if (!(ok = wait(bar(L::VF + v.slot), v.phase))) break;
+                        if (!(ok = wait(bar(L::PR + q), (turns >> q) & 1))) break;
+                        turns ^= 1u << q;
+                        tc_fence_after();
+                        issue_pv(q, i == 0);
+                        umma_commit(bar(L::VE + v.slot));
+                        umma_commit(bar(L::PD));
+                        v.next();
+                        if (i + 2 < t.steps) {
+                            if (!(ok = wait(bar(L::KF + k.slot), k.phase))) break;
+                            issue_s(q);
+                            after_s(i + 3 == t.steps);
+                        }
+                    }
+                }
+                for (int i = 0; !L::two_s && i < t.steps; ++i) {
                     const bool more = i + 1 < t.steps;
                     if (!(ok = wait(bar(L::VF + v.slot), v.phase))) break;
                     if (!(ok = wait(bar(L::PR), parity[0]))) break;
@@ -505,7 +538,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             // every product has completed before TMEM is freed
             umma_commit(bar(L::END));
             mbar_wait(bar(L::END), 0, limit_ns);
-        } else if (L::matrix && lane == 0 && warp == 11) {
+        } else if (L::matrix && lane == 0 && warp == L::other + 3) {
             // ======================================================== K (P - I), NT = 1
             constexpr uint32_t ID_D = idesc_b16(128, D, true);
             constexpr uint64_t kAtom = L::atom >> 4, kTile = L::tile >> 4, kPart = (NA * D * 128) >> 4;
@@ -537,15 +570,16 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             umma_commit(bar(L::END + 1));
             mbar_wait(bar(L::END + 1), 0, limit_ns);
         }
-    } else if (NT == 1 && !L::duo && warp >= 4) {
+    } else if (L::update && warp >= 4) {
         // ============================================================ the keys' update
         if (L::split) reg_dec<L::reg_update>();
         const int r = tid - 128;
         const uint32_t tm = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + L::cD;
         bool ok = true;
         uint32_t j = 0, seg = 0;
+        bool held = false;
         Walk walk;
-        for (long long at = L::update ? u_begin : u_end; ok && at < u_end; ++seg) {
+        for (long long at = u_begin; ok && at < u_end; ++seg) {
             const Stretch t = stretch_of(walk, at);
             at += t.steps;
             // single: the token's w and beta. (A stretch's first step has a barrier behind which nobody reads
@@ -650,10 +684,19 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                         for (int x = 0; x < NA; ++x)
                             tma_store_3d(&tm_k, key_slot(j) + x * L::atom + lane * box * 128, 64 * x,
                                          (pos0 + lane * box) & (page - 1), id * a.c.Hkv + t.h);
-                        bulk_wait_read();
+                        if (!L::single) bulk_wait_read();
+                    }
+                    // single: a slot is released a step later, while the next step's keys leave
+                    if (L::single) {
+                        if (whole) bulk_wait_read_but<NA>();
+                        else bulk_wait_read();
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(L::KE + j % NK));
+                    if (lane == 0) {
+                        if (L::single && held) mbar_arrive(bar(L::KE + (j - 1) % NK));
+                        if (!L::single || !whole) mbar_arrive(bar(L::KE + j % NK));
+                    }
+                    held = whole;
                 }
             }
         }
@@ -673,7 +716,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
         Walk walk;
         // duo: the other half's x of the row (a step later its column is written again at the earliest), or
         // (of nothing) until it has read its logits
-        uint32_t turn = 0;
+        uint32_t turn = 0, phases = 0;  // (two_s: bits of the two places' logits)
         auto meet = [&]() {
             tc_fence_before();
             mbar_arrive_warp(bar(L::EX));
@@ -791,9 +834,12 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                                 ((pos0 + c) & (page - 1))));
                     }
                 }
-                if (!(ok = wait.warp(bar(L::SF + w), j & 1))) break;
+                const int place = L::two_s ? i & 1 : w;
+                const uint32_t cS = L::cS + (L::two_s ? place * L::cS2 : 0);
+                if (!(ok = wait.warp(bar(L::SF + place), (L::two_s ? phases >> place : j) & 1))) break;
+                if (L::two_s) phases ^= 1u << place;
                 tc_fence_after();
-                if (releases) {
+                if (releases && !L::two_s) {
                     if (!L::update) release(L::KE, step % NK);
                     if (i > 0) release(L::VE, (step - 1) % NV);
                 }
@@ -838,17 +884,21 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                         return fmax3(fmax3(mx[0], mx[1], mx[2]), mx[3], fmax3(fmaxf(v[28], v[29]), v[30], v[31]));
                     };
                     // the running maximum of the row; O follows it when it has risen by 2^8. (S of this
-                    // step is complete, so the previous P V is too.)
+                    // step is complete, so the previous P V is too, but with two places for S.)
                     float use;
                     auto raise = [&]() {
                         float alpha = 1.f;
-                        const bool had = L::duo ? m_run > -INFINITY : l_run > 0.f;
+                        const bool had = L::duo ? m_run > -INFINITY : l_run > 0.f;  // (duo: the same for both halves)
                         if (top > m_run + kRescale || (m_run == -INFINITY && top > -INFINITY)) {
                             alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - top);
                             m_run = top;
                         }
                         const bool resc = alpha != 1.f && had;
                         if (__any_sync(0xffffffffu, resc)) {
+                            if (L::two_s) {  // that product may still run
+                                ok = wait.warp(bar(L::PD), (j - 1) & 1);
+                                tc_fence_after();
+                            }
                             if (halves) tmem_scale<D / 2>(tm + L::cO + half * (D / 2), resc ? alpha : 1.f);
                             else tmem_scale<D>(tm + L::cO, resc ? alpha : 1.f);
                         }
@@ -875,7 +925,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                         if (warp_live && !idle)
 #pragma unroll 1
                             for (int c = c_begin; c < c_begin + cols; c += 32) {
-                                tld32(tm + L::cS + c, x);
+                                tld32(tm + cS + c, x);
                                 gate(c, x);
                                 top = fmaxf(top, max32(x));
                             }
@@ -885,12 +935,12 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                         if (warp_live && !idle) {
                             raise();
                             if (cols > 32) {
-                                tld32(tm + L::cS + c_begin, x);
+                                tld32(tm + cS + c_begin, x);
                                 gate(c_begin, x);
                             }
                             weigh(x, p, p, false);
                             if (cols > 32) {
-                                tld32(tm + L::cS + c_begin + 32, x);
+                                tld32(tm + cS + c_begin + 32, x);
                                 gate(c_begin + 32, x);
                                 weigh(x, p2, p2, false);
                             }
@@ -898,14 +948,14 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                         if (halves && cols > 32) meet();
                         if (!ok) break;
                         if (warp_live && !idle) {
-                            tmem_st16(tm + L::cS + c_begin / 2, p);
-                            if (cols > 32) tmem_st16(tm + L::cS + c_begin / 2 + 16, p2);
+                            tmem_st16(tm + cS + c_begin / 2, p);
+                            if (cols > 32) tmem_st16(tm + cS + c_begin / 2 + 16, p2);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) p[e] = 0u;
 #pragma unroll 1
                             for (int c = 0; c < 128; c += 32)
                                 if (half == 0 && (c < c_copy || c >= c_copy + (128 >> cp)))
-                                    tmem_st16(tm + L::cS + c / 2, p);
+                                    tmem_st16(tm + cS + c / 2, p);
                         }
                     } else if (kTwice) {
                         // registers are short: the logits of more than 32 columns are read twice. The
@@ -915,7 +965,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                         top = -INFINITY;
 #pragma unroll 1
                         for (int c = c_begin; c < c_begin + cols; c += 32) {
-                            tld32(tm + L::cS + c, x);
+                            tld32(tm + cS + c, x);
                             gate(c, x);
                             top = fmaxf(top, max32(x));
                         }
@@ -924,22 +974,22 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
 #pragma unroll 1
                         for (int c = c_begin; c < c_begin + cols; c += 32) {
                             if (cols > 32) {
-                                tld32(tm + L::cS + c, x);
+                                tld32(tm + cS + c, x);
                                 gate(c, x);
                             }
                             weigh(x, p, p, false);
-                            tmem_st16(tm + L::cS + c / 2, p);
+                            tmem_st16(tm + cS + c / 2, p);
                         }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) p[e] = 0u;
 #pragma unroll 1
                         for (int c = 0; c < 128; c += 32)
-                            if (c < c_begin || c >= c_begin + cols) tmem_st16(tm + L::cS + c / 2, p);
+                            if (c < c_begin || c >= c_begin + cols) tmem_st16(tm + cS + c / 2, p);
                     } else {
                         float x[128];
                         uint32_t(*u)[32] = reinterpret_cast<uint32_t(*)[32]>(x);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld32(tm + L::cS + 32 * c, u[c]);
+                        for (int c = 0; c < 4; ++c) tmem_ld32(tm + cS + 32 * c, u[c]);
                         tmem_ld_wait();
                         float mx[4];
 #pragma unroll
@@ -953,15 +1003,15 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                         for (int c = 0; c < 128; c += 32) {
                             uint32_t p[16], l[16];
                             weigh(x + c, p, l, c < kLow);
-                            tmem_st16(tm + L::cS + c / 2, p);
-                            if (c < kLow) tmem_st16(tm + L::cS + 64 + c / 2, l);
+                            tmem_st16(tm + cS + c / 2, p);
+                            if (c < kLow) tmem_st16(tm + cS + 64 + c / 2, l);
                         }
                     }
                     if (!idle) l_run += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_st_wait();
                 }
                 tc_fence_before();
-                mbar_arrive_warp(bar(L::PR + w));
+                mbar_arrive_warp(bar(L::PR + place));
             }
             // the next stretch's rows while the last product of values runs
             if (L::ahead && ok && at < u_end) {
@@ -971,7 +1021,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             if (!ok || !(ok = wait.warp(bar(L::FIN + w), seg & 1))) break;
             ++seg;
             tc_fence_after();
-            if (releases) release(L::VE, (step - 1) % NV);
+            if (releases && !L::two_s) release(L::VE, (step - 1) % NV);
             if (halves) {  // the row's sum
                 l_run += exchange(l_run);
                 if (!ok) break;
@@ -1005,7 +1055,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == L::other) {
         tc_fence_after();
         tmem_dealloc(tmem, L::cols);
     }
