@@ -34,6 +34,11 @@ struct Step {
     int N, max_chunk;
     float scale_log2;
     uint32_t *status;
+};
+
+// A step through a window or of sequences that continue prefixes. (Kernels are compiled for either kind of
+// step, A below: what a plain one would only test costs its cached pass 3%.)
+struct StepMore : Step {
     int window, sinks;  // window 0: every new token sees every position before it
     // Sequences that continue a prefix (paged_prefix.cuh): the row that each continues (below 0: none),
     // and of each row of queries (Hkv, N G) the softmax part of its prefix's keys.
@@ -48,29 +53,37 @@ struct Seq {
     int first, T, n;
 };
 
-__device__ __forceinline__ int cu_at(const Step &a, int b) { return a.shared ? a.cu[b] : __ldg(a.cu + b); }
+__device__ __forceinline__ int cu_at(const Step &a, int b) { return __ldg(a.cu + b); }
+__device__ __forceinline__ int cu_at(const StepMore &a, int b) { return a.shared ? a.cu[b] : __ldg(a.cu + b); }
 
 // Whether sequence b's row p can be its prefix: a row of the cache without tokens in this step and
 // without a prefix of its own.
-__device__ __forceinline__ bool prefix_fits(const Step &a, int b, int p) {
+__device__ __forceinline__ bool prefix_fits(const StepMore &a, int b, int p) {
     if (p >= a.c.seqs || p == b) return false;
     const int n = __ldg(a.c.lens + p);
     return __ldg(a.prefix_of + p) < 0 && __ldg(a.cu + p) == __ldg(a.cu + p + 1) && n >= 0 &&
            n <= (long long)a.c.max_pages << a.c.page_shift;
 }
 
+// Whether a sequence's prefix is one, and whether its new tokens need places in the cache.
+__device__ __forceinline__ bool prefix_ok(const Step &, const Seq &, int) { return true; }
+__device__ __forceinline__ bool prefix_ok(const StepMore &a, const Seq &s, int b) {
+    if (a.prefix_of == nullptr || s.T == 0) return true;
+    const int p = __ldg(a.prefix_of + b);
+    return p < 0 || prefix_fits(a, b, p);
+}
+__device__ __forceinline__ bool enters(const Step &) { return true; }
+__device__ __forceinline__ bool enters(const StepMore &a) { return !a.shared; }
+
 // T = 0 (and the status word set) where the lengths do not fit the step or the cache, or the
 // prefix is none.
-__device__ __forceinline__ Seq seq_of(const Step &a, int b) {
+template <typename A>
+__device__ __forceinline__ Seq seq_of(const A &a, int b) {
     const int c0 = cu_at(a, b), c1 = cu_at(a, b + 1), n = __ldg(a.c.lens + b);
     Seq s{c0, c1 - c0, n};
-    bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.N && s.T <= a.max_chunk && n >= 0 &&
-              (long long)n + (a.shared ? 0 : s.T) <= ((long long)a.c.max_pages << a.c.page_shift);
-    if (a.prefix_of != nullptr && s.T > 0) {
-        const int p = __ldg(a.prefix_of + b);
-        ok = ok && (p < 0 || prefix_fits(a, b, p));
-    }
-    if (!ok) {
+    const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.N && s.T <= a.max_chunk && n >= 0 &&
+                    (long long)n + (enters(a) ? s.T : 0) <= ((long long)a.c.max_pages << a.c.page_shift);
+    if (!ok || !prefix_ok(a, s, b)) {
         report_status(a.status, kStatusCache);
         s.T = 0;
     }
@@ -106,12 +119,18 @@ struct Sight {
         return i < from ? i : i + skip_to(n, size) - from;
     }
 };
-__device__ __forceinline__ Sight sight_of(const Step &a, const Seq &s) {
+__device__ __forceinline__ Sight sight_of(const Step &, const Seq &) { return Sight{0, 0}; }
+__device__ __forceinline__ Sight sight_of(const StepMore &a, const Seq &s) {
     const int lo = a.window > 0 && s.n >= a.window ? s.n + 1 - a.window : 0;
     return Sight{a.sinks < lo ? a.sinks : lo, lo};
 }
+__device__ __forceinline__ int window_of(const Step &) { return 0; }
+__device__ __forceinline__ int window_of(const StepMore &a) { return a.window; }
+__device__ __forceinline__ int sinks_of(const Step &) { return 0; }
+__device__ __forceinline__ int sinks_of(const StepMore &a) { return a.sinks; }
 // Positions of a sequence that a step can have in sight, at most.
-inline long long most_seen(const Step &a) {
+inline long long most_seen(const Step &a) { return (long long)a.c.max_pages << a.c.page_shift; }
+inline long long most_seen(const StepMore &a) {
     const long long cap = (long long)a.c.max_pages << a.c.page_shift, seen = (long long)a.window - 1 + a.sinks;
     return a.window > 0 && seen < cap ? seen : cap;
 }
@@ -133,7 +152,8 @@ __device__ __forceinline__ int slot_of(const Seq &s, int b, int c) { return s.fi
 
 // The (sequence, block) of a slot; false for a slot that no block has. The first slots of
 // the sequences rise with b, so a binary search finds the last one at or below the slot.
-__device__ __forceinline__ bool block_of(const Step &a, int slot, int &b, int &c, Seq &s) {
+template <typename A>
+__device__ __forceinline__ bool block_of(const A &a, int slot, int &b, int &c, Seq &s) {
     int lo = 0, hi = a.c.seqs - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;

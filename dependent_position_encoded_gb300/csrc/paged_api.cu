@@ -11,17 +11,20 @@ namespace path {
 namespace paged {
 bool decode_takes(int G);
 size_t decode_part_bytes(const Cache &c, int d);
-cudaError_t launch_decode(const Step &a, int d, bool bf16, const Behind *behind, float *part, cudaStream_t stream);
+template <typename A>
+cudaError_t launch_decode(const A &a, int d, bool bf16, const Behind *behind, float *part, cudaStream_t stream);
 size_t f32_ws_bytes(const Cache &c, int N, int d, bool fox);
-cudaError_t launch_f32(Step a, int d, void *ws, float *carry, float *gates, void *pws, cudaStream_t stream);
+template <typename A>
+cudaError_t launch_f32(A a, int d, void *ws, float *carry, float *gates, void *pws, cudaStream_t stream);
 size_t tc_ws_bytes(const Cache &c, int N, int max_chunk, int d, bool fox);
-cudaError_t launch_tc(const Step &a, int d, void *ws, float *carry, float *gates, void *pws, uint64_t limit_ns,
+template <typename A>
+cudaError_t launch_tc(const A &a, int d, void *ws, float *carry, float *gates, void *pws, uint64_t limit_ns,
                       cudaStream_t stream);
-size_t prefix_tc_bytes(const Step &a, int d);
-size_t prefix_f32_bytes(const Step &a, int d);
-cudaError_t launch_prefix_tc(const Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
+size_t prefix_tc_bytes(const StepMore &a, int d);
+size_t prefix_f32_bytes(const StepMore &a, int d);
+cudaError_t launch_prefix_tc(const StepMore &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
                              uint64_t limit_ns, Behind *behind, cudaStream_t stream);
-cudaError_t launch_prefix_f32(Step &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws, bool first,
+cudaError_t launch_prefix_f32(StepMore &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws, bool first,
                               cudaStream_t stream);
 size_t pages_ws_bytes(const Cache &c);
 cudaError_t launch_reserve(const Cache &c, const int *extra, void *ws, cudaStream_t stream);
@@ -156,7 +159,7 @@ struct More {
 };
 
 size_t prefix_bytes(const path_paged_cache *p, int N) {
-    paged::Step a{};
+    paged::StepMore a{};
     a.c = to_cache(p);
     a.N = N;
     return p->dtype == PATH_BF16 ? paged::prefix_tc_bytes(a, p->d) : paged::prefix_f32_bytes(a, p->d);
@@ -191,29 +194,33 @@ path_status extend(const path_paged_cache *p, const void *q, const void *k, cons
     for (const paged::Stride &r : {sb, sf})
         if (r.tok < 0 || r.head < 0) return PATH_ERR_ALIGN;
     const Cache c = to_cache(p);
-    paged::Step a{c, q, k, v, w, beta, fox ? log_f : nullptr, out,
-                        sq, sk, sv, sw, sb, sf, so,
-                        cu_tokens, N, max_chunk, scale * kLog2e, static_cast<uint32_t *>(ws),
-                  more.window, more.sinks, more.prefix_of, nullptr, nullptr, false};
-    const bool bf16 = p->dtype == PATH_BF16, prefix = more.prefix_of != nullptr;
+    const paged::Step plain{c, q, k, v, w, beta, fox ? log_f : nullptr, out,
+                            sq, sk, sv, sw, sb, sf, so,
+                            cu_tokens, N, max_chunk, scale * kLog2e, static_cast<uint32_t *>(ws)};
+    paged::StepMore a{plain, more.window, more.sinks, more.prefix_of, nullptr, nullptr, false};
+    const bool bf16 = p->dtype == PATH_BF16, prefix = more.prefix_of != nullptr, is_plain = !prefix && more.window == 0;
     const long long seen = paged::most_seen(a);
     const size_t own = align256(step_ws_bytes(p, seen, N, max_chunk, fox));
     if ((st = check_workspace(ws, ws_bytes, own + (prefix ? prefix_bytes(p, N) : 0))) != PATH_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char *const pws = static_cast<char *>(ws) + own;
     if (one_pass(c, seen, max_chunk, bf16, fox)) {
+        float *const part = reinterpret_cast<float *>(static_cast<char *>(ws) + 256);
+        if (is_plain) return cuda_status(paged::launch_decode(plain, p->d, bf16, nullptr, part, s));
         cudaError_t e = cudaSuccess;
         paged::Behind behind = {};
         if (prefix)
             e = bf16 ? paged::launch_prefix_tc(a, p->d, more.carry, more.gates, nullptr, pws, true, kWaitLimitNs,
                                                &behind, s)
                      : paged::launch_prefix_f32(a, p->d, more.carry, more.gates, nullptr, nullptr, pws, true, s);
-        if (e == cudaSuccess)
-            e = paged::launch_decode(a, p->d, bf16, &behind, reinterpret_cast<float *>(static_cast<char *>(ws) + 256), s);
-        return cuda_status(e);
+        return cuda_status(e == cudaSuccess ? paged::launch_decode(a, p->d, bf16, &behind, part, s) : e);
     }
-    if (bf16) return cuda_status(paged::launch_tc(a, p->d, ws, more.carry, more.gates, pws, kWaitLimitNs, s));
-    return cuda_status(paged::launch_f32(a, p->d, ws, more.carry, more.gates, pws, s));
+    if (bf16)
+        return cuda_status(is_plain
+                               ? paged::launch_tc(plain, p->d, ws, nullptr, nullptr, nullptr, kWaitLimitNs, s)
+                               : paged::launch_tc(a, p->d, ws, more.carry, more.gates, pws, kWaitLimitNs, s));
+    return cuda_status(is_plain ? paged::launch_f32(plain, p->d, ws, nullptr, nullptr, nullptr, s)
+                                : paged::launch_f32(a, p->d, ws, more.carry, more.gates, pws, s));
 }
 
 path_status check_window(int window, int sinks) {

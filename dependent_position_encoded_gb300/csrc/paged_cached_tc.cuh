@@ -265,7 +265,7 @@ __device__ __forceinline__ bool tile_whole(int pos0, int n, unsigned have, int b
 
 template <int NT, int D, bool FOX, Pass M>
 __global__ void __launch_bounds__(CachedCfg<NT, D, M>::threads, CachedCfg<NT, D, M>::ctas_per_sm)
-tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap tm_x,
+tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtensorMap tm_x,
                  const __grid_constant__ CUtensorMap tm_l, const __grid_constant__ CUtensorMap tm_m,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
     using L = CachedCfg<NT, D, M>;
@@ -321,9 +321,10 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
     auto stretch_of = [&](Walk &walk, long long at) {
         return L::ahead ? walk.at(a, plan, D, NT, at, u_end) : Walk().at(a, plan, D, NT, at, u_end);
     };
+    const int window = window_of(a), sinks = sinks_of(a);
     // what the first new token sees, the first position of a stretch's step i, and whether the page of
     // the lane's box at j is wanted
-    auto sight = [&](const Stretch &t) { return WIN ? sight_of(a, t.s) : Sight{0, 0}; };
+    auto sight = [&](const Stretch &t) { return sight_of(a, t.s); };
     auto pos_of = [&](const Stretch &t, const Sight &seen, int i) {
         return 128 * (WIN ? seen.tile(t.k0 + i, t.s.n, 128) : t.k0 + i);
     };
@@ -779,8 +780,8 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
             if (L::rows_in_tmem && !L::single) load_rows(t);
             // a window: the row sees the keys from `from` on (and the sinks); `edge`: where all rows' do
             const Sight seen = sight(t);
-            const int from = WIN ? t.s.n + 1 - a.window + (live ? (row0 + rw) / G : 0) : 0;
-            const int edge = WIN && a.window > 0 ? t.s.n + t.s.T - a.window : 0;
+            const int from = WIN ? t.s.n + 1 - window + (live ? (row0 + rw) / G : 0) : 0;
+            const int edge = WIN && window > 0 ? t.s.n + t.s.T - window : 0;
             float m_run = -INFINITY, l_run = 0.f;
             int kid1, vid1;  // the pages of the next tile's boxes
             auto look_up = [&](int pos0) {
@@ -869,7 +870,7 @@ tc_cached_kernel(const Step a, const TcWs y, const __grid_constant__ CUtensorMap
                             }
                         }
                         if (WIN && pos0 + c < edge) {
-                            const int over = a.sinks - pos0 - c, under = from - pos0 - c;
+                            const int over = sinks - pos0 - c, under = from - pos0 - c;
 #pragma unroll
                             for (int q = 0; q < 32; ++q) x[q] = q < over || q >= under ? x[q] : -INFINITY;
                         }
@@ -1082,7 +1083,7 @@ cudaError_t big_smem(K kern, size_t bytes) {
 }  // namespace
 
 template <int NT, int D, bool FOX, Pass M>
-cudaError_t launch_cached(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream) {
+cudaError_t launch_cached(const StepOf<M> &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream) {
     CUtensorMap tx, tl, tm, tk, tv;
     // a map has no empty axis; of an empty pool nothing is loaded, every page number is outside it
     auto heads = [&](int pages) { return (long long)std::max(pages, 1) * a.c.Hkv; };
@@ -1103,7 +1104,7 @@ cudaError_t launch_cached(const Step &a, const TcWs &y, uint64_t limit_ns, cudaS
     WHAT(1, 64, false, M) WHAT(2, 64, false, M) WHAT(1, 128, false, M) WHAT(2, 128, false, M)   \
     WHAT(1, 64, true, M) WHAT(2, 64, true, M) WHAT(1, 128, true, M) WHAT(2, 128, true, M)
 #define PASS(NT, D, FOX, M) \
-    template cudaError_t launch_cached<NT, D, FOX, M>(const Step &, const TcWs &, uint64_t, cudaStream_t);
+    template cudaError_t launch_cached<NT, D, FOX, M>(const StepMore &, const TcWs &, uint64_t, cudaStream_t);
 #define EXTERN_PASS(NT, D, FOX, M) extern PASS(NT, D, FOX, M)
 #define ONE_PASS(WHAT) \
     WHAT(1, 64, false, Pass::one) WHAT(1, 128, false, Pass::one) WHAT(1, 64, true, Pass::one) WHAT(1, 128, true, Pass::one)

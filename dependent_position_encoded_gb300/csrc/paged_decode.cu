@@ -66,10 +66,11 @@ __device__ __forceinline__ uint4 ld16(const T *p) {
     return *reinterpret_cast<const uint4 *>(p);
 }
 
-// WIN: the splits' positions are those in sight, numbered through (Sight::position).
-template <typename T, bool FOX, int D, int G, bool WIN>
+// StepMore: the splits' positions are those in sight, numbered through (Sight::position).
+template <typename T, bool FOX, int D, int G, typename A>
 __global__ void __launch_bounds__(kThreads, G == 4 ? 2 : 3)
-paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part) {
+paged_decode_split(const A a, int chunk, int nsplit, float *__restrict__ part) {
+    constexpr bool WIN = std::is_same<A, StepMore>::value;
     constexpr int E = Row<T>::E;
     constexpr int TPK = D / E;     // lanes per key
     constexpr int KPW = 32 / TPK;  // keys per warp pass
@@ -81,7 +82,7 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
     const int sp = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     grid_begin();  // the first of the call: nothing to wait for
     const Seq s = seq_of(a, b);
-    const Sight seen = WIN ? sight_of(a, s) : Sight{0, 0};
+    const Sight seen = sight_of(a, s);
     const int j0 = sp * chunk, j1 = min(j0 + chunk, WIN ? seen.count(s.n) : s.n);
     if (s.T != 1 || j0 >= j1) return;  // the merge skips the splits past the end
     const int shift = a.c.page_shift, pmask = a.c.page - 1;
@@ -286,10 +287,10 @@ paged_decode_split(const Step a, int chunk, int nsplit, float *__restrict__ part
 
 // D threads per (query head, sequence): score the new token, merge the splits and, for the
 // first query head of a key head, append the new key and value.
-// BEHIND: sequences with prefixes, whose parts are joined too.
-template <typename T, bool FOX, int D, bool BEHIND>
+// StepMore: sequences may have prefixes, whose parts are joined too.
+template <typename T, bool FOX, int D, typename A>
 __global__ void __launch_bounds__(D)
-paged_decode_merge(const Step a, const Behind z, int chunk, int nsplit, const float *part) {
+paged_decode_merge(const A a, const Behind z, int chunk, int nsplit, const float *part) {
     __shared__ float red[D / 32];
     const int hq = blockIdx.x, b = blockIdx.y, c = threadIdx.x;
     grid_begin();
@@ -335,47 +336,45 @@ paged_decode_merge(const Step a, const Behind z, int chunk, int nsplit, const fl
         Ls += pp[i * (D + 2) + 1] * f;
         Oc += pp[i * (D + 2) + 2 + c] * f;
     }
-    if (BEHIND && std::is_same<T, __nv_bfloat16>::value && __ldg(z.of + b) >= 0) {
-        // the keys of the sequence's prefix
-        const RowParts x = parts_behind(a, z, b, h, 0, hq % a.c.G);
-        float top = M;
+    if constexpr (std::is_same<A, StepMore>::value)
+        if (a.prefix_of != nullptr && __ldg(a.prefix_of + b) >= 0) {  // the keys of the sequence's prefix
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                const RowParts x = parts_behind(a, z, b, h, 0, hq % a.c.G);
+                float top = M;
 #pragma unroll 8
-        for (int q = 0; q < x.number; ++q) top = fmaxf(top, x.sml[x.at(q)].x);
-        const float f0 = exp2f(M - top);
-        Ls *= f0;
-        Oc *= f0;
+                for (int q = 0; q < x.number; ++q) top = fmaxf(top, x.sml[x.at(q)].x);
+                const float f0 = exp2f(M - top);
+                Ls *= f0;
+                Oc *= f0;
 #pragma unroll 8
-        for (int q = 0; q < x.number; ++q) {
-            const float2 ml = x.sml[x.at(q)];
-            const float f = exp2f(ml.x - top);
-            Ls = fmaf(ml.y, f, Ls);
-            Oc = fmaf(x.so[x.at(q) * D + c], f, Oc);
+                for (int q = 0; q < x.number; ++q) {
+                    const float2 ml = x.sml[x.at(q)];
+                    const float f = exp2f(ml.x - top);
+                    Ls = fmaf(ml.y, f, Ls);
+                    Oc = fmaf(x.so[x.at(q) * D + c], f, Oc);
+                }
+            } else {
+                const size_t row = ((size_t)h * a.N + s.first) * a.c.G + hq % a.c.G;
+                const float2 ml = a.pxml[row];
+                const float top = fmaxf(M, ml.x), f0 = exp2f(M - top), f1 = exp2f(ml.x - top);
+                Ls = fmaf(ml.y, f1, Ls * f0);
+                Oc = fmaf(a.px[row * D + c], f1, Oc * f0);
+            }
         }
-    }
-    if (BEHIND && std::is_same<T, float>::value && __ldg(a.prefix_of + b) >= 0) {
-        const size_t row = ((size_t)h * a.N + s.first) * a.c.G + hq % a.c.G;
-        const float2 ml = a.pxml[row];
-        const float top = fmaxf(M, ml.x), f0 = exp2f(M - top), f1 = exp2f(ml.x - top);
-        Ls = fmaf(ml.y, f1, Ls * f0);
-        Oc = fmaf(a.px[row * D + c], f1, Oc * f0);
-    }
     static_cast<T *>(a.out)[s.first * a.so.tok + hq * a.so.head + c] = Elt<T>::from_f(Oc / Ls);
 }
 
-template <typename T, bool FOX, int D, int G>
-cudaError_t launch_g(const Step &a, const Behind &x, int chunk, int nsplit, float *part, cudaStream_t stream) {
+template <typename T, bool FOX, int D, int G, typename A>
+cudaError_t launch_g(const A &a, const Behind &x, int chunk, int nsplit, float *part, cudaStream_t stream) {
     if (nsplit > 0) {
-        const cudaError_t e = launch(a.window > 0 ? paged_decode_split<T, FOX, D, G, true>
-                                                  : paged_decode_split<T, FOX, D, G, false>,
-                                     dim3(nsplit, a.c.Hkv, a.c.seqs), kThreads, 0, stream, true, a, chunk, nsplit, part);
+        const cudaError_t e = launch(paged_decode_split<T, FOX, D, G, A>, dim3(nsplit, a.c.Hkv, a.c.seqs), kThreads, 0, stream, true, a, chunk, nsplit, part);
         if (e != cudaSuccess) return e;
     }
-    return launch(a.prefix_of != nullptr ? paged_decode_merge<T, FOX, D, true> : paged_decode_merge<T, FOX, D, false>,
-                  dim3(a.c.Hq, a.c.seqs), D, 0, stream, nsplit == 0, a, x, chunk, nsplit, part);
+    return launch(paged_decode_merge<T, FOX, D, A>, dim3(a.c.Hq, a.c.seqs), D, 0, stream, nsplit == 0, a, x, chunk, nsplit, part);
 }
 
-template <typename T, bool FOX, int D>
-cudaError_t launch_d(const Step &a, const Behind &x, int chunk, int nsplit, float *part, cudaStream_t stream) {
+template <typename T, bool FOX, int D, typename A>
+cudaError_t launch_d(const A &a, const Behind &x, int chunk, int nsplit, float *part, cudaStream_t stream) {
     switch (a.c.G) {
         case 1: return launch_g<T, FOX, D, 1>(a, x, chunk, nsplit, part, stream);
         case 2: return launch_g<T, FOX, D, 2>(a, x, chunk, nsplit, part, stream);
@@ -407,7 +406,8 @@ size_t decode_part_bytes(const Cache &c, int d) {
 }
 
 // behind: of a bf16 step with prefixes, their parts
-cudaError_t launch_decode(const Step &a, int d, bool bf16, const Behind *behind, float *part, cudaStream_t stream) {
+template <typename A>
+cudaError_t launch_decode(const A &a, int d, bool bf16, const Behind *behind, float *part, cudaStream_t stream) {
     const Behind x = behind != nullptr ? *behind : Behind{};
     const long long cap = most_seen(a);
     const int chunk = decode_chunk(a.c, cap), nsplit = (int)((cap + chunk - 1) / chunk);
@@ -422,6 +422,9 @@ cudaError_t launch_decode(const Step &a, int d, bool bf16, const Behind *behind,
     };
     return bf16 ? pick(__nv_bfloat16{}) : pick(0.f);
 }
+
+template cudaError_t launch_decode(const Step &, int, bool, const Behind *, float *, cudaStream_t);
+template cudaError_t launch_decode(const StepMore &, int, bool, const Behind *, float *, cudaStream_t);
 
 }  // namespace paged
 }  // namespace path

@@ -33,8 +33,8 @@ namespace {
 template <int D>
 constexpr size_t prep_smem() { return ((size_t)(4 * (D / 64) + 4) * TILE + 6 * kC) * 4 + 2 * kC * 8; }
 
-template <int D>
-__global__ void __launch_bounds__(kThr) f32_prep_kernel(const Step a, const Ws y) {
+template <int D, typename AnyStep>
+__global__ void __launch_bounds__(kThr) f32_prep_kernel(const AnyStep a, const Ws y) {
     constexpr int NH = D / 64;
     extern __shared__ float sm[];
     float *W = sm, *K = W + NH * TILE, *U = K + NH * TILE, *Q = U + NH * TILE, *A = Q + NH * TILE,
@@ -224,8 +224,8 @@ constexpr size_t scan_smem() {
     return ((size_t)(3 * (D / 64) + (D / 64) * (D / 64) + 1) * TILE + 5 * kC) * 4;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThr) f32_scan_kernel(const Step a, const Ws y) {
+template <int D, typename AnyStep>
+__global__ void __launch_bounds__(kThr) f32_scan_kernel(const AnyStep a, const Ws y) {
     constexpr int NH = D / 64;
     extern __shared__ float sm[];
     float *X = sm, *K = X + NH * TILE, *V = K + NH * TILE, *P = V + NH * TILE, *S = P + NH * NH * TILE,
@@ -312,8 +312,8 @@ __global__ void __launch_bounds__(kThr) f32_scan_kernel(const Step a, const Ws y
 
 // ---------------------------------------------------------------- combine
 // One warp per row, eight parts' rows in flight at a time; grid (slots, Hq, 8).
-template <int D>
-__global__ void __launch_bounds__(kThr) f32_combine_kernel(const Step a, const Ws y) {
+template <int D, typename AnyStep>
+__global__ void __launch_bounds__(kThr) f32_combine_kernel(const AnyStep a, const Ws y) {
     constexpr int E = D / 32;
     const int slot = blockIdx.x, hq = blockIdx.y, lane = threadIdx.x & 31;
     const int r = blockIdx.z * 8 + (threadIdx.x >> 5);
@@ -359,14 +359,15 @@ __global__ void __launch_bounds__(kThr) f32_combine_kernel(const Step a, const W
             for (int e = 0; e < E; ++e) O[e] = fmaf(v[i][e], f, O[e]);
         }
     }
-    if (a.px != nullptr && __ldg(a.prefix_of + b) >= 0) {  // the keys of the sequence's prefix
-        const size_t at = ((size_t)(hq / a.c.G) * a.N + s.first + c * kC + r) * a.c.G + hq % a.c.G;
-        const float2 ml = a.pxml[at];
-        const float top = fmaxf(M, ml.x), f0 = exp2f(M - top), f1 = exp2f(ml.x - top);
-        L = fmaf(ml.y, f1, L * f0);
+    if constexpr (std::is_same<AnyStep, StepMore>::value)
+        if (a.px != nullptr && __ldg(a.prefix_of + b) >= 0) {  // the keys of the sequence's prefix
+            const size_t at = ((size_t)(hq / a.c.G) * a.N + s.first + c * kC + r) * a.c.G + hq % a.c.G;
+            const float2 ml = a.pxml[at];
+            const float top = fmaxf(M, ml.x), f0 = exp2f(M - top), f1 = exp2f(ml.x - top);
+            L = fmaf(ml.y, f1, L * f0);
 #pragma unroll
-        for (int e = 0; e < E; ++e) O[e] = fmaf(a.px[at * D + lane * E + e], f1, O[e] * f0);
-    }
+            for (int e = 0; e < E; ++e) O[e] = fmaf(a.px[at * D + lane * E + e], f1, O[e] * f0);
+        }
     float *dst = static_cast<float *>(a.out) + (long long)(s.first + c * kC + r) * a.so.tok + hq * a.so.head + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) dst[e] = O[e] / L;
@@ -377,8 +378,8 @@ template <int D>
 constexpr size_t carry_smem() { return (size_t)(D / 64 + (D / 64) * (D / 64)) * TILE * 4; }
 
 // Items of a key head: the slots, then D / 64 row tiles of the identity per sequence.
-template <int D>
-__global__ void __launch_bounds__(kThr) f32_carry_kernel(const Step a, const Ws y, int nslots) {
+template <int D, typename AnyStep>
+__global__ void __launch_bounds__(kThr) f32_carry_kernel(const AnyStep a, const Ws y, int nslots) {
     constexpr int NH = D / 64;
     extern __shared__ float sm[];
     float *Y = sm, *P = Y + NH * TILE;
@@ -456,8 +457,8 @@ constexpr size_t transform_smem() { return (size_t)(D / 64 + (D / 64) * (D / 64)
 
 // grid (parts, key heads, sequences): a CTA keeps P in shared memory and takes every parts-th
 // tile of 64 cached keys.
-template <int D>
-__global__ void __launch_bounds__(kThr) f32_transform_kernel(const Step a, const Ws y) {
+template <int D, typename AnyStep>
+__global__ void __launch_bounds__(kThr) f32_transform_kernel(const AnyStep a, const Ws y) {
     constexpr int NH = D / 64;
     extern __shared__ float sm[];
     float *K = sm, *P = K + NH * TILE;
@@ -510,42 +511,42 @@ __global__ void __launch_bounds__(kThr) f32_transform_kernel(const Step a, const
 }
 
 // What a step's own tokens give: the blocks' factors, and the queries carried to the chunk's start.
-template <int D>
-cudaError_t launch_blocks(const Step &a, const Ws &y, cudaStream_t stream) {
+template <int D, typename AnyStep>
+cudaError_t launch_blocks(const AnyStep &a, const Ws &y, cudaStream_t stream) {
     const int nslots = slots_of(a.N, a.c.seqs), Hq = a.c.Hq, Hkv = a.c.Hkv;
     cudaError_t e;
-    if ((e = big_smem(f32_prep_kernel<D>, prep_smem<D>())) != cudaSuccess ||
-        (e = big_smem(f32_scan_kernel<D>, scan_smem<D>())) != cudaSuccess)
+    if ((e = big_smem(f32_prep_kernel<D, AnyStep>, prep_smem<D>())) != cudaSuccess ||
+        (e = big_smem(f32_scan_kernel<D, AnyStep>, scan_smem<D>())) != cudaSuccess)
         return e;
     // while half of the SMs would be idle, a CTA for the keys and others for the query heads
     const int room = 152 / (nslots * Hkv), z = room < 2 ? 1 : 1 + (room - 1 < a.c.G ? room - 1 : a.c.G);
-    e = launch(f32_prep_kernel<D>, dim3(nslots, Hkv, z), kThr, prep_smem<D>(), stream, true, a, y);
+    e = launch(f32_prep_kernel<D, AnyStep>, dim3(nslots, Hkv, z), kThr, prep_smem<D>(), stream, true, a, y);
     if (e == cudaSuccess && a.max_chunk > kC)
-        e = launch(f32_scan_kernel<D>, dim3(nslots, Hq), kThr, scan_smem<D>(), stream, false, a, y);
+        e = launch(f32_scan_kernel<D, AnyStep>, dim3(nslots, Hq), kThr, scan_smem<D>(), stream, false, a, y);
     return e;
 }
 
 // The cached keys, the outputs and the cache.
-template <int D>
-cudaError_t launch_cache(const Step &a, const Ws &y, cudaStream_t stream) {
+template <int D, typename AnyStep>
+cudaError_t launch_cache(const AnyStep &a, const Ws &y, cudaStream_t stream) {
     const int nslots = slots_of(a.N, a.c.seqs), Hq = a.c.Hq, Hkv = a.c.Hkv;
     cudaError_t e;
-    if ((e = big_smem(f32_cached_kernel<D, false>, cached_smem<D>())) != cudaSuccess ||
-        (e = big_smem(f32_carry_kernel<D>, carry_smem<D>())) != cudaSuccess ||
-        (e = big_smem(f32_transform_kernel<D>, transform_smem<D>())) != cudaSuccess)
+    if ((e = big_smem(f32_cached_kernel<D, false, AnyStep>, cached_smem<D>())) != cudaSuccess ||
+        (e = big_smem(f32_carry_kernel<D, AnyStep>, carry_smem<D>())) != cudaSuccess ||
+        (e = big_smem(f32_transform_kernel<D, AnyStep>, transform_smem<D>())) != cudaSuccess)
         return e;
     const long long cap = most_seen(a);
-    e = launch(f32_cached_kernel<D, false>, dim3(nslots, Hq, y.splits), kThr, cached_smem<D>(), stream, false, a, y);
+    e = launch(f32_cached_kernel<D, false, AnyStep>, dim3(nslots, Hq, y.splits), kThr, cached_smem<D>(), stream, false, a, y);
     if (e == cudaSuccess)
-        e = launch(f32_combine_kernel<D>, dim3(nslots, Hq, kC / 8), kThr, 0, stream, false, a, y);
+        e = launch(f32_combine_kernel<D, AnyStep>, dim3(nslots, Hq, kC / 8), kThr, 0, stream, false, a, y);
     if (e == cudaSuccess)
-        e = launch(f32_carry_kernel<D>, dim3(nslots + a.c.seqs * (D / 64), Hkv), kThr, carry_smem<D>(), stream, false,
+        e = launch(f32_carry_kernel<D, AnyStep>, dim3(nslots + a.c.seqs * (D / 64), Hkv), kThr, carry_smem<D>(), stream, false,
                    a, y, nslots);
     // CTAs of 64 cached keys, or of several where that makes more than four to an SM
     long long parts = 4 * 152 / ((long long)Hkv * a.c.seqs) + 1;
     if (parts > (cap + kC - 1) / kC) parts = (cap + kC - 1) / kC;
     if (e == cudaSuccess && parts > 0)
-        e = launch(f32_transform_kernel<D>, dim3((unsigned)parts, Hkv, a.c.seqs), kThr, transform_smem<D>(), stream,
+        e = launch(f32_transform_kernel<D, AnyStep>, dim3((unsigned)parts, Hkv, a.c.seqs), kThr, transform_smem<D>(), stream,
                    false, a, y);
     return e;
 }
@@ -590,9 +591,10 @@ F32Layout f32_layout(const Cache &c, int N, int d, bool fox) {
 bool decode_takes(int G);
 size_t decode_part_bytes(const Cache &c, int d);
 struct Behind;
-cudaError_t launch_decode(const Step &a, int d, bool bf16, const Behind *behind, float *part, cudaStream_t stream);
+template <typename A>
+cudaError_t launch_decode(const A &a, int d, bool bf16, const Behind *behind, float *part, cudaStream_t stream);
 
-cudaError_t launch_prefix_f32(Step &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws, bool first,
+cudaError_t launch_prefix_f32(StepMore &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws, bool first,
                               cudaStream_t stream);
 
 size_t f32_ws_bytes(const Cache &c, int N, int d, bool fox) {
@@ -600,7 +602,8 @@ size_t f32_ws_bytes(const Cache &c, int N, int d, bool fox) {
 }
 
 // carry: of a step with prefixes (gates, and pws, the workspace's part for them, likewise)
-cudaError_t launch_f32(Step a, int d, void *ws, float *carry, float *gates, void *pws, cudaStream_t stream) {
+template <typename A>
+cudaError_t launch_f32(A a, int d, void *ws, float *carry, float *gates, void *pws, cudaStream_t stream) {
     const F32Layout f = f32_layout(a.c, a.N, d, a.log_f != nullptr);
     char *w = static_cast<char *>(ws);
     auto at = [&](size_t off) { return reinterpret_cast<float *>(w + off); };
@@ -615,13 +618,17 @@ cudaError_t launch_f32(Step a, int d, void *ws, float *carry, float *gates, void
     cudaError_t e = cudaSuccess;
     if (carry != nullptr) {  // before any joining
         e = blocks();
-        if (e == cudaSuccess) e = launch_prefix_f32(a, d, carry, gates, y.qt, y.gq, pws, false, stream);
+        if constexpr (std::is_same<A, StepMore>::value)
+            if (e == cudaSuccess) e = launch_prefix_f32(a, d, carry, gates, y.qt, y.gq, pws, false, stream);
     }
     if (e == cudaSuccess && singles) e = launch_decode(a, d, false, nullptr, at(f.total), stream);
     if (e == cudaSuccess && carry == nullptr) e = blocks();
     if (e != cudaSuccess) return e;
     return d == 64 ? launch_cache<64>(a, y, stream) : launch_cache<128>(a, y, stream);
 }
+
+template cudaError_t launch_f32(Step, int, void *, float *, float *, void *, cudaStream_t);
+template cudaError_t launch_f32(StepMore, int, void *, float *, float *, void *, cudaStream_t);
 
 }  // namespace paged
 }  // namespace path

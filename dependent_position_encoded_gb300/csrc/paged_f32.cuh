@@ -130,7 +130,8 @@ __device__ __forceinline__ void load_tokens(float *dst, const void *src, Stride 
 
 // The page numbers of the slots of 64 cached positions from j0 (-1: bad, or nothing there is in
 // sight); returns the first slot.
-__device__ __forceinline__ int find_pages(const Step &a, int *ids, const int *table, int pool, int b, int j0, int n,
+template <typename A>
+__device__ __forceinline__ int find_pages(const A &a, int *ids, const int *table, int pool, int b, int j0, int n,
                                           const Sight &seen) {
     const int slot0 = j0 >> a.c.page_shift, last = (min(j0 + kC, n) - 1) >> a.c.page_shift, i = threadIdx.x;
     if (i <= last - slot0)
@@ -232,8 +233,8 @@ template <int D>
 constexpr size_t cached_smem() { return ((size_t)(3 * (D / 64) + 1) * TILE + 4 * kC) * 4 + 16 * 4; }
 
 // SHARED: over the keys of prefixes (paged_prefix.cuh), whose rows are placed by a kernel of this call.
-template <int D, bool SHARED>
-__global__ void __launch_bounds__(kThr) f32_cached_kernel(const Step a, const Ws y) {
+template <int D, bool SHARED, typename A>
+__global__ void __launch_bounds__(kThr) f32_cached_kernel(const A a, const Ws y) {
     constexpr int NH = D / 64;
     extern __shared__ float sm[];
     float *X = sm, *K = X + NH * TILE, *V = K + NH * TILE, *S = V + NH * TILE, *m = S + TILE,
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kThr) f32_cached_kernel(const Step a, const Ws
 #pragma unroll
     for (int x = 0; x < NH; ++x) zero(o[x]);
     // a window: row i of the block sees the positions from `from` + i on, and the sinks
-    const int from = s.n + c * kC + 1 - a.window, past = a.window > 0 ? a.sinks : INT_MAX;
+    const int from = s.n + c * kC + 1 - window_of(a), past = window_of(a) > 0 ? sinks_of(a) : INT_MAX;
     for (int t = t0; t < t1; ++t) {
         const int j = kC * seen.tile(t, s.n, kC);
         __syncthreads();

@@ -37,7 +37,7 @@ constexpr int kPrefixThr = 256;
 // so that no more than N tokens are placed. visit(b, p, T): what thread b % kPrefixThr finds of sequence b,
 // p < 0 where it has no place; every thread of the CTA calls it in each round.
 template <typename V>
-__device__ __forceinline__ void each_sequence(const Step &a, const int *of, int *sums, V visit) {
+__device__ __forceinline__ void each_sequence(const StepMore &a, const int *of, int *sums, V visit) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = a.c.seqs;
     int top = 0;
     for (int base = 0; base < S; base += kPrefixThr) {
@@ -67,7 +67,7 @@ __device__ __forceinline__ void each_sequence(const Step &a, const int *of, int 
 }
 
 // The plan, by one CTA: x.cu and x.start.
-__device__ __forceinline__ void place_tokens(const Step &a, const Prefix &x) {
+__device__ __forceinline__ void place_tokens(const StepMore &a, const Prefix &x) {
     __shared__ int row[kPrefixThr], tokens[kPrefixThr], sums[kPrefixThr / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = a.c.seqs;
     for (int p = tid; p <= S; p += kPrefixThr) x.cu[p] = 0;
@@ -113,7 +113,7 @@ __device__ __forceinline__ void place_tokens(const Step &a, const Prefix &x) {
 
 // What the plan gives sequence b, by a CTA of its own: the tokens of the prefixes before its own, and of the
 // sequences before it. -1: it has no place.
-__device__ __forceinline__ int place_one(const Step &a, const Prefix &x, int mine) {
+__device__ __forceinline__ int place_one(const StepMore &a, const Prefix &x, int mine) {
     __shared__ int sums[kPrefixThr / 32], total, found;
     const int tid = threadIdx.x, of = __ldg(x.of + mine);
     int before = 0;
@@ -131,8 +131,8 @@ __device__ __forceinline__ int place_one(const Step &a, const Prefix &x, int min
 }
 
 // The step whose sequences are the prefixes.
-inline Step shared_step(const Step &a, const Prefix &x) {
-    Step v = a;
+inline StepMore shared_step(const StepMore &a, const Prefix &x) {
+    StepMore v = a;
     v.cu = x.cu;
     v.max_chunk = a.N;
     v.window = v.sinks = 0;
@@ -147,7 +147,7 @@ inline Step shared_step(const Step &a, const Prefix &x) {
 // carry's update from one read of the carry, all in fp32. Eight lanes share a row of C, 16 bytes each at
 // a time. put(g, i, x): entry i of query head g's carried query; gate(g, x): its gates.
 template <typename T, int D, typename P, typename F>
-__device__ __forceinline__ void prefix_single(const Step &a, const Prefix &x, const Seq &s, int b, int h, P put,
+__device__ __forceinline__ void prefix_single(const StepMore &a, const Prefix &x, const Seq &s, int b, int h, P put,
                                               F gate) {
     constexpr int NC = D / 32, NR = D / 32, kHeads = 16;  // columns / 32 of a row, rows / 32 of C
     __shared__ __align__(16) float ws[D], qs[kHeads][D], os[kHeads][D];
@@ -234,7 +234,7 @@ __device__ __forceinline__ void prefix_single(const Step &a, const Prefix &x, co
 constexpr int kCarryThr = 128, kCarryPer = 4, kCarryRows = kCarryThr / 8 * kCarryPer, kCarryTokens = 32, kCarryBlock = 8;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kCarryThr) prefix_carry_kernel(const Step a, const Prefix x) {
+__global__ void __launch_bounds__(kCarryThr) prefix_carry_kernel(const StepMore a, const Prefix x) {
     constexpr int NC = D / 32, B = kCarryBlock, NB = kCarryTokens / B;
     constexpr int E = 16 / sizeof(T), PER = D / E, IT = kCarryTokens * PER / kCarryThr, LD = D + 4;
     __shared__ __align__(16) float ws[kCarryTokens][LD];  // (rows begin in different banks)
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kCarryThr) prefix_carry_kernel(const Step a, c
 }
 
 template <typename T, int D>
-cudaError_t launch_prefix_carry(const Step &a, const Prefix &x, cudaStream_t stream) {
+cudaError_t launch_prefix_carry(const StepMore &a, const Prefix &x, cudaStream_t stream) {
     if (a.max_chunk <= 1) return cudaSuccess;
     return launch(prefix_carry_kernel<T, D>, dim3(D / kCarryRows, a.c.Hkv, a.c.seqs), kCarryThr, 0, stream, false, a, x);
 }

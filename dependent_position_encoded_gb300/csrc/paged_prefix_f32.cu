@@ -10,7 +10,7 @@ namespace {
 
 static_assert(kThr == kPrefixThr, "place_tokens");
 
-__global__ void __launch_bounds__(kThr) prefix_plan_f32_kernel(const Step a, const Prefix x) {
+__global__ void __launch_bounds__(kThr) prefix_plan_f32_kernel(const StepMore a, const Prefix x) {
     grid_begin();
     place_tokens(a, x);
     grid_wait();  // what it writes is this call's alone
@@ -34,7 +34,7 @@ constexpr size_t query_smem() { return (size_t)2 * (D / 64) * TILE * 4; }
 // 64 tokens of a query head, X C^T, or all heads of a key head of a sequence's only token; y: the step's,
 // z: those of the shared step.
 template <int D>
-__global__ void __launch_bounds__(kThr) prefix_query_f32_kernel(const Step a, const Prefix x, const Ws y, const Ws z) {
+__global__ void __launch_bounds__(kThr) prefix_query_f32_kernel(const StepMore a, const Prefix x, const Ws y, const Ws z) {
     constexpr int NH = D / 64;
     extern __shared__ float sm[];
     float *const X = sm, *const C = X + NH * TILE;
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThr) prefix_query_f32_kernel(const Step a, co
 // ---------------------------------------------------------------- join
 // A warp per row: the parts of its prefix's keys into one; grid (slots, Hq, 8).
 template <int D>
-__global__ void __launch_bounds__(kThr) prefix_join_f32_kernel(const Step a, const Step v, const Prefix x, const Ws z) {
+__global__ void __launch_bounds__(kThr) prefix_join_f32_kernel(const StepMore a, const StepMore v, const Prefix x, const Ws z) {
     constexpr int E = D / 32;
     const int slot = blockIdx.x, hq = blockIdx.y, lane = threadIdx.x & 31, r = blockIdx.z * 8 + (threadIdx.x >> 5);
     int b, c;
@@ -115,18 +115,18 @@ __global__ void __launch_bounds__(kThr) prefix_join_f32_kernel(const Step a, con
 }
 
 template <int D>
-cudaError_t launch_all(const Step &a, const Prefix &x, const Ws &y, const Ws &z, bool first, cudaStream_t stream) {
-    const Step v = shared_step(a, x);
+cudaError_t launch_all(const StepMore &a, const Prefix &x, const Ws &y, const Ws &z, bool first, cudaStream_t stream) {
+    const StepMore v = shared_step(a, x);
     const int nslots = slots_of(a.N, a.c.seqs);
     cudaError_t e;
     if ((e = big_smem(prefix_query_f32_kernel<D>, query_smem<D>())) != cudaSuccess ||
-        (e = big_smem(f32_cached_kernel<D, true>, cached_smem<D>())) != cudaSuccess)
+        (e = big_smem(f32_cached_kernel<D, true, StepMore>, cached_smem<D>())) != cudaSuccess)
         return e;
     e = launch(prefix_plan_f32_kernel, dim3(1), kThr, 0, stream, first, a, x);
     if (e == cudaSuccess)
         e = launch(prefix_query_f32_kernel<D>, dim3(nslots, a.c.Hq), kThr, query_smem<D>(), stream, false, a, x, y, z);
     if (e == cudaSuccess)
-        e = launch(f32_cached_kernel<D, true>, dim3(nslots, a.c.Hq, z.splits), kThr, cached_smem<D>(), stream, false, v,
+        e = launch(f32_cached_kernel<D, true, StepMore>, dim3(nslots, a.c.Hq, z.splits), kThr, cached_smem<D>(), stream, false, v,
                    z);
     if (e == cudaSuccess)
         e = launch(prefix_join_f32_kernel<D>, dim3(nslots, a.c.Hq, kC / 8), kThr, 0, stream, false, a, v, x, z);
@@ -135,7 +135,7 @@ cudaError_t launch_all(const Step &a, const Prefix &x, const Ws &y, const Ws &z,
 }
 
 // The workspace's part for prefixes, from `w` on.
-size_t layout(const Step &a, int d, char *w, Prefix *x, Ws *z) {
+size_t layout(const StepMore &a, int d, char *w, Prefix *x, Ws *z) {
     const Cache &c = a.c;
     const size_t rows = (size_t)a.N * c.G * c.Hkv, slots = slots_of(a.N, c.seqs), blocks = slots * c.Hq;
     const long long cap = (long long)c.max_pages << c.page_shift, most = (cap + 63) / 64,
@@ -161,7 +161,7 @@ size_t layout(const Step &a, int d, char *w, Prefix *x, Ws *z) {
 
 }  // namespace
 
-size_t prefix_f32_bytes(const Step &a, int d) {
+size_t prefix_f32_bytes(const StepMore &a, int d) {
     Prefix x;
     Ws z;
     return layout(a, d, nullptr, &x, &z);
@@ -169,7 +169,7 @@ size_t prefix_f32_bytes(const Step &a, int d) {
 
 // y_qt, y_gq: the step's queries carried to the chunk's start and their gates, null where it has single
 // tokens alone (theirs are formed from the inputs).
-cudaError_t launch_prefix_f32(Step &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws, bool first,
+cudaError_t launch_prefix_f32(StepMore &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws, bool first,
                               cudaStream_t stream) {
     Prefix x;
     Ws z = {};

@@ -21,7 +21,7 @@ static_assert(kThr == kPrefixThr, "make_plans");
 constexpr int kFused = 1024;
 
 template <int D, bool OWN, bool BEHIND>
-__global__ void __launch_bounds__(kThr) tc_single_kernel(const Step a, const Step v, const Prefix x, const TcWs y,
+__global__ void __launch_bounds__(kThr) tc_single_kernel(const StepMore a, const StepMore v, const Prefix x, const TcWs y,
                                                          const TcWs z, int plans, bool fused) {
     __shared__ long long sums[2 * kThr / 32];
     const int G = a.c.G;
@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(kThr) tc_single_kernel(const Step a, const Ste
 }
 
 template <int D, bool OWN, bool BEHIND>
-cudaError_t launch_tokens(const Step &a, const Prefix &x, const TcWs &y, const TcWs &z, bool first, cudaStream_t stream) {
-    const Step v = BEHIND ? shared_step(a, x) : a;
+cudaError_t launch_tokens(const StepMore &a, const Prefix &x, const TcWs &y, const TcWs &z, bool first, cudaStream_t stream) {
+    const StepMore v = BEHIND ? shared_step(a, x) : a;
     const int items = a.c.seqs * a.c.Hkv, plans = (OWN ? 1 : 0) + (BEHIND ? 1 : 0);
     const auto kern = tc_single_kernel<D, OWN, BEHIND>;
     if (!BEHIND || a.c.seqs <= kFused)
@@ -85,7 +85,7 @@ struct QuerySmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThr, 2) prefix_query_kernel(const Step a, const Prefix x, const TcWs y, const TcWs z) {
+__global__ void __launch_bounds__(kThr, 2) prefix_query_kernel(const StepMore a, const Prefix x, const TcWs y, const TcWs z) {
     using S = QuerySmem<D>;
     constexpr int LDD = S::LDD, NT = D / 16, PER = D / 8, IT = kC * PER / kThr;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -153,15 +153,15 @@ __global__ void __launch_bounds__(kThr, 2) prefix_query_kernel(const Step a, con
 
 // The attention of the prefixes' sequences, behind their queries.
 template <int D, bool FOX>
-cudaError_t launch_shared(const Step &a, const Prefix &x, const TcWs &z, uint64_t limit_ns, cudaStream_t stream) {
-    const Step v = shared_step(a, x);
+cudaError_t launch_shared(const StepMore &a, const Prefix &x, const TcWs &z, uint64_t limit_ns, cudaStream_t stream) {
+    const StepMore v = shared_step(a, x);
     const cudaError_t e = launch_cached<1, D, FOX, Pass::shared>(v, z, limit_ns, stream);
     if (e != cudaSuccess || (long long)a.N * a.c.G <= 128) return e;
     return launch_cached<2, D, FOX, Pass::shared>(v, z, limit_ns, stream);
 }
 
 template <int D, bool FOX>
-cudaError_t launch_all(const Step &a, const Prefix &x, const TcWs *y, const TcWs &z, bool first, uint64_t limit_ns,
+cudaError_t launch_all(const StepMore &a, const Prefix &x, const TcWs *y, const TcWs &z, bool first, uint64_t limit_ns,
                        cudaStream_t stream) {
     cudaError_t e = launch_tokens<D, false, true>(a, x, z, z, first, stream);
     if (a.max_chunk > 1) {
@@ -177,7 +177,7 @@ cudaError_t launch_all(const Step &a, const Prefix &x, const TcWs *y, const TcWs
 
 // A step of single tokens, through a window or behind prefixes, up to its joining.
 template <int D, bool FOX>
-cudaError_t launch_ones(const Step &a, const Prefix *x, const TcWs &y, const TcWs &z, uint64_t limit_ns,
+cudaError_t launch_ones(const StepMore &a, const Prefix *x, const TcWs &y, const TcWs &z, uint64_t limit_ns,
                         cudaStream_t stream) {
     cudaError_t e = x != nullptr ? launch_tokens<D, true, true>(a, *x, y, z, true, stream)
                                  : launch_tokens<D, true, false>(a, Prefix{}, y, z, true, stream);
@@ -187,7 +187,7 @@ cudaError_t launch_ones(const Step &a, const Prefix *x, const TcWs &y, const TcW
 }
 
 // The workspace's part for prefixes, from the byte `off` on: plan, queries, parts of the shared step.
-size_t layout(const Step &a, int d, char *w, Prefix *x, TcWs *z) {
+size_t layout(const StepMore &a, int d, char *w, Prefix *x, TcWs *z) {
     const Cache &c = a.c;
     const size_t rows = (size_t)a.N * c.G * c.Hkv;
     size_t off = 0;
@@ -218,7 +218,7 @@ size_t layout(const Step &a, int d, char *w, Prefix *x, TcWs *z) {
 
 }  // namespace
 
-size_t prefix_tc_bytes(const Step &a, int d) {
+size_t prefix_tc_bytes(const StepMore &a, int d) {
     Prefix x;
     TcWs z;
     return layout(a, d, nullptr, &x, &z);
@@ -226,7 +226,7 @@ size_t prefix_tc_bytes(const Step &a, int d) {
 
 namespace {
 
-Prefix prefix_at(const Step &a, int d, float *carry, float *gates, void *ws, TcWs *z, Behind *behind) {
+Prefix prefix_at(const StepMore &a, int d, float *carry, float *gates, void *ws, TcWs *z, Behind *behind) {
     Prefix x = {};
     layout(a, d, static_cast<char *>(ws), &x, z);
     x.of = a.prefix_of;
@@ -240,7 +240,7 @@ Prefix prefix_at(const Step &a, int d, float *carry, float *gates, void *ws, TcW
 
 // y: the step's workspace, null for single tokens alone, whose queries are formed from the inputs;
 // behind: what the step's joining takes up
-cudaError_t launch_prefix_tc(const Step &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
+cudaError_t launch_prefix_tc(const StepMore &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
                              uint64_t limit_ns, Behind *behind, cudaStream_t stream) {
     TcWs z = {};
     const Prefix x = prefix_at(a, d, carry, gates, ws, &z, behind);
@@ -250,7 +250,7 @@ cudaError_t launch_prefix_tc(const Step &a, int d, float *carry, float *gates, c
     return fox ? all(launch_all<128, true>) : all(launch_all<128, false>);
 }
 
-cudaError_t launch_singles(const Step &a, int d, const TcWs &y, float *carry, float *gates, void *ws, uint64_t limit_ns,
+cudaError_t launch_singles(const StepMore &a, int d, const TcWs &y, float *carry, float *gates, void *ws, uint64_t limit_ns,
                            Behind *behind, cudaStream_t stream) {
     TcWs z = {};
     Prefix x = {};

@@ -1,0 +1,15 @@
+// The kernels of paged_prep_tc.cuh for steps through a window or behind prefixes.
+#include "paged_prep_tc.cuh"
+
+namespace path {
+namespace paged {
+
+template cudaError_t launch_tc_prep<64>(const StepMore &, const TcWs &, cudaStream_t);
+template cudaError_t launch_tc_prep<128>(const StepMore &, const TcWs &, cudaStream_t);
+template cudaError_t launch_tc_carry<64>(const StepMore &, const TcWs &, cudaStream_t);
+template cudaError_t launch_tc_carry<128>(const StepMore &, const TcWs &, cudaStream_t);
+template cudaError_t launch_tc_finish<64>(const StepMore &, const TcWs &, const Behind &, cudaStream_t);
+template cudaError_t launch_tc_finish<128>(const StepMore &, const TcWs &, const Behind &, cudaStream_t);
+
+}  // namespace paged
+}  // namespace path

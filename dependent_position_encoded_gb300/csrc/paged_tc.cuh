@@ -6,6 +6,8 @@
 // one behind the other, R = N G of them.
 #pragma once
 
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace path {
@@ -81,14 +83,18 @@ __host__ __device__ __forceinline__ bool one_tile(int T, int G, int D, bool fox)
 // Whether queries carried to the chunk's start are left in two parts: for the cached keys' pass, or to
 // be carried on to a prefix.
 __device__ __forceinline__ bool low_queries(const Step &a, int T, int D) {
+    return keeps_low(one_tile(T, a.c.G, D, a.log_f != nullptr) ? 1 : 2, D);
+}
+__device__ __forceinline__ bool low_queries(const StepMore &a, int T, int D) {
     return a.prefix_of != nullptr || keeps_low(one_tile(T, a.c.G, D, a.log_f != nullptr) ? 1 : 2, D);
 }
 
 // Row tiles and key tiles of a sequence in the plan of NT (0 where it goes with the other).
-__device__ __forceinline__ void plan_of(const Step &a, const Seq &s, int D, int NT, int &tiles, int &ktiles) {
+template <typename A>
+__device__ __forceinline__ void plan_of(const A &a, const Seq &s, int D, int NT, int &tiles, int &ktiles) {
     const int G = a.c.G, rows = s.T * G;  // T G <= N G, which the host keeps within an int
     ktiles = sight_of(a, s).tiles(s.n, 128);
-    const bool one = a.shared ? rows <= 128 : one_tile(s.T, G, D, a.log_f != nullptr);
+    const bool one = enters(a) ? one_tile(s.T, G, D, a.log_f != nullptr) : rows <= 128;
     tiles = one == (NT == 1) ? (rows + 128 * NT - 1) / (128 * NT) : 0;
 }
 
@@ -110,7 +116,8 @@ struct Walk {
     long long u0 = 0, u1 = -1, items = 0;  // the sequence's units and its first item
     Seq s;
     int b, tiles, kt;
-    __device__ __forceinline__ Stretch at(const Step &a, const Plan &p, int D, int NT, long long u, long long end) {
+    template <typename A>
+    __device__ __forceinline__ Stretch at(const A &a, const Plan &p, int D, int NT, long long u, long long end) {
         if (u >= u1) {
             int lo = 0, hi = a.c.seqs - 1;  // the last sequence with units[b] <= u: it has units
             while (lo < hi) {
@@ -146,8 +153,8 @@ constexpr int kThr = 256;  // threads of a CTA of the kernels beside the attenti
 // buffers hold what sequences without common tokens can need, so one that begins before an
 // earlier one's begin or end (cu_tokens falls somewhere, which the falling sequence reports) gets
 // no work: with m the largest cu_tokens so far, a sequence counts where cu_tokens = m.
-template <int D>
-__device__ __forceinline__ void make_plans(const Step &a, const TcWs &y, long long *sums) {
+template <int D, typename A>
+__device__ __forceinline__ void make_plans(const A &a, const TcWs &y, long long *sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int *const tops = reinterpret_cast<int *>(sums + kThr / 32);
     long long run[4] = {0, 0, 0, 0};
@@ -206,8 +213,8 @@ __device__ __forceinline__ void make_plans(const Step &a, const TcWs &y, long lo
 
 // A sequence's only token: H = I - beta w w^T, q~ = q - beta (w . q) w, and the token's own key
 // and value enter the cache as they are. A warp per query head in turns.
-template <int D>
-__device__ __forceinline__ void enter_single(const Step &a, const TcWs &y, const Seq &s, int b, int slot, int h) {
+template <int D, typename A>
+__device__ __forceinline__ void enter_single(const A &a, const TcWs &y, const Seq &s, int b, int slot, int h) {
     using bf = __nv_bfloat16;
     constexpr int E = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.c.G, kw = kThr / 32;
@@ -309,7 +316,8 @@ __device__ __forceinline__ RowParts parts_of(const Y &y, int seqs, int rows, int
     return x;
 }
 // The parts of sequence b's row of new token t and query head g of key head h with its prefix.
-__device__ __forceinline__ RowParts parts_behind(const Step &a, const Behind &x, int b, int h, int t, int g) {
+template <typename A>
+__device__ __forceinline__ RowParts parts_behind(const A &a, const Behind &x, int b, int h, int t, int g) {
     const int start = x.start[b];
     if (start < 0) return RowParts{};
     const int p = __ldg(x.of + b), first = x.cu[p], rows = (x.cu[p + 1] - first) * a.c.G;
@@ -322,7 +330,8 @@ __device__ __forceinline__ RowParts parts_behind(const Step &a, const Behind &x,
 __host__ __device__ __forceinline__ int tile_slots(int N, int G, int seqs, int rows) {
     return (int)((long long)N * G / rows) + seqs;
 }
-__device__ __forceinline__ bool tile_of(const Step &a, int slot, int rows, int &b, int &i, Seq &s) {
+template <typename A>
+__device__ __forceinline__ bool tile_of(const A &a, int slot, int rows, int &b, int &i, Seq &s) {
     const int G = a.c.G;
     int lo = 0, hi = a.c.seqs - 1;
     while (lo < hi) {
@@ -573,8 +582,10 @@ __device__ __forceinline__ void each_pair(float (&acc)[NT][4], int m0, int n0, F
 }
 
 // (paged_cached_tc.cuh)
+template <Pass M>
+using StepOf = std::conditional_t<M == Pass::step, Step, StepMore>;
 template <int NT, int D, bool FOX, Pass M>
-cudaError_t launch_cached(const Step &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream);
+cudaError_t launch_cached(const StepOf<M> &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream);
 
 }  // namespace paged
 }  // namespace path
