@@ -473,7 +473,7 @@ cudaError_t launch_all(const A &a, const TcWs &y, const PrefixArgs &x, uint64_t 
     if constexpr (more)
         if (a.max_chunk == 1 && a.c.G <= 128) {
             TcWs one = y;
-            one.plan[0].ctas = 152 * CachedCfg<1, D, Pass::one>::ctas_per_sm;
+            one.plan[0].ctas = 152 * CachedCfg<1, D, Pass::one, FOX>::ctas_per_sm;
             e = launch_singles(a, D, one, x.carry, x.gates, x.ws, limit_ns, &behind, stream);
             return e != cudaSuccess ? e : launch_tc_finish<D>(a, one, behind, stream);
         }
@@ -516,7 +516,7 @@ TcLayout tc_layout(const Cache &c, int N, int max_chunk, int d, bool fox) {
     y.pml = take(rows * 8);
     for (int p = 0; p < 2; ++p) {
         // one CTA per SM, or two: every SM of the part (152) has its share of the units
-        y.ctas[p] = 152 * (p == 0 && d == 64 ? CachedCfg<1, 64, Pass::step>::ctas_per_sm : 1);
+        y.ctas[p] = 152 * (p == 0 && d == 64 ? CachedCfg<1, 64, Pass::step, false>::ctas_per_sm : 1);
         const bool used = p == 0 || !one_tile(max_chunk, c.G, d, fox);
         const size_t tile = 128 * (p + 1);
         const size_t parts =

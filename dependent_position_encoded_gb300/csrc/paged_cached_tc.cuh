@@ -87,16 +87,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr));
 }
 
-// one column of the thread's row
-__device__ __forceinline__ void tmem_st1(uint32_t taddr, float x) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
-    tmem_st_wait();
-}
-__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
-    uint32_t x;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(taddr));
-    tmem_ld_wait();
-    return __uint_as_float(x);
+// `bytes` (a multiple of 16) of global memory into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 // Waits until all committed stores but the last N have finished reading shared memory.
@@ -132,6 +127,8 @@ constexpr float kRescale = 8.f;  // the running maximum may lag by 2^8 before O 
 // PaTH-FoX: how far (a power of two) below a row's maximum a weight counts for nothing, and how far
 // above its gates a logit is not expected (only what is fetched early goes by that)
 constexpr float kNothing = 64.f, kGuess = 32.f;
+// query heads of a key head whose gates come through a ring in shared memory; of more they are read in place
+constexpr int kGateHeads = 8;
 
 // ================================================================ cached keys
 // Persistent: a CTA walks its stretches of units (paged_tc.cuh), each of them one item: NT tiles
@@ -167,7 +164,7 @@ constexpr float kNothing = 64.f, kGuess = 32.f;
 // tensor core: 976 us for 2,048 tokens of 32 heads against 32,768 keys at D = 128, a quarter of it
 // the weights' second part (755 us and 1.46 PFLOP/s without; instructions take 77 to 85 cycles of the
 // 64 that they need alone).
-template <int NT, int D, Pass M>
+template <int NT, int D, Pass M, bool FOX>
 struct CachedCfg {
     static constexpr uint32_t tile = 128 * D * 2, atom = 128 * 128;
     // The rows' tiles, their high parts and then (keeps_low) their low ones; for NT = 1 at D = 128,
@@ -181,21 +178,27 @@ struct CachedCfg {
     static constexpr bool duo = NT == 1 && D == 128 && M == Pass::shared, two_s = duo || single;
     // the next stretch is looked up, and its rows fetched, before the last one's end
     static constexpr bool ahead = NT == 1 && !matrix;
-    static constexpr bool rows_in_tmem = single || (update && D == 128), low = keeps_low(NT, D);
+    // gates come through a ring of their own, of up to kGateHeads query heads
+    static constexpr bool ring = FOX && ahead;
+    static constexpr bool rows_in_tmem = ahead || (update && D == 128), low = keeps_low(NT, D);
     static constexpr uint32_t X = 0, xbytes = rows_in_tmem ? 0 : NT * (low ? 2 : 1) * tile;
     static constexpr uint32_t P = X + xbytes, pbytes = matrix ? 2 * D * D * 2 : 0;
     // slots of keys and of values: what fits beside; for NT = 1 and D = 64 so that two CTAs share
     // an SM. With NT = 1 a key slot is held until the updated keys have left it.
     static constexpr int NK = matrix ? (D == 64 ? 2 : 3)
-                              : single ? (D == 64 ? 8 : 4) : NT == 1 ? 3 : (D == 64 ? 4 : 3);
-    static constexpr int NV = single ? (D == 64 ? 5 : 3) : NT == 1 ? 2 : (D == 64 ? 4 : 2);
+                              : NT == 2 ? (D == 64 ? 4 : 3)
+                                        : (single && D == 64 ? 8 : 4) - (ring ? 1 : 0);
+    static constexpr int NV = matrix ? 2 : NT == 2 ? (D == 64 ? 4 : 2) : single && D == 64 ? 5 : 3;
+    static constexpr int NG = ring ? (single || D == 128 ? 4 : 3) : 0, NG_ = ring ? NG : 1;
     static constexpr uint32_t K = P + pbytes, V = K + NK * tile, bars = V + NV * tile;
     static constexpr int KF = 0, KE = NK, VF = 2 * NK, VE = VF + NV, XF = VE + NV, XE = XF + 1, SF = XE + 1,
                          PR = SF + 2, FIN = PR + 2, DF = FIN + 2, DE = DF + NK, TMP = DE + 1, END = TMP + 2,
-                         XT = END + 2, EX = XT + 1, PD = EX + 1, count = PD + 1;
-    // behind the barriers: TMEM's address and the abort flag; single: the token's w, two of them
+                         XT = END + 2, EX = XT + 1, PD = EX + 1, GF = PD + 1, GE = GF + NG, count = GE + NG;
+    // behind the barriers: TMEM's address and the abort flag; single: the token's w, two of them; duo: what the
+    // halves of a row tell each other, two turns of it; the ring of gates
     static constexpr uint32_t W = (bars + count * 8 + 16 + 15) / 16 * 16;  // read 16 bytes at a time
-    static constexpr uint32_t bytes = W + (single ? 2 * D * 4 : 0);  // from a 1024-byte boundary
+    static constexpr uint32_t gates = W + (single ? 2 * D * 4 : duo ? 2 * 256 * 4 : 0), gslot = kGateHeads * 128 * 4;
+    static constexpr uint32_t bytes = gates + NG * gslot;  // from a 1024-byte boundary
     // warps: those of the rows, the update's, then the others from `other` on
     static constexpr int other = update || duo || NT == 2 ? 8 : 4, threads = 32 * (other + 4);
     static constexpr int ctas_per_sm = NT == 1 && D == 64 && !single ? 2 : 1;
@@ -204,24 +207,26 @@ struct CachedCfg {
     static constexpr bool split = NT == 2 || (matrix && D == 64);
     static constexpr int reg_row = NT == 2 ? 200 : 104, reg_update = 72, reg_other = NT == 2 ? 104 : 64;
     // TMEM columns: per row tile S 128 (the weights over it) and O; NT = 1: the update's product, or the
-    // rows' two parts, or (duo) what the halves of a row tell each other
+    // rows' two parts
     static constexpr uint32_t cS = 0, cO = 128, per_tile = 256, cD = 128 + D, cX = D == 64 ? 192 : 384;
     static constexpr uint32_t cS2 = 256;  // two_s: the odd steps' logits and weights
     static constexpr uint32_t cols = NT == 1 && D == 64 && !single ? 256 : 512;
 };
-template <Pass M>
+template <Pass M, bool FOX>
 struct CachedFits {
-    using A = CachedCfg<1, 64, M>;
-    using B = CachedCfg<2, 64, M>;
-    static_assert(CachedCfg<1, 128, M>::bytes <= 227 * 1024 && CachedCfg<2, 128, M>::bytes <= 227 * 1024 &&
+    using A = CachedCfg<1, 64, M, FOX>;
+    using B = CachedCfg<2, 64, M, FOX>;
+    static_assert(CachedCfg<1, 128, M, FOX>::bytes <= 227 * 1024 && CachedCfg<2, 128, M, FOX>::bytes <= 227 * 1024 &&
                       A::bytes <= 227 * 1024 && A::ctas_per_sm * (A::bytes + 1024) <= 228 * 1024,
                   "shared memory");
     static_assert(256 * B::reg_row + 128 * B::reg_other <= 384 * 168, "registers");
     static_assert(128 * (A::reg_row + A::reg_update + A::reg_other) <= 384 * 80, "registers");
 };
-template struct CachedFits<Pass::step>;
-template struct CachedFits<Pass::one>;
-template struct CachedFits<Pass::shared>;
+template struct CachedFits<Pass::step, false>;
+template struct CachedFits<Pass::one, false>;
+template struct CachedFits<Pass::one, true>;
+template struct CachedFits<Pass::shared, false>;
+template struct CachedFits<Pass::shared, true>;
 
 template <int N>
 __device__ __forceinline__ void reg_inc() {
@@ -264,11 +269,11 @@ __device__ __forceinline__ bool tile_whole(int pos0, int n, unsigned have, int b
 }
 
 template <int NT, int D, bool FOX, Pass M>
-__global__ void __launch_bounds__(CachedCfg<NT, D, M>::threads, CachedCfg<NT, D, M>::ctas_per_sm)
+__global__ void __launch_bounds__(CachedCfg<NT, D, M, FOX>::threads, CachedCfg<NT, D, M, FOX>::ctas_per_sm)
 tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtensorMap tm_x,
                  const __grid_constant__ CUtensorMap tm_l, const __grid_constant__ CUtensorMap tm_m,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
-    using L = CachedCfg<NT, D, M>;
+    using L = CachedCfg<NT, D, M, FOX>;
     constexpr bool WIN = M == Pass::window || M == Pass::one;
     constexpr int NA = D / 64, NK = L::NK, NV = L::NV, kLow = low_weights(NT, D, FOX);
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -295,10 +300,10 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
         // four warps (duo: eight): weights written, update's product read; both issuing threads (NT = 1):
         // rows' tile free, keys read by their products; both row tiles (NT = 2): keys and values read
         for (int i = 0; i < L::count; ++i) {
-            const bool four = (i >= L::PR && i < L::FIN) || i == L::DE || i == L::XT || i == L::EX;
+            const bool four = (i >= L::PR && i < L::FIN) || i == L::DE || i == L::XT || i == L::EX || i >= L::GE;
             const bool both = NT == 1 ? L::matrix && ((i == L::XE && !L::rows_in_tmem) || (i >= L::DF && i < L::DE))
                                       : (i >= L::KE && i < L::VF) || (i >= L::VE && i < L::XF);
-            mbar_init(bar(i), four ? (L::duo ? 8u : 4u) : both ? 2u : 1u);
+            mbar_init(bar(i), four ? (L::duo && i != L::XT ? 8u : 4u) : both ? 2u : 1u);
         }
         fence_mbar_init();
     }
@@ -347,7 +352,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
             for (long long at = u_begin; ok && at < u_end; ++seg) {
                 const Stretch t = stretch_of(walk, at);
                 at += t.steps;
-                if (keys && !L::single) {
+                if (keys && !L::ahead) {
                     // the rows' tile (and the update's product) once the last stretch's are read
                     if (seg > 0 && !(ok = wait.warp(bar(L::XE), (seg - 1) & 1))) break;
                     if (lane == 0) {
@@ -388,7 +393,10 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                     const uint32_t sl = j % ring, turn = j / ring;
                     if (turn > 0 && !(ok = wait.warp(bar(empty0 + sl), (turn - 1) & 1))) break;
                     const uint32_t dst = keys ? key_slot(j) : value_slot(j);
-                    const uint32_t full = bar(full0 + sl), target = whole ? full : tmp;
+                    // (ahead: keys that are none need not be zero, their logits are masked and nothing of them
+                    // is written)
+                    const bool direct = whole || (L::ahead && keys);
+                    const uint32_t full = bar(full0 + sl), target = direct ? full : tmp;
                     if (lane == 0) mbar_arrive_expect_tx(target, (uint32_t)__popc(have) * box * D * 2);
                     __syncwarp();
                     if (id >= 0)
@@ -396,7 +404,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                         for (int x = 0; x < NA; ++x)
                             tma_load_3d(dst + x * L::atom + lane * box * 128, keys ? &tm_k : &tm_v, target, 64 * x,
                                         (pos0 + lane * box) & (page - 1), id * a.c.Hkv + t.h);
-                    if (!whole) {
+                    if (!direct) {
                         // zero the rows that hold no cached position or one that no new token sees, then
                         // hand the slot on
                         if (!(ok = wait.warp(tmp, tmp_phase))) break;
@@ -425,7 +433,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
             if (!ok) {
                 for (uint32_t v = j > ring ? j - ring : 0; v < j; ++v)
                     mbar_wait(bar(full0 + v % ring), (v / ring) & 1, limit_ns);
-                if (keys && !L::single) mbar_wait(bar(L::XF), seg & 1, limit_ns);
+                if (keys && !L::ahead) mbar_wait(bar(L::XF), seg & 1, limit_ns);
             }
         } else if (lane == 0 && warp == L::other) {
             // ======================================================== S and P V
@@ -539,6 +547,36 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
             // every product has completed before TMEM is freed
             umma_commit(bar(L::END));
             mbar_wait(bar(L::END), 0, limit_ns);
+        } else if (L::ring && G <= kGateHeads && warp == L::other + 3) {
+            // ======================================================== gates into their ring
+            uint32_t j = 0;
+            bool ok = true;
+            Walk walk;
+            for (long long at = u_begin; ok && at < u_end;) {
+                const Stretch t = stretch_of(walk, at);
+                at += t.steps;
+                const Sight seen = sight(t);
+                for (int i = 0; i < t.steps; ++i, ++j) {
+                    const int pos0 = pos_of(t, seen, i);
+                    int id = -1;
+                    if (box_in(t, seen, pos0 + lane * box))
+                        id = page_of(a, a.c.k_table, t.b, (pos0 + lane * box) >> a.c.page_shift, a.c.nk);
+                    const unsigned have = __ballot_sync(0xffffffffu, id >= 0);
+                    const uint32_t sl = j % L::NG_, turn = j / L::NG_;
+                    if (turn > 0 && !(ok = wait.warp(bar(L::GE + sl), (turn - 1) & 1))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(L::GF + sl), (uint32_t)__popc(have) * box * G * 4);
+                    __syncwarp();
+                    if (id >= 0)
+                        for (int g = 0; g < G; ++g)
+                            bulk_load(base + L::gates + sl * L::gslot + (g * 128 + lane * box) * 4,
+                                      a.c.g_pages + (((size_t)id * a.c.Hq + t.h * G + g) << a.c.page_shift) +
+                                          ((pos0 + lane * box) & (page - 1)),
+                                      box * 4, bar(L::GF + sl));
+                }
+            }
+            if (!ok)  // on an abort: as above
+                for (uint32_t v = j > L::NG_ ? j - L::NG_ : 0; v < j; ++v)
+                    mbar_wait(bar(L::GF + v % L::NG_), (v / L::NG_) & 1, limit_ns);
         } else if (L::matrix && lane == 0 && warp == L::other + 3) {
             // ======================================================== K (P - I), NT = 1
             constexpr uint32_t ID_D = idesc_b16(128, D, true);
@@ -725,10 +763,10 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
             tc_fence_after();
         };
         auto exchange = [&](float x) {
-            const uint32_t at = tm + L::cX + 2 * (turn & 3);
-            tmem_st1(at + half, x);
+            float *const at = reinterpret_cast<float *>(sm + L::W) + (turn & 1) * 256 + r;
+            at[128 * half] = x;
             meet();
-            return tmem_ld1(at + 1 - half);
+            return at[128 * (1 - half)];
         };
         // the row's two parts into tensor memory (the last products of the stretch before have ended)
         auto load_rows = [&](const Stretch &t) {
@@ -758,7 +796,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
         };
         Stretch next;
         if (L::ahead) next = stretch_of(walk, u_begin);
-        if (L::single) load_rows(next);
+        if (L::ahead && half == 0) load_rows(next);
         for (long long at = u_begin; ok && at < u_end;) {
             const Stretch t = L::ahead ? next : stretch_of(walk, at);
             at += t.steps;
@@ -774,10 +812,11 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
             const bool halves = L::duo && cp < 2, idle = L::duo && cp == 2 && half == 1;
             const int cols = 128 >> (cp + (halves ? 1 : 0)), c_begin = c_copy + (halves ? half * cols : 0);
             const bool live = row0 + rw < rows_all, warp_live = row0 + (rw & ~31) < rows_all;
-            const int hq = t.h * G + (live ? (row0 + rw) % G : 0);
+            const int head = live ? (row0 + rw) % G : 0, hq = t.h * G + head;
+            const bool staged = L::ring && G <= kGateHeads;
             const float gq =
                 FOX && live ? y.gq[(size_t)t.h * y.R + (size_t)t.s.first * G + row0 + rw] * kLog2e : 0.f;
-            if (L::rows_in_tmem && !L::single) load_rows(t);
+            if (L::rows_in_tmem && !L::ahead) load_rows(t);
             // a window: the row sees the keys from `from` on (and the sinks); `edge`: where all rows' do
             const Sight seen = sight(t);
             const int from = WIN ? t.s.n + 1 - window + (live ? (row0 + rw) / G : 0) : 0;
@@ -806,6 +845,13 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                 const bool whole = tile_whole(pos0, t.s.n, have, box_shift);
                 // gate sums of 32 keys from column c for the row's query head
                 auto gates_of = [&](int c, float4 *v) {
+                    if (staged) {
+                        const float4 *const gp = reinterpret_cast<const float4 *>(
+                            sm + L::gates + (j % L::NG_) * L::gslot + (head * 128 + c) * 4);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) v[q] = gp[q];
+                        return;
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; e += 4) {  // 16 positions lie in one page
                         const int bx = (c + 4 * e) >> box_shift;
@@ -820,12 +866,12 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                 };
                 // on their way while the product runs: in registers where there are enough for the 32
                 // columns of a copy, else into L1
-                constexpr bool kAhead = FOX && NT == 1 && D == 128;
+                constexpr bool kAhead = FOX && NT == 1 && D == 128 && !L::ahead;
                 float4 ahead[kAhead ? 8 : 1];
                 const bool early = kAhead && cols == 32;
                 if (early) {
                     gates_of(c_begin, ahead);
-                } else if (FOX) {
+                } else if (FOX && !staged) {
 #pragma unroll 1
                     for (int c = c_begin; c < c_begin + cols; c += 16) {
                         const int bx = c >> box_shift, pid = __shfl_sync(0xffffffffu, id, bx);
@@ -839,6 +885,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                 const uint32_t cS = L::cS + (L::two_s ? place * L::cS2 : 0);
                 if (!(ok = wait.warp(bar(L::SF + place), (L::two_s ? phases >> place : j) & 1))) break;
                 if (L::two_s) phases ^= 1u << place;
+                if (staged && !(ok = wait.warp(bar(L::GF + j % L::NG_), (j / L::NG_) & 1))) break;
                 tc_fence_after();
                 if (releases && !L::two_s) {
                     if (!L::update) release(L::KE, step % NK);
@@ -1013,11 +1060,12 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                 }
                 tc_fence_before();
                 mbar_arrive_warp(bar(L::PR + place));
+                if (staged) mbar_arrive_warp(bar(L::GE + j % L::NG_));
             }
             // the next stretch's rows while the last product of values runs
             if (L::ahead && ok && at < u_end) {
                 next = stretch_of(walk, at);
-                if (L::single) load_rows(next);
+                if (half == 0) load_rows(next);
             }
             if (!ok || !(ok = wait.warp(bar(L::FIN + w), seg & 1))) break;
             ++seg;
@@ -1092,7 +1140,7 @@ cudaError_t launch_cached(const StepOf<M> &a, const TcWs &y, uint64_t limit_ns, 
         !make_map(&tk, a.c.k_pages, D, a.c.page, heads(a.c.nk), a.c.page < 128 ? a.c.page : 128) ||
         !make_map(&tv, a.c.v_pages, D, a.c.page, heads(a.c.nv), a.c.page < 128 ? a.c.page : 128))
         return cudaErrorInvalidValue;
-    using L = CachedCfg<NT, D, M>;
+    using L = CachedCfg<NT, D, M, FOX>;
     auto kern = tc_cached_kernel<NT, D, FOX, M>;
     const cudaError_t e = big_smem(kern, L::bytes);
     if (e != cudaSuccess) return e;

@@ -143,17 +143,18 @@ inline StepMore shared_step(const StepMore &a, const Prefix &x) {
     return v;
 }
 
-// A sequence's only token, one CTA per key head: its queries carried to the prefix's end and the
-// carry's update from one read of the carry, all in fp32. Eight lanes share a row of C, 16 bytes each at
-// a time. put(g, i, x): entry i of query head g's carried query; gate(g, x): its gates.
-template <typename T, int D, typename P, typename F>
-__device__ __forceinline__ void prefix_single(const StepMore &a, const Prefix &x, const Seq &s, int b, int h, P put,
-                                              F gate) {
-    constexpr int NC = D / 32, NR = D / 32, kHeads = 16;  // columns / 32 of a row, rows / 32 of C
-    __shared__ __align__(16) float ws[D], qs[kHeads][D], os[kHeads][D];
+// A sequence's only token and a key head: its queries carried to the prefix's end and the carry's
+// update from one read of the carry, all in fp32, by a CTA for `R` rows of C from `row0` on (they do not
+// meet; that of row 0 sees to the gates). Eight lanes share a row, 16 bytes each at a time. put(g, i, x):
+// entry i of query head g's carried query; gate(g, x): its gates.
+template <typename T, int D, int R, typename P, typename F>
+__device__ __forceinline__ void prefix_single(const StepMore &a, const Prefix &x, const Seq &s, int b, int h, int row0,
+                                              P put, F gate) {
+    constexpr int NC = D / 32, NR = R / 32, kHeads = 16;  // columns / 32 of a row, rows / 32
+    __shared__ __align__(16) float ws[D], qs[kHeads][D], os[kHeads][R];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.c.G;
     const int sub = lane & 7, r0 = tid >> 3;
-    float4 *const C = reinterpret_cast<float4 *>(x.carry + ((size_t)b * a.c.Hkv + h) * D * D);
+    float4 *const C = reinterpret_cast<float4 *>(x.carry + (((size_t)b * a.c.Hkv + h) * D + row0) * D);
     float4 c[NR][NC];
 #pragma unroll
     for (int i = 0; i < NR; ++i)
@@ -203,7 +204,7 @@ __device__ __forceinline__ void prefix_single(const StepMore &a, const Prefix &x
                 if (sub == 0) os[g][r0 + 32 * i] = z;
             }
         __syncthreads();
-        for (int e = tid; e < some * D; e += kPrefixThr) put(g0 + e / D, e % D, os[e / D][e % D]);
+        for (int e = tid; e < some * R; e += kPrefixThr) put(g0 + e / R, row0 + e % R, os[e / R][e % R]);
     }
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
@@ -216,7 +217,7 @@ __device__ __forceinline__ void prefix_single(const StepMore &a, const Prefix &x
                             fmaf(-z, f.w, c[i][k].w));
         }
     }
-    if (a.log_f != nullptr)
+    if (a.log_f != nullptr && row0 == 0)
         for (int g = tid; g < G; g += kPrefixThr) {
             float *const p = x.gates + (size_t)b * a.c.Hq + h * G + g;
             const float t = *p + a.log_f[(long long)s.first * a.sf.tok + (long long)(h * G + g) * a.sf.head];

@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(kThr) prefix_query_f32_kernel(const StepMore a
     if (s.T == 1) {
         if (hq % a.c.G != 0) return;
         const size_t at = place_of(x, b, p, 0);
-        prefix_single<float, D>(
-            a, x, s, b, h, [&](int g, int i, float q) { z.qt[row_of(at, a.c.Hq, h * a.c.G + g) * D + i] = q; },
+        prefix_single<float, D, D>(
+            a, x, s, b, h, 0, [&](int g, int i, float q) { z.qt[row_of(at, a.c.Hq, h * a.c.G + g) * D + i] = q; },
             [&](int g, float t) { z.gq[row_of(at, a.c.Hq, h * a.c.G + g)] = t; });
         return;
     }

@@ -14,7 +14,7 @@ static_assert(kThr == kPrefixThr, "make_plans");
 
 // ---------------------------------------------------------------- plans and single tokens
 // The first CTA makes the plan of the prefixes, the next one (OWN) that of the step, the others take the
-// single tokens, a sequence and key head each: OWN, of a step that has no others, enter them into
+// single tokens, a sequence and key head each (BEHIND: and 64 rows of its carry): OWN, of a step that has no others, enter them into
 // the cache and leave their queries and parts; BEHIND, carry their queries to the prefix's end. With up
 // to kFused sequences these find their places by themselves beside the plan, else by one made before
 // (plan: by a launch of this kernel with no sequence).
@@ -37,17 +37,23 @@ __global__ void __launch_bounds__(kThr) tc_single_kernel(const StepMore a, const
         grid_wait();
         return;
     }
-    const int item = blockIdx.x - plans, h = item % a.c.Hkv, b = item / a.c.Hkv;
+    constexpr int kParts = BEHIND ? D / 64 : 1;
+    const int item = (blockIdx.x - plans) / kParts, part = (blockIdx.x - plans) % kParts;
+    const int h = item % a.c.Hkv, b = item / a.c.Hkv;
     if (!fused) grid_wait();
     const Seq s = seq_of(a, b);
     if (s.T == 1) {
         int start = -1;
+        // the carry's rows are on their way while the place is looked for
+        if (BEHIND && (int)threadIdx.x < 64 * D * 4 / 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(x.carry + (((size_t)b * a.c.Hkv + h) * D + 64 * part) * D +
+                                                          threadIdx.x * 32));
         if (BEHIND && __ldg(x.of + b) >= 0) start = fused ? place_one(a, x, b) : x.start[b];
-        if (OWN) enter_single<D>(a, y, s, b, slot_of(s, b, 0), h);
+        if (OWN && part == 0) enter_single<D>(a, y, s, b, slot_of(s, b, 0), h);
         if (BEHIND && start >= 0) {
             const size_t to = (size_t)h * z.R + (size_t)start * G;
-            prefix_single<bf, D>(
-                a, x, s, b, h,
+            prefix_single<bf, D, 64>(
+                a, x, s, b, h, 64 * part,
                 [&](int g, int i, float q) {
                     q *= a.scale_log2;
                     const bf hi = __float2bfloat16_rn(q);
@@ -63,7 +69,7 @@ __global__ void __launch_bounds__(kThr) tc_single_kernel(const StepMore a, const
 template <int D, bool OWN, bool BEHIND>
 cudaError_t launch_tokens(const StepMore &a, const Prefix &x, const TcWs &y, const TcWs &z, bool first, cudaStream_t stream) {
     const StepMore v = BEHIND ? shared_step(a, x) : a;
-    const int items = a.c.seqs * a.c.Hkv, plans = (OWN ? 1 : 0) + (BEHIND ? 1 : 0);
+    const int items = a.c.seqs * a.c.Hkv * (BEHIND ? D / 64 : 1), plans = (OWN ? 1 : 0) + (BEHIND ? 1 : 0);
     const auto kern = tc_single_kernel<D, OWN, BEHIND>;
     if (!BEHIND || a.c.seqs <= kFused)
         return launch(kern, dim3(plans + items), kThr, 0, stream, first, a, v, x, y, z, plans, true);
@@ -202,7 +208,7 @@ size_t layout(const StepMore &a, int d, char *w, Prefix *x, TcWs *z) {
     z->ql = reinterpret_cast<bf *>(take(rows * d * 2));
     z->gq = reinterpret_cast<float *>(take(rows * 4));
     for (int p = 0; p < 2; ++p) {
-        const int ctas = 152;  // one a SM
+        const int ctas = 152 * (p == 0 && d == 64 ? CachedCfg<1, 64, Pass::shared, false>::ctas_per_sm : 1);
         const size_t tile = 128 * (p + 1);
         // (both plans in any case: the sizes must not fall as the step grows)
         const size_t parts = ctas + (size_t)tile_slots(a.N, c.G, c.seqs < a.N ? c.seqs : a.N, (int)tile) * c.Hkv;
