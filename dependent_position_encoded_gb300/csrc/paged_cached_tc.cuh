@@ -330,8 +330,11 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
     // what the first new token sees, the first position of a stretch's step i, and whether the page of
     // the lane's box at j is wanted
     auto sight = [&](const Stretch &t) { return sight_of(a, t.s); };
+    // (gates, but for a plain step: from the last tile to the first, since a row's maximum then comes early
+    // and its sums seldom have to follow it)
     auto pos_of = [&](const Stretch &t, const Sight &seen, int i) {
-        return 128 * (WIN ? seen.tile(t.k0 + i, t.s.n, 128) : t.k0 + i);
+        const int tile = FOX && M != Pass::step ? t.kt - 1 - t.k0 - i : t.k0 + i;
+        return 128 * (WIN ? seen.tile(tile, t.s.n, 128) : tile);
     };
     auto box_in = [&](const Stretch &t, const Sight &seen, int j) {
         return lane < nbox && j < t.s.n && (!WIN || seen.any(j, box));

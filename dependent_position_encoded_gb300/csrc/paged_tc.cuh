@@ -107,7 +107,7 @@ __device__ __forceinline__ long long plan_per(const Plan &p, int seqs) {
 // The stretch of units from u on that lies in one item and below `end`.
 struct Stretch {
     Seq s;
-    int b, h, tile, k0, steps;
+    int b, h, tile, k0, steps, kt;  // kt: key tiles of the item
     long long item;  // over all sequences
 };
 // One after the other: the sequence of the last one is kept, since its next key head or row tile mostly
@@ -138,6 +138,7 @@ struct Walk {
         const long long rem = u - u0;
         const int it = (int)(rem / kt);
         t.k0 = (int)(rem - (long long)it * kt);
+        t.kt = kt;
         t.h = it / tiles;
         t.tile = it - t.h * tiles;
         t.item = items + it;
