@@ -178,6 +178,12 @@ struct CachedCfg {
     static constexpr bool duo = NT == 1 && D == 128 && M == Pass::shared, two_s = duo || single;
     // the next stretch is looked up, and its rows fetched, before the last one's end
     static constexpr bool ahead = NT == 1 && !matrix;
+    // single tokens at D = 64: the thread's key stays in registers between its product with w and its update.
+    // At D = 128 and with gates it is read from its slot again: the softmax's threads have no more registers
+    // than these. (64 sequences, W = 4,096, 16 heads, D = 64: 228 us a step held, 272 read again; with gates
+    // and four query heads to a key head: 441 and 375. 16 sequences, W = 2,048, 8 key heads of four query
+    // heads, D = 128: 60 and 56, with gates 81 and 71.)
+    static constexpr bool held = single && D == 64 && !FOX;
     // gates come through a ring of their own, of up to kGateHeads query heads
     static constexpr bool ring = FOX && ahead;
     static constexpr bool rows_in_tmem = ahead || (update && D == 128), low = keeps_low(NT, D);
@@ -650,15 +656,19 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                 const bool whole = tile_whole(pos0, t.s.n, have, box_shift) && (!WIN || seen.all(pos0, 128));
                 const int mine = __shfl_sync(0xffffffffu, id, r >> box_shift);
                 uint8_t *const kt = sm + (key_slot(j) - base);
-                uint4 key[L::single ? D / 8 : 1];
+                auto key_at = [&](int c) {
+                    return reinterpret_cast<uint4 *>(kt + (c >> 3) * L::atom + sw128_offset(r, c & 7));
+                };
+                uint4 key[L::held ? D / 8 : 1];
                 float al = 0.f;  // -beta (w . k) of the thread's key
                 if (L::single) {
                     if (!(ok = wait.warp(bar(L::KF + j % NK), (j / NK) & 1))) break;
                     float2 dot[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+#pragma unroll(L::held ? D / 8 : 4)
                     for (int c = 0; c < D / 8; ++c) {
-                        key[c] = *reinterpret_cast<const uint4 *>(kt + (c >> 3) * L::atom + sw128_offset(r, c & 7));
-                        const uint32_t k4[4] = {key[c].x, key[c].y, key[c].z, key[c].w};
+                        const uint4 k8 = *key_at(c);
+                        if (L::held) key[c] = k8;
+                        const uint32_t k4[4] = {k8.x, k8.y, k8.z, k8.w};
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {
                             const float4 w4 = *reinterpret_cast<const float4 *>(wv + 8 * c + 2 * e);
@@ -677,9 +687,10 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                                            ((pos0 + r) & (page - 1))) * D
                                     : nullptr;
                 if (L::single) {
-#pragma unroll
+#pragma unroll(L::held ? D / 8 : 4)
                     for (int c = 0; c < D / 8; ++c) {
-                        const uint32_t k4[4] = {key[c].x, key[c].y, key[c].z, key[c].w};
+                        const uint4 k8 = L::held ? key[c] : *key_at(c);
+                        const uint32_t k4[4] = {k8.x, k8.y, k8.z, k8.w};
                         uint32_t o[4];
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {
@@ -691,7 +702,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                             o[e + 1] = pack_bf16x2(hi.x, hi.y);
                         }
                         const uint4 v = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (whole) *reinterpret_cast<uint4 *>(kt + (c >> 3) * L::atom + sw128_offset(r, c & 7)) = v;
+                        if (whole) *key_at(c) = v;
                         else if (dst) *reinterpret_cast<uint4 *>(dst + 8 * c) = v;
                     }
                 }
