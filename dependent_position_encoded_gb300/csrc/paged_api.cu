@@ -24,8 +24,8 @@ size_t prefix_tc_bytes(const StepMore &a, int d);
 size_t prefix_f32_bytes(const StepMore &a, int d);
 cudaError_t launch_prefix_tc(const StepMore &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
                              uint64_t limit_ns, Behind *behind, cudaStream_t stream);
-cudaError_t launch_prefix_f32(StepMore &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws, bool first,
-                              cudaStream_t stream);
+cudaError_t launch_prefix_f32(StepMore &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws,
+                              bool first, cudaStream_t stream);
 size_t pages_ws_bytes(const Cache &c);
 cudaError_t launch_reserve(const Cache &c, const int *extra, void *ws, cudaStream_t stream);
 cudaError_t launch_fork(const Cache &c, const Rows<kMaxRows> &src, const Rows<kMaxRows> &dst, int row_bytes,
@@ -98,8 +98,8 @@ path_status check_workspace(const void *ws, size_t bytes, size_t need) {
 // one-pass kernel on the CUDA cores scores them from registers and needs one launch more for
 // the join, where the block kernels need three; but it does G products per key on the CUDA cores.
 // The rule goes by what the tables can hold (query heads x positions of the whole cache, or of the
-// window and the sinks), not by the lengths, which only the device knows. Measured for bf16 with tables that are full (us, one-pass /
-// block kernels; 8 key heads, 1 to 8 sequences):
+// window and the sinks), not by the lengths, which only the device knows. Measured for bf16 plain steps
+// with tables that are full (us, one-pass / block kernels; 8 key heads, 1 to 8 sequences):
 //                        2^14       2^15       2^16       2^17       2^18       2^19       2^20      2^22
 //   G = 1, d =  64    12.5/18.5  18.6/22.6  29.7/28.5  26.0/28.7  32.8/35.5  44.3/47.5  78/73   248/210
 //              128    14.5/23.1  22.6/28.8  34.9/34.4  34.4/38.5  61.4/57.6  79.6/79.9  141/128 468/412

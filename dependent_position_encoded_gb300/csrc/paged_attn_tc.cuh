@@ -452,8 +452,8 @@ template <int D, typename A>
 cudaError_t launch_tc_finish(const A &a, const TcWs &y, const Behind &x, cudaStream_t stream);
 cudaError_t launch_prefix_tc(const StepMore &a, int d, float *carry, float *gates, const TcWs *y, void *ws, bool first,
                              uint64_t limit_ns, Behind *behind, cudaStream_t stream);
-cudaError_t launch_singles(const StepMore &a, int d, const TcWs &y, float *carry, float *gates, void *ws, uint64_t limit_ns,
-                           Behind *behind, cudaStream_t stream);
+cudaError_t launch_singles(const StepMore &a, int d, const TcWs &y, float *carry, float *gates, void *ws,
+                           uint64_t limit_ns, Behind *behind, cudaStream_t stream);
 
 namespace {
 

@@ -1,4 +1,4 @@
-// Helpers of the kernels of paged_attn_tc.cu, and the pass of carried queries over cached keys, whose
+// Helpers of the kernels of paged_attn_tc.cuh, and the pass of carried queries over cached keys, whose
 // forms (paged_tc.cuh, Pass) are compiled in files of their own.
 #pragma once
 
@@ -144,31 +144,56 @@ constexpr int kGateHeads = 8;
 // NT = 1 is for sequences whose rows fit one tile (a few tokens: bound by the cache's bytes)
 // and updates the keys too: a second MMA forms K (P - I) with the loaded keys as the A operand
 // (P - I split into two bf16 parts), and the second warpgroup adds it to the keys in shared
-// memory and stores them back, so each key is read once and written once.
+// memory and stores them back, so each key is read once and written once. That is the pass of a
+// plain step and, over the key tiles in sight, of one through a window (Pass::step, window). Two more
+// have an NT = 1 of their own, whose rows lie in TMEM and come while the stretch before ends:
+//
+// Pass::one, steps of single tokens through a window or behind prefixes. P - I is -beta w w^T, so the
+// second warpgroup forms -beta (w . k) w itself, a thread to a key: no product in TMEM and no P - I in
+// shared memory. The room goes to a second place for S, so that a tile's logits wait for the softmax and
+// not it for them, and (D = 64) to rings of eight and five slots; a key slot is given back a step after
+// its store was issued. 64 sequences, W = 4,096, 16 heads, D = 64: 219 us, 5.8 TB/s (with the product, two
+// CTAs an SM: 234, and 15 to prepare it where this takes 7); 16, W = 2,048, 8 key heads of four query heads,
+// D = 128, gates: the whole step 71 (with the product 81). Plain steps keep the product, and with it their
+// results to the bit.
+//
+// Pass::shared, the read-only pass over a prefix's keys. At D = 64 two CTAs share an SM; at D = 128, where
+// the slots leave room for one, two warpgroups share a row tile's softmax, half the columns each (they meet
+// once for the row's maximum and once before a half's weights cover the other's logits), with two places
+// for S: 4 prefixes of up to 16,384, 8 key heads of four query heads, gates, D = 128, 16 single tokens
+// behind each: 64 us, 3.4 TB/s (one warpgroup and one place: 78); at D = 64 the halves' meetings cost more
+// than they give (32 tokens behind 8,192 keys of 16 heads: 18 us, with halves 19).
+//
+// With gates these two take them from a ring in shared memory that a warp fills (up to kGateHeads query
+// heads; of more the softmax's warps read them in place): 183 us -> 176 for the whole step of the 4
+// prefixes. Their softmax is then bound by its instructions' way to the SM, which with four roles of
+// straight code come from beyond the nearest cache (no instruction there: the largest stall, 1.9 cycles
+// an issue), not by bytes: 326 us where the same step without gates takes 221 (64 sequences, W = 4,096, 16
+// key heads of four query heads, D = 64). Deeper rings, gates a tile ahead and rows padded against bank
+// conflicts changed nothing.
 //
 // With NT = 1 and at most 64 (32) rows, the tile holds two (four) copies of them and each copy's
 // softmax takes a half (quarter) of the key tile's columns, with weights of 0 in the others: the
 // warps share the row's softmax, and the copies' sums are parts to join like any others.
 //
-// Warps: 0-3 softmax of tile 0; 4-7 softmax of tile 1 (NT = 2) or the keys' update (NT = 1); 8
-// allocates TMEM and issues the MMAs of S and P V; 11 those of the update (NT = 1); 9 and 10
-// stream the key and the value pages. One thread issues both row tiles' MMAs: two of them, whose
-// products mix on the tensor core, were a sixth slower (n = 32768, T = 2048, D = 128: 1,420 us a
-// step against 1,200), and so were weights handed over in two halves (1,243).
+// Warps: 0-3 softmax of tile 0; 4-7 softmax of tile 1 (NT = 2), the keys' update (NT = 1) or the
+// softmax's second half (shared keys at D = 128; at D = 64 they have none, and the others follow from
+// 4); 8 allocates TMEM and issues the MMAs of S and P V; 11 those of the update, or fills the ring
+// of gates; 9 and 10 stream the key and the value pages. One thread issues both row tiles' MMAs: two
+// of them, whose products mix on the tensor core, were a sixth slower (n = 32768, T = 2048, D = 128:
+// 1,420 us a step against 1,200), and so were weights handed over in two halves (1,243).
 // Positions past the sequence's n and those on bad pages: the streaming warp zeroes their rows
 // after the copy, and the softmax masks them.
 //
-// NT = 1 is bound by the bytes of keys (read and written) and values: 194 us for 1.17 GB of them
-// (32 sequences of up to 8,192, 16 heads, D = 64, one token each: 6.0 TB/s), 226 us for 1.2 GB (16
-// of up to 16,384, 8 key heads of four query heads, D = 128, gates: 5.4 TB/s). NT = 2 by the
+// NT = 1 of a plain step is bound by the bytes of keys (read and written) and values: 194 us for
+// 1.17 GB of them (32 sequences of up to 8,192, 16 heads, D = 64, one token each: 6.0 TB/s), 226 us
+// for 1.2 GB (16 of up to 16,384, 8 key heads of four query heads, D = 128, gates: 5.4 TB/s). NT = 2 by the
 // tensor core: 976 us for 2,048 tokens of 32 heads against 32,768 keys at D = 128, a quarter of it
 // the weights' second part (755 us and 1.46 PFLOP/s without; instructions take 77 to 85 cycles of the
 // 64 that they need alone).
 template <int NT, int D, Pass M, bool FOX>
 struct CachedCfg {
     static constexpr uint32_t tile = 128 * D * 2, atom = 128 * 128;
-    // The rows' tiles, their high parts and then (keeps_low) their low ones; for NT = 1 at D = 128,
-    // where the update's product takes 64 KB, they lie in tensor memory instead.
     // the keys' update in this pass: by a product with P - I, or (single tokens) on the CUDA cores
     static constexpr bool update = NT == 1 && M != Pass::shared, single = NT == 1 && M == Pass::one,
                           matrix = update && !single;
@@ -186,11 +211,13 @@ struct CachedCfg {
     static constexpr bool held = single && D == 64 && !FOX;
     // gates come through a ring of their own, of up to kGateHeads query heads
     static constexpr bool ring = FOX && ahead;
+    // The rows' tiles, their high parts and then (keeps_low) their low ones, in shared memory, or in tensor
+    // memory: where the update's product takes 64 KB (D = 128), and where they come ahead.
     static constexpr bool rows_in_tmem = ahead || (update && D == 128), low = keeps_low(NT, D);
     static constexpr uint32_t X = 0, xbytes = rows_in_tmem ? 0 : NT * (low ? 2 : 1) * tile;
     static constexpr uint32_t P = X + xbytes, pbytes = matrix ? 2 * D * D * 2 : 0;
-    // slots of keys and of values: what fits beside; for NT = 1 and D = 64 so that two CTAs share
-    // an SM. With NT = 1 a key slot is held until the updated keys have left it.
+    // slots of keys and of values: what fits beside; for NT = 1 and D = 64 (but for single tokens) so that
+    // two CTAs share an SM. A key slot is held until the updated keys have left it.
     static constexpr int NK = matrix ? (D == 64 ? 2 : 3)
                               : NT == 2 ? (D == 64 ? 4 : 3)
                                         : (single && D == 64 ? 8 : 4) - (ring ? 1 : 0);
@@ -465,7 +492,8 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t b = kd + (kk >> 2) * kAtom + 2 * (kk & 3);
                         if (L::rows_in_tmem)
-                            umma_tA(tmem + L::cS + (L::two_s ? L::cS2 * q : 0), tmem + L::cX + part * (D / 2) + 8 * kk, b, ID_S, part > 0 || kk > 0);
+                            umma_tA(tmem + L::cS + (L::two_s ? L::cS2 * q : 0), tmem + L::cX + part * (D / 2) + 8 * kk,
+                                    b, ID_S, part > 0 || kk > 0);
                         else
                             umma_bf16(tmem + (L::two_s ? L::cS2 : L::per_tile) * q + L::cS,
                                       xd + part * NT * kTile + (kk >> 2) * kAtom + 2 * (kk & 3), b, ID_S,
@@ -475,7 +503,8 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
             };
             auto issue_pv = [&](int q, bool first) {
                 const uint64_t vd = v_desc + v.slot * kTile;
-                const uint32_t tm = tmem + (L::two_s ? 0 : L::per_tile * q), p = tm + L::cS + (L::two_s ? L::cS2 * q : 0);
+                const uint32_t tm = tmem + (L::two_s ? 0 : L::per_tile * q);
+                const uint32_t p = tm + L::cS + (L::two_s ? L::cS2 * q : 0);
                 umma_tA(tm + L::cO, p, vd, ID_O, !first);
 #pragma unroll
                 for (int kk = 1; kk < 8; ++kk) umma_tA(tm + L::cO, p + 8 * kk, vd + 128 * kk, ID_O, 1);
@@ -1146,15 +1175,15 @@ cudaError_t big_smem(K kern, size_t bytes) {
 
 template <int NT, int D, bool FOX, Pass M>
 cudaError_t launch_cached(const StepOf<M> &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream) {
-    CUtensorMap tx, tl, tm, tk, tv;
+    using L = CachedCfg<NT, D, M, FOX>;
+    CUtensorMap tx{}, tl{}, tm{}, tk, tv;  // (rows that come ahead, and no P - I, need no map)
     // a map has no empty axis; of an empty pool nothing is loaded, every page number is outside it
     auto heads = [&](int pages) { return (long long)std::max(pages, 1) * a.c.Hkv; };
-    if (!make_map(&tx, y.qt, D, y.R, a.c.Hkv, 32) || !make_map(&tl, y.ql, D, y.R, a.c.Hkv, 32) ||
-        !make_map(&tm, y.mt, D, D, (long long)std::min(a.c.seqs, a.N) * a.c.Hkv * 2, D) ||
+    if ((!L::ahead && (!make_map(&tx, y.qt, D, y.R, a.c.Hkv, 32) || !make_map(&tl, y.ql, D, y.R, a.c.Hkv, 32))) ||
+        (L::matrix && !make_map(&tm, y.mt, D, D, (long long)std::min(a.c.seqs, a.N) * a.c.Hkv * 2, D)) ||
         !make_map(&tk, a.c.k_pages, D, a.c.page, heads(a.c.nk), a.c.page < 128 ? a.c.page : 128) ||
         !make_map(&tv, a.c.v_pages, D, a.c.page, heads(a.c.nv), a.c.page < 128 ? a.c.page : 128))
         return cudaErrorInvalidValue;
-    using L = CachedCfg<NT, D, M, FOX>;
     auto kern = tc_cached_kernel<NT, D, FOX, M>;
     const cudaError_t e = big_smem(kern, L::bytes);
     if (e != cudaSuccess) return e;
@@ -1168,8 +1197,9 @@ cudaError_t launch_cached(const StepOf<M> &a, const TcWs &y, uint64_t limit_ns, 
 #define PASS(NT, D, FOX, M) \
     template cudaError_t launch_cached<NT, D, FOX, M>(const StepMore &, const TcWs &, uint64_t, cudaStream_t);
 #define EXTERN_PASS(NT, D, FOX, M) extern PASS(NT, D, FOX, M)
-#define ONE_PASS(WHAT) \
-    WHAT(1, 64, false, Pass::one) WHAT(1, 128, false, Pass::one) WHAT(1, 64, true, Pass::one) WHAT(1, 128, true, Pass::one)
+#define ONE_PASS(WHAT)                                                                          \
+    WHAT(1, 64, false, Pass::one) WHAT(1, 128, false, Pass::one)                                \
+    WHAT(1, 64, true, Pass::one) WHAT(1, 128, true, Pass::one)
 EACH_PASS(EXTERN_PASS, Pass::window)
 EACH_PASS(EXTERN_PASS, Pass::shared)
 ONE_PASS(EXTERN_PASS)

@@ -594,8 +594,8 @@ struct Behind;
 template <typename A>
 cudaError_t launch_decode(const A &a, int d, bool bf16, const Behind *behind, float *part, cudaStream_t stream);
 
-cudaError_t launch_prefix_f32(StepMore &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws, bool first,
-                              cudaStream_t stream);
+cudaError_t launch_prefix_f32(StepMore &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws,
+                              bool first, cudaStream_t stream);
 
 size_t f32_ws_bytes(const Cache &c, int N, int d, bool fox) {
     return f32_layout(c, N, d, fox).total + (decode_takes(c.G) ? align256(decode_part_bytes(c, d)) : 0);

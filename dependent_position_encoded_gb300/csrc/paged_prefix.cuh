@@ -145,7 +145,9 @@ inline StepMore shared_step(const StepMore &a, const Prefix &x) {
 
 // A sequence's only token and a key head: its queries carried to the prefix's end and the carry's
 // update from one read of the carry, all in fp32, by a CTA for `R` rows of C from `row0` on (they do not
-// meet; that of row 0 sees to the gates). Eight lanes share a row, 16 bytes each at a time. put(g, i, x):
+// meet; that of row 0 sees to the gates). Eight lanes share a row, 16 bytes each at a time; bound by the
+// carry's bytes, there and back (22.5 us for 64 tokens of 8 key heads at D = 128, 67 MB: 3.0 TB/s, beside
+// the look for a place). put(g, i, x):
 // entry i of query head g's carried query; gate(g, x): its gates.
 template <typename T, int D, int R, typename P, typename F>
 __device__ __forceinline__ void prefix_single(const StepMore &a, const Prefix &x, const Seq &s, int b, int h, int row0,
@@ -231,8 +233,11 @@ __device__ __forceinline__ void prefix_single(const StepMore &a, const Prefix &x
 // part of W W^T, D = diag(beta)), C <- C - sum_t (A y)_t w_t^T. The rows of C do not meet: a CTA takes 64
 // of them, eight lanes to four rows (the tokens' w come from shared memory, whose reads bound the kernel
 // with fewer), and forms the factors of 32 tokens by itself. In fp32 because a carry outlives its step:
-// bf16 parts would leave 2^-17 of it with every chunk. CARRYTIME
-constexpr int kCarryThr = 128, kCarryPer = 4, kCarryRows = kCarryThr / 8 * kCarryPer, kCarryTokens = 32, kCarryBlock = 8;
+// bf16 parts would leave 2^-17 of it with every chunk. Bound by that chain, whose CTAs are few: 100 us for 8
+// sequences of up to 512 tokens and 8 heads at D = 128, 128 CTAs, each at a third of its SM's fp32 rate
+// (token by token 198, with one row of C to eight lanes 136).
+constexpr int kCarryThr = 128, kCarryPer = 4, kCarryRows = kCarryThr / 8 * kCarryPer;
+constexpr int kCarryTokens = 32, kCarryBlock = 8;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kCarryThr) prefix_carry_kernel(const StepMore a, const Prefix x) {
@@ -241,7 +246,8 @@ __global__ void __launch_bounds__(kCarryThr) prefix_carry_kernel(const StepMore 
     __shared__ __align__(16) float ws[kCarryTokens][LD];  // (rows begin in different banks)
     __shared__ __align__(16) float As[NB][B][B], Gs[NB][B][B];  // A, by rows; W W^T
     __shared__ float bs[kCarryTokens];
-    const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, sub = tid & 7, r = blockIdx.x * kCarryRows + (tid >> 3) * kCarryPer;
+    const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, sub = tid & 7;
+    const int r = blockIdx.x * kCarryRows + (tid >> 3) * kCarryPer;
     grid_begin();
     const Seq s = seq_of(a, b);
     const bool mine = s.T > 1 && __ldg(x.of + b) >= 0;
@@ -278,7 +284,8 @@ __global__ void __launch_bounds__(kCarryThr) prefix_carry_kernel(const StepMore 
 #pragma unroll
             for (int q = 0; q < E; q += 4)
                 *reinterpret_cast<float4 *>(&ws[e / PER][e % PER * E + q]) =
-                    make_float4(Elt<T>::to_f(v[q]), Elt<T>::to_f(v[q + 1]), Elt<T>::to_f(v[q + 2]), Elt<T>::to_f(v[q + 3]));
+                    make_float4(Elt<T>::to_f(v[q]), Elt<T>::to_f(v[q + 1]), Elt<T>::to_f(v[q + 2]),
+                                Elt<T>::to_f(v[q + 3]));
         }
         if (tid < kCarryTokens) bs[tid] = beta;
         __syncthreads();
@@ -384,7 +391,8 @@ __global__ void __launch_bounds__(kCarryThr) prefix_carry_kernel(const StepMore 
 template <typename T, int D>
 cudaError_t launch_prefix_carry(const StepMore &a, const Prefix &x, cudaStream_t stream) {
     if (a.max_chunk <= 1) return cudaSuccess;
-    return launch(prefix_carry_kernel<T, D>, dim3(D / kCarryRows, a.c.Hkv, a.c.seqs), kCarryThr, 0, stream, false, a, x);
+    return launch(prefix_carry_kernel<T, D>, dim3(D / kCarryRows, a.c.Hkv, a.c.seqs), kCarryThr, 0, stream, false, a,
+                  x);
 }
 
 }  // namespace paged

@@ -34,7 +34,8 @@ constexpr size_t query_smem() { return (size_t)2 * (D / 64) * TILE * 4; }
 // 64 tokens of a query head, X C^T, or all heads of a key head of a sequence's only token; y: the step's,
 // z: those of the shared step.
 template <int D>
-__global__ void __launch_bounds__(kThr) prefix_query_f32_kernel(const StepMore a, const Prefix x, const Ws y, const Ws z) {
+__global__ void __launch_bounds__(kThr)
+prefix_query_f32_kernel(const StepMore a, const Prefix x, const Ws y, const Ws z) {
     constexpr int NH = D / 64;
     extern __shared__ float sm[];
     float *const X = sm, *const C = X + NH * TILE;
@@ -81,7 +82,8 @@ __global__ void __launch_bounds__(kThr) prefix_query_f32_kernel(const StepMore a
 // ---------------------------------------------------------------- join
 // A warp per row: the parts of its prefix's keys into one; grid (slots, Hq, 8).
 template <int D>
-__global__ void __launch_bounds__(kThr) prefix_join_f32_kernel(const StepMore a, const StepMore v, const Prefix x, const Ws z) {
+__global__ void __launch_bounds__(kThr)
+prefix_join_f32_kernel(const StepMore a, const StepMore v, const Prefix x, const Ws z) {
     constexpr int E = D / 32;
     const int slot = blockIdx.x, hq = blockIdx.y, lane = threadIdx.x & 31, r = blockIdx.z * 8 + (threadIdx.x >> 5);
     int b, c;
@@ -169,8 +171,8 @@ size_t prefix_f32_bytes(const StepMore &a, int d) {
 
 // y_qt, y_gq: the step's queries carried to the chunk's start and their gates, null where it has single
 // tokens alone (theirs are formed from the inputs).
-cudaError_t launch_prefix_f32(StepMore &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws, bool first,
-                              cudaStream_t stream) {
+cudaError_t launch_prefix_f32(StepMore &a, int d, float *carry, float *gates, float *y_qt, float *y_gq, void *ws,
+                              bool first, cudaStream_t stream) {
     Prefix x;
     Ws z = {};
     layout(a, d, static_cast<char *>(ws), &x, &z);

@@ -14,15 +14,17 @@ static_assert(kThr == kPrefixThr, "make_plans");
 
 // ---------------------------------------------------------------- plans and single tokens
 // The first CTA makes the plan of the prefixes, the next one (OWN) that of the step, the others take the
-// single tokens, a sequence and key head each (BEHIND: and 64 rows of its carry): OWN, of a step that has no others, enter them into
-// the cache and leave their queries and parts; BEHIND, carry their queries to the prefix's end. With up
-// to kFused sequences these find their places by themselves beside the plan, else by one made before
-// (plan: by a launch of this kernel with no sequence).
+// single tokens, a sequence and key head each (BEHIND: and 64 rows of its carry): OWN, of a step that has
+// no others, enter them into the cache and leave their queries and parts; BEHIND, carry their queries to
+// the prefix's end, as a high and a low bf16 part (16 bits of significand: a single part would cost the
+// output more than its own rounding, keeps_low). With up to kFused sequences these find their places by
+// themselves beside the plan (each CTA reads all sequences' lengths, from L2), else in one made before, by a
+// launch of this kernel without sequences: a launch more, 4 us.
 constexpr int kFused = 1024;
 
 template <int D, bool OWN, bool BEHIND>
-__global__ void __launch_bounds__(kThr) tc_single_kernel(const StepMore a, const StepMore v, const Prefix x, const TcWs y,
-                                                         const TcWs z, int plans, bool fused) {
+__global__ void __launch_bounds__(kThr) tc_single_kernel(const StepMore a, const StepMore v, const Prefix x,
+                                                         const TcWs y, const TcWs z, int plans, bool fused) {
     __shared__ long long sums[2 * kThr / 32];
     const int G = a.c.G;
     grid_begin();
@@ -67,7 +69,8 @@ __global__ void __launch_bounds__(kThr) tc_single_kernel(const StepMore a, const
 }
 
 template <int D, bool OWN, bool BEHIND>
-cudaError_t launch_tokens(const StepMore &a, const Prefix &x, const TcWs &y, const TcWs &z, bool first, cudaStream_t stream) {
+cudaError_t launch_tokens(const StepMore &a, const Prefix &x, const TcWs &y, const TcWs &z, bool first,
+                          cudaStream_t stream) {
     const StepMore v = BEHIND ? shared_step(a, x) : a;
     const int items = a.c.seqs * a.c.Hkv * (BEHIND ? D / 64 : 1), plans = (OWN ? 1 : 0) + (BEHIND ? 1 : 0);
     const auto kern = tc_single_kernel<D, OWN, BEHIND>;
@@ -79,8 +82,9 @@ cudaError_t launch_tokens(const StepMore &a, const Prefix &x, const TcWs &y, con
 
 // ---------------------------------------------------------------- queries of several tokens
 // X C^T over tiles of 64 rows of a sequence and key head, kTiles of them on one load of C, both factors
-// in two bf16 parts (16 bits of significand). y: the step's, whose queries have been carried to the chunk's
-// start; z: those of the shared step.
+// in two bf16 parts (16 bits of significand; 3 of the 4 products, mma.sync: the rows' bytes bound it). 51 us
+// for 80,000 rows at D = 128, 82 MB of them: 1.6 TB/s, two CTAs an SM. y: the step's, whose queries have been
+// carried to the chunk's start; z: those of the shared step.
 constexpr int kTiles = 4;
 
 template <int D>
@@ -91,7 +95,8 @@ struct QuerySmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThr, 2) prefix_query_kernel(const StepMore a, const Prefix x, const TcWs y, const TcWs z) {
+__global__ void __launch_bounds__(kThr, 2)
+prefix_query_kernel(const StepMore a, const Prefix x, const TcWs y, const TcWs z) {
     using S = QuerySmem<D>;
     constexpr int LDD = S::LDD, NT = D / 16, PER = D / 8, IT = kC * PER / kThr;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -217,7 +222,6 @@ size_t layout(const StepMore &a, int d, char *w, Prefix *x, TcWs *z) {
         long long *const units = reinterpret_cast<long long *>(take(((size_t)c.seqs + 1) * 8));
         z->plan[p] = Plan{units, reinterpret_cast<long long *>(take(((size_t)c.seqs + 1) * 8)), ctas};
     }
-    z->mt = z->qt;  // no keys are advanced
     z->R = (long long)a.N * c.G;
     return off;
 }
@@ -256,8 +260,8 @@ cudaError_t launch_prefix_tc(const StepMore &a, int d, float *carry, float *gate
     return fox ? all(launch_all<128, true>) : all(launch_all<128, false>);
 }
 
-cudaError_t launch_singles(const StepMore &a, int d, const TcWs &y, float *carry, float *gates, void *ws, uint64_t limit_ns,
-                           Behind *behind, cudaStream_t stream) {
+cudaError_t launch_singles(const StepMore &a, int d, const TcWs &y, float *carry, float *gates, void *ws,
+                           uint64_t limit_ns, Behind *behind, cudaStream_t stream) {
     TcWs z = {};
     Prefix x = {};
     if (carry != nullptr) x = prefix_at(a, d, carry, gates, ws, &z, behind);

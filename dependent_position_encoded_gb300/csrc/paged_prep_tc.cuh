@@ -2,7 +2,7 @@
 // the new keys' way into the cache, the cached keys' update and the joining of the softmax
 // parts. Warp-level MMAs (mma.sync, bf16 operands, fp32 accumulators): every product here is
 // 64 x 64 x d or the pass is bound by memory, and none of them is worth a tensor-memory
-// pipeline; the attention itself is in paged_attn_tc.cu.
+// pipeline; the attention itself is in paged_attn_tc.cuh.
 //
 // Precision. The inputs are bf16; what is computed from them (A, U, Lq, R A^T, P_b) enters
 // further products as a high and a low bf16 part (16 bits of significand, see split2), so
@@ -864,7 +864,8 @@ __global__ void __launch_bounds__(kThr) tc_gates_kernel(const A a, const TcWs y)
 // the look-up took longer. 19 us for 79,000 rows without parts at D = 64 (1.6 TB/s, most of it
 // from L2), 7 us for 512 rows of ten parts or so.
 // BEHIND: sequences with prefixes, whose parts are joined too. W: the warps of a row, each with its share
-// of the prefix's parts, of which few rows may have many.
+// of the prefix's parts, of which few rows may have many (512 rows of 80 or so at D = 64: 16.5 -> 11.3 us
+// with four warps each). 55 us for 80,000 rows of 2 to 4 parts at D = 128 (131 MB of them: 2.4 TB/s).
 template <int D, int P, bool BEHIND, int W, typename A>
 __global__ void __launch_bounds__(kThr) tc_combine_kernel(const A a, const TcWs y, const Behind x, int rows) {
     constexpr int E = D / 32;
@@ -1072,7 +1073,7 @@ cudaError_t launch_tc_finish(const A &a, const TcWs &y, const Behind &x, cudaStr
     if (a.log_f != nullptr) {
         // CTAs of 4 kThr positions, or of several times that where tables are wide and many: most of
         // these CTAs would find nothing (68 sequences of 200 positions in tables of 17,000, 32 heads: 41 ->
-        // GATES us)
+        // 13 us)
         const long long parts = (cap + 4 * kThr - 1) / (4 * kThr), room = 8192 / ((long long)a.c.Hq * a.c.seqs) + 1;
         e = launch(tc_gates_kernel<A>, dim3((unsigned)(parts < room ? parts : room), a.c.Hq, a.c.seqs), kThr, 0, stream,
                    false, a, y);

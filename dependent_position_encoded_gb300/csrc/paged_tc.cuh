@@ -52,7 +52,7 @@ __host__ __device__ constexpr bool keeps_low(int NT, int D) { return NT == 1 || 
 // and, where a chunk may have several blocks of 64 tokens:
 //   kh, kl (slots, Hkv, 64 + D, D) bf16 high and low parts of [k~; P_b - I]
 //   vb   (slots, Hkv, 64, D) bf16 the block's values, zero past its tokens
-// and, where it may have several groups of blocks (paged_prep_tc.cu):
+// and, where it may have several groups of blocks (paged_prep_tc.cuh):
 //   ch, cl (slots, Hkv, 64, D) bf16 high and low parts of the new keys at their group's end
 //   gp   (groups, Hkv, 2, D, D) bf16 high and low parts of the groups' products less I
 struct TcWs {
