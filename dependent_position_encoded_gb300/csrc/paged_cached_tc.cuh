@@ -860,10 +860,11 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
             const float gq =
                 FOX && live ? y.gq[(size_t)t.h * y.R + (size_t)t.s.first * G + row0 + rw] * kLog2e : 0.f;
             if (L::rows_in_tmem && !L::ahead) load_rows(t);
-            // a window: the row sees the keys from `from` on (and the sinks); `edge`: where all rows' do
+            // a window: the row sees the keys from `from` on (and the sinks); from `edge` on all rows of the
+            // tile do
             const Sight seen = sight(t);
             const int from = WIN ? t.s.n + 1 - window + (live ? (row0 + rw) / G : 0) : 0;
-            const int edge = WIN && window > 0 ? t.s.n + t.s.T - window : 0;
+            const int edge = WIN && window > 0 ? t.s.n + 1 - window + (min(rows_all, row0 + 128) - 1) / G : 0;
             float m_run = -INFINITY, l_run = 0.f;
             int kid1, vid1;  // the pages of the next tile's boxes
             auto look_up = [&](int pos0) {
