@@ -821,6 +821,14 @@ def path_fox_paged_extend(q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, 
                          max_chunk, scale, out, workspace, stream)
 
 
+def _window(window, sinks):
+    """A window and its sinks as C ints, which would take the low bits of larger numbers."""
+    window, sinks = int(window), int(sinks)
+    if not (-2**31 <= window < 2**31 and -2**31 <= sinks < 2**31):
+        raise ValueError("window and sinks must be 32-bit ints")
+    return window, sinks
+
+
 def path_paged_window_extend(q, k, v, w, beta, cu_tokens, cache, max_chunk, window, sinks=0,
                              scale=None, out=None, workspace=None, stream=None):
     """path_paged_extend through a sliding window: every new token sees the last `window`
@@ -828,7 +836,7 @@ def path_paged_window_extend(q, k, v, w, beta, cu_tokens, cache, max_chunk, wind
     be larger than the window. Cached keys that no new token sees are neither read nor advanced;
     path_paged_trim gives their pages back."""
     return _paged_extend("path_paged_window_extend", q, k, v, w, beta, None, cu_tokens, cache,
-                         max_chunk, scale, out, workspace, stream, (int(window), int(sinks)))
+                         max_chunk, scale, out, workspace, stream, _window(window, sinks))
 
 
 def path_fox_paged_window_extend(q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, window,
@@ -836,7 +844,7 @@ def path_fox_paged_window_extend(q, k, v, w, beta, log_f, cu_tokens, cache, max_
     """path_paged_window_extend with the forget gates of path_fox_paged_extend."""
     _paged_gates(log_f, cache)
     return _paged_extend("path_fox_paged_window_extend", q, k, v, w, beta, log_f, cu_tokens, cache,
-                         max_chunk, scale, out, workspace, stream, (int(window), int(sinks)))
+                         max_chunk, scale, out, workspace, stream, _window(window, sinks))
 
 
 def _prefix_tensors(q, cache, prefix_of, carry, gates=None, fox=False):
@@ -973,7 +981,7 @@ def path_paged_free(rows, cache, workspace=None, stream=None):
 def path_paged_trim(cache, window, sinks=0, workspace=None, stream=None):
     """Gives back the pages that no later step through this window reaches: the slots behind them
     move down and cache.lens falls by their tokens. Workspaces as in path_paged_reserve."""
-    return _paged_call("path_paged_trim", cache, workspace, stream, int(window), int(sinks))
+    return _paged_call("path_paged_trim", cache, workspace, stream, *_window(window, sinks))
 
 
 def path_paged_compact(cache, workspace=None, stream=None):

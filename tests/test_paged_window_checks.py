@@ -81,3 +81,13 @@ def test_trim_needs_the_page_calls_workspace(so):
     need = so.path_paged_workspace_bytes(_c(), 0, 0)
     assert so.path_paged_trim(_c(), 8, 0, FAKE, need - 1, None) == pa.ERR_WORKSPACE
     assert so.path_paged_trim(_c(), 8, 0, None, need, None) == pa.ERR_NULL
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 32 + 8, 1), (8, 2 ** 32 + 1), (2 ** 40, 0), (-2 ** 33 + 8, 0)])
+def test_numbers_that_no_int_holds(window, sinks):
+    with pytest.raises(ValueError, match="32-bit"):
+        pa.path_paged_window_extend(*[x for n, x in _step().items() if n != "log_f"], _cache(), 2, window, sinks)
+    with pytest.raises(ValueError, match="32-bit"):
+        pa.path_fox_paged_window_extend(*_step().values(), _cache(), 2, window, sinks)
+    with pytest.raises(ValueError, match="32-bit"):
+        pa.path_paged_trim(_cache(), window, sinks)
