@@ -863,8 +863,9 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
             // a window: the row sees the keys from `from` on (and the sinks); from `edge` on all rows of the
             // tile do
             const Sight seen = sight(t);
-            const int from = WIN ? t.s.n + 1 - window + (live ? (row0 + rw) / G : 0) : 0;
-            const int edge = WIN && window > 0 ? t.s.n + 1 - window + (min(rows_all, row0 + 128) - 1) / G : 0;
+            const int from = WIN ? t.s.n + 1 - window + (live && M != Pass::one ? (row0 + rw) / G : 0) : 0;
+            const int last = M != Pass::one ? (min(rows_all, row0 + 128) - 1) / G : 0;  // the tile's last token
+            const int edge = WIN && window > 0 ? t.s.n + 1 - window + last : 0;
             float m_run = -INFINITY, l_run = 0.f;
             int kid1, vid1;  // the pages of the next tile's boxes
             auto look_up = [&](int pos0) {

@@ -367,10 +367,12 @@ paged_decode_merge(const A a, const Behind z, int chunk, int nsplit, const float
 template <typename T, bool FOX, int D, int G, typename A>
 cudaError_t launch_g(const A &a, const Behind &x, int chunk, int nsplit, float *part, cudaStream_t stream) {
     if (nsplit > 0) {
-        const cudaError_t e = launch(paged_decode_split<T, FOX, D, G, A>, dim3(nsplit, a.c.Hkv, a.c.seqs), kThreads, 0, stream, true, a, chunk, nsplit, part);
+        const cudaError_t e = launch(paged_decode_split<T, FOX, D, G, A>, dim3(nsplit, a.c.Hkv, a.c.seqs), kThreads, 0,
+                                     stream, true, a, chunk, nsplit, part);
         if (e != cudaSuccess) return e;
     }
-    return launch(paged_decode_merge<T, FOX, D, A>, dim3(a.c.Hq, a.c.seqs), D, 0, stream, nsplit == 0, a, x, chunk, nsplit, part);
+    return launch(paged_decode_merge<T, FOX, D, A>, dim3(a.c.Hq, a.c.seqs), D, 0, stream, nsplit == 0, a, x, chunk, nsplit,
+                  part);
 }
 
 template <typename T, bool FOX, int D, typename A>

@@ -536,18 +536,19 @@ cudaError_t launch_cache(const AnyStep &a, const Ws &y, cudaStream_t stream) {
         (e = big_smem(f32_transform_kernel<D, AnyStep>, transform_smem<D>())) != cudaSuccess)
         return e;
     const long long cap = most_seen(a);
-    e = launch(f32_cached_kernel<D, false, AnyStep>, dim3(nslots, Hq, y.splits), kThr, cached_smem<D>(), stream, false, a, y);
+    e = launch(f32_cached_kernel<D, false, AnyStep>, dim3(nslots, Hq, y.splits), kThr, cached_smem<D>(), stream, false, a,
+               y);
     if (e == cudaSuccess)
         e = launch(f32_combine_kernel<D, AnyStep>, dim3(nslots, Hq, kC / 8), kThr, 0, stream, false, a, y);
     if (e == cudaSuccess)
-        e = launch(f32_carry_kernel<D, AnyStep>, dim3(nslots + a.c.seqs * (D / 64), Hkv), kThr, carry_smem<D>(), stream, false,
-                   a, y, nslots);
+        e = launch(f32_carry_kernel<D, AnyStep>, dim3(nslots + a.c.seqs * (D / 64), Hkv), kThr, carry_smem<D>(), stream,
+                   false, a, y, nslots);
     // CTAs of 64 cached keys, or of several where that makes more than four to an SM
     long long parts = 4 * 152 / ((long long)Hkv * a.c.seqs) + 1;
     if (parts > (cap + kC - 1) / kC) parts = (cap + kC - 1) / kC;
     if (e == cudaSuccess && parts > 0)
-        e = launch(f32_transform_kernel<D, AnyStep>, dim3((unsigned)parts, Hkv, a.c.seqs), kThr, transform_smem<D>(), stream,
-                   false, a, y);
+        e = launch(f32_transform_kernel<D, AnyStep>, dim3((unsigned)parts, Hkv, a.c.seqs), kThr, transform_smem<D>(),
+                   stream, false, a, y);
     return e;
 }
 

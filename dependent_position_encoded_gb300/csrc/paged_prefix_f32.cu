@@ -76,7 +76,8 @@ prefix_query_f32_kernel(const StepMore a, const Prefix x, const Ws y, const Ws z
         }
     }
     if (a.log_f != nullptr && tid < rows)
-        z.gq[row_of(place_of(x, b, p, c * kC + tid), a.c.Hq, hq)] = y.gq[bq * kC + tid] + x.gates[(size_t)b * a.c.Hq + hq];
+        z.gq[row_of(place_of(x, b, p, c * kC + tid), a.c.Hq, hq)] =
+            y.gq[bq * kC + tid] + x.gates[(size_t)b * a.c.Hq + hq];
 }
 
 // ---------------------------------------------------------------- join
@@ -128,8 +129,8 @@ cudaError_t launch_all(const StepMore &a, const Prefix &x, const Ws &y, const Ws
     if (e == cudaSuccess)
         e = launch(prefix_query_f32_kernel<D>, dim3(nslots, a.c.Hq), kThr, query_smem<D>(), stream, false, a, x, y, z);
     if (e == cudaSuccess)
-        e = launch(f32_cached_kernel<D, true, StepMore>, dim3(nslots, a.c.Hq, z.splits), kThr, cached_smem<D>(), stream, false, v,
-                   z);
+        e = launch(f32_cached_kernel<D, true, StepMore>, dim3(nslots, a.c.Hq, z.splits), kThr, cached_smem<D>(), stream,
+                   false, v, z);
     if (e == cudaSuccess)
         e = launch(prefix_join_f32_kernel<D>, dim3(nslots, a.c.Hq, kC / 8), kThr, 0, stream, false, a, v, x, z);
     if (e == cudaSuccess) e = launch_prefix_carry<float, D>(a, x, stream);

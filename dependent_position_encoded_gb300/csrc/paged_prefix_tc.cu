@@ -13,13 +13,13 @@ namespace {
 static_assert(kThr == kPrefixThr, "make_plans");
 
 // ---------------------------------------------------------------- plans and single tokens
-// The first CTA makes the plan of the prefixes, the next one (OWN) that of the step, the others take the
-// single tokens, a sequence and key head each (BEHIND: and 64 rows of its carry): OWN, of a step that has
-// no others, enter them into the cache and leave their queries and parts; BEHIND, carry their queries to
-// the prefix's end, as a high and a low bf16 part (16 bits of significand: a single part would cost the
-// output more than its own rounding, keeps_low). With up to kFused sequences these find their places by
-// themselves beside the plan (each CTA reads all sequences' lengths, from L2), else in one made before, by a
-// launch of this kernel without sequences: a launch more, 4 us.
+// Grid (plans and sequences, key heads). The first CTA makes the plan of the prefixes, the next one (OWN)
+// that of the step, the others take the single tokens, a sequence and key head each (BEHIND: and 64 rows
+// of its carry): OWN, of a step that has no others, enter them into the cache and leave their queries and
+// parts; BEHIND, carry their queries to the prefix's end, as a high and a low bf16 part (16 bits of
+// significand: keeps_low says what one part costs). With up to kFused sequences these find their places
+// by themselves beside the plan (each CTA reads all sequences' lengths, from L2), else in one made before,
+// by a launch of this kernel without sequences.
 constexpr int kFused = 1024;
 
 template <int D, bool OWN, bool BEHIND>
@@ -30,18 +30,19 @@ __global__ void __launch_bounds__(kThr) tc_single_kernel(const StepMore a, const
     grid_begin();
     // (no kernel before reads or writes what this one does, but for a plan made before)
     if ((int)blockIdx.x < plans) {
-        if (BEHIND && blockIdx.x == 0) {
-            place_tokens(a, x);
-            make_plans<D>(v, z, sums);
-        } else if (OWN) {
-            make_plans<D>(a, y, sums);
+        if (blockIdx.y == 0) {
+            if (BEHIND && blockIdx.x == 0) {
+                place_tokens(a, x);
+                make_plans<D>(v, z, sums);
+            } else if (OWN) {
+                make_plans<D>(a, y, sums);
+            }
         }
         grid_wait();
         return;
     }
     constexpr int kParts = BEHIND ? D / 64 : 1;
-    const int item = (blockIdx.x - plans) / kParts, part = (blockIdx.x - plans) % kParts;
-    const int h = item % a.c.Hkv, b = item / a.c.Hkv;
+    const int b = (blockIdx.x - plans) / kParts, part = (blockIdx.x - plans) % kParts, h = blockIdx.y;
     if (!fused) grid_wait();
     const Seq s = seq_of(a, b);
     if (s.T == 1) {
@@ -72,12 +73,12 @@ template <int D, bool OWN, bool BEHIND>
 cudaError_t launch_tokens(const StepMore &a, const Prefix &x, const TcWs &y, const TcWs &z, bool first,
                           cudaStream_t stream) {
     const StepMore v = BEHIND ? shared_step(a, x) : a;
-    const int items = a.c.seqs * a.c.Hkv * (BEHIND ? D / 64 : 1), plans = (OWN ? 1 : 0) + (BEHIND ? 1 : 0);
+    const int items = a.c.seqs * (BEHIND ? D / 64 : 1), plans = (OWN ? 1 : 0) + (BEHIND ? 1 : 0);
     const auto kern = tc_single_kernel<D, OWN, BEHIND>;
     if (!BEHIND || a.c.seqs <= kFused)
-        return launch(kern, dim3(plans + items), kThr, 0, stream, first, a, v, x, y, z, plans, true);
+        return launch(kern, dim3(plans + items, a.c.Hkv), kThr, 0, stream, first, a, v, x, y, z, plans, true);
     const cudaError_t e = launch(kern, dim3(plans), kThr, 0, stream, first, a, v, x, y, z, plans, true);
-    return e != cudaSuccess ? e : launch(kern, dim3(items), kThr, 0, stream, false, a, v, x, y, z, 0, false);
+    return e != cudaSuccess ? e : launch(kern, dim3(items, a.c.Hkv), kThr, 0, stream, false, a, v, x, y, z, 0, false);
 }
 
 // ---------------------------------------------------------------- queries of several tokens
