@@ -154,23 +154,25 @@ constexpr int kGateHeads = 8;
 // not it for them, and (D = 64) to rings of eight and five slots; a key slot is given back a step after
 // its store was issued. 64 sequences, W = 4,096, 16 heads, D = 64: 219 us, 5.8 TB/s (with the product, two
 // CTAs an SM: 234, and 15 to prepare it where this takes 7); 16, W = 2,048, 8 key heads of four query heads,
-// D = 128, gates: the whole step 71 (with the product 81). Plain steps keep the product, and with it their
+// D = 128, gates: the whole step 69 (with the product 81). Plain steps keep the product, and with it their
 // results to the bit.
 //
 // Pass::shared, the read-only pass over a prefix's keys. At D = 64 two CTAs share an SM; at D = 128, where
 // the slots leave room for one, two warpgroups share a row tile's softmax, half the columns each (they meet
 // once for the row's maximum and once before a half's weights cover the other's logits), with two places
 // for S: 4 prefixes of up to 16,384, 8 key heads of four query heads, gates, D = 128, 16 single tokens
-// behind each: 64 us, 3.4 TB/s (one warpgroup and one place: 78); at D = 64 the halves' meetings cost more
+// behind each: 61 us, 3.6 TB/s (one warpgroup and one place: 78, this then 64); at D = 64 the halves' meetings cost more
 // than they give (32 tokens behind 8,192 keys of 16 heads: 18 us, with halves 19).
 //
-// With gates these two take them from a ring in shared memory that a warp fills (up to kGateHeads query
-// heads; of more the softmax's warps read them in place): 183 us -> 176 for the whole step of the 4
-// prefixes. Their softmax is then bound by its instructions' way to the SM, which with four roles of
-// straight code come from beyond the nearest cache (no instruction there: the largest stall, 1.9 cycles
-// an issue), not by bytes: 326 us where the same step without gates takes 221 (64 sequences, W = 4,096, 16
-// key heads of four query heads, D = 64). Deeper rings, gates a tile ahead and rows padded against bank
-// conflicts changed nothing.
+// With gates these two take them from a ring in shared memory that a warp fills (183 us -> 176 for the
+// whole step of the 4 prefixes); where more than kGateHeads query heads share a key head, kernels
+// compiled apart read them in place. The softmax is then bound not by bytes but by its instructions' way to
+// the SM, which four roles of straight code do not hold near (no instruction there: the largest stall, 1.9
+// cycles an issue): 325 us where the same pass without gates takes 218 (64 sequences, W = 4,096, 16 key
+// heads of four query heads, D = 64). So less code is faster code: one way of reading gates in a kernel and
+// the update's loops unrolled twice (four times without gates) took the whole step from 72 us to 69 (16
+// sequences, W = 2,048, D = 128) and the 4 prefixes from 165 to 162.5. Deeper rings, gates a tile ahead
+// and rows padded against bank conflicts changed nothing.
 //
 // With NT = 1 and at most 64 (32) rows, the tile holds two (four) copies of them and each copy's
 // softmax takes a half (quarter) of the key tile's columns, with weights of 0 in the others: the
@@ -191,7 +193,7 @@ constexpr int kGateHeads = 8;
 // tensor core: 976 us for 2,048 tokens of 32 heads against 32,768 keys at D = 128, a quarter of it
 // the weights' second part (755 us and 1.46 PFLOP/s without; instructions take 77 to 85 cycles of the
 // 64 that they need alone).
-template <int NT, int D, Pass M, bool FOX>
+template <int NT, int D, Pass M, bool FOX, bool RING = FOX && NT == 1 && (M == Pass::one || M == Pass::shared)>
 struct CachedCfg {
     static constexpr uint32_t tile = 128 * D * 2, atom = 128 * 128;
     // the keys' update in this pass: by a product with P - I, or (single tokens) on the CUDA cores
@@ -210,7 +212,8 @@ struct CachedCfg {
     // heads, D = 128: 60 and 56, with gates 81 and 71.)
     static constexpr bool held = single && D == 64 && !FOX;
     // gates come through a ring of their own, of up to kGateHeads query heads
-    static constexpr bool ring = FOX && ahead;
+    static constexpr bool ring = RING;
+    static_assert(!RING || (FOX && ahead), "a ring of gates");
     // The rows' tiles, their high parts and then (keeps_low) their low ones, in shared memory, or in tensor
     // memory: where the update's product takes 64 KB (D = 128), and where they come ahead.
     static constexpr bool rows_in_tmem = ahead || (update && D == 128), low = keeps_low(NT, D);
@@ -245,11 +248,11 @@ struct CachedCfg {
     static constexpr uint32_t cS2 = 256;  // two_s: the odd steps' logits and weights
     static constexpr uint32_t cols = NT == 1 && D == 64 && !single ? 256 : 512;
 };
-template <Pass M, bool FOX>
+template <Pass M, bool FOX, bool RING = FOX>
 struct CachedFits {
-    using A = CachedCfg<1, 64, M, FOX>;
+    using A = CachedCfg<1, 64, M, FOX, RING>;
     using B = CachedCfg<2, 64, M, FOX>;
-    static_assert(CachedCfg<1, 128, M, FOX>::bytes <= 227 * 1024 && CachedCfg<2, 128, M, FOX>::bytes <= 227 * 1024 &&
+    static_assert(CachedCfg<1, 128, M, FOX, RING>::bytes <= 227 * 1024 && CachedCfg<2, 128, M, FOX>::bytes <= 227 * 1024 &&
                       A::bytes <= 227 * 1024 && A::ctas_per_sm * (A::bytes + 1024) <= 228 * 1024,
                   "shared memory");
     static_assert(256 * B::reg_row + 128 * B::reg_other <= 384 * 168, "registers");
@@ -258,8 +261,10 @@ struct CachedFits {
 template struct CachedFits<Pass::step, false>;
 template struct CachedFits<Pass::one, false>;
 template struct CachedFits<Pass::one, true>;
+template struct CachedFits<Pass::one, true, false>;
 template struct CachedFits<Pass::shared, false>;
 template struct CachedFits<Pass::shared, true>;
+template struct CachedFits<Pass::shared, true, false>;
 
 template <int N>
 __device__ __forceinline__ void reg_inc() {
@@ -301,12 +306,12 @@ __device__ __forceinline__ bool tile_whole(int pos0, int n, unsigned have, int b
     return pos0 + 128 <= n && have == (1u << (128 >> box_shift)) - 1u;
 }
 
-template <int NT, int D, bool FOX, Pass M>
-__global__ void __launch_bounds__(CachedCfg<NT, D, M, FOX>::threads, CachedCfg<NT, D, M, FOX>::ctas_per_sm)
+template <int NT, int D, bool FOX, Pass M, bool RING>
+__global__ void __launch_bounds__(CachedCfg<NT, D, M, FOX, RING>::threads, CachedCfg<NT, D, M, FOX, RING>::ctas_per_sm)
 tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtensorMap tm_x,
                  const __grid_constant__ CUtensorMap tm_l, const __grid_constant__ CUtensorMap tm_m,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
-    using L = CachedCfg<NT, D, M, FOX>;
+    using L = CachedCfg<NT, D, M, FOX, RING>;
     constexpr bool WIN = M == Pass::window || M == Pass::one;
     constexpr int NA = D / 64, NK = L::NK, NV = L::NV, kLow = low_weights(NT, D, FOX);
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -585,7 +590,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
             // every product has completed before TMEM is freed
             umma_commit(bar(L::END));
             mbar_wait(bar(L::END), 0, limit_ns);
-        } else if (L::ring && G <= kGateHeads && warp == L::other + 3) {
+        } else if (RING && warp == L::other + 3) {
             // ======================================================== gates into their ring
             uint32_t j = 0;
             bool ok = true;
@@ -693,7 +698,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                 if (L::single) {
                     if (!(ok = wait.warp(bar(L::KF + j % NK), (j / NK) & 1))) break;
                     float2 dot[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll(L::held ? D / 8 : 4)
+#pragma unroll(L::held ? D / 8 : FOX ? 2 : 4)
                     for (int c = 0; c < D / 8; ++c) {
                         const uint4 k8 = *key_at(c);
                         if (L::held) key[c] = k8;
@@ -716,7 +721,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                                            ((pos0 + r) & (page - 1))) * D
                                     : nullptr;
                 if (L::single) {
-#pragma unroll(L::held ? D / 8 : 4)
+#pragma unroll(L::held ? D / 8 : FOX ? 2 : 4)
                     for (int c = 0; c < D / 8; ++c) {
                         const uint4 k8 = L::held ? key[c] : *key_at(c);
                         const uint32_t k4[4] = {k8.x, k8.y, k8.z, k8.w};
@@ -856,7 +861,6 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
             const int cols = 128 >> (cp + (halves ? 1 : 0)), c_begin = c_copy + (halves ? half * cols : 0);
             const bool live = row0 + rw < rows_all, warp_live = row0 + (rw & ~31) < rows_all;
             const int head = live ? (row0 + rw) % G : 0, hq = t.h * G + head;
-            const bool staged = L::ring && G <= kGateHeads;
             const float gq =
                 FOX && live ? y.gq[(size_t)t.h * y.R + (size_t)t.s.first * G + row0 + rw] * kLog2e : 0.f;
             if (L::rows_in_tmem && !L::ahead) load_rows(t);
@@ -890,7 +894,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                 const bool whole = tile_whole(pos0, t.s.n, have, box_shift);
                 // gate sums of 32 keys from column c for the row's query head
                 auto gates_of = [&](int c, float4 *v) {
-                    if (staged) {
+                    if (RING) {
                         const float4 *const gp = reinterpret_cast<const float4 *>(
                             sm + L::gates + (j % L::NG_) * L::gslot + (head * 128 + c) * 4);
 #pragma unroll
@@ -916,7 +920,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                 const bool early = kAhead && cols == 32;
                 if (early) {
                     gates_of(c_begin, ahead);
-                } else if (FOX && !staged) {
+                } else if (FOX && !RING) {
 #pragma unroll 1
                     for (int c = c_begin; c < c_begin + cols; c += 16) {
                         const int bx = c >> box_shift, pid = __shfl_sync(0xffffffffu, id, bx);
@@ -930,7 +934,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                 const uint32_t cS = L::cS + (L::two_s ? place * L::cS2 : 0);
                 if (!(ok = wait.warp(bar(L::SF + place), (L::two_s ? phases >> place : j) & 1))) break;
                 if (L::two_s) phases ^= 1u << place;
-                if (staged && !(ok = wait.warp(bar(L::GF + j % L::NG_), (j / L::NG_) & 1))) break;
+                if (RING && !(ok = wait.warp(bar(L::GF + j % L::NG_), (j / L::NG_) & 1))) break;
                 tc_fence_after();
                 if (releases && !L::two_s) {
                     if (!L::update) release(L::KE, step % NK);
@@ -1105,7 +1109,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                 }
                 tc_fence_before();
                 mbar_arrive_warp(bar(L::PR + place));
-                if (staged) mbar_arrive_warp(bar(L::GE + j % L::NG_));
+                if (RING) mbar_arrive_warp(bar(L::GE + j % L::NG_));
             }
             // the next stretch's rows while the last product of values runs
             if (L::ahead && ok && at < u_end) {
@@ -1175,9 +1179,9 @@ cudaError_t big_smem(K kern, size_t bytes) {
 
 }  // namespace
 
-template <int NT, int D, bool FOX, Pass M>
-cudaError_t launch_cached(const StepOf<M> &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream) {
-    using L = CachedCfg<NT, D, M, FOX>;
+template <int NT, int D, bool FOX, Pass M, bool RING>
+cudaError_t launch_cached_as(const StepOf<M> &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream) {
+    using L = CachedCfg<NT, D, M, FOX, RING>;
     CUtensorMap tx{}, tl{}, tm{}, tk, tv;  // (rows that come ahead, and no P - I, need no map)
     // a map has no empty axis; of an empty pool nothing is loaded, every page number is outside it
     auto heads = [&](int pages) { return (long long)std::max(pages, 1) * a.c.Hkv; };
@@ -1186,11 +1190,18 @@ cudaError_t launch_cached(const StepOf<M> &a, const TcWs &y, uint64_t limit_ns, 
         !make_map(&tk, a.c.k_pages, D, a.c.page, heads(a.c.nk), a.c.page < 128 ? a.c.page : 128) ||
         !make_map(&tv, a.c.v_pages, D, a.c.page, heads(a.c.nv), a.c.page < 128 ? a.c.page : 128))
         return cudaErrorInvalidValue;
-    auto kern = tc_cached_kernel<NT, D, FOX, M>;
+    auto kern = tc_cached_kernel<NT, D, FOX, M, RING>;
     const cudaError_t e = big_smem(kern, L::bytes);
     if (e != cudaSuccess) return e;
     return launch(kern, dim3(y.plan[NT - 1].ctas), L::threads, L::bytes, stream, false, a, y, tx, tl, tm, tk, tv,
                   limit_ns);
+}
+
+template <int NT, int D, bool FOX, Pass M>
+cudaError_t launch_cached(const StepOf<M> &a, const TcWs &y, uint64_t limit_ns, cudaStream_t stream) {
+    if constexpr (CachedCfg<NT, D, M, FOX>::ring)
+        if (a.c.G > kGateHeads) return launch_cached_as<NT, D, FOX, M, false>(a, y, limit_ns, stream);
+    return launch_cached_as<NT, D, FOX, M, CachedCfg<NT, D, M, FOX>::ring>(a, y, limit_ns, stream);
 }
 
 #define EACH_PASS(WHAT, M)                                                                      \
