@@ -45,6 +45,7 @@ struct StepMore : Step {
     const int *prefix_of;
     const float *px;
     const float2 *pxml;
+    int one_rows;  // a prefix's queries go with NT = 1 up to so many rows (prefix_one_rows)
     bool shared;  // the step whose sequences are the prefixes: `cu` is a kernel's of this call
 };
 

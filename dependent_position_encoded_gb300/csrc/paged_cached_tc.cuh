@@ -1207,6 +1207,10 @@ cudaError_t launch_cached(const StepOf<M> &a, const TcWs &y, uint64_t limit_ns, 
 #define EACH_PASS(WHAT, M)                                                                      \
     WHAT(1, 64, false, M) WHAT(2, 64, false, M) WHAT(1, 128, false, M) WHAT(2, 128, false, M)   \
     WHAT(1, 64, true, M) WHAT(2, 64, true, M) WHAT(1, 128, true, M) WHAT(2, 128, true, M)
+#define SHARED_PASS(WHAT)                                                                       \
+    WHAT(1, 64, false, Pass::shared) WHAT(2, 64, false, Pass::shared)                           \
+    WHAT(1, 128, false, Pass::shared) WHAT(2, 128, false, Pass::shared)                         \
+    WHAT(1, 64, true, Pass::shared) WHAT(1, 128, true, Pass::shared) WHAT(2, 128, true, Pass::shared)
 #define PASS(NT, D, FOX, M) \
     template cudaError_t launch_cached<NT, D, FOX, M>(const StepMore &, const TcWs &, uint64_t, cudaStream_t);
 #define EXTERN_PASS(NT, D, FOX, M) extern PASS(NT, D, FOX, M)
@@ -1214,7 +1218,7 @@ cudaError_t launch_cached(const StepOf<M> &a, const TcWs &y, uint64_t limit_ns, 
     WHAT(1, 64, false, Pass::one) WHAT(1, 128, false, Pass::one)                                \
     WHAT(1, 64, true, Pass::one) WHAT(1, 128, true, Pass::one)
 EACH_PASS(EXTERN_PASS, Pass::window)
-EACH_PASS(EXTERN_PASS, Pass::shared)
+SHARED_PASS(EXTERN_PASS)
 ONE_PASS(EXTERN_PASS)
 
 }  // namespace paged

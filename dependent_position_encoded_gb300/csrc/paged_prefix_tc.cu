@@ -6,7 +6,7 @@
 namespace path {
 namespace paged {
 
-EACH_PASS(PASS, Pass::shared)
+SHARED_PASS(PASS)
 
 namespace {
 
@@ -168,8 +168,9 @@ template <int D, bool FOX>
 cudaError_t launch_shared(const StepMore &a, const Prefix &x, const TcWs &z, uint64_t limit_ns, cudaStream_t stream) {
     const StepMore v = shared_step(a, x);
     const cudaError_t e = launch_cached<1, D, FOX, Pass::shared>(v, z, limit_ns, stream);
-    if (e != cudaSuccess || (long long)a.N * a.c.G <= 128) return e;
-    return launch_cached<2, D, FOX, Pass::shared>(v, z, limit_ns, stream);
+    if (e != cudaSuccess || (long long)a.N * a.c.G <= a.one_rows) return e;
+    if constexpr (D == 64 && FOX) return cudaErrorInvalidValue;  // (prefix_one_rows: all go with NT = 1)
+    else return launch_cached<2, D, FOX, Pass::shared>(v, z, limit_ns, stream);
 }
 
 template <int D, bool FOX>

@@ -6,6 +6,7 @@
 // one behind the other, R = N G of them.
 #pragma once
 
+#include <climits>
 #include <type_traits>
 
 #include "paged.cuh"
@@ -80,6 +81,15 @@ __host__ __device__ __forceinline__ bool one_tile(int T, int G, int D, bool fox)
     return (T <= kC || D == 128 || fox) && (long long)T * G <= 128;
 }
 
+// Rows of a prefix's queries up to which they go by one row tile at a time. At D = 64 all of them: two CTAs
+// on an SM, each with a tile, are ahead of one CTA with two (one token each of G = 4 behind 16,384 keys, 384
+// rows 54 us against 66, 16,384 rows 1,219 against 1,380; with gates 90 and 97, 2,172 and 2,288), but that
+// queries of several blocks need the weights' second part (low_weights), unless there are gates. At
+// D = 128 a key slot is worth two tiles (1,536 rows: 393 us by one, 368 by two).
+inline int prefix_one_rows(int D, int max_chunk, bool fox) {
+    return D == 64 && (max_chunk <= kC || fox) ? INT_MAX : 128;
+}
+
 // Whether queries carried to the chunk's start are left in two parts: for the cached keys' pass, or to
 // be carried on to a prefix.
 __device__ __forceinline__ bool low_queries(const Step &a, int T, int D) {
@@ -89,12 +99,15 @@ __device__ __forceinline__ bool low_queries(const StepMore &a, int T, int D) {
     return a.prefix_of != nullptr || keeps_low(one_tile(T, a.c.G, D, a.log_f != nullptr) ? 1 : 2, D);
 }
 
+__host__ __device__ constexpr int rows_by_one(const Step &) { return 0; }  // (a plain step has no prefixes)
+__host__ __device__ inline int rows_by_one(const StepMore &a) { return a.one_rows; }
+
 // Row tiles and key tiles of a sequence in the plan of NT (0 where it goes with the other).
 template <typename A>
 __device__ __forceinline__ void plan_of(const A &a, const Seq &s, int D, int NT, int &tiles, int &ktiles) {
     const int G = a.c.G, rows = s.T * G;  // T G <= N G, which the host keeps within an int
     ktiles = sight_of(a, s).tiles(s.n, 128);
-    const bool one = enters(a) ? one_tile(s.T, G, D, a.log_f != nullptr) : rows <= 128;
+    const bool one = enters(a) ? one_tile(s.T, G, D, a.log_f != nullptr) : rows <= rows_by_one(a);
     tiles = one == (NT == 1) ? (rows + 128 * NT - 1) / (128 * NT) : 0;
 }
 
@@ -322,7 +335,7 @@ __device__ __forceinline__ RowParts parts_behind(const A &a, const Behind &x, in
     const int start = x.start[b];
     if (start < 0) return RowParts{};
     const int p = __ldg(x.of + b), first = x.cu[p], rows = (x.cu[p + 1] - first) * a.c.G;
-    return parts_of(x, a.c.seqs, rows, (__ldg(a.c.lens + p) + 127) / 128, rows <= 128, p, h,
+    return parts_of(x, a.c.seqs, rows, (__ldg(a.c.lens + p) + 127) / 128, rows <= rows_by_one(a), p, h,
                     (start - first + t) * a.c.G + g);
 }
 
