@@ -17,10 +17,12 @@ static_assert(kThr == kPrefixThr, "make_plans");
 // that of the step, the others take the single tokens, a sequence and key head each (BEHIND: and 64 rows
 // of its carry): OWN, of a step that has no others, enter them into the cache and leave their queries and
 // parts; BEHIND, carry their queries to the prefix's end, as a high and a low bf16 part (16 bits of
-// significand: keeps_low says what one part costs). With up to kFused sequences these find their places
-// by themselves beside the plan (each CTA reads all sequences' lengths, from L2), else in one made before,
-// by a launch of this kernel without sequences.
-constexpr int kFused = 1024;
+// significand: keeps_low says what one part costs). With few sequences and heads these find their places
+// by themselves beside the plan, each CTA reading all sequences' lengths, else in one made before, by a
+// launch of this kernel without sequences. Steps of single tokens behind 500 keys, us, beside / before:
+//   2 heads, d = 64:   30 sequences 21/25, 500 64/70, 1,000 105/113, 2,000 225/226, 4,000 501/428
+//   8 heads, d = 128:  30 sequences 28/32, 250 152/153, 500 281/269, 1,000 567/502, 4,000 3,613/1,968
+constexpr long long kFused = 1 << 20;  // lengths read by all CTAs, at most
 
 template <int D, bool OWN, bool BEHIND>
 __global__ void __launch_bounds__(kThr) tc_single_kernel(const StepMore a, const StepMore v, const Prefix x,
@@ -75,7 +77,7 @@ cudaError_t launch_tokens(const StepMore &a, const Prefix &x, const TcWs &y, con
     const StepMore v = BEHIND ? shared_step(a, x) : a;
     const int items = a.c.seqs * (BEHIND ? D / 64 : 1), plans = (OWN ? 1 : 0) + (BEHIND ? 1 : 0);
     const auto kern = tc_single_kernel<D, OWN, BEHIND>;
-    if (!BEHIND || a.c.seqs <= kFused)
+    if (!BEHIND || (long long)items * a.c.Hkv * a.c.seqs <= kFused)
         return launch(kern, dim3(plans + items, a.c.Hkv), kThr, 0, stream, first, a, v, x, y, z, plans, true);
     const cudaError_t e = launch(kern, dim3(plans), kThr, 0, stream, first, a, v, x, y, z, plans, true);
     return e != cudaSuccess ? e : launch(kern, dim3(items, a.c.Hkv), kThr, 0, stream, false, a, v, x, y, z, 0, false);
