@@ -81,13 +81,18 @@ __host__ __device__ __forceinline__ bool one_tile(int T, int G, int D, bool fox)
     return (T <= kC || D == 128 || fox) && (long long)T * G <= 128;
 }
 
-// Rows of a prefix's queries up to which they go by one row tile at a time. At D = 64 all of them: two CTAs
-// on an SM, each with a tile, are ahead of one CTA with two (one token each of G = 4 behind 16,384 keys, 384
-// rows 54 us against 66, 16,384 rows 1,219 against 1,380; with gates 90 and 97, 2,172 and 2,288), but that
-// queries of several blocks need the weights' second part (low_weights), unless there are gates. At
-// D = 128 a key slot is worth two tiles (1,536 rows: 393 us by one, 368 by two).
+// Rows of a prefix's queries up to which they go by one row tile at a time (NT = 1).
+// At D = 64 all of them: two CTAs on an SM, each with a tile, are ahead of one CTA with two (one token each
+// of G = 4 behind 16,384 keys, 384 rows 54 us against 66, 16,384 rows 1,219 against 1,380; with gates 90 and
+// 97, 2,172 and 2,288), but that queries of several blocks need the weights' second part (low_weights),
+// unless there are gates.
+// At D = 128 a key slot is worth two tiles (1,536 rows: 319 us by one, 309 by two; 10,000 rows of chunks of
+// up to 512: 1,259 and 1,121), but two leave no room for the queries' second part (keeps_low), whose
+// rounding is behind a prefix of thousands the largest. Errors of the output by one and by two, in
+// chunks of 7: 2.27e-3 and 2.55e-3 of the norm, 64: 2.35 and 2.54, 100: 2.31 and 2.47, 200: 2.33 and 2.42,
+// 500: 2.33 and 2.29, whose chunks' own roundings are the most by then. With gates few keys count: 1.9e-3.
 inline int prefix_one_rows(int D, int max_chunk, bool fox) {
-    return D == 64 && (max_chunk <= kC || fox) ? INT_MAX : 128;
+    return (D == 64 ? max_chunk <= kC || fox : max_chunk <= 4 * kC && !fox) ? INT_MAX : 128;
 }
 
 // Whether queries carried to the chunk's start are left in two parts: for the cached keys' pass, or to
