@@ -296,8 +296,11 @@ struct Ring {
 // batch of 32: 232 -> 246 us a step) and 20% of a long chunk at D = 128 (2,048 behind 32,768: 1,143 ->
 // 1,370 us). NT = 1, whose queries have fewer steps behind them, stays at 2.2e-3 without; with
 // gates few keys count: below 2.0e-3.
-__host__ __device__ constexpr int low_weights(int NT, int D, bool fox) {
-    return NT == 1 || fox ? 0 : D == 64 ? 128 : 64;
+// A window's pass at D = 128 has it for three quarters: behind a window of thousands a half leaves 2.51e-3
+// in chunks of 64 and of 100 tokens (W = 12,000), three quarters 2.40e-3 (two chunks of up to 1,024, W = 4,096: the
+// whole step 396 -> 406 us).
+__host__ __device__ constexpr int low_weights(int NT, int D, bool fox, Pass M) {
+    return NT == 1 || fox ? 0 : D == 64 ? 128 : M == Pass::window ? 96 : 64;
 }
 
 // Whether all boxes of a key tile lie on good pages below n: `have` one bit per box of
@@ -313,7 +316,7 @@ tc_cached_kernel(const StepOf<M> a, const TcWs y, const __grid_constant__ CUtens
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, uint64_t limit_ns) {
     using L = CachedCfg<NT, D, M, FOX, RING>;
     constexpr bool WIN = M == Pass::window || M == Pass::one;
-    constexpr int NA = D / 64, NK = L::NK, NV = L::NV, kLow = low_weights(NT, D, FOX);
+    constexpr int NA = D / 64, NK = L::NK, NV = L::NV, kLow = low_weights(NT, D, FOX, M);
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t base = smem_u32(sm);
     auto bar = [&](int i) { return base + L::bars + 8u * (uint32_t)i; };
