@@ -40,9 +40,10 @@ struct Step {
 // step, A below: what a plain one would only test costs its cached pass 3%.)
 struct StepMore : Step {
     int window, sinks;  // window 0: every new token sees every position before it
-    // Sequences that continue a prefix (paged_prefix.cuh): the row that each continues (below 0: none),
-    // and of each row of queries (Hkv, N G) the softmax part of its prefix's keys.
-    const int *prefix_of;
+    // Sequences that continue a prefix (paged_prefix.cuh): the row that each continues (below 0: none);
+    // fp32: its place among the prefix's tokens (below 0: it has none, and no part either), and of each
+    // row of queries (Hkv, N G) the softmax part of its prefix's keys.
+    const int *prefix_of, *pstart;
     const float *px;
     const float2 *pxml;
     int one_rows;  // a prefix's queries go with NT = 1 up to so many rows (prefix_one_rows)

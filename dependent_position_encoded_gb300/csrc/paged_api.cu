@@ -197,7 +197,7 @@ path_status extend(const path_paged_cache *p, const void *q, const void *k, cons
     const paged::Step plain{c, q, k, v, w, beta, fox ? log_f : nullptr, out,
                             sq, sk, sv, sw, sb, sf, so,
                             cu_tokens, N, max_chunk, scale * kLog2e, static_cast<uint32_t *>(ws)};
-    paged::StepMore a{plain, more.window, more.sinks, more.prefix_of, nullptr, nullptr,
+    paged::StepMore a{plain, more.window, more.sinks, more.prefix_of, nullptr, nullptr, nullptr,
                       paged::prefix_one_rows(p->d, max_chunk, fox), false};
     const bool bf16 = p->dtype == PATH_BF16, prefix = more.prefix_of != nullptr, is_plain = !prefix && more.window == 0;
     const long long seen = paged::most_seen(a);

@@ -353,7 +353,7 @@ paged_decode_merge(const A a, const Behind z, int chunk, int nsplit, const float
                     Ls = fmaf(ml.y, f, Ls);
                     Oc = fmaf(x.so[x.at(q) * D + c], f, Oc);
                 }
-            } else {
+            } else if (a.pstart[b] >= 0) {
                 const size_t row = ((size_t)h * a.N + s.first) * a.c.G + hq % a.c.G;
                 const float2 ml = a.pxml[row];
                 const float top = fmaxf(M, ml.x), f0 = exp2f(M - top), f1 = exp2f(ml.x - top);

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThr) f32_combine_kernel(const AnyStep a, cons
         }
     }
     if constexpr (std::is_same<AnyStep, StepMore>::value)
-        if (a.px != nullptr && __ldg(a.prefix_of + b) >= 0) {  // the keys of the sequence's prefix
+        if (a.px != nullptr && __ldg(a.prefix_of + b) >= 0 && a.pstart[b] >= 0) {  // the keys of the sequence's prefix
             const size_t at = ((size_t)(hq / a.c.G) * a.N + s.first + c * kC + r) * a.c.G + hq % a.c.G;
             const float2 ml = a.pxml[at];
             const float top = fmaxf(M, ml.x), f0 = exp2f(M - top), f1 = exp2f(ml.x - top);

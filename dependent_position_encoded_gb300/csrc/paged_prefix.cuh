@@ -137,6 +137,7 @@ inline StepMore shared_step(const StepMore &a, const Prefix &x) {
     v.max_chunk = a.N;
     v.window = v.sinks = 0;
     v.prefix_of = nullptr;
+    v.pstart = nullptr;
     v.px = nullptr;
     v.pxml = nullptr;
     v.shared = true;

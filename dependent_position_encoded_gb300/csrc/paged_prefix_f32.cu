@@ -180,6 +180,7 @@ cudaError_t launch_prefix_f32(StepMore &a, int d, float *carry, float *gates, fl
     x.of = a.prefix_of;
     x.carry = carry;
     x.gates = gates;
+    a.pstart = x.start;
     a.px = x.px;
     a.pxml = x.pxml;
     Ws y = z;
