@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kCarryThr) prefix_carry_kernel(const StepMore 
     const Seq s = seq_of(a, b);
     const bool mine = s.T > 1 && __ldg(x.of + b) >= 0;
     grid_wait();
-    if (!mine) return;
+    if (!mine || x.start[b] < 0) return;  // (no place among the prefix's tokens: left as it was)
     float4 *const C = reinterpret_cast<float4 *>(x.carry + (((size_t)b * a.c.Hkv + h) * D + r) * D);
     float4 c[kCarryPer][NC];
 #pragma unroll

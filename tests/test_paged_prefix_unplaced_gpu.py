@@ -1,5 +1,6 @@
 """Steps behind shared prefixes whose cu_tokens falls, with a sequence that gets no place among its
-prefix's tokens: what a workspace held before the call has no part in any result."""
+prefix's tokens: what a workspace held before the call has no part in any result, and the sequence's
+carry stays as it was."""
 import pytest
 import torch
 
@@ -49,3 +50,15 @@ def test_outputs_without_a_place(lib, unplaced, dtype, fox, d):
         assert lib.path_check_workspace(ws) == lib.ERR_CACHE
         first = out.clone() if first is None else first
         assert same_bits(out, first)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fox", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_carries_without_a_place(lib, unplaced, dtype, fox, d):
+    x, _, ws, step = unplaced(lib, dtype, fox, d)
+    before = px.snapshot(x)
+    step()
+    assert lib.path_check_workspace(ws) == lib.ERR_CACHE
+    assert torch.equal(x["carry"], before["carry"])
+    assert not fox or torch.equal(x["gate_carry"], before["gate_carry"])
