@@ -906,8 +906,8 @@ def new_paged_carry(cache, Hq=None):
     torch = _torch()
     c = _paged_cache(cache, Hq=Hq)
     dev = cache.k_pages.device
-    carry = torch.eye(c.d, device=dev).repeat(c.seqs, c.Hkv, 1, 1)
-    return carry, torch.zeros((c.seqs, c.Hq), device=dev)
+    carry = torch.eye(c.d, dtype=torch.float32, device=dev).repeat(c.seqs, c.Hkv, 1, 1)
+    return carry, torch.zeros((c.seqs, c.Hq), dtype=torch.float32, device=dev)
 
 
 def _paged_gates(log_f, cache):
