@@ -37,8 +37,8 @@ EXPORTED = ("path_workspace_bytes", "path_attn_fwd", "path_fox_fwd", "path_fwd_p
             "path_fox_bwd", "path_paged_workspace_bytes", "path_paged_extend",
             "path_fox_paged_extend", "path_paged_reserve", "path_paged_fork", "path_paged_free",
             "path_paged_compact", "path_paged_window_extend", "path_fox_paged_window_extend",
-            "path_paged_trim", "path_paged_prefix_workspace_bytes", "path_paged_prefix_extend",
-            "path_fox_paged_prefix_extend")
+            "path_paged_trim", "path_paged_trim_rows", "path_paged_prefix_workspace_bytes",
+            "path_paged_prefix_extend", "path_fox_paged_prefix_extend")
 
 _lib = None
 
@@ -127,6 +127,8 @@ def _load():
     lib.path_fox_paged_prefix_extend.restype = I
     lib.path_paged_trim.argtypes = [C, I, I, P, S, P]
     lib.path_paged_trim.restype = I
+    lib.path_paged_trim_rows.argtypes = [C, P, I, I, I, P, S, P]
+    lib.path_paged_trim_rows.restype = I
     lib.path_paged_reserve.argtypes = [C, P, P, S, P]
     lib.path_paged_reserve.restype = I
     lib.path_paged_fork.argtypes = [C, P, P, I, P, S, P]
@@ -978,10 +980,15 @@ def path_paged_free(rows, cache, workspace=None, stream=None):
     return _paged_call("path_paged_free", cache, workspace, stream, a, n)
 
 
-def path_paged_trim(cache, window, sinks=0, workspace=None, stream=None):
+def path_paged_trim(cache, window, sinks=0, workspace=None, stream=None, rows=None):
     """Gives back the pages that no later step through this window reaches: the slots behind them
-    move down and cache.lens falls by their tokens. Workspaces as in path_paged_reserve."""
-    return _paged_call("path_paged_trim", cache, workspace, stream, *_window(window, sinks))
+    move down and cache.lens falls by their tokens. rows (a list of ints): the sequences that are
+    trimmed, by default every one of the cache. Rows that other steps read whole (prefixes, sequences
+    behind them or of path_paged_extend) must not be among them. Workspaces as in path_paged_reserve."""
+    if rows is None:
+        return _paged_call("path_paged_trim", cache, workspace, stream, *_window(window, sinks))
+    a, n = _rows(rows)
+    return _paged_call("path_paged_trim_rows", cache, workspace, stream, a, n, *_window(window, sinks))
 
 
 def path_paged_compact(cache, workspace=None, stream=None):

@@ -32,7 +32,8 @@ cudaError_t launch_fork(const Cache &c, const Rows<kMaxRows> &src, const Rows<kM
                         void *ws, cudaStream_t stream);
 cudaError_t launch_free(const Cache &c, const Rows<kMaxRows> &rows, void *ws, cudaStream_t stream);
 cudaError_t launch_compact(const Cache &c, int row_bytes, void *ws, cudaStream_t stream);
-cudaError_t launch_trim(const Cache &c, int window, int sinks, void *ws, cudaStream_t stream);
+cudaError_t launch_trim(const Cache &c, const Rows<kMaxRows> &rows, int window, int sinks, void *ws,
+                        cudaStream_t stream);
 }  // namespace paged
 }  // namespace path
 
@@ -274,6 +275,16 @@ bool repeats(const Rows &a) {
     return false;
 }
 
+path_status trim(const path_paged_cache *p, const Rows &rows, int window, int sinks, void *ws, size_t ws_bytes,
+                 void *stream) {
+    path_status st = check_cache(p, true);
+    if (st != PATH_OK) return st;
+    const Cache c = to_cache(p);
+    if ((st = check_workspace(ws, ws_bytes, paged::pages_ws_bytes(c))) != PATH_OK) return st;
+    if (c.max_pages == 0) return PATH_OK;
+    return cuda_status(paged::launch_trim(c, rows, window, sinks, ws, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -368,11 +379,19 @@ path_status path_paged_trim(const path_paged_cache *cache, int window, int sinks
     if (st != PATH_OK) return st;
     if ((st = check_window(window, sinks)) != PATH_OK) return st;
     if (cache->seqs == 0) return PATH_OK;
-    if ((st = check_cache(cache, true)) != PATH_OK) return st;
-    const Cache c = to_cache(cache);
-    if ((st = check_workspace(ws, ws_bytes, paged::pages_ws_bytes(c))) != PATH_OK) return st;
-    if (c.max_pages == 0) return PATH_OK;
-    return cuda_status(paged::launch_trim(c, window, sinks, ws, static_cast<cudaStream_t>(stream)));
+    return trim(cache, Rows{}, window, sinks, ws, ws_bytes, stream);
+}
+
+path_status path_paged_trim_rows(const path_paged_cache *cache, const int *rows, int num_rows, int window,
+                                 int sinks, void *ws, size_t ws_bytes, void *stream) {
+    path_status st = check_cache_sizes(cache);
+    if (st != PATH_OK) return st;
+    Rows a;
+    if ((st = check_rows(cache, rows, num_rows, &a)) != PATH_OK) return st;
+    if (repeats(a)) return PATH_ERR_ARG;
+    if ((st = check_window(window, sinks)) != PATH_OK) return st;
+    if (num_rows == 0) return PATH_OK;
+    return trim(cache, a, window, sinks, ws, ws_bytes, stream);
 }
 
 path_status path_paged_reserve(const path_paged_cache *cache, const int *extra, void *ws,

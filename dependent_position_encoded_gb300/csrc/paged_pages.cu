@@ -314,12 +314,14 @@ __global__ void __launch_bounds__(256) free_kernel(const Cache c, const Rows<N> 
 // The pages whose every position lies behind the window of the next token and past the sinks leave
 // the sequence. The logits go by distances and no position has a number of its own, so the slots
 // behind them move down and the length falls by as many pages; what a window sees is the same. A
-// CTA per sequence; slots move down in rounds of kTrimThr * kTrimItems, read before they are
-// written.
+// CTA per sequence, of `rows` or (where that names none) of all; slots move down in rounds of
+// kTrimThr * kTrimItems, read before they are written.
 constexpr int kTrimThr = 256, kTrimItems = 8;
 
-__global__ void __launch_bounds__(kTrimThr) trim_kernel(const Cache c, int window, int sinks, const PagesWs y) {
-    const int s = blockIdx.x, tid = threadIdx.x, n = c.lens[s];
+template <int N>
+__global__ void __launch_bounds__(kTrimThr)
+trim_kernel(const Cache c, const Rows<N> rows, int window, int sinks, const PagesWs y) {
+    const int s = rows.n > 0 ? rows.row[blockIdx.x] : blockIdx.x, tid = threadIdx.x, n = c.lens[s];
     if (n < 0 || n > (long long)c.max_pages << c.page_shift) {
         if (tid == 0) report_status(y.status, kStatusCache);
         return;
@@ -512,8 +514,14 @@ cudaError_t launch_free(const Cache &c, const Rows<kMaxRows> &rows, void *ws, cu
                : launch(free_kernel<kMaxRows>, dim3(rows.n, 2), 256, 0, stream, true, c, rows, y);
 }
 
-cudaError_t launch_trim(const Cache &c, int window, int sinks, void *ws, cudaStream_t stream) {
-    return launch(trim_kernel, dim3(c.seqs), kTrimThr, 0, stream, true, c, window, sinks, pages_ws(c, ws, nullptr));
+// rows: the sequences (n = 0: all of the cache)
+cudaError_t launch_trim(const Cache &c, const Rows<kMaxRows> &rows, int window, int sinks, void *ws,
+                        cudaStream_t stream) {
+    const PagesWs y = pages_ws(c, ws, nullptr);
+    const dim3 grid(rows.n > 0 ? rows.n : c.seqs);
+    return rows.n <= kFewRows
+               ? launch(trim_kernel<kFewRows>, grid, kTrimThr, 0, stream, true, c, few_rows(rows), window, sinks, y)
+               : launch(trim_kernel<kMaxRows>, grid, kTrimThr, 0, stream, true, c, rows, window, sinks, y);
 }
 
 cudaError_t launch_compact(const Cache &c, int row_bytes, void *ws, cudaStream_t stream) {

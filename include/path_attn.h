@@ -473,9 +473,16 @@ path_status path_fox_paged_prefix_extend(const path_paged_cache *cache, const vo
  * falls by their tokens (logits go by distances, so nothing else changes): a stream's cache
  * stays within about window + sinks + page tokens. A shared value page's count falls by one. A
  * sequence whose length does not fit the cache is left as it was (PATH_ERR_CACHE).
+ * Every sequence of the cache is trimmed. A row that other steps read whole (a prefix, a sequence
+ * behind one, a sequence of path_paged_extend) would lose positions that they still see: where the
+ * cache holds such rows, name the others to path_paged_trim_rows.
  */
 path_status path_paged_trim(const path_paged_cache *cache, int window, int sinks, void *ws,
                             size_t ws_bytes, void *stream);
+
+/* path_paged_trim of the given rows alone (host list of at most 1024, none twice). */
+path_status path_paged_trim_rows(const path_paged_cache *cache, const int *rows, int num_rows, int window,
+                                 int sinks, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * Maps free pages so that sequence s can hold lens[s] + extra[s] tokens (extra: (seqs) int32
