@@ -239,8 +239,12 @@ struct CachedCfg {
     static constexpr int other = update || duo || NT == 2 ? 8 : 4, threads = 32 * (other + 4);
     static constexpr int ctas_per_sm = NT == 1 && D == 64 && !single ? 2 : 1;
     // registers after the split of what the CTA is launched with (NT = 2: 168 for each thread; NT = 1
-    // with two CTAs per SM: 80): the softmax's warpgroups, the update's and the last one
-    static constexpr bool split = NT == 2 || (matrix && D == 64);
+    // with two CTAs per SM: 80): the softmax's warpgroups, the update's and the last one. A window's pass of
+    // NT = 1 goes without: a form of it that held more across its steps raised an illegal address whose cause
+    // nobody found, and so had one of the plain step's, both with this split. Its softmax spills instead (64
+    // streams of 4 tokens, W = 4,096, 16 heads: 361 -> 367 us a step; 32 with gates and four query heads to a
+    // key head 148 -> 182).
+    static constexpr bool split = NT == 2 || (matrix && D == 64 && M == Pass::step);
     static constexpr int reg_row = NT == 2 ? 200 : 104, reg_update = 72, reg_other = NT == 2 ? 104 : 64;
     // TMEM columns: per row tile S 128 (the weights over it) and O; NT = 1: the update's product, or the
     // rows' two parts
