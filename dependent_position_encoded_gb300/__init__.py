@@ -696,13 +696,25 @@ class _on:
             g.__exit__(*e)
 
 
+def _ints(names, *values):
+    """The values as C ints, which would take the low bits of larger numbers."""
+    values = tuple(int(x) for x in values)
+    if not all(-2**31 <= x < 2**31 for x in values):
+        raise ValueError("%s must be 32-bit ints" % names)
+    return values
+
+
+def _window(window, sinks):
+    return _ints("window and sinks", window, sinks)
+
+
 def path_paged_workspace_bytes(cache, num_tokens=0, max_chunk=0, Hq=None, prefix=False):
     """Workspace bytes of every call on `cache` with up to num_tokens new tokens in all and
     max_chunk per sequence (0: the page calls alone); of those behind a prefix only with
     prefix=True. Hq: query heads, where the cache has no g_pages to tell (default: the key heads)."""
     c = _paged_cache(cache, Hq=Hq)
     call = _load().path_paged_prefix_workspace_bytes if prefix else _load().path_paged_workspace_bytes
-    return int(call(ctypes.byref(c), int(num_tokens), int(max_chunk)))
+    return int(call(ctypes.byref(c), *_ints("num_tokens and max_chunk", num_tokens, max_chunk)))
 
 
 def new_paged_workspace(cache, num_tokens=0, max_chunk=0, Hq=None, prefix=False):
@@ -748,6 +760,9 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
         raise ValueError("q has head size %d, the cache %d" % (d, c.d))
     if out is not None and (N > 1 and o0[0] == 0 or Hq > 1 and o0[1] == 0):
         raise ValueError("out must not repeat its own memory")
+    most = int(max_chunk)
+    if not -2**31 <= most < 2**31:  # (as _ints, on the way of every step)
+        raise ValueError("max_chunk must be a 32-bit int")
     _paged_workspace(workspace)
     dev = _paged_devices(cache, q, k, v, w, beta, log_f, out, cu_tokens, workspace, *tensors)
     gate = () if log_f is None else (log_f.data_ptr(),)
@@ -760,7 +775,7 @@ def _paged_extend(name, q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, sc
             workspace = new_paged_workspace(cache, N, max_chunk, Hq, prefix=len(tensors) > 0)
         _check(getattr(_load(), name)(
             ctypes.byref(c), q.data_ptr(), k.data_ptr(), v.data_ptr(), w.data_ptr(),
-            beta.data_ptr(), *gate, cu_tokens.data_ptr(), N, int(max_chunk), *more,
+            beta.data_ptr(), *gate, cu_tokens.data_ptr(), N, most, *more,
             *(t.data_ptr() for t in tensors), _scale(scale, d),
             out.data_ptr(), _C14(q0[0], q0[1], k0[0], k0[1], v0[0], v0[1], w0[0], w0[1], b0[0], b0[1],
                                  f0[0], f0[1], o0[0], o0[1]), None if workspace is None else workspace.data_ptr(),
@@ -821,14 +836,6 @@ def path_fox_paged_extend(q, k, v, w, beta, log_f, cu_tokens, cache, max_chunk, 
     _paged_gates(log_f, cache)
     return _paged_extend("path_fox_paged_extend", q, k, v, w, beta, log_f, cu_tokens, cache,
                          max_chunk, scale, out, workspace, stream)
-
-
-def _window(window, sinks):
-    """A window and its sinks as C ints, which would take the low bits of larger numbers."""
-    window, sinks = int(window), int(sinks)
-    if not (-2**31 <= window < 2**31 and -2**31 <= sinks < 2**31):
-        raise ValueError("window and sinks must be 32-bit ints")
-    return window, sinks
 
 
 def path_paged_window_extend(q, k, v, w, beta, cu_tokens, cache, max_chunk, window, sinks=0,
