@@ -900,39 +900,23 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const A a, const TcWs 
             v[E - 1] = t.w;
         }
     };
+    // the row's maximum, sum and values
     float M, L, O[E];
-    // the parts from..number in steps of `step`, P at a time; at(q): where part q is
-    auto join = [&](int from, int number, int step, const float *so, const float2 *sml, auto at) {
-        for (int p0 = from; p0 < number; p0 += P * step) {
-            float2 ml[P];
-            float v[P][E];
+    auto fold = [&](const float2 (&ml)[P], const float (&v)[P][E]) {
+        float m = M;
 #pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const int q = p0 + j * step;
-                ml[j] = make_float2(-INFINITY, 0.f);
+        for (int j = 0; j < P; ++j) m = fmaxf(m, ml[j].x);
+        const float use = W > 1 && m == -INFINITY ? 0.f : m, f0 = exp2f(M - use);
+        M = m;
+        L *= f0;
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[j][e] = 0.f;
-                if (q < number) {
-                    const size_t i = at(q);
-                    ml[j] = sml[i];
-                    load(so + i * D, v[j]);
-                }
-            }
-            float m = M;
+        for (int e = 0; e < E; ++e) O[e] *= f0;
 #pragma unroll
-            for (int j = 0; j < P; ++j) m = fmaxf(m, ml[j].x);
-            const float use = W > 1 && m == -INFINITY ? 0.f : m, f0 = exp2f(M - use);
-            M = m;
-            L *= f0;
+        for (int j = 0; j < P; ++j) {
+            const float f = exp2f(ml[j].x - use);  // absent keys alone: 0, and their row 0
+            L = fmaf(ml[j].y, f, L);
 #pragma unroll
-            for (int e = 0; e < E; ++e) O[e] *= f0;
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const float f = exp2f(ml[j].x - use);  // absent keys alone: 0, and their row 0
-                L = fmaf(ml[j].y, f, L);
-#pragma unroll
-                for (int e = 0; e < E; ++e) O[e] = fmaf(v[j][e], f, O[e]);
-            }
+            for (int e = 0; e < E; ++e) O[e] = fmaf(v[j][e], f, O[e]);
         }
     };
     // of the row looked up last: rows below `known` are of the same tile
@@ -974,16 +958,48 @@ __global__ void __launch_bounds__(kThr) tc_combine_kernel(const A a, const TcWs 
             const float2 z = y.pml[row];
             M = z.x, L = z.y;  // M is never -inf: a row has its own key
             load(y.po + row * D, O);
-            join(0, number, 1, tile == 128 ? y.so[0] : y.so[1], tile == 128 ? y.sml[0] : y.sml[1], [&](int q) {
-                return at0 + (size_t)(q >> cp) * tile + (q & ((1 << cp) - 1)) * (128 >> cp);
-            });
+            const float *const so = tile == 128 ? y.so[0] : y.so[1];
+            const float2 *const sml = tile == 128 ? y.sml[0] : y.sml[1];
+            for (int p0 = 0; p0 < number; p0 += P) {
+                float2 ml[P];
+                float v[P][E];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const int q = p0 + j;
+                    ml[j] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[j][e] = 0.f;
+                    if (q < number) {
+                        const size_t at = at0 + (size_t)(q >> cp) * tile + (q & ((1 << cp) - 1)) * (128 >> cp);
+                        ml[j] = sml[at];
+                        load(so + at * D, v[j]);
+                    }
+                }
+                fold(ml, v);
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < E; ++e) O[e] = 0.f;
         }
         if (BEHIND && __ldg(x.of + lo) >= 0) {
             const RowParts behind = parts_behind(a, x, lo, h, tok - s.first, r - tok * G);
-            join(sub, behind.number, W, behind.so, behind.sml, [&](int q) { return behind.at(q); });
+            for (int p0 = sub; p0 < behind.number; p0 += P * W) {
+                float2 ml[P];
+                float v[P][E];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const int q = p0 + j * W;
+                    ml[j] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[j][e] = 0.f;
+                    if (q < behind.number) {
+                        const size_t at = behind.at(q);
+                        ml[j] = behind.sml[at];
+                        load(behind.so + at * D, v[j]);
+                    }
+                }
+                fold(ml, v);
+            }
         }
         if (W > 1) {  // one row a warp: every warp of the CTA comes by
 #pragma unroll
