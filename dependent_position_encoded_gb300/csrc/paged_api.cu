@@ -118,6 +118,15 @@ path_status check_workspace(const void *ws, size_t bytes, size_t need) {
 // With gates and G = 1 the one-pass kernel leaves most value rows unread and takes every size: behind at
 // 2^16 and from 2^21 on, ahead between. Its weights are fp32 where the block kernels' are bf16, so
 // equal times go to it. fp32 inputs have no tensor path: one-pass wherever it takes G.
+// A window counts by what it can have in sight. Behind prefixes the positions are those of the tables still,
+// which are as wide as the prefix, while these kernels go over the sequences' own tails, and each tail is
+// cut into splits by that width. Whole steps there, with 8 key heads, pages of 64 and one prefix (us,
+// one-pass / block kernels; sequences, prefix, tails):
+//                         4, 2,000, 64  32, 2,000, 64  4, 16,384, 64  32, 16,384, 64  8, 16,384, 2,000
+//   gates, G = 1, d =  64    30.2/32.4      37.1/39.7      49.9/39.5       63.0/51.7        68.5/48.3
+//                    128     37.6/36.5      50.0/47.6      54.8/47.4       86.6/70.2       105.5/79.9
+// so from tables of 2^19 on the rule takes the slower side there. Without gates, G = 1, it takes the one-pass
+// kernels in the first column alone (25.0/27.6, 27.3/31.5).
 bool one_pass(const Cache &c, long long seen, int max_chunk, bool bf16, bool fox) {
     if (max_chunk != 1 || !paged::decode_takes(c.G)) return false;
     if (!bf16 || (fox && c.G == 1)) return true;

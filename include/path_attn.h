@@ -441,7 +441,9 @@ path_status path_fox_paged_window_extend(const path_paged_cache *cache, const vo
  * New token i's logit with key j of the prefix is scale * k_j^T (C H_1 ... H_i) q_i; the sequence's own
  * cached and new keys are scored and advanced as in path_paged_extend, and one softmax goes over all of
  * them. A prefix is a row that steps have filled as any other; it may grow again, once it is nobody's
- * prefix any more. path_paged_fork copies a sequence's own pages: copy its row of carry with it.
+ * prefix any more. A row whose length is 0 counts as a prefix without keys: free or trim none that is
+ * somebody's. path_paged_fork copies a sequence's own pages: copy its rows of prefix_of, carry and
+ * gate_carry with them.
  *   ws     : path_paged_prefix_workspace_bytes(cache, num_tokens, max_chunk) bytes, which serves every
  *            other call on the cache too
  */
